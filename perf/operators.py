@@ -189,7 +189,7 @@ def prepare(case, seed):
             s["labels"][first:first + length // 4] = -100
         s["ref"][s["labels"] < 0] = 0
         s["beta"], s["smoothing"], s["grad_scale"] = 0.1, 0.05, 1024.0
-        for name, n in (("logp", rows), ("lse", rows), ("coef", rows), ("loss", 1), ("pair_loss", pairs),
+        for name, n in (("logp", rows), ("stats", 2 * rows), ("coef", rows), ("loss", 1), ("pair_loss", pairs),
                         ("rewards", 2 * pairs)):
             s[name] = torch.empty(n, device="cuda")
         s["dlogits"] = torch.empty_like(s["logits"]) if case["train"] else None
@@ -254,12 +254,12 @@ def _run_own(s):
         drop = s["drop"] or Z.Drop(0.0, s["seed"], site=SITE, step=STEP, first=s["first"])
         Z.zero_dropout(s["x"], s["res"], s["out"], code, drop)
         return s["out"]
-    Z.zero_token_logp(s["logits"], code, s["labels"], s["logp"], s["lse"], s["ws"])
+    Z.zero_token_logp(s["logits"], code, s["labels"], s["logp"], s["stats"], s["ws"])
     Z.zero_preference_loss(s["offsets"], s["labels"], s["vocab"], s["logp"], s["ref"], s["beta"], s["smoothing"],
                            s["grad_scale"], s["loss"], s["pair_loss"], s["rewards"], s["coef"])
     got = {"loss": s["loss"], "rewards": s["rewards"], "logp": s["logp"]}
     if s["train"]:
-        Z.zero_token_logp_grad(s["logits"], code, s["labels"], s["lse"], s["coef"], s["dlogits"])
+        Z.zero_token_logp_grad(s["logits"], code, s["labels"], s["stats"], s["coef"], s["dlogits"])
         got["dlogits"] = s["dlogits"]
     return got
 
