@@ -353,6 +353,224 @@ ZERO_API zero_status zero_set_warm_read(int32_t enable);
  */
 ZERO_API zero_status zero_set_stream_write_window(void* stream, int64_t period_ticks, int64_t open_ticks);
 
+/* ------------------------------------------------------------------------
+ * Operators at the two ends of the model whose step the calls above take:
+ * the vocabulary table's lookup and gradient, which read and write the flat
+ * buffers a plan lays out, dropout, and the paired preference loss with the
+ * gradient of its logits.  They are not operations of the pages.
+ *
+ * The conventions above hold for them too: nothing is allocated, nothing
+ * synchronises, every table travels in the kernel arguments, and no launch
+ * depends on memory that an earlier call left behind, so that every call can
+ * be captured into a graph.  A workspace may be reused by the next call on
+ * the same stream; two calls that can run at once (two streams, two graphs
+ * replayed beside each other) need one each.  The calls are issued to the
+ * current device, which has to be the one of the buffers and of the stream.
+ * Sums, softmax statistics and norms are held in fp32 or more and are taken
+ * in an order that depends on the sizes alone, so that a call repeated on the
+ * same inputs gives the same bits.
+ *
+ * Integers in device memory (tokens, labels, offsets) cannot be checked on
+ * the host.  Each kernel checks them itself: an id outside its range is
+ * treated as a padding id, as each entry says, and never read or written
+ * through.
+ * --------------------------------------------------------------------- */
+
+typedef enum zero_itype { ZERO_I32 = 0, ZERO_I64 = 1 } zero_itype;
+
+/* Which elements a dropout keeps: a function of these numbers and of the
+ * element's position alone, so that the backward pass asks for the same mask
+ * again and no mask is stored.
+ *   key = seed, then for f in (site, step): key = mix64((key ^ f) + GAMMA)
+ *   element e takes the 16 bits at position (e mod 4) of
+ *   mix64(key + (e div 4 + 1) * GAMMA), lowest bits first
+ *   and is kept where they are >= cut = round-half-even(p * 65536)
+ * mix64 and GAMMA are SplitMix64's (Steele, Lea & Flood, OOPSLA 2014).  p is
+ * thereby rounded to a multiple of 2^-16; kept elements are multiplied by
+ * 65536 / (65536 - cut), which keeps the mean exact. */
+typedef struct zero_drop {
+  double p;                /* share dropped, in [0, 1]; 1 drops everything */
+  uint64_t seed;           /* e.g. one per run and rank */
+  uint64_t site;           /* which dropout of the model */
+  uint64_t step;           /* training step */
+  const uint64_t* step_dev;/* device address read when the kernel runs, in
+                              place of step (a captured graph then takes
+                              another mask at each replay), or NULL */
+  int64_t first;           /* e of the call's first element, >= 0 (a rank that
+                              holds a piece of a tensor passes where it
+                              starts) */
+} zero_drop;
+
+/*
+ * zero_embed -- lookup in a table that is a tensor of the plan.
+ *   out[i, c] = (16-bit or fp32 rounding of) table[tokens[i], c] * f
+ *   f = fp32(scale * 65536 / (65536 - cut)); a dropped element is 0.
+ *   plan, tensor  which tensor of the plan; its numel must be a multiple of
+ *               hidden, and it is read as rows of `hidden` elements.
+ *   params      the full flat parameter buffer (psi_pad elements), as
+ *               zero_adam_step with dst_is_full or zero_gather_pack leaves it.
+ *   tokens      device array of n ids; one outside [0, rows) is a padding id:
+ *               its output row is zero.
+ *   drop        dropout of the output, element i * hidden + c at first + that,
+ *               or NULL.
+ *   out         n rows of `hidden` elements, out_stride elements apart
+ *               (>= hidden; what lies between rows is left as it was).
+ * Errors: EINVAL for nulls, a tensor index out of range, hidden < 1 or not
+ * dividing the tensor, a negative n, a short stride, misalignment, p outside
+ * [0, 1], or out overlapping params or tokens; EUNSUPPORTED for more than
+ * 2^31 - 2 rows or hidden above 2^24.
+ */
+ZERO_API zero_status zero_embed(zero_plan_t plan, int32_t tensor, int64_t hidden, const void* params,
+                                zero_dtype param_dt, const void* tokens, zero_itype token_it, int64_t n,
+                                double scale, const zero_drop* drop, void* out, zero_dtype out_dt,
+                                int64_t out_stride, void* stream);
+
+/*
+ * zero_token_order -- the positions of n tokens in token order, equal tokens
+ * in position order: what zero_embed_grad sums by.  It needs the tokens
+ * alone, so that it can run beside the forward pass.
+ *   rows        rows of the table; a token outside [0, rows) is a padding id
+ *               and goes to the end.
+ *   sorted      device int32[n]: the tokens in order, a padding id as `rows`.
+ *   order       device int32[n]: the position each came from.
+ *   workspace, ws_bytes  device workspace of
+ *               zero_token_order_workspace_bytes(n, rows) bytes, 16-byte
+ *               aligned.
+ * Errors: EINVAL for nulls, misalignment, a negative n, rows < 0, a short
+ * workspace or overlapping buffers; EUNSUPPORTED for n above 2^30 or rows
+ * above 2^31 - 2.
+ */
+ZERO_API size_t zero_token_order_workspace_bytes(int64_t n, int64_t rows);
+ZERO_API zero_status zero_token_order(const void* tokens, zero_itype token_it, int64_t n, int64_t rows,
+                                      int32_t* sorted, int32_t* order, void* workspace, size_t ws_bytes,
+                                      void* stream);
+
+/*
+ * zero_embed_grad -- the gradient of zero_embed's table: a rank's
+ * contribution to zero_shard_reduce or zero_adam_step, written where those
+ * read it.
+ *   g[r, c] = f * sum over the positions i with tokens[i] == r, ascending,
+ *             of keep(i, c) * dy[i, c]            (f as in zero_embed)
+ *   The sum is fp32, in an order fixed by n and hidden; g is rounded once.
+ *   sorted, order  what zero_token_order wrote for these n tokens.
+ *   dy          n rows of `hidden` elements, dy_stride elements apart.
+ *   scale, drop what the forward call had (scale may hold a loss scale too).
+ *   dst         rank < 0: the full flat gradient buffer (psi_pad elements);
+ *               the tensor's range is written, nothing else.
+ *               rank >= 0: a compact slice of shard_total elements for that
+ *               owner; the part of the tensor that the owner holds is
+ *               written, nothing else.  What lies outside that part is not
+ *               summed, and its rows of dy are not read.
+ *   accumulate  0: every element of that range is written, a row without a
+ *               token as zero.  1: g is added to what dst holds (in fp32,
+ *               rounded once), for a table that is also the output matrix;
+ *               rows without a token are left as they were.
+ *   workspace, ws_bytes  zero_embed_grad_workspace_bytes(n, hidden) bytes,
+ *               16-byte aligned; it may be the one zero_token_order used.
+ * The stores are non-temporal, as zero_adam_step likes its slices.
+ * Errors: as zero_embed, and EINVAL for rank >= n_d, accumulate other than 0
+ * or 1, a short workspace or overlapping buffers; EUNSUPPORTED for n above
+ * 2^30.
+ */
+ZERO_API size_t zero_embed_grad_workspace_bytes(int64_t n, int64_t hidden);
+ZERO_API zero_status zero_embed_grad(zero_plan_t plan, int32_t tensor, int64_t hidden, const int32_t* sorted,
+                                     const int32_t* order, int64_t n, const void* dy, zero_dtype dy_dt,
+                                     int64_t dy_stride, double scale, const zero_drop* drop, void* dst,
+                                     zero_dtype dst_dt, int32_t rank, int32_t accumulate, void* workspace,
+                                     size_t ws_bytes, void* stream);
+
+/*
+ * zero_dropout -- dropout of n contiguous elements, with an optional residual.
+ *   out[e] = residual[e] + (kept ? x[e] * fp32(65536 / (65536 - cut)) : 0)
+ * in fp32, rounded once.  A dropped element contributes nothing, whatever x
+ * holds there.  The backward pass is the same call on dy without a residual
+ * (the residual's own gradient is dy).
+ *   x, out      the same element type; out may be x or the residual itself.
+ *   residual    the same type, or NULL.
+ *   drop        not NULL; p = 0 keeps everything.
+ * Errors: EINVAL for nulls, a negative n, misalignment, p outside [0, 1], or
+ * out overlapping x or the residual without being it.
+ */
+ZERO_API zero_status zero_dropout(const void* x, const void* residual, void* out, int64_t n, zero_dtype dt,
+                                  const zero_drop* drop, void* stream);
+
+/*
+ * zero_token_logp -- log-probability of each row's label.
+ *   max[t]  = max_j logits[t, j]
+ *   sum[t]  = log sum_j exp(logits[t, j] - max[t])
+ *   logp[t] = (logits[t, label[t]] - max[t]) - sum[t]
+ *   logits      n rows of `vocab` elements, `stride` elements apart.
+ *   labels      device array of n ids; a row whose label lies outside
+ *               [0, vocab) is not scored: its logits are not read, and its
+ *               logp and stats are 0.
+ *   logp        device fp32[n].
+ *   stats       device fp32[2 * n]: max[t] and sum[t] of row t, side by side
+ *               (kept apart, since their sum in fp32 loses the small one where
+ *               logits are large).
+ *   workspace, ws_bytes  zero_token_logp_workspace_bytes(n, vocab) bytes,
+ *               16-byte aligned (few rows are split over the GPU).
+ * -inf logits (masked ids) count as probability 0; a row of nothing else, and
+ * a row with NaN or +inf, gives logp NaN, as the formula does.
+ * Errors: EINVAL for nulls, n < 0, vocab < 1, a short stride, misalignment, a
+ * short workspace or overlapping buffers; EUNSUPPORTED for vocab above 2^30 or
+ * n above 2^31 - 1.
+ */
+ZERO_API size_t zero_token_logp_workspace_bytes(int64_t n, int64_t vocab);
+ZERO_API zero_status zero_token_logp(const void* logits, zero_dtype dt, int64_t n, int64_t vocab, int64_t stride,
+                                     const void* labels, zero_itype label_it, float* logp, float* stats,
+                                     void* workspace, size_t ws_bytes, void* stream);
+
+/*
+ * zero_preference_loss -- the paired preference loss of n_pairs pairs of
+ * sequences (direct preference optimisation), and its derivative by each
+ * row's logp.
+ *   reward[s] = beta * sum over the scored rows t of sequence s of
+ *               (logp[t] - ref_logp[t])
+ *   h_i       = reward[i] - reward[n_pairs + i]
+ *   pair_loss[i] = -(1 - smoothing) log sigmoid(h_i) - smoothing log sigmoid(-h_i)
+ *   loss      = mean of pair_loss (0 for no pairs)
+ *   coef[t]   = grad_scale * d loss / d logp[t]
+ * The sums over a sequence are fp64.
+ *   offsets     device array of 2 * n_pairs + 1 row numbers, ascending:
+ *               sequence s holds the rows [offsets[s], offsets[s + 1]), the
+ *               chosen ones first, then the rejected ones in the same order.
+ *               Row numbers are held to [0, n].  An empty sequence has
+ *               reward 0.
+ *   labels, vocab  as in zero_token_logp: a row whose label lies outside
+ *               [0, vocab) counts for nothing, whatever its logp and ref_logp
+ *               hold, and its coef is 0.  labels may be NULL: every row
+ *               counts.
+ *   logp, ref_logp  device fp32[n]; ref_logp may be NULL (zero).
+ *   grad_scale  loss scale of the backward pass, 1 for none; zero_adam_step's
+ *               grad_scale takes it out again.
+ *   loss[1], pair_loss[n_pairs], rewards[2 * n_pairs], coef[n]  device fp32.
+ *               coef of rows in no sequence is 0.
+ * Errors: EINVAL for nulls, negative sizes, smoothing outside [0, 1], a
+ * non-finite beta or grad_scale, misalignment or overlapping buffers;
+ * EUNSUPPORTED for n_pairs above 2^29 or n above 2^31 - 1.
+ */
+ZERO_API zero_status zero_preference_loss(int64_t n_pairs, const void* offsets, zero_itype offset_it, int64_t n,
+                                          const void* labels, zero_itype label_it, int64_t vocab,
+                                          const float* logp, const float* ref_logp, double beta,
+                                          double smoothing, double grad_scale, float* loss, float* pair_loss,
+                                          float* rewards, float* coef, void* stream);
+
+/*
+ * zero_token_logp_grad -- gradient of the logits from the derivative by logp.
+ *   dlogits[t, j] = coef[t] * ((j == label[t]) - exp((logits[t, j] - max[t]) - sum[t]))
+ *   stats       what zero_token_logp wrote.
+ *   coef        device fp32[n]; a row that is not scored, or whose coef is 0,
+ *               gives a row of zeros and its logits are not read.
+ *   dlogits     n rows, dl_stride elements apart, the logits' type; it may be
+ *               the logits buffer itself (with the same stride).
+ * Errors: as zero_token_logp, and EINVAL for dlogits overlapping the logits
+ * without being them.
+ */
+ZERO_API zero_status zero_token_logp_grad(const void* logits, zero_dtype dt, int64_t n, int64_t vocab,
+                                          int64_t stride, const void* labels, zero_itype label_it,
+                                          const float* stats, const float* coef, void* dlogits,
+                                          int64_t dl_stride, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -1,0 +1,195 @@
+"""The operators at the model's two ends, without a GPU: the refusals of the C
+entries and of the binding (all before anything is launched), the workspace
+sizes, and the plain forms the GPU tests compare with against each other."""
+import ctypes
+import math
+
+import numpy as np
+import pytest
+
+from tests import ops_reference as R
+
+BASE = 1 << 40        # fake addresses, never dereferenced
+GIB = 1 << 30
+
+
+def P(i):
+    return BASE + i * 64 * GIB
+
+
+@pytest.fixture()
+def Z(zero_lib):
+    return zero_lib
+
+
+def _drop(Z, p=0.1, first=0, step_dev=0):
+    return ctypes.byref(Z._Drop(p, 1, 2, 3, step_dev or None, first))
+
+
+def _embed(Z, plan, tensor=1, hidden=8, params=P(0), pdt=2, tokens=P(1), it=1, n=10, scale=1.0, drop=None,
+           out=P(2), odt=2, stride=8):
+    return Z.load().zero_embed(plan.handle if plan else None, tensor, hidden, params, pdt, tokens, it, n, scale,
+                               drop, out, odt, stride, None)
+
+
+def test_embed_refuses(Z):
+    p = Z.zero_plan(805, 2, [5, 800], 0, 8)
+    bad = [dict(tensor=2), dict(tensor=-1), dict(hidden=0), dict(hidden=7, stride=7), dict(params=0), dict(tokens=0),
+           dict(out=0), dict(n=-1), dict(pdt=3), dict(odt=-1), dict(it=2), dict(stride=7), dict(scale=math.inf),
+           dict(scale=math.nan), dict(params=P(0) + 1), dict(tokens=P(1) + 4), dict(tokens=P(1) + 2, it=0),
+           dict(out=P(2) + 2, odt=0), dict(out=P(0) + 16), dict(out=P(1) + 8), dict(stride=1 << 60),
+           dict(drop=_drop(Z, 1.1)), dict(drop=_drop(Z, -0.1)), dict(drop=_drop(Z, math.nan)),
+           dict(drop=_drop(Z, first=-1)), dict(drop=_drop(Z, first=(1 << 63) - 1)), dict(drop=_drop(Z, step_dev=BASE + 4))]
+    for kw in bad:
+        assert _embed(Z, p, **kw) == Z.ZERO_EINVAL, kw
+        assert Z.zero_last_error()
+    assert _embed(Z, None) == Z.ZERO_EINVAL
+    wide = Z.zero_plan(1 << 25, 1, [1 << 25], 0, 1)
+    assert _embed(Z, wide, tensor=0, hidden=1 << 25, stride=1 << 25) == Z.ZERO_EUNSUPPORTED
+    many = Z.zero_plan(1 << 32, 1, [1 << 32], 0, 1)
+    assert _embed(Z, many, tensor=0, hidden=1, stride=1) == Z.ZERO_EUNSUPPORTED
+    assert _embed(Z, p, n=0) == Z.ZERO_OK                    # nothing to do, nothing launched
+    assert _embed(Z, p, n=0, tokens=0, out=0) == Z.ZERO_OK
+
+
+def _order(Z, tokens=P(0), it=1, n=10, rows=100, sorted=P(1), order=P(2), ws=P(3), ws_bytes=1 << 40):
+    return Z.load().zero_token_order(tokens, it, n, rows, sorted, order, ws, ws_bytes, None)
+
+
+def test_token_order_refuses(Z):
+    for kw in [dict(tokens=0), dict(sorted=0), dict(order=0), dict(n=-1), dict(rows=-1), dict(it=7),
+               dict(tokens=P(0) + 4), dict(sorted=P(1) + 2), dict(order=P(1) + 8), dict(sorted=P(0) + 16),
+               dict(n=9000, ws=0), dict(n=9000, ws_bytes=8), dict(n=9000, ws=P(3) + 8), dict(n=9000, ws=P(0) + 64)]:
+        assert _order(Z, **kw) == Z.ZERO_EINVAL, kw
+    assert _order(Z, n=(1 << 30) + 1) == Z.ZERO_EUNSUPPORTED
+    assert _order(Z, rows=(1 << 31) - 1) == Z.ZERO_EUNSUPPORTED
+    assert _order(Z, n=0, tokens=0, sorted=0, order=0, ws=0, ws_bytes=0) == Z.ZERO_OK
+
+
+def test_workspaces(Z):
+    assert Z.zero_token_order_workspace_bytes(0, 10) == 0
+    assert Z.zero_token_order_workspace_bytes(8192, 50257) == 0           # ranked by counting
+    assert Z.zero_token_order_workspace_bytes(8192, 1 << 20) > 0
+    assert Z.zero_token_order_workspace_bytes(1 << 20, 50257) >= 8 << 20  # one more copy of tokens and positions
+    assert Z.zero_token_order_workspace_bytes(-1, 10) == 0
+    assert Z.zero_embed_grad_workspace_bytes(0, 768) == 0
+    for n, h in ((1, 1), (1000, 65), (65536, 8192), (1 << 20, 768)):
+        b = Z.zero_embed_grad_workspace_bytes(n, h)
+        assert 8 * h <= b <= 8 * h * (n // 8 + 1)
+    assert Z.zero_token_logp_workspace_bytes(0, 10) == 0
+    assert Z.zero_token_logp_workspace_bytes(4096, 131072) == 0
+    assert Z.zero_token_logp_workspace_bytes(2, 131072) == 2 * 16 * 8
+
+
+def _grad(Z, plan, tensor=1, hidden=8, sorted=P(0), order=P(1), n=10, dy=P(2), ydt=2, stride=8, scale=1.0, drop=None,
+          dst=P(3), ddt=2, rank=-1, acc=0, ws=P(4), ws_bytes=1 << 30):
+    return Z.load().zero_embed_grad(plan.handle if plan else None, tensor, hidden, sorted, order, n, dy, ydt, stride,
+                                    scale, drop, dst, ddt, rank, acc, ws, ws_bytes, None)
+
+
+def test_embed_grad_refuses(Z):
+    p = Z.zero_plan(805, 2, [5, 800], 0, 8)
+    for kw in [dict(tensor=2), dict(hidden=3, stride=3), dict(sorted=0), dict(order=0), dict(dy=0), dict(dst=0),
+               dict(n=-1), dict(ydt=9), dict(ddt=9), dict(stride=7), dict(scale=math.inf), dict(rank=2),
+               dict(acc=2), dict(acc=-1), dict(ws=0), dict(ws_bytes=16), dict(ws=P(4) + 8), dict(dst=P(2) + 16),
+               dict(dst=P(0) + 16), dict(ws=P(3) + 16), dict(ws=P(2) + 16), dict(sorted=P(0) + 2),
+               dict(dst=P(3) + 1), dict(drop=_drop(Z, 2.0))]:
+        assert _grad(Z, p, **kw) == Z.ZERO_EINVAL, kw
+    assert _grad(Z, None) == Z.ZERO_EINVAL
+    assert _grad(Z, p, n=(1 << 30) + 1) == Z.ZERO_EUNSUPPORTED
+    # Nothing to write: the other owner's slice holds no part of the tensor, or
+    # nothing is added.
+    q = Z.zero_plan(8 + 1000, 2, [8, 1000], 8, 8)      # tensor 0 alone in its bucket: 4 padded to 8 a rank
+    assert _grad(Z, q, tensor=0, rank=1, n=0, sorted=0, order=0, dy=0, ws=0, ws_bytes=0) == Z.ZERO_OK
+    assert _grad(Z, p, n=0, acc=1, sorted=0, order=0, dy=0, ws=0, ws_bytes=0) == Z.ZERO_OK
+
+
+def test_dropout_refuses(Z):
+    L = Z.load()
+
+    def call(x=P(0), res=0, out=P(1), n=100, dt=2, drop=True):
+        return L.zero_dropout(x, res, out, n, dt, _drop(Z) if drop is True else drop, None)
+    for kw in [dict(x=0), dict(out=0), dict(n=-1), dict(dt=5), dict(drop=None), dict(drop=_drop(Z, 1.5)),
+               dict(out=P(0) + 2), dict(res=P(1) + 2), dict(x=P(0) + 1), dict(res=P(2) + 1), dict(n=1 << 62)]:
+        assert call(**kw) == Z.ZERO_EINVAL, kw
+    assert call(n=0) == Z.ZERO_OK
+
+
+def test_token_logp_refuses(Z):
+    L = Z.load()
+
+    def logp(x=P(0), dt=2, n=4, v=100, stride=100, lab=P(1), it=1, lp=P(2), st=P(3), ws=P(4), wb=1 << 30):
+        return L.zero_token_logp(x, dt, n, v, stride, lab, it, lp, st, ws, wb, None)
+    for kw in [dict(x=0), dict(lab=0), dict(lp=0), dict(st=0), dict(n=-1), dict(v=0), dict(stride=99), dict(dt=4),
+               dict(it=3), dict(x=P(0) + 1), dict(lab=P(1) + 4), dict(lp=P(3) + 8), dict(st=P(0) + 64),
+               dict(stride=1 << 60), dict(v=1 << 17, stride=1 << 17, ws=0), dict(v=1 << 17, stride=1 << 17, wb=7)]:
+        assert logp(**kw) == Z.ZERO_EINVAL, kw
+    assert logp(v=(1 << 30) + 1, stride=1 << 31) == Z.ZERO_EUNSUPPORTED
+    assert logp(n=1 << 31) == Z.ZERO_EUNSUPPORTED
+    assert logp(n=0) == Z.ZERO_OK
+
+    def grad(x=P(0), dt=2, n=4, v=100, stride=100, lab=P(1), it=1, st=P(2), co=P(3), d=P(4), ds=100):
+        return L.zero_token_logp_grad(x, dt, n, v, stride, lab, it, st, co, d, ds, None)
+    for kw in [dict(x=0), dict(lab=0), dict(st=0), dict(co=0), dict(d=0), dict(ds=99), dict(d=P(0) + 2),
+               dict(d=P(0), ds=101), dict(d=P(2) + 4), dict(v=0), dict(n=-1), dict(dt=3)]:
+        assert grad(**kw) == Z.ZERO_EINVAL, kw
+    assert grad(n=0) == Z.ZERO_OK
+
+
+def test_preference_loss_refuses(Z):
+    L = Z.load()
+
+    def call(pairs=2, off=P(0), oit=1, n=50, lab=P(1), lit=1, v=10, lp=P(2), ref=P(3), beta=0.1, eps=0.0, gs=1.0,
+             loss=P(4), pl=P(5), rw=P(6), co=P(7)):
+        return L.zero_preference_loss(pairs, off, oit, n, lab, lit, v, lp, ref, beta, eps, gs, loss, pl, rw, co, None)
+    for kw in [dict(pairs=-1), dict(off=0), dict(oit=4), dict(n=-1), dict(lit=4), dict(v=0), dict(lp=0),
+               dict(beta=math.nan), dict(gs=math.inf), dict(eps=-0.1), dict(eps=1.5), dict(loss=0), dict(pl=0),
+               dict(rw=0), dict(co=0), dict(co=P(2)), dict(rw=P(5) + 4), dict(loss=P(6)), dict(off=P(0) + 4),
+               dict(co=P(3) + 4), dict(ref=P(3) + 2)]:
+        assert call(**kw) == Z.ZERO_EINVAL, kw
+    assert call(pairs=(1 << 29) + 1) == Z.ZERO_EUNSUPPORTED
+    assert call(n=1 << 31) == Z.ZERO_EUNSUPPORTED
+
+
+def test_binding_refuses(Z, monkeypatch):
+    """The binding's own checks, on CPU tensors: no C call is made."""
+    import torch
+    p = Z.zero_plan(805, 2, [5, 800], 0, 8)
+    monkeypatch.setattr(Z, "load", lambda: (_ for _ in ()).throw(AssertionError("the C library was called")))
+    ids, f = torch.zeros(10, dtype=torch.int64), torch.empty
+    with pytest.raises(ValueError, match="not on a GPU"):
+        Z.zero_embed(p, 1, 8, 1 << 40, Z.ZERO_BF16, ids, 1.0, 1 << 41, Z.ZERO_BF16, stream=0)
+    with pytest.raises(ValueError, match="int32 or int64"):
+        Z.zero_embed(p, 1, 8, 1 << 40, Z.ZERO_BF16, ids.short(), 1.0, 1 << 41, Z.ZERO_BF16, stream=0)
+    with pytest.raises(ValueError, match="pass its count"):
+        Z.zero_embed(p, 1, 8, 1 << 40, Z.ZERO_BF16, 1 << 42, 1.0, 1 << 41, Z.ZERO_BF16, stream=0)
+    with pytest.raises(ValueError, match="10 rows of 8"):
+        Z.zero_embed(p, 1, 8, 1 << 40, Z.ZERO_BF16, 1 << 42, 1.0, f(81, dtype=torch.bfloat16), Z.ZERO_BF16, stream=0,
+                     n=10, token_it=Z.ZERO_I64)
+    with pytest.raises(ValueError, match="bytes"):
+        Z.zero_dropout(f(10), None, f(10), Z.ZERO_BF16, Z.Drop(0.1, 1), stream=0)
+    with pytest.raises(TypeError, match="Drop"):
+        Z.zero_dropout(1 << 40, None, 1 << 41, Z.ZERO_BF16, 0.1, stream=0, n=8)
+    with pytest.raises(ValueError, match="not on a GPU"):
+        Z.Drop(0.1, 1, step_dev=torch.zeros(1, dtype=torch.int64))
+
+
+def test_reference_masks_agree():
+    """The vectorised mask against plain integers, at every offset in a word
+    and far out; the share dropped is within 4 standard deviations."""
+    for first in (0, 1, 2, 3, 6, (1 << 34) + 3):
+        a = R.mask_block(5, 6, 7, 0.3, first, 41)
+        assert np.array_equal(a, R.keep_mask(5, 6, 7, 0.3, range(first, first + 41)))
+    n = 1 << 18
+    share = 1 - R.mask_block(9, 0, 0, 0.1, 0, n).mean()
+    p = R.cut_of(0.1) / 65536
+    assert abs(share - p) < 4 * math.sqrt(p * (1 - p) / n)
+
+
+def test_reference_preference_by_hand():
+    """One pair of one-row sequences: h = beta (a - b), loss log(1 + e^-h)."""
+    loss, pair, rewards, coef = R.preference(np.array([0, 1, 2]), np.array([True, True]), np.array([-1.0, -2.0]),
+                                             None, 0.5, 0.0, 1.0)
+    assert abs(loss - math.log(1 + math.exp(-0.5))) < 1e-15
+    assert np.allclose(rewards, [-0.5, -1.0])
+    assert np.allclose(coef, np.array([-1, 1]) * 0.5 / (1 + math.exp(0.5)))

@@ -26,6 +26,7 @@ HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(HERE, "libzero.so")
 
 ZERO_F32, ZERO_F16, ZERO_BF16 = 0, 1, 2
+ZERO_I32, ZERO_I64 = 0, 1
 ZERO_OK, ZERO_EINVAL, ZERO_EUNSUPPORTED, ZERO_ENOMEM, ZERO_EHIP = 0, -1, -2, -3, -4
 ZERO_MAX_RANKS = 128
 
@@ -36,7 +37,11 @@ STATUS_NAMES = {0: "ZERO_OK", -1: "ZERO_EINVAL", -2: "ZERO_EUNSUPPORTED", -3: "Z
 ENTRY_POINTS = ("zero_version", "zero_last_error", "zero_plan", "zero_plan_destroy",
                 "zero_plan_info", "zero_plan_bucket", "zero_plan_tensor", "zero_flatten_workspace_bytes",
                 "zero_flatten", "zero_shard_reduce", "zero_adam_step", "zero_gather_pack", "zero_reshard",
-                "zero_set_write_window", "zero_set_stream_write_window", "zero_set_warm_read")
+                "zero_set_write_window", "zero_set_stream_write_window", "zero_set_warm_read",
+                "zero_embed", "zero_token_order_workspace_bytes", "zero_token_order",
+                "zero_embed_grad_workspace_bytes", "zero_embed_grad", "zero_dropout",
+                "zero_token_logp_workspace_bytes", "zero_token_logp", "zero_preference_loss",
+                "zero_token_logp_grad")
 
 
 class ZeroError(RuntimeError):
@@ -53,6 +58,11 @@ class _AdamHyper(ctypes.Structure):
 class _GradSrc(ctypes.Structure):
     _fields_ = [("dtype", ctypes.c_int32), ("n", ctypes.c_int32),
                 ("ptrs", ctypes.POINTER(ctypes.c_void_p)), ("is_full", ctypes.POINTER(ctypes.c_uint8))]
+
+
+class _Drop(ctypes.Structure):
+    _fields_ = [("p", ctypes.c_double), ("seed", ctypes.c_uint64), ("site", ctypes.c_uint64),
+                ("step", ctypes.c_uint64), ("step_dev", ctypes.c_void_p), ("first", ctypes.c_int64)]
 
 
 _lib = None
@@ -114,6 +124,29 @@ def load():
     L.zero_set_stream_write_window.argtypes = [vp, i64, i64]
     L.zero_set_warm_read.restype = i32
     L.zero_set_warm_read.argtypes = [i32]
+    f64, size = ctypes.c_double, ctypes.c_size_t
+    p_drop = ctypes.POINTER(_Drop)
+    L.zero_embed.restype = i32
+    L.zero_embed.argtypes = [vp, i32, i64, vp, i32, vp, i32, i64, f64, p_drop, vp, i32, i64, vp]
+    L.zero_token_order_workspace_bytes.restype = size
+    L.zero_token_order_workspace_bytes.argtypes = [i64, i64]
+    L.zero_token_order.restype = i32
+    L.zero_token_order.argtypes = [vp, i32, i64, i64, vp, vp, vp, size, vp]
+    L.zero_embed_grad_workspace_bytes.restype = size
+    L.zero_embed_grad_workspace_bytes.argtypes = [i64, i64]
+    L.zero_embed_grad.restype = i32
+    L.zero_embed_grad.argtypes = [vp, i32, i64, vp, vp, i64, vp, i32, i64, f64, p_drop, vp, i32, i32, i32, vp,
+                                  size, vp]
+    L.zero_dropout.restype = i32
+    L.zero_dropout.argtypes = [vp, vp, vp, i64, i32, p_drop, vp]
+    L.zero_token_logp_workspace_bytes.restype = size
+    L.zero_token_logp_workspace_bytes.argtypes = [i64, i64]
+    L.zero_token_logp.restype = i32
+    L.zero_token_logp.argtypes = [vp, i32, i64, i64, i64, vp, i32, vp, vp, vp, size, vp]
+    L.zero_preference_loss.restype = i32
+    L.zero_preference_loss.argtypes = [i64, vp, i32, i64, vp, i32, i64, vp, vp, f64, f64, f64, vp, vp, vp, vp, vp]
+    L.zero_token_logp_grad.restype = i32
+    L.zero_token_logp_grad.argtypes = [vp, i32, i64, i64, i64, vp, i32, vp, vp, vp, i64, vp]
     _lib = L
     return L
 
@@ -387,3 +420,264 @@ def zero_reshard(src_plan: Plan, dst_plan: Plan, dst_rank: int, src_shards: Sequ
     arr = _arg_list(src_shards, "src_shards", src_plan.n_d, es, src_plan.shard_total)
     out = _arg(dst_shard, "dst_shard", es, dst_plan.shard_total)
     _check(load().zero_reshard(src_plan.handle, dst_plan.handle, dst_rank, arr, dt, out, _stream(stream)))
+
+
+# ---------------------------------------------------------------------------
+# Operators at the two ends of the model (see include/zero.h)
+# ---------------------------------------------------------------------------
+#
+# Tensors are checked as above.  2-D arguments may have rows further apart than
+# they are wide (a slice of a wider activation); a contiguous tensor of any
+# shape with n * width elements is taken as n rows.  A call whose tensors lie
+# on another GPU than the current one is issued there, on that GPU's current
+# stream unless a stream is passed.  Where addresses are passed as integers,
+# the keyword arguments give what a tensor would tell.
+
+class Drop:
+    """Which elements a dropout keeps (zero_drop): the share dropped, and the
+    numbers that the mask follows from.  step_dev, an int64 or uint64 tensor
+    of one element on the GPU (or its address), is read when the kernel runs
+    in place of step."""
+
+    def __init__(self, p: float, seed: int, site: int = 0, step: int = 0, first: int = 0, step_dev=None):
+        mask = (1 << 64) - 1
+        self._keep = step_dev
+        addr = _arg(step_dev, "step_dev", 8, 1)
+        self.c = _Drop(p, seed & mask, site & mask, step & mask, addr or None, first)
+
+
+class _Call:
+    """The device and stream of one call, gathered from its tensors."""
+
+    def __init__(self, stream):
+        self.stream, self.device = stream, None
+
+    def see(self, x, name: str) -> None:
+        if x is None or isinstance(x, int):
+            return
+        if not x.is_cuda:
+            raise ValueError(f"{name} is not on a GPU ({x.device})")
+        i = x.device.index
+        if self.device is None:
+            self.device = i
+        elif self.device != i:
+            raise ValueError(f"{name} is on cuda:{i}, other arguments on cuda:{self.device}")
+
+    def flat(self, x, name: str, esize: int, need: int, optional: bool = False) -> int:
+        """Address of a contiguous buffer of at least need elements."""
+        if x is None and not optional and need > 0:
+            raise ValueError(f"{name} is None")
+        if x is None or isinstance(x, int):
+            return _addr(x)
+        addr = _arg(x, name, esize, need)
+        self.see(x, name)
+        return addr
+
+    def rows(self, x, name: str, esize: int, n: int, width: int, stride):
+        """(address, row stride) of n rows of width elements."""
+        if x is None:
+            if n > 0:
+                raise ValueError(f"{name} is None")
+            return 0, width
+        if isinstance(x, int):
+            return x, width if stride is None else stride
+        if not hasattr(x, "data_ptr") or not hasattr(x, "element_size"):
+            raise TypeError(f"{name}: expected a torch tensor or an integer device address, got {type(x).__name__}")
+        if x.element_size() != esize:
+            raise ValueError(f"{name}: elements of {x.element_size()} bytes ({x.dtype}), expected {esize}")
+        if x.numel() != n * width:
+            raise ValueError(f"{name} holds {x.numel()} elements, expected {n} rows of {width}")
+        self.see(x, name)
+        if x.is_contiguous():
+            return int(x.data_ptr()), width
+        if x.dim() != 2 or x.shape[1] != width or (width > 1 and x.stride(1) != 1) or (n > 1 and x.stride(0) < width):
+            raise ValueError(f"{name}: rows must be contiguous (shape {tuple(x.shape)}, strides {x.stride()})")
+        return int(x.data_ptr()), int(x.stride(0)) if n > 1 else width
+
+    def ids(self, x, name: str, n, it):
+        """(address, integer type, count) of an id list."""
+        if x is None or isinstance(x, int):
+            if n is None or it is None:
+                raise ValueError(f"{name} is not a tensor: pass its count and integer type")
+            return _addr(x), it, int(n)
+        if not hasattr(x, "data_ptr") or not hasattr(x, "element_size"):
+            raise TypeError(f"{name}: expected a torch tensor or an integer device address, got {type(x).__name__}")
+        kinds = {"torch.int32": ZERO_I32, "torch.int64": ZERO_I64}
+        if str(x.dtype) not in kinds:
+            raise ValueError(f"{name} must be int32 or int64, got {x.dtype}")
+        if not x.is_contiguous():
+            raise ValueError(f"{name} is not contiguous")
+        self.see(x, name)
+        if n is not None and int(n) != x.numel():
+            raise ValueError(f"{name} holds {x.numel()} elements, expected {n}")
+        return int(x.data_ptr()), kinds[str(x.dtype)], int(x.numel())
+
+    def workspace(self, x, need: int):
+        """(address, bytes); an integer address is taken to hold what is needed."""
+        if x is None or isinstance(x, int):
+            return _addr(x), need if x else 0
+        if not hasattr(x, "data_ptr") or not x.is_contiguous():
+            raise ValueError("workspace must be a contiguous tensor or an integer device address")
+        self.see(x, "workspace")
+        return int(x.data_ptr()), int(x.numel() * x.element_size())
+
+    def drop(self, d):
+        if d is None:
+            return None
+        if not isinstance(d, Drop):
+            raise TypeError(f"drop: expected a Drop, got {type(d).__name__}")
+        self.see(d._keep, "step_dev")
+        return ctypes.byref(d.c)
+
+    def issue(self, name: str, *args) -> None:
+        fn = getattr(load(), name)
+        if self.device is None:
+            _check(fn(*args, _stream(self.stream)))
+            return
+        import torch
+        if torch.cuda.current_device() == self.device:
+            _check(fn(*args, _stream(self.stream)))
+        else:
+            with torch.cuda.device(self.device):
+                _check(fn(*args, _stream(self.stream)))
+
+
+def zero_embed(plan: Plan, tensor: int, hidden: int, params, param_dt: int, tokens, scale: float, out, out_dt: int,
+               drop: Optional[Drop] = None, stream=None, n: Optional[int] = None, token_it: Optional[int] = None,
+               out_stride: Optional[int] = None) -> None:
+    """out[i] = dropout(scale * table[tokens[i]]); the table is a tensor of the
+    plan inside the full parameter buffer params.  Ids outside the table give
+    rows of zeros."""
+    c = _Call(stream)
+    par = c.flat(params, "params", _esize(param_dt), plan.psi_pad)
+    tok, it, n = c.ids(tokens, "tokens", n, token_it)
+    o, ostride = c.rows(out, "out", _esize(out_dt), n, hidden, out_stride)
+    c.issue("zero_embed", plan.handle, tensor, hidden, par, param_dt, tok, it, n, scale, c.drop(drop), o, out_dt,
+            ostride)
+
+
+def zero_token_order_workspace_bytes(n: int, rows: int) -> int:
+    return int(load().zero_token_order_workspace_bytes(n, rows))
+
+
+def zero_token_order(tokens, rows: int, sorted, order, workspace=None, stream=None, n: Optional[int] = None,
+                     token_it: Optional[int] = None) -> None:
+    """Positions of the tokens in token order (order, int32) and the tokens in
+    that order (sorted, int32; padding ids last, as rows)."""
+    c = _Call(stream)
+    tok, it, n = c.ids(tokens, "tokens", n, token_it)
+    s = c.flat(sorted, "sorted", 4, n)
+    o = c.flat(order, "order", 4, n)
+    ws, ws_bytes = c.workspace(workspace, zero_token_order_workspace_bytes(n, rows))
+    c.issue("zero_token_order", tok, it, n, rows, s, o, ws, ws_bytes)
+
+
+def zero_embed_grad_workspace_bytes(n: int, hidden: int) -> int:
+    return int(load().zero_embed_grad_workspace_bytes(n, hidden))
+
+
+def zero_embed_grad(plan: Plan, tensor: int, hidden: int, sorted, order, dy, dy_dt: int, scale: float, dst,
+                    dst_dt: int, drop: Optional[Drop] = None, rank: int = -1, accumulate: bool = False,
+                    workspace=None, stream=None, n: Optional[int] = None, dy_stride: Optional[int] = None) -> None:
+    """Gradient of zero_embed's table into the full flat gradient buffer dst,
+    or with rank >= 0 into the compact slice that this owner receives."""
+    c = _Call(stream)
+    if n is None:
+        if sorted is None or isinstance(sorted, int):
+            raise ValueError("sorted is not a tensor: pass n")
+        n = int(sorted.numel())
+    s = c.flat(sorted, "sorted", 4, n)
+    o = c.flat(order, "order", 4, n)
+    y, ystride = c.rows(dy, "dy", _esize(dy_dt), n, hidden, dy_stride)
+    d = c.flat(dst, "dst", _esize(dst_dt), plan.psi_pad if rank < 0 else plan.shard_total)
+    ws, ws_bytes = c.workspace(workspace, zero_embed_grad_workspace_bytes(n, hidden))
+    c.issue("zero_embed_grad", plan.handle, tensor, hidden, s, o, n, y, dy_dt, ystride, scale, c.drop(drop), d,
+            dst_dt, rank, 1 if accumulate else 0, ws, ws_bytes)
+
+
+def zero_dropout(x, residual, out, dt: int, drop: Drop, stream=None, n: Optional[int] = None) -> None:
+    """out = residual + dropout(x) (residual may be None; out may be x or the
+    residual).  The backward pass is the same call on the gradient."""
+    c = _Call(stream)
+    if n is None:
+        if x is None or isinstance(x, int):
+            raise ValueError("x is not a tensor: pass n")
+        n = int(x.numel())
+    es = _esize(dt)
+    xa = c.flat(x, "x", es, n)
+    ra = c.flat(residual, "residual", es, n, optional=True)
+    oa = c.flat(out, "out", es, n)
+    c.issue("zero_dropout", xa, ra, oa, n, dt, c.drop(drop))
+
+
+def zero_token_logp_workspace_bytes(n: int, vocab: int) -> int:
+    return int(load().zero_token_logp_workspace_bytes(n, vocab))
+
+
+def _vocab(logits, vocab: Optional[int]) -> int:
+    if vocab is not None:
+        return int(vocab)
+    if logits is None or isinstance(logits, int):
+        raise ValueError("logits is not a tensor: pass vocab")
+    return int(logits.shape[-1])
+
+
+def zero_token_logp(logits, dt: int, labels, logp, stats, workspace=None, stream=None, n: Optional[int] = None,
+                    vocab: Optional[int] = None, stride: Optional[int] = None,
+                    label_it: Optional[int] = None) -> None:
+    """logp[t] = log softmax(logits[t])[labels[t]]; stats[2 t], stats[2 t + 1]
+    are the row's maximum and the log of its sum relative to it.  Rows whose
+    label lies outside the vocabulary are not scored (0)."""
+    c = _Call(stream)
+    v = _vocab(logits, vocab)
+    lab, it, n = c.ids(labels, "labels", n, label_it)
+    x, xstride = c.rows(logits, "logits", _esize(dt), n, v, stride)
+    lp = c.flat(logp, "logp", 4, n)
+    st = c.flat(stats, "stats", 4, 2 * n)
+    ws, ws_bytes = c.workspace(workspace, zero_token_logp_workspace_bytes(n, v))
+    c.issue("zero_token_logp", x, dt, n, v, xstride, lab, it, lp, st, ws, ws_bytes)
+
+
+def zero_preference_loss(offsets, labels, vocab: int, logp, ref_logp, beta: float, smoothing: float,
+                         grad_scale: float, loss, pair_loss, rewards, coef, stream=None,
+                         n_pairs: Optional[int] = None, n: Optional[int] = None,
+                         offset_it: Optional[int] = None, label_it: Optional[int] = None) -> None:
+    """Paired preference loss of the sequences that offsets bounds (the chosen
+    ones, then the rejected ones), and coef[t] = grad_scale * dloss/dlogp[t]."""
+    c = _Call(stream)
+    off, oit, n_off = c.ids(offsets, "offsets", None if n_pairs is None else 2 * n_pairs + 1, offset_it)
+    if n_off % 2 == 0:
+        raise ValueError(f"offsets holds {n_off} entries, expected 2 * n_pairs + 1")
+    pairs = n_off // 2
+    if n is None:
+        if logp is None or isinstance(logp, int):
+            raise ValueError("logp is not a tensor: pass n")
+        n = int(logp.numel())
+    if labels is None:
+        lab, lit = 0, ZERO_I64
+    else:
+        lab, lit, _ = c.ids(labels, "labels", n, label_it)
+    lp = c.flat(logp, "logp", 4, n)
+    ref = c.flat(ref_logp, "ref_logp", 4, n, optional=True)
+    lo = c.flat(loss, "loss", 4, 1)
+    pl = c.flat(pair_loss, "pair_loss", 4, pairs)
+    rw = c.flat(rewards, "rewards", 4, 2 * pairs)
+    co = c.flat(coef, "coef", 4, n)
+    c.issue("zero_preference_loss", pairs, off, oit, n, lab, lit, vocab, lp, ref, beta, smoothing, grad_scale, lo,
+            pl, rw, co)
+
+
+def zero_token_logp_grad(logits, dt: int, labels, stats, coef, dlogits, stream=None, n: Optional[int] = None,
+                         vocab: Optional[int] = None, stride: Optional[int] = None,
+                         dl_stride: Optional[int] = None, label_it: Optional[int] = None) -> None:
+    """dlogits[t] = coef[t] * (onehot(labels[t]) - softmax(logits[t])); rows
+    that are not scored are zero.  dlogits may be the logits themselves."""
+    c = _Call(stream)
+    v = _vocab(logits, vocab)
+    lab, it, n = c.ids(labels, "labels", n, label_it)
+    es = _esize(dt)
+    x, xstride = c.rows(logits, "logits", es, n, v, stride)
+    st = c.flat(stats, "stats", 4, 2 * n)
+    co = c.flat(coef, "coef", 4, n)
+    d, dstride = c.rows(dlogits, "dlogits", es, n, v, dl_stride)
+    c.issue("zero_token_logp_grad", x, dt, n, v, xstride, lab, it, st, co, d, dstride)

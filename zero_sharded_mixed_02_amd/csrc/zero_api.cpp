@@ -7,9 +7,7 @@
 // buckets).  Nothing here allocates device memory; every kernel receives its
 // tables in its kernel arguments, split over several launches when a plan has
 // more pieces than one argument block holds.
-#include <stdarg.h>
 #include <stdint.h>
-#include <stdio.h>
 #include <string.h>
 
 #include <algorithm>
@@ -17,71 +15,18 @@
 #include <cmath>
 #include <mutex>
 #include <new>
-#include <string>
 #include <utility>
 #include <vector>
 
 #include "zero.h"
+#include "zero_host.h"
 #include "zero_internal.h"
 
 #define ZERO_VERSION_NUMBER 200  // 0.2.0
 
-struct zero_plan_s {
-  int64_t psi = 0;
-  int32_t n_d = 1;
-  int64_t bucket_cap = 0;
-  int32_t align = 1;
-  int64_t psi_pad = 0;
-  int64_t shard_total = 0;
-  struct Bucket {
-    int64_t flat_off, numel, padded, shard_numel, shard_off;
-  };
-  std::vector<Bucket> buckets;
-  std::vector<int64_t> t_numel;
-  std::vector<int64_t> t_off;
-  std::vector<int32_t> t_bucket;
-};
+using namespace zk::host;
 
 namespace {
-
-thread_local std::string g_err;
-
-zero_status fail(zero_status st, const char* fmt, ...) {
-  char buf[512];
-  va_list ap;
-  va_start(ap, fmt);
-  vsnprintf(buf, sizeof buf, fmt, ap);
-  va_end(ap);
-  g_err = buf;
-  return st;
-}
-
-zero_status ok() { return ZERO_OK; }
-
-int esize(int dt) { return dt == ZERO_F32 ? 4 : 2; }
-bool is16(int dt) { return dt == ZERO_F16 || dt == ZERO_BF16; }
-bool valid_dt(int dt) { return dt == ZERO_F32 || dt == ZERO_F16 || dt == ZERO_BF16; }
-
-struct Range {
-  uint64_t lo, hi;  // [lo, hi) bytes
-  const char* what;
-};
-
-Range range_of(const void* p, int64_t elems, int es, const char* what) {
-  const uint64_t lo = (uint64_t)(uintptr_t)p;
-  return Range{lo, lo + (uint64_t)elems * (uint64_t)es, what};
-}
-
-bool overlap(const Range& a, const Range& b) {
-  if (a.hi == a.lo || b.hi == b.lo) return false;
-  return a.lo < b.hi && b.lo < a.hi;
-}
-
-bool aligned(const void* p, int bytes) { return ((uintptr_t)p % (uintptr_t)bytes) == 0; }
-
-zero_status hip_fail(int err) {
-  return fail(ZERO_EHIP, "HIP launch failed: %s (%d)", zk::hip_error_string(err), err);
-}
 
 // The nine fp32 constants of step t, rounded once from fp64.
 void adam_consts(const zero_adam_hyper& h, int64_t t, float c[9]) {
@@ -320,11 +265,6 @@ zero_status check_src(const zero_plan_s& p, const zero_grad_src* src, std::vecto
     if (!aligned(g, 8)) vec_ok = false;   // the vector kernel loads 4 elements (8 bytes) per rank
     reads.push_back(range_of(g, n, 2, "gradient"));
   }
-  return ok();
-}
-
-zero_status check_plan(zero_plan_t p) {
-  if (!p) return fail(ZERO_EINVAL, "plan is NULL");
   return ok();
 }
 

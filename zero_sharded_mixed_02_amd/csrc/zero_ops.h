@@ -1,0 +1,177 @@
+// zero_ops.h -- structures shared by the host entries (zero_ops_api.cpp) and
+// the gfx950 kernels (zero_ops.hip) of the vocabulary operators.
+#pragma once
+
+#include <stdint.h>
+
+#include "zero.h"
+
+namespace zk {
+namespace ops {
+
+// SplitMix64's increment and output function (Steele, Lea & Flood, OOPSLA 2014).
+constexpr uint64_t kGamma = 0x9E3779B97F4A7C15ull;
+constexpr uint64_t kMix1 = 0xBF58476D1CE4E5B9ull;
+constexpr uint64_t kMix2 = 0x94D049BB133111EBull;
+
+// A dropout as the kernels take it.
+struct DropArgs {
+  uint64_t key;               // of the mask, when step_dev is NULL
+  uint64_t site_key;          // key before the step is mixed in
+  const uint64_t* step_dev;   // step read on the device, or NULL
+  int64_t first;              // mask position of the call's first element
+  uint32_t cut;               // 16-bit draws below it are dropped; 0: keep all
+  uint32_t pad_;
+};
+
+struct EmbedArgs {
+  const void* table;
+  const void* tokens;
+  void* out;
+  int64_t n;
+  int64_t out_stride;
+  int32_t rows;
+  int32_t hidden;
+  int32_t upr;       // units of one access per row
+  int32_t tok64;     // tokens are int64
+  float f;
+  int32_t pad_;
+  DropArgs drop;
+};
+
+// Sorting tokens: positions are ranked by counting when there are few, and by
+// radix passes of at most kDigitBits bits otherwise.
+constexpr int kSmallSort = 8192;         // most positions ranked by counting
+constexpr int kSmallSortPosBits = 13;
+constexpr int kRankThreads = 1024;
+constexpr int kRankItems = 32;           // positions ranked per workgroup
+constexpr int kDigitBits = 9;
+constexpr int kBins = 1 << kDigitBits;
+constexpr int kSortThreads = 512;        // also one thread per bin
+constexpr int kSortKeys = 8;             // keys per thread and tile
+constexpr int kSortTile = kSortThreads * kSortKeys;
+constexpr int kSortBlocks = 256;         // most workgroups of a pass
+
+struct RankArgs {
+  const void* tokens;
+  int32_t* sorted;
+  int32_t* order;
+  int32_t n;
+  int32_t rows;
+  int32_t tok64;
+};
+
+struct RadixArgs {
+  const void* tokens;       // first pass: ids
+  const int32_t* key_in;    // later passes
+  const int32_t* pos_in;
+  int32_t* key_out;
+  int32_t* pos_out;
+  uint32_t* hist;           // [n_blocks][kBins]
+  int64_t n;
+  int32_t rows;
+  int32_t tok64;
+  int32_t first;            // reads tokens
+  int32_t shift;
+  int32_t bits;
+  int32_t n_blocks;
+  int64_t tiles_per_block;
+};
+
+// Gradient of the table: positions in token order are cut into chunks of
+// `chunk`; see zero_ops.hip.
+constexpr int kGradThreads = 256;
+constexpr int kJoinThreads = 512;
+constexpr int kJoinTile = 256;           // columns of a wave in the join
+
+struct GradArgs {
+  const int32_t* sorted;
+  const int32_t* order;
+  const void* dy;
+  void* dst;               // element lo of the tensor
+  float* part;             // [2 * n_chunks][hidden]
+  int64_t n;
+  int64_t dy_stride;
+  int64_t lo, hi;          // elements of the tensor that are written
+  int32_t row_lo, row_hi;  // rows they lie in
+  int32_t rows;
+  int32_t hidden;
+  int32_t chunk;
+  int32_t n_chunks;
+  int32_t tiles;           // column tiles of the chunk kernel
+  int32_t fill_rows;       // rows of one zero-fill workgroup
+  int32_t accumulate;
+  float f;
+  int64_t chunk_blocks;    // workgroups before the fill workgroups
+  DropArgs drop;
+};
+
+struct DropoutArgs {
+  const void* x;
+  const void* residual;
+  void* out;
+  int64_t n;
+  float f;
+  int32_t pad_;
+  DropArgs drop;
+};
+
+constexpr int kLogpThreads = 512;
+constexpr int kDlogitsThreads = 256;
+
+struct LogpArgs {
+  const void* logits;
+  const void* labels;
+  float* logp;
+  float* stats;
+  float* part;        // [n][splits][2] when splits > 1
+  const float* coef;  // gradient
+  void* dlogits;
+  int64_t n;
+  int64_t stride;
+  int64_t dl_stride;
+  int32_t vocab;
+  int32_t lab64;
+  int32_t splits;     // workgroups per row
+  int32_t pad_;
+};
+
+constexpr int kPrefThreads = 1024;
+
+struct PrefArgs {
+  const void* offsets;
+  const void* labels;      // or NULL
+  const float* logp;
+  const float* ref;        // or NULL
+  float* loss;
+  float* pair_loss;
+  float* rewards;
+  float* coef;
+  int64_t n;
+  int64_t n_pairs;
+  int64_t vocab;
+  double beta, smoothing, slope;   // slope = beta * grad_scale / n_pairs
+  int32_t off64;
+  int32_t lab64;
+};
+
+// Launchers (zero_ops.hip).  Return a hipError_t as int.
+int launch_embed(const EmbedArgs& a, int tdt, int odt, bool vec, int64_t blocks, void* stream);
+int launch_rank(const RankArgs& a, int64_t blocks, void* stream);
+int launch_radix(const RadixArgs& a, void* stream);
+int launch_grad(const GradArgs& a, int ydt, int gdt, int vec, int64_t blocks, void* stream);
+int launch_grad_join(const GradArgs& a, int gdt, bool vec, void* stream);
+int launch_dropout(const DropoutArgs& a, int dt, int64_t blocks, void* stream);
+int launch_logp(const LogpArgs& a, int dt, void* stream);
+int launch_logp_join(const LogpArgs& a, int dt, void* stream);
+int launch_dlogits(const LogpArgs& a, int dt, void* stream);
+int launch_preference(const PrefArgs& a, void* stream);
+
+// Elements of one access of the embedding kernels: 16 bytes of a 16-bit
+// buffer, or four elements where an fp32 buffer takes part.
+constexpr int vec_of(int a, int b) { return a == ZERO_F32 || b == ZERO_F32 ? 4 : 8; }
+constexpr int kUnroll = 4;        // units per thread of the streaming kernels
+constexpr int kStreamThreads = 256;
+
+}  // namespace ops
+}  // namespace zk

@@ -1,0 +1,1080 @@
+// zero_ops.hip -- gfx950 kernels of the vocabulary operators: embedding lookup
+// and its gradient, dropout, token log-probabilities and the paired preference
+// loss.
+//
+// None of them is a contraction: each reads its inputs once, does a few fp32
+// operations per element and writes its outputs once, so HBM bounds the large
+// calls and launch latency the small ones.  Rows start at any element offset
+// (a table behind an odd-sized tensor, a vocabulary of odd size), so accesses
+// are 16 bytes wide at element alignment, which gfx950 takes from global
+// memory at any address; where a row's length is no multiple of an access, its
+// last access is moved back to end with the row.
+//
+// Floating point: compiled with -ffp-contract=off; fused multiply-adds are
+// written out where they are meant.
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include <type_traits>
+
+#include "zero_internal.h"
+#include "zero_ops.h"
+
+#pragma clang fp contract(off)
+
+namespace zk {
+namespace ops {
+namespace {
+
+#define AS1 __attribute__((address_space(1)))
+
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+// The same at element alignment.
+typedef uint32_t u32x4h __attribute__((ext_vector_type(4), aligned(2)));
+typedef uint32_t u32x2h __attribute__((ext_vector_type(2), aligned(2)));
+typedef uint32_t u32x4w __attribute__((ext_vector_type(4), aligned(4)));
+
+constexpr float kLog2eHi = 1.44269504f;                                   // fp32(log2 e)
+constexpr float kLog2eLo = (float)(1.4426950408889634 - (double)kLog2eHi);
+
+__device__ __forceinline__ float neg_inf() { return -__builtin_inff(); }
+
+// ---------------------------------------------------------------------------
+// Elements
+// ---------------------------------------------------------------------------
+
+template <int DT>
+constexpr int es_of = DT == ZERO_F32 ? 4 : 2;
+
+template <int DT>
+__device__ __forceinline__ float widen(uint32_t h) {
+  if constexpr (DT == ZERO_F32) return __uint_as_float(h);
+  else if constexpr (DT == ZERO_BF16) return __uint_as_float(h << 16);
+  else return (float)__builtin_bit_cast(_Float16, (uint16_t)h);
+}
+
+// fp32 -> element, round to nearest even (the one rounding of every operator).
+template <int DT>
+__device__ __forceinline__ uint32_t narrow(float x) {
+  if constexpr (DT == ZERO_F32) return __float_as_uint(x);
+  else if constexpr (DT == ZERO_BF16) return __builtin_bit_cast(uint16_t, (__bf16)x);
+  else return __builtin_bit_cast(uint16_t, (_Float16)x);
+}
+
+// N consecutive elements as they lie in memory.
+template <int DT, int N>
+struct Raw {
+  static constexpr int kWords = N * es_of<DT> >= 4 ? N * es_of<DT> / 4 : 1;
+  uint32_t w[kWords];
+};
+
+template <int DT, int N>
+__device__ __forceinline__ uint64_t at(const void* base, int64_t e) {
+  return (uint64_t)(uintptr_t)base + (uint64_t)(e * es_of<DT>);
+}
+
+template <int DT, int N, bool NT = false>
+__device__ __forceinline__ Raw<DT, N> load(const void* base, int64_t e) {
+  Raw<DT, N> r;
+  const uint64_t p = at<DT, N>(base, e);
+  constexpr int bytes = N * es_of<DT>;
+  if constexpr (bytes == 2) {
+    r.w[0] = *(const AS1 uint16_t*)p;
+  } else if constexpr (bytes == 4) {
+    r.w[0] = *(const AS1 uint32_t*)p;
+  } else if constexpr (bytes == 8) {
+    const u32x2 v = NT ? __builtin_nontemporal_load((const AS1 u32x2h*)p) : *(const AS1 u32x2h*)p;
+    r.w[0] = v[0];
+    r.w[1] = v[1];
+  } else {
+    static_assert(bytes == 16, "access size");
+    const u32x4 v = NT ? __builtin_nontemporal_load((const AS1 u32x4h*)p) : *(const AS1 u32x4h*)p;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) r.w[i] = v[i];
+  }
+  return r;
+}
+
+template <int DT, int N, bool NT = false>
+__device__ __forceinline__ void store(void* base, int64_t e, const Raw<DT, N>& r) {
+  const uint64_t p = at<DT, N>(base, e);
+  constexpr int bytes = N * es_of<DT>;
+  if constexpr (bytes == 2) {
+    *(AS1 uint16_t*)p = (uint16_t)r.w[0];
+  } else if constexpr (bytes == 4) {
+    *(AS1 uint32_t*)p = r.w[0];
+  } else if constexpr (bytes == 8) {
+    const u32x2 v = {r.w[0], r.w[1]};
+    if (NT) __builtin_nontemporal_store(v, (AS1 u32x2h*)p);
+    else *(AS1 u32x2h*)p = v;
+  } else {
+    static_assert(bytes == 16, "access size");
+    const u32x4 v = {r.w[0], r.w[1], r.w[2], r.w[3]};
+    if (NT) __builtin_nontemporal_store(v, (AS1 u32x4h*)p);
+    else *(AS1 u32x4h*)p = v;
+  }
+}
+
+template <int DT, int N>
+__device__ __forceinline__ void to_float(const Raw<DT, N>& r, float (&x)[N]) {
+  if constexpr (DT == ZERO_F32 || N == 1) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) x[i] = widen<DT>(r.w[i]);
+  } else {
+#pragma unroll
+    for (int i = 0; i < N / 2; ++i) {
+      x[2 * i] = DT == ZERO_BF16 ? widen<DT>(r.w[i]) : widen<DT>(r.w[i] & 0xffffu);
+      x[2 * i + 1] = DT == ZERO_BF16 ? __uint_as_float(r.w[i] & 0xffff0000u) : widen<DT>(r.w[i] >> 16);
+    }
+  }
+}
+
+template <int DT, int N>
+__device__ __forceinline__ Raw<DT, N> from_float(const float (&x)[N]) {
+  Raw<DT, N> r;
+  if constexpr (DT == ZERO_F32 || N == 1) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) r.w[i] = narrow<DT>(x[i]);
+  } else {
+#pragma unroll
+    for (int i = 0; i < N / 2; ++i) r.w[i] = narrow<DT>(x[2 * i]) | (narrow<DT>(x[2 * i + 1]) << 16);
+  }
+  return r;
+}
+
+__device__ __forceinline__ int64_t load_id(const void* p, int64_t i, int wide) {
+  return wide ? ((const AS1 int64_t*)(uintptr_t)p)[i] : (int64_t)((const AS1 int32_t*)(uintptr_t)p)[i];
+}
+
+// The table row an id names, or `rows` for a padding id.
+__device__ __forceinline__ int32_t row_of(int64_t id, int32_t rows) {
+  return (uint64_t)id < (uint64_t)rows ? (int32_t)id : rows;
+}
+
+// ---------------------------------------------------------------------------
+// Dropout's mask
+// ---------------------------------------------------------------------------
+
+__device__ __forceinline__ uint64_t mix64(uint64_t z) {
+  z = (z ^ (z >> 30)) * kMix1;
+  z = (z ^ (z >> 27)) * kMix2;
+  return z ^ (z >> 31);
+}
+
+__device__ __forceinline__ uint64_t mask_key(const DropArgs& d) {
+  return d.step_dev ? mix64((d.site_key ^ *(const AS1 uint64_t*)(uintptr_t)d.step_dev) + kGamma) : d.key;
+}
+
+// Zeroes the dropped ones among N elements whose first stands at mask position
+// e.  One mix64 gives four elements 16 bits each, so a group that starts
+// inside a word takes one word more and shifts.  16 bits an element and not
+// 32 halve the generator's work, which at 32 bits would be as long as the
+// memory traffic of a 16-bit tensor; p is a multiple of 2^-16 for it.
+template <int N>
+__device__ __forceinline__ void drop(float (&x)[N], uint64_t key, int64_t e, uint32_t cut) {
+  const uint64_t z = key + (uint64_t)((e >> 2) + 1) * kGamma;
+  const uint32_t off = ((uint32_t)e & 3u) * 16u;
+  constexpr int W = (N + 3) / 4;
+  uint64_t w[W];
+#pragma unroll
+  for (int i = 0; i < W; ++i) w[i] = mix64(z + (uint64_t)i * kGamma);
+  if (off) {
+    if constexpr (N > 1) {
+      const uint64_t last = mix64(z + (uint64_t)W * kGamma);
+#pragma unroll
+      for (int i = 0; i < W; ++i) w[i] = (w[i] >> off) | ((i + 1 < W ? w[i + 1] : last) << (64 - off));
+    } else {
+      w[0] >>= off;
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    const uint32_t draw = (uint32_t)(w[i / 4] >> (16 * (i % 4))) & 0xffffu;
+    x[i] = draw >= cut ? x[i] : 0.0f;
+  }
+}
+
+// ---------------------------------------------------------------------------
+// Embedding lookup
+// ---------------------------------------------------------------------------
+
+// A thread owns kUnroll accesses of N elements, kStreamThreads accesses apart,
+// numbered row by row through the output.
+template <int TDT, int ODT, int N>
+__global__ __launch_bounds__(kStreamThreads) void embed_kernel(const EmbedArgs a) {
+  const int64_t u0 = (int64_t)blockIdx.x * (kStreamThreads * kUnroll);
+  const int64_t row0 = u0 / a.upr;
+  const uint32_t rem0 = (uint32_t)(u0 - row0 * a.upr);
+  const uint64_t key = a.drop.cut ? mask_key(a.drop) : 0;
+  int64_t row[kUnroll];
+  int32_t col[kUnroll], id[kUnroll];
+#pragma unroll
+  for (int j = 0; j < kUnroll; ++j) {
+    const uint32_t t = rem0 + j * kStreamThreads + threadIdx.x;
+    const uint32_t r = t / (uint32_t)a.upr;
+    row[j] = row0 + r;
+    const int32_t c = (int32_t)(t - r * (uint32_t)a.upr) * N;
+    col[j] = c < a.hidden - N ? c : a.hidden - N;   // the last access ends with the row
+    id[j] = row[j] < a.n ? row_of(load_id(a.tokens, row[j], a.tok64), a.rows) : a.rows;
+  }
+  Raw<TDT, N> raw[kUnroll];
+  if (a.rows > 0) {
+#pragma unroll
+    for (int j = 0; j < kUnroll; ++j)
+      raw[j] = load<TDT, N>(a.table, (int64_t)(id[j] < a.rows ? id[j] : 0) * a.hidden + col[j]);
+  } else {
+#pragma unroll
+    for (int j = 0; j < kUnroll; ++j) raw[j] = Raw<TDT, N>{};
+  }
+#pragma unroll
+  for (int j = 0; j < kUnroll; ++j) {
+    if (row[j] >= a.n) continue;
+    float x[N];
+    to_float<TDT, N>(raw[j], x);
+#pragma unroll
+    for (int i = 0; i < N; ++i) x[i] = id[j] < a.rows ? x[i] * a.f : 0.0f;
+    if (a.drop.cut) drop<N>(x, key, a.drop.first + row[j] * a.hidden + col[j], a.drop.cut);
+    store<ODT, N>(a.out, row[j] * a.out_stride + col[j], from_float<ODT, N>(x));
+  }
+}
+
+// ---------------------------------------------------------------------------
+// Token order
+// ---------------------------------------------------------------------------
+
+// Few positions: the place of position i is the number of positions whose
+// (token, position) is smaller, counted outright: n^2 comparisons of one word
+// that holds both, all over the chip, in one launch.
+__global__ __launch_bounds__(kRankThreads) void rank_kernel(const RankArgs a) {
+  __shared__ uint4 word4[kSmallSort / 4];
+  __shared__ int count[kRankItems];
+  uint32_t* word = (uint32_t*)word4;
+  constexpr int kSegs = kRankThreads / kRankItems;
+  const int padded = (a.n + 4 * kSegs - 1) / (4 * kSegs) * (4 * kSegs);
+  for (int i = threadIdx.x; i < padded; i += kRankThreads)
+    word[i] = i < a.n ? ((uint32_t)row_of(load_id(a.tokens, i, a.tok64), a.rows) << kSmallSortPosBits) | (uint32_t)i
+                      : 0xffffffffu;
+  if (threadIdx.x < kRankItems) count[threadIdx.x] = 0;
+  __syncthreads();
+  const int item = threadIdx.x % kRankItems, seg = threadIdx.x / kRankItems;
+  const int i = blockIdx.x * kRankItems + item;
+  const uint32_t mine = i < a.n ? word[i] : 0;
+  const int len = padded / kSegs / 4;
+  const uint4* w = word4 + seg * len;
+  int c = 0;
+#pragma unroll 4
+  for (int j = 0; j < len; ++j) {
+    const uint4 v = w[j];
+    c += (v.x < mine) + (v.y < mine) + (v.z < mine) + (v.w < mine);
+  }
+  atomicAdd(&count[item], c);
+  __syncthreads();
+  if (threadIdx.x < kRankItems && i < a.n) {
+    const int place = count[item];
+    a.sorted[place] = (int32_t)(mine >> kSmallSortPosBits);
+    a.order[place] = i;
+  }
+}
+
+__device__ __forceinline__ void radix_read(const RadixArgs& a, int64_t i, int32_t& key, int32_t& pos) {
+  if (a.first) {
+    key = row_of(load_id(a.tokens, i, a.tok64), a.rows);
+    pos = (int32_t)i;
+  } else {
+    key = a.key_in[i];
+    pos = a.pos_in[i];
+  }
+}
+
+// One stable pass by `bits` bits of the token.  Each workgroup owns a run of
+// tiles; this counts its digits.
+__global__ __launch_bounds__(kSortThreads) void radix_count_kernel(const RadixArgs a) {
+  __shared__ uint32_t bin[kBins];
+  bin[threadIdx.x] = 0;
+  __syncthreads();
+  const uint32_t mask = (1u << a.bits) - 1;
+  const int64_t lo = (int64_t)blockIdx.x * a.tiles_per_block * kSortTile;
+  int64_t hi = lo + a.tiles_per_block * kSortTile;
+  if (hi > a.n) hi = a.n;
+  for (int64_t i = lo + threadIdx.x; i < hi; i += kSortThreads) {
+    int32_t key, pos;
+    radix_read(a, i, key, pos);
+    atomicAdd(&bin[((uint32_t)key >> a.shift) & mask], 1u);
+  }
+  __syncthreads();
+  a.hist[(int64_t)blockIdx.x * kBins + threadIdx.x] = bin[threadIdx.x];
+}
+
+// ... and this moves its positions.  A digit's place is the count of smaller
+// digits, plus the same digit in earlier workgroups, plus its rank in this
+// one.  In a tile each wave owns 64 * kSortKeys consecutive positions and takes
+// them 64 at a time: lanes of the same digit find each other with one ballot
+// per bit, and rank themselves by lane, so equal tokens keep their order.
+__global__ __launch_bounds__(kSortThreads) void radix_move_kernel(const RadixArgs a) {
+  constexpr int kWaves = kSortThreads / 64;
+  __shared__ uint32_t base[kBins];               // next place of each digit
+  __shared__ uint32_t scan[kWaves];
+  __shared__ uint32_t cnt[kWaves][kBins];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  {
+    uint32_t before = 0, total = 0;
+    for (int b = 0; b < a.n_blocks; ++b) {
+      const uint32_t h = a.hist[(int64_t)b * kBins + threadIdx.x];
+      before += b < (int)blockIdx.x ? h : 0;
+      total += h;
+    }
+    uint32_t inc = total;
+#pragma unroll
+    for (int d = 1; d < 64; d <<= 1) {
+      const uint32_t v = __shfl_up(inc, d);
+      if (lane >= d) inc += v;
+    }
+    if (lane == 63) scan[wave] = inc;
+    __syncthreads();
+    uint32_t prev = 0;
+    for (int w = 0; w < wave; ++w) prev += scan[w];
+    base[threadIdx.x] = prev + inc - total + before;
+  }
+  const uint32_t mask = (1u << a.bits) - 1;
+  const int64_t tile0 = (int64_t)blockIdx.x * a.tiles_per_block;
+  for (int64_t t = 0; t < a.tiles_per_block; ++t) {
+    const int64_t lo = (tile0 + t) * kSortTile;
+    if (lo >= a.n) break;   // uniform
+#pragma unroll
+    for (int w = 0; w < kWaves; ++w) cnt[w][threadIdx.x] = 0;
+    __syncthreads();
+    int32_t key[kSortKeys], pos[kSortKeys];
+    uint32_t rank[kSortKeys];
+    const int64_t first = lo + wave * (64 * kSortKeys) + lane;
+#pragma unroll
+    for (int k = 0; k < kSortKeys; ++k) {
+      const int64_t i = first + k * 64;
+      key[k] = pos[k] = 0;
+      if (i < a.n) radix_read(a, i, key[k], pos[k]);
+    }
+#pragma unroll
+    for (int k = 0; k < kSortKeys; ++k) {
+      const bool in = first + k * 64 < a.n;
+      const uint32_t d = ((uint32_t)key[k] >> a.shift) & mask;
+      uint64_t same = __ballot(in);
+      for (int b = 0; b < a.bits; ++b) {
+        const bool bit = (d >> b) & 1u;
+        const uint64_t set = __ballot(bit);
+        same &= bit ? set : ~set;
+      }
+      const uint32_t below = __popcll(same & ((1ull << lane) - 1));
+      const uint32_t old = cnt[wave][d];
+      rank[k] = old + below;
+      __builtin_amdgcn_wave_barrier();
+      __threadfence_block();
+      if (in && below == 0) cnt[wave][d] = old + __popcll(same);
+      __threadfence_block();
+      __builtin_amdgcn_wave_barrier();
+    }
+    __syncthreads();
+    uint32_t run = base[threadIdx.x];
+#pragma unroll
+    for (int w = 0; w < kWaves; ++w) {
+      const uint32_t c = cnt[w][threadIdx.x];
+      cnt[w][threadIdx.x] = run;
+      run += c;
+    }
+    base[threadIdx.x] = run;
+    __syncthreads();
+#pragma unroll
+    for (int k = 0; k < kSortKeys; ++k) {
+      if (first + k * 64 >= a.n) continue;
+      const uint32_t d = ((uint32_t)key[k] >> a.shift) & mask;
+      const int64_t place = (int64_t)cnt[wave][d] + rank[k];
+      if (place < a.n) {
+        a.key_out[place] = key[k];
+        a.pos_out[place] = pos[k];
+      }
+    }
+    __syncthreads();
+  }
+}
+
+// ---------------------------------------------------------------------------
+// Gradient of the table
+// ---------------------------------------------------------------------------
+//
+// The positions in token order are cut into chunks of equal length, whatever
+// their tokens, so that a token that makes up half a batch costs no more than
+// rare ones.  A wave owns one chunk and one tile of columns and sums its runs
+// of equal tokens in fp32 registers.  A run inside a chunk is finished there.
+// One that crosses a boundary leaves a partial row (fp32, in the workspace) in
+// each chunk it touches: slot 2c of chunk c if it came in from the chunk
+// before, slot 2c + 1 if it begins in c and goes on; the join kernel adds
+// those up in order.  Further workgroups of the same launch write zeros to the
+// rows that no token names.
+
+// First index in [0, n) whose sorted token is >= key (n if none), found by a
+// whole wave, 64 probes at a time.
+__device__ __forceinline__ int64_t wave_lower_bound(const int32_t* sorted, int64_t n, int64_t key) {
+  const int lane = threadIdx.x & 63;
+  int64_t lo = 0, hi = n;
+  while (hi > lo) {
+    const int64_t step = (hi - lo + 63) / 64;
+    const int64_t i = lo + (lane + 1) * step - 1;
+    const uint64_t less = __ballot(i < hi && (int64_t)sorted[i < hi ? i : lo] < key);
+    lo += (int64_t)__popcll(less) * step;
+    if (lo > hi) lo = hi;
+    hi = hi < lo + step - 1 ? hi : lo + step - 1;
+  }
+  return lo;
+}
+
+// Writes N columns of a finished row; `begin` is the first column that this
+// lane owns (col < begin where its access was moved back).
+template <int GDT, int N>
+__device__ __forceinline__ void write_row(const GradArgs& a, int32_t row, int32_t col, int32_t begin,
+                                          const float (&sum)[N]) {
+  const int64_t e = (int64_t)row * a.hidden + col;
+  constexpr bool NT = N > 1;
+  if (e >= a.lo && e + N <= a.hi && (begin == col || !a.accumulate)) {
+    float x[N];
+    if (a.accumulate) {
+      float old[N];
+      to_float<GDT, N>(load<GDT, N>(a.dst, e - a.lo), old);
+#pragma unroll
+      for (int i = 0; i < N; ++i) x[i] = old[i] + sum[i] * a.f;
+    } else {
+#pragma unroll
+      for (int i = 0; i < N; ++i) x[i] = sum[i] * a.f;
+    }
+    store<GDT, N, NT>(a.dst, e - a.lo, from_float<GDT, N>(x));
+    return;
+  }
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    if (e + i < a.lo || e + i >= a.hi || col + i < begin) continue;
+    float x[1] = {sum[i] * a.f};
+    if (a.accumulate) {
+      float old[1];
+      to_float<GDT, 1>(load<GDT, 1>(a.dst, e + i - a.lo), old);
+      x[0] = old[0] + x[0];
+    }
+    store<GDT, 1>(a.dst, e + i - a.lo, from_float<GDT, 1>(x));
+  }
+}
+
+template <int N>
+__device__ __forceinline__ void write_part(const GradArgs& a, int64_t slot, int32_t col, const float (&sum)[N]) {
+  const int64_t e = slot * a.hidden + col;
+  if constexpr (N == 1) {
+    store<ZERO_F32, 1>(a.part, e, from_float<ZERO_F32, 1>(sum));
+  } else {
+#pragma unroll
+    for (int i = 0; i < N; i += 4) {
+      const float x[4] = {sum[i], sum[i + 1], sum[i + 2], sum[i + 3]};
+      store<ZERO_F32, 4>(a.part, e + i, from_float<ZERO_F32, 4>(x));
+    }
+  }
+}
+
+template <int GDT>
+__device__ void fill_rows(const GradArgs& a, int64_t block) {
+  __shared__ uint8_t named[1024];
+  constexpr int N = 16 / es_of<GDT>;
+  const int64_t r0 = a.row_lo + block * a.fill_rows;
+  int64_t r1 = r0 + a.fill_rows;
+  if (r1 > a.row_hi) r1 = a.row_hi;
+  const int64_t from = wave_lower_bound(a.sorted, a.n, r0);
+  const int64_t to = wave_lower_bound(a.sorted, a.n, r1);
+  for (int64_t r = r0 + threadIdx.x; r < r1; r += kGradThreads) {
+    int64_t lo = from, hi = to;
+    while (lo < hi) {
+      const int64_t mid = lo + (hi - lo) / 2;
+      if (a.sorted[mid] < r) lo = mid + 1;
+      else hi = mid;
+    }
+    named[r - r0] = lo < a.n && a.sorted[lo] == r;
+  }
+  __syncthreads();
+  const uint32_t upr = (uint32_t)(a.hidden + N - 1) / N;
+  const uint32_t units = (uint32_t)(r1 - r0) * upr;   // fill_rows keeps this small
+  for (uint32_t u = threadIdx.x; u < units; u += kGradThreads) {
+    const uint32_t r = u / upr;
+    if (named[r]) continue;
+    const int64_t row_e = (r0 + r) * a.hidden;
+    const int64_t e = row_e + (int64_t)(u - r * upr) * N;
+    const int64_t end = row_e + a.hidden < e + N ? row_e + a.hidden : e + N;
+    if (e + N <= end && e >= a.lo && e + N <= a.hi) {
+      store<GDT, N, true>(a.dst, e - a.lo, Raw<GDT, N>{});
+    } else {
+      for (int64_t i = e; i < end; ++i)
+        if (i >= a.lo && i < a.hi) store<GDT, 1>(a.dst, i - a.lo, Raw<GDT, 1>{});
+    }
+  }
+}
+
+template <int YDT, int GDT, int N, bool DROP>
+__global__ __launch_bounds__(kGradThreads) void grad_kernel(const GradArgs a) {
+  if ((int64_t)blockIdx.x >= a.chunk_blocks) {
+    fill_rows<GDT>(a, (int64_t)blockIdx.x - a.chunk_blocks);
+    return;
+  }
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
+  const int64_t w = (int64_t)blockIdx.x * (kGradThreads / 64) + wave;
+  const int64_t c = w / a.tiles;
+  if (c >= a.n_chunks) return;
+  const int32_t begin = ((int32_t)(w - c * a.tiles) * 64 + lane) * N;
+  const bool on = begin < a.hidden;
+  const int32_t col = begin < a.hidden - N ? begin : a.hidden - N;
+  const int64_t s = c * a.chunk;
+  const int64_t e = s + a.chunk < a.n ? s + a.chunk : a.n;
+  if (a.sorted[s] >= a.row_hi || a.sorted[e - 1] < a.row_lo) return;
+  const bool came_in = s > 0 && a.sorted[s - 1] == a.sorted[s];
+  const uint64_t key = DROP ? mask_key(a.drop) : 0;
+
+  float acc[N];
+  int32_t cur = a.sorted[s];
+  bool head = came_in;
+#pragma unroll
+  for (int i = 0; i < N; ++i) acc[i] = 0.0f;
+  constexpr int U = 8;
+  for (int64_t i0 = s; i0 < e; i0 += U) {
+    int32_t row[U], pos[U];
+    Raw<YDT, N> raw[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int64_t i = i0 + u < e ? i0 + u : e - 1;
+      row[u] = a.sorted[i];
+      pos[u] = a.order[i];
+      const bool good = (uint32_t)pos[u] < (uint64_t)a.n;
+      raw[u] = load<YDT, N>(a.dy, (int64_t)(good ? pos[u] : 0) * a.dy_stride + col);
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      if (i0 + u >= e) break;
+      if (row[u] != cur) {
+        if (on && cur >= a.row_lo && cur < a.row_hi) {
+          if (head) write_part<N>(a, 2 * c, col, acc);
+          else write_row<GDT, N>(a, cur, col, begin, acc);
+        }
+        head = false;
+        cur = row[u];
+#pragma unroll
+        for (int i = 0; i < N; ++i) acc[i] = 0.0f;
+      }
+      if ((uint32_t)pos[u] < (uint64_t)a.n) {
+        float x[N];
+        to_float<YDT, N>(raw[u], x);
+        if constexpr (DROP) drop<N>(x, key, a.drop.first + (int64_t)pos[u] * a.hidden + col, a.drop.cut);
+#pragma unroll
+        for (int i = 0; i < N; ++i) acc[i] += x[i];
+      }
+    }
+  }
+  if (!on || cur < a.row_lo || cur >= a.row_hi) return;
+  if (head) write_part<N>(a, 2 * c, col, acc);
+  else if (e < a.n && a.sorted[e] == cur) write_part<N>(a, 2 * c + 1, col, acc);
+  else write_row<GDT, N>(a, cur, col, begin, acc);
+}
+
+// Joins the run that begins in chunk blockIdx.x and goes on: its partial rows
+// in chunk order.  Short runs take one wave per tile of columns; long ones are
+// cut into eight pieces, one a wave, joined in order in shared memory.
+template <int GDT, int N>
+__global__ __launch_bounds__(kJoinThreads) void grad_join_kernel(const GradArgs a) {
+  constexpr int kWaves = kJoinThreads / 64;
+  __shared__ float piece[kWaves][64 * N];
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
+  const int64_t c = blockIdx.x;
+  const int64_t s = c * a.chunk, e = s + a.chunk;
+  if (e >= a.n) return;
+  const int32_t row = a.sorted[e - 1];
+  if (a.sorted[e] != row || row < a.row_lo || row >= a.row_hi) return;
+  if (s > 0 && a.sorted[s - 1] == row) return;   // began in an earlier chunk
+  // Chunks that the run comes into: those whose first token is still its.
+  const int64_t end = wave_lower_bound(a.sorted, a.n, (int64_t)row + 1);
+  const int64_t last = end > e ? (end - 1) / a.chunk : c;
+  const int64_t count = last - c + 1;            // partial rows
+  const int tiles = (a.hidden + 64 * N - 1) / (64 * N);
+  const bool split = count > 2 * kWaves;
+  const int64_t per = split ? (count + kWaves - 1) / kWaves : count;
+  for (int t0 = (int)blockIdx.y * kWaves; t0 < tiles && t0 < ((int)blockIdx.y + 1) * kWaves;
+       t0 += split ? 1 : kWaves) {
+    const int t = split ? t0 : t0 + wave;
+    const int32_t begin = (t * 64 + lane) * N;
+    const bool on = t < tiles && begin < a.hidden;
+    const int32_t col = begin < a.hidden - N ? begin : a.hidden - N;
+    const int64_t j0 = split ? wave * per : 0;
+    const int64_t j1 = j0 + per < count ? j0 + per : count;
+    float acc[N];
+#pragma unroll
+    for (int i = 0; i < N; ++i) acc[i] = 0.0f;
+    if (on) {
+#pragma unroll 4
+      for (int64_t j = j0; j < j1; ++j) {
+        const int64_t slot = j == 0 ? 2 * c + 1 : 2 * (c + j);
+        float x[N];
+        to_float<ZERO_F32, N>(load<ZERO_F32, N>(a.part, slot * a.hidden + col), x);
+#pragma unroll
+        for (int i = 0; i < N; ++i) acc[i] += x[i];
+      }
+    }
+    if (split) {
+#pragma unroll
+      for (int i = 0; i < N; ++i) piece[wave][lane * N + i] = acc[i];
+      __syncthreads();
+      if (wave == 0) {
+#pragma unroll
+        for (int v = 1; v < kWaves; ++v)
+#pragma unroll
+          for (int i = 0; i < N; ++i) acc[i] += piece[v][lane * N + i];
+      }
+      __syncthreads();
+    }
+    if (on && (!split || wave == 0)) write_row<GDT, N>(a, row, col, begin, acc);
+  }
+}
+
+// ---------------------------------------------------------------------------
+// Dropout
+// ---------------------------------------------------------------------------
+
+template <int DT, int N>
+__device__ __forceinline__ void dropout_one(const DropoutArgs& a, uint64_t key, int64_t e, const Raw<DT, N>& xr,
+                                            const Raw<DT, N>& rr) {
+  float x[N];
+  to_float<DT, N>(xr, x);
+  if (a.drop.cut) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) x[i] = x[i] * a.f;
+    drop<N>(x, key, a.drop.first + e, a.drop.cut);
+  }
+  if (a.residual) {
+    float r[N];
+    to_float<DT, N>(rr, r);
+#pragma unroll
+    for (int i = 0; i < N; ++i) x[i] = r[i] + x[i];
+  }
+  store<DT, N>(a.out, e, from_float<DT, N>(x));
+}
+
+template <int DT, int N>
+__global__ __launch_bounds__(kStreamThreads) void dropout_kernel(const DropoutArgs a) {
+  const uint64_t key = a.drop.cut ? mask_key(a.drop) : 0;
+  const int64_t e0 = ((int64_t)blockIdx.x * (kStreamThreads * kUnroll) + threadIdx.x) * N;
+  Raw<DT, N> x[kUnroll], r[kUnroll];
+#pragma unroll
+  for (int j = 0; j < kUnroll; ++j) {
+    const int64_t e = e0 + (int64_t)j * kStreamThreads * N;
+    r[j] = Raw<DT, N>{};
+    if (e + N <= a.n) {
+      x[j] = load<DT, N>(a.x, e);
+      if (a.residual) r[j] = load<DT, N>(a.residual, e);
+    }
+  }
+#pragma unroll
+  for (int j = 0; j < kUnroll; ++j) {
+    const int64_t e = e0 + (int64_t)j * kStreamThreads * N;
+    if (e + N <= a.n) {
+      dropout_one<DT, N>(a, key, e, x[j], r[j]);
+    } else {
+      for (int64_t i = e; i < a.n; ++i)   // fewer than N, in one thread
+        dropout_one<DT, 1>(a, key, i, load<DT, 1>(a.x, i),
+                           a.residual ? load<DT, 1>(a.residual, i) : Raw<DT, 1>{});
+    }
+  }
+}
+
+// ---------------------------------------------------------------------------
+// Token log-probabilities
+// ---------------------------------------------------------------------------
+
+// exp(z) for z <= 0 as 2^(z log2 e), log2 e in two parts: with the leading
+// part alone every term of a sum over the vocabulary would be off the same
+// way, by 1.3e-8 |z|.
+__device__ __forceinline__ float exp_of(float z) {
+  return __builtin_amdgcn_exp2f(__builtin_fmaf(z, kLog2eHi, z * kLog2eLo));
+}
+
+// A running maximum and the sum of exp(x - max), extended by K values.  The
+// maximum of nothing is -inf; it is not subtracted while it is (-inf - -inf).
+template <int K>
+__device__ __forceinline__ void absorb(const float (&x)[K], float& m, float& s) {
+  float top = x[0];
+#pragma unroll
+  for (int i = 1; i < K; ++i) top = __builtin_fmaxf(top, x[i]);
+  if (top > m) {
+    s = s * exp_of(m - top);
+    m = top;
+  }
+  const float base = m == neg_inf() ? 0.0f : m;
+  float part = 0.0f;
+#pragma unroll
+  for (int i = 0; i < K; ++i) part += exp_of(x[i] - base);
+  s += part;
+}
+
+// s of maximum m, as a share of the sum over the maximum top >= m.
+__device__ __forceinline__ float rebase(float m, float s, float top) {
+  return m == top || m == neg_inf() ? s : s * exp_of(m - top);
+}
+
+// Reduces (m, s) over the workgroup, in a fixed order; valid in thread 0.
+template <int THREADS>
+__device__ __forceinline__ void reduce_stats(float& m, float& s) {
+  constexpr int kWaves = THREADS / 64;
+  __shared__ float sm[kWaves], ss[kWaves];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  float top = m;
+#pragma unroll
+  for (int d = 32; d > 0; d >>= 1) top = __builtin_fmaxf(top, __shfl_xor(top, d));
+  s = rebase(m, s, top);
+#pragma unroll
+  for (int d = 32; d > 0; d >>= 1) s += __shfl_xor(s, d);
+  if (lane == 0) {
+    sm[wave] = top;
+    ss[wave] = s;
+  }
+  __syncthreads();
+  m = sm[0];
+#pragma unroll
+  for (int w = 1; w < kWaves; ++w) m = __builtin_fmaxf(m, sm[w]);
+  s = 0.0f;
+#pragma unroll
+  for (int w = 0; w < kWaves; ++w) s += rebase(sm[w], ss[w], m);
+}
+
+template <int DT>
+__device__ __forceinline__ void write_stats(const LogpArgs& a, int64_t t, int64_t label, float m, float s) {
+  const double ls = log((double)s);
+  float y[1];
+  to_float<DT, 1>(load<DT, 1>(a.logits, t * a.stride + label), y);
+  a.stats[2 * t] = m;
+  a.stats[2 * t + 1] = (float)ls;
+  a.logp[t] = (float)(((double)y[0] - (double)m) - ls);
+}
+
+// One row, or one of `splits` pieces of a row, per workgroup.  Loads are
+// aligned: the elements before the first 16-byte boundary of the row and
+// behind the last one are taken singly.
+template <int DT>
+__global__ __launch_bounds__(kLogpThreads) void logp_kernel(const LogpArgs a) {
+  constexpr int N = 16 / es_of<DT>;
+  constexpr int U = 4;
+  const int64_t t = blockIdx.x / (uint32_t)a.splits;
+  const int part = (int)(blockIdx.x - (uint32_t)t * (uint32_t)a.splits);
+  const int64_t label = load_id(a.labels, t, a.lab64);
+  if ((uint64_t)label >= (uint64_t)a.vocab) {
+    if (part == 0 && threadIdx.x == 0) {
+      a.stats[2 * t] = a.stats[2 * t + 1] = 0.0f;
+      a.logp[t] = 0.0f;
+    }
+    return;
+  }
+  const int64_t row = t * a.stride;
+  const uint32_t skew = (uint32_t)(at<DT, 1>(a.logits, row) & 15u);
+  int head = skew ? (int)(16 - skew) / es_of<DT> : 0;
+  if (head > a.vocab) head = a.vocab;
+  const int vecs = (a.vocab - head) / N;
+  const int tail = a.vocab - head - vecs * N;
+  const int per = (vecs + a.splits - 1) / a.splits;
+  const int v0 = part * per;
+  const int v1 = v0 + per < vecs ? v0 + per : vecs;
+  float m = neg_inf(), s = 0.0f;
+  const int tid = threadIdx.x;
+  int v = v0;
+  for (; v + U * kLogpThreads <= v1; v += U * kLogpThreads) {
+    float x[U * N];
+#pragma unroll
+    for (int j = 0; j < U; ++j) {
+      float y[N];
+      to_float<DT, N>(load<DT, N>(a.logits, row + head + (int64_t)(v + j * kLogpThreads + tid) * N), y);
+#pragma unroll
+      for (int i = 0; i < N; ++i) x[j * N + i] = y[i];
+    }
+    absorb<U * N>(x, m, s);
+  }
+  for (v += tid; v < v1; v += kLogpThreads) {
+    float x[N];
+    to_float<DT, N>(load<DT, N>(a.logits, row + head + (int64_t)v * N), x);
+    absorb<N>(x, m, s);
+  }
+  if (part == 0 && tid < head) {
+    float x[1];
+    to_float<DT, 1>(load<DT, 1>(a.logits, row + tid), x);
+    absorb<1>(x, m, s);
+  }
+  if (part == a.splits - 1 && tid < tail) {
+    float x[1];
+    to_float<DT, 1>(load<DT, 1>(a.logits, row + a.vocab - tail + tid), x);
+    absorb<1>(x, m, s);
+  }
+  reduce_stats<kLogpThreads>(m, s);
+  if (tid != 0) return;
+  if (a.splits > 1) {
+    a.part[2 * (int64_t)blockIdx.x] = m;
+    a.part[2 * (int64_t)blockIdx.x + 1] = s;
+  } else {
+    write_stats<DT>(a, t, label, m, s);
+  }
+}
+
+// Joins the pieces of each row: one thread per row.
+template <int DT>
+__global__ __launch_bounds__(64) void logp_join_kernel(const LogpArgs a) {
+  const int64_t t = (int64_t)blockIdx.x * 64 + threadIdx.x;
+  if (t >= a.n) return;
+  const int64_t label = load_id(a.labels, t, a.lab64);
+  if ((uint64_t)label >= (uint64_t)a.vocab) return;   // written by logp_kernel
+  const float* p = a.part + 2 * t * a.splits;
+  float m = neg_inf();
+  for (int k = 0; k < a.splits; ++k) m = __builtin_fmaxf(m, p[2 * k]);
+  float s = 0.0f;
+  for (int k = 0; k < a.splits; ++k) s += rebase(p[2 * k], p[2 * k + 1], m);
+  write_stats<DT>(a, t, label, m, s);
+}
+
+// Gradient of the logits: one piece of a row per workgroup.
+template <int DT>
+__global__ __launch_bounds__(kDlogitsThreads) void dlogits_kernel(const LogpArgs a) {
+  constexpr int N = 16 / es_of<DT>;
+  constexpr int U = 4;
+  const int64_t t = blockIdx.x / (uint32_t)a.splits;
+  const int part = (int)(blockIdx.x - (uint32_t)t * (uint32_t)a.splits);
+  const int64_t label = load_id(a.labels, t, a.lab64);
+  const bool scored = (uint64_t)label < (uint64_t)a.vocab;
+  const float coef = scored ? a.coef[t] : 0.0f;
+  const bool zero = coef == 0.0f;   // uniform over the workgroup
+  const float m = zero ? 0.0f : a.stats[2 * t], ls = zero ? 0.0f : a.stats[2 * t + 1];
+  const int64_t row = t * a.stride, drow = t * a.dl_stride;
+  const uint32_t skew = (uint32_t)(at<DT, 1>(a.logits, row) & 15u);
+  int head = skew ? (int)(16 - skew) / es_of<DT> : 0;
+  if (head > a.vocab) head = a.vocab;
+  const int vecs = (a.vocab - head) / N;
+  const int tail = a.vocab - head - vecs * N;
+  const int per = (vecs + a.splits - 1) / a.splits;
+  const int v0 = part * per;
+  const int v1 = v0 + per < vecs ? v0 + per : vecs;
+  const int tid = threadIdx.x;
+  auto grad = [&](float x, int j) {
+    const float p = exp_of((x - m) - ls);
+    return zero ? 0.0f : (j == (int)label ? coef * (1.0f - p) : -coef * p);
+  };
+  auto one = [&](int j) {
+    float x[1] = {0.0f};
+    if (!zero) to_float<DT, 1>(load<DT, 1>(a.logits, row + j), x);
+    x[0] = grad(x[0], j);
+    store<DT, 1>(a.dlogits, drow + j, from_float<DT, 1>(x));
+  };
+  for (int v = v0 + tid; v < v1; v += U * kDlogitsThreads) {
+    Raw<DT, N> raw[U];
+#pragma unroll
+    for (int j = 0; j < U; ++j) {
+      raw[j] = Raw<DT, N>{};
+      const int u = v + j * kDlogitsThreads;
+      if (!zero) raw[j] = load<DT, N, true>(a.logits, row + head + (int64_t)(u < v1 ? u : v) * N);
+    }
+#pragma unroll
+    for (int j = 0; j < U; ++j) {
+      const int u = v + j * kDlogitsThreads;
+      if (u >= v1) continue;
+      float x[N];
+      to_float<DT, N>(raw[j], x);
+      const int c = head + u * N;
+#pragma unroll
+      for (int i = 0; i < N; ++i) x[i] = grad(x[i], c + i);
+      store<DT, N, true>(a.dlogits, drow + c, from_float<DT, N>(x));
+    }
+  }
+  if (part == 0 && tid < head) one(tid);
+  if (part == a.splits - 1 && tid < tail) one(a.vocab - tail + tid);
+}
+
+// ---------------------------------------------------------------------------
+// Paired preference loss
+// ---------------------------------------------------------------------------
+
+__device__ __forceinline__ int64_t row_limit(const PrefArgs& a, int64_t i, int64_t floor_) {
+  int64_t v = load_id(a.offsets, i, a.off64);
+  if (v > a.n) v = a.n;
+  return v < floor_ ? floor_ : v;
+}
+
+__device__ __forceinline__ bool counts(const PrefArgs& a, int64_t t) {
+  return !a.labels || (uint64_t)load_id(a.labels, t, a.lab64) < (uint64_t)a.vocab;
+}
+
+// Sum over a sequence's scored rows, fp64, in an order fixed by its length;
+// valid in every thread.
+__device__ __forceinline__ double sum_sequence(const PrefArgs& a, int64_t lo, int64_t hi) {
+  __shared__ double part[kPrefThreads / 64];
+  double s = 0.0;
+  for (int64_t t = lo + threadIdx.x; t < hi; t += kPrefThreads)
+    if (counts(a, t)) s += (double)a.logp[t] - (a.ref ? (double)a.ref[t] : 0.0);
+#pragma unroll
+  for (int d = 32; d > 0; d >>= 1) s += __shfl_xor(s, d);
+  __syncthreads();   // the array's last readers are done
+  if ((threadIdx.x & 63) == 0) part[threadIdx.x >> 6] = s;
+  __syncthreads();
+  s = 0.0;
+  for (int w = 0; w < kPrefThreads / 64; ++w) s += part[w];
+  return s;
+}
+
+// -log sigmoid(h) = log(1 + e^-h)
+__device__ __forceinline__ double softplus_neg(double h) {
+  return h >= 0 ? log1p(exp(-h)) : log1p(exp(h)) - h;
+}
+
+// A pair per workgroup; one more writes the rows in no sequence.
+__global__ __launch_bounds__(kPrefThreads) void preference_kernel(const PrefArgs a) {
+  const int64_t i = blockIdx.x;
+  if (i == a.n_pairs) {
+    const int64_t lo = a.n_pairs ? row_limit(a, 0, 0) : a.n;
+    const int64_t hi = a.n_pairs ? row_limit(a, 2 * a.n_pairs, lo) : a.n;
+    for (int64_t t = threadIdx.x; t < lo; t += kPrefThreads) a.coef[t] = 0.0f;
+    for (int64_t t = hi + threadIdx.x; t < a.n; t += kPrefThreads) a.coef[t] = 0.0f;
+    return;
+  }
+  const int64_t j = a.n_pairs + i;
+  const int64_t c0 = row_limit(a, i, 0), c1 = row_limit(a, i + 1, c0);
+  const int64_t r0 = row_limit(a, j, 0), r1 = row_limit(a, j + 1, r0);
+  const double chosen = a.beta * sum_sequence(a, c0, c1);
+  const double rejected = a.beta * sum_sequence(a, r0, r1);
+  const double h = chosen - rejected;
+  if (threadIdx.x == 0) {
+    a.rewards[i] = (float)chosen;
+    a.rewards[j] = (float)rejected;
+    const double up = softplus_neg(h), down = softplus_neg(-h);
+    a.pair_loss[i] = (float)((a.smoothing < 1 ? (1.0 - a.smoothing) * up : 0.0) +
+                             (a.smoothing > 0 ? a.smoothing * down : 0.0));
+  }
+  const double sig = h >= 0 ? 1.0 / (1.0 + exp(-h)) : exp(h) / (1.0 + exp(h));       // sigmoid(h)
+  const double sig_neg = h >= 0 ? exp(-h) / (1.0 + exp(-h)) : 1.0 / (1.0 + exp(h));  // sigmoid(-h)
+  const float coef = (float)(a.slope * (a.smoothing * sig - (1.0 - a.smoothing) * sig_neg));
+  for (int64_t t = c0 + threadIdx.x; t < c1; t += kPrefThreads) a.coef[t] = counts(a, t) ? coef : 0.0f;
+  for (int64_t t = r0 + threadIdx.x; t < r1; t += kPrefThreads) a.coef[t] = counts(a, t) ? -coef : 0.0f;
+}
+
+__global__ __launch_bounds__(256) void mean_kernel(const PrefArgs a) {
+  __shared__ double part[256];
+  double s = 0.0;
+  for (int64_t i = threadIdx.x; i < a.n_pairs; i += 256) s += (double)a.pair_loss[i];
+  part[threadIdx.x] = s;
+  __syncthreads();
+  for (int d = 128; d > 0; d >>= 1) {
+    if ((int)threadIdx.x < d) part[threadIdx.x] += part[threadIdx.x + d];
+    __syncthreads();
+  }
+  if (threadIdx.x == 0) a.loss[0] = a.n_pairs ? (float)(part[0] / (double)a.n_pairs) : 0.0f;
+}
+
+// ---------------------------------------------------------------------------
+// Launch
+// ---------------------------------------------------------------------------
+
+template <typename F>
+int by_type(int dt, F f) {
+  switch (dt) {
+    case ZERO_F32: return f(std::integral_constant<int, ZERO_F32>{});
+    case ZERO_F16: return f(std::integral_constant<int, ZERO_F16>{});
+    default: return f(std::integral_constant<int, ZERO_BF16>{});
+  }
+}
+
+int last() { return (int)hipGetLastError(); }
+
+}  // namespace
+
+int launch_embed(const EmbedArgs& a, int tdt, int odt, bool vec, int64_t blocks, void* stream) {
+  return by_type(tdt, [&](auto T) {
+    return by_type(odt, [&](auto O) {
+      constexpr int t = decltype(T)::value, o = decltype(O)::value;
+      if (vec) embed_kernel<t, o, vec_of(t, o)><<<(uint32_t)blocks, kStreamThreads, 0, (hipStream_t)stream>>>(a);
+      else embed_kernel<t, o, 1><<<(uint32_t)blocks, kStreamThreads, 0, (hipStream_t)stream>>>(a);
+      return last();
+    });
+  });
+}
+
+int launch_rank(const RankArgs& a, int64_t blocks, void* stream) {
+  rank_kernel<<<(uint32_t)blocks, kRankThreads, 0, (hipStream_t)stream>>>(a);
+  return last();
+}
+
+int launch_radix(const RadixArgs& a, void* stream) {
+  radix_count_kernel<<<a.n_blocks, kSortThreads, 0, (hipStream_t)stream>>>(a);
+  if (const int err = last()) return err;
+  radix_move_kernel<<<a.n_blocks, kSortThreads, 0, (hipStream_t)stream>>>(a);
+  return last();
+}
+
+int launch_grad(const GradArgs& a, int ydt, int gdt, int vec, int64_t blocks, void* stream) {
+  return by_type(ydt, [&](auto Y) {
+    return by_type(gdt, [&](auto G) {
+      constexpr int y = decltype(Y)::value, g = decltype(G)::value;
+      auto go = [&](auto N) {
+        constexpr int n = decltype(N)::value;
+        if (a.drop.cut)
+          grad_kernel<y, g, n, true><<<(uint32_t)blocks, kGradThreads, 0, (hipStream_t)stream>>>(a);
+        else
+          grad_kernel<y, g, n, false><<<(uint32_t)blocks, kGradThreads, 0, (hipStream_t)stream>>>(a);
+        return last();
+      };
+      if (vec == 1) return go(std::integral_constant<int, 1>{});
+      if constexpr (vec_of(y, g) == 8)
+        if (vec == 8) return go(std::integral_constant<int, 8>{});
+      return go(std::integral_constant<int, 4>{});
+    });
+  });
+}
+
+int launch_grad_join(const GradArgs& a, int gdt, bool vec, void* stream) {
+  return by_type(gdt, [&](auto G) {
+    constexpr int g = decltype(G)::value;
+    const int n = vec ? 4 : 1;
+    const int tiles = (a.hidden + 64 * n - 1) / (64 * n);
+    const dim3 grid((uint32_t)a.n_chunks, (uint32_t)((tiles + 7) / 8));
+    if (vec) grad_join_kernel<g, 4><<<grid, kJoinThreads, 0, (hipStream_t)stream>>>(a);
+    else grad_join_kernel<g, 1><<<grid, kJoinThreads, 0, (hipStream_t)stream>>>(a);
+    return last();
+  });
+}
+
+int launch_dropout(const DropoutArgs& a, int dt, int64_t blocks, void* stream) {
+  return by_type(dt, [&](auto D) {
+    constexpr int d = decltype(D)::value;
+    dropout_kernel<d, vec_of(d, d)><<<(uint32_t)blocks, kStreamThreads, 0, (hipStream_t)stream>>>(a);
+    return last();
+  });
+}
+
+int launch_logp(const LogpArgs& a, int dt, void* stream) {
+  return by_type(dt, [&](auto D) {
+    logp_kernel<decltype(D)::value><<<(uint32_t)(a.n * a.splits), kLogpThreads, 0, (hipStream_t)stream>>>(a);
+    return last();
+  });
+}
+
+int launch_logp_join(const LogpArgs& a, int dt, void* stream) {
+  return by_type(dt, [&](auto D) {
+    logp_join_kernel<decltype(D)::value><<<(uint32_t)((a.n + 63) / 64), 64, 0, (hipStream_t)stream>>>(a);
+    return last();
+  });
+}
+
+int launch_dlogits(const LogpArgs& a, int dt, void* stream) {
+  return by_type(dt, [&](auto D) {
+    dlogits_kernel<decltype(D)::value><<<(uint32_t)(a.n * a.splits), kDlogitsThreads, 0, (hipStream_t)stream>>>(a);
+    return last();
+  });
+}
+
+int launch_preference(const PrefArgs& a, void* stream) {
+  preference_kernel<<<(uint32_t)(a.n_pairs + 1), kPrefThreads, 0, (hipStream_t)stream>>>(a);
+  if (const int err = last()) return err;
+  mean_kernel<<<1, 256, 0, (hipStream_t)stream>>>(a);
+  return last();
+}
+
+}  // namespace ops
+}  // namespace zk
