@@ -125,7 +125,7 @@ def load():
     L.zero_set_warm_read.restype = i32
     L.zero_set_warm_read.argtypes = [i32]
     f64, size = ctypes.c_double, ctypes.c_size_t
-    p_drop = ctypes.POINTER(_Drop)
+    p_drop = vp   # a zero_drop by reference, or NULL
     L.zero_embed.restype = i32
     L.zero_embed.argtypes = [vp, i32, i64, vp, i32, vp, i32, i64, f64, p_drop, vp, i32, i64, vp]
     L.zero_token_order_workspace_bytes.restype = size
