@@ -35,7 +35,7 @@ struct EmbedArgs {
   int32_t upr;       // units of one access per row
   int32_t tok64;     // tokens are int64
   float f;
-  int32_t pad_;
+  uint32_t magic;    // floor(2^32 / upr) + 1, 0 for upr = 1
   DropArgs drop;
 };
 
@@ -48,8 +48,8 @@ constexpr int kRankItems = 32;           // positions ranked per workgroup
 constexpr int kDigitBits = 9;
 constexpr int kBins = 1 << kDigitBits;
 constexpr int kSortThreads = 512;        // also one thread per bin
-constexpr int kSortKeys = 8;             // keys per thread and tile
-constexpr int kSortTile = kSortThreads * kSortKeys;
+constexpr int kSortKeysFew = 2;          // keys per thread and tile: fewer
+constexpr int kSortKeysMany = 8;         //   where more would leave CUs without a tile
 constexpr int kSortBlocks = 256;         // most workgroups of a pass
 
 struct RankArgs {
@@ -75,6 +75,7 @@ struct RadixArgs {
   int32_t shift;
   int32_t bits;
   int32_t n_blocks;
+  int32_t tile;             // positions of a tile
   int64_t tiles_per_block;
 };
 
@@ -82,7 +83,9 @@ struct RadixArgs {
 // `chunk`; see zero_ops.hip.
 constexpr int kGradThreads = 256;
 constexpr int kJoinThreads = 512;
-constexpr int kJoinTile = 256;           // columns of a wave in the join
+constexpr int kJoinTile = 256;           // columns of a workgroup in the join
+constexpr int kJoinChunks = 16;          // chunks it looks after
+constexpr int kJoinLong = 64;            // chunks from which a run is cut into pieces
 
 struct GradArgs {
   const int32_t* sorted;
@@ -102,7 +105,9 @@ struct GradArgs {
   int32_t fill_rows;       // rows of one zero-fill workgroup
   int32_t accumulate;
   float f;
-  int64_t chunk_blocks;    // workgroups before the fill workgroups
+  int64_t chunk_blocks;    // workgroups before those that write zero rows
+  int32_t stream_dy;       // dy is read past the caches
+  int32_t pad_;
   DropArgs drop;
 };
 
@@ -117,7 +122,11 @@ struct DropoutArgs {
 };
 
 constexpr int kLogpThreads = 512;
-constexpr int kDlogitsThreads = 256;
+constexpr int kLogpShortRow = 8192;      // rows shorter than this take one wave
+constexpr int kDlogitsThreads = 128;
+constexpr int kDlogitsUnroll = 2;
+constexpr int kDlogitsPiece = 2048;      // elements of a row per workgroup
+constexpr int64_t kCachedBytes = int64_t(128) << 20;
 
 struct LogpArgs {
   const void* logits;
@@ -133,10 +142,11 @@ struct LogpArgs {
   int32_t vocab;
   int32_t lab64;
   int32_t splits;     // workgroups per row
-  int32_t pad_;
+  int32_t cached_from;   // first row that is read through the caches
 };
 
 constexpr int kPrefThreads = 1024;
+constexpr int kPrefSmallRows = 1024;     // most rows of the one-launch form
 
 struct PrefArgs {
   const void* offsets;
@@ -170,8 +180,9 @@ int launch_preference(const PrefArgs& a, void* stream);
 // Elements of one access of the embedding kernels: 16 bytes of a 16-bit
 // buffer, or four elements where an fp32 buffer takes part.
 constexpr int vec_of(int a, int b) { return a == ZERO_F32 || b == ZERO_F32 ? 4 : 8; }
-constexpr int kUnroll = 4;        // units per thread of the streaming kernels
-constexpr int kStreamThreads = 256;
+constexpr int kEmbedUnroll = 4;     // accesses per thread
+constexpr int kEmbedThreads = 256;
+constexpr int kDropoutThreads = 512;
 
 }  // namespace ops
 }  // namespace zk

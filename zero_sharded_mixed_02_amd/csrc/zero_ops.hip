@@ -143,6 +143,14 @@ __device__ __forceinline__ Raw<DT, N> from_float(const float (&x)[N]) {
   return r;
 }
 
+// Keeps the compiler from widening a row ahead of its use: all rows of a batch
+// widened at once would take twice the registers.
+template <int DT, int N>
+__device__ __forceinline__ void pin(Raw<DT, N>& r) {
+#pragma unroll
+  for (int i = 0; i < Raw<DT, N>::kWords; ++i) asm volatile("" : "+v"(r.w[i]));
+}
+
 __device__ __forceinline__ int64_t load_id(const void* p, int64_t i, int wide) {
   return wide ? ((const AS1 int64_t*)(uintptr_t)p)[i] : (int64_t)((const AS1 int32_t*)(uintptr_t)p)[i];
 }
@@ -156,30 +164,59 @@ __device__ __forceinline__ int32_t row_of(int64_t id, int32_t rows) {
 // Dropout's mask
 // ---------------------------------------------------------------------------
 
+// z ^ (z >> K) for K < 32, in 32-bit halves: gfx950 shifts 64 bits at a
+// fraction of the rate.
+template <int K>
+__device__ __forceinline__ uint64_t xorshift(uint64_t z) {
+  const uint32_t lo = (uint32_t)z, hi = (uint32_t)(z >> 32);
+  const uint32_t l = lo ^ __builtin_amdgcn_alignbit(hi, lo, K), h = hi ^ (hi >> K);
+  return ((uint64_t)h << 32) | l;
+}
+
 __device__ __forceinline__ uint64_t mix64(uint64_t z) {
-  z = (z ^ (z >> 30)) * kMix1;
-  z = (z ^ (z >> 27)) * kMix2;
-  return z ^ (z >> 31);
+  z = xorshift<30>(z) * kMix1;
+  z = xorshift<27>(z) * kMix2;
+  return xorshift<31>(z);
 }
 
 __device__ __forceinline__ uint64_t mask_key(const DropArgs& d) {
   return d.step_dev ? mix64((d.site_key ^ *(const AS1 uint64_t*)(uintptr_t)d.step_dev) + kGamma) : d.key;
 }
 
-// Zeroes the dropped ones among N elements whose first stands at mask position
-// e.  One mix64 gives four elements 16 bits each, so a group that starts
-// inside a word takes one word more and shifts.  16 bits an element and not
+// A mask from a position that the whole wave (or workgroup) shares: its word
+// is found on the scalar unit, and the lanes add to it.
+struct MaskBase {
+  uint64_t z;        // state of the word that holds the shared position
+  uint32_t sub;      // the position's place in that word, 0..3
+};
+
+__device__ __forceinline__ MaskBase mask_base(uint64_t key, int64_t position) {
+  return MaskBase{key + (uint64_t)((position >> 2) + 1) * kGamma, (uint32_t)position & 3u};
+}
+
+// Zeroes the dropped ones among N elements whose first stands `local` behind
+// the shared position.  One mix64 gives four elements 16 bits each, so a group
+// that starts inside a word takes one word more and shifts.  16 bits an element and not
 // 32 halve the generator's work, which at 32 bits would be as long as the
 // memory traffic of a 16-bit tensor; p is a multiple of 2^-16 for it.
-template <int N>
-__device__ __forceinline__ void drop(float (&x)[N], uint64_t key, int64_t e, uint32_t cut) {
-  const uint64_t z = key + (uint64_t)((e >> 2) + 1) * kGamma;
-  const uint32_t off = ((uint32_t)e & 3u) * 16u;
+// A draw is compared where it stands: the upper half of a register against
+// cut << 16 (cut < 65536 here; p = 1 drops everything without draws).
+// ALIGNED: every group starts a word (the positions are multiples of 4).
+template <int N, bool ALIGNED = false>
+__device__ __forceinline__ void drop(float (&x)[N], const MaskBase& b, uint32_t local, uint32_t cut) {
+  if (cut > 0xffffu) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) x[i] = 0.0f;
+    return;
+  }
+  const uint32_t p = b.sub + local;
+  const uint64_t z = b.z + (uint64_t)(p >> 2) * kGamma;
+  const uint32_t off = (p & 3u) * 16u;
   constexpr int W = (N + 3) / 4;
   uint64_t w[W];
 #pragma unroll
   for (int i = 0; i < W; ++i) w[i] = mix64(z + (uint64_t)i * kGamma);
-  if (off) {
+  if (!ALIGNED && off) {
     if constexpr (N > 1) {
       const uint64_t last = mix64(z + (uint64_t)W * kGamma);
 #pragma unroll
@@ -190,8 +227,9 @@ __device__ __forceinline__ void drop(float (&x)[N], uint64_t key, int64_t e, uin
   }
 #pragma unroll
   for (int i = 0; i < N; ++i) {
-    const uint32_t draw = (uint32_t)(w[i / 4] >> (16 * (i % 4))) & 0xffffu;
-    x[i] = draw >= cut ? x[i] : 0.0f;
+    const uint32_t half = (uint32_t)(w[i / 4] >> (32 * (i / 2 % 2)));
+    const bool keep = i % 2 ? half >= (cut << 16) : (uint16_t)half >= (uint16_t)cut;
+    x[i] = keep ? x[i] : 0.0f;
   }
 }
 
@@ -199,43 +237,52 @@ __device__ __forceinline__ void drop(float (&x)[N], uint64_t key, int64_t e, uin
 // Embedding lookup
 // ---------------------------------------------------------------------------
 
-// A thread owns kUnroll accesses of N elements, kStreamThreads accesses apart,
+// t / upr for t < upr + kEmbedThreads * kEmbedUnroll: at most 1 where upr is that
+// long, else by the reciprocal floor(2^32 / upr) + 1, exact since
+// t * upr < 2^32 (0 stands for upr = 1).
+__device__ __forceinline__ uint32_t row_in(uint32_t t, uint32_t upr, uint32_t magic) {
+  if (upr > kEmbedThreads * kEmbedUnroll) return t >= upr;
+  return magic ? __umulhi(t, magic) : t;
+}
+
+// A thread owns kEmbedUnroll accesses of N elements, kEmbedThreads accesses apart,
 // numbered row by row through the output.
 template <int TDT, int ODT, int N>
-__global__ __launch_bounds__(kStreamThreads) void embed_kernel(const EmbedArgs a) {
-  const int64_t u0 = (int64_t)blockIdx.x * (kStreamThreads * kUnroll);
+__global__ __launch_bounds__(kEmbedThreads) void embed_kernel(const EmbedArgs a) {
+  const int64_t u0 = (int64_t)blockIdx.x * (kEmbedThreads * kEmbedUnroll);
   const int64_t row0 = u0 / a.upr;
   const uint32_t rem0 = (uint32_t)(u0 - row0 * a.upr);
-  const uint64_t key = a.drop.cut ? mask_key(a.drop) : 0;
-  int64_t row[kUnroll];
-  int32_t col[kUnroll], id[kUnroll];
+  const int64_t left = a.n - row0;   // rows from here on
+  const MaskBase mask = a.drop.cut ? mask_base(mask_key(a.drop), a.drop.first + row0 * a.hidden) : MaskBase{};
+  void* const out = (char*)a.out + row0 * a.out_stride * es_of<ODT>;
+  uint32_t row[kEmbedUnroll];             // behind row0
+  int32_t col[kEmbedUnroll], id[kEmbedUnroll];
 #pragma unroll
-  for (int j = 0; j < kUnroll; ++j) {
-    const uint32_t t = rem0 + j * kStreamThreads + threadIdx.x;
-    const uint32_t r = t / (uint32_t)a.upr;
-    row[j] = row0 + r;
-    const int32_t c = (int32_t)(t - r * (uint32_t)a.upr) * N;
+  for (int j = 0; j < kEmbedUnroll; ++j) {
+    const uint32_t t = rem0 + j * kEmbedThreads + threadIdx.x;
+    row[j] = row_in(t, (uint32_t)a.upr, a.magic);
+    const int32_t c = (int32_t)(t - row[j] * (uint32_t)a.upr) * N;
     col[j] = c < a.hidden - N ? c : a.hidden - N;   // the last access ends with the row
-    id[j] = row[j] < a.n ? row_of(load_id(a.tokens, row[j], a.tok64), a.rows) : a.rows;
+    id[j] = row[j] < left ? row_of(load_id(a.tokens, row0 + row[j], a.tok64), a.rows) : a.rows;
   }
-  Raw<TDT, N> raw[kUnroll];
+  Raw<TDT, N> raw[kEmbedUnroll];
   if (a.rows > 0) {
 #pragma unroll
-    for (int j = 0; j < kUnroll; ++j)
-      raw[j] = load<TDT, N>(a.table, (int64_t)(id[j] < a.rows ? id[j] : 0) * a.hidden + col[j]);
+    for (int j = 0; j < kEmbedUnroll; ++j)
+      raw[j] = load<TDT, N>(a.table, (int64_t)((uint64_t)(uint32_t)(id[j] < a.rows ? id[j] : 0) * (uint32_t)a.hidden) + col[j]);
   } else {
 #pragma unroll
-    for (int j = 0; j < kUnroll; ++j) raw[j] = Raw<TDT, N>{};
+    for (int j = 0; j < kEmbedUnroll; ++j) raw[j] = Raw<TDT, N>{};
   }
 #pragma unroll
-  for (int j = 0; j < kUnroll; ++j) {
-    if (row[j] >= a.n) continue;
+  for (int j = 0; j < kEmbedUnroll; ++j) {
+    if (row[j] >= left) continue;
     float x[N];
     to_float<TDT, N>(raw[j], x);
 #pragma unroll
     for (int i = 0; i < N; ++i) x[i] = id[j] < a.rows ? x[i] * a.f : 0.0f;
-    if (a.drop.cut) drop<N>(x, key, a.drop.first + row[j] * a.hidden + col[j], a.drop.cut);
-    store<ODT, N>(a.out, row[j] * a.out_stride + col[j], from_float<ODT, N>(x));
+    if (a.drop.cut) drop<N>(x, mask, row[j] * (uint32_t)a.hidden + col[j], a.drop.cut);
+    store<ODT, N, (N > 1)>(out, (int64_t)row[j] * a.out_stride + col[j], from_float<ODT, N>(x));
   }
 }
 
@@ -294,8 +341,8 @@ __global__ __launch_bounds__(kSortThreads) void radix_count_kernel(const RadixAr
   bin[threadIdx.x] = 0;
   __syncthreads();
   const uint32_t mask = (1u << a.bits) - 1;
-  const int64_t lo = (int64_t)blockIdx.x * a.tiles_per_block * kSortTile;
-  int64_t hi = lo + a.tiles_per_block * kSortTile;
+  const int64_t lo = (int64_t)blockIdx.x * a.tiles_per_block * a.tile;
+  int64_t hi = lo + a.tiles_per_block * a.tile;
   if (hi > a.n) hi = a.n;
   for (int64_t i = lo + threadIdx.x; i < hi; i += kSortThreads) {
     int32_t key, pos;
@@ -308,9 +355,10 @@ __global__ __launch_bounds__(kSortThreads) void radix_count_kernel(const RadixAr
 
 // ... and this moves its positions.  A digit's place is the count of smaller
 // digits, plus the same digit in earlier workgroups, plus its rank in this
-// one.  In a tile each wave owns 64 * kSortKeys consecutive positions and takes
+// one.  In a tile each wave owns 64 * KEYS consecutive positions and takes
 // them 64 at a time: lanes of the same digit find each other with one ballot
 // per bit, and rank themselves by lane, so equal tokens keep their order.
+template <int KEYS>
 __global__ __launch_bounds__(kSortThreads) void radix_move_kernel(const RadixArgs a) {
   constexpr int kWaves = kSortThreads / 64;
   __shared__ uint32_t base[kBins];               // next place of each digit
@@ -319,6 +367,7 @@ __global__ __launch_bounds__(kSortThreads) void radix_move_kernel(const RadixArg
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   {
     uint32_t before = 0, total = 0;
+#pragma unroll 32   // one latency for many workgroups' counts
     for (int b = 0; b < a.n_blocks; ++b) {
       const uint32_t h = a.hist[(int64_t)b * kBins + threadIdx.x];
       before += b < (int)blockIdx.x ? h : 0;
@@ -339,22 +388,22 @@ __global__ __launch_bounds__(kSortThreads) void radix_move_kernel(const RadixArg
   const uint32_t mask = (1u << a.bits) - 1;
   const int64_t tile0 = (int64_t)blockIdx.x * a.tiles_per_block;
   for (int64_t t = 0; t < a.tiles_per_block; ++t) {
-    const int64_t lo = (tile0 + t) * kSortTile;
+    const int64_t lo = (tile0 + t) * (kSortThreads * KEYS);
     if (lo >= a.n) break;   // uniform
 #pragma unroll
     for (int w = 0; w < kWaves; ++w) cnt[w][threadIdx.x] = 0;
     __syncthreads();
-    int32_t key[kSortKeys], pos[kSortKeys];
-    uint32_t rank[kSortKeys];
-    const int64_t first = lo + wave * (64 * kSortKeys) + lane;
+    int32_t key[KEYS], pos[KEYS];
+    uint32_t rank[KEYS];
+    const int64_t first = lo + wave * (64 * KEYS) + lane;
 #pragma unroll
-    for (int k = 0; k < kSortKeys; ++k) {
+    for (int k = 0; k < KEYS; ++k) {
       const int64_t i = first + k * 64;
       key[k] = pos[k] = 0;
       if (i < a.n) radix_read(a, i, key[k], pos[k]);
     }
 #pragma unroll
-    for (int k = 0; k < kSortKeys; ++k) {
+    for (int k = 0; k < KEYS; ++k) {
       const bool in = first + k * 64 < a.n;
       const uint32_t d = ((uint32_t)key[k] >> a.shift) & mask;
       uint64_t same = __ballot(in);
@@ -383,7 +432,7 @@ __global__ __launch_bounds__(kSortThreads) void radix_move_kernel(const RadixArg
     base[threadIdx.x] = run;
     __syncthreads();
 #pragma unroll
-    for (int k = 0; k < kSortKeys; ++k) {
+    for (int k = 0; k < KEYS; ++k) {
       if (first + k * 64 >= a.n) continue;
       const uint32_t d = ((uint32_t)key[k] >> a.shift) & mask;
       const int64_t place = (int64_t)cnt[wave][d] + rank[k];
@@ -410,54 +459,86 @@ __global__ __launch_bounds__(kSortThreads) void radix_move_kernel(const RadixArg
 // those up in order.  Further workgroups of the same launch write zeros to the
 // rows that no token names.
 
-// First index in [0, n) whose sorted token is >= key (n if none), found by a
-// whole wave, 64 probes at a time.
-__device__ __forceinline__ int64_t wave_lower_bound(const int32_t* sorted, int64_t n, int64_t key) {
+// First indices in [0, n) whose sorted token is >= key0 and >= key1 (n if
+// none), found by a whole wave: both at once, 64 probes each at a time.
+__device__ __forceinline__ void wave_lower_bounds(const int32_t* sorted, int64_t n, int64_t key0, int64_t key1,
+                                                  int64_t& at0, int64_t& at1) {
   const int lane = threadIdx.x & 63;
-  int64_t lo = 0, hi = n;
-  while (hi > lo) {
-    const int64_t step = (hi - lo + 63) / 64;
-    const int64_t i = lo + (lane + 1) * step - 1;
-    const uint64_t less = __ballot(i < hi && (int64_t)sorted[i < hi ? i : lo] < key);
-    lo += (int64_t)__popcll(less) * step;
-    if (lo > hi) lo = hi;
-    hi = hi < lo + step - 1 ? hi : lo + step - 1;
+  int64_t lo[2] = {0, 0}, hi[2] = {n, n};
+  const int64_t key[2] = {key0, key1};
+  while (hi[0] > lo[0] || hi[1] > lo[1]) {
+    int32_t probe[2];
+    bool in[2];
+    int64_t step[2];
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      step[k] = (hi[k] - lo[k] + 63) / 64;
+      const int64_t i = lo[k] + (lane + 1) * step[k] - 1;
+      in[k] = i < hi[k];
+      probe[k] = sorted[in[k] ? i : 0];
+    }
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      const uint64_t less = __ballot(in[k] && (int64_t)probe[k] < key[k]);
+      lo[k] += (int64_t)__popcll(less) * step[k];
+      if (lo[k] > hi[k]) lo[k] = hi[k];
+      if (step[k] > 0 && lo[k] + step[k] - 1 < hi[k]) hi[k] = lo[k] + step[k] - 1;
+    }
   }
-  return lo;
+  at0 = lo[0];
+  at1 = lo[1];
 }
 
-// Writes N columns of a finished row; `begin` is the first column that this
-// lane owns (col < begin where its access was moved back).
+__device__ __forceinline__ int64_t wave_lower_bound(const int32_t* sorted, int64_t n, int64_t key) {
+  int64_t a, b;
+  wave_lower_bounds(sorted, n, key, key, a, b);
+  return a;
+}
+
+// A finished row's value at one element, from its sum.
+template <int GDT>
+__device__ __forceinline__ void write_one(const GradArgs& a, int64_t e, float sum) {
+  float x[1] = {sum * a.f};
+  if (a.accumulate) {
+    float old[1];
+    to_float<GDT, 1>(load<GDT, 1>(a.dst, e - a.lo), old);
+    x[0] = old[0] + x[0];
+  }
+  store<GDT, 1>(a.dst, e - a.lo, from_float<GDT, 1>(x));
+}
+
+// Writes N columns of a finished row, the whole wave together.  `begin` is
+// the first column that this lane owns (col < begin where its access was
+// moved back), `whole` says that no lane's access was, or that writing a value
+// twice does no harm.  Rows that the written range cuts, and moved accesses
+// that add to dst, go element by element, through shared memory so that the
+// loop needs no registers by index.
 template <int GDT, int N>
-__device__ __forceinline__ void write_row(const GradArgs& a, int32_t row, int32_t col, int32_t begin,
-                                          const float (&sum)[N]) {
-  const int64_t e = (int64_t)row * a.hidden + col;
-  constexpr bool NT = N > 1;
-  if (e >= a.lo && e + N <= a.hi && (begin == col || !a.accumulate)) {
+__device__ __forceinline__ void write_row(const GradArgs& a, int32_t row, int32_t col, int32_t begin, bool on,
+                                          bool whole, const float (&sum)[N], float* lds) {
+  const int64_t e = (int64_t)row * a.hidden;
+  if (whole && e >= a.lo && e + a.hidden <= a.hi) {
+    if (!on) return;
+    void* dst = (char*)a.dst + (e - a.lo) * es_of<GDT>;
     float x[N];
+#pragma unroll
+    for (int i = 0; i < N; ++i) x[i] = sum[i] * a.f;
     if (a.accumulate) {
       float old[N];
-      to_float<GDT, N>(load<GDT, N>(a.dst, e - a.lo), old);
+      to_float<GDT, N>(load<GDT, N>(dst, col), old);
 #pragma unroll
-      for (int i = 0; i < N; ++i) x[i] = old[i] + sum[i] * a.f;
-    } else {
-#pragma unroll
-      for (int i = 0; i < N; ++i) x[i] = sum[i] * a.f;
+      for (int i = 0; i < N; ++i) x[i] = old[i] + x[i];
     }
-    store<GDT, N, NT>(a.dst, e - a.lo, from_float<GDT, N>(x));
+    store<GDT, N, (N > 1)>(dst, col, from_float<GDT, N>(x));
     return;
   }
+  float* mine = lds + (threadIdx.x & 63) * N;
 #pragma unroll
-  for (int i = 0; i < N; ++i) {
-    if (e + i < a.lo || e + i >= a.hi || col + i < begin) continue;
-    float x[1] = {sum[i] * a.f};
-    if (a.accumulate) {
-      float old[1];
-      to_float<GDT, 1>(load<GDT, 1>(a.dst, e + i - a.lo), old);
-      x[0] = old[0] + x[0];
-    }
-    store<GDT, 1>(a.dst, e + i - a.lo, from_float<GDT, 1>(x));
-  }
+  for (int i = 0; i < N; ++i) mine[i] = sum[i];
+  if (!on) return;
+#pragma unroll 1
+  for (int i = 0; i < N; ++i)
+    if (col + i >= begin && e + col + i >= a.lo && e + col + i < a.hi) write_one<GDT>(a, e + col + i, mine[i]);
 }
 
 template <int N>
@@ -481,16 +562,25 @@ __device__ void fill_rows(const GradArgs& a, int64_t block) {
   const int64_t r0 = a.row_lo + block * a.fill_rows;
   int64_t r1 = r0 + a.fill_rows;
   if (r1 > a.row_hi) r1 = a.row_hi;
-  const int64_t from = wave_lower_bound(a.sorted, a.n, r0);
-  const int64_t to = wave_lower_bound(a.sorted, a.n, r1);
-  for (int64_t r = r0 + threadIdx.x; r < r1; r += kGradThreads) {
-    int64_t lo = from, hi = to;
-    while (lo < hi) {
-      const int64_t mid = lo + (hi - lo) / 2;
-      if (a.sorted[mid] < r) lo = mid + 1;
-      else hi = mid;
+  int64_t from, to;
+  wave_lower_bounds(a.sorted, a.n, r0, r1, from, to);
+  if (to - from <= 2 * kGradThreads) {   // few positions: each marks its row
+    for (int r = threadIdx.x; r < a.fill_rows; r += kGradThreads) named[r] = 0;
+    __syncthreads();
+    for (int64_t i = from + threadIdx.x; i < to; i += kGradThreads) {
+      const int64_t r = a.sorted[i] - r0;
+      if ((uint64_t)r < (uint64_t)a.fill_rows) named[r] = 1;
     }
-    named[r - r0] = lo < a.n && a.sorted[lo] == r;
+  } else {                               // many, as where a token repeats: each row looks for one
+    for (int64_t r = r0 + threadIdx.x; r < r1; r += kGradThreads) {
+      int64_t lo = from, hi = to;
+      while (lo < hi) {
+        const int64_t mid = lo + (hi - lo) / 2;
+        if (a.sorted[mid] < r) lo = mid + 1;
+        else hi = mid;
+      }
+      named[r - r0] = lo < a.n && a.sorted[lo] == r;
+    }
   }
   __syncthreads();
   const uint32_t upr = (uint32_t)(a.hidden + N - 1) / N;
@@ -510,127 +600,173 @@ __device__ void fill_rows(const GradArgs& a, int64_t block) {
   }
 }
 
-template <int YDT, int GDT, int N, bool DROP>
+// DROP: 0 no dropout, 1 every access starts a word of the mask, 2 any.
+template <int YDT, int GDT, int N, int DROP, bool NT>
 __global__ __launch_bounds__(kGradThreads) void grad_kernel(const GradArgs a) {
   if ((int64_t)blockIdx.x >= a.chunk_blocks) {
     fill_rows<GDT>(a, (int64_t)blockIdx.x - a.chunk_blocks);
     return;
   }
+  __shared__ float bounce[kGradThreads / 64][64 * N];
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
   const int64_t w = (int64_t)blockIdx.x * (kGradThreads / 64) + wave;
   const int64_t c = w / a.tiles;
   if (c >= a.n_chunks) return;
-  const int32_t begin = ((int32_t)(w - c * a.tiles) * 64 + lane) * N;
+  const int32_t tile = (int32_t)(w - c * a.tiles) * 64 * N;
+  const int32_t begin = tile + lane * N;
   const bool on = begin < a.hidden;
   const int32_t col = begin < a.hidden - N ? begin : a.hidden - N;
+  const bool whole = !a.accumulate || tile + 64 * N <= a.hidden || a.hidden % N == 0;
+
+  // The chunk's tokens and positions, one a lane (a chunk has at most 64).
   const int64_t s = c * a.chunk;
-  const int64_t e = s + a.chunk < a.n ? s + a.chunk : a.n;
-  if (a.sorted[s] >= a.row_hi || a.sorted[e - 1] < a.row_lo) return;
-  const bool came_in = s > 0 && a.sorted[s - 1] == a.sorted[s];
+  const int len = (int)(s + a.chunk < a.n ? a.chunk : a.n - s);
+  const int64_t mine = s + (lane < len ? lane : len - 1);
+  const int32_t rows = a.sorted[mine], from = a.order[mine];
+  const int32_t before = a.sorted[s > 0 ? s - 1 : 0], after = a.sorted[s + len < a.n ? s + len : 0];
+  const int32_t poss = (uint32_t)from < (uint64_t)a.n ? from : -1;
+  const uint64_t here = __ballot(lane < len && rows >= a.row_lo && rows < a.row_hi);
+  if (!here) return;
+  const int p0 = __builtin_ctzll(here), p1 = 64 - __builtin_clzll(here);   // what is written, in sorted rows
+  const int32_t left_of = __shfl_up(rows, 1);   // by all lanes: a lane reads only from active ones
+  const uint64_t starts = __ballot(lane > 0 && lane < len && rows != left_of);
+  bool head = p0 == 0 && s > 0 && before == __builtin_amdgcn_readlane(rows, 0);   // came in from the chunk before
+  const bool goes_on = p1 == len && s + len < a.n && after == __builtin_amdgcn_readlane(rows, len - 1);
   const uint64_t key = DROP ? mask_key(a.drop) : 0;
 
+  constexpr int U = 8;
   float acc[N];
-  int32_t cur = a.sorted[s];
-  bool head = came_in;
 #pragma unroll
   for (int i = 0; i < N; ++i) acc[i] = 0.0f;
-  constexpr int U = 8;
-  for (int64_t i0 = s; i0 < e; i0 += U) {
-    int32_t row[U], pos[U];
-    Raw<YDT, N> raw[U];
+  auto fetch = [&](int q, Raw<YDT, N>& raw) {
+    const int32_t pos = __builtin_amdgcn_readlane(poss, q < p1 ? q : p1 - 1);
+    raw = load<YDT, N, NT>((const char*)a.dy + (int64_t)(pos < 0 ? 0 : pos) * a.dy_stride * es_of<YDT>, col);
+  };
+  Raw<YDT, N> cur[U], next[U];
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int64_t i = i0 + u < e ? i0 + u : e - 1;
-      row[u] = a.sorted[i];
-      pos[u] = a.order[i];
-      const bool good = (uint32_t)pos[u] < (uint64_t)a.n;
-      raw[u] = load<YDT, N>(a.dy, (int64_t)(good ? pos[u] : 0) * a.dy_stride + col);
+  for (int u = 0; u < U; ++u) fetch(p0 + u, cur[u]);
+  for (int b = p0; b < p1; b += U) {
+    // The next positions' rows are on their way while these are summed.
+    if (b + U < p1) {
+#pragma unroll
+      for (int u = 0; u < U; ++u) fetch(b + U + u, next[u]);
     }
+    const int n = p1 - b < U ? p1 - b : U;
+    int u0 = 0;
+    while (u0 < n) {
+      // The run of position b + u0 ends before `end`, in this batch or later.
+      const uint64_t later = b + u0 < 63 ? starts >> (b + u0 + 1) << (b + u0 + 1) : 0;
+      int end = later ? __builtin_ctzll(later) : p1;
+      if (end > p1) end = p1;
+      const int u1 = end - b < n ? end - b : n;
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      if (i0 + u >= e) break;
-      if (row[u] != cur) {
-        if (on && cur >= a.row_lo && cur < a.row_hi) {
-          if (head) write_part<N>(a, 2 * c, col, acc);
-          else write_row<GDT, N>(a, cur, col, begin, acc);
-        }
-        head = false;
-        cur = row[u];
-#pragma unroll
-        for (int i = 0; i < N; ++i) acc[i] = 0.0f;
-      }
-      if ((uint32_t)pos[u] < (uint64_t)a.n) {
+      for (int u = 0; u < U; ++u) {
+        if (u < u0 || u >= u1) continue;
+        const int32_t pos = __builtin_amdgcn_readlane(poss, b + u);
+        if (pos < 0) continue;
         float x[N];
-        to_float<YDT, N>(raw[u], x);
-        if constexpr (DROP) drop<N>(x, key, a.drop.first + (int64_t)pos[u] * a.hidden + col, a.drop.cut);
+        pin(cur[u]);
+        to_float<YDT, N>(cur[u], x);
+        if constexpr (DROP != 0)
+          drop<N, DROP == 1>(x, mask_base(key, a.drop.first + (int64_t)pos * a.hidden), (uint32_t)col, a.drop.cut);
 #pragma unroll
         for (int i = 0; i < N; ++i) acc[i] += x[i];
       }
+      u0 = u1;
+      if (end - b > n) break;   // it goes on in the next batch
+      const int32_t row = __builtin_amdgcn_readlane(rows, end - 1);
+      const bool tail = end == p1 && goes_on;
+      if (row >= a.row_lo && row < a.row_hi) {
+        if (!head && !tail) write_row<GDT, N>(a, row, col, begin, on, whole, acc, bounce[wave]);
+        else if (on) write_part<N>(a, 2 * c + (head ? 0 : 1), col, acc);
+      }
+      head = false;
+#pragma unroll
+      for (int i = 0; i < N; ++i) acc[i] = 0.0f;
     }
+#pragma unroll
+    for (int u = 0; u < U; ++u) cur[u] = next[u];
   }
-  if (!on || cur < a.row_lo || cur >= a.row_hi) return;
-  if (head) write_part<N>(a, 2 * c, col, acc);
-  else if (e < a.n && a.sorted[e] == cur) write_part<N>(a, 2 * c + 1, col, acc);
-  else write_row<GDT, N>(a, cur, col, begin, acc);
 }
 
-// Joins the run that begins in chunk blockIdx.x and goes on: its partial rows
-// in chunk order.  Short runs take one wave per tile of columns; long ones are
-// cut into eight pieces, one a wave, joined in order in shared memory.
+// Joins runs that cross chunk boundaries: their partial rows in chunk order.
+// A workgroup looks after the runs that begin in kJoinChunks chunks, for one
+// tile of columns.  A lane each finds out which chunks have one; short runs go
+// to a wave each, and long ones are cut into one piece a wave, joined in order
+// in shared memory.
 template <int GDT, int N>
 __global__ __launch_bounds__(kJoinThreads) void grad_join_kernel(const GradArgs a) {
   constexpr int kWaves = kJoinThreads / 64;
   __shared__ float piece[kWaves][64 * N];
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
-  const int64_t c = blockIdx.x;
-  const int64_t s = c * a.chunk, e = s + a.chunk;
-  if (e >= a.n) return;
-  const int32_t row = a.sorted[e - 1];
-  if (a.sorted[e] != row || row < a.row_lo || row >= a.row_hi) return;
-  if (s > 0 && a.sorted[s - 1] == row) return;   // began in an earlier chunk
-  // Chunks that the run comes into: those whose first token is still its.
-  const int64_t end = wave_lower_bound(a.sorted, a.n, (int64_t)row + 1);
-  const int64_t last = end > e ? (end - 1) / a.chunk : c;
-  const int64_t count = last - c + 1;            // partial rows
-  const int tiles = (a.hidden + 64 * N - 1) / (64 * N);
-  const bool split = count > 2 * kWaves;
-  const int64_t per = split ? (count + kWaves - 1) / kWaves : count;
-  for (int t0 = (int)blockIdx.y * kWaves; t0 < tiles && t0 < ((int)blockIdx.y + 1) * kWaves;
-       t0 += split ? 1 : kWaves) {
-    const int t = split ? t0 : t0 + wave;
-    const int32_t begin = (t * 64 + lane) * N;
-    const bool on = t < tiles && begin < a.hidden;
-    const int32_t col = begin < a.hidden - N ? begin : a.hidden - N;
-    const int64_t j0 = split ? wave * per : 0;
-    const int64_t j1 = j0 + per < count ? j0 + per : count;
-    float acc[N];
+  const int32_t tile = (int32_t)blockIdx.y * 64 * N;
+  const int32_t begin = tile + lane * N;
+  const bool on = begin < a.hidden;
+  const int32_t col = begin < a.hidden - N ? begin : a.hidden - N;
+  const bool whole = !a.accumulate || tile + 64 * N <= a.hidden || a.hidden % N == 0;
+
+  const int64_t c0 = (int64_t)blockIdx.x * kJoinChunks;
+  const int64_t mine = c0 + lane, s = mine * a.chunk, e = s + a.chunk;
+  const int64_t next = e + a.chunk, far = e + (int64_t)kJoinLong * a.chunk;
+  const int64_t end = a.n - 1;
+  const bool look = lane < kJoinChunks && e < a.n;
+  // One latency for all five.
+  const int32_t before = a.sorted[look && s > 0 ? s - 1 : 0], row = a.sorted[look ? e - 1 : 0],
+                after = a.sorted[look ? e : 0], third = a.sorted[look && next < a.n ? next : end],
+                last = a.sorted[look && far < a.n ? far : end];
+  const bool has = look && after == row && row >= a.row_lo && row < a.row_hi && !(s > 0 && before == row);
+  const bool more = has && next < a.n && third == row;   // it comes into a third chunk
+  const bool lots = has && far < a.n && last == row;
+  const uint64_t runs = __ballot(has), many = __ballot(more), longs = __ballot(lots);
+
+  // Sums partial rows [j0, j1) of the run that begins in chunk c.
+  auto sum = [&](int64_t c, int64_t j0, int64_t j1, float (&acc)[N]) {
 #pragma unroll
     for (int i = 0; i < N; ++i) acc[i] = 0.0f;
-    if (on) {
-#pragma unroll 4
-      for (int64_t j = j0; j < j1; ++j) {
-        const int64_t slot = j == 0 ? 2 * c + 1 : 2 * (c + j);
-        float x[N];
-        to_float<ZERO_F32, N>(load<ZERO_F32, N>(a.part, slot * a.hidden + col), x);
+    if (!on) return;
+#pragma unroll 8
+    for (int64_t j = j0; j < j1; ++j) {
+      const int64_t slot = j == 0 ? 2 * c + 1 : 2 * (c + j);
+      float x[N];
+      to_float<ZERO_F32, N>(load<ZERO_F32, N>(a.part, slot * a.hidden + col), x);
 #pragma unroll
-        for (int i = 0; i < N; ++i) acc[i] += x[i];
-      }
+      for (int i = 0; i < N; ++i) acc[i] += x[i];
     }
-    if (split) {
+  };
+  auto parts = [&](int64_t c, int32_t r) {   // partial rows of that run
+    return (wave_lower_bound(a.sorted, a.n, (int64_t)r + 1) - 1) / a.chunk - c + 1;
+  };
+  int k = 0;
+  for (uint64_t left = runs & ~longs; left; left &= left - 1, ++k) {
+    if (k % kWaves != wave) continue;
+    const int l = __builtin_ctzll(left);
+    const int64_t c = c0 + l;
+    const int32_t r = __builtin_amdgcn_readlane(row, l);
+    const int64_t count = (many >> l) & 1 ? parts(c, r) : 2;
+    float acc[N];
+    sum(c, 0, count, acc);
+    write_row<GDT, N>(a, r, col, begin, on, whole, acc, piece[wave]);
+  }
+  for (uint64_t left = longs; left; left &= left - 1) {   // the same in every wave
+    const int l = __builtin_ctzll(left);
+    const int64_t c = c0 + l;
+    const int32_t r = __builtin_amdgcn_readlane(row, l);
+    const int64_t count = parts(c, r);
+    const int64_t per = (count + kWaves - 1) / kWaves, j0 = wave * per;
+    float acc[N];
+    sum(c, j0, j0 + per < count ? j0 + per : count, acc);
+    __syncthreads();
 #pragma unroll
-      for (int i = 0; i < N; ++i) piece[wave][lane * N + i] = acc[i];
-      __syncthreads();
-      if (wave == 0) {
+    for (int i = 0; i < N; ++i) piece[wave][lane * N + i] = acc[i];
+    __syncthreads();
+    if (wave == 0) {
+      for (int v = 1; v < kWaves; ++v)
 #pragma unroll
-        for (int v = 1; v < kWaves; ++v)
-#pragma unroll
-          for (int i = 0; i < N; ++i) acc[i] += piece[v][lane * N + i];
-      }
-      __syncthreads();
+        for (int i = 0; i < N; ++i) acc[i] += piece[v][lane * N + i];
+      write_row<GDT, N>(a, r, col, begin, on, whole, acc, piece[0]);
     }
-    if (on && (!split || wave == 0)) write_row<GDT, N>(a, row, col, begin, acc);
   }
 }
 
@@ -639,14 +775,15 @@ __global__ __launch_bounds__(kJoinThreads) void grad_join_kernel(const GradArgs 
 // ---------------------------------------------------------------------------
 
 template <int DT, int N>
-__device__ __forceinline__ void dropout_one(const DropoutArgs& a, uint64_t key, int64_t e, const Raw<DT, N>& xr,
-                                            const Raw<DT, N>& rr) {
+__device__ __forceinline__ void dropout_one(const DropoutArgs& a, const MaskBase& mask, int64_t e0, uint32_t local,
+                                            const Raw<DT, N>& xr, const Raw<DT, N>& rr) {
+  const int64_t e = e0 + local;
   float x[N];
   to_float<DT, N>(xr, x);
   if (a.drop.cut) {
 #pragma unroll
     for (int i = 0; i < N; ++i) x[i] = x[i] * a.f;
-    drop<N>(x, key, a.drop.first + e, a.drop.cut);
+    drop<N>(x, mask, local, a.drop.cut);
   }
   if (a.residual) {
     float r[N];
@@ -654,34 +791,23 @@ __device__ __forceinline__ void dropout_one(const DropoutArgs& a, uint64_t key, 
 #pragma unroll
     for (int i = 0; i < N; ++i) x[i] = r[i] + x[i];
   }
-  store<DT, N>(a.out, e, from_float<DT, N>(x));
+  store<DT, N, (N > 1)>(a.out, e, from_float<DT, N>(x));
 }
 
 template <int DT, int N>
-__global__ __launch_bounds__(kStreamThreads) void dropout_kernel(const DropoutArgs a) {
-  const uint64_t key = a.drop.cut ? mask_key(a.drop) : 0;
-  const int64_t e0 = ((int64_t)blockIdx.x * (kStreamThreads * kUnroll) + threadIdx.x) * N;
-  Raw<DT, N> x[kUnroll], r[kUnroll];
-#pragma unroll
-  for (int j = 0; j < kUnroll; ++j) {
-    const int64_t e = e0 + (int64_t)j * kStreamThreads * N;
-    r[j] = Raw<DT, N>{};
-    if (e + N <= a.n) {
-      x[j] = load<DT, N>(a.x, e);
-      if (a.residual) r[j] = load<DT, N>(a.residual, e);
-    }
+__global__ __launch_bounds__(kDropoutThreads) void dropout_kernel(const DropoutArgs a) {
+  const int64_t e0 = (int64_t)blockIdx.x * (kDropoutThreads * N);   // first element of the workgroup
+  const MaskBase mask = a.drop.cut ? mask_base(mask_key(a.drop), a.drop.first + e0) : MaskBase{};
+  const int64_t left = a.n - e0;
+  const uint32_t e = threadIdx.x * N;
+  if ((int64_t)e + N <= left) {
+    dropout_one<DT, N>(a, mask, e0, e, load<DT, N, true>(a.x, e0 + e),
+                       a.residual ? load<DT, N, true>(a.residual, e0 + e) : Raw<DT, N>{});
+    return;
   }
-#pragma unroll
-  for (int j = 0; j < kUnroll; ++j) {
-    const int64_t e = e0 + (int64_t)j * kStreamThreads * N;
-    if (e + N <= a.n) {
-      dropout_one<DT, N>(a, key, e, x[j], r[j]);
-    } else {
-      for (int64_t i = e; i < a.n; ++i)   // fewer than N, in one thread
-        dropout_one<DT, 1>(a, key, i, load<DT, 1>(a.x, i),
-                           a.residual ? load<DT, 1>(a.residual, i) : Raw<DT, 1>{});
-    }
-  }
+  for (uint32_t i = e; i < left; ++i)   // fewer than N, in one thread
+    dropout_one<DT, 1>(a, mask, e0, i, load<DT, 1>(a.x, e0 + i),
+                       a.residual ? load<DT, 1>(a.residual, e0 + i) : Raw<DT, 1>{});
 }
 
 // ---------------------------------------------------------------------------
@@ -756,10 +882,10 @@ __device__ __forceinline__ void write_stats(const LogpArgs& a, int64_t t, int64_
 // One row, or one of `splits` pieces of a row, per workgroup.  Loads are
 // aligned: the elements before the first 16-byte boundary of the row and
 // behind the last one are taken singly.
-template <int DT>
-__global__ __launch_bounds__(kLogpThreads) void logp_kernel(const LogpArgs a) {
+template <int DT, int THREADS>
+__global__ __launch_bounds__(THREADS) void logp_kernel(const LogpArgs a) {
   constexpr int N = 16 / es_of<DT>;
-  constexpr int U = 4;
+  constexpr int U = 2;
   const int64_t t = blockIdx.x / (uint32_t)a.splits;
   const int part = (int)(blockIdx.x - (uint32_t)t * (uint32_t)a.splits);
   const int64_t label = load_id(a.labels, t, a.lab64);
@@ -782,18 +908,22 @@ __global__ __launch_bounds__(kLogpThreads) void logp_kernel(const LogpArgs a) {
   float m = neg_inf(), s = 0.0f;
   const int tid = threadIdx.x;
   int v = v0;
-  for (; v + U * kLogpThreads <= v1; v += U * kLogpThreads) {
-    float x[U * N];
+  auto stream = [&](auto nt) {
+    for (; v + U * THREADS <= v1; v += U * THREADS) {
+      float x[U * N];
 #pragma unroll
-    for (int j = 0; j < U; ++j) {
-      float y[N];
-      to_float<DT, N>(load<DT, N>(a.logits, row + head + (int64_t)(v + j * kLogpThreads + tid) * N), y);
+      for (int j = 0; j < U; ++j) {
+        float y[N];
+        to_float<DT, N>(load<DT, N, decltype(nt)::value>(a.logits, row + head + (int64_t)(v + j * THREADS + tid) * N), y);
 #pragma unroll
-      for (int i = 0; i < N; ++i) x[j * N + i] = y[i];
+        for (int i = 0; i < N; ++i) x[j * N + i] = y[i];
+      }
+      absorb<U * N>(x, m, s);
     }
-    absorb<U * N>(x, m, s);
-  }
-  for (v += tid; v < v1; v += kLogpThreads) {
+  };
+  if (t < a.cached_from) stream(std::true_type{});
+  else stream(std::false_type{});
+  for (v += tid; v < v1; v += THREADS) {
     float x[N];
     to_float<DT, N>(load<DT, N>(a.logits, row + head + (int64_t)v * N), x);
     absorb<N>(x, m, s);
@@ -808,7 +938,7 @@ __global__ __launch_bounds__(kLogpThreads) void logp_kernel(const LogpArgs a) {
     to_float<DT, 1>(load<DT, 1>(a.logits, row + a.vocab - tail + tid), x);
     absorb<1>(x, m, s);
   }
-  reduce_stats<kLogpThreads>(m, s);
+  reduce_stats<THREADS>(m, s);
   if (tid != 0) return;
   if (a.splits > 1) {
     a.part[2 * (int64_t)blockIdx.x] = m;
@@ -837,14 +967,14 @@ __global__ __launch_bounds__(64) void logp_join_kernel(const LogpArgs a) {
 template <int DT>
 __global__ __launch_bounds__(kDlogitsThreads) void dlogits_kernel(const LogpArgs a) {
   constexpr int N = 16 / es_of<DT>;
-  constexpr int U = 4;
-  const int64_t t = blockIdx.x / (uint32_t)a.splits;
-  const int part = (int)(blockIdx.x - (uint32_t)t * (uint32_t)a.splits);
+  constexpr int U = kDlogitsUnroll;
+  const uint32_t back = blockIdx.x / (uint32_t)a.splits;
+  const int64_t t = a.n - 1 - back;   // last rows first: see kCachedBytes
+  const int part = (int)(blockIdx.x - back * (uint32_t)a.splits);
   const int64_t label = load_id(a.labels, t, a.lab64);
-  const bool scored = (uint64_t)label < (uint64_t)a.vocab;
-  const float coef = scored ? a.coef[t] : 0.0f;
+  const float c = a.coef[t], m = a.stats[2 * t], ls = a.stats[2 * t + 1];
+  const float coef = (uint64_t)label < (uint64_t)a.vocab ? c : 0.0f;
   const bool zero = coef == 0.0f;   // uniform over the workgroup
-  const float m = zero ? 0.0f : a.stats[2 * t], ls = zero ? 0.0f : a.stats[2 * t + 1];
   const int64_t row = t * a.stride, drow = t * a.dl_stride;
   const uint32_t skew = (uint32_t)(at<DT, 1>(a.logits, row) & 15u);
   int head = skew ? (int)(16 - skew) / es_of<DT> : 0;
@@ -879,10 +1009,10 @@ __global__ __launch_bounds__(kDlogitsThreads) void dlogits_kernel(const LogpArgs
       if (u >= v1) continue;
       float x[N];
       to_float<DT, N>(raw[j], x);
-      const int c = head + u * N;
+      const int at0 = head + u * N;
 #pragma unroll
-      for (int i = 0; i < N; ++i) x[i] = grad(x[i], c + i);
-      store<DT, N, true>(a.dlogits, drow + c, from_float<DT, N>(x));
+      for (int i = 0; i < N; ++i) x[i] = grad(x[i], at0 + i);
+      store<DT, N, true>(a.dlogits, drow + at0, from_float<DT, N>(x));
     }
   }
   if (part == 0 && tid < head) one(tid);
@@ -903,69 +1033,126 @@ __device__ __forceinline__ bool counts(const PrefArgs& a, int64_t t) {
   return !a.labels || (uint64_t)load_id(a.labels, t, a.lab64) < (uint64_t)a.vocab;
 }
 
-// Sum over a sequence's scored rows, fp64, in an order fixed by its length;
-// valid in every thread.
-__device__ __forceinline__ double sum_sequence(const PrefArgs& a, int64_t lo, int64_t hi) {
-  __shared__ double part[kPrefThreads / 64];
+// Lane's share of the sum over a sequence's scored rows, fp64.
+template <int THREADS>
+__device__ __forceinline__ double sum_rows(const PrefArgs& a, int64_t lo, int64_t hi, int tid) {
   double s = 0.0;
-  for (int64_t t = lo + threadIdx.x; t < hi; t += kPrefThreads)
-    if (counts(a, t)) s += (double)a.logp[t] - (a.ref ? (double)a.ref[t] : 0.0);
-#pragma unroll
-  for (int d = 32; d > 0; d >>= 1) s += __shfl_xor(s, d);
-  __syncthreads();   // the array's last readers are done
-  if ((threadIdx.x & 63) == 0) part[threadIdx.x >> 6] = s;
-  __syncthreads();
-  s = 0.0;
-  for (int w = 0; w < kPrefThreads / 64; ++w) s += part[w];
+#pragma unroll 4
+  for (int64_t t = lo + tid; t < hi; t += THREADS)
+    s += counts(a, t) ? (double)a.logp[t] - (a.ref ? (double)a.ref[t] : 0.0) : 0.0;
   return s;
 }
 
-// -log sigmoid(h) = log(1 + e^-h)
-__device__ __forceinline__ double softplus_neg(double h) {
-  return h >= 0 ? log1p(exp(-h)) : log1p(exp(h)) - h;
+__device__ __forceinline__ double wave_sum(double s) {
+#pragma unroll
+  for (int d = 32; d > 0; d >>= 1) s += __shfl_xor(s, d);
+  return s;
 }
 
-// A pair per workgroup; one more writes the rows in no sequence.
+// Loss and slope of a pair with difference h; one exponential serves both:
+// with t = exp(-|h|), sigmoid is 1 / (1 + t) on one side and t / (1 + t) on
+// the other, and -log sigmoid(h) = log(1 + t) + max(-h, 0).
+struct Pair {
+  double loss;
+  float coef;
+};
+
+__device__ __forceinline__ Pair pair_of(const PrefArgs& a, double h) {
+  const double t = exp(-fabs(h)), soft = log1p(t);
+  const double big = 1.0 / (1.0 + t), small = t / (1.0 + t);
+  const double sig = h >= 0 ? big : small, sig_neg = h >= 0 ? small : big;
+  const double up = soft + (h < 0 ? -h : 0.0), down = soft + (h > 0 ? h : 0.0);
+  Pair p;
+  p.loss = (a.smoothing < 1 ? (1.0 - a.smoothing) * up : 0.0) + (a.smoothing > 0 ? a.smoothing * down : 0.0);
+  p.coef = (float)(a.slope * (a.smoothing * sig - (1.0 - a.smoothing) * sig_neg));
+  return p;
+}
+
+template <int THREADS>
+__device__ __forceinline__ void write_coef(const PrefArgs& a, int64_t lo, int64_t hi, int tid, float coef) {
+#pragma unroll 4
+  for (int64_t t = lo + tid; t < hi; t += THREADS) a.coef[t] = counts(a, t) ? coef : 0.0f;
+}
+
+// Rows in no sequence.
+template <int THREADS>
+__device__ __forceinline__ void write_outside(const PrefArgs& a, int tid) {
+  const int64_t lo = a.n_pairs ? row_limit(a, 0, 0) : a.n;
+  const int64_t hi = a.n_pairs ? row_limit(a, 2 * a.n_pairs, lo) : a.n;
+  for (int64_t t = tid; t < lo; t += THREADS) a.coef[t] = 0.0f;
+  for (int64_t t = hi + tid; t < a.n; t += THREADS) a.coef[t] = 0.0f;
+}
+
+// A pair per workgroup, half of it for each sequence; one more workgroup
+// writes the rows in no sequence.
 __global__ __launch_bounds__(kPrefThreads) void preference_kernel(const PrefArgs a) {
+  constexpr int kHalf = kPrefThreads / 2;
+  __shared__ double part[kPrefThreads / 64];
   const int64_t i = blockIdx.x;
+  const int tid = threadIdx.x;
   if (i == a.n_pairs) {
-    const int64_t lo = a.n_pairs ? row_limit(a, 0, 0) : a.n;
-    const int64_t hi = a.n_pairs ? row_limit(a, 2 * a.n_pairs, lo) : a.n;
-    for (int64_t t = threadIdx.x; t < lo; t += kPrefThreads) a.coef[t] = 0.0f;
-    for (int64_t t = hi + threadIdx.x; t < a.n; t += kPrefThreads) a.coef[t] = 0.0f;
+    write_outside<kPrefThreads>(a, tid);
     return;
   }
-  const int64_t j = a.n_pairs + i;
-  const int64_t c0 = row_limit(a, i, 0), c1 = row_limit(a, i + 1, c0);
-  const int64_t r0 = row_limit(a, j, 0), r1 = row_limit(a, j + 1, r0);
-  const double chosen = a.beta * sum_sequence(a, c0, c1);
-  const double rejected = a.beta * sum_sequence(a, r0, r1);
-  const double h = chosen - rejected;
-  if (threadIdx.x == 0) {
-    a.rewards[i] = (float)chosen;
-    a.rewards[j] = (float)rejected;
-    const double up = softplus_neg(h), down = softplus_neg(-h);
-    a.pair_loss[i] = (float)((a.smoothing < 1 ? (1.0 - a.smoothing) * up : 0.0) +
-                             (a.smoothing > 0 ? a.smoothing * down : 0.0));
+  const int side = tid / kHalf;   // 0 chosen, 1 rejected
+  const int64_t seq = i + side * a.n_pairs;
+  const int64_t lo = row_limit(a, seq, 0), hi = row_limit(a, seq + 1, lo);
+  const double s = wave_sum(sum_rows<kHalf>(a, lo, hi, tid % kHalf));
+  if (tid % 64 == 0) part[tid / 64] = s;
+  __syncthreads();
+  double chosen = 0.0, rejected = 0.0;
+#pragma unroll
+  for (int w = 0; w < kHalf / 64; ++w) {
+    chosen += part[w];
+    rejected += part[kHalf / 64 + w];
   }
-  const double sig = h >= 0 ? 1.0 / (1.0 + exp(-h)) : exp(h) / (1.0 + exp(h));       // sigmoid(h)
-  const double sig_neg = h >= 0 ? exp(-h) / (1.0 + exp(-h)) : 1.0 / (1.0 + exp(h));  // sigmoid(-h)
-  const float coef = (float)(a.slope * (a.smoothing * sig - (1.0 - a.smoothing) * sig_neg));
-  for (int64_t t = c0 + threadIdx.x; t < c1; t += kPrefThreads) a.coef[t] = counts(a, t) ? coef : 0.0f;
-  for (int64_t t = r0 + threadIdx.x; t < r1; t += kPrefThreads) a.coef[t] = counts(a, t) ? -coef : 0.0f;
+  chosen *= a.beta;
+  rejected *= a.beta;
+  const Pair p = pair_of(a, chosen - rejected);
+  if (tid == 0) {
+    a.rewards[i] = (float)chosen;
+    a.rewards[a.n_pairs + i] = (float)rejected;
+    a.pair_loss[i] = (float)p.loss;
+  }
+  write_coef<kHalf>(a, lo, hi, tid % kHalf, side ? -p.coef : p.coef);
 }
 
-__global__ __launch_bounds__(256) void mean_kernel(const PrefArgs a) {
-  __shared__ double part[256];
+__global__ __launch_bounds__(64) void mean_kernel(const PrefArgs a) {
   double s = 0.0;
-  for (int64_t i = threadIdx.x; i < a.n_pairs; i += 256) s += (double)a.pair_loss[i];
-  part[threadIdx.x] = s;
-  __syncthreads();
-  for (int d = 128; d > 0; d >>= 1) {
-    if ((int)threadIdx.x < d) part[threadIdx.x] += part[threadIdx.x + d];
-    __syncthreads();
+#pragma unroll 4
+  for (int64_t i = threadIdx.x; i < a.n_pairs; i += 64) s += (double)a.pair_loss[i];
+  s = wave_sum(s);
+  if (threadIdx.x == 0) a.loss[0] = a.n_pairs ? (float)(s / (double)a.n_pairs) : 0.0f;
+}
+
+// Few pairs of few rows: all of it in one workgroup and one launch, a wave per
+// pair.
+__global__ __launch_bounds__(kPrefThreads) void preference_small_kernel(const PrefArgs a) {
+  __shared__ float loss[kPrefThreads / 64];
+  const int wave = threadIdx.x / 64, lane = threadIdx.x % 64;
+  if (wave < a.n_pairs) {
+    const int64_t j = a.n_pairs + wave;
+    const int64_t c0 = row_limit(a, wave, 0), c1 = row_limit(a, wave + 1, c0);
+    const int64_t r0 = row_limit(a, j, 0), r1 = row_limit(a, j + 1, r0);
+    const double chosen = a.beta * wave_sum(sum_rows<64>(a, c0, c1, lane));
+    const double rejected = a.beta * wave_sum(sum_rows<64>(a, r0, r1, lane));
+    const Pair p = pair_of(a, chosen - rejected);
+    if (lane == 0) {
+      a.rewards[wave] = (float)chosen;
+      a.rewards[j] = (float)rejected;
+      a.pair_loss[wave] = (float)p.loss;
+      loss[wave] = (float)p.loss;
+    }
+    write_coef<64>(a, c0, c1, lane, p.coef);
+    write_coef<64>(a, r0, r1, lane, -p.coef);
   }
-  if (threadIdx.x == 0) a.loss[0] = a.n_pairs ? (float)(part[0] / (double)a.n_pairs) : 0.0f;
+  write_outside<kPrefThreads>(a, threadIdx.x);
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    double s = 0.0;
+    for (int w = 0; w < a.n_pairs; ++w) s += (double)loss[w];
+    a.loss[0] = a.n_pairs ? (float)(s / (double)a.n_pairs) : 0.0f;
+  }
 }
 
 // ---------------------------------------------------------------------------
@@ -989,8 +1176,8 @@ int launch_embed(const EmbedArgs& a, int tdt, int odt, bool vec, int64_t blocks,
   return by_type(tdt, [&](auto T) {
     return by_type(odt, [&](auto O) {
       constexpr int t = decltype(T)::value, o = decltype(O)::value;
-      if (vec) embed_kernel<t, o, vec_of(t, o)><<<(uint32_t)blocks, kStreamThreads, 0, (hipStream_t)stream>>>(a);
-      else embed_kernel<t, o, 1><<<(uint32_t)blocks, kStreamThreads, 0, (hipStream_t)stream>>>(a);
+      if (vec) embed_kernel<t, o, vec_of(t, o)><<<(uint32_t)blocks, kEmbedThreads, 0, (hipStream_t)stream>>>(a);
+      else embed_kernel<t, o, 1><<<(uint32_t)blocks, kEmbedThreads, 0, (hipStream_t)stream>>>(a);
       return last();
     });
   });
@@ -1004,7 +1191,10 @@ int launch_rank(const RankArgs& a, int64_t blocks, void* stream) {
 int launch_radix(const RadixArgs& a, void* stream) {
   radix_count_kernel<<<a.n_blocks, kSortThreads, 0, (hipStream_t)stream>>>(a);
   if (const int err = last()) return err;
-  radix_move_kernel<<<a.n_blocks, kSortThreads, 0, (hipStream_t)stream>>>(a);
+  if (a.tile == kSortThreads * kSortKeysFew)
+    radix_move_kernel<kSortKeysFew><<<a.n_blocks, kSortThreads, 0, (hipStream_t)stream>>>(a);
+  else
+    radix_move_kernel<kSortKeysMany><<<a.n_blocks, kSortThreads, 0, (hipStream_t)stream>>>(a);
   return last();
 }
 
@@ -1014,11 +1204,18 @@ int launch_grad(const GradArgs& a, int ydt, int gdt, int vec, int64_t blocks, vo
       constexpr int y = decltype(Y)::value, g = decltype(G)::value;
       auto go = [&](auto N) {
         constexpr int n = decltype(N)::value;
-        if (a.drop.cut)
-          grad_kernel<y, g, n, true><<<(uint32_t)blocks, kGradThreads, 0, (hipStream_t)stream>>>(a);
-        else
-          grad_kernel<y, g, n, false><<<(uint32_t)blocks, kGradThreads, 0, (hipStream_t)stream>>>(a);
-        return last();
+        const hipStream_t st = (hipStream_t)stream;
+        auto run = [&](auto NT) {
+          constexpr bool nt = decltype(NT)::value;
+          if (!a.drop.cut) grad_kernel<y, g, n, 0, nt><<<(uint32_t)blocks, kGradThreads, 0, st>>>(a);
+          else if (n > 1 && a.hidden % 4 == 0 && a.drop.first % 4 == 0)
+            grad_kernel<y, g, n, (n > 1 ? 1 : 2), nt><<<(uint32_t)blocks, kGradThreads, 0, st>>>(a);
+          else grad_kernel<y, g, n, 2, nt><<<(uint32_t)blocks, kGradThreads, 0, st>>>(a);
+          return last();
+        };
+        if constexpr (n > 1)
+          if (a.stream_dy) return run(std::true_type{});
+        return run(std::false_type{});
       };
       if (vec == 1) return go(std::integral_constant<int, 1>{});
       if constexpr (vec_of(y, g) == 8)
@@ -1033,7 +1230,7 @@ int launch_grad_join(const GradArgs& a, int gdt, bool vec, void* stream) {
     constexpr int g = decltype(G)::value;
     const int n = vec ? 4 : 1;
     const int tiles = (a.hidden + 64 * n - 1) / (64 * n);
-    const dim3 grid((uint32_t)a.n_chunks, (uint32_t)((tiles + 7) / 8));
+    const dim3 grid((uint32_t)((a.n_chunks + kJoinChunks - 1) / kJoinChunks), (uint32_t)tiles);
     if (vec) grad_join_kernel<g, 4><<<grid, kJoinThreads, 0, (hipStream_t)stream>>>(a);
     else grad_join_kernel<g, 1><<<grid, kJoinThreads, 0, (hipStream_t)stream>>>(a);
     return last();
@@ -1043,14 +1240,17 @@ int launch_grad_join(const GradArgs& a, int gdt, bool vec, void* stream) {
 int launch_dropout(const DropoutArgs& a, int dt, int64_t blocks, void* stream) {
   return by_type(dt, [&](auto D) {
     constexpr int d = decltype(D)::value;
-    dropout_kernel<d, vec_of(d, d)><<<(uint32_t)blocks, kStreamThreads, 0, (hipStream_t)stream>>>(a);
+    dropout_kernel<d, vec_of(d, d)><<<(uint32_t)blocks, kDropoutThreads, 0, (hipStream_t)stream>>>(a);
     return last();
   });
 }
 
 int launch_logp(const LogpArgs& a, int dt, void* stream) {
   return by_type(dt, [&](auto D) {
-    logp_kernel<decltype(D)::value><<<(uint32_t)(a.n * a.splits), kLogpThreads, 0, (hipStream_t)stream>>>(a);
+    constexpr int d = decltype(D)::value;
+    const uint32_t blocks = (uint32_t)(a.n * a.splits);
+    if (a.vocab < kLogpShortRow) logp_kernel<d, 64><<<blocks, 64, 0, (hipStream_t)stream>>>(a);
+    else logp_kernel<d, kLogpThreads><<<blocks, kLogpThreads, 0, (hipStream_t)stream>>>(a);
     return last();
   });
 }
@@ -1070,9 +1270,13 @@ int launch_dlogits(const LogpArgs& a, int dt, void* stream) {
 }
 
 int launch_preference(const PrefArgs& a, void* stream) {
+  if (a.n_pairs <= kPrefThreads / 64 && a.n <= kPrefSmallRows) {
+    preference_small_kernel<<<1, kPrefThreads, 0, (hipStream_t)stream>>>(a);
+    return last();
+  }
   preference_kernel<<<(uint32_t)(a.n_pairs + 1), kPrefThreads, 0, (hipStream_t)stream>>>(a);
   if (const int err = last()) return err;
-  mean_kernel<<<1, 256, 0, (hipStream_t)stream>>>(a);
+  mean_kernel<<<1, 64, 0, (hipStream_t)stream>>>(a);
   return last();
 }
 

@@ -25,6 +25,7 @@ constexpr int64_t kMaxRows = INT32_MAX - 1;
 constexpr int64_t kMaxHidden = int64_t(1) << 24;
 constexpr int64_t kMaxTokens = int64_t(1) << 30;
 constexpr int64_t kMaxVocab = int64_t(1) << 30;
+constexpr int64_t kInfinityCache = int64_t(256) << 20;   // memory-side cache of MI355X
 constexpr int64_t kMaxElems = int64_t(1) << 59;   // of one buffer: byte offsets stay in int64
 
 bool valid_it(int it) { return it == ZERO_I32 || it == ZERO_I64; }
@@ -116,7 +117,7 @@ int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 struct SortShape {
   bool small;           // ranked by counting
   int passes, bits;
-  int64_t blocks, tiles_per_block;
+  int64_t tile, blocks, tiles_per_block;
   size_t bytes;
 };
 
@@ -129,7 +130,8 @@ SortShape sort_shape(int64_t n, int64_t rows) {
   while ((rows >> key_bits) != 0) ++key_bits;   // tokens are 0..rows
   s.passes = (int)ceil_div(key_bits, kDigitBits);
   s.bits = (int)ceil_div(key_bits, s.passes);
-  const int64_t tiles = ceil_div(n, kSortTile);
+  s.tile = kSortThreads * (n <= (int64_t)kSortBlocks * kSortThreads * kSortKeysFew ? kSortKeysFew : kSortKeysMany);
+  const int64_t tiles = ceil_div(n, s.tile);
   s.tiles_per_block = ceil_div(tiles, std::min<int64_t>(tiles, kSortBlocks));
   s.blocks = ceil_div(tiles, s.tiles_per_block);
   s.bytes = (size_t)s.blocks * kBins * 4 + (s.passes > 1 ? (size_t)n * 8 : 0);
@@ -151,7 +153,7 @@ int64_t logp_splits(int64_t n, int64_t vocab) {
   return std::max<int64_t>(1, std::min<int64_t>(ceil_div(1024, n), vocab / 8192));
 }
 
-int64_t dlogits_splits(int64_t vocab) { return std::max<int64_t>(1, ceil_div(vocab, 16384)); }
+int64_t dlogits_splits(int64_t vocab) { return std::max<int64_t>(1, ceil_div(vocab, kDlogitsPiece)); }
 
 zero_status check_logits(const void* logits, zero_dtype dt, int64_t n, int64_t vocab, int64_t stride,
                          const void* labels, zero_itype label_it, int64_t& span) {
@@ -222,9 +224,10 @@ zero_status zero_embed(zero_plan_t p, int32_t tensor, int64_t hidden, const void
     a.rows = (int32_t)rows;
     a.hidden = (int32_t)hidden;
     a.upr = (int32_t)(wide ? ceil_div(hidden, vec) : hidden);
+    a.magic = a.upr > 1 ? (uint32_t)((uint64_t(1) << 32) / a.upr + 1) : 0;
     a.tok64 = token_it == ZERO_I64;
     a.f = (float)(scale * keep);
-    const int64_t blocks = ceil_div(n * a.upr, kStreamThreads * kUnroll);
+    const int64_t blocks = ceil_div(n * a.upr, kEmbedThreads * kEmbedUnroll);
     if (zero_status st = check_blocks(blocks)) return st;
     return launched(launch_embed(a, param_dt, out_dt, wide, blocks, stream));
   });
@@ -269,6 +272,7 @@ zero_status zero_token_order(const void* tokens, zero_itype token_it, int64_t n,
     a.tok64 = token_it == ZERO_I64;
     a.bits = s.bits;
     a.n_blocks = (int32_t)s.blocks;
+    a.tile = (int32_t)s.tile;
     a.tiles_per_block = s.tiles_per_block;
     for (int pass = 0; pass < s.passes; ++pass) {   // the last pass writes the outputs
       const bool to_out = (s.passes - 1 - pass) % 2 == 0;
@@ -355,8 +359,13 @@ zero_status zero_embed_grad(zero_plan_t p, int32_t tensor, int64_t hidden, const
     a.chunk = (int32_t)grad_chunk(n, hidden);
     a.n_chunks = (int32_t)ceil_div(n, a.chunk);
     a.tiles = (int32_t)ceil_div(hidden, 64 * vec);
+    // Zero rows: 128 KiB a workgroup, down to 8 KiB where that leaves fewer than
+    // about 2048 workgroups.
+    const int64_t row_bytes = hidden * esize(dst_dt);
+    const int64_t fill_bytes = std::max<int64_t>(8192, std::min<int64_t>(131072, (a.row_hi - a.row_lo) * row_bytes / 2048));
+    a.fill_rows = (int32_t)std::max<int64_t>(1, std::min<int64_t>(1024, fill_bytes / row_bytes));
     a.chunk_blocks = ceil_div((int64_t)a.n_chunks * a.tiles, kGradThreads / 64);
-    a.fill_rows = (int32_t)std::max<int64_t>(1, std::min<int64_t>(1024, 131072 / (hidden * esize(dst_dt))));
+    a.stream_dy = n * hidden * esize(dy_dt) > kInfinityCache;
     const int64_t blocks = a.chunk_blocks + (accumulate ? 0 : ceil_div(a.row_hi - a.row_lo, a.fill_rows));
     if (zero_status st = check_blocks(blocks)) return st;
     if (const int err = launch_grad(a, dy_dt, dst_dt, vec, blocks, stream)) return hip_fail(err);
@@ -388,7 +397,7 @@ zero_status zero_dropout(const void* x, const void* residual, void* out, int64_t
     a.out = out;
     a.n = n;
     a.f = (float)keep;
-    const int64_t blocks = ceil_div(n, (int64_t)kStreamThreads * kUnroll * vec_of(dt, dt));
+    const int64_t blocks = ceil_div(n, (int64_t)kDropoutThreads * vec_of(dt, dt));
     if (zero_status st = check_blocks(blocks)) return st;
     return launched(launch_dropout(a, dt, blocks, stream));
   });
@@ -427,6 +436,7 @@ zero_status zero_token_logp(const void* logits, zero_dtype dt, int64_t n, int64_
     a.vocab = (int32_t)vocab;
     a.lab64 = label_it == ZERO_I64;
     a.splits = (int32_t)logp_splits(n, vocab);
+    a.cached_from = (int32_t)std::max<int64_t>(0, n - kCachedBytes / (vocab * esize(dt)));
     if (zero_status st = check_blocks(n * a.splits)) return st;
     if (const int err = launch_logp(a, dt, stream)) return hip_fail(err);
     return a.splits > 1 ? launched(launch_logp_join(a, dt, stream)) : ok();
