@@ -444,10 +444,37 @@ class Drop:
         self._keep = step_dev
         addr = _arg(step_dev, "step_dev", 8, 1)
         self.c = _Drop(p, seed & mask, site & mask, step & mask, addr or None, first)
+        self._ref = ctypes.byref(self.c)
+
+
+_raw_stream = None   # torch's current stream of a device, as an integer
+
+
+def _current_stream(device: int) -> int:
+    """hipStream_t of torch's current stream on a device, without building a
+    Stream object where torch offers that (2.8 us a call)."""
+    global _raw_stream
+    if _raw_stream is None:
+        import torch
+        _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+            lambda d: int(torch.cuda.current_stream(d).cuda_stream))
+    return _raw_stream(device)
+
+
+_ID_TYPES = {}       # torch integer types -> zero_itype
+
+
+def _id_type(dtype):
+    if not _ID_TYPES:
+        import torch
+        _ID_TYPES.update({torch.int32: ZERO_I32, torch.int64: ZERO_I64})
+    return _ID_TYPES.get(dtype)
 
 
 class _Call:
     """The device and stream of one call, gathered from its tensors."""
+
+    __slots__ = ("stream", "device")
 
     def __init__(self, stream):
         self.stream, self.device = stream, None
@@ -457,7 +484,7 @@ class _Call:
             return
         if not x.is_cuda:
             raise ValueError(f"{name} is not on a GPU ({x.device})")
-        i = x.device.index
+        i = x.get_device()
         if self.device is None:
             self.device = i
         elif self.device != i:
@@ -465,10 +492,19 @@ class _Call:
 
     def flat(self, x, name: str, esize: int, need: int, optional: bool = False) -> int:
         """Address of a contiguous buffer of at least need elements."""
-        if x is None and not optional and need > 0:
-            raise ValueError(f"{name} is None")
-        if x is None or isinstance(x, int):
-            return _addr(x)
+        if x is None:
+            if not optional and need > 0:
+                raise ValueError(f"{name} is None")
+            return 0
+        try:   # the common case: a tensor that fits, on the call's device
+            device = x.get_device()
+            if (device >= 0 and (self.device is None or device == self.device) and x.numel() >= need
+                    and x.element_size() == esize and x.is_contiguous()):
+                self.device = device
+                return x.data_ptr()
+        except AttributeError:
+            if isinstance(x, int):
+                return x
         addr = _arg(x, name, esize, need)
         self.see(x, name)
         return addr
@@ -489,10 +525,10 @@ class _Call:
             raise ValueError(f"{name} holds {x.numel()} elements, expected {n} rows of {width}")
         self.see(x, name)
         if x.is_contiguous():
-            return int(x.data_ptr()), width
+            return x.data_ptr(), width
         if x.dim() != 2 or x.shape[1] != width or (width > 1 and x.stride(1) != 1) or (n > 1 and x.stride(0) < width):
             raise ValueError(f"{name}: rows must be contiguous (shape {tuple(x.shape)}, strides {x.stride()})")
-        return int(x.data_ptr()), int(x.stride(0)) if n > 1 else width
+        return x.data_ptr(), x.stride(0) if n > 1 else width
 
     def ids(self, x, name: str, n, it):
         """(address, integer type, count) of an id list."""
@@ -502,24 +538,25 @@ class _Call:
             return _addr(x), it, int(n)
         if not hasattr(x, "data_ptr") or not hasattr(x, "element_size"):
             raise TypeError(f"{name}: expected a torch tensor or an integer device address, got {type(x).__name__}")
-        kinds = {"torch.int32": ZERO_I32, "torch.int64": ZERO_I64}
-        if str(x.dtype) not in kinds:
+        kind = _id_type(x.dtype)
+        if kind is None:
             raise ValueError(f"{name} must be int32 or int64, got {x.dtype}")
         if not x.is_contiguous():
             raise ValueError(f"{name} is not contiguous")
         self.see(x, name)
-        if n is not None and int(n) != x.numel():
-            raise ValueError(f"{name} holds {x.numel()} elements, expected {n}")
-        return int(x.data_ptr()), kinds[str(x.dtype)], int(x.numel())
+        count = x.numel()
+        if n is not None and int(n) != count:
+            raise ValueError(f"{name} holds {count} elements, expected {n}")
+        return x.data_ptr(), kind, count
 
-    def workspace(self, x, need: int):
-        """(address, bytes); an integer address is taken to hold what is needed."""
+    def workspace(self, x, need):
+        """(address, bytes); an integer address is taken to hold the need()."""
         if x is None or isinstance(x, int):
-            return _addr(x), need if x else 0
+            return _addr(x), need() if x else 0
         if not hasattr(x, "data_ptr") or not x.is_contiguous():
             raise ValueError("workspace must be a contiguous tensor or an integer device address")
         self.see(x, "workspace")
-        return int(x.data_ptr()), int(x.numel() * x.element_size())
+        return x.data_ptr(), x.numel() * x.element_size()
 
     def drop(self, d):
         if d is None:
@@ -527,19 +564,22 @@ class _Call:
         if not isinstance(d, Drop):
             raise TypeError(f"drop: expected a Drop, got {type(d).__name__}")
         self.see(d._keep, "step_dev")
-        return ctypes.byref(d.c)
+        return d._ref
 
-    def issue(self, name: str, *args) -> None:
-        fn = getattr(load(), name)
+    def issue(self, fn, *args) -> None:
+        """Calls fn with the stream, on the tensors' device."""
         if self.device is None:
-            _check(fn(*args, _stream(self.stream)))
-            return
-        import torch
-        if torch.cuda.current_device() == self.device:
-            _check(fn(*args, _stream(self.stream)))
+            status = fn(*args, _stream(self.stream))
         else:
-            with torch.cuda.device(self.device):
-                _check(fn(*args, _stream(self.stream)))
+            import torch
+            stream = _current_stream(self.device) if self.stream is None else _stream(self.stream)
+            if torch.cuda.current_device() == self.device:
+                status = fn(*args, stream)
+            else:
+                with torch.cuda.device(self.device):
+                    status = fn(*args, stream)
+        if status != ZERO_OK:
+            _check(status)
 
 
 def zero_embed(plan: Plan, tensor: int, hidden: int, params, param_dt: int, tokens, scale: float, out, out_dt: int,
@@ -552,7 +592,8 @@ def zero_embed(plan: Plan, tensor: int, hidden: int, params, param_dt: int, toke
     par = c.flat(params, "params", _esize(param_dt), plan.psi_pad)
     tok, it, n = c.ids(tokens, "tokens", n, token_it)
     o, ostride = c.rows(out, "out", _esize(out_dt), n, hidden, out_stride)
-    c.issue("zero_embed", plan.handle, tensor, hidden, par, param_dt, tok, it, n, scale, c.drop(drop), o, out_dt,
+    keep = c.drop(drop)
+    c.issue(load().zero_embed, plan.handle, tensor, hidden, par, param_dt, tok, it, n, scale, keep, o, out_dt,
             ostride)
 
 
@@ -568,8 +609,8 @@ def zero_token_order(tokens, rows: int, sorted, order, workspace=None, stream=No
     tok, it, n = c.ids(tokens, "tokens", n, token_it)
     s = c.flat(sorted, "sorted", 4, n)
     o = c.flat(order, "order", 4, n)
-    ws, ws_bytes = c.workspace(workspace, zero_token_order_workspace_bytes(n, rows))
-    c.issue("zero_token_order", tok, it, n, rows, s, o, ws, ws_bytes)
+    ws, ws_bytes = c.workspace(workspace, lambda: zero_token_order_workspace_bytes(n, rows))
+    c.issue(load().zero_token_order, tok, it, n, rows, s, o, ws, ws_bytes)
 
 
 def zero_embed_grad_workspace_bytes(n: int, hidden: int) -> int:
@@ -590,8 +631,9 @@ def zero_embed_grad(plan: Plan, tensor: int, hidden: int, sorted, order, dy, dy_
     o = c.flat(order, "order", 4, n)
     y, ystride = c.rows(dy, "dy", _esize(dy_dt), n, hidden, dy_stride)
     d = c.flat(dst, "dst", _esize(dst_dt), plan.psi_pad if rank < 0 else plan.shard_total)
-    ws, ws_bytes = c.workspace(workspace, zero_embed_grad_workspace_bytes(n, hidden))
-    c.issue("zero_embed_grad", plan.handle, tensor, hidden, s, o, n, y, dy_dt, ystride, scale, c.drop(drop), d,
+    ws, ws_bytes = c.workspace(workspace, lambda: zero_embed_grad_workspace_bytes(n, hidden))
+    keep = c.drop(drop)
+    c.issue(load().zero_embed_grad, plan.handle, tensor, hidden, s, o, n, y, dy_dt, ystride, scale, keep, d,
             dst_dt, rank, 1 if accumulate else 0, ws, ws_bytes)
 
 
@@ -607,7 +649,8 @@ def zero_dropout(x, residual, out, dt: int, drop: Drop, stream=None, n: Optional
     xa = c.flat(x, "x", es, n)
     ra = c.flat(residual, "residual", es, n, optional=True)
     oa = c.flat(out, "out", es, n)
-    c.issue("zero_dropout", xa, ra, oa, n, dt, c.drop(drop))
+    keep = c.drop(drop)
+    c.issue(load().zero_dropout, xa, ra, oa, n, dt, keep)
 
 
 def zero_token_logp_workspace_bytes(n: int, vocab: int) -> int:
@@ -634,8 +677,8 @@ def zero_token_logp(logits, dt: int, labels, logp, stats, workspace=None, stream
     x, xstride = c.rows(logits, "logits", _esize(dt), n, v, stride)
     lp = c.flat(logp, "logp", 4, n)
     st = c.flat(stats, "stats", 4, 2 * n)
-    ws, ws_bytes = c.workspace(workspace, zero_token_logp_workspace_bytes(n, v))
-    c.issue("zero_token_logp", x, dt, n, v, xstride, lab, it, lp, st, ws, ws_bytes)
+    ws, ws_bytes = c.workspace(workspace, lambda: zero_token_logp_workspace_bytes(n, v))
+    c.issue(load().zero_token_logp, x, dt, n, v, xstride, lab, it, lp, st, ws, ws_bytes)
 
 
 def zero_preference_loss(offsets, labels, vocab: int, logp, ref_logp, beta: float, smoothing: float,
@@ -663,7 +706,7 @@ def zero_preference_loss(offsets, labels, vocab: int, logp, ref_logp, beta: floa
     pl = c.flat(pair_loss, "pair_loss", 4, pairs)
     rw = c.flat(rewards, "rewards", 4, 2 * pairs)
     co = c.flat(coef, "coef", 4, n)
-    c.issue("zero_preference_loss", pairs, off, oit, n, lab, lit, vocab, lp, ref, beta, smoothing, grad_scale, lo,
+    c.issue(load().zero_preference_loss, pairs, off, oit, n, lab, lit, vocab, lp, ref, beta, smoothing, grad_scale, lo,
             pl, rw, co)
 
 
@@ -680,4 +723,4 @@ def zero_token_logp_grad(logits, dt: int, labels, stats, coef, dlogits, stream=N
     st = c.flat(stats, "stats", 4, 2 * n)
     co = c.flat(coef, "coef", 4, n)
     d, dstride = c.rows(dlogits, "dlogits", es, n, v, dl_stride)
-    c.issue("zero_token_logp_grad", x, dt, n, v, xstride, lab, it, st, co, d, dstride)
+    c.issue(load().zero_token_logp_grad, x, dt, n, v, xstride, lab, it, st, co, d, dstride)
