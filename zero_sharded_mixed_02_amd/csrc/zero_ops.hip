@@ -136,6 +136,12 @@ __device__ __forceinline__ Raw<DT, N> from_float(const float (&x)[N]) {
   if constexpr (DT == ZERO_F32 || N == 1) {
 #pragma unroll
     for (int i = 0; i < N; ++i) r.w[i] = narrow<DT>(x[i]);
+  } else if constexpr (DT == ZERO_F16) {
+    typedef float f32x2 __attribute__((ext_vector_type(2)));
+    typedef _Float16 f16x2 __attribute__((ext_vector_type(2)));
+#pragma unroll
+    for (int i = 0; i < N / 2; ++i)   // one conversion for both halves
+      r.w[i] = __builtin_bit_cast(uint32_t, __builtin_convertvector(f32x2{x[2 * i], x[2 * i + 1]}, f16x2));
   } else {
 #pragma unroll
     for (int i = 0; i < N / 2; ++i) r.w[i] = narrow<DT>(x[2 * i]) | (narrow<DT>(x[2 * i + 1]) << 16);
@@ -153,6 +159,18 @@ __device__ __forceinline__ void pin(Raw<DT, N>& r) {
 
 __device__ __forceinline__ int64_t load_id(const void* p, int64_t i, int wide) {
   return wide ? ((const AS1 int64_t*)(uintptr_t)p)[i] : (int64_t)((const AS1 int32_t*)(uintptr_t)p)[i];
+}
+
+// K ids at once: the loads are issued together, whichever their type.
+template <int K>
+__device__ __forceinline__ void load_ids(const void* p, const int64_t (&i)[K], int wide, int64_t (&id)[K]) {
+  if (wide) {
+#pragma unroll
+    for (int k = 0; k < K; ++k) id[k] = ((const AS1 int64_t*)(uintptr_t)p)[i[k]];
+  } else {
+#pragma unroll
+    for (int k = 0; k < K; ++k) id[k] = ((const AS1 int32_t*)(uintptr_t)p)[i[k]];
+  }
 }
 
 // The table row an id names, or `rows` for a padding id.
@@ -257,14 +275,18 @@ __global__ __launch_bounds__(kEmbedThreads) void embed_kernel(const EmbedArgs a)
   void* const out = (char*)a.out + row0 * a.out_stride * es_of<ODT>;
   uint32_t row[kEmbedUnroll];             // behind row0
   int32_t col[kEmbedUnroll], id[kEmbedUnroll];
+  int64_t where[kEmbedUnroll], token[kEmbedUnroll];
 #pragma unroll
   for (int j = 0; j < kEmbedUnroll; ++j) {
     const uint32_t t = rem0 + j * kEmbedThreads + threadIdx.x;
     row[j] = row_in(t, (uint32_t)a.upr, a.magic);
     const int32_t c = (int32_t)(t - row[j] * (uint32_t)a.upr) * N;
     col[j] = c < a.hidden - N ? c : a.hidden - N;   // the last access ends with the row
-    id[j] = row[j] < left ? row_of(load_id(a.tokens, row0 + row[j], a.tok64), a.rows) : a.rows;
+    where[j] = row0 + (row[j] < left ? row[j] : 0);
   }
+  load_ids(a.tokens, where, a.tok64, token);
+#pragma unroll
+  for (int j = 0; j < kEmbedUnroll; ++j) id[j] = row_of(token[j], a.rows);
   Raw<TDT, N> raw[kEmbedUnroll];
   if (a.rows > 0) {
 #pragma unroll
@@ -299,9 +321,19 @@ __global__ __launch_bounds__(kRankThreads) void rank_kernel(const RankArgs a) {
   uint32_t* word = (uint32_t*)word4;
   constexpr int kSegs = kRankThreads / kRankItems;
   const int padded = (a.n + 4 * kSegs - 1) / (4 * kSegs) * (4 * kSegs);
-  for (int i = threadIdx.x; i < padded; i += kRankThreads)
-    word[i] = i < a.n ? ((uint32_t)row_of(load_id(a.tokens, i, a.tok64), a.rows) << kSmallSortPosBits) | (uint32_t)i
-                      : 0xffffffffu;
+  int64_t where[kSmallSort / kRankThreads], token[kSmallSort / kRankThreads];
+#pragma unroll
+  for (int k = 0; k < kSmallSort / kRankThreads; ++k) {
+    const int i = k * kRankThreads + threadIdx.x;
+    where[k] = i < a.n ? i : a.n - 1;
+  }
+  load_ids(a.tokens, where, a.tok64, token);
+#pragma unroll
+  for (int k = 0; k < kSmallSort / kRankThreads; ++k) {
+    const int i = k * kRankThreads + threadIdx.x;
+    if (i < padded)
+      word[i] = i < a.n ? ((uint32_t)row_of(token[k], a.rows) << kSmallSortPosBits) | (uint32_t)i : 0xffffffffu;
+  }
   if (threadIdx.x < kRankItems) count[threadIdx.x] = 0;
   __syncthreads();
   const int item = threadIdx.x % kRankItems, seg = threadIdx.x / kRankItems;
@@ -324,13 +356,27 @@ __global__ __launch_bounds__(kRankThreads) void rank_kernel(const RankArgs a) {
   }
 }
 
-__device__ __forceinline__ void radix_read(const RadixArgs& a, int64_t i, int32_t& key, int32_t& pos) {
+// K positions of a pass and their tokens, from index i on, 64 or more apart;
+// past the end the last one.
+template <int K>
+__device__ __forceinline__ void radix_read(const RadixArgs& a, int64_t i, int step, int32_t (&key)[K], int32_t (&pos)[K]) {
+  int64_t where[K];
+#pragma unroll
+  for (int k = 0; k < K; ++k) where[k] = i + k * step < a.n ? i + k * step : a.n - 1;
   if (a.first) {
-    key = row_of(load_id(a.tokens, i, a.tok64), a.rows);
-    pos = (int32_t)i;
+    int64_t token[K];
+    load_ids(a.tokens, where, a.tok64, token);
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+      key[k] = row_of(token[k], a.rows);
+      pos[k] = (int32_t)where[k];
+    }
   } else {
-    key = a.key_in[i];
-    pos = a.pos_in[i];
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+      key[k] = a.key_in[where[k]];
+      pos[k] = a.pos_in[where[k]];
+    }
   }
 }
 
@@ -344,10 +390,13 @@ __global__ __launch_bounds__(kSortThreads) void radix_count_kernel(const RadixAr
   const int64_t lo = (int64_t)blockIdx.x * a.tiles_per_block * a.tile;
   int64_t hi = lo + a.tiles_per_block * a.tile;
   if (hi > a.n) hi = a.n;
-  for (int64_t i = lo + threadIdx.x; i < hi; i += kSortThreads) {
-    int32_t key, pos;
-    radix_read(a, i, key, pos);
-    atomicAdd(&bin[((uint32_t)key >> a.shift) & mask], 1u);
+  constexpr int K = 2;
+  for (int64_t i = lo + threadIdx.x; i < hi; i += K * kSortThreads) {
+    int32_t key[K], pos[K];
+    radix_read(a, i, kSortThreads, key, pos);
+#pragma unroll
+    for (int k = 0; k < K; ++k)
+      if (i + k * kSortThreads < hi) atomicAdd(&bin[((uint32_t)key[k] >> a.shift) & mask], 1u);
   }
   __syncthreads();
   a.hist[(int64_t)blockIdx.x * kBins + threadIdx.x] = bin[threadIdx.x];
@@ -396,12 +445,7 @@ __global__ __launch_bounds__(kSortThreads) void radix_move_kernel(const RadixArg
     int32_t key[KEYS], pos[KEYS];
     uint32_t rank[KEYS];
     const int64_t first = lo + wave * (64 * KEYS) + lane;
-#pragma unroll
-    for (int k = 0; k < KEYS; ++k) {
-      const int64_t i = first + k * 64;
-      key[k] = pos[k] = 0;
-      if (i < a.n) radix_read(a, i, key[k], pos[k]);
-    }
+    radix_read(a, first, 64, key, pos);
 #pragma unroll
     for (int k = 0; k < KEYS; ++k) {
       const bool in = first + k * 64 < a.n;
