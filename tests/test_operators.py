@@ -78,7 +78,7 @@ def test_workspaces(Z):
         assert 8 * h <= b <= 8 * h * (n // 8 + 1)
     assert Z.zero_token_logp_workspace_bytes(0, 10) == 0
     assert Z.zero_token_logp_workspace_bytes(4096, 131072) == 0
-    assert Z.zero_token_logp_workspace_bytes(2, 131072) == 2 * 16 * 8
+    assert Z.zero_token_logp_workspace_bytes(2, 131072) == 2 * 8 * 8
 
 
 def _grad(Z, plan, tensor=1, hidden=8, sorted=P(0), order=P(1), n=10, dy=P(2), ydt=2, stride=8, scale=1.0, drop=None,

@@ -122,7 +122,11 @@ struct DropoutArgs {
 };
 
 constexpr int kLogpThreads = 512;
-constexpr int kLogpShortRow = 8192;      // rows shorter than this take one wave
+// Rows shorter than this take one wave instead of eight, and rows four times
+// as long where there are waves for all CUs anyway: 8192 rows of 2000 in 17 us
+// against 30 (bf16), of 16000 in 45 against 49.
+constexpr int kLogpShortRow = 8192;
+constexpr int kLogpManyRows = 4096;
 constexpr int kDlogitsThreads = 128;
 constexpr int kDlogitsUnroll = 2;
 constexpr int kDlogitsPiece = 2048;      // elements of a row per workgroup

@@ -265,13 +265,21 @@ __device__ __forceinline__ uint32_t row_in(uint32_t t, uint32_t upr, uint32_t ma
 
 // A thread owns kEmbedUnroll accesses of N elements, kEmbedThreads accesses apart,
 // numbered row by row through the output.
-template <int TDT, int ODT, int N>
+// DROP: 0 no dropout, 1 rows of whole accesses, so that the mask runs on with
+// the accesses, each starting a word of it, 2 any.
+template <int TDT, int ODT, int N, int DROP>
 __global__ __launch_bounds__(kEmbedThreads) void embed_kernel(const EmbedArgs a) {
   const int64_t u0 = (int64_t)blockIdx.x * (kEmbedThreads * kEmbedUnroll);
   const int64_t row0 = u0 / a.upr;
   const uint32_t rem0 = (uint32_t)(u0 - row0 * a.upr);
   const int64_t left = a.n - row0;   // rows from here on
-  const MaskBase mask = a.drop.cut ? mask_base(mask_key(a.drop), a.drop.first + row0 * a.hidden) : MaskBase{};
+  MaskBase mask{};
+  if constexpr (DROP == 1) {
+    mask = mask_base(mask_key(a.drop), a.drop.first + u0 * N);
+    mask.z += (uint64_t)(threadIdx.x * (N / 4)) * kGamma;
+  } else if constexpr (DROP == 2) {
+    mask = mask_base(mask_key(a.drop), a.drop.first + row0 * a.hidden);
+  }
   void* const out = (char*)a.out + row0 * a.out_stride * es_of<ODT>;
   uint32_t row[kEmbedUnroll];             // behind row0
   int32_t col[kEmbedUnroll], id[kEmbedUnroll];
@@ -303,7 +311,11 @@ __global__ __launch_bounds__(kEmbedThreads) void embed_kernel(const EmbedArgs a)
     to_float<TDT, N>(raw[j], x);
 #pragma unroll
     for (int i = 0; i < N; ++i) x[i] = id[j] < a.rows ? x[i] * a.f : 0.0f;
-    if (a.drop.cut) drop<N>(x, mask, row[j] * (uint32_t)a.hidden + col[j], a.drop.cut);
+    if constexpr (DROP == 1) {
+      drop<N, true>(x, MaskBase{mask.z + (uint64_t)(j * kEmbedThreads * (N / 4)) * kGamma, 0}, 0, a.drop.cut);
+    } else if constexpr (DROP == 2) {
+      drop<N>(x, mask, row[j] * (uint32_t)a.hidden + col[j], a.drop.cut);
+    }
     store<ODT, N, (N > 1)>(out, (int64_t)row[j] * a.out_stride + col[j], from_float<ODT, N>(x));
   }
 }
@@ -1220,8 +1232,13 @@ int launch_embed(const EmbedArgs& a, int tdt, int odt, bool vec, int64_t blocks,
   return by_type(tdt, [&](auto T) {
     return by_type(odt, [&](auto O) {
       constexpr int t = decltype(T)::value, o = decltype(O)::value;
-      if (vec) embed_kernel<t, o, vec_of(t, o)><<<(uint32_t)blocks, kEmbedThreads, 0, (hipStream_t)stream>>>(a);
-      else embed_kernel<t, o, 1><<<(uint32_t)blocks, kEmbedThreads, 0, (hipStream_t)stream>>>(a);
+      constexpr int n = vec_of(t, o);
+      const hipStream_t st = (hipStream_t)stream;
+      const uint32_t b = (uint32_t)blocks;
+      if (!vec) embed_kernel<t, o, 1, 2><<<b, kEmbedThreads, 0, st>>>(a);   // p = 0 keeps all
+      else if (!a.drop.cut) embed_kernel<t, o, n, 0><<<b, kEmbedThreads, 0, st>>>(a);
+      else if (a.hidden % n == 0 && a.drop.first % 4 == 0) embed_kernel<t, o, n, 1><<<b, kEmbedThreads, 0, st>>>(a);
+      else embed_kernel<t, o, n, 2><<<b, kEmbedThreads, 0, st>>>(a);
       return last();
     });
   });
@@ -1293,7 +1310,7 @@ int launch_logp(const LogpArgs& a, int dt, void* stream) {
   return by_type(dt, [&](auto D) {
     constexpr int d = decltype(D)::value;
     const uint32_t blocks = (uint32_t)(a.n * a.splits);
-    if (a.vocab < kLogpShortRow) logp_kernel<d, 64><<<blocks, 64, 0, (hipStream_t)stream>>>(a);
+    if (a.vocab < (a.n < kLogpManyRows ? kLogpShortRow : 4 * kLogpShortRow)) logp_kernel<d, 64><<<blocks, 64, 0, (hipStream_t)stream>>>(a);
     else logp_kernel<d, kLogpThreads><<<blocks, kLogpThreads, 0, (hipStream_t)stream>>>(a);
     return last();
   });

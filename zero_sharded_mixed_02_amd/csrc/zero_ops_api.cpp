@@ -138,19 +138,30 @@ SortShape sort_shape(int64_t n, int64_t rows) {
   return s;
 }
 
-// Positions per chunk: as many as leave the GPU about 4096 waves, within
-// [8, 64].
-int64_t grad_chunk(int64_t n, int64_t hidden) {
-  const int64_t tiles = ceil_div(hidden, kJoinTile);
-  const int64_t want = ceil_div(n * tiles, 4096 * 8) * 8;
+// Positions per chunk, of the `part` that an owner holds of all of them: as
+// many as leave the GPU about 4096 waves, within [8, 64], but no fewer than
+// the workspace is made for (16384 waves of all positions).  Longer chunks
+// write fewer partial rows (n = 32768 x 768: 53 us at 24, 59 at 8), shorter ones
+// give a slice's few chunks more waves (an eighth of 65536 x 2048: 58 us at
+// 64, 48 at 32).
+int64_t chunk_for(int64_t n, int64_t hidden, int64_t waves, double part) {
+  const double tiles = (double)ceil_div(hidden, 256);
+  const int64_t want = ((int64_t)((double)n * part * tiles / (double)waves) + 7) / 8 * 8;
   return std::min<int64_t>(64, std::max<int64_t>(8, want));
 }
 
+int64_t least_chunk(int64_t n, int64_t hidden) { return chunk_for(n, hidden, 16384, 1.0); }
+
+int64_t grad_chunk(int64_t n, int64_t hidden, double part) {
+  return std::max(least_chunk(n, hidden), chunk_for(n, hidden, 4096, part));
+}
+
 // Workgroups per row: one where the rows fill the GPU, else enough for about
-// 1024, each with 8192 elements or more.
+// 1024, each with 16384 elements or more (two rows of 131072 in 7.2 us; 7.9 at
+// 8192, 10.2 at 4096, for the pieces that the join then reads).
 int64_t logp_splits(int64_t n, int64_t vocab) {
   if (n <= 0 || n >= 1024) return 1;
-  return std::max<int64_t>(1, std::min<int64_t>(ceil_div(1024, n), vocab / 8192));
+  return std::max<int64_t>(1, std::min<int64_t>(ceil_div(1024, n), vocab / 16384));
 }
 
 int64_t dlogits_splits(int64_t vocab) { return std::max<int64_t>(1, ceil_div(vocab, kDlogitsPiece)); }
@@ -290,7 +301,7 @@ zero_status zero_token_order(const void* tokens, zero_itype token_it, int64_t n,
 
 size_t zero_embed_grad_workspace_bytes(int64_t n, int64_t hidden) {
   if (n <= 0 || n > kMaxTokens || hidden < 1 || hidden > kMaxHidden) return 0;
-  return (size_t)(2 * ceil_div(n, grad_chunk(n, hidden))) * (size_t)hidden * 4;
+  return (size_t)(2 * ceil_div(n, least_chunk(n, hidden))) * (size_t)hidden * 4;
 }
 
 zero_status zero_embed_grad(zero_plan_t p, int32_t tensor, int64_t hidden, const int32_t* sorted,
@@ -356,7 +367,7 @@ zero_status zero_embed_grad(zero_plan_t p, int32_t tensor, int64_t hidden, const
     // Eight columns a lane, unless four leave fewer lanes of the last tile idle.
     int vec = hidden < 4 ? 1 : 4;
     if (vec_of(dy_dt, dst_dt) == 8 && hidden >= 8 && ceil_div(hidden, 512) * 2 == ceil_div(hidden, 256)) vec = 8;
-    a.chunk = (int32_t)grad_chunk(n, hidden);
+    a.chunk = (int32_t)grad_chunk(n, hidden, (double)(a.hi - a.lo) / (double)numel);
     a.n_chunks = (int32_t)ceil_div(n, a.chunk);
     a.tiles = (int32_t)ceil_div(hidden, 64 * vec);
     // Zero rows: 128 KiB a workgroup, down to 8 KiB where that leaves fewer than
