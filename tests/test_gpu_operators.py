@@ -777,3 +777,111 @@ def test_a_training_step_from_tokens_to_parameters(gpu, zero_lib):
     moved = R.to64(master) - w[:S]
     big = np.abs(want) > 1e-3 * np.abs(want).max()
     assert np.all(np.sign(moved[big]) == -np.sign(want[big]))
+
+
+# ---------------------------------------------------------------------------
+# Offsets past 32 bits
+# ---------------------------------------------------------------------------
+
+@pytest.mark.big
+def test_embed_and_grad_past_32_bits(gpu, zero_lib):
+    """A table of 2.4e9 elements behind an odd-sized tensor: the rows that are
+    named, the last ones among them, and zeros everywhere else."""
+    import torch
+    Z = zero_lib
+    rows, hidden, before, n = 300_001, 8192, 5, 211
+    say("[big] embed and its gradient")
+    plan = Z.zero_plan(before + rows * hidden, 1, [before, rows * hidden], 0, 1)
+    g = torch.Generator(device=gpu).manual_seed(1)
+    buf = torch.empty(plan.psi_pad, dtype=torch.bfloat16, device=gpu).normal_(generator=g)
+    ids = torch.randint(0, rows, (n,), generator=g, device=gpu)
+    ids[:4] = torch.tensor([rows - 1, rows - 2, 0, rows], device=gpu)
+    ids[100:130] = rows - 1
+    good = ids < rows
+    table = buf[before:].view(rows, hidden)
+    out = torch.empty((n, hidden), dtype=torch.bfloat16, device=gpu)
+    Z.zero_embed(plan, 1, hidden, buf, BF16, ids, 3.0, out, BF16)
+    want = torch.where(good[:, None], table[ids.clamp(max=rows - 1)].float() * 3.0, 0.0).bfloat16()
+    assert torch.equal(out, want)             # one product, one rounding: the same bits
+    del table
+    dy = torch.empty((n, hidden), dtype=torch.bfloat16, device=gpu).normal_(generator=g)
+    buf.fill_(7)
+    s, o = order_of(torch, Z, ids, rows)
+    ws = torch.empty(Z.zero_embed_grad_workspace_bytes(n, hidden), dtype=torch.uint8, device=gpu)
+    Z.zero_embed_grad(plan, 1, hidden, s, o, dy, BF16, 1.0, buf, BF16, workspace=ws)
+    torch.cuda.synchronize()
+    assert bool((buf[:before] == 7).all())
+    grad = buf[before:].view(rows, hidden)
+    named = torch.unique(ids[good])
+    idn = ids.cpu().numpy()
+    for r in named.tolist():
+        rows_of = R.to64(dy[torch.from_numpy(np.flatnonzero(idn == r)).to(gpu)])
+        w, mag = rows_of.sum(0), np.abs(rows_of).sum(0)
+        tol = mag * (len(rows_of) * 1.01 + 3) * U
+        R.check(R.to64(grad[r]), w, tol + R.half_step(np.abs(w) + tol, BF16), f"row {r}")
+    grad[named] = 0
+    assert not bool(torch.any(grad.view(torch.int16)))
+
+
+@pytest.mark.big
+def test_embed_grad_of_many_activations(gpu, zero_lib):
+    """dy of 2.4e9 elements, a third of it one token: some columns at both ends
+    against 64 bits."""
+    import torch
+    Z = zero_lib
+    n, rows, hidden = 300_001, 1000, 8192
+    say("[big] gradient of many activations")
+    g = torch.Generator(device=gpu).manual_seed(2)
+    dy = torch.empty((n, hidden), dtype=torch.bfloat16, device=gpu).normal_(generator=g)
+    ids = torch.randint(-1, rows, (n,), generator=g, device=gpu)
+    ids[::3] = 17
+    plan = Z.zero_plan(rows * hidden, 1, [rows * hidden], 0, 1)
+    s, o = order_of(torch, Z, ids, rows)
+    ws = torch.empty(Z.zero_embed_grad_workspace_bytes(n, hidden), dtype=torch.uint8, device=gpu)
+    grad = torch.empty(plan.psi_pad, dtype=torch.float32, device=gpu)
+    Z.zero_embed_grad(plan, 0, hidden, s, o, dy, BF16, 1.0, grad, F32, workspace=ws)
+    cols = torch.tensor([0, 1, 255, 256, 4095, hidden - 9, hidden - 2, hidden - 1], device=gpu)
+    want, bound = R.embed_grad(ids.cpu().numpy(), R.to64(dy[:, cols]), rows, 1.0, None)
+    R.check(R.to64(grad[:rows * hidden].view(rows, hidden)[:, cols]), want, bound, "columns")
+
+
+@pytest.mark.big
+def test_logits_past_32_bits(gpu, zero_lib):
+    """2.6e9 logits: the first and the last rows, forward and in place backward."""
+    import torch
+    Z = zero_lib
+    n, vocab = 20_003, 131_071
+    say("[big] logits")
+    g = torch.Generator(device=gpu).manual_seed(3)
+    x = torch.empty((n, vocab), dtype=torch.bfloat16, device=gpu).normal_(0, 2, generator=g)
+    labels = torch.randint(0, vocab, (n,), generator=g, device=gpu)
+    lp, st = torch.empty(n, device=gpu), torch.empty(2 * n, device=gpu)
+    Z.zero_token_logp(x, BF16, labels, lp, st)
+    pick = [0, 1, 2, 16_383, 16_384, 16_385, n - 2, n - 1]       # 2^31 elements lie before row 16384
+    x64, lab = R.to64(x[pick]), labels[pick].cpu().numpy()
+    top, ls, want = R.softmax_rows(x64, lab)
+    e = R.logsum_bound(vocab)
+    R.check(R.to64(lp[pick]), want, e + np.abs(want) * 2 * U, "logp")
+    Z.zero_token_logp_grad(x, BF16, labels, st, torch.ones(n, device=gpu), x)
+    z = x64 - top[:, None]
+    p = np.exp(z - ls[:, None])
+    hot = np.zeros_like(p)
+    hot[np.arange(len(pick)), lab] = 1
+    d = hot - p
+    tol = p * ((5 * (np.abs(z) + ls[:, None]) + 4) * U + e) + 2 * U * (hot + p)
+    R.check(R.to64(x[pick]), d, tol + R.half_step(np.abs(d) + tol, BF16) + 2.0 ** -126, "dlogits")
+
+
+@pytest.mark.big
+def test_dropout_past_32_bits(gpu, zero_lib):
+    import torch
+    Z = zero_lib
+    n = (1 << 31) + 1001
+    say("[big] dropout")
+    x = torch.ones(n, dtype=torch.bfloat16, device=gpu)
+    Z.zero_dropout(x, None, x, BF16, Z.Drop(0.25, 9, 8, 7, first=3))
+    torch.cuda.synchronize()
+    for a in (0, (1 << 31) - 500, n - 1000):
+        keep = R.mask_block(9, 8, 7, 0.25, 3 + a, 1000)
+        want = torch.where(torch.from_numpy(keep), torch.tensor(4 / 3, dtype=torch.float32).bfloat16(), torch.zeros((), dtype=torch.bfloat16))
+        assert torch.equal(x[a:a + 1000].cpu(), want)

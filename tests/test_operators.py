@@ -3,11 +3,16 @@ entries and of the binding (all before anything is launched), the workspace
 sizes, and the plain forms the GPU tests compare with against each other."""
 import ctypes
 import math
+import os
+import shutil
+import subprocess
 
 import numpy as np
 import pytest
 
 from tests import ops_reference as R
+
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 
 BASE = 1 << 40        # fake addresses, never dereferenced
 GIB = 1 << 30
@@ -193,3 +198,20 @@ def test_reference_preference_by_hand():
     assert abs(loss - math.log(1 + math.exp(-0.5))) < 1e-15
     assert np.allclose(rewards, [-0.5, -1.0])
     assert np.allclose(coef, np.array([-1, 1]) * 0.5 / (1 + math.exp(0.5)))
+
+
+@pytest.mark.skipif(shutil.which("g++") is None, reason="g++ not available")
+def test_launch_shapes(tmp_path):
+    """The host code with stand-ins for the launchers, over a few thousand
+    random sizes, types and owners: every launch covers its work and stays
+    inside its workspace (tests/native/ops_shapes.cpp)."""
+    exe = tmp_path / "ops_shapes"
+    csrc = os.path.join(ROOT, "zero_sharded_mixed_02_amd", "csrc")
+    cmd = ["g++", "-std=c++17", "-O1", "-g", "-fsanitize=address,undefined", "-fno-sanitize-recover=undefined", "-Wall",
+           "-Werror", "-I", os.path.join(ROOT, "include"), "-I", csrc, os.path.join(ROOT, "tests", "native", "ops_shapes.cpp"),
+           os.path.join(csrc, "zero_api.cpp"), os.path.join(csrc, "zero_ops_api.cpp"), "-o", str(exe)]
+    subprocess.run(cmd, check=True, capture_output=True, text=True)
+    env = dict(os.environ, ASAN_OPTIONS="detect_leaks=1:verify_asan_link_order=0")
+    r = subprocess.run([str(exe)], capture_output=True, text=True, env=env, timeout=300)
+    assert r.returncode == 0, r.stdout + r.stderr
+    assert " 0 failures" in r.stdout
