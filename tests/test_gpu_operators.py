@@ -104,7 +104,7 @@ def test_embed(gpu, zero_lib, case):
     plan = Z.zero_plan(before + rows * hidden + 11, 3, [before, rows * hidden, 11], 0, 1)
     params = randn(torch, gpu, rng, plan.psi_pad, tdt)
     ids_t, ids = as_ids(torch, gpu, make_ids(rng, n, rows, kind), wide)
-    drop, spec = make_drop(Z, p, first=rng.integers(0, 9))
+    drop, spec = make_drop(Z, p, first=int(rng.integers(0, 9)) + (hidden % 2 << 40))
     stride = hidden + gap
     g = Guarded(torch, gpu, max(0, n * stride), R.torch_type(odt))
     out = g.t.view(n, stride)[:, :hidden]
@@ -202,7 +202,7 @@ def test_embed_grad(gpu, zero_lib, case, accumulate):
     ids_t, ids = as_ids(torch, gpu, make_ids(rng, n, rows, kind), n % 3 != 0)
     wide = randn(torch, gpu, rng, (n, hidden + gap), ydt)
     dy = wide[:, :hidden]
-    drop, spec = make_drop(Z, p, first=int(rng.integers(0, 9)))
+    drop, spec = make_drop(Z, p, first=int(rng.integers(0, 9)) + (hidden % 2 << 40))
     s, o = order_of(torch, Z, ids_t, rows)
     ws = torch.empty(max(1, Z.zero_embed_grad_workspace_bytes(n, hidden)), dtype=torch.uint8, device=gpu)
     scale = 0.37
@@ -234,6 +234,45 @@ def test_embed_grad(gpu, zero_lib, case, accumulate):
             R.check(got[lo:hi], np.where(here, base + w, base), np.where(here, tol, 0.0), f"rank {rank}")
         else:
             R.check(got[lo:hi], w, np.where(here, b + R.half_step(np.abs(w) + b, gdt) + 2.0 ** -149, 0.0), f"rank {rank}")
+
+
+@pytest.mark.parametrize("first", [0, 1, 4])
+@pytest.mark.parametrize("hidden", [64, 66, 520])
+def test_embed_and_grad_in_a_later_bucket(gpu, zero_lib, hidden, first):
+    """A table whose bucket is not the plan's first, so that an owner's slice
+    holds it behind other buckets' parts; masks that start a word and that do
+    not."""
+    import torch
+    Z = zero_lib
+    n, rows, n_d = 900, 60, 3
+    rng = np.random.default_rng(hidden + first)
+    sizes = [500, 33, rows * hidden, 77]
+    plan = Z.zero_plan(sum(sizes), n_d, sizes, 540, 4)
+    assert plan.tensor(2)[0] == 1 and plan.n_buckets == 3
+    ids_t, ids = as_ids(torch, gpu, make_ids(rng, n, rows, "wild"), True)
+    drop, spec = make_drop(Z, 0.3, first=first)
+    params = randn(torch, gpu, rng, plan.psi_pad, BF16)
+    off = plan.tensor(2)[1]
+    y = torch.empty((n, hidden), dtype=torch.bfloat16, device=gpu)
+    Z.zero_embed(plan, 2, hidden, params, BF16, ids_t, 0.5, y, BF16, drop=drop)
+    want = R.embed(R.to64(params[off:off + rows * hidden]).reshape(rows, hidden), ids, 0.5, spec)
+    R.check(R.to64(y), want, np.abs(want) * 3 * U + R.half_step(want * (1 + 3 * U), BF16), "embed")
+    dy = randn(torch, gpu, rng, (n, hidden), F16)
+    s, o = order_of(torch, Z, ids_t, rows)
+    ws = torch.empty(Z.zero_embed_grad_workspace_bytes(n, hidden), dtype=torch.uint8, device=gpu)
+    want, bound = (v.ravel() for v in R.embed_grad(ids, R.to64(dy), rows, 0.5, spec))
+    tol = bound + R.half_step(np.abs(want) + bound, F16)
+    _, _, _, share, shard_off = plan.bucket(1)
+    flat_off = plan.bucket(1)[0]
+    for rank in range(n_d):
+        dst = torch.full((plan.shard_total,), 5, dtype=torch.float16, device=gpu)
+        Z.zero_embed_grad(plan, 2, hidden, s, o, dy, F16, 0.5, dst, F16, drop=drop, rank=rank, workspace=ws)
+        got = R.to64(dst)
+        at = flat_off + rank * share - off              # tensor element of the slice's part of this bucket
+        lo, hi = max(0, at), min(rows * hidden, at + share)
+        a, b = shard_off + lo - at, shard_off + hi - at
+        R.check(got[a:b], want[lo:hi], tol[lo:hi], f"rank {rank}")
+        assert (got[:a] == 5).all() and (got[b:] == 5).all()
 
 
 def test_embed_grad_repeats_bit_for_bit(gpu, zero_lib):

@@ -515,29 +515,39 @@ class _Call:
             if n > 0:
                 raise ValueError(f"{name} is None")
             return 0, width
-        if isinstance(x, int):
-            return x, width if stride is None else stride
-        if not hasattr(x, "data_ptr") or not hasattr(x, "element_size"):
+        try:   # the common case, as above
+            device = x.get_device()
+            if (device >= 0 and (self.device is None or device == self.device) and x.numel() == n * width
+                    and x.element_size() == esize and x.is_contiguous()):
+                self.device = device
+                return x.data_ptr(), width
+        except AttributeError:
+            if isinstance(x, int):
+                return x, width if stride is None else stride
             raise TypeError(f"{name}: expected a torch tensor or an integer device address, got {type(x).__name__}")
         if x.element_size() != esize:
             raise ValueError(f"{name}: elements of {x.element_size()} bytes ({x.dtype}), expected {esize}")
         if x.numel() != n * width:
             raise ValueError(f"{name} holds {x.numel()} elements, expected {n} rows of {width}")
         self.see(x, name)
-        if x.is_contiguous():
-            return x.data_ptr(), width
         if x.dim() != 2 or x.shape[1] != width or (width > 1 and x.stride(1) != 1) or (n > 1 and x.stride(0) < width):
             raise ValueError(f"{name}: rows must be contiguous (shape {tuple(x.shape)}, strides {x.stride()})")
         return x.data_ptr(), x.stride(0) if n > 1 else width
 
     def ids(self, x, name: str, n, it):
         """(address, integer type, count) of an id list."""
-        if x is None or isinstance(x, int):
+        try:   # the common case, as above
+            device, kind = x.get_device(), _ID_TYPES.get(x.dtype)
+            if (kind is not None and device >= 0 and (self.device is None or device == self.device)
+                    and x.is_contiguous() and (n is None or n == x.numel())):
+                self.device = device
+                return x.data_ptr(), kind, x.numel()
+        except AttributeError:
+            if x is not None and not isinstance(x, int):
+                raise TypeError(f"{name}: expected a torch tensor or an integer device address, got {type(x).__name__}")
             if n is None or it is None:
                 raise ValueError(f"{name} is not a tensor: pass its count and integer type")
             return _addr(x), it, int(n)
-        if not hasattr(x, "data_ptr") or not hasattr(x, "element_size"):
-            raise TypeError(f"{name}: expected a torch tensor or an integer device address, got {type(x).__name__}")
         kind = _id_type(x.dtype)
         if kind is None:
             raise ValueError(f"{name} must be int32 or int64, got {x.dtype}")
@@ -556,7 +566,7 @@ class _Call:
         if not hasattr(x, "data_ptr") or not x.is_contiguous():
             raise ValueError("workspace must be a contiguous tensor or an integer device address")
         self.see(x, "workspace")
-        return x.data_ptr(), x.numel() * x.element_size()
+        return x.data_ptr(), x.nbytes
 
     def drop(self, d):
         if d is None:
