@@ -108,7 +108,7 @@ int launch_grad(const GradArgs& a, int ydt, int gdt, int vec, int64_t blocks, vo
   EXPECT(a.n == 0 || in_ws(a.part, 2 * (int64_t)a.n_chunks * a.hidden * 4), "partial rows outside the workspace");
   EXPECT(vec == 1 || (vec == 4 && a.hidden >= 4) || (vec == 8 && a.hidden >= 8 && vec_of(ydt, gdt) == 8), "vec %d", vec);
   EXPECT((int64_t)a.tiles * 64 * vec >= a.hidden, "tiles");
-  EXPECT(a.chunk_blocks * (kGradThreads / 64) >= (int64_t)a.n_chunks * a.tiles, "chunk blocks");
+  EXPECT(a.chunk_blocks == (a.n_chunks + kGradChunks - 1) / kGradChunks * (int64_t)a.tiles, "chunk blocks");
   EXPECT(a.fill_rows >= 1 && a.fill_rows <= 1024, "fill rows %d", a.fill_rows);
   EXPECT((int64_t)a.fill_rows * a.hidden < (int64_t(1) << 31), "fill units");
   EXPECT(a.lo >= 0 && a.lo < a.hi && a.hi <= g_rows * g_hidden, "range");

@@ -82,6 +82,7 @@ struct RadixArgs {
 // Gradient of the table: positions in token order are cut into chunks of
 // `chunk`; see zero_ops.hip.
 constexpr int kGradThreads = 256;
+constexpr int kGradChunks = kGradThreads / 64;   // neighbouring chunks of a workgroup, one a wave
 constexpr int kJoinThreads = 512;
 constexpr int kJoinTile = 256;           // columns of a workgroup in the join
 constexpr int kJoinChunks = 16;          // chunks it looks after

@@ -506,14 +506,16 @@ __global__ __launch_bounds__(kSortThreads) void radix_move_kernel(const RadixArg
 // ---------------------------------------------------------------------------
 //
 // The positions in token order are cut into chunks of equal length, whatever
-// their tokens, so that a token that makes up half a batch costs no more than
-// rare ones.  A wave owns one chunk and one tile of columns and sums its runs
-// of equal tokens in fp32 registers.  A run inside a chunk is finished there.
-// One that crosses a boundary leaves a partial row (fp32, in the workspace) in
-// each chunk it touches: slot 2c of chunk c if it came in from the chunk
-// before, slot 2c + 1 if it begins in c and goes on; the join kernel adds
-// those up in order.  Further workgroups of the same launch write zeros to the
-// rows that no token names.
+// their tokens, so that frequent tokens spread over as many waves as rare ones.
+// A wave owns one chunk and one tile of columns and sums its runs of equal
+// tokens in fp32 registers.  A run inside a chunk is finished there.  One that
+// crosses a boundary leaves a partial row (fp32, in the workspace) in each
+// chunk it touches: slot 2c of chunk c if it came in from the chunk before,
+// slot 2c + 1 if it begins in c and goes on.  A workgroup's waves own
+// neighbouring chunks: where one run passes through all of them, they add up
+// their rows first, and slot 2c of the first holds the sum.  The join kernel
+// adds the partial rows in order.  Further workgroups of the same launch write
+// zeros to the rows that no token names.
 
 // First indices in [0, n) whose sorted token is >= key0 and >= key1 (n if
 // none), found by a whole wave: both at once, 64 probes each at a time.
@@ -663,88 +665,115 @@ __global__ __launch_bounds__(kGradThreads) void grad_kernel(const GradArgs a) {
     fill_rows<GDT>(a, (int64_t)blockIdx.x - a.chunk_blocks);
     return;
   }
-  __shared__ float bounce[kGradThreads / 64][64 * N];
+  __shared__ float bounce[kGradChunks][64 * N];
+  __shared__ int through[kGradChunks];
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
-  const int64_t w = (int64_t)blockIdx.x * (kGradThreads / 64) + wave;
-  const int64_t c = w / a.tiles;
-  if (c >= a.n_chunks) return;
-  const int32_t tile = (int32_t)(w - c * a.tiles) * 64 * N;
+  const int64_t group = blockIdx.x / (uint32_t)a.tiles;
+  const int64_t c = group * kGradChunks + wave;
+  const int32_t tile = (int32_t)(blockIdx.x - group * a.tiles) * 64 * N;
   const int32_t begin = tile + lane * N;
   const bool on = begin < a.hidden;
   const int32_t col = begin < a.hidden - N ? begin : a.hidden - N;
   const bool whole = !a.accumulate || tile + 64 * N <= a.hidden || a.hidden % N == 0;
-
-  // The chunk's tokens and positions, one a lane (a chunk has at most 64).
-  const int64_t s = c * a.chunk;
-  const int len = (int)(s + a.chunk < a.n ? a.chunk : a.n - s);
-  const int64_t mine = s + (lane < len ? lane : len - 1);
-  const int32_t rows = a.sorted[mine], from = a.order[mine];
-  const int32_t before = a.sorted[s > 0 ? s - 1 : 0], after = a.sorted[s + len < a.n ? s + len : 0];
-  const int32_t poss = (uint32_t)from < (uint64_t)a.n ? from : -1;
-  const uint64_t here = __ballot(lane < len && rows >= a.row_lo && rows < a.row_hi);
-  if (!here) return;
-  const int p0 = __builtin_ctzll(here), p1 = 64 - __builtin_clzll(here);   // what is written, in sorted rows
-  const int32_t left_of = __shfl_up(rows, 1);   // by all lanes: a lane reads only from active ones
-  const uint64_t starts = __ballot(lane > 0 && lane < len && rows != left_of);
-  bool head = p0 == 0 && s > 0 && before == __builtin_amdgcn_readlane(rows, 0);   // came in from the chunk before
-  const bool goes_on = p1 == len && s + len < a.n && after == __builtin_amdgcn_readlane(rows, len - 1);
-  const uint64_t key = DROP ? mask_key(a.drop) : 0;
-
-  // Rows in a batch.  From HBM eight at a time are faster (65536 x 8192: 397 us
-  // against 403), from the Infinity Cache four (32768 x 768: 51 against 54).
-  constexpr int U = NT ? 8 : 4;
   float acc[N];
 #pragma unroll
   for (int i = 0; i < N; ++i) acc[i] = 0.0f;
-  auto fetch = [&](int q, Raw<YDT, N>& raw) {
-    const int32_t pos = __builtin_amdgcn_readlane(poss, q < p1 ? q : p1 - 1);
-    raw = load<YDT, N, NT>((const char*)a.dy + (int64_t)(pos < 0 ? 0 : pos) * a.dy_stride * es_of<YDT>, col);
+
+  // Sums the wave's chunk; true if all of it belongs to a run that came in and
+  // goes on, whose sum is then left in acc.
+  auto sum_chunk = [&]() -> bool {
+    // The chunk's tokens and positions, one a lane (a chunk has at most 64).
+    const int64_t s = c * a.chunk;
+    const int len = (int)(s + a.chunk < a.n ? a.chunk : a.n - s);
+    const int64_t mine = s + (lane < len ? lane : len - 1);
+    const int32_t rows = a.sorted[mine], from = a.order[mine];
+    const int32_t before = a.sorted[s > 0 ? s - 1 : 0], after = a.sorted[s + len < a.n ? s + len : 0];
+    const int32_t poss = (uint32_t)from < (uint64_t)a.n ? from : -1;
+    const uint64_t here = __ballot(lane < len && rows >= a.row_lo && rows < a.row_hi);
+    if (!here) return false;
+    const int p0 = __builtin_ctzll(here), p1 = 64 - __builtin_clzll(here);   // what is written, in sorted rows
+    const int32_t left_of = __shfl_up(rows, 1);   // by all lanes: a lane reads only from active ones
+    const uint64_t starts = __ballot(lane > 0 && lane < len && rows != left_of);
+    bool head = p0 == 0 && s > 0 && before == __builtin_amdgcn_readlane(rows, 0);   // came in from the chunk before
+    const bool goes_on = p1 == len && s + len < a.n && after == __builtin_amdgcn_readlane(rows, len - 1);
+    const bool whole_run = head && goes_on && !starts;
+    const uint64_t key = DROP ? mask_key(a.drop) : 0;
+
+    // Rows in a batch.  From HBM eight at a time are faster (65536 x 8192: 397 us
+    // against 403), from the Infinity Cache four (32768 x 768: 51 against 54).
+    constexpr int U = NT ? 8 : 4;
+    auto fetch = [&](int q, Raw<YDT, N>& raw) {
+      const int32_t pos = __builtin_amdgcn_readlane(poss, q < p1 ? q : p1 - 1);
+      raw = load<YDT, N, NT>((const char*)a.dy + (int64_t)(pos < 0 ? 0 : pos) * a.dy_stride * es_of<YDT>, col);
+    };
+    Raw<YDT, N> cur[U], next[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) fetch(p0 + u, cur[u]);
+    for (int b = p0; b < p1; b += U) {
+      // The next positions' rows are on their way while these are summed.
+      if (b + U < p1) {
+#pragma unroll
+        for (int u = 0; u < U; ++u) fetch(b + U + u, next[u]);
+      }
+      const int n = p1 - b < U ? p1 - b : U;
+      int u0 = 0;
+      while (u0 < n) {
+        // The run of position b + u0 ends before `end`, in this batch or later.
+        const uint64_t later = b + u0 < 63 ? starts >> (b + u0 + 1) << (b + u0 + 1) : 0;
+        int end = later ? __builtin_ctzll(later) : p1;
+        if (end > p1) end = p1;
+        const int u1 = end - b < n ? end - b : n;
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+          if (u < u0 || u >= u1) continue;
+          const int32_t pos = __builtin_amdgcn_readlane(poss, b + u);
+          if (pos < 0) continue;
+          float x[N];
+          pin(cur[u]);
+          to_float<YDT, N>(cur[u], x);
+          if constexpr (DROP != 0)
+            drop<N, DROP == 1>(x, mask_base(key, a.drop.first + (int64_t)pos * a.hidden), (uint32_t)col, a.drop.cut);
+#pragma unroll
+          for (int i = 0; i < N; ++i) acc[i] += x[i];
+        }
+        u0 = u1;
+        if (end - b > n) break;   // it goes on in the next batch
+        if (whole_run) return true;
+        const int32_t row = __builtin_amdgcn_readlane(rows, end - 1);
+        const bool tail = end == p1 && goes_on;
+        if (row >= a.row_lo && row < a.row_hi) {
+          if (!head && !tail) write_row<GDT, N>(a, row, col, begin, on, whole, acc, bounce[wave]);
+          else if (on) write_part<N>(a, 2 * c + (head ? 0 : 1), col, acc);
+        }
+        head = false;
+#pragma unroll
+        for (int i = 0; i < N; ++i) acc[i] = 0.0f;
+      }
+#pragma unroll
+      for (int u = 0; u < U; ++u) cur[u] = next[u];
+    }
+    return false;
   };
-  Raw<YDT, N> cur[U], next[U];
+  const bool pass = c < a.n_chunks && sum_chunk();
+  if (lane == 0) through[wave] = pass;
+  __syncthreads();
+  bool all = true;
 #pragma unroll
-  for (int u = 0; u < U; ++u) fetch(p0 + u, cur[u]);
-  for (int b = p0; b < p1; b += U) {
-    // The next positions' rows are on their way while these are summed.
-    if (b + U < p1) {
+  for (int w = 0; w < kGradChunks; ++w) all &= through[w] != 0;
+  if (!all) {
+    if (pass && on) write_part<N>(a, 2 * c, col, acc);
+    return;
+  }
 #pragma unroll
-      for (int u = 0; u < U; ++u) fetch(b + U + u, next[u]);
-    }
-    const int n = p1 - b < U ? p1 - b : U;
-    int u0 = 0;
-    while (u0 < n) {
-      // The run of position b + u0 ends before `end`, in this batch or later.
-      const uint64_t later = b + u0 < 63 ? starts >> (b + u0 + 1) << (b + u0 + 1) : 0;
-      int end = later ? __builtin_ctzll(later) : p1;
-      if (end > p1) end = p1;
-      const int u1 = end - b < n ? end - b : n;
+  for (int i = 0; i < N; ++i) bounce[wave][lane * N + i] = acc[i];
+  __syncthreads();
+  if (wave == 0 && on) {
 #pragma unroll
-      for (int u = 0; u < U; ++u) {
-        if (u < u0 || u >= u1) continue;
-        const int32_t pos = __builtin_amdgcn_readlane(poss, b + u);
-        if (pos < 0) continue;
-        float x[N];
-        pin(cur[u]);
-        to_float<YDT, N>(cur[u], x);
-        if constexpr (DROP != 0)
-          drop<N, DROP == 1>(x, mask_base(key, a.drop.first + (int64_t)pos * a.hidden), (uint32_t)col, a.drop.cut);
+    for (int w = 1; w < kGradChunks; ++w)
 #pragma unroll
-        for (int i = 0; i < N; ++i) acc[i] += x[i];
-      }
-      u0 = u1;
-      if (end - b > n) break;   // it goes on in the next batch
-      const int32_t row = __builtin_amdgcn_readlane(rows, end - 1);
-      const bool tail = end == p1 && goes_on;
-      if (row >= a.row_lo && row < a.row_hi) {
-        if (!head && !tail) write_row<GDT, N>(a, row, col, begin, on, whole, acc, bounce[wave]);
-        else if (on) write_part<N>(a, 2 * c + (head ? 0 : 1), col, acc);
-      }
-      head = false;
-#pragma unroll
-      for (int i = 0; i < N; ++i) acc[i] = 0.0f;
-    }
-#pragma unroll
-    for (int u = 0; u < U; ++u) cur[u] = next[u];
+      for (int i = 0; i < N; ++i) acc[i] += bounce[w][lane * N + i];
+    write_part<N>(a, 2 * c, col, acc);
   }
 }
 
@@ -779,22 +808,41 @@ __global__ __launch_bounds__(kJoinThreads) void grad_join_kernel(const GradArgs 
   const bool lots = has && far < a.n && last == row;
   const uint64_t runs = __ballot(has), many = __ballot(more), longs = __ballot(lots);
 
-  // Sums partial rows [j0, j1) of the run that begins in chunk c.
-  auto sum = [&](int64_t c, int64_t j0, int64_t j1, float (&acc)[N]) {
+  // The partial rows of the run from chunk c to chunk l: the one of c, single
+  // chunks up to a group that it passes through, such groups, single chunks.
+  struct Run {
+    int64_t c, first, groups, group0, rest0, count;
+  };
+  auto run_of = [&](int64_t c, int64_t l) {
+    const int64_t g0 = (c + kGradChunks) / kGradChunks, g1 = l / kGradChunks;   // groups [g0, g1)
+    Run r;
+    r.c = c;
+    r.groups = g1 > g0 ? g1 - g0 : 0;
+    r.first = r.groups ? g0 * kGradChunks - (c + 1) : l - c;
+    r.group0 = g0 * kGradChunks;
+    r.rest0 = g1 * kGradChunks;
+    r.count = 1 + r.first + r.groups + (r.groups ? l - r.rest0 + 1 : 0);
+    return r;
+  };
+  // Sums its partial rows [j0, j1).
+  auto sum = [&](const Run& run, int64_t j0, int64_t j1, float (&acc)[N]) {
 #pragma unroll
     for (int i = 0; i < N; ++i) acc[i] = 0.0f;
     if (!on) return;
 #pragma unroll 8
     for (int64_t j = j0; j < j1; ++j) {
-      const int64_t slot = j == 0 ? 2 * c + 1 : 2 * (c + j);
+      const int64_t k = j - 1 - run.first;
+      const int64_t chunk = k < 0 ? run.c + j : k < run.groups ? run.group0 + k * kGradChunks : run.rest0 + (k - run.groups);
+      const int64_t slot = 2 * chunk + (j == 0);
       float x[N];
       to_float<ZERO_F32, N>(load<ZERO_F32, N>(a.part, slot * a.hidden + col), x);
 #pragma unroll
       for (int i = 0; i < N; ++i) acc[i] += x[i];
     }
   };
-  auto parts = [&](int64_t c, int32_t r) {   // partial rows of that run
-    return (wave_lower_bound(a.sorted, a.n, (int64_t)r + 1) - 1) / a.chunk - c + 1;
+  auto last_chunk = [&](int64_t c, int32_t r) {   // of the run of row r
+    const int64_t l = (wave_lower_bound(a.sorted, a.n, (int64_t)r + 1) - 1) / a.chunk;
+    return l > c ? l : c;
   };
   int k = 0;
   for (uint64_t left = runs & ~longs; left; left &= left - 1, ++k) {
@@ -802,19 +850,19 @@ __global__ __launch_bounds__(kJoinThreads) void grad_join_kernel(const GradArgs 
     const int l = __builtin_ctzll(left);
     const int64_t c = c0 + l;
     const int32_t r = __builtin_amdgcn_readlane(row, l);
-    const int64_t count = (many >> l) & 1 ? parts(c, r) : 2;
+    const Run run = run_of(c, (many >> l) & 1 ? last_chunk(c, r) : c + 1);
     float acc[N];
-    sum(c, 0, count, acc);
+    sum(run, 0, run.count, acc);
     write_row<GDT, N>(a, r, col, begin, on, whole, acc, piece[wave]);
   }
   for (uint64_t left = longs; left; left &= left - 1) {   // the same in every wave
     const int l = __builtin_ctzll(left);
     const int64_t c = c0 + l;
     const int32_t r = __builtin_amdgcn_readlane(row, l);
-    const int64_t count = parts(c, r);
-    const int64_t per = (count + kWaves - 1) / kWaves, j0 = wave * per;
+    const Run run = run_of(c, last_chunk(c, r));
+    const int64_t per = (run.count + kWaves - 1) / kWaves, j0 = wave * per;
     float acc[N];
-    sum(c, j0, j0 + per < count ? j0 + per : count, acc);
+    sum(run, j0, j0 + per < run.count ? j0 + per : run.count, acc);
     __syncthreads();
 #pragma unroll
     for (int i = 0; i < N; ++i) piece[wave][lane * N + i] = acc[i];

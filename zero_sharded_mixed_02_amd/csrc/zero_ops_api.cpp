@@ -375,7 +375,7 @@ zero_status zero_embed_grad(zero_plan_t p, int32_t tensor, int64_t hidden, const
     const int64_t row_bytes = hidden * esize(dst_dt);
     const int64_t fill_bytes = std::max<int64_t>(8192, std::min<int64_t>(131072, (a.row_hi - a.row_lo) * row_bytes / 2048));
     a.fill_rows = (int32_t)std::max<int64_t>(1, std::min<int64_t>(1024, fill_bytes / row_bytes));
-    a.chunk_blocks = ceil_div((int64_t)a.n_chunks * a.tiles, kGradThreads / 64);
+    a.chunk_blocks = ceil_div(a.n_chunks, kGradChunks) * a.tiles;
     a.stream_dy = n * hidden * esize(dy_dt) > kInfinityCache;
     const int64_t blocks = a.chunk_blocks + (accumulate ? 0 : ceil_div(a.row_hi - a.row_lo, a.fill_rows));
     if (zero_status st = check_blocks(blocks)) return st;
