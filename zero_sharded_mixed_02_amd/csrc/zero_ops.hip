@@ -700,9 +700,9 @@ __global__ __launch_bounds__(kGradThreads) void grad_kernel(const GradArgs a) {
     const bool whole_run = head && goes_on && !starts;
     const uint64_t key = DROP ? mask_key(a.drop) : 0;
 
-    // Rows in a batch.  From HBM eight at a time are faster (65536 x 8192: 397 us
-    // against 403), from the Infinity Cache four (32768 x 768: 51 against 54).
-    constexpr int U = NT ? 8 : 4;
+    // Rows in a batch.  Eight gain under 1% where dy comes from HBM (2^20 x 768)
+    // and lose 4% where it sits in the Infinity Cache (32768 x 768).
+    constexpr int U = 4;
     auto fetch = [&](int q, Raw<YDT, N>& raw) {
       const int32_t pos = __builtin_amdgcn_readlane(poss, q < p1 ? q : p1 - 1);
       raw = load<YDT, N, NT>((const char*)a.dy + (int64_t)(pos < 0 ? 0 : pos) * a.dy_stride * es_of<YDT>, col);
