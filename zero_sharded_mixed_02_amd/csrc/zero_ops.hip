@@ -553,31 +553,15 @@ __device__ __forceinline__ int64_t wave_lower_bound(const int32_t* sorted, int64
   return a;
 }
 
-// A finished row's value at one element, from its sum.
-template <int GDT>
-__device__ __forceinline__ void write_one(const GradArgs& a, int64_t e, float sum) {
-  float x[1] = {sum * a.f};
-  if (a.accumulate) {
-    float old[1];
-    to_float<GDT, 1>(load<GDT, 1>(a.dst, e - a.lo), old);
-    x[0] = old[0] + x[0];
-  }
-  store<GDT, 1>(a.dst, e - a.lo, from_float<GDT, 1>(x));
-}
-
-// Writes N columns of a finished row, the whole wave together.  `begin` is
-// the first column that this lane owns (col < begin where its access was
-// moved back), `whole` says that no lane's access was, or that writing a value
-// twice does no harm.  Rows that the written range cuts, and moved accesses
-// that add to dst, go element by element, through shared memory so that the
-// loop needs no registers by index.
+// Writes N columns of a finished row; `begin` is the first column that this
+// lane owns (col < begin where its access was moved back: written twice with
+// the same value, but added to dst once).
 template <int GDT, int N>
-__device__ __forceinline__ void write_row(const GradArgs& a, int32_t row, int32_t col, int32_t begin, bool on,
-                                          bool whole, const float (&sum)[N], float* lds) {
-  const int64_t e = (int64_t)row * a.hidden;
-  if (whole && e >= a.lo && e + a.hidden <= a.hi) {
-    if (!on) return;
-    void* dst = (char*)a.dst + (e - a.lo) * es_of<GDT>;
+__device__ __forceinline__ void write_row(const GradArgs& a, int32_t row, int32_t col, int32_t begin,
+                                          const float (&sum)[N]) {
+  const int64_t row_e = (int64_t)row * a.hidden, e = row_e + col;
+  void* const dst = (char*)a.dst + (row_e - a.lo) * es_of<GDT>;   // of the row's first column
+  if (e >= a.lo && e + N <= a.hi && (begin == col || !a.accumulate)) {
     float x[N];
 #pragma unroll
     for (int i = 0; i < N; ++i) x[i] = sum[i] * a.f;
@@ -590,13 +574,23 @@ __device__ __forceinline__ void write_row(const GradArgs& a, int32_t row, int32_
     store<GDT, N, (N > 1)>(dst, col, from_float<GDT, N>(x));
     return;
   }
-  float* mine = lds + (threadIdx.x & 63) * N;
+  bool mine[N];
+  float old[N];
 #pragma unroll
-  for (int i = 0; i < N; ++i) mine[i] = sum[i];
-  if (!on) return;
-#pragma unroll 1
-  for (int i = 0; i < N; ++i)
-    if (col + i >= begin && e + col + i >= a.lo && e + col + i < a.hi) write_one<GDT>(a, e + col + i, mine[i]);
+  for (int i = 0; i < N; ++i) {
+    mine[i] = col + i >= begin && e + i >= a.lo && e + i < a.hi;
+    old[i] = 0.0f;
+    if (mine[i] && a.accumulate) {
+      float v[1];
+      to_float<GDT, 1>(load<GDT, 1>(dst, col + i), v);
+      old[i] = v[0];
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    const float x[1] = {a.accumulate ? old[i] + sum[i] * a.f : sum[i] * a.f};
+    if (mine[i]) store<GDT, 1>(dst, col + i, from_float<GDT, 1>(x));
+  }
 }
 
 template <int N>
@@ -675,7 +669,6 @@ __global__ __launch_bounds__(kGradThreads) void grad_kernel(const GradArgs a) {
   const int32_t begin = tile + lane * N;
   const bool on = begin < a.hidden;
   const int32_t col = begin < a.hidden - N ? begin : a.hidden - N;
-  const bool whole = !a.accumulate || tile + 64 * N <= a.hidden || a.hidden % N == 0;
   float acc[N];
 #pragma unroll
   for (int i = 0; i < N; ++i) acc[i] = 0.0f;
@@ -743,8 +736,12 @@ __global__ __launch_bounds__(kGradThreads) void grad_kernel(const GradArgs a) {
         const int32_t row = __builtin_amdgcn_readlane(rows, end - 1);
         const bool tail = end == p1 && goes_on;
         if (row >= a.row_lo && row < a.row_hi) {
-          if (!head && !tail) write_row<GDT, N>(a, row, col, begin, on, whole, acc, bounce[wave]);
-          else if (on) write_part<N>(a, 2 * c + (head ? 0 : 1), col, acc);
+          if (!on) {
+          } else if (!head && !tail) {
+            write_row<GDT, N>(a, row, col, begin, acc);
+          } else {
+            write_part<N>(a, 2 * c + (head ? 0 : 1), col, acc);
+          }
         }
         head = false;
 #pragma unroll
@@ -792,7 +789,6 @@ __global__ __launch_bounds__(kJoinThreads) void grad_join_kernel(const GradArgs 
   const int32_t begin = tile + lane * N;
   const bool on = begin < a.hidden;
   const int32_t col = begin < a.hidden - N ? begin : a.hidden - N;
-  const bool whole = !a.accumulate || tile + 64 * N <= a.hidden || a.hidden % N == 0;
 
   const int64_t c0 = (int64_t)blockIdx.x * kJoinChunks;
   const int64_t mine = c0 + lane, s = mine * a.chunk, e = s + a.chunk;
@@ -853,7 +849,7 @@ __global__ __launch_bounds__(kJoinThreads) void grad_join_kernel(const GradArgs 
     const Run run = run_of(c, (many >> l) & 1 ? last_chunk(c, r) : c + 1);
     float acc[N];
     sum(run, 0, run.count, acc);
-    write_row<GDT, N>(a, r, col, begin, on, whole, acc, piece[wave]);
+    if (on) write_row<GDT, N>(a, r, col, begin, acc);
   }
   for (uint64_t left = longs; left; left &= left - 1) {   // the same in every wave
     const int l = __builtin_ctzll(left);
@@ -871,7 +867,7 @@ __global__ __launch_bounds__(kJoinThreads) void grad_join_kernel(const GradArgs 
       for (int v = 1; v < kWaves; ++v)
 #pragma unroll
         for (int i = 0; i < N; ++i) acc[i] += piece[v][lane * N + i];
-      write_row<GDT, N>(a, r, col, begin, on, whole, acc, piece[0]);
+      if (on) write_row<GDT, N>(a, r, col, begin, acc);
     }
   }
 }

@@ -139,15 +139,15 @@ SortShape sort_shape(int64_t n, int64_t rows) {
 }
 
 // Positions per chunk, of the `part` that an owner holds of all of them: as
-// many as leave the GPU about 4096 waves, within [16, 64], but no fewer than
+// many as leave the GPU about 4096 waves, within [4, 64], but no fewer than
 // the workspace is made for (16384 waves of all positions).  Longer chunks
 // write fewer partial rows (32768 x 768: 53 us at 24, 59 at 8), shorter ones
 // give a slice's few chunks more waves (an eighth of 65536 x 2048: 58 us at
 // 64, 48 at 32).
 int64_t chunk_for(int64_t n, int64_t hidden, int64_t waves, double part) {
   const double tiles = (double)ceil_div(hidden, 256);
-  const int64_t want = (int64_t)((double)n * part * tiles / (double)waves + 7.0) / 8 * 8;
-  return std::min<int64_t>(64, std::max<int64_t>(16, want));
+  const int64_t want = (int64_t)((double)n * part * tiles / (double)waves + 3.0) / 4 * 4;
+  return std::min<int64_t>(64, std::max<int64_t>(4, want));
 }
 
 int64_t least_chunk(int64_t n, int64_t hidden) { return chunk_for(n, hidden, 16384, 1.0); }
