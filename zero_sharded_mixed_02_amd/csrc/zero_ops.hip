@@ -10,6 +10,9 @@
 // memory at any address; where a row's length is no multiple of an access, its
 // last access is moved back to end with the row.
 //
+// Times below are of single launches on one MI355X.  There a large copy moves
+// 6.0 TB/s (read and written together) and a large read 7.1 TB/s.
+//
 // Floating point: compiled with -ffp-contract=off; fused multiply-adds are
 // written out where they are meant.
 #include <hip/hip_runtime.h>
@@ -33,7 +36,6 @@ typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
 // The same at element alignment.
 typedef uint32_t u32x4h __attribute__((ext_vector_type(4), aligned(2)));
 typedef uint32_t u32x2h __attribute__((ext_vector_type(2), aligned(2)));
-typedef uint32_t u32x4w __attribute__((ext_vector_type(4), aligned(4)));
 
 constexpr float kLog2eHi = 1.44269504f;                                   // fp32(log2 e)
 constexpr float kLog2eLo = (float)(1.4426950408889634 - (double)kLog2eHi);
@@ -214,11 +216,13 @@ __device__ __forceinline__ MaskBase mask_base(uint64_t key, int64_t position) {
 
 // Zeroes the dropped ones among N elements whose first stands `local` behind
 // the shared position.  One mix64 gives four elements 16 bits each, so a group
-// that starts inside a word takes one word more and shifts.  16 bits an element and not
-// 32 halve the generator's work, which at 32 bits would be as long as the
-// memory traffic of a 16-bit tensor; p is a multiple of 2^-16 for it.
-// A draw is compared where it stands: the upper half of a register against
-// cut << 16 (cut < 65536 here; p = 1 drops everything without draws).
+// that starts inside a word takes one word more and shifts.  16 bits an
+// element and not 32 halve the generator's work: two 64-bit products a word,
+// at 20 cycles a wave each, are already a third of the arithmetic of the
+// lookup (65536 x 8192 fp16: 250 us without dropout, 283 with); p is a
+// multiple of 2^-16 for it.  A draw is compared where it stands: the upper half of a
+// register against cut << 16 (cut < 65536 here; p = 1 drops everything
+// without draws).
 // ALIGNED: every group starts a word (the positions are multiples of 4).
 template <int N, bool ALIGNED = false>
 __device__ __forceinline__ void drop(float (&x)[N], const MaskBase& b, uint32_t local, uint32_t cut) {
@@ -263,8 +267,15 @@ __device__ __forceinline__ uint32_t row_in(uint32_t t, uint32_t upr, uint32_t ma
   return magic ? __umulhi(t, magic) : t;
 }
 
-// A thread owns kEmbedUnroll accesses of N elements, kEmbedThreads accesses apart,
-// numbered row by row through the output.
+// y[i, :] = keep(i, :) * f * table[token[i], :].  A thread owns kEmbedUnroll
+// accesses of N elements, kEmbedThreads accesses apart, numbered row by row
+// through the output, so that every lane has work at any row length; their ids
+// are loaded together, then their rows.  Bound by the output's stores beside
+// row reads that the caches serve in part: 65536 rows of 8192 fp16 of skewed
+// ids in 250 us, 1.07 GB written and 0.27 GB of different rows (5.4 TB/s; 283 us
+// with dropout).  Stores are non-temporal (8% there); one, two or eight
+// accesses a thread take 343, 291 and 266 us, and walking the table in column
+// tiles, for more hits in the L2, 268 us and more.
 // DROP: 0 no dropout, 1 rows of whole accesses, so that the mask runs on with
 // the accesses, each starting a word of it, 2 any.
 template <int TDT, int ODT, int N, int DROP>
@@ -326,7 +337,9 @@ __global__ __launch_bounds__(kEmbedThreads) void embed_kernel(const EmbedArgs a)
 
 // Few positions: the place of position i is the number of positions whose
 // (token, position) is smaller, counted outright: n^2 comparisons of one word
-// that holds both, all over the chip, in one launch.
+// that holds both, all over the chip, in one launch.  Bound by the comparisons
+// (two instructions each): 2.8 us for 37 positions, 7.8 for 8192, where the
+// radix passes below take 17.4; at twice as many it would lose.
 __global__ __launch_bounds__(kRankThreads) void rank_kernel(const RankArgs a) {
   __shared__ uint4 word4[kSmallSort / 4];
   __shared__ int count[kRankItems];
@@ -393,7 +406,8 @@ __device__ __forceinline__ void radix_read(const RadixArgs& a, int64_t i, int st
 }
 
 // One stable pass by `bits` bits of the token.  Each workgroup owns a run of
-// tiles; this counts its digits.
+// tiles; this counts its digits.  A pass is bound by latency: 50257 tokens take
+// two, 18 us for 65536 positions and 54 for 2^20.
 __global__ __launch_bounds__(kSortThreads) void radix_count_kernel(const RadixArgs a) {
   __shared__ uint32_t bin[kBins];
   bin[threadIdx.x] = 0;
@@ -516,6 +530,13 @@ __global__ __launch_bounds__(kSortThreads) void radix_move_kernel(const RadixArg
 // their rows first, and slot 2c of the first holds the sum.  The join kernel
 // adds the partial rows in order.  Further workgroups of the same launch write
 // zeros to the rows that no token names.
+//
+// Bound by HBM at the large end: 65536 x 8192 bf16 with dropout into 50257 rows
+// takes 372 us for 1.07 GB read and 0.85 GB written (5.2 TB/s) and 17 us for the
+// join.  How often a token repeats does not matter: 2^20 positions of 768 take
+// 355 us evenly spread and 364 us all of one token.  At GPT-2-small's size
+// (8192 x 768, 20 + 6 us) 77 MB of mostly zero rows and the latencies of search,
+// gather and join count.
 
 // First indices in [0, n) whose sorted token is >= key0 and >= key1 (n if
 // none), found by a whole wave: both at once, 64 probes each at a time.
@@ -607,6 +628,8 @@ __device__ __forceinline__ void write_part(const GradArgs& a, int64_t slot, int3
   }
 }
 
+// Zero rows of one workgroup, behind the chunks in the grid: before them, or
+// mixed with them, the whole is 4-12% slower (65536 x 8192).
 template <int GDT>
 __device__ void fill_rows(const GradArgs& a, int64_t block) {
   __shared__ uint8_t named[1024];
@@ -653,6 +676,9 @@ __device__ void fill_rows(const GradArgs& a, int64_t block) {
 }
 
 // DROP: 0 no dropout, 1 every access starts a word of the mask, 2 any.
+// NT: dy is read past the caches, which is faster where it exceeds the Infinity
+// Cache (2^20 x 768: 528 us against 544) and slower where it may sit there
+// (32768 x 768: 64 against 54), as it does when the backward pass just wrote it.
 template <int YDT, int GDT, int N, int DROP, bool NT>
 __global__ __launch_bounds__(kGradThreads) void grad_kernel(const GradArgs a) {
   if ((int64_t)blockIdx.x >= a.chunk_blocks) {
@@ -777,8 +803,9 @@ __global__ __launch_bounds__(kGradThreads) void grad_kernel(const GradArgs a) {
 // Joins runs that cross chunk boundaries: their partial rows in chunk order.
 // A workgroup looks after the runs that begin in kJoinChunks chunks, for one
 // tile of columns.  A lane each finds out which chunks have one; short runs go
-// to a wave each, and long ones are cut into one piece a wave, joined in order
-// in shared memory.
+// to a wave each, and long ones (64 chunks and more) are cut into one piece a
+// wave, joined in order in shared memory.  Bound by latency: 6 us after 8192 x
+// 768, 17 after 65536 x 8192.
 template <int GDT, int N>
 __global__ __launch_bounds__(kJoinThreads) void grad_join_kernel(const GradArgs a) {
   constexpr int kWaves = kJoinThreads / 64;
@@ -896,6 +923,10 @@ __device__ __forceinline__ void dropout_one(const DropoutArgs& a, const MaskBase
   store<DT, N, (N > 1)>(a.out, e, from_float<DT, N>(x));
 }
 
+// out = residual + keep * f * x, one access a thread: short workgroups keep
+// loads and stores flowing side by side.  Bound by HBM: 2^26 bf16 elements with a
+// residual in 62 us (6.5 TB/s); 65 at two accesses a thread, 69 at four, 75
+// with cached accesses.
 template <int DT, int N>
 __global__ __launch_bounds__(kDropoutThreads) void dropout_kernel(const DropoutArgs a) {
   const int64_t e0 = (int64_t)blockIdx.x * (kDropoutThreads * N);   // first element of the workgroup
@@ -981,9 +1012,13 @@ __device__ __forceinline__ void write_stats(const LogpArgs& a, int64_t t, int64_
   a.logp[t] = (float)(((double)y[0] - (double)m) - ls);
 }
 
-// One row, or one of `splits` pieces of a row, per workgroup.  Loads are
-// aligned: the elements before the first 16-byte boundary of the row and
-// behind the last one are taken singly.
+// log softmax at the label, in one pass over the logits with a running maximum
+// and sum in every thread.  One row, or one of `splits` pieces of a row, per
+// workgroup.  Loads are aligned: the elements before the first 16-byte boundary
+// of the row and behind the last one are taken singly.  Bound by HBM: 12288 scored
+// rows of 131072 bf16 in 480 us (6.7 TB/s), 6144 of 50257 in 95 us (6.5 TB/s).
+// Loads past the caches gain 10% at the large end; the last kCachedBytes of
+// rows go through them, for the gradient that may follow.
 template <int DT, int THREADS>
 __global__ __launch_bounds__(THREADS) void logp_kernel(const LogpArgs a) {
   constexpr int N = 16 / es_of<DT>;
@@ -1065,7 +1100,11 @@ __global__ __launch_bounds__(64) void logp_join_kernel(const LogpArgs a) {
   write_stats<DT>(a, t, label, m, s);
 }
 
-// Gradient of the logits: one piece of a row per workgroup.
+// Gradient of the logits, coef (onehot - softmax): one piece of a row per
+// workgroup, the last rows first.  Bound by HBM: 16384 rows of 131072 bf16, 12288 of
+// them scored, in 1173 us for 7.5 GB (6.4 TB/s).  Short workgroups do best: with
+// the forward pass 1637 us at 128 threads of two accesses, 1697 at 256, 1810 at
+// four accesses, 2000 and more at one; cached stores cost another 3%.
 template <int DT>
 __global__ __launch_bounds__(kDlogitsThreads) void dlogits_kernel(const LogpArgs a) {
   constexpr int N = 16 / es_of<DT>;
@@ -1228,7 +1267,8 @@ __global__ __launch_bounds__(64) void mean_kernel(const PrefArgs a) {
 }
 
 // Few pairs of few rows: all of it in one workgroup and one launch, a wave per
-// pair.
+// pair (48 rows: 4 us, and a launch less; 8192 rows would take 8 us longer than
+// the two launches).
 __global__ __launch_bounds__(kPrefThreads) void preference_small_kernel(const PrefArgs a) {
   __shared__ float loss[kPrefThreads / 64];
   const int wave = threadIdx.x / 64, lane = threadIdx.x % 64;
