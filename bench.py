@@ -1319,6 +1319,32 @@ def copy_probe(torch):
     print(json.dumps({"probe": "copy", "bytes_read_per_dispatch": 4 * n, "bytes_written_per_dispatch": 4 * n}))
 
 
+def operators_run(torch):
+    """Times the vocabulary operators over the cases of perf/operators.py, with
+    the launches queued back to back (two states in turn, so that a call finds
+    another call's data in the caches); one JSON line."""
+    import importlib.util
+    spec = importlib.util.spec_from_file_location("operator_cases", os.path.join(ROOT, "perf", "operators.py"))
+    cases = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(cases)
+    cases.own = True
+    out = {}
+    for case in cases.listed():
+        states = [cases.prepare(case, seed) for seed in (1, 2)]
+        turn = [0]
+
+        def run():
+            turn[0] ^= 1
+            cases.run(states[turn[0]])
+        ms = _time_launches(torch, run)
+        nbytes = cases.work(case)["bytes"]
+        out[case["name"]] = {"us": round(ms * 1e3, 2), "needed_bytes": round(nbytes), "gbps": round(nbytes / ms / 1e6, 1)}
+        log(f"{case['name']}: {ms * 1e3:.2f} us")
+        del states
+        release(torch)
+    print(json.dumps({"metric": "vocabulary operators, us a call", "data": "synthetic", "operators": out}))
+
+
 def main():
     ap = argparse.ArgumentParser()
     ap.add_argument("--gpus", type=int, default=1)
@@ -1348,6 +1374,9 @@ def main():
                     help="summarise --counter-run counter CSVs into a bytes-per-element table and exit")
     ap.add_argument("--copy-probe", action="store_true",
                     help="time a plain 4 GiB device copy (calibrates HBM byte counters)")
+    ap.add_argument("--operators", action="store_true",
+                    help="time the embedding, dropout and preference-loss operators over the cases of "
+                         "perf/operators.py, print one JSON line and exit")
     ap.add_argument("--no-cpu-baseline", action="store_true")
     ap.add_argument("--kernels", action="store_true",
                     help="also time every entry point at its own workload (adds a 'kernels' object)")
@@ -1395,6 +1424,11 @@ def main():
         return
     if args.copy_probe:
         copy_probe(torch)
+        return
+    if args.operators:
+        from __graft_entry__ import _ensure_built
+        _ensure_built()
+        operators_run(torch)
         return
     from synth.workloads import WORKLOADS, GpuRun
     from __graft_entry__ import _ensure_built
