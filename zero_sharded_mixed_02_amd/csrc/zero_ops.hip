@@ -214,21 +214,21 @@ __device__ __forceinline__ MaskBase mask_base(uint64_t key, int64_t position) {
   return MaskBase{key + (uint64_t)((position >> 2) + 1) * kGamma, (uint32_t)position & 3u};
 }
 
-// Zeroes the dropped ones among N elements whose first stands `local` behind
-// the shared position.  One mix64 gives four elements 16 bits each, so a group
-// that starts inside a word takes one word more and shifts.  16 bits an
-// element and not 32 halve the generator's work: two 64-bit products a word,
-// at 20 cycles a wave each, are already a third of the arithmetic of the
-// lookup (65536 x 8192 fp16: 250 us without dropout, 283 with); p is a
-// multiple of 2^-16 for it.  A draw is compared where it stands: the upper half of a
-// register against cut << 16 (cut < 65536 here; p = 1 drops everything
-// without draws).
+// Zeroes the dropped ones among N elements, as they lie in memory, whose first
+// stands `local` behind the shared position: before any arithmetic, so that
+// what is dropped may hold anything.  One mix64 gives four elements 16 bits
+// each, so a group that starts inside a word takes one word more and shifts.
+// 16 bits an element and not 32 halve the generator's work, which is what
+// dropout costs (a lookup of 65536 x 8192 fp16 takes 250 us without and 270
+// with it); p is a multiple of 2^-16 for it.  Two draws are compared at once,
+// beside the two 16-bit elements they decide on: draw - (cut - 1), held at 0
+// below, is 0 for a dropped one, and at most 1 it is the factor of the
+// element's bits (0 < cut < 65536; p = 1 drops everything without draws).
 // ALIGNED: every group starts a word (the positions are multiples of 4).
-template <int N, bool ALIGNED = false>
-__device__ __forceinline__ void drop(float (&x)[N], const MaskBase& b, uint32_t local, uint32_t cut) {
+template <int DT, int N, bool ALIGNED = false>
+__device__ __forceinline__ void drop(Raw<DT, N>& r, const MaskBase& b, uint32_t local, uint32_t cut) {
   if (cut > 0xffffu) {
-#pragma unroll
-    for (int i = 0; i < N; ++i) x[i] = 0.0f;
+    r = Raw<DT, N>{};
     return;
   }
   const uint32_t p = b.sub + local;
@@ -247,11 +247,23 @@ __device__ __forceinline__ void drop(float (&x)[N], const MaskBase& b, uint32_t 
       w[0] >>= off;
     }
   }
+  if constexpr (DT != ZERO_F32 && N > 1) {
+    const uint32_t below = (cut - 1) * 0x10001u;
 #pragma unroll
-  for (int i = 0; i < N; ++i) {
-    const uint32_t half = (uint32_t)(w[i / 4] >> (32 * (i / 2 % 2)));
-    const bool keep = i % 2 ? half >= (cut << 16) : (uint16_t)half >= (uint16_t)cut;
-    x[i] = keep ? x[i] : 0.0f;
+    for (int i = 0; i < N / 2; ++i) {
+      const uint32_t draw = (uint32_t)(w[i / 2] >> (32 * (i % 2)));
+      uint32_t keep;   // as instructions, since the compiler makes two compares and two selects of it
+      asm("v_pk_sub_u16 %0, %1, %2 clamp" : "=v"(keep) : "v"(draw), "s"(below));
+      asm("v_pk_min_u16 %0, %1, %2" : "=v"(keep) : "v"(keep), "s"(0x10001u));
+      asm("v_pk_mul_lo_u16 %0, %1, %2" : "=v"(r.w[i]) : "v"(r.w[i]), "v"(keep));
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const uint32_t half = (uint32_t)(w[i / 4] >> (32 * (i / 2 % 2)));
+      const bool keep = i % 2 ? half >= (cut << 16) : (uint16_t)half >= (uint16_t)cut;
+      r.w[i] = keep ? r.w[i] : 0;
+    }
   }
 }
 
@@ -272,7 +284,7 @@ __device__ __forceinline__ uint32_t row_in(uint32_t t, uint32_t upr, uint32_t ma
 // through the output, so that every lane has work at any row length; their ids
 // are loaded together, then their rows.  Bound by the output's stores beside
 // row reads that the caches serve in part: 65536 rows of 8192 fp16 of skewed
-// ids in 250 us, 1.07 GB written and 0.27 GB of different rows (5.4 TB/s; 283 us
+// ids in 250 us, 1.07 GB written and 0.27 GB of different rows (5.4 TB/s; 270 us
 // with dropout).  Stores are non-temporal (8% there); one, two or eight
 // accesses a thread take 343, 291 and 266 us, and walking the table in column
 // tiles, for more hits in the L2, 268 us and more.
@@ -318,15 +330,16 @@ __global__ __launch_bounds__(kEmbedThreads) void embed_kernel(const EmbedArgs a)
 #pragma unroll
   for (int j = 0; j < kEmbedUnroll; ++j) {
     if (row[j] >= left) continue;
+    if (id[j] >= a.rows) raw[j] = Raw<TDT, N>{};   // a padding id
+    if constexpr (DROP == 1) {
+      drop<TDT, N, true>(raw[j], MaskBase{mask.z + (uint64_t)(j * kEmbedThreads * (N / 4)) * kGamma, 0}, 0, a.drop.cut);
+    } else if constexpr (DROP == 2) {
+      if (a.drop.cut) drop<TDT, N>(raw[j], mask, row[j] * (uint32_t)a.hidden + col[j], a.drop.cut);
+    }
     float x[N];
     to_float<TDT, N>(raw[j], x);
 #pragma unroll
-    for (int i = 0; i < N; ++i) x[i] = id[j] < a.rows ? x[i] * a.f : 0.0f;
-    if constexpr (DROP == 1) {
-      drop<N, true>(x, MaskBase{mask.z + (uint64_t)(j * kEmbedThreads * (N / 4)) * kGamma, 0}, 0, a.drop.cut);
-    } else if constexpr (DROP == 2) {
-      drop<N>(x, mask, row[j] * (uint32_t)a.hidden + col[j], a.drop.cut);
-    }
+    for (int i = 0; i < N; ++i) x[i] = x[i] * a.f;
     store<ODT, N, (N > 1)>(out, (int64_t)row[j] * a.out_stride + col[j], from_float<ODT, N>(x));
   }
 }
@@ -750,9 +763,10 @@ __global__ __launch_bounds__(kGradThreads) void grad_kernel(const GradArgs a) {
           if (pos < 0) continue;
           float x[N];
           pin(cur[u]);
-          to_float<YDT, N>(cur[u], x);
           if constexpr (DROP != 0)
-            drop<N, DROP == 1>(x, mask_base(key, a.drop.first + (int64_t)pos * a.hidden), (uint32_t)col, a.drop.cut);
+            drop<YDT, N, DROP == 1>(cur[u], mask_base(key, a.drop.first + (int64_t)pos * a.hidden), (uint32_t)col,
+                                    a.drop.cut);
+          to_float<YDT, N>(cur[u], x);
 #pragma unroll
           for (int i = 0; i < N; ++i) acc[i] += x[i];
         }
@@ -905,15 +919,13 @@ __global__ __launch_bounds__(kJoinThreads) void grad_join_kernel(const GradArgs 
 
 template <int DT, int N>
 __device__ __forceinline__ void dropout_one(const DropoutArgs& a, const MaskBase& mask, int64_t e0, uint32_t local,
-                                            const Raw<DT, N>& xr, const Raw<DT, N>& rr) {
+                                            Raw<DT, N> xr, const Raw<DT, N>& rr) {
   const int64_t e = e0 + local;
+  if (a.drop.cut) drop<DT, N>(xr, mask, local, a.drop.cut);
   float x[N];
   to_float<DT, N>(xr, x);
-  if (a.drop.cut) {
 #pragma unroll
-    for (int i = 0; i < N; ++i) x[i] = x[i] * a.f;
-    drop<N>(x, mask, local, a.drop.cut);
-  }
+  for (int i = 0; i < N; ++i) x[i] = x[i] * a.f;   // 1 where nothing is dropped
   if (a.residual) {
     float r[N];
     to_float<DT, N>(rr, r);
