@@ -417,7 +417,7 @@ typedef struct zero_drop {
  *               (>= hidden; what lies between rows is left as it was).
  * Errors: EINVAL for nulls, a tensor index out of range, hidden < 1 or not
  * dividing the tensor, a negative n, a short stride, misalignment, p outside
- * [0, 1], or out overlapping params or tokens; EUNSUPPORTED for more than
+ * [0, 1], an f that is not finite, or out overlapping params or tokens; EUNSUPPORTED for more than
  * 2^31 - 2 rows or hidden above 2^24.
  */
 ZERO_API zero_status zero_embed(zero_plan_t plan, int32_t tensor, int64_t hidden, const void* params,
@@ -562,7 +562,8 @@ ZERO_API zero_status zero_preference_loss(int64_t n_pairs, const void* offsets, 
  *   coef        device fp32[n]; a row that is not scored, or whose coef is 0,
  *               gives a row of zeros and its logits are not read.
  *   dlogits     n rows, dl_stride elements apart, the logits' type; it may be
- *               the logits buffer itself (with the same stride).
+ *               the logits buffer itself (with the same stride).  What lies
+ *               between rows is left as it was.
  * Errors: as zero_token_logp, and EINVAL for dlogits overlapping the logits
  * without being them.
  */

@@ -41,7 +41,7 @@ def test_embed_refuses(Z):
     p = Z.zero_plan(805, 2, [5, 800], 0, 8)
     bad = [dict(tensor=2), dict(tensor=-1), dict(hidden=0), dict(hidden=7, stride=7), dict(params=0), dict(tokens=0),
            dict(out=0), dict(n=-1), dict(pdt=3), dict(odt=-1), dict(it=2), dict(stride=7), dict(scale=math.inf),
-           dict(scale=math.nan), dict(params=P(0) + 1), dict(tokens=P(1) + 4), dict(tokens=P(1) + 2, it=0),
+           dict(scale=math.nan), dict(scale=1e39), dict(scale=-2e38, drop=_drop(Z, 0.5)), dict(params=P(0) + 1), dict(tokens=P(1) + 4), dict(tokens=P(1) + 2, it=0),
            dict(out=P(2) + 2, odt=0), dict(out=P(0) + 16), dict(out=P(1) + 8), dict(stride=1 << 60),
            dict(drop=_drop(Z, 1.1)), dict(drop=_drop(Z, -0.1)), dict(drop=_drop(Z, math.nan)),
            dict(drop=_drop(Z, first=-1)), dict(drop=_drop(Z, first=(1 << 63) - 1)), dict(drop=_drop(Z, step_dev=BASE + 4))]

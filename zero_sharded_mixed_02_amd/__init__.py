@@ -442,23 +442,24 @@ class Drop:
     def __init__(self, p: float, seed: int, site: int = 0, step: int = 0, first: int = 0, step_dev=None):
         mask = (1 << 64) - 1
         self._keep = step_dev
-        addr = _arg(step_dev, "step_dev", 8, 1)
-        self.c = _Drop(p, seed & mask, site & mask, step & mask, addr or None, first)
+        addr = None if step_dev is None else _arg(step_dev, "step_dev", 8, 1) or None
+        self.c = _Drop(p, seed & mask, site & mask, step & mask, addr, first)
         self._ref = ctypes.byref(self.c)
 
 
-_raw_stream = None   # torch's current stream of a device, as an integer
+# torch's current stream of a device as an integer, and its current device:
+# the functions below torch.cuda's own, where torch has them, since a Stream
+# object alone takes 2.8 us to build.
+_raw_stream = _current_device = None
 
 
-def _current_stream(device: int) -> int:
-    """hipStream_t of torch's current stream on a device, without building a
-    Stream object where torch offers that (2.8 us a call)."""
-    global _raw_stream
-    if _raw_stream is None:
-        import torch
-        _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
-            lambda d: int(torch.cuda.current_stream(d).cuda_stream))
-    return _raw_stream(device)
+def _bind_torch() -> None:
+    global _raw_stream, _current_device
+    import torch
+    torch.cuda.current_device()   # initialises torch's GPU side
+    _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+        lambda d: int(torch.cuda.current_stream(d).cuda_stream))
+    _current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
 
 
 _ID_TYPES = {}       # torch integer types -> zero_itype
@@ -573,20 +574,24 @@ class _Call:
             return None
         if not isinstance(d, Drop):
             raise TypeError(f"drop: expected a Drop, got {type(d).__name__}")
-        self.see(d._keep, "step_dev")
+        if d._keep is not None:
+            self.see(d._keep, "step_dev")
         return d._ref
 
     def issue(self, fn, *args) -> None:
         """Calls fn with the stream, on the tensors' device."""
-        if self.device is None:
+        device = self.device
+        if device is None:
             status = fn(*args, _stream(self.stream))
         else:
-            import torch
-            stream = _current_stream(self.device) if self.stream is None else _stream(self.stream)
-            if torch.cuda.current_device() == self.device:
+            if _current_device is None:
+                _bind_torch()
+            stream = _raw_stream(device) if self.stream is None else _stream(self.stream)
+            if _current_device() == device:
                 status = fn(*args, stream)
             else:
-                with torch.cuda.device(self.device):
+                import torch
+                with torch.cuda.device(device):
                     status = fn(*args, stream)
         if status != ZERO_OK:
             _check(status)

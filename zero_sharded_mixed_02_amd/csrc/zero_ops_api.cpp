@@ -208,7 +208,6 @@ zero_status zero_embed(zero_plan_t p, int32_t tensor, int64_t hidden, const void
     if (!valid_dt(out_dt)) return fail(ZERO_EINVAL, "unknown dtype %d", (int)out_dt);
     if (!valid_it(token_it)) return fail(ZERO_EINVAL, "unknown token type %d", (int)token_it);
     if (n < 0) return fail(ZERO_EINVAL, "n must be >= 0 (got %lld)", (long long)n);
-    if (!std::isfinite(scale)) return fail(ZERO_EINVAL, "scale is not finite");
     if (out_stride < hidden)
       return fail(ZERO_EINVAL, "out_stride %lld is shorter than a row of %lld", (long long)out_stride, (long long)hidden);
     const int64_t span = span_of(n, out_stride, hidden);
@@ -220,6 +219,7 @@ zero_status zero_embed(zero_plan_t p, int32_t tensor, int64_t hidden, const void
     memset(&a, 0, sizeof a);
     double keep;
     if (zero_status st = make_drop(drop, span, a.drop, keep)) return st;
+    if (!std::isfinite((float)(scale * keep))) return fail(ZERO_EINVAL, "scale %g is beyond fp32", scale);
     if (zero_status st = check_disjoint({range_of(out, span, esize(out_dt), "out")},
                                         {range_of(params, p->psi_pad, esize(param_dt), "params"),
                                          range_of(tokens, n, isize(token_it), "tokens")}))
@@ -317,7 +317,6 @@ zero_status zero_embed_grad(zero_plan_t p, int32_t tensor, int64_t hidden, const
     if (n > kMaxTokens) return fail(ZERO_EUNSUPPORTED, "n = %lld exceeds %lld", (long long)n, (long long)kMaxTokens);
     if (rank >= p->n_d) return fail(ZERO_EINVAL, "rank %d outside [0, %d)", rank, p->n_d);
     if (accumulate != 0 && accumulate != 1) return fail(ZERO_EINVAL, "accumulate must be 0 or 1 (got %d)", accumulate);
-    if (!std::isfinite(scale)) return fail(ZERO_EINVAL, "scale is not finite");
     if (dy_stride < hidden)
       return fail(ZERO_EINVAL, "dy_stride %lld is shorter than a row of %lld", (long long)dy_stride, (long long)hidden);
     const int64_t span = span_of(n, dy_stride, hidden);
@@ -333,6 +332,7 @@ zero_status zero_embed_grad(zero_plan_t p, int32_t tensor, int64_t hidden, const
     memset(&a, 0, sizeof a);
     double keep;
     if (zero_status st = make_drop(drop, span, a.drop, keep)) return st;
+    if (!std::isfinite((float)(scale * keep))) return fail(ZERO_EINVAL, "scale %g is beyond fp32", scale);
     if (zero_status st = check_disjoint({range_of(dst, dst_elems, esize(dst_dt), "dst"),
                                          range_of(workspace, (int64_t)need, 1, "workspace")},
                                         {range_of(sorted, n, 4, "sorted"), range_of(order, n, 4, "order"),
