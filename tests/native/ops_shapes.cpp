@@ -118,8 +118,10 @@ int launch_grad(const GradArgs& a, int ydt, int gdt, int vec, int64_t blocks, vo
   return 0;
 }
 
-int launch_grad_join(const GradArgs& a, int, bool vec, void*) {
+int launch_grad_join(const GradArgs& a, int, bool vec, int64_t blocks, void*) {
   ++g_launches;
+  EXPECT((int64_t)a.join_tiles * (vec ? 256 : 64) >= a.hidden, "join tiles");
+  EXPECT(blocks == (a.n_chunks + kJoinChunks - 1) / kJoinChunks * (int64_t)a.join_tiles, "join workgroups");
   EXPECT(a.n_chunks >= 2 && vec == (a.hidden >= 4), "join");
   return 0;
 }

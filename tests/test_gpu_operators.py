@@ -703,6 +703,40 @@ def test_graph_replays(gpu, zero_lib):
     assert torch.equal(seen[0], seen[1]) and not torch.equal(seen[1], seen[2])
 
 
+def test_an_error_left_by_another_call_is_not_reported(gpu, zero_lib):
+    """A runtime error that some other part of the program left pending (here a
+    device number that does not exist) is neither returned nor cleared."""
+    import ctypes
+    import torch
+    Z = zero_lib
+    hip = ctypes.CDLL(next(line.split()[-1] for line in open("/proc/self/maps") if "libamdhip64" in line))
+    x = torch.ones(1000, device=gpu)
+    out, lp, st, co = torch.empty(1000, device=gpu), torch.empty(2, device=gpu), torch.empty(4, device=gpu), torch.empty(2, device=gpu)
+    ids, lab = torch.zeros(10, dtype=torch.int64, device=gpu), torch.zeros(2, dtype=torch.int64, device=gpu)
+    s, o = torch.empty(10, dtype=torch.int32, device=gpu), torch.empty(10, dtype=torch.int32, device=gpu)
+    plan = Z.zero_plan(1000, 1, [1000], 0, 1)
+    ws = torch.empty(4096, dtype=torch.uint8, device=gpu)
+    y = torch.empty((10, 10), device=gpu)
+    off = torch.tensor([0, 1, 2], device=gpu)
+    one, pl, two = (torch.empty(k, device=gpu) for k in (1, 1, 2))
+    torch.cuda.synchronize()
+    stream = int(torch.cuda.current_stream().cuda_stream)
+    assert hip.hipSetDevice(12345) != 0
+    try:
+        Z.zero_dropout(x, None, out, F32, Z.Drop(0.5, 1), stream=stream)
+        Z.zero_embed(plan, 0, 10, x, F32, ids, 2.0, y, F32, stream=stream)
+        Z.zero_token_order(ids, 100, s, o, stream=stream)
+        Z.zero_embed_grad(plan, 0, 10, s, o, y, F32, 1.0, out, F32, workspace=ws, stream=stream)
+        Z.zero_token_logp(x.view(2, 500), F32, lab, lp, st, stream=stream)
+        Z.zero_preference_loss(off, lab, 500, lp, None, 0.1, 0.0, 1.0, one, pl, two, co, stream=stream)
+        Z.zero_token_logp_grad(x.view(2, 500), F32, lab, st, co, out.view(2, 500), stream=stream)
+    finally:
+        pending = hip.hipGetLastError()
+        torch.cuda.synchronize()
+    assert pending != 0
+    assert bool((y == 2).all())
+
+
 def test_two_streams(gpu, zero_lib):
     """Two gradients at once, each on its own stream with its own workspace."""
     import torch

@@ -200,6 +200,21 @@ def test_reference_preference_by_hand():
     assert np.allclose(coef, np.array([-1, 1]) * 0.5 / (1 + math.exp(0.5)))
 
 
+@pytest.mark.skipif(shutil.which("gcc") is None, reason="gcc not available")
+def test_header_is_plain_c(tmp_path):
+    """The operators' declarations compile as C11 and a call type-checks."""
+    src = tmp_path / "use.c"
+    src.write_text("""#include "zero.h"
+zero_status use(zero_plan_t p, const void* x, void* y, const int64_t* ids, const uint64_t* step, void* stream) {
+  zero_drop d = {.p = 0.1, .seed = 1, .site = 2, .step_dev = step};
+  zero_status st = zero_embed(p, 0, 8, x, ZERO_BF16, ids, ZERO_I64, 4, 1.0, &d, y, ZERO_BF16, 8, stream);
+  return st ? st : zero_dropout(y, x, y, 32, ZERO_BF16, &d, stream);
+}
+""")
+    subprocess.run(["gcc", "-std=c11", "-Wall", "-Wextra", "-Werror", "-fsyntax-only", "-I", os.path.join(ROOT, "include"),
+                    str(src)], check=True)
+
+
 @pytest.mark.skipif(shutil.which("g++") is None, reason="g++ not available")
 def test_launch_shapes(tmp_path):
     """The host code with stand-ins for the launchers, over a few thousand

@@ -88,7 +88,6 @@ struct RadixArgs {
 constexpr int kGradThreads = 256;
 constexpr int kGradChunks = kGradThreads / 64;   // neighbouring chunks of a workgroup, one a wave
 constexpr int kJoinThreads = 512;
-constexpr int kJoinTile = 256;           // columns of a workgroup in the join
 constexpr int kJoinChunks = 16;          // chunks it looks after
 constexpr int kJoinLong = 64;            // chunks from which a run is cut into pieces
 
@@ -112,7 +111,7 @@ struct GradArgs {
   float f;
   int64_t chunk_blocks;    // workgroups before those that write zero rows
   int32_t stream_dy;       // dy is read past the caches
-  int32_t pad_;
+  int32_t join_tiles;      // column tiles of the join
   DropArgs drop;
 };
 
@@ -183,7 +182,7 @@ int launch_embed(const EmbedArgs& a, int tdt, int odt, bool vec, int64_t blocks,
 int launch_rank(const RankArgs& a, int64_t blocks, void* stream);
 int launch_radix(const RadixArgs& a, void* stream);
 int launch_grad(const GradArgs& a, int ydt, int gdt, int vec, int64_t blocks, void* stream);
-int launch_grad_join(const GradArgs& a, int gdt, bool vec, void* stream);
+int launch_grad_join(const GradArgs& a, int gdt, bool vec, int64_t blocks, void* stream);
 int launch_dropout(const DropoutArgs& a, int dt, int64_t blocks, void* stream);
 int launch_logp(const LogpArgs& a, int dt, void* stream);
 int launch_logp_join(const LogpArgs& a, int dt, void* stream);

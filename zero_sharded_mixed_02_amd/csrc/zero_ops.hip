@@ -826,12 +826,12 @@ __global__ __launch_bounds__(kJoinThreads) void grad_join_kernel(const GradArgs 
   __shared__ float piece[kWaves][64 * N];
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
-  const int32_t tile = (int32_t)blockIdx.y * 64 * N;
-  const int32_t begin = tile + lane * N;
+  const int64_t group = blockIdx.x / (uint32_t)a.join_tiles;
+  const int32_t begin = ((int32_t)(blockIdx.x - group * a.join_tiles) * 64 + lane) * N;
   const bool on = begin < a.hidden;
   const int32_t col = begin < a.hidden - N ? begin : a.hidden - N;
 
-  const int64_t c0 = (int64_t)blockIdx.x * kJoinChunks;
+  const int64_t c0 = group * kJoinChunks;
   const int64_t mine = c0 + lane, s = mine * a.chunk, e = s + a.chunk;
   const int64_t next = e + a.chunk, far = e + (int64_t)kJoinLong * a.chunk;
   const int64_t end = a.n - 1;
@@ -1322,121 +1322,101 @@ int by_type(int dt, F f) {
   }
 }
 
-int last() { return (int)hipGetLastError(); }
+// The launch's own error, and none that an earlier call of the program left.
+template <typename Args>
+int launch(void (*kernel)(Args), int64_t blocks, int threads, const Args& a, void* stream) {
+  void* args[] = {const_cast<void*>((const void*)&a)};
+  return (int)hipLaunchKernel((const void*)kernel, dim3((uint32_t)blocks), dim3((uint32_t)threads), args, 0,
+                              (hipStream_t)stream);
+}
 
 }  // namespace
 
 int launch_embed(const EmbedArgs& a, int tdt, int odt, bool vec, int64_t blocks, void* stream) {
   return by_type(tdt, [&](auto T) {
     return by_type(odt, [&](auto O) {
-      constexpr int t = decltype(T)::value, o = decltype(O)::value;
-      constexpr int n = vec_of(t, o);
-      const hipStream_t st = (hipStream_t)stream;
-      const uint32_t b = (uint32_t)blocks;
-      if (!vec) embed_kernel<t, o, 1, 2><<<b, kEmbedThreads, 0, st>>>(a);   // p = 0 keeps all
-      else if (!a.drop.cut) embed_kernel<t, o, n, 0><<<b, kEmbedThreads, 0, st>>>(a);
-      else if (a.hidden % n == 0 && a.drop.first % 4 == 0) embed_kernel<t, o, n, 1><<<b, kEmbedThreads, 0, st>>>(a);
-      else embed_kernel<t, o, n, 2><<<b, kEmbedThreads, 0, st>>>(a);
-      return last();
+      constexpr int t = decltype(T)::value, o = decltype(O)::value, n = vec_of(t, o);
+      auto kernel = embed_kernel<t, o, n, 2>;
+      if (!vec) kernel = embed_kernel<t, o, 1, 2>;   // p = 0 keeps all
+      else if (!a.drop.cut) kernel = embed_kernel<t, o, n, 0>;
+      else if (a.hidden % n == 0 && a.drop.first % 4 == 0) kernel = embed_kernel<t, o, n, 1>;
+      return launch(kernel, blocks, kEmbedThreads, a, stream);
     });
   });
 }
 
 int launch_rank(const RankArgs& a, int64_t blocks, void* stream) {
-  rank_kernel<<<(uint32_t)blocks, kRankThreads, 0, (hipStream_t)stream>>>(a);
-  return last();
+  return launch(rank_kernel, blocks, kRankThreads, a, stream);
 }
 
 int launch_radix(const RadixArgs& a, void* stream) {
-  radix_count_kernel<<<a.n_blocks, kSortThreads, 0, (hipStream_t)stream>>>(a);
-  if (const int err = last()) return err;
-  if (a.tile == kSortThreads * kSortKeysFew)
-    radix_move_kernel<kSortKeysFew><<<a.n_blocks, kSortThreads, 0, (hipStream_t)stream>>>(a);
-  else
-    radix_move_kernel<kSortKeysMany><<<a.n_blocks, kSortThreads, 0, (hipStream_t)stream>>>(a);
-  return last();
+  if (const int err = launch(radix_count_kernel, a.n_blocks, kSortThreads, a, stream)) return err;
+  return launch(a.tile == kSortThreads * kSortKeysFew ? radix_move_kernel<kSortKeysFew> : radix_move_kernel<kSortKeysMany>,
+                a.n_blocks, kSortThreads, a, stream);
 }
 
 int launch_grad(const GradArgs& a, int ydt, int gdt, int vec, int64_t blocks, void* stream) {
   return by_type(ydt, [&](auto Y) {
     return by_type(gdt, [&](auto G) {
       constexpr int y = decltype(Y)::value, g = decltype(G)::value;
-      auto go = [&](auto N) {
+      auto go = [&](auto N, auto NT) {
         constexpr int n = decltype(N)::value;
-        const hipStream_t st = (hipStream_t)stream;
-        auto run = [&](auto NT) {
-          constexpr bool nt = decltype(NT)::value;
-          if (!a.drop.cut) grad_kernel<y, g, n, 0, nt><<<(uint32_t)blocks, kGradThreads, 0, st>>>(a);
-          else if (n > 1 && a.hidden % 4 == 0 && a.drop.first % 4 == 0)
-            grad_kernel<y, g, n, (n > 1 ? 1 : 2), nt><<<(uint32_t)blocks, kGradThreads, 0, st>>>(a);
-          else grad_kernel<y, g, n, 2, nt><<<(uint32_t)blocks, kGradThreads, 0, st>>>(a);
-          return last();
-        };
-        if constexpr (n > 1)
-          if (a.stream_dy) return run(std::true_type{});
-        return run(std::false_type{});
+        constexpr bool nt = decltype(NT)::value;
+        auto kernel = grad_kernel<y, g, n, 2, nt>;
+        constexpr int whole_words = n > 1 ? 1 : 2;
+        if (!a.drop.cut) kernel = grad_kernel<y, g, n, 0, nt>;
+        else if (a.hidden % 4 == 0 && a.drop.first % 4 == 0) kernel = grad_kernel<y, g, n, whole_words, nt>;
+        return launch(kernel, blocks, kGradThreads, a, stream);
       };
-      if (vec == 1) return go(std::integral_constant<int, 1>{});
+      auto wide = [&](auto N) { return a.stream_dy ? go(N, std::true_type{}) : go(N, std::false_type{}); };
+      if (vec == 1) return go(std::integral_constant<int, 1>{}, std::false_type{});
       if constexpr (vec_of(y, g) == 8)
-        if (vec == 8) return go(std::integral_constant<int, 8>{});
-      return go(std::integral_constant<int, 4>{});
+        if (vec == 8) return wide(std::integral_constant<int, 8>{});
+      return wide(std::integral_constant<int, 4>{});
     });
   });
 }
 
-int launch_grad_join(const GradArgs& a, int gdt, bool vec, void* stream) {
+int launch_grad_join(const GradArgs& a, int gdt, bool vec, int64_t blocks, void* stream) {
   return by_type(gdt, [&](auto G) {
     constexpr int g = decltype(G)::value;
-    const int n = vec ? 4 : 1;
-    const int tiles = (a.hidden + 64 * n - 1) / (64 * n);
-    const dim3 grid((uint32_t)((a.n_chunks + kJoinChunks - 1) / kJoinChunks), (uint32_t)tiles);
-    if (vec) grad_join_kernel<g, 4><<<grid, kJoinThreads, 0, (hipStream_t)stream>>>(a);
-    else grad_join_kernel<g, 1><<<grid, kJoinThreads, 0, (hipStream_t)stream>>>(a);
-    return last();
+    return launch(vec ? grad_join_kernel<g, 4> : grad_join_kernel<g, 1>, blocks, kJoinThreads, a, stream);
   });
 }
 
 int launch_dropout(const DropoutArgs& a, int dt, int64_t blocks, void* stream) {
   return by_type(dt, [&](auto D) {
     constexpr int d = decltype(D)::value;
-    dropout_kernel<d, vec_of(d, d)><<<(uint32_t)blocks, kDropoutThreads, 0, (hipStream_t)stream>>>(a);
-    return last();
+    return launch(dropout_kernel<d, vec_of(d, d)>, blocks, kDropoutThreads, a, stream);
   });
 }
 
 int launch_logp(const LogpArgs& a, int dt, void* stream) {
   return by_type(dt, [&](auto D) {
     constexpr int d = decltype(D)::value;
-    const uint32_t blocks = (uint32_t)(a.n * a.splits);
-    if (a.vocab < (a.n < kLogpManyRows ? kLogpShortRow : 4 * kLogpShortRow)) logp_kernel<d, 64><<<blocks, 64, 0, (hipStream_t)stream>>>(a);
-    else logp_kernel<d, kLogpThreads><<<blocks, kLogpThreads, 0, (hipStream_t)stream>>>(a);
-    return last();
+    const bool brief = a.vocab < (a.n < kLogpManyRows ? kLogpShortRow : 4 * kLogpShortRow);
+    return brief ? launch(logp_kernel<d, 64>, a.n * a.splits, 64, a, stream)
+                 : launch(logp_kernel<d, kLogpThreads>, a.n * a.splits, kLogpThreads, a, stream);
   });
 }
 
 int launch_logp_join(const LogpArgs& a, int dt, void* stream) {
   return by_type(dt, [&](auto D) {
-    logp_join_kernel<decltype(D)::value><<<(uint32_t)((a.n + 63) / 64), 64, 0, (hipStream_t)stream>>>(a);
-    return last();
+    return launch(logp_join_kernel<decltype(D)::value>, (a.n + 63) / 64, 64, a, stream);
   });
 }
 
 int launch_dlogits(const LogpArgs& a, int dt, void* stream) {
   return by_type(dt, [&](auto D) {
-    dlogits_kernel<decltype(D)::value><<<(uint32_t)(a.n * a.splits), kDlogitsThreads, 0, (hipStream_t)stream>>>(a);
-    return last();
+    return launch(dlogits_kernel<decltype(D)::value>, a.n * a.splits, kDlogitsThreads, a, stream);
   });
 }
 
 int launch_preference(const PrefArgs& a, void* stream) {
-  if (a.n_pairs <= kPrefThreads / 64 && a.n <= kPrefSmallRows) {
-    preference_small_kernel<<<1, kPrefThreads, 0, (hipStream_t)stream>>>(a);
-    return last();
-  }
-  preference_kernel<<<(uint32_t)(a.n_pairs + 1), kPrefThreads, 0, (hipStream_t)stream>>>(a);
-  if (const int err = last()) return err;
-  mean_kernel<<<1, 64, 0, (hipStream_t)stream>>>(a);
-  return last();
+  if (a.n_pairs <= kPrefThreads / 64 && a.n <= kPrefSmallRows)
+    return launch(preference_small_kernel, 1, kPrefThreads, a, stream);
+  if (const int err = launch(preference_kernel, a.n_pairs + 1, kPrefThreads, a, stream)) return err;
+  return launch(mean_kernel, 1, 64, a, stream);
 }
 
 }  // namespace ops

@@ -380,10 +380,12 @@ zero_status zero_embed_grad(zero_plan_t p, int32_t tensor, int64_t hidden, const
     a.chunk_blocks = ceil_div(a.n_chunks, kGradChunks) * a.tiles;
     a.stream_dy = n * hidden * esize(dy_dt) > kInfinityCache;
     const int64_t blocks = a.chunk_blocks + (accumulate ? 0 : ceil_div(a.row_hi - a.row_lo, a.fill_rows));
-    if (zero_status st = check_blocks(blocks)) return st;
+    a.join_tiles = (int32_t)ceil_div(hidden, hidden >= 4 ? 256 : 64);
+    const int64_t joins = ceil_div(a.n_chunks, kJoinChunks) * a.join_tiles;
+    if (zero_status st = check_blocks(std::max(blocks, joins))) return st;
     if (const int err = launch_grad(a, dy_dt, dst_dt, vec, blocks, stream)) return hip_fail(err);
     if (a.n_chunks < 2) return ok();   // no run crosses a boundary
-    return launched(launch_grad_join(a, dst_dt, hidden >= 4, stream));
+    return launched(launch_grad_join(a, dst_dt, hidden >= 4, joins, stream));
   });
 }
 
