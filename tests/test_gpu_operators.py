@@ -958,3 +958,34 @@ def test_dropout_past_32_bits(gpu, zero_lib):
         keep = R.mask_block(9, 8, 7, 0.25, 3 + a, 1000)
         want = torch.where(torch.from_numpy(keep), torch.tensor(4 / 3, dtype=torch.float32).bfloat16(), torch.zeros((), dtype=torch.bfloat16))
         assert torch.equal(x[a:a + 1000].cpu(), want)
+
+
+# ---------------------------------------------------------------------------
+# Seeded random sizes, types, ids and owners
+# ---------------------------------------------------------------------------
+
+@pytest.mark.parametrize("seed", range(8))
+def test_random_cases(gpu, zero_lib, seed):
+    """The tests above at drawn sizes, spread over their logarithm."""
+    import math
+    import random
+    r = random.Random(1000 + seed)
+    size = lambda hi: int(round(math.exp(r.uniform(0, math.log(hi)))))  # noqa: E731
+    for _ in range(12):
+        n, rows, hidden = size(6000), size(3000), size(1500)
+        if r.random() < 0.4:
+            hidden = max(8, hidden // 8 * 8)
+        n, rows = min(n, max(1, 1500000 // hidden)), min(rows, max(1, 1500000 // hidden))
+        kind = r.choice(["uniform", "skew", "one", "wild", "wild", "padding"])
+        case = (n, rows, hidden, r.randrange(3), r.randrange(3), r.choice([None, None, 0.1, 0.5, 1.0]),
+                r.choice([0, r.randrange(100)]), r.choice([0, 0, 3, 8]), kind)
+        test_embed_grad(gpu, zero_lib, case + (r.randint(1, 5),), r.random() < 0.5)
+        test_embed(gpu, zero_lib, case + (r.random() < 0.5,))
+        test_token_order(gpu, zero_lib, size(60000), r.choice([size(100000), size(2 ** 31 - 2)]), kind)
+        test_token_logp_and_grad(gpu, zero_lib, (size(60), size(9000), r.randrange(3), r.choice([0, 1, 5]), r.random() < 0.5))
+        test_dropout(gpu, zero_lib, size(200000), r.randrange(3), r.choice([0.0, 0.1, 0.7]), r.random() < 0.5,
+                     r.randrange(1 << 36), r.choice(["", "x", "residual"]))
+        pairs = r.randint(1, 30)
+        test_preference_loss(gpu, zero_lib, ([r.randrange(60) for _ in range(pairs)], [r.randrange(60) for _ in range(pairs)],
+                                             r.randrange(4), r.randrange(4), 2 * r.random(), r.random(), r.uniform(-9, 9),
+                                             r.random() < 0.5, r.random() < 0.5, r.random() < 0.5))
