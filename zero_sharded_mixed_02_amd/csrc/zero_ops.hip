@@ -1186,13 +1186,26 @@ __device__ __forceinline__ bool counts(const PrefArgs& a, int64_t t) {
   return !a.labels || (uint64_t)load_id(a.labels, t, a.lab64) < (uint64_t)a.vocab;
 }
 
-// Lane's share of the sum over a sequence's scored rows, fp64.
+// Lane's share of the sum over a sequence's scored rows, fp64.  What a row
+// holds is loaded before it is known to count, so that the loads of U rows
+// share one latency.
 template <int THREADS>
 __device__ __forceinline__ double sum_rows(const PrefArgs& a, int64_t lo, int64_t hi, int tid) {
+  constexpr int U = THREADS == 64 ? 8 : 2;
   double s = 0.0;
-#pragma unroll 4
-  for (int64_t t = lo + tid; t < hi; t += THREADS)
-    s += counts(a, t) ? (double)a.logp[t] - (a.ref ? (double)a.ref[t] : 0.0) : 0.0;
+  for (int64_t t0 = lo + tid; t0 < hi; t0 += U * THREADS) {
+    float lp[U], ref[U];
+    bool in[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int64_t t = t0 + u * THREADS, at = t < hi ? t : t0;
+      lp[u] = a.logp[at];
+      ref[u] = a.ref ? a.ref[at] : 0.0f;
+      in[u] = counts(a, at) && t < hi;
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) s += in[u] ? (double)lp[u] - (double)ref[u] : 0.0;
+  }
   return s;
 }
 
@@ -1279,33 +1292,38 @@ __global__ __launch_bounds__(64) void mean_kernel(const PrefArgs a) {
 }
 
 // Few pairs of few rows: all of it in one workgroup and one launch, a wave per
-// pair (48 rows: 4 us, and a launch less; 8192 rows would take 8 us longer than
-// the two launches).
+// sequence (see kPrefSmallRows).
 __global__ __launch_bounds__(kPrefThreads) void preference_small_kernel(const PrefArgs a) {
-  __shared__ float loss[kPrefThreads / 64];
-  const int wave = threadIdx.x / 64, lane = threadIdx.x % 64;
-  if (wave < a.n_pairs) {
-    const int64_t j = a.n_pairs + wave;
-    const int64_t c0 = row_limit(a, wave, 0), c1 = row_limit(a, wave + 1, c0);
-    const int64_t r0 = row_limit(a, j, 0), r1 = row_limit(a, j + 1, r0);
-    const double chosen = a.beta * wave_sum(sum_rows<64>(a, c0, c1, lane));
-    const double rejected = a.beta * wave_sum(sum_rows<64>(a, r0, r1, lane));
-    const Pair p = pair_of(a, chosen - rejected);
+  __shared__ double reward[2 * kPrefSmallPairs];
+  __shared__ float coef[kPrefSmallPairs], loss[kPrefSmallPairs];
+  constexpr int kWaves = kPrefThreads / 64;
+  const int wave = threadIdx.x / 64, lane = threadIdx.x % 64, tid = threadIdx.x;
+  const int pairs = (int)a.n_pairs;
+  for (int seq = wave; seq < 2 * pairs; seq += kWaves) {
+    const int64_t lo = row_limit(a, seq, 0), hi = row_limit(a, seq + 1, lo);
+    const double s = a.beta * wave_sum(sum_rows<64>(a, lo, hi, lane));
     if (lane == 0) {
-      a.rewards[wave] = (float)chosen;
-      a.rewards[j] = (float)rejected;
-      a.pair_loss[wave] = (float)p.loss;
-      loss[wave] = (float)p.loss;
+      reward[seq] = s;
+      a.rewards[seq] = (float)s;
     }
-    write_coef<64>(a, c0, c1, lane, p.coef);
-    write_coef<64>(a, r0, r1, lane, -p.coef);
   }
-  write_outside<kPrefThreads>(a, threadIdx.x);
   __syncthreads();
-  if (threadIdx.x == 0) {
+  if (tid < pairs) {
+    const Pair p = pair_of(a, reward[tid] - reward[pairs + tid]);
+    coef[tid] = p.coef;
+    loss[tid] = (float)p.loss;
+    a.pair_loss[tid] = (float)p.loss;
+  }
+  __syncthreads();
+  for (int seq = wave; seq < 2 * pairs; seq += kWaves) {
+    const int64_t lo = row_limit(a, seq, 0), hi = row_limit(a, seq + 1, lo);
+    write_coef<64>(a, lo, hi, lane, seq < pairs ? coef[seq] : -coef[seq - pairs]);
+  }
+  write_outside<kPrefThreads>(a, tid);
+  if (tid == 0) {
     double s = 0.0;
-    for (int w = 0; w < a.n_pairs; ++w) s += (double)loss[w];
-    a.loss[0] = a.n_pairs ? (float)(s / (double)a.n_pairs) : 0.0f;
+    for (int i = 0; i < pairs; ++i) s += (double)loss[i];
+    a.loss[0] = pairs ? (float)(s / (double)pairs) : 0.0f;
   }
 }
 
@@ -1413,7 +1431,7 @@ int launch_dlogits(const LogpArgs& a, int dt, void* stream) {
 }
 
 int launch_preference(const PrefArgs& a, void* stream) {
-  if (a.n_pairs <= kPrefThreads / 64 && a.n <= kPrefSmallRows)
+  if (a.n_pairs <= kPrefSmallPairs && a.n <= kPrefSmallRows)
     return launch(preference_small_kernel, 1, kPrefThreads, a, stream);
   if (const int err = launch(preference_kernel, a.n_pairs + 1, kPrefThreads, a, stream)) return err;
   return launch(mean_kernel, 1, 64, a, stream);
