@@ -366,6 +366,7 @@ ZERO_API zero_status zero_set_stream_write_window(void* stream, int64_t period_t
  * the same stream; two calls that can run at once (two streams, two graphs
  * replayed beside each other) need one each.  The calls are issued to the
  * current device, which has to be the one of the buffers and of the stream.
+ * A call whose work exceeds one launch (2^32 work items) issues several.
  * Sums, softmax statistics and norms are held in fp32 or more and are taken
  * in an order that depends on the sizes alone, so that a call repeated on the
  * same inputs gives the same bits.
@@ -470,7 +471,8 @@ ZERO_API zero_status zero_token_order(const void* tokens, zero_itype token_it, i
  * The stores are non-temporal, as zero_adam_step likes its slices.
  * Errors: as zero_embed, and EINVAL for rank >= n_d, accumulate other than 0
  * or 1, a short workspace or overlapping buffers; EUNSUPPORTED for n above
- * 2^30.
+ * 2^30, or where the sums need 2^32 work items or more (n * hidden of about
+ * 2^41 and beyond).
  */
 ZERO_API size_t zero_embed_grad_workspace_bytes(int64_t n, int64_t hidden);
 ZERO_API zero_status zero_embed_grad(zero_plan_t plan, int32_t tensor, int64_t hidden, const int32_t* sorted,

@@ -961,6 +961,109 @@ def test_dropout_past_32_bits(gpu, zero_lib):
 
 
 # ---------------------------------------------------------------------------
+# More work than one launch takes (2^32 work items)
+# ---------------------------------------------------------------------------
+
+@pytest.mark.big
+def test_dropout_of_two_launches(gpu, zero_lib):
+    """2^35 elements and some in place: around the place where the second
+    launch begins, and at both ends."""
+    import torch
+    Z = zero_lib
+    n = (1 << 35) + 1001
+    say("[big] dropout of two launches")
+    x = torch.ones(n, dtype=torch.bfloat16, device=gpu)
+    Z.zero_dropout(x, None, x, BF16, Z.Drop(0.25, 9, 8, 7, first=3))
+    torch.cuda.synchronize()
+    for a in (0, (1 << 35) - 4096 - 500, n - 1000):
+        keep = R.mask_block(9, 8, 7, 0.25, 3 + a, 1000)
+        want = torch.where(torch.from_numpy(keep), torch.tensor(4 / 3, dtype=torch.float32).bfloat16(), torch.zeros((), dtype=torch.bfloat16))
+        assert torch.equal(x[a:a + 1000].cpu(), want)
+
+
+@pytest.mark.big
+def test_embed_of_two_launches(gpu, zero_lib):
+    """Rows of seven elements, each taken singly: 2^34 of them and more."""
+    import torch
+    Z = zero_lib
+    rows, hidden = 5, 7
+    n = ((1 << 34) + 5000) // hidden
+    say("[big] embed of two launches")
+    plan = Z.zero_plan(rows * hidden, 1, [rows * hidden], 0, 1)
+    params = torch.arange(1, rows * hidden + 1, device=gpu).to(torch.bfloat16)
+    ids = torch.randint(-1, rows, (n,), generator=torch.Generator(device=gpu).manual_seed(4), device=gpu, dtype=torch.int32)
+    out = torch.empty((n, hidden), dtype=torch.bfloat16, device=gpu)
+    Z.zero_embed(plan, 0, hidden, params, BF16, ids, 1.0, out, BF16, drop=Z.Drop(0.5, 9, 8, 7, first=2))
+    torch.cuda.synchronize()
+    for a in (0, n // 2 - 400, n // 2, n - 800):        # the launches take equal parts
+        got, i = R.to64(out[a:a + 800]), ids[a:a + 800].cpu().numpy()
+        table = np.arange(1, rows * hidden + 1, dtype=np.float64).reshape(rows, hidden)
+        want = R.embed(table, i, 1.0, (9, 8, 7, 0.5, 2 + a * hidden))       # whole numbers up to 70: exact
+        assert np.array_equal(got, want), a
+
+
+@pytest.mark.big
+def test_logits_of_two_launches(gpu, zero_lib):
+    """2^26 rows of two logits and some more (2^26 is one launch of the forward
+    pass and two of the gradient), all rows against 64 bits."""
+    import torch
+    Z = zero_lib
+    n, vocab = (1 << 26) + 999, 2
+    say("[big] logits of two launches")
+    g = torch.Generator(device=gpu).manual_seed(6)
+    x = torch.empty((n, vocab), dtype=torch.bfloat16, device=gpu).normal_(0, 2, generator=g)
+    labels = torch.randint(-1, vocab, (n,), generator=g, device=gpu, dtype=torch.int32)
+    coef = torch.empty(n, device=gpu).normal_(generator=g)
+    lp, st = torch.full((n,), 7.0, device=gpu), torch.full((2 * n,), 7.0, device=gpu)
+    keep = x.clone()
+    Z.zero_token_logp(x, BF16, labels, lp, st)
+    Z.zero_token_logp_grad(x, BF16, labels, st, coef, x)
+    e = R.logsum_bound(vocab)
+    for a in range(0, n, 1 << 24):
+        z, lab, c = keep[a:a + (1 << 24)].double(), labels[a:a + (1 << 24)].long(), coef[a:a + (1 << 24)].double()
+        good = lab >= 0
+        at = lab.clamp(min=0)[:, None]
+        logp = torch.log_softmax(z, 1)
+        want = torch.where(good, logp.gather(1, at)[:, 0], 0.0)
+        assert bool(((lp[a:a + (1 << 24)].double() - want).abs() <= e + want.abs() * 2 * U).all())
+        hot = torch.zeros_like(z).scatter_(1, at, 1.0)
+        p, span = logp.exp(), (z[:, :1] - z[:, 1:]).abs()
+        want = torch.where(good[:, None], c[:, None] * (hot - p), 0.0)
+        tol = c.abs()[:, None] * (p * ((5 * (span + 1) + 4) * U + e) + 2 * U * (hot + p))
+        tol = tol + (want.abs() + tol) * 2.0 ** -8 + 2.0 ** -126        # one rounding to bf16
+        assert bool(((x[a:a + (1 << 24)].double() - want).abs() <= tol * good[:, None]).all())
+
+
+@pytest.mark.big
+def test_preference_of_two_launches(gpu, zero_lib):
+    """2^22 pairs and some of one or two rows each, all against 64 bits."""
+    import torch
+    Z = zero_lib
+    pairs, beta, eps, gs = (1 << 22) + 77, 0.5, 0.1, 64.0
+    say("[big] preference of two launches")
+    g = torch.Generator(device=gpu).manual_seed(7)
+    lens = torch.randint(1, 3, (2 * pairs,), generator=g, device=gpu)
+    offsets = torch.cat([lens.new_zeros(1), lens.cumsum(0)]) + 3
+    n = int(offsets[-1]) + 5
+    logp = -torch.rand(n, generator=g, device=gpu) * 4
+    loss, pl, rw, co = (torch.full((k,), 7.0, device=gpu) for k in (1, pairs, 2 * pairs, n))
+    Z.zero_preference_loss(offsets, None, 1, logp, None, beta, eps, gs, loss, pl, rw, co)
+    total = torch.cat([logp.new_zeros(1).double(), logp.double().cumsum(0)])
+    reward = beta * (total[offsets[1:]] - total[offsets[:-1]])
+    # the running total of 1.3e7 rows of up to 4 is off by its own roundings in 64 bits
+    slack = 5e7 * 2.0 ** -50
+    assert bool(((rw.double() - reward).abs() <= reward.abs() * U + slack).all())
+    h = reward[:pairs] - reward[pairs:]
+    want = -(1 - eps) * torch.nn.functional.logsigmoid(h) - eps * torch.nn.functional.logsigmoid(-h)
+    assert bool(((pl.double() - want).abs() <= want * U + 2 * slack).all())
+    assert abs(float(loss) - float(want.mean())) <= float(want.mean()) * 2 * U + 2 * slack
+    slope = beta * gs / pairs * (eps * torch.sigmoid(h) - (1 - eps) * torch.sigmoid(-h))
+    rows = torch.repeat_interleave(torch.cat([slope, -slope]), lens)
+    assert bool(((co[3:-5].double() - rows).abs() <= rows.abs() * (U + 4 * slack) + 2.0 ** -126 + beta * gs / pairs * 2 * slack).all())
+    assert not bool(co[:3].any()) and not bool(co[-5:].any())
+
+
+# ---------------------------------------------------------------------------
 # Seeded random sizes, types, ids and owners
 # ---------------------------------------------------------------------------
 

@@ -177,9 +177,21 @@ struct PrefArgs {
   int64_t n_pairs;
   int64_t vocab;
   double beta, smoothing, slope;   // slope = beta * grad_scale / n_pairs
+  int64_t pair0, pair_count;       // pairs of this launch
   int32_t off64;
   int32_t lab64;
 };
+
+// A launch has fewer than 2^32 work items in each dimension (HIP's limit on
+// grid times workgroup).  A call with more work takes several launches, each
+// over a part of the rows, elements or pairs.
+constexpr int64_t kLaunchItems = (int64_t(1) << 32) - 1;
+constexpr int64_t most_blocks(int threads) { return kLaunchItems / threads; }
+
+// Threads per row, or per piece of one (see kLogpShortRow).
+constexpr int logp_threads(int64_t n, int64_t vocab) {
+  return vocab < (n < kLogpManyRows ? kLogpShortRow : 4 * kLogpShortRow) ? 64 : kLogpThreads;
+}
 
 // Launchers (zero_ops.hip).  Return a hipError_t as int.
 int launch_embed(const EmbedArgs& a, int tdt, int odt, bool vec, int64_t blocks, void* stream);

@@ -1249,12 +1249,12 @@ __device__ __forceinline__ void write_outside(const PrefArgs& a, int tid) {
   for (int64_t t = hi + tid; t < a.n; t += THREADS) a.coef[t] = 0.0f;
 }
 
-// A pair per workgroup, half of it for each sequence; one more workgroup
-// writes the rows in no sequence.
+// A pair per workgroup, half of it for each sequence; one more workgroup, in
+// the launch of the last pairs, writes the rows in no sequence.
 __global__ __launch_bounds__(kPrefThreads) void preference_kernel(const PrefArgs a) {
   constexpr int kHalf = kPrefThreads / 2;
   __shared__ double part[kPrefThreads / 64];
-  const int64_t i = blockIdx.x;
+  const int64_t i = a.pair0 + blockIdx.x;
   const int tid = threadIdx.x;
   if (i == a.n_pairs) {
     write_outside<kPrefThreads>(a, tid);
@@ -1412,9 +1412,8 @@ int launch_dropout(const DropoutArgs& a, int dt, int64_t blocks, void* stream) {
 int launch_logp(const LogpArgs& a, int dt, void* stream) {
   return by_type(dt, [&](auto D) {
     constexpr int d = decltype(D)::value;
-    const bool brief = a.vocab < (a.n < kLogpManyRows ? kLogpShortRow : 4 * kLogpShortRow);
-    return brief ? launch(logp_kernel<d, 64>, a.n * a.splits, 64, a, stream)
-                 : launch(logp_kernel<d, kLogpThreads>, a.n * a.splits, kLogpThreads, a, stream);
+    return logp_threads(a.n, a.vocab) == 64 ? launch(logp_kernel<d, 64>, a.n * a.splits, 64, a, stream)
+                                            : launch(logp_kernel<d, kLogpThreads>, a.n * a.splits, kLogpThreads, a, stream);
   });
 }
 
@@ -1433,8 +1432,9 @@ int launch_dlogits(const LogpArgs& a, int dt, void* stream) {
 int launch_preference(const PrefArgs& a, void* stream) {
   if (a.n_pairs <= kPrefSmallPairs && a.n <= kPrefSmallRows)
     return launch(preference_small_kernel, 1, kPrefThreads, a, stream);
-  if (const int err = launch(preference_kernel, a.n_pairs + 1, kPrefThreads, a, stream)) return err;
-  return launch(mean_kernel, 1, 64, a, stream);
+  const bool last = a.pair0 + a.pair_count == a.n_pairs;
+  if (const int err = launch(preference_kernel, a.pair_count + last, kPrefThreads, a, stream)) return err;
+  return last ? launch(mean_kernel, 1, 64, a, stream) : 0;
 }
 
 }  // namespace ops

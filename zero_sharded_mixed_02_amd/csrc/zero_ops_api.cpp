@@ -103,12 +103,17 @@ zero_status table_of(zero_plan_t p, int32_t tensor, int64_t hidden, int64_t& row
   return ok();
 }
 
-zero_status check_blocks(int64_t blocks) {
-  if (blocks > INT32_MAX) return fail(ZERO_EUNSUPPORTED, "the call needs %lld workgroups", (long long)blocks);
+int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
+
+zero_status check_blocks(int64_t blocks, int threads) {
+  if (blocks > most_blocks(threads))
+    return fail(ZERO_EUNSUPPORTED, "the call needs %lld workgroups of %d, one launch takes %lld", (long long)blocks, threads,
+                (long long)most_blocks(threads));
   return ok();
 }
 
-int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
+// Size of the equal parts of n > 0 things of which one launch takes `most`.
+int64_t part_of(int64_t n, int64_t most) { return ceil_div(n, ceil_div(n, most)); }
 
 // ---------------------------------------------------------------------------
 // Launch shapes
@@ -228,9 +233,6 @@ zero_status zero_embed(zero_plan_t p, int32_t tensor, int64_t hidden, const void
     const int vec = vec_of(param_dt, out_dt);
     const bool wide = hidden >= vec;
     a.table = (const char*)params + p->t_off[tensor] * esize(param_dt);
-    a.tokens = tokens;
-    a.out = out;
-    a.n = n;
     a.out_stride = out_stride;
     a.rows = (int32_t)rows;
     a.hidden = (int32_t)hidden;
@@ -238,9 +240,16 @@ zero_status zero_embed(zero_plan_t p, int32_t tensor, int64_t hidden, const void
     a.magic = a.upr > 1 ? (uint32_t)((uint64_t(1) << 32) / a.upr + 1) : 0;
     a.tok64 = token_it == ZERO_I64;
     a.f = (float)(scale * keep);
-    const int64_t blocks = ceil_div(n * a.upr, kEmbedThreads * kEmbedUnroll);
-    if (zero_status st = check_blocks(blocks)) return st;
-    return launched(launch_embed(a, param_dt, out_dt, wide, blocks, stream));
+    const int64_t units = (int64_t)kEmbedThreads * kEmbedUnroll, part = part_of(n, most_blocks(kEmbedThreads) * units / a.upr);
+    const int64_t first = a.drop.first;
+    for (int64_t r = 0; r < n; r += part) {
+      a.n = std::min(part, n - r);
+      a.tokens = (const char*)tokens + r * isize(token_it);
+      a.out = (char*)out + r * out_stride * esize(out_dt);
+      a.drop.first = first + r * hidden;
+      if (const int err = launch_embed(a, param_dt, out_dt, wide, ceil_div(a.n * a.upr, units), stream)) return hip_fail(err);
+    }
+    return ok();
   });
 }
 
@@ -382,7 +391,8 @@ zero_status zero_embed_grad(zero_plan_t p, int32_t tensor, int64_t hidden, const
     const int64_t blocks = a.chunk_blocks + (accumulate ? 0 : ceil_div(a.row_hi - a.row_lo, a.fill_rows));
     a.join_tiles = (int32_t)ceil_div(hidden, hidden >= 4 ? 256 : 64);
     const int64_t joins = ceil_div(a.n_chunks, kJoinChunks) * a.join_tiles;
-    if (zero_status st = check_blocks(std::max(blocks, joins))) return st;
+    if (zero_status st = check_blocks(blocks, kGradThreads)) return st;
+    if (zero_status st = check_blocks(joins, kJoinThreads)) return st;
     if (const int err = launch_grad(a, dy_dt, dst_dt, vec, blocks, stream)) return hip_fail(err);
     if (a.n_chunks < 2) return ok();   // no run crosses a boundary
     return launched(launch_grad_join(a, dst_dt, hidden >= 4, joins, stream));
@@ -407,14 +417,18 @@ zero_status zero_dropout(const void* x, const void* residual, void* out, int64_t
     if (residual && out != residual && overlap(w, range_of(residual, n, esize(dt), "residual")))
       return fail(ZERO_EINVAL, "out overlaps the residual without being it");
     if (n == 0) return ok();
-    a.x = x;
-    a.residual = residual;
-    a.out = out;
-    a.n = n;
     a.f = (float)keep;
-    const int64_t blocks = ceil_div(n, (int64_t)kDropoutThreads * vec_of(dt, dt));
-    if (zero_status st = check_blocks(blocks)) return st;
-    return launched(launch_dropout(a, dt, blocks, stream));
+    const int64_t per = (int64_t)kDropoutThreads * vec_of(dt, dt), part = most_blocks(kDropoutThreads) * per;
+    const int64_t first = a.drop.first;
+    for (int64_t e = 0; e < n; e += part) {   // parts of whole workgroups keep the accesses' alignment
+      a.n = std::min(part, n - e);
+      a.x = (const char*)x + e * esize(dt);
+      a.residual = residual ? (const char*)residual + e * esize(dt) : nullptr;
+      a.out = (char*)out + e * esize(dt);
+      a.drop.first = first + e;
+      if (const int err = launch_dropout(a, dt, ceil_div(a.n, per), stream)) return hip_fail(err);
+    }
+    return ok();
   });
 }
 
@@ -441,19 +455,22 @@ zero_status zero_token_logp(const void* logits, zero_dtype dt, int64_t n, int64_
     if (n == 0) return ok();
     LogpArgs a;
     memset(&a, 0, sizeof a);
-    a.logits = logits;
-    a.labels = labels;
-    a.logp = logp;
-    a.stats = stats;
     a.part = (float*)workspace;
-    a.n = n;
     a.stride = stride;
     a.vocab = (int32_t)vocab;
     a.lab64 = label_it == ZERO_I64;
-    a.splits = (int32_t)logp_splits(n, vocab);
-    a.cached_from = (int32_t)std::max<int64_t>(0, n - kCachedBytes / (vocab * esize(dt)));
-    if (zero_status st = check_blocks(n * a.splits)) return st;
-    if (const int err = launch_logp(a, dt, stream)) return hip_fail(err);
+    a.splits = (int32_t)logp_splits(n, vocab);   // 1 wherever the rows take several launches
+    const int64_t cached_from = n - kCachedBytes / (vocab * esize(dt));
+    const int64_t part = part_of(n, most_blocks(logp_threads(n, vocab)) / a.splits);
+    for (int64_t r = 0; r < n; r += part) {
+      a.n = std::min(part, n - r);
+      a.logits = (const char*)logits + r * stride * esize(dt);
+      a.labels = (const char*)labels + r * isize(label_it);
+      a.logp = logp + r;
+      a.stats = stats + 2 * r;
+      a.cached_from = (int32_t)std::max<int64_t>(0, std::min(a.n, cached_from - r));
+      if (const int err = launch_logp(a, dt, stream)) return hip_fail(err);
+    }
     return a.splits > 1 ? launched(launch_logp_join(a, dt, stream)) : ok();
   });
 }
@@ -507,7 +524,14 @@ zero_status zero_preference_loss(int64_t n_pairs, const void* offsets, zero_ityp
     a.slope = n_pairs ? beta * grad_scale / (double)n_pairs : 0.0;
     a.off64 = offset_it == ZERO_I64;
     a.lab64 = label_it == ZERO_I64;
-    return launched(launch_preference(a, stream));
+    // The launch of the last pairs also takes the rows in no sequence, and the mean.
+    const int64_t most = most_blocks(kPrefThreads) - 1;
+    do {
+      a.pair_count = std::min(most, n_pairs - a.pair0);
+      if (const int err = launch_preference(a, stream)) return hip_fail(err);
+      a.pair0 += a.pair_count;
+    } while (a.pair0 < n_pairs);
+    return ok();
   });
 }
 
@@ -531,19 +555,23 @@ zero_status zero_token_logp_grad(const void* logits, zero_dtype dt, int64_t n, i
     if (n == 0) return ok();
     LogpArgs a;
     memset(&a, 0, sizeof a);
-    a.logits = logits;
-    a.labels = labels;
-    a.stats = const_cast<float*>(stats);
-    a.coef = coef;
-    a.dlogits = dlogits;
-    a.n = n;
     a.stride = stride;
     a.dl_stride = dl_stride;
     a.vocab = (int32_t)vocab;
     a.lab64 = label_it == ZERO_I64;
     a.splits = (int32_t)dlogits_splits(vocab);
-    if (zero_status st = check_blocks(n * a.splits)) return st;
-    return launched(launch_dlogits(a, dt, stream));
+    const int64_t part = part_of(n, most_blocks(kDlogitsThreads) / a.splits);
+    for (int64_t end = n; end > 0; end -= part) {   // the last rows first, as in each launch
+      const int64_t r = std::max<int64_t>(0, end - part);
+      a.n = end - r;
+      a.logits = (const char*)logits + r * stride * esize(dt);
+      a.labels = (const char*)labels + r * isize(label_it);
+      a.stats = const_cast<float*>(stats) + 2 * r;
+      a.coef = coef + r;
+      a.dlogits = (char*)dlogits + r * dl_stride * esize(dt);
+      if (const int err = launch_dlogits(a, dt, stream)) return hip_fail(err);
+    }
+    return ok();
   });
 }
 
