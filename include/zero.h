@@ -368,8 +368,8 @@ ZERO_API zero_status zero_set_stream_write_window(void* stream, int64_t period_t
  * current device, which has to be the one of the buffers and of the stream.
  * A call whose work exceeds one launch (2^32 work items) issues several.
  * Sums, softmax statistics and norms are held in fp32 or more and are taken
- * in an order that depends on the sizes alone, so that a call repeated on the
- * same inputs gives the same bits.
+ * in an order that the sizes, the ids and the alignment of the buffers fix, so
+ * that a call repeated on the same buffers gives the same bits.
  *
  * Integers in device memory (tokens, labels, offsets) cannot be checked on
  * the host.  Each kernel checks them itself: an id outside its range is
@@ -452,7 +452,10 @@ ZERO_API zero_status zero_token_order(const void* tokens, zero_itype token_it, i
  * read it.
  *   g[r, c] = f * sum over the positions i with tokens[i] == r, ascending,
  *             of keep(i, c) * dy[i, c]            (f as in zero_embed)
- *   The sum is fp32, in an order fixed by n and hidden; g is rounded once.
+ *   The sum is fp32, in an order fixed by n, hidden and the tokens; g is
+ *   rounded once.  Neither the plan, rank, accumulate, the types nor the
+ *   buffers change that order: an owner's slice holds the bits that the full
+ *   buffer holds there.
  *   sorted, order  what zero_token_order wrote for these n tokens.
  *   dy          n rows of `hidden` elements, dy_stride elements apart.
  *   scale, drop what the forward call had (scale may hold a loss scale too).

@@ -299,6 +299,58 @@ def test_embed_grad_repeats_bit_for_bit(gpu, zero_lib):
     assert torch.equal(a[:rows * hidden].view(torch.int16), b[:rows * hidden].view(torch.int16))
 
 
+SLICES = [
+    # n, rows, hidden, dy, p, before, kind, n_d
+    (8192, 5000, 768, F32, None, 0, "skew", 8),
+    (8192, 300, 768, BF16, 0.1, 33, "uniform", 8),
+    (16384, 3000, 2048, F32, 0.1, 7, "skew", 8),
+    (65536, 5000, 512, F32, None, 0, "skew", 16),
+    (20000, 40, 1601, F32, 0.3, 1, "skew", 3),
+    (30001, 60000, 640, F32, None, 0, "wild", 64),
+    (65536, 700, 2048, BF16, None, 64, "skew", 4),
+    (40000, 900, 768, F32, 0.25, 0, "one", 2),
+]
+
+
+@pytest.mark.parametrize("case", SLICES, ids=lambda c: "-".join(map(str, c)))
+def test_embed_grad_slices_hold_the_bits_of_the_whole(gpu, zero_lib, case):
+    """What each owner's slice receives is what the full buffer holds there,
+    bit for bit in fp32, whether the waves share chunks or not; and the full
+    buffer is right."""
+    import torch
+    Z = zero_lib
+    n, rows, hidden, ydt, p, before, kind, n_d = case
+    say(f"[slices] {case}")
+    rng = np.random.default_rng(n + hidden)
+    plan = Z.zero_plan(before + rows * hidden, n_d, [before, rows * hidden], 0, 1)
+    ids = make_ids(rng, n, rows, kind)
+    if kind == "skew":                       # a third of them over the whole table, in every owner's slice
+        ids[::3] = rng.integers(0, rows, len(ids[::3]))
+    ids_t, _ = as_ids(torch, gpu, ids, True, extra=False)
+    dy = randn(torch, gpu, rng, (n, hidden), ydt)
+    drop, spec = make_drop(Z, p, first=5)
+    s, o = order_of(torch, Z, ids_t, rows)
+    ws = torch.empty(Z.zero_embed_grad_workspace_bytes(n, hidden), dtype=torch.uint8, device=gpu)
+    full = torch.zeros(plan.psi_pad, device=gpu)
+    Z.zero_embed_grad(plan, 1, hidden, s, o, dy, ydt, 0.7, full, F32, drop=drop, workspace=ws)
+    S = plan.shard_total
+    for rank in range(n_d):
+        part = torch.zeros(S, device=gpu)
+        Z.zero_embed_grad(plan, 1, hidden, s, o, dy, ydt, 0.7, part, F32, drop=drop, rank=rank, workspace=ws)
+        assert torch.equal(part.view(torch.int32), full[rank * S:(rank + 1) * S].view(torch.int32)), rank
+    cols = sorted({0, hidden // 2, hidden - 1})
+    dyn = np.zeros((n, len(cols)))
+    for k, c in enumerate(cols):             # columns of the definition: the mask's positions are of whole rows
+        dyn[:, k] = R.to64(dy[:, c])
+        if spec is not None:
+            keep = np.concatenate([R.mask_block(*spec[:4], spec[4] + i * hidden + c, 1) for i in range(n)])
+            dyn[:, k] = np.where(keep, dyn[:, k], 0.0)
+    f = 0.7 * (R.keep_factor(p) if p else 1.0)
+    want, bound = R.embed_grad(ids, dyn, rows, f, None)
+    got = R.to64(full[before:before + rows * hidden].view(rows, hidden)[:, cols])
+    R.check(got, want, bound + np.abs(want) * U + 2.0 ** -149, "columns")
+
+
 def test_embed_grad_against_differences(gpu, zero_lib):
     """The lookup is linear in the table: <dy, embed(T + D) - embed(T)> equals
     <grad, D> up to rounding, with the same dropout in both."""

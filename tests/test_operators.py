@@ -232,18 +232,31 @@ def test_launch_shapes(tmp_path):
     assert " 0 failures" in r.stdout
 
 
-@pytest.mark.skipif(shutil.which("g++") is None, reason="g++ not available")
-def test_launch_limits(tmp_path):
-    """Calls at the limits of the documented sizes and beyond what one launch
-    takes (2^32 work items): cut into launches that cover the work once, or
-    refused (tests/native/ops_limits.cpp)."""
-    exe = tmp_path / "ops_limits"
+def _run_native(tmp_path, name):
+    """Builds tests/native/<name>.cpp, which stands in for the launchers, with
+    the host sources under sanitizers, and runs it."""
+    exe = tmp_path / name
     csrc = os.path.join(ROOT, "zero_sharded_mixed_02_amd", "csrc")
     cmd = ["g++", "-std=c++17", "-O1", "-g", "-fsanitize=address,undefined", "-fno-sanitize-recover=undefined", "-Wall",
-           "-Werror", "-I", os.path.join(ROOT, "include"), "-I", csrc, os.path.join(ROOT, "tests", "native", "ops_limits.cpp"),
+           "-Werror", "-I", os.path.join(ROOT, "include"), "-I", csrc, os.path.join(ROOT, "tests", "native", name + ".cpp"),
            os.path.join(csrc, "zero_api.cpp"), os.path.join(csrc, "zero_ops_api.cpp"), "-o", str(exe)]
     subprocess.run(cmd, check=True, capture_output=True, text=True)
     env = dict(os.environ, ASAN_OPTIONS="detect_leaks=1:verify_asan_link_order=0")
     r = subprocess.run([str(exe)], capture_output=True, text=True, env=env, timeout=300)
     assert r.returncode == 0, r.stdout + r.stderr
     assert " 0 failures" in r.stdout
+
+
+@pytest.mark.skipif(shutil.which("g++") is None, reason="g++ not available")
+def test_launch_limits(tmp_path):
+    """Calls at the limits of the documented sizes and beyond what one launch
+    takes (2^32 work items): cut into launches that cover the work once, or
+    refused (tests/native/ops_limits.cpp)."""
+    _run_native(tmp_path, "ops_limits")
+
+
+@pytest.mark.skipif(shutil.which("g++") is None, reason="g++ not available")
+def test_slices_are_cut_like_the_whole(tmp_path):
+    """The table's gradient: an owner's slice has the whole buffer's chunks, and
+    waves that share one take whole runs (tests/native/ops_shapes_order.cpp)."""
+    _run_native(tmp_path, "ops_shapes_order")

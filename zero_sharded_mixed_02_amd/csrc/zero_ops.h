@@ -91,6 +91,22 @@ constexpr int kJoinThreads = 512;
 constexpr int kJoinChunks = 16;          // chunks it looks after
 constexpr int kJoinLong = 64;            // chunks from which a run is cut into pieces
 
+// Positions [lo, hi) of a chunk.
+struct Span {
+  int lo, hi;
+};
+
+// What one of `parts` waves takes of the positions [p0, p1) of a chunk: the
+// runs that begin in its part, whole, the first one beginning at p0.  `starts`
+// has a bit for each position where a token differs from the one before.
+constexpr Span runs_of_part(uint64_t starts, int p0, int p1, int chunk, int parts, int part) {
+  const uint64_t begins = (starts | (uint64_t(1) << p0)) >> p0 << p0;
+  const int each = chunk / parts, q0 = part * each, q1 = part + 1 < parts ? q0 + each : 64;
+  const uint64_t from0 = begins >> q0 << q0, from1 = q1 < 64 ? begins >> q1 << q1 : 0;
+  const int lo = from0 ? __builtin_ctzll(from0) : p1, hi = from1 ? __builtin_ctzll(from1) : p1;
+  return Span{lo < p1 ? lo : p1, hi < p1 ? hi : p1};
+}
+
 struct GradArgs {
   const int32_t* sorted;
   const int32_t* order;
@@ -105,13 +121,14 @@ struct GradArgs {
   int32_t hidden;
   int32_t chunk;
   int32_t n_chunks;
-  int32_t tiles;           // column tiles of the chunk kernel
+  int32_t tiles;           // workgroups of a group of chunks: column tiles times parts
   int32_t fill_rows;       // rows of one zero-fill workgroup
   int32_t accumulate;
   float f;
   int64_t chunk_blocks;    // workgroups before those that write zero rows
   int32_t stream_dy;       // dy is read past the caches
   int32_t join_tiles;      // column tiles of the join
+  int32_t parts;           // waves that share a chunk's runs
   DropArgs drop;
 };
 

@@ -535,7 +535,8 @@ __global__ __launch_bounds__(kSortThreads) void radix_move_kernel(const RadixArg
 // The positions in token order are cut into chunks of equal length, whatever
 // their tokens, so that frequent tokens spread over as many waves as rare ones.
 // A wave owns one chunk and one tile of columns and sums its runs of equal
-// tokens in fp32 registers.  A run inside a chunk is finished there.  One that
+// tokens in fp32 registers; for a slice with few chunks, two or four waves share
+// the runs of one.  A run inside a chunk is finished there.  One that
 // crosses a boundary leaves a partial row (fp32, in the workspace) in each
 // chunk it touches: slot 2c of chunk c if it came in from the chunk before,
 // slot 2c + 1 if it begins in c and goes on.  A workgroup's waves own
@@ -704,7 +705,11 @@ __global__ __launch_bounds__(kGradThreads) void grad_kernel(const GradArgs a) {
   const int wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
   const int64_t group = blockIdx.x / (uint32_t)a.tiles;
   const int64_t c = group * kGradChunks + wave;
-  const int32_t tile = (int32_t)(blockIdx.x - group * a.tiles) * 64 * N;
+  const uint32_t piece = (uint32_t)(blockIdx.x - group * a.tiles);
+  const int32_t tile = (int32_t)(piece / (uint32_t)a.parts) * 64 * N;
+  // Consecutive workgroups go to the XCDs in turn: the part changes with the
+  // group, so that no XCD gets the parts where long runs begin alone.
+  const int part = (int)((piece + (uint32_t)group) % (uint32_t)a.parts);
   const int32_t begin = tile + lane * N;
   const bool on = begin < a.hidden;
   const int32_t col = begin < a.hidden - N ? begin : a.hidden - N;
@@ -718,15 +723,21 @@ __global__ __launch_bounds__(kGradThreads) void grad_kernel(const GradArgs a) {
     // The chunk's tokens and positions, one a lane (a chunk has at most 64).
     const int64_t s = c * a.chunk;
     const int len = (int)(s + a.chunk < a.n ? a.chunk : a.n - s);
-    const int64_t mine = s + (lane < len ? lane : len - 1);
-    const int32_t rows = a.sorted[mine], from = a.order[mine];
+    const int64_t at = s + (lane < len ? lane : len - 1);
+    const int32_t rows = a.sorted[at], from = a.order[at];
     const int32_t before = a.sorted[s > 0 ? s - 1 : 0], after = a.sorted[s + len < a.n ? s + len : 0];
     const int32_t poss = (uint32_t)from < (uint64_t)a.n ? from : -1;
     const uint64_t here = __ballot(lane < len && rows >= a.row_lo && rows < a.row_hi);
     if (!here) return false;
-    const int p0 = __builtin_ctzll(here), p1 = 64 - __builtin_clzll(here);   // what is written, in sorted rows
+    int p0 = __builtin_ctzll(here), p1 = 64 - __builtin_clzll(here);   // what is written, in sorted rows
     const int32_t left_of = __shfl_up(rows, 1);   // by all lanes: a lane reads only from active ones
     const uint64_t starts = __ballot(lane > 0 && lane < len && rows != left_of);
+    if (a.parts > 1) {
+      const Span mine = runs_of_part(starts, p0, p1, a.chunk, a.parts, part);
+      p0 = mine.lo;
+      p1 = mine.hi;
+      if (p0 >= p1) return false;
+    }
     bool head = p0 == 0 && s > 0 && before == __builtin_amdgcn_readlane(rows, 0);   // came in from the chunk before
     const bool goes_on = p1 == len && s + len < a.n && after == __builtin_amdgcn_readlane(rows, len - 1);
     const bool whole_run = head && goes_on && !starts;

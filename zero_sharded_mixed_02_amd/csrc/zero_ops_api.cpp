@@ -143,22 +143,27 @@ SortShape sort_shape(int64_t n, int64_t rows) {
   return s;
 }
 
-// Positions per chunk, of the `part` that an owner holds of all of them: as
-// many as leave the GPU about 4096 waves, within [4, 64], but no fewer than
-// the workspace is made for (16384 waves of all positions).  Longer chunks
-// write fewer partial rows (32768 x 768: 53 us at 24, 59 at 8), shorter ones
-// give few positions more waves (an eighth of 65536 x 2048: 58 us at 64, 48 at
-// 32; 64 x 768: 12.3 us at 16, 7.3 at 4).
-int64_t chunk_for(int64_t n, int64_t hidden, int64_t waves, double part) {
+// Positions per chunk, from n and hidden alone: a run is summed chunk by chunk,
+// so that an owner's slice holds the bits of the whole buffer only if it is cut
+// alike.  As many as leave the GPU about 4096 waves, from 4 to 32, and 64 where
+// that still leaves 32768 waves.  Longer chunks write fewer partial rows (the
+// whole buffer of 32768 x 768: 47 us at 24, 54 at 8; of 2^20 x 768: 410 at 64,
+// 427 at 32), shorter ones have fewer rows in a row in one wave (an eighth of
+// 65536 x 2048: 59 us at 64, 48 at 32; the whole: 127 and 131).
+int64_t grad_chunk(int64_t n, int64_t hidden) {
   const double tiles = (double)ceil_div(hidden, 256);
-  const int64_t want = (int64_t)((double)n * part * tiles / (double)waves + 3.0) / 4 * 4;
-  return std::min<int64_t>(64, std::max<int64_t>(4, want));
+  const int64_t want = (int64_t)((double)n * tiles / 4096.0 + 3.0) / 4 * 4;
+  return want >= 512 ? 64 : std::min<int64_t>(32, std::max<int64_t>(4, want));
 }
 
-int64_t least_chunk(int64_t n, int64_t hidden) { return chunk_for(n, hidden, 16384, 1.0); }
-
-int64_t grad_chunk(int64_t n, int64_t hidden, double part) {
-  return std::max(least_chunk(n, hidden), chunk_for(n, hidden, 4096, part));
+// Waves that share a chunk's runs, where a slice leaves the GPU few: none with
+// fewer than 8 positions.  An eighth of 65536 x 2048 in 47.8, 44.5 and 49.5 us
+// at 1, 2 and 4, of 8192 x 8192 in 41.7, 37.3 and 40.2; a 64th of 65536 x 768 in
+// 39.9, 35.1 and 32.9; half of 65536 x 2048 in 75, 81 and 86.
+int32_t grad_parts(int64_t n, int64_t hidden, int64_t chunk, double share) {
+  const double waves = (double)n * share * (double)ceil_div(hidden, 256) / (double)chunk;
+  const int64_t parts = waves > 2048 ? 1 : waves > 256 ? 2 : 4;
+  return (int32_t)std::max<int64_t>(1, std::min(parts, chunk / 8));
 }
 
 // Workgroups per row: one where the rows fill the GPU, else enough for about
@@ -310,7 +315,7 @@ zero_status zero_token_order(const void* tokens, zero_itype token_it, int64_t n,
 
 size_t zero_embed_grad_workspace_bytes(int64_t n, int64_t hidden) {
   if (n <= 0 || n > kMaxTokens || hidden < 1 || hidden > kMaxHidden) return 0;
-  return (size_t)(2 * ceil_div(n, least_chunk(n, hidden))) * (size_t)hidden * 4;
+  return (size_t)(2 * ceil_div(n, grad_chunk(n, hidden))) * (size_t)hidden * 4;
 }
 
 zero_status zero_embed_grad(zero_plan_t p, int32_t tensor, int64_t hidden, const int32_t* sorted,
@@ -378,9 +383,10 @@ zero_status zero_embed_grad(zero_plan_t p, int32_t tensor, int64_t hidden, const
     // eight, 408 with four).
     int vec = hidden < 4 ? 1 : 4;
     if (vec_of(dy_dt, dst_dt) == 8 && hidden >= 8 && ceil_div(hidden, 512) * 2 == ceil_div(hidden, 256)) vec = 8;
-    a.chunk = (int32_t)grad_chunk(n, hidden, (double)(a.hi - a.lo) / (double)numel);
+    a.chunk = (int32_t)grad_chunk(n, hidden);
     a.n_chunks = (int32_t)ceil_div(n, a.chunk);
-    a.tiles = (int32_t)ceil_div(hidden, 64 * vec);
+    a.parts = grad_parts(n, hidden, a.chunk, (double)(a.hi - a.lo) / (double)numel);
+    a.tiles = (int32_t)ceil_div(hidden, 64 * vec) * a.parts;
     // Zero rows: 128 KiB a workgroup, down to 8 KiB where that leaves fewer than
     // about 2048 workgroups.
     const int64_t row_bytes = hidden * esize(dst_dt);
