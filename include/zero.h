@@ -514,6 +514,9 @@ ZERO_API zero_status zero_dropout(const void* x, const void* residual, void* out
  *               logits are large).
  *   workspace, ws_bytes  zero_token_logp_workspace_bytes(n, vocab) bytes,
  *               16-byte aligned (few rows are split over the GPU).
+ * The label's own term is added to the others' sum last and in fp64, so that
+ * logp, and the label's gradient below, keep their relative accuracy where the
+ * label is nearly certain.
  * -inf logits (masked ids) count as probability 0; a row of nothing else, and
  * a row with NaN or +inf, gives logp NaN, as the formula does.
  * Errors: EINVAL for nulls, n < 0, vocab < 1, a short stride, misalignment, a

@@ -564,6 +564,96 @@ def test_token_logp_without_a_distribution(gpu, zero_lib):
                 R.check(d[t], want, np.abs(want) * 2 * (tol + 20 * U) + R.half_step(np.abs(want) * (1 + tol), dt), f"row {t}")
 
 
+SURE = [(7, 9, 1), (12, 1009, 0), (9, 1009, 2), (7, 8200, 1), (6, 50257, 0), (5, 50257, 2), (3, 131071, 0), (4, 131072, 2),
+        (1030, 300, 0)]
+
+
+@pytest.mark.parametrize("n,vocab,dt", SURE)
+def test_labels_that_are_almost_certain(gpu, zero_lib, n, vocab, dt):
+    """Labels whose logit stands up to 90 above the others', at the row's ends
+    and inside: the log-probability, the log of the sum and the label's
+    gradient keep their relative accuracy, however close the probability is to
+    1, and a row's gradient sums to zero."""
+    import torch
+    Z = zero_lib
+    say(f"[sure] {n} x {vocab} dt={dt}")
+    rng = np.random.default_rng(vocab + n)
+    g = Guarded(torch, gpu, n * vocab, R.torch_type(dt))
+    x = g.t.view(n, vocab)
+    x.copy_(randn(torch, gpu, rng, (n, vocab), dt))
+    labels = rng.integers(0, vocab, n)
+    labels[:2] = 0, vocab - 1
+    x[torch.arange(n), torch.from_numpy(labels).to(gpu)] = torch.tensor([6.0, 10, 14, 18, 22, 28, 40, 90])[np.arange(n) % 8].to(x.dtype).to(gpu)
+    lab_t = torch.from_numpy(labels).to(gpu)
+    lp, st, d = torch.empty(n, device=gpu), torch.empty(2 * n, device=gpu), torch.empty((n, vocab), dtype=x.dtype, device=gpu)
+    ws = torch.empty(max(1, Z.zero_token_logp_workspace_bytes(n, vocab)), dtype=torch.uint8, device=gpu)
+    coef = rng.standard_normal(n).astype(np.float32)
+    Z.zero_token_logp(x, dt, lab_t, lp, st, ws)
+    Z.zero_token_logp_grad(x, dt, lab_t, st, torch.from_numpy(coef).to(gpu), d)
+    torch.cuda.synchronize()
+    g.check()
+    x64, coef = R.to64(x), coef.astype(np.float64)
+    y = x64[np.arange(n), labels]
+    others = x64.copy()
+    others[np.arange(n), labels] = -np.inf
+    with np.errstate(under="ignore"):
+        rest = np.exp(others - y[:, None]).sum(1)
+    top = np.maximum(y, others.max(1))
+    ls = np.where(y == top, np.log1p(rest), np.log1p(rest) + (y - top))
+    # the sum over the others is off by e of itself, and log1p and expm1 of it by
+    # no more; each result rounds once, and 2^-149 is fp32's smallest step
+    e = R.logsum_bound(vocab)
+    R.check(R.to64(st).reshape(n, 2)[:, 1], ls, np.where(y == top, ls, 1 + np.abs(ls)) * (e + 2 * U) + 2.0 ** -149, "log of the sum")
+    R.check(R.to64(lp), -np.log1p(rest), np.log1p(rest) * (e + 2 * U) * np.where(y == top, 1, 4) + 2.0 ** -149, "logp")
+    want = coef * (rest / (1 + rest))
+    # where the label is not the maximum, (x - max) - ls is rounded twice more
+    rel = e + (8 + np.where(y == top, 0, 4 * (np.abs(y - top) + 1))) * U
+    got = R.to64(d)
+    R.check(got[np.arange(n), labels], want, np.abs(want) * rel + R.half_step(want * (1 + rel), dt) + 2.0 ** -126, "label")
+    if dt == F32:
+        off = got.sum(1)                      # in 64 bits, of entries that are off by their own rounding
+        with np.errstate(under="ignore"):
+            z = np.where(np.isfinite(others), np.abs(others - top[:, None]), 0)
+            span = (np.exp(others - y[:, None]) / (1 + rest[:, None]) * z).sum(1)      # the exponents' roundings
+        R.check(off, np.zeros(n), np.abs(coef) * (2 * rest / (1 + rest) * (rel + e + 16 * U) + 6 * U * span) + vocab * 2.0 ** -126, "row sum")
+
+
+def test_labels_on_special_logits(gpu, zero_lib):
+    """Labels whose own logit is NaN or +inf (no log-probability), -inf beside
+    finite ones, and finite beside nothing but -inf (probability 1)."""
+    import torch
+    Z = zero_lib
+    for dt in (F32, F16, BF16):
+        for vocab in (1, 2, 5, 1001, 9000, 70001):
+            say(f"[logp] special labels dt={dt} vocab={vocab}")
+            at = vocab // 2
+            x = torch.zeros((5, vocab), dtype=R.torch_type(dt), device=gpu)
+            x[0, at] = float("nan")
+            x[1, at] = float("inf")
+            x[2, at] = float("-inf")
+            x[3] = float("-inf")
+            x[3, at] = -3.0
+            x[4, at] = torch.finfo(R.torch_type(dt)).min
+            labels = torch.full((5,), at, dtype=torch.int64, device=gpu)
+            lp, st, d = torch.empty(5, device=gpu), torch.empty(10, device=gpu), torch.empty_like(x)
+            ws = torch.empty(max(1, Z.zero_token_logp_workspace_bytes(5, vocab)), dtype=torch.uint8, device=gpu)
+            Z.zero_token_logp(x, dt, labels, lp, st, ws)
+            Z.zero_token_logp_grad(x, dt, labels, st, torch.full((5,), 2.0, device=gpu), d)
+            got, d = R.to64(lp), R.to64(d)
+            assert np.isnan(got[:2]).all() and np.isnan(d[0]).all() and np.isnan(d[1, at]), got
+            assert got[3] == 0 and not d[3].any()
+            if vocab == 1:                       # nothing but -inf, and one finite logit
+                assert np.isnan(got[2]) and got[4] == 0 and d[4, 0] == 0
+                continue
+            want = R.to64(x[4, at]).item() - np.log(vocab - 1)
+            assert got[2] == -np.inf and abs(got[4] - want) <= abs(want) * 2 * U + R.logsum_bound(vocab), got
+            p = np.full(vocab, -2 / (vocab - 1))
+            p[at] = 2
+            for t in (2, 4):                     # exp of fp16's lowest value is 0 in fp32
+                tol = np.abs(p) * (R.logsum_bound(vocab) + 24 * U)
+                R.check(d[t], p, tol + R.half_step(np.abs(p) + tol, dt), f"row {t}")
+
+
 # ---------------------------------------------------------------------------
 # Preference loss
 # ---------------------------------------------------------------------------

@@ -1025,14 +1025,30 @@ __device__ __forceinline__ void reduce_stats(float& m, float& s) {
   for (int w = 0; w < kWaves; ++w) s += rebase(sm[w], ss[w], m);
 }
 
+// exp(z) for z <= 0 to 3 * 2^-24 of itself, however far down: fp32's
+// exponential takes the fraction of z log2 e, and a double its whole part.
+__device__ __forceinline__ double far_exp(double z) {
+  if (z < -10000.0) return 0.0;
+  const double t = z * 1.4426950408889634, k = rint(t);
+  return ldexp((double)__builtin_amdgcn_exp2f((float)(t - k)), (int)k);
+}
+
+// Statistics and log-probability of a row from its label's logit y and from
+// the maximum m and the sum s of exp(x - m) over the other logits.  Kept apart,
+// since a likely label's term would drown them: with y at the top, the log of
+// the sum is log(1 + rest), right in its last bits however small the rest.
 template <int DT>
-__device__ __forceinline__ void write_stats(const LogpArgs& a, int64_t t, int64_t label, float m, float s) {
-  const double ls = log((double)s);
-  float y[1];
-  to_float<DT, 1>(load<DT, 1>(a.logits, t * a.stride + label), y);
-  a.stats[2 * t] = m;
+__device__ __forceinline__ void write_stats(const LogpArgs& a, int64_t t, const Raw<DT, 1>& logit, float m, float s) {
+  const float y = widen<DT>(logit.w[0]), top = __builtin_fmaxf(m, y);
+  const double gap = (double)y - (double)m, small = m == y ? 1.0 : far_exp(gap > 0 ? -gap : gap);
+  const bool first = y >= m;
+  const double rest = first ? (double)s * small : (double)s + small - 1.0;
+  double ls = log(top == neg_inf() ? (double)s : 1.0 + rest);
+  if (first && rest < 0x1p-20) ls = top == neg_inf() ? ls : rest - 0.5 * rest * rest;
+  ls += first && top != neg_inf() ? (double)y - (double)top : 0.0;   // 0, or NaN where y is infinite
+  a.stats[2 * t] = top;
   a.stats[2 * t + 1] = (float)ls;
-  a.logp[t] = (float)(((double)y[0] - (double)m) - ls);
+  a.logp[t] = (float)(((double)y - (double)top) - ls);
 }
 
 // log softmax at the label, in one pass over the logits with a running maximum
@@ -1065,8 +1081,16 @@ __global__ __launch_bounds__(THREADS) void logp_kernel(const LogpArgs a) {
   const int per = (vecs + a.splits - 1) / a.splits;
   const int v0 = part * per;
   const int v1 = v0 + per < vecs ? v0 + per : vecs;
-  float m = neg_inf(), s = 0.0f;
+  float m = neg_inf(), s = 0.0f;   // of all but the label: see write_stats
   const int tid = threadIdx.x;
+  const Raw<DT, 1> logit = load<DT, 1>(a.logits, row + label);   // on its way while the rest is read
+  const int lab = (int)label - head, lab_vec = lab >= 0 ? lab / N : -1, lab_in = lab % N;   // its access, its place there
+  auto without_label = [&](float* x) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) x[i] = i == lab_in ? neg_inf() : x[i];
+  };
+  // The step of the workgroup's accesses that meets it.
+  const int lab_step = lab_vec < v0 ? -1 : v0 + (lab_vec - v0) / (U * THREADS) * (U * THREADS);
   int v = v0;
   auto stream = [&](auto nt) {
     for (; v + U * THREADS <= v1; v += U * THREADS) {
@@ -1078,6 +1102,11 @@ __global__ __launch_bounds__(THREADS) void logp_kernel(const LogpArgs a) {
 #pragma unroll
         for (int i = 0; i < N; ++i) x[j * N + i] = y[i];
       }
+      if (v == lab_step) {   // uniform
+#pragma unroll
+        for (int j = 0; j < U; ++j)
+          if (v + j * THREADS + tid == lab_vec) without_label(x + j * N);
+      }
       absorb<U * N>(x, m, s);
     }
   };
@@ -1086,14 +1115,15 @@ __global__ __launch_bounds__(THREADS) void logp_kernel(const LogpArgs a) {
   for (v += tid; v < v1; v += THREADS) {
     float x[N];
     to_float<DT, N>(load<DT, N>(a.logits, row + head + (int64_t)v * N), x);
+    if (v == lab_vec) without_label(x);
     absorb<N>(x, m, s);
   }
-  if (part == 0 && tid < head) {
+  if (part == 0 && tid < head && tid != (int)label) {
     float x[1];
     to_float<DT, 1>(load<DT, 1>(a.logits, row + tid), x);
     absorb<1>(x, m, s);
   }
-  if (part == a.splits - 1 && tid < tail) {
+  if (part == a.splits - 1 && tid < tail && a.vocab - tail + tid != (int)label) {
     float x[1];
     to_float<DT, 1>(load<DT, 1>(a.logits, row + a.vocab - tail + tid), x);
     absorb<1>(x, m, s);
@@ -1104,7 +1134,7 @@ __global__ __launch_bounds__(THREADS) void logp_kernel(const LogpArgs a) {
     a.part[2 * (int64_t)blockIdx.x] = m;
     a.part[2 * (int64_t)blockIdx.x + 1] = s;
   } else {
-    write_stats<DT>(a, t, label, m, s);
+    write_stats<DT>(a, t, logit, m, s);
   }
 }
 
@@ -1116,11 +1146,12 @@ __global__ __launch_bounds__(64) void logp_join_kernel(const LogpArgs a) {
   const int64_t label = load_id(a.labels, t, a.lab64);
   if ((uint64_t)label >= (uint64_t)a.vocab) return;   // written by logp_kernel
   const float* p = a.part + 2 * t * a.splits;
+  const Raw<DT, 1> logit = load<DT, 1>(a.logits, t * a.stride + label);
   float m = neg_inf();
   for (int k = 0; k < a.splits; ++k) m = __builtin_fmaxf(m, p[2 * k]);
   float s = 0.0f;
   for (int k = 0; k < a.splits; ++k) s += rebase(p[2 * k], p[2 * k + 1], m);
-  write_stats<DT>(a, t, label, m, s);
+  write_stats<DT>(a, t, logit, m, s);
 }
 
 // Gradient of the logits, coef (onehot - softmax): one piece of a row per
@@ -1149,14 +1180,14 @@ __global__ __launch_bounds__(kDlogitsThreads) void dlogits_kernel(const LogpArgs
   const int v0 = part * per;
   const int v1 = v0 + per < vecs ? v0 + per : vecs;
   const int tid = threadIdx.x;
-  auto grad = [&](float x, int j) {
-    const float p = exp_of((x - m) - ls);
-    return zero ? 0.0f : (j == (int)label ? coef * (1.0f - p) : -coef * p);
-  };
+  const int lab = zero ? -1 : (int)label;
+  auto grad = [&](float x) { return zero ? 0.0f : -coef * exp_of((x - m) - ls); };
+  // 1 - p of the label, which keeps its bits where p is close to 1.
+  auto label_grad = [&](float x) { return coef * -expm1f((x - m) - ls); };
   auto one = [&](int j) {
     float x[1] = {0.0f};
     if (!zero) to_float<DT, 1>(load<DT, 1>(a.logits, row + j), x);
-    x[0] = grad(x[0], j);
+    x[0] = j == lab ? label_grad(x[0]) : grad(x[0]);
     store<DT, 1>(a.dlogits, drow + j, from_float<DT, 1>(x));
   };
   for (int v = v0 + tid; v < v1; v += U * kDlogitsThreads) {
@@ -1174,8 +1205,15 @@ __global__ __launch_bounds__(kDlogitsThreads) void dlogits_kernel(const LogpArgs
       float x[N];
       to_float<DT, N>(raw[j], x);
       const int at0 = head + u * N;
+      const bool has = (uint32_t)(lab - at0) < (uint32_t)N;
+      float hot = 0.0f;
+      if (has) {
 #pragma unroll
-      for (int i = 0; i < N; ++i) x[i] = grad(x[i], at0 + i);
+        for (int i = 0; i < N; ++i) hot = at0 + i == lab ? x[i] : hot;
+        hot = label_grad(hot);
+      }
+#pragma unroll
+      for (int i = 0; i < N; ++i) x[i] = has && at0 + i == lab ? hot : grad(x[i]);
       store<DT, N, true>(a.dlogits, drow + at0, from_float<DT, N>(x));
     }
   }
