@@ -260,3 +260,17 @@ def test_slices_are_cut_like_the_whole(tmp_path):
     """The table's gradient: an owner's slice has the whole buffer's chunks, and
     waves that share one take whole runs (tests/native/ops_shapes_order.cpp)."""
     _run_native(tmp_path, "ops_shapes_order")
+
+
+@pytest.mark.skipif(shutil.which("g++") is None, reason="g++ not available")
+def test_search_stays_inside(tmp_path):
+    """The gradient's search among the sorted tokens looks at no index outside
+    them, also once it has ended (tests/native/ops_search.cpp)."""
+    exe = tmp_path / "ops_search"
+    csrc = os.path.join(ROOT, "zero_sharded_mixed_02_amd", "csrc")
+    subprocess.run(["g++", "-std=c++17", "-O1", "-g", "-fsanitize=address,undefined", "-fno-sanitize-recover=undefined", "-Wall",
+                    "-Werror", "-I", os.path.join(ROOT, "include"), "-I", csrc,
+                    os.path.join(ROOT, "tests", "native", "ops_search.cpp"), "-o", str(exe)], check=True, capture_output=True, text=True)
+    env = dict(os.environ, ASAN_OPTIONS="verify_asan_link_order=0")
+    r = subprocess.run([str(exe)], capture_output=True, text=True, env=env, timeout=300)
+    assert r.returncode == 0, r.stdout + r.stderr

@@ -91,6 +91,23 @@ constexpr int kJoinThreads = 512;
 constexpr int kJoinChunks = 16;          // chunks it looks after
 constexpr int kJoinLong = 64;            // chunks from which a run is cut into pieces
 
+// A search for the first index in [lo, hi) whose key is not below the wanted
+// one, by 64 lanes that look at an index each.
+struct LowerBound {
+  int64_t lo, hi;
+  constexpr bool open() const { return hi > lo; }
+  // At least 1, so that a search which has ended (beside another that goes on)
+  // has all lanes at hi or beyond.
+  constexpr int64_t step() const { return hi - lo > 64 ? (hi - lo + 63) / 64 : 1; }
+  constexpr int64_t probe(int lane) const { return lo + (lane + 1) * step() - 1; }   // nothing to look at from hi on
+  constexpr void narrow(int below) {   // that many lanes saw a key below
+    const int64_t s = step();
+    lo += below * s;
+    if (lo > hi) lo = hi;
+    if (lo + s - 1 < hi) hi = lo + s - 1;
+  }
+};
+
 // Positions [lo, hi) of a chunk.
 struct Span {
   int lo, hi;

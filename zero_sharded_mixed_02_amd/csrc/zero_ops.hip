@@ -557,29 +557,22 @@ __global__ __launch_bounds__(kSortThreads) void radix_move_kernel(const RadixArg
 __device__ __forceinline__ void wave_lower_bounds(const int32_t* sorted, int64_t n, int64_t key0, int64_t key1,
                                                   int64_t& at0, int64_t& at1) {
   const int lane = threadIdx.x & 63;
-  int64_t lo[2] = {0, 0}, hi[2] = {n, n};
+  LowerBound search[2] = {{0, n}, {0, n}};
   const int64_t key[2] = {key0, key1};
-  while (hi[0] > lo[0] || hi[1] > lo[1]) {
+  while (search[0].open() || search[1].open()) {
     int32_t probe[2];
     bool in[2];
-    int64_t step[2];
 #pragma unroll
     for (int k = 0; k < 2; ++k) {
-      step[k] = (hi[k] - lo[k] + 63) / 64;
-      const int64_t i = lo[k] + (lane + 1) * step[k] - 1;
-      in[k] = i < hi[k];
+      const int64_t i = search[k].probe(lane);
+      in[k] = i < search[k].hi;
       probe[k] = sorted[in[k] ? i : 0];
     }
 #pragma unroll
-    for (int k = 0; k < 2; ++k) {
-      const uint64_t less = __ballot(in[k] && (int64_t)probe[k] < key[k]);
-      lo[k] += (int64_t)__popcll(less) * step[k];
-      if (lo[k] > hi[k]) lo[k] = hi[k];
-      if (step[k] > 0 && lo[k] + step[k] - 1 < hi[k]) hi[k] = lo[k] + step[k] - 1;
-    }
+    for (int k = 0; k < 2; ++k) search[k].narrow(__popcll(__ballot(in[k] && (int64_t)probe[k] < key[k])));
   }
-  at0 = lo[0];
-  at1 = lo[1];
+  at0 = search[0].lo;
+  at1 = search[1].lo;
 }
 
 __device__ __forceinline__ int64_t wave_lower_bound(const int32_t* sorted, int64_t n, int64_t key) {
