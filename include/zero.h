@@ -554,7 +554,8 @@ ZERO_API zero_status zero_token_logp(const void* logits, zero_dtype dt, int64_t 
  *   loss[1], pair_loss[n_pairs], rewards[2 * n_pairs], coef[n]  device fp32.
  *               coef of rows in no sequence is 0.
  * Errors: EINVAL for nulls, negative sizes, smoothing outside [0, 1], a
- * non-finite beta or grad_scale, misalignment or overlapping buffers;
+ * non-finite beta or grad_scale, beta * grad_scale / n_pairs beyond fp32,
+ * misalignment or overlapping buffers;
  * EUNSUPPORTED for n_pairs above 2^29 or n above 2^31 - 1.
  */
 ZERO_API zero_status zero_preference_loss(int64_t n_pairs, const void* offsets, zero_itype offset_it, int64_t n,

@@ -156,6 +156,18 @@ def test_preference_loss_refuses(Z):
     assert call(n=1 << 31) == Z.ZERO_EUNSUPPORTED
 
 
+def test_preference_loss_refuses_a_slope_beyond_fp32(Z):
+    """beta and grad_scale that are finite each, but whose product is not, or is
+    no fp32: the coefficients would be infinite or NaN."""
+    L = Z.load()
+
+    def call(beta, gs, pairs=2):
+        return L.zero_preference_loss(pairs, P(0), 1, 50, P(1), 1, 10, P(2), P(3), beta, 0.0, gs, P(4), P(5), P(6), P(7), None)
+    for beta, gs in ((1e200, 1e200), (-1e300, 1e10), (1e20, 1e20), (3.5e38, 2.0)):
+        assert call(beta, gs) == Z.ZERO_EINVAL, (beta, gs)
+        assert "fp32" in Z.zero_last_error()
+
+
 def test_binding_refuses(Z, monkeypatch):
     """The binding's own checks, on CPU tensors: no C call is made."""
     import torch

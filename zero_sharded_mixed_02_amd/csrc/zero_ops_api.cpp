@@ -494,6 +494,8 @@ zero_status zero_preference_loss(int64_t n_pairs, const void* offsets, zero_ityp
     if (!(smoothing >= 0.0 && smoothing <= 1.0)) return fail(ZERO_EINVAL, "smoothing must lie in [0, 1] (got %g)", smoothing);
     if (!std::isfinite(beta)) return fail(ZERO_EINVAL, "beta is not finite");
     if (!std::isfinite(grad_scale)) return fail(ZERO_EINVAL, "grad_scale is not finite");
+    const double slope = n_pairs > 0 ? beta * grad_scale / (double)n_pairs : 0.0;
+    if (!std::isfinite((float)slope)) return fail(ZERO_EINVAL, "beta * grad_scale / n_pairs = %g is beyond fp32", slope);
     if (n_pairs > (int64_t(1) << 29)) return fail(ZERO_EUNSUPPORTED, "n_pairs = %lld exceeds 2^29", (long long)n_pairs);
     if (n > INT32_MAX) return fail(ZERO_EUNSUPPORTED, "n = %lld exceeds %d", (long long)n, INT32_MAX);
     const int64_t n_off = n_pairs ? 2 * n_pairs + 1 : 0;
@@ -527,7 +529,7 @@ zero_status zero_preference_loss(int64_t n_pairs, const void* offsets, zero_ityp
     a.vocab = vocab;
     a.beta = beta;
     a.smoothing = smoothing;
-    a.slope = n_pairs ? beta * grad_scale / (double)n_pairs : 0.0;
+    a.slope = slope;
     a.off64 = offset_it == ZERO_I64;
     a.lab64 = label_it == ZERO_I64;
     // The launch of the last pairs also takes the rows in no sequence, and the mean.
