@@ -85,6 +85,17 @@ def mask_block(seed, site, step, p, first, n):
     return z.view(np.uint16)[first - 4 * a:first - 4 * a + n].astype(np.int64) >= cut_of(p)
 
 
+def mask_at(seed, site, step, p, positions):
+    """The same at an array of positions."""
+    e = np.asarray(positions, np.int64)
+    with np.errstate(over="ignore"):
+        z = (e // 4 + 1).astype(np.uint64) * np.uint64(GAMMA) + np.uint64(drop_key(seed, site, step))
+        z = (z ^ (z >> np.uint64(30))) * np.uint64(MIX1)
+        z = (z ^ (z >> np.uint64(27))) * np.uint64(MIX2)
+        z = z ^ (z >> np.uint64(31))
+    return (z >> (16 * (e % 4)).astype(np.uint64) & np.uint64(0xFFFF)).astype(np.int64) >= cut_of(p)
+
+
 def keep_factor(p):
     cut = cut_of(p)
     return 65536.0 / (65536 - cut) if cut < 65536 else 0.0

@@ -1061,6 +1061,74 @@ def test_embed_grad_of_many_activations(gpu, zero_lib):
 
 
 @pytest.mark.big
+@pytest.mark.parametrize("hidden,dt,gdt,first,n_d", [(1024, BF16, BF16, 0, 1), (1024, F16, F16, 3, 1), (1536, BF16, F16, 4, 8),
+                                                     (1030, BF16, BF16, 1, 1), (512, F32, BF16, 4, 1), (1024, BF16, BF16, None, 4)])
+def test_embed_grad_past_the_caches(gpu, zero_lib, hidden, dt, gdt, first, n_d):
+    """dy larger than the 256 MiB cache, which is read past it, into 16-bit
+    gradients: masks that start a word and that do not, and none; some columns
+    against 64 bits, of the full buffer and of an owner's slice."""
+    import torch
+    Z = zero_lib
+    rows, before = 3000, 64
+    n = (260 << 20) // (hidden * (4 if dt == F32 else 2)) + 77
+    say(f"[big] gradient past the caches {n} x {hidden} dt={dt}")
+    g = torch.Generator(device=gpu).manual_seed(5)
+    dy = torch.empty((n, hidden), dtype=R.torch_type(dt), device=gpu).normal_(generator=g)
+    ids = torch.randint(-1, rows, (n,), generator=g, device=gpu)
+    ids[::4] = 17                            # one token in many chunks
+    idn = ids.cpu().numpy()
+    plan = Z.zero_plan(before + rows * hidden, n_d, [before, rows * hidden], 0, 8)
+    drop, spec = (None, None) if first is None else make_drop(Z, 0.1, first=first)
+    s, o = order_of(torch, Z, ids, rows)
+    ws = torch.empty(Z.zero_embed_grad_workspace_bytes(n, hidden), dtype=torch.uint8, device=gpu)
+    full = torch.empty(plan.psi_pad, dtype=R.torch_type(gdt), device=gpu)
+    Z.zero_embed_grad(plan, 1, hidden, s, o, dy, dt, 0.03, full, gdt, drop=drop, workspace=ws)
+    cols = [0, 1, 7, 255, 256, 511, hidden // 2 + 3, hidden - 9, hidden - 2, hidden - 1]
+    part = R.to64(dy[:, torch.tensor(cols, device=gpu)])
+    f = 0.03
+    if spec is not None:
+        at = spec[4] + np.arange(n)[:, None] * hidden + np.array(cols)[None]
+        part, f = np.where(R.mask_at(*spec[:4], at), part, 0.0), f * R.keep_factor(0.1)
+    want, bound = R.embed_grad(idn, part, rows, f, None)
+    got = full[before:before + rows * hidden].view(rows, hidden)[:, torch.tensor(cols, device=gpu)]
+    tol = bound + np.abs(want) * U
+    R.check(R.to64(got), want, tol + R.half_step(np.abs(want) + tol, gdt), "columns")
+    if n_d > 1:
+        S = plan.shard_total
+        for rank in (0, n_d - 1):
+            mine = torch.zeros(S, dtype=full.dtype, device=gpu)
+            Z.zero_embed_grad(plan, 1, hidden, s, o, dy, dt, 0.03, mine, gdt, drop=drop, rank=rank, workspace=ws)
+            lo, hi = max(0, before - rank * S), min(S, before + rows * hidden - rank * S)
+            assert torch.equal(mine[lo:hi], full[rank * S + lo:rank * S + hi]), rank
+
+
+@pytest.mark.big
+@pytest.mark.parametrize("n,vocab,dt", [(4100, 9001, BF16), (4096, 32767, F16), (4097, 8192, F32), (4095, 9001, BF16)])
+def test_logp_of_many_middling_rows(gpu, zero_lib, n, vocab, dt):
+    """Rows that one wave reads where there are 4096 of them (and a whole
+    workgroup where there is one less), some against 64 bits."""
+    import torch
+    Z = zero_lib
+    say(f"[big] logp {n} x {vocab} dt={dt}")
+    g = torch.Generator(device=gpu).manual_seed(n)
+    x = torch.empty((n, vocab), dtype=R.torch_type(dt), device=gpu).normal_(0, 2, generator=g)
+    labels = torch.randint(0, vocab, (n,), generator=g, device=gpu)
+    labels[5::9] = -100
+    lp, st = torch.full((n,), 7.0, device=gpu), torch.full((2 * n,), 7.0, device=gpu)
+    Z.zero_token_logp(x, dt, labels, lp, st)
+    pick = sorted({0, 1, 2, 5, 63, 64, n // 2, n - 2, n - 1})
+    lab = labels[pick].cpu().numpy()
+    top, ls, want = R.softmax_rows(R.to64(x[pick]), lab)
+    # one wave's threads see eight times as many groups as logsum_bound counts,
+    # each a sum of 16 terms (or 8) and a change of the maximum at worst
+    e = R.logsum_bound(vocab) + (vocab / 512 + 4) * (4 + np.log2(vocab + 1)) * U
+    R.check(R.to64(st).reshape(n, 2)[pick, 0], top, 0.0, "max")
+    R.check(R.to64(lp[pick]), want, e + np.abs(want) * 2 * U, "logp")
+    whole = torch.where(labels >= 0, torch.log_softmax(x.float(), 1).gather(1, labels.clamp(min=0)[:, None])[:, 0], 0.0)
+    assert float((lp - whole).abs().max()) <= 2 * (e + 32 * 2 * U)       # torch's fp32 form is off as much at most, by its own sums
+
+
+@pytest.mark.big
 def test_logits_past_32_bits(gpu, zero_lib):
     """2.6e9 logits: the first and the last rows, forward and in place backward."""
     import torch

@@ -203,6 +203,12 @@ def test_reference_masks_agree():
     assert abs(share - p) < 4 * math.sqrt(p * (1 - p) / n)
 
 
+def test_reference_mask_at_positions():
+    for first in (0, 3, (1 << 34) + 3):
+        at = np.arange(first, first + 41, 5)
+        assert np.array_equal(R.mask_at(5, 6, 7, 0.3, at), R.keep_mask(5, 6, 7, 0.3, at))
+
+
 def test_reference_preference_by_hand():
     """One pair of one-row sequences: h = beta (a - b), loss log(1 + e^-h)."""
     loss, pair, rewards, coef = R.preference(np.array([0, 1, 2]), np.array([True, True]), np.array([-1.0, -2.0]),
