@@ -1319,27 +1319,70 @@ def copy_probe(torch):
     print(json.dumps({"probe": "copy", "bytes_read_per_dispatch": 4 * n, "bytes_written_per_dispatch": 4 * n}))
 
 
+def operator_forms(cases):
+    """(name, case, pass) of the cases of perf/operators.py, and of uses beside
+    them: the gradient added to a tied table's, the logits' gradient in place,
+    fp32."""
+    import zero_sharded_mixed_02_amd as Z
+
+    def accumulating(s):
+        Z.zero_token_order(s["ids"], s["vocab"], s["sorted"], s["order"], s["ws"])
+        Z.zero_embed_grad(s["plan"], 1, s["hidden"], s["sorted"], s["order"], s["dy"], s["code"], s["scale"], s["grad"],
+                          s["code"], drop=s["drop"], rank=s["rank"], accumulate=True, workspace=s["ws"])
+
+    def in_place(s):
+        # what a pass leaves are finite numbers, which the next one takes for logits
+        Z.zero_token_logp(s["logits"], s["code"], s["labels"], s["logp"], s["stats"], s["ws"])
+        Z.zero_preference_loss(s["offsets"], s["labels"], s["vocab"], s["logp"], s["ref"], s["beta"], s["smoothing"],
+                               s["grad_scale"], s["loss"], s["pair_loss"], s["rewards"], s["coef"])
+        Z.zero_token_logp_grad(s["logits"], s["code"], s["labels"], s["stats"], s["coef"], s["logits"])
+
+    forms = [(c["name"], c, cases.run) for c in cases.listed()]
+    named = {c["name"]: c for c in cases.listed()}
+    for name in ("embed_grad small odd", "embed_grad gpt2", "embed_grad wide"):
+        forms.append((name + ", accumulating", named[name], accumulating))
+    for name in ("preference train", "preference train wide"):
+        forms.append((name + ", in place", named[name], in_place))
+    for name in ("embed wide", "embed_grad gpt2", "embed_grad owner slice", "dropout residual", "preference train"):
+        forms.append((name + ", fp32", dict(named[name], dtype="f32"), cases.run))
+    return forms
+
+
+def operator_bytes(torch, cases, case, state, name):
+    """Bytes that a pass has to read and write; of a table, the rows that the
+    ids really name."""
+    nbytes = cases.work(case)["bytes"]
+    es = cases.BYTES[case["dtype"]]
+    if case["op"] == "embed":
+        rows = int(torch.unique(state["ids"][state["ids"] >= 0]).numel())
+        nbytes -= (min(case["tokens"], case["vocab"]) - rows) * case["hidden"] * es
+    if name.endswith("accumulating"):     # the rows that are named, read and written, in place of the whole table
+        rows = int(torch.unique(state["ids"][state["ids"] >= 0]).numel())
+        nbytes += (2 * rows - case["vocab"]) * case["hidden"] * es
+    return nbytes
+
+
 def operators_run(torch):
-    """Times the vocabulary operators over the cases of perf/operators.py, with
-    the launches queued back to back (two states in turn, so that a call finds
-    another call's data in the caches); one JSON line."""
+    """Times the vocabulary operators, with the launches queued back to back
+    (two states in turn, so that a call finds another call's data in the
+    caches); one JSON line."""
     import importlib.util
     spec = importlib.util.spec_from_file_location("operator_cases", os.path.join(ROOT, "perf", "operators.py"))
     cases = importlib.util.module_from_spec(spec)
     spec.loader.exec_module(cases)
     cases.own = True
     out = {}
-    for case in cases.listed():
+    for name, case, run_pass in operator_forms(cases):
         states = [cases.prepare(case, seed) for seed in (1, 2)]
         turn = [0]
 
         def run():
             turn[0] ^= 1
-            cases.run(states[turn[0]])
+            run_pass(states[turn[0]])
         ms = _time_launches(torch, run)
-        nbytes = cases.work(case)["bytes"]
-        out[case["name"]] = {"us": round(ms * 1e3, 2), "needed_bytes": round(nbytes), "gbps": round(nbytes / ms / 1e6, 1)}
-        log(f"{case['name']}: {ms * 1e3:.2f} us")
+        nbytes = operator_bytes(torch, cases, case, states[0], name)
+        out[name] = {"us": round(ms * 1e3, 2), "needed_bytes": round(nbytes), "gbps": round(nbytes / ms / 1e6, 1)}
+        log(f"{name}: {ms * 1e3:.2f} us")
         del states
         release(torch)
     print(json.dumps({"metric": "vocabulary operators, us a call", "data": "synthetic", "operators": out}))
@@ -1376,7 +1419,7 @@ def main():
                     help="time a plain 4 GiB device copy (calibrates HBM byte counters)")
     ap.add_argument("--operators", action="store_true",
                     help="time the embedding, dropout and preference-loss operators over the cases of "
-                         "perf/operators.py, print one JSON line and exit")
+                         "perf/operators.py, and accumulating, in place and in fp32; print one JSON line and exit")
     ap.add_argument("--no-cpu-baseline", action="store_true")
     ap.add_argument("--kernels", action="store_true",
                     help="also time every entry point at its own workload (adds a 'kernels' object)")

@@ -10,8 +10,9 @@
 // memory at any address; where a row's length is no multiple of an access, its
 // last access is moved back to end with the row.
 //
-// Times below are of single launches on one MI355X.  There a large copy moves
-// 6.0 TB/s (read and written together) and a large read 7.1 TB/s.
+// Times below are on one MI355X, where a large copy moves 6.0 TB/s (read and
+// written together) and a large read 7.1 TB/s: of single launches, after some
+// tens of the same, or of whole calls where they say so.
 //
 // Floating point: compiled with -ffp-contract=off; fused multiply-adds are
 // written out where they are meant.
@@ -285,7 +286,8 @@ __device__ __forceinline__ uint32_t row_in(uint32_t t, uint32_t upr, uint32_t ma
 // are loaded together, then their rows.  Bound by the output's stores beside
 // row reads that the caches serve in part: 65536 rows of 8192 fp16 of skewed
 // ids in 250 us, 1.07 GB written and 0.27 GB of different rows (5.4 TB/s; 270 us
-// with dropout).  Stores are non-temporal (8% there); one, two or eight
+// with dropout, and up to 350 some fifteen calls after a pause, while the clock
+// dips).  Stores are non-temporal (8% there); one, two or eight
 // accesses a thread take 343, 291 and 266 us, and walking the table in column
 // tiles, for more hits in the L2, 268 us and more.
 // DROP: 0 no dropout, 1 rows of whole accesses, so that the mask runs on with
@@ -546,10 +548,10 @@ __global__ __launch_bounds__(kSortThreads) void radix_move_kernel(const RadixArg
 // zeros to the rows that no token names.
 //
 // Bound by HBM at the large end: 65536 x 8192 bf16 with dropout into 50257 rows
-// takes 372 us for 1.07 GB read and 0.85 GB written (5.2 TB/s) and 17 us for the
-// join.  How often a token repeats does not matter: 2^20 positions of 768 take
-// 355 us evenly spread and 364 us all of one token.  At GPT-2-small's size
-// (8192 x 768, 20 + 6 us) 77 MB of mostly zero rows and the latencies of search,
+// takes 369 us for 1.07 GB read and 0.85 GB written (5.2 TB/s) and 15 us for the
+// join.  How often a token repeats hardly matters: 2^20 positions of 768 take
+// 333 + 23 us evenly spread and 280 + 83 us all of one token.  At GPT-2-small's
+// size (8192 x 768, 20 + 6 us) 77 MB of mostly zero rows and the latencies of search,
 // gather and join count.
 
 // First indices in [0, n) whose sorted token is >= key0 and >= key1 (n if
@@ -684,8 +686,8 @@ __device__ void fill_rows(const GradArgs& a, int64_t block) {
 
 // DROP: 0 no dropout, 1 every access starts a word of the mask, 2 any.
 // NT: dy is read past the caches, which is faster where it exceeds the Infinity
-// Cache (2^20 x 768: 528 us against 544) and slower where it may sit there
-// (32768 x 768: 64 against 54), as it does when the backward pass just wrote it.
+// Cache (calls of 2^20 x 768: 408 us against 440, of 65536 x 8192: 403 against
+// 415) and slower where it may sit there (32768 x 768: 55 against 48), as it does when the backward pass just wrote it.
 template <int YDT, int GDT, int N, int DROP, bool NT>
 __global__ __launch_bounds__(kGradThreads) void grad_kernel(const GradArgs a) {
   if ((int64_t)blockIdx.x >= a.chunk_blocks) {
@@ -823,7 +825,7 @@ __global__ __launch_bounds__(kGradThreads) void grad_kernel(const GradArgs a) {
 // tile of columns.  A lane each finds out which chunks have one; short runs go
 // to a wave each, and long ones (64 chunks and more) are cut into one piece a
 // wave, joined in order in shared memory.  Bound by latency: 6 us after 8192 x
-// 768, 17 after 65536 x 8192.
+// 768, 15 after 65536 x 8192.
 template <int GDT, int N>
 __global__ __launch_bounds__(kJoinThreads) void grad_join_kernel(const GradArgs a) {
   constexpr int kWaves = kJoinThreads / 64;
@@ -1048,7 +1050,7 @@ __device__ __forceinline__ void write_stats(const LogpArgs& a, int64_t t, const 
 // and sum in every thread.  One row, or one of `splits` pieces of a row, per
 // workgroup.  Loads are aligned: the elements before the first 16-byte boundary
 // of the row and behind the last one are taken singly.  Bound by HBM: 12288 scored
-// rows of 131072 bf16 in 480 us (6.7 TB/s), 6144 of 50257 in 95 us (6.5 TB/s).
+// rows of 131072 bf16 in 467 us (6.9 TB/s), 6144 of 50257 in 97 us (6.4 TB/s).
 // Loads past the caches gain 10% at the large end; the last kCachedBytes of
 // rows go through them, for the gradient that may follow.
 template <int DT, int THREADS>
@@ -1149,9 +1151,9 @@ __global__ __launch_bounds__(64) void logp_join_kernel(const LogpArgs a) {
 
 // Gradient of the logits, coef (onehot - softmax): one piece of a row per
 // workgroup, the last rows first.  Bound by HBM: 16384 rows of 131072 bf16, 12288 of
-// them scored, in 1173 us for 7.5 GB (6.4 TB/s).  Short workgroups do best: with
-// the forward pass 1637 us at 128 threads of two accesses, 1697 at 256, 1810 at
-// four accesses, 2000 and more at one; cached stores cost another 3%.
+// them scored, in 1162 us for 7.5 GB (6.5 TB/s).  Short workgroups do best: with
+// the forward pass 1636 us at 128 threads of two accesses, 1689 at 256, 1748 at
+// four accesses, 1898 at one; cached stores cost another 3%.
 template <int DT>
 __global__ __launch_bounds__(kDlogitsThreads) void dlogits_kernel(const LogpArgs a) {
   constexpr int N = 16 / es_of<DT>;

@@ -379,8 +379,8 @@ zero_status zero_embed_grad(zero_plan_t p, int32_t tensor, int64_t hidden, const
     a.accumulate = accumulate;
     a.f = (float)(scale * keep);
     // Eight columns a lane, unless four leave fewer lanes of the last tile idle
-    // (2^20 x 768: 407 us with four, 427 with eight; 65536 x 8192: 397 with
-    // eight, 408 with four).
+    // (calls of 2^20 x 768: 408 us with four, 428 with eight; of 65536 x 8192: 403
+    // with eight, 430 with four).
     int vec = hidden < 4 ? 1 : 4;
     if (vec_of(dy_dt, dst_dt) == 8 && hidden >= 8 && ceil_div(hidden, 512) * 2 == ceil_div(hidden, 256)) vec = 8;
     a.chunk = (int32_t)grad_chunk(n, hidden);
