@@ -75,7 +75,7 @@ int main() {
   // Chunks of random runs, cut at both ends by what the slice holds.
   std::mt19937_64 rng(3);
   for (int trial = 0; trial < 200000; ++trial) {
-    const int chunk = 4 * (1 + (int)(rng() % 16)), parts = 1 << (rng() % 3), len = trial % 4 ? chunk : 1 + (int)(rng() % chunk);
+    const int chunk = 4 * (1 + (int)(rng() % 16)), parts = 1 + (int)(rng() % 4), len = trial % 4 ? chunk : 1 + (int)(rng() % chunk);
     uint64_t starts = rng();
     for (int k = (int)(rng() % 4); k > 0; --k) starts &= rng();
     starts &= (len < 64 ? (uint64_t(1) << len) - 1 : ~uint64_t(0)) & ~uint64_t(1);

@@ -309,6 +309,8 @@ SLICES = [
     (30001, 60000, 640, F32, None, 0, "wild", 64),
     (65536, 700, 2048, BF16, None, 64, "skew", 4),
     (40000, 900, 768, F32, 0.25, 0, "one", 2),
+    (36000, 2000, 700, F32, None, 5, "skew", 64),             # chunks of 28, shared by three waves
+    ((1 << 21) - 77, 5000, 8, F32, None, 1, "skew", 128),     # chunks of 64, shared by four
 ]
 
 

@@ -537,7 +537,7 @@ __global__ __launch_bounds__(kSortThreads) void radix_move_kernel(const RadixArg
 // The positions in token order are cut into chunks of equal length, whatever
 // their tokens, so that frequent tokens spread over as many waves as rare ones.
 // A wave owns one chunk and one tile of columns and sums its runs of equal
-// tokens in fp32 registers; for a slice with few chunks, two or four waves share
+// tokens in fp32 registers; for a slice with few chunks, up to four waves share
 // the runs of one.  A run inside a chunk is finished there.  One that
 // crosses a boundary leaves a partial row (fp32, in the workspace) in each
 // chunk it touches: slot 2c of chunk c if it came in from the chunk before,
