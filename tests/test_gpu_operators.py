@@ -310,7 +310,7 @@ SLICES = [
     (65536, 700, 2048, BF16, None, 64, "skew", 4),
     (40000, 900, 768, F32, 0.25, 0, "one", 2),
     (36000, 2000, 700, F32, None, 5, "skew", 64),             # chunks of 28, shared by three waves
-    ((1 << 21) - 77, 5000, 8, F32, None, 1, "skew", 128),     # chunks of 64, shared by four
+    ((1 << 21) - 77, 5000, 8, F32, None, 1, "uniform", 128),     # chunks of 64, shared by four
 ]
 
 
@@ -340,6 +340,13 @@ def test_embed_grad_slices_hold_the_bits_of_the_whole(gpu, zero_lib, case):
         part = torch.zeros(S, device=gpu)
         Z.zero_embed_grad(plan, 1, hidden, s, o, dy, ydt, 0.7, part, F32, drop=drop, rank=rank, workspace=ws)
         assert torch.equal(part.view(torch.int32), full[rank * S:(rank + 1) * S].view(torch.int32)), rank
+    sums = torch.arange(plan.psi_pad, device=gpu).remainder(97).float()          # added to a tied table's gradient
+    old = sums.clone()
+    Z.zero_embed_grad(plan, 1, hidden, s, o, dy, ydt, 0.7, sums, F32, drop=drop, accumulate=True, workspace=ws)
+    for rank in range(n_d):
+        part = old[rank * S:(rank + 1) * S].clone()
+        Z.zero_embed_grad(plan, 1, hidden, s, o, dy, ydt, 0.7, part, F32, drop=drop, rank=rank, accumulate=True, workspace=ws)
+        assert torch.equal(part.view(torch.int32), sums[rank * S:(rank + 1) * S].view(torch.int32)), rank
     cols = sorted({0, hidden // 2, hidden - 1})
     dyn = np.zeros((n, len(cols)))
     for k, c in enumerate(cols):             # columns of the definition: the mask's positions are of whole rows
@@ -351,6 +358,9 @@ def test_embed_grad_slices_hold_the_bits_of_the_whole(gpu, zero_lib, case):
     want, bound = R.embed_grad(ids, dyn, rows, f, None)
     got = R.to64(full[before:before + rows * hidden].view(rows, hidden)[:, cols])
     R.check(got, want, bound + np.abs(want) * U + 2.0 ** -149, "columns")
+    base = R.to64(old[before:before + rows * hidden].view(rows, hidden)[:, cols])
+    got = R.to64(sums[before:before + rows * hidden].view(rows, hidden)[:, cols])
+    R.check(got, base + want, bound + (2 * np.abs(want) + np.abs(base)) * 2 * U, "columns of the sum")
 
 
 def test_embed_grad_against_differences(gpu, zero_lib):
