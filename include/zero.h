@@ -581,6 +581,216 @@ ZERO_API zero_status zero_token_logp_grad(const void* logits, zero_dtype dt, int
                                           const float* stats, const float* coef, void* dlogits,
                                           int64_t dl_stride, void* stream);
 
+/* ------------------------------------------------------------------------
+ * The model's hidden matrices: their products, forward and backward, on the
+ * flat buffers that a plan lays out, and the step by orthogonalised momentum
+ * (Muon) that trains them in the place of Adam.  They are not operations of
+ * the pages.  The conventions of the operators above hold: nothing is
+ * allocated, nothing synchronises, every call can be captured, a workspace
+ * belongs to one call at a time, and a call repeated on the same buffers gives
+ * the same bits.
+ *
+ * The products read 16-bit operands (ZERO_F16 or ZERO_BF16, one type for a
+ * call) on the matrix units, sum in fp32 and round the finished value once.
+ * Rows may start at any element; operands whose rows are 16-byte aligned and a
+ * multiple of 8 elements long are read faster.  Infinities and NaN go through
+ * as in the formulas.
+ * --------------------------------------------------------------------- */
+
+/* gelu: z Phi(z); gelu_tanh: z sigmoid(2 sqrt(2/pi) (z + 0.044715 z^3)); silu:
+ * z sigmoid(z).  gelu and silu are 0 at -inf, their limit; the slope of relu
+ * at 0 is 0.  Evaluated in fp32, to a few 10^-6 of the value. */
+typedef enum zero_act {
+  ZERO_ACT_NONE = 0,
+  ZERO_ACT_RELU = 1,
+  ZERO_ACT_GELU = 2,
+  ZERO_ACT_GELU_TANH = 3,
+  ZERO_ACT_SILU = 4
+} zero_act;
+
+/*
+ * zero_linear -- a linear layer whose weight is a tensor of the plan.
+ *   z[i, o] = sum_j x[i, j] W[o, j] + b[o]
+ *   y[i, o] = act(z[i, o]) + residual[i, o]
+ *   plan, weight  which tensor; its numel must be a multiple of in_features,
+ *               and it is read as out_features rows of in_features elements.
+ *               The tied vocabulary table is such a weight: y are the logits.
+ *   bias        which tensor holds b (out_features elements), or -1.
+ *   params, dt  the full flat 16-bit parameter buffer; x, residual, pre and y
+ *               have the same type.
+ *   x           n rows, x_stride elements apart.
+ *   residual    n rows of out_features, or NULL.
+ *   pre         receives z for the backward pass (n rows), or NULL.
+ *   y           n rows, y_stride elements apart; it may be the residual itself
+ *               (with the same stride).  What lies between rows is left as it
+ *               was.
+ *   workspace, ws_bytes  zero_linear_workspace_bytes(plan, weight,
+ *               in_features, n) bytes, 16-byte aligned.
+ * Errors: EINVAL for nulls, a tensor index out of range, in_features < 1 or
+ * not dividing the tensor, a bias of another size, a negative n, a short
+ * stride, misalignment, an unknown act, a short workspace, or an output that
+ * overlaps an input (other than y the residual) or another output;
+ * EUNSUPPORTED for fp32, n or out_features above 2^30, or in_features or a
+ * stride above 2^21.
+ */
+ZERO_API size_t zero_linear_workspace_bytes(zero_plan_t plan, int32_t weight, int64_t in_features, int64_t n);
+ZERO_API zero_status zero_linear(zero_plan_t plan, int32_t weight, int32_t bias, int64_t in_features,
+                                 const void* params, zero_dtype dt, const void* x, int64_t n, int64_t x_stride,
+                                 zero_act act, const void* residual, int64_t residual_stride, void* pre,
+                                 int64_t pre_stride, void* y, int64_t y_stride, void* workspace, size_t ws_bytes,
+                                 void* stream);
+
+/*
+ * zero_linear_input_grad -- the gradient of zero_linear's x, on through the
+ * activation that x came out of.
+ *   dx[i, j] = (sum_o dz[i, o] W[o, j]) * act'(pre[i, j]) + addend[i, j]
+ *   dz          the gradient of z: the gradient of y where that layer had no
+ *               activation, else zero_activation_grad's result or this call's
+ *               for the layer behind.
+ *   act, pre    the activation that made x, and what it was taken of (n rows of
+ *               in_features); pre is NULL exactly for ZERO_ACT_NONE.
+ *   addend      a gradient that reaches x by another way, or NULL.
+ *   dx          n rows of in_features; it may be the addend itself.
+ *   workspace, ws_bytes  zero_linear_input_grad_workspace_bytes(...) bytes.
+ * Errors: as zero_linear; EUNSUPPORTED also for out_features above 2^21.
+ */
+ZERO_API size_t zero_linear_input_grad_workspace_bytes(zero_plan_t plan, int32_t weight, int64_t in_features, int64_t n);
+ZERO_API zero_status zero_linear_input_grad(zero_plan_t plan, int32_t weight, int64_t in_features,
+                                            const void* params, zero_dtype dt, const void* dz, int64_t n,
+                                            int64_t dz_stride, zero_act act, const void* pre, int64_t pre_stride,
+                                            const void* addend, int64_t addend_stride, void* dx,
+                                            int64_t dx_stride, void* workspace, size_t ws_bytes, void* stream);
+
+/*
+ * zero_linear_weight_grad -- the gradients of zero_linear's weight and bias: a
+ * rank's contribution to zero_shard_reduce, zero_adam_step or
+ * zero_muon_momentum, written where those read it.
+ *   dW[o, j] = scale * sum_i dz[i, o] x[i, j],  db[o] = scale * sum_i dz[i, o]
+ *   The sums are fp32, in an order fixed by n and the weight's shape; each
+ *   value is rounded once.  Neither the rank, accumulate, dst_dt nor the
+ *   buffers change that order: an owner's slice holds the bits that the full
+ *   buffer holds there.
+ *   bias        which tensor, or -1: no db.
+ *   dst, dst_dt, rank, accumulate  as in zero_embed_grad: rank < 0 is the full
+ *               flat gradient buffer, rank >= 0 that owner's compact slice (of
+ *               which the parts that hold the two tensors are written, and
+ *               what lies outside is not computed); accumulate 1 adds to what
+ *               dst holds.  n = 0 gives zeros, or leaves dst.
+ *   workspace, ws_bytes  zero_linear_weight_grad_workspace_bytes(...) bytes,
+ *               16-byte aligned.
+ * Errors: as zero_linear, and EINVAL for rank >= n_d, accumulate other than 0
+ * or 1, a scale beyond fp32, or weight and bias the same tensor; EUNSUPPORTED
+ * also for out_features above 2^21.
+ */
+ZERO_API size_t zero_linear_weight_grad_workspace_bytes(zero_plan_t plan, int32_t weight, int64_t in_features,
+                                                        int64_t n, int32_t rank);
+ZERO_API zero_status zero_linear_weight_grad(zero_plan_t plan, int32_t weight, int32_t bias, int64_t in_features,
+                                             const void* dz, int64_t dz_stride, const void* x, int64_t x_stride,
+                                             zero_dtype dt, int64_t n, double scale, void* dst, zero_dtype dst_dt,
+                                             int32_t rank, int32_t accumulate, void* workspace, size_t ws_bytes,
+                                             void* stream);
+
+/*
+ * zero_activation_grad -- dz[e] = dy[e] * act'(pre[e]), n contiguous 16-bit
+ * elements, rounded once; dz may be dy.  For a layer whose output's gradient
+ * does not come out of zero_linear_input_grad.
+ * Errors: EINVAL for nulls, a negative n, misalignment, an unknown act, or dz
+ * overlapping pre, or dy without being it; EUNSUPPORTED for fp32.
+ */
+ZERO_API zero_status zero_activation_grad(const void* dy, const void* pre, void* dz, int64_t n, zero_dtype dt,
+                                          zero_act act, void* stream);
+
+/* Muon's hyper-parameters, as decimal values, each rounded once to fp32. */
+typedef struct zero_muon_hyper {
+  double lr;
+  double momentum;         /* mu */
+  double weight_decay;
+  double grad_scale;       /* multiplies the rank sum; 1/N_d gives the mean */
+  int32_t nesterov;        /* 0 or 1 */
+} zero_muon_hyper;
+
+/*
+ * zero_muon_momentum -- the step's first half for the owner's partition of a
+ * plan that holds matrices (other tensors take zero_adam_step, in a plan of
+ * their own): the rank sum and the momentum, in fp32.
+ *   g      = (sum over ranks in rank order) * grad_scale   (zero_adam_step's)
+ *   M      = mu M + g
+ *   update = nesterov ? g + mu M : M, rounded to 16 bits
+ * One IEEE rounding per operation, no fused multiply-add.
+ *   slices, reduced  exactly one, as in zero_adam_step.
+ *   momentum    fp32[shard_total].
+ *   update, update_dt, update_is_full  1: the full flat buffer (psi_pad
+ *               elements) at the owner's ranges, where an all-gather of the
+ *               owners' ranges makes whole matrices for zero_orthogonalize;
+ *               0: a shard-local buffer of shard_total elements.  bf16 holds
+ *               gradients of any scale.
+ * Errors: as zero_adam_step, and EINVAL for hyper-parameters that are not
+ * finite in fp32 or nesterov other than 0 or 1.
+ */
+ZERO_API zero_status zero_muon_momentum(zero_plan_t plan, int32_t rank, const zero_muon_hyper* hyper,
+                                        const zero_grad_src* slices, const float* reduced, float* momentum,
+                                        void* update, zero_dtype update_dt, int32_t update_is_full, void* stream);
+
+/* A tensor of the plan as matrices: its numel is a multiple of rows * cols, and
+ * it holds that many after another. */
+typedef struct zero_matrix {
+  int32_t tensor;
+  int64_t rows, cols;
+  double scale;            /* of the result, e.g. sqrt(max(1, rows / cols)) */
+} zero_matrix;
+
+/* The polynomial, as decimal values.  NULL in its place: 5 steps of
+ * (3.4445, -4.7750, 2.0315), eps 1e-7. */
+typedef struct zero_newton_schulz {
+  int32_t steps;           /* 1 to 32 */
+  double a, b, c;          /* each at most 1000 in size */
+  double eps;              /* > 0, at most 1e30 */
+} zero_newton_schulz;
+
+/*
+ * zero_orthogonalize -- each matrix G of the list towards the nearest matrix
+ * with orthonormal rows or columns.
+ *   X = G / (|G|_F + eps); `steps` times: A = X X^T, X = a X + (b A + c A A) X
+ *   dst = scale * X
+ *   (For rows > cols A = X^T X and X A take their places, which is the same X.)
+ *   The norm is fp64.  X is held in fp32 and enters the products in fp16, as A
+ *   and b A + c A A do; sums are fp32.  The result is within about 0.002 of the
+ *   64-bit one (2-norm over the matrix) for the default polynomial.  A matrix
+ *   of zeros gives zeros, one that holds NaN or an infinity NaN throughout.
+ *   matrices, n_matrices  host array.  No tensor twice.  Matrices of one shape
+ *               run together, whatever their order.
+ *   src, src_dt the full flat 16-bit buffer.
+ *   dst, dst_dt the full flat 16-bit buffer of the results; it may be src, with
+ *               its type.  Only the listed tensors' ranges are written.
+ *   workspace, ws_bytes  zero_orthogonalize_workspace_bytes(...) bytes,
+ *               256-byte aligned.
+ * Errors: EINVAL for nulls, a tensor out of range or twice, rows or cols < 1 or
+ * not dividing the tensor, a scale beyond fp32, a polynomial outside its
+ * limits, misalignment, a short workspace or overlapping buffers; EUNSUPPORTED
+ * for fp32 or rows or cols above 2^20.
+ */
+ZERO_API size_t zero_orthogonalize_workspace_bytes(zero_plan_t plan, const zero_matrix* matrices, int32_t n_matrices);
+ZERO_API zero_status zero_orthogonalize(zero_plan_t plan, const zero_matrix* matrices, int32_t n_matrices,
+                                        const zero_newton_schulz* poly, const void* src, zero_dtype src_dt,
+                                        void* dst, zero_dtype dst_dt, void* workspace, size_t ws_bytes,
+                                        void* stream);
+
+/*
+ * zero_muon_apply -- the step's second half for the owner's partition.
+ *   w = (1 - lr * weight_decay) w - lr * O, in fp32, one rounding per
+ *   operation (1 - lr * weight_decay is taken in fp64 and rounded once), and
+ *   the 16-bit parameters.
+ *   direction, direction_dt, direction_is_full  O: what zero_orthogonalize left
+ *               in the full flat buffer (1), or a shard-local buffer (0).
+ *   master      fp32[shard_total].
+ *   param_dst, param_dt, dst_is_full  as in zero_adam_step.
+ * Errors: as zero_muon_momentum.
+ */
+ZERO_API zero_status zero_muon_apply(zero_plan_t plan, int32_t rank, const zero_muon_hyper* hyper,
+                                     const void* direction, zero_dtype direction_dt, int32_t direction_is_full,
+                                     float* master, void* param_dst, zero_dtype param_dt, int32_t dst_is_full,
+                                     void* stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -27,6 +27,7 @@ LIB_PATH = os.path.join(HERE, "libzero.so")
 
 ZERO_F32, ZERO_F16, ZERO_BF16 = 0, 1, 2
 ZERO_I32, ZERO_I64 = 0, 1
+ZERO_ACT_NONE, ZERO_ACT_RELU, ZERO_ACT_GELU, ZERO_ACT_GELU_TANH, ZERO_ACT_SILU = range(5)
 ZERO_OK, ZERO_EINVAL, ZERO_EUNSUPPORTED, ZERO_ENOMEM, ZERO_EHIP = 0, -1, -2, -3, -4
 ZERO_MAX_RANKS = 128
 
@@ -41,7 +42,11 @@ ENTRY_POINTS = ("zero_version", "zero_last_error", "zero_plan", "zero_plan_destr
                 "zero_embed", "zero_token_order_workspace_bytes", "zero_token_order",
                 "zero_embed_grad_workspace_bytes", "zero_embed_grad", "zero_dropout",
                 "zero_token_logp_workspace_bytes", "zero_token_logp", "zero_preference_loss",
-                "zero_token_logp_grad")
+                "zero_token_logp_grad",
+                "zero_linear_workspace_bytes", "zero_linear", "zero_linear_input_grad_workspace_bytes",
+                "zero_linear_input_grad", "zero_linear_weight_grad_workspace_bytes", "zero_linear_weight_grad",
+                "zero_activation_grad", "zero_muon_momentum", "zero_orthogonalize_workspace_bytes",
+                "zero_orthogonalize", "zero_muon_apply")
 
 
 class ZeroError(RuntimeError):
@@ -63,6 +68,21 @@ class _GradSrc(ctypes.Structure):
 class _Drop(ctypes.Structure):
     _fields_ = [("p", ctypes.c_double), ("seed", ctypes.c_uint64), ("site", ctypes.c_uint64),
                 ("step", ctypes.c_uint64), ("step_dev", ctypes.c_void_p), ("first", ctypes.c_int64)]
+
+
+class _MuonHyper(ctypes.Structure):
+    _fields_ = [("lr", ctypes.c_double), ("momentum", ctypes.c_double), ("weight_decay", ctypes.c_double),
+                ("grad_scale", ctypes.c_double), ("nesterov", ctypes.c_int32)]
+
+
+class _Matrix(ctypes.Structure):
+    _fields_ = [("tensor", ctypes.c_int32), ("rows", ctypes.c_int64), ("cols", ctypes.c_int64),
+                ("scale", ctypes.c_double)]
+
+
+class _NewtonSchulz(ctypes.Structure):
+    _fields_ = [("steps", ctypes.c_int32), ("a", ctypes.c_double), ("b", ctypes.c_double), ("c", ctypes.c_double),
+                ("eps", ctypes.c_double)]
 
 
 _lib = None
@@ -147,6 +167,31 @@ def load():
     L.zero_preference_loss.argtypes = [i64, vp, i32, i64, vp, i32, i64, vp, vp, f64, f64, f64, vp, vp, vp, vp, vp]
     L.zero_token_logp_grad.restype = i32
     L.zero_token_logp_grad.argtypes = [vp, i32, i64, i64, i64, vp, i32, vp, vp, vp, i64, vp]
+    L.zero_linear_workspace_bytes.restype = size
+    L.zero_linear_workspace_bytes.argtypes = [vp, i32, i64, i64]
+    L.zero_linear.restype = i32
+    L.zero_linear.argtypes = [vp, i32, i32, i64, vp, i32, vp, i64, i64, i32, vp, i64, vp, i64, vp, i64, vp, size, vp]
+    L.zero_linear_input_grad_workspace_bytes.restype = size
+    L.zero_linear_input_grad_workspace_bytes.argtypes = [vp, i32, i64, i64]
+    L.zero_linear_input_grad.restype = i32
+    L.zero_linear_input_grad.argtypes = [vp, i32, i64, vp, i32, vp, i64, i64, i32, vp, i64, vp, i64, vp, i64, vp, size,
+                                         vp]
+    L.zero_linear_weight_grad_workspace_bytes.restype = size
+    L.zero_linear_weight_grad_workspace_bytes.argtypes = [vp, i32, i64, i64, i32]
+    L.zero_linear_weight_grad.restype = i32
+    L.zero_linear_weight_grad.argtypes = [vp, i32, i32, i64, vp, i64, vp, i64, i32, i64, f64, vp, i32, i32, i32, vp,
+                                          size, vp]
+    L.zero_activation_grad.restype = i32
+    L.zero_activation_grad.argtypes = [vp, vp, vp, i64, i32, i32, vp]
+    p_hyper = vp  # a zero_muon_hyper, zero_grad_src, zero_matrix or zero_newton_schulz by reference
+    L.zero_muon_momentum.restype = i32
+    L.zero_muon_momentum.argtypes = [vp, i32, p_hyper, vp, vp, vp, vp, i32, i32, vp]
+    L.zero_orthogonalize_workspace_bytes.restype = size
+    L.zero_orthogonalize_workspace_bytes.argtypes = [vp, vp, i32]
+    L.zero_orthogonalize.restype = i32
+    L.zero_orthogonalize.argtypes = [vp, vp, i32, vp, vp, i32, vp, i32, vp, size, vp]
+    L.zero_muon_apply.restype = i32
+    L.zero_muon_apply.argtypes = [vp, i32, p_hyper, vp, i32, i32, vp, vp, i32, i32, vp]
     _lib = L
     return L
 
@@ -739,3 +784,202 @@ def zero_token_logp_grad(logits, dt: int, labels, stats, coef, dlogits, stream=N
     co = c.flat(coef, "coef", 4, n)
     d, dstride = c.rows(dlogits, "dlogits", es, n, v, dl_stride)
     c.issue(load().zero_token_logp_grad, x, dt, n, v, xstride, lab, it, st, co, d, dstride)
+
+
+# ---------------------------------------------------------------------------
+# The model's hidden matrices: products and the step by orthogonalised
+# momentum (see include/zero.h)
+# ---------------------------------------------------------------------------
+#
+# Arguments are checked and calls issued as for the operators above.
+
+def _count(x, n: Optional[int], width: int, name: str) -> int:
+    """Rows of x, or n where x is an address."""
+    if n is not None:
+        return int(n)
+    if x is None or isinstance(x, int):
+        raise ValueError(f"{name} is not a tensor: pass n")
+    return int(x.numel()) // max(1, width)
+
+
+def _out_features(plan: Plan, weight: int, in_features: int) -> int:
+    if not 0 <= weight < plan.n_tensors:
+        raise ValueError(f"weight tensor {weight} out of range")
+    if in_features < 1 or plan.tensor_numel[weight] % in_features:
+        raise ValueError(f"tensor {weight} holds {plan.tensor_numel[weight]} elements, no multiple of "
+                         f"in_features = {in_features}")
+    return plan.tensor_numel[weight] // in_features
+
+
+def zero_linear_workspace_bytes(plan: Plan, weight: int, in_features: int, n: int) -> int:
+    return int(load().zero_linear_workspace_bytes(plan.handle, weight, in_features, n))
+
+
+def zero_linear(plan: Plan, weight: int, in_features: int, params, dt: int, x, y, bias: int = -1,
+                act: int = ZERO_ACT_NONE, residual=None, pre=None, workspace=None, stream=None,
+                n: Optional[int] = None, x_stride: Optional[int] = None, y_stride: Optional[int] = None,
+                residual_stride: Optional[int] = None, pre_stride: Optional[int] = None) -> None:
+    """y = act(x W^T + b) + residual, W and b tensors of the plan inside the
+    full 16-bit parameter buffer params; pre receives x W^T + b.  y may be the
+    residual."""
+    c = _Call(stream)
+    out = _out_features(plan, weight, in_features)
+    n = _count(x, n, in_features, "x")
+    es = _esize(dt)
+    par = c.flat(params, "params", es, plan.psi_pad)
+    xa, xs = c.rows(x, "x", es, n, in_features, x_stride)
+    ya, ys = c.rows(y, "y", es, n, out, y_stride)
+    ra, rs = (0, out) if residual is None else c.rows(residual, "residual", es, n, out, residual_stride)
+    pa, ps = (0, out) if pre is None else c.rows(pre, "pre", es, n, out, pre_stride)
+    ws, ws_bytes = c.workspace(workspace, lambda: zero_linear_workspace_bytes(plan, weight, in_features, n))
+    c.issue(load().zero_linear, plan.handle, weight, bias, in_features, par, dt, xa, n, xs, act, ra, rs, pa, ps, ya,
+            ys, ws, ws_bytes)
+
+
+def zero_linear_input_grad_workspace_bytes(plan: Plan, weight: int, in_features: int, n: int) -> int:
+    return int(load().zero_linear_input_grad_workspace_bytes(plan.handle, weight, in_features, n))
+
+
+def zero_linear_input_grad(plan: Plan, weight: int, in_features: int, params, dt: int, dz, dx,
+                           act: int = ZERO_ACT_NONE, pre=None, addend=None, workspace=None, stream=None,
+                           n: Optional[int] = None, dz_stride: Optional[int] = None,
+                           dx_stride: Optional[int] = None, pre_stride: Optional[int] = None,
+                           addend_stride: Optional[int] = None) -> None:
+    """dx = (dz W) * act'(pre) + addend.  dx may be the addend."""
+    c = _Call(stream)
+    out = _out_features(plan, weight, in_features)
+    n = _count(dx, n, in_features, "dx")
+    es = _esize(dt)
+    par = c.flat(params, "params", es, plan.psi_pad)
+    za, zs = c.rows(dz, "dz", es, n, out, dz_stride)
+    xa, xs = c.rows(dx, "dx", es, n, in_features, dx_stride)
+    pa, ps = (0, in_features) if pre is None else c.rows(pre, "pre", es, n, in_features, pre_stride)
+    aa, as_ = (0, in_features) if addend is None else c.rows(addend, "addend", es, n, in_features, addend_stride)
+    ws, ws_bytes = c.workspace(workspace, lambda: zero_linear_input_grad_workspace_bytes(plan, weight, in_features, n))
+    c.issue(load().zero_linear_input_grad, plan.handle, weight, in_features, par, dt, za, n, zs, act, pa, ps, aa, as_,
+            xa, xs, ws, ws_bytes)
+
+
+def zero_linear_weight_grad_workspace_bytes(plan: Plan, weight: int, in_features: int, n: int, rank: int = -1) -> int:
+    return int(load().zero_linear_weight_grad_workspace_bytes(plan.handle, weight, in_features, n, rank))
+
+
+def zero_linear_weight_grad(plan: Plan, weight: int, in_features: int, dz, x, dt: int, scale: float, dst,
+                            dst_dt: int, bias: int = -1, rank: int = -1, accumulate: bool = False, workspace=None,
+                            stream=None, n: Optional[int] = None, dz_stride: Optional[int] = None,
+                            x_stride: Optional[int] = None) -> None:
+    """dW = scale * dz^T x and db = scale * the column sums of dz, into the full
+    flat gradient buffer dst, or with rank >= 0 into that owner's slice."""
+    c = _Call(stream)
+    out = _out_features(plan, weight, in_features)
+    n = _count(x, n, in_features, "x")
+    es = _esize(dt)
+    za, zs = c.rows(dz, "dz", es, n, out, dz_stride)
+    xa, xs = c.rows(x, "x", es, n, in_features, x_stride)
+    d = c.flat(dst, "dst", _esize(dst_dt), plan.psi_pad if rank < 0 else plan.shard_total)
+    ws, ws_bytes = c.workspace(workspace,
+                               lambda: zero_linear_weight_grad_workspace_bytes(plan, weight, in_features, n, rank))
+    c.issue(load().zero_linear_weight_grad, plan.handle, weight, bias, in_features, za, zs, xa, xs, dt, n, scale, d,
+            dst_dt, rank, 1 if accumulate else 0, ws, ws_bytes)
+
+
+def zero_activation_grad(dy, pre, dz, dt: int, act: int, stream=None, n: Optional[int] = None) -> None:
+    """dz = dy * act'(pre); dz may be dy."""
+    c = _Call(stream)
+    n = _count(dy, n, 1, "dy")
+    es = _esize(dt)
+    ya = c.flat(dy, "dy", es, n)
+    pa = c.flat(pre, "pre", es, n)
+    za = c.flat(dz, "dz", es, n)
+    c.issue(load().zero_activation_grad, ya, pa, za, n, dt, act)
+
+
+class MuonHyper:
+    """Muon's hyper-parameters (zero_muon_hyper)."""
+
+    def __init__(self, lr: float, momentum: float = 0.95, weight_decay: float = 0.0, grad_scale: float = 1.0,
+                 nesterov: bool = True):
+        self.c = _MuonHyper(lr, momentum, weight_decay, grad_scale, 1 if nesterov else 0)
+        self._ref = ctypes.byref(self.c)
+
+
+class Matrices:
+    """Tensors of a plan as matrices: (tensor, rows, cols, scale of the result)
+    for each; a tensor of several times rows * cols holds that many."""
+
+    def __init__(self, entries: Sequence):
+        entries = [(int(t), int(r), int(k), float(s)) for t, r, k, s in entries]
+        self.n = len(entries)
+        self.c = (_Matrix * max(1, self.n))(*[_Matrix(*e) for e in entries])
+
+
+class NewtonSchulz:
+    """The polynomial of zero_orthogonalize (zero_newton_schulz)."""
+
+    def __init__(self, steps: int = 5, a: float = 3.4445, b: float = -4.7750, c: float = 2.0315, eps: float = 1e-7):
+        self.c = _NewtonSchulz(steps, a, b, c, eps)
+        self._ref = ctypes.byref(self.c)
+
+
+def _kind(x, cls, name: str):
+    if not isinstance(x, cls):
+        raise TypeError(f"{name}: expected a {cls.__name__}, got {type(x).__name__}")
+    return x
+
+
+def zero_muon_momentum(plan: Plan, rank: int, hyper: MuonHyper, slices: Optional[GradSrc], reduced, momentum, update,
+                       update_dt: int, update_is_full: bool, stream=None) -> None:
+    """momentum = mu momentum + g, g the scaled rank sum of slices (or reduced),
+    and update = g + mu momentum (or momentum) in 16 bits."""
+    c = _Call(stream)
+    S = plan.shard_total
+    _kind(hyper, MuonHyper, "hyper")
+    src, red = None, 0
+    if slices is not None:
+        slices.check(plan)
+        for q, g in enumerate(slices._keep):
+            c.see(g, f"gradient of rank {q}")
+        src = ctypes.byref(slices.c)
+    if reduced is not None:
+        red = c.flat(reduced, "reduced", 4, S)
+    m = c.flat(momentum, "momentum", 4, S)
+    if update_dt not in (ZERO_F16, ZERO_BF16):
+        raise ValueError(f"update dtype {update_dt} is not 16-bit")
+    u = c.flat(update, "update", 2, plan.psi_pad if update_is_full else S)
+    c.issue(load().zero_muon_momentum, plan.handle, rank, hyper._ref, src, red, m, u, update_dt,
+            1 if update_is_full else 0)
+
+
+def zero_orthogonalize_workspace_bytes(plan: Plan, matrices: Matrices) -> int:
+    _kind(matrices, Matrices, "matrices")
+    return int(load().zero_orthogonalize_workspace_bytes(plan.handle, matrices.c, matrices.n))
+
+
+def zero_orthogonalize(plan: Plan, matrices: Matrices, src, src_dt: int, dst, dst_dt: int,
+                       poly: Optional[NewtonSchulz] = None, workspace=None, stream=None) -> None:
+    """Each listed matrix of the full 16-bit buffer src orthogonalised by
+    Newton-Schulz products into dst (which may be src)."""
+    c = _Call(stream)
+    _kind(matrices, Matrices, "matrices")
+    s = c.flat(src, "src", _esize(src_dt), plan.psi_pad)
+    d = c.flat(dst, "dst", _esize(dst_dt), plan.psi_pad)
+    ws, ws_bytes = c.workspace(workspace, lambda: zero_orthogonalize_workspace_bytes(plan, matrices))
+    q = None if poly is None else _kind(poly, NewtonSchulz, "poly")._ref
+    c.issue(load().zero_orthogonalize, plan.handle, matrices.c, matrices.n, q, s, src_dt, d, dst_dt, ws, ws_bytes)
+
+
+def zero_muon_apply(plan: Plan, rank: int, hyper: MuonHyper, direction, direction_dt: int, direction_is_full: bool,
+                    master, param_dst, param_dt: int, dst_is_full: bool, stream=None) -> None:
+    """master = (1 - lr weight_decay) master - lr direction, and the 16-bit
+    parameters."""
+    c = _Call(stream)
+    S = plan.shard_total
+    _kind(hyper, MuonHyper, "hyper")
+    for name, d in (("direction", direction_dt), ("parameter", param_dt)):
+        if d not in (ZERO_F16, ZERO_BF16):
+            raise ValueError(f"{name} dtype {d} is not 16-bit")
+    o = c.flat(direction, "direction", 2, plan.psi_pad if direction_is_full else S)
+    w = c.flat(master, "master", 4, S)
+    p = c.flat(param_dst, "param_dst", 2, plan.psi_pad if dst_is_full else S)
+    c.issue(load().zero_muon_apply, plan.handle, rank, hyper._ref, o, direction_dt, 1 if direction_is_full else 0, w, p,
+            param_dt, 1 if dst_is_full else 0)

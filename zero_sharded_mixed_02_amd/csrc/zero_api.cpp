@@ -159,8 +159,9 @@ void auto_window(int mode, int gdt, int pdt, int ndc, int n_ranks, int64_t elems
   const double hz = zk::wall_clock_hz();
   const double peak = zk::hbm_peak_bps();
   if (!(hz > 0) || !(peak > 0)) return;
-  const double read = 2.0 * n_ranks + (mode == zk::kFused ? 12.0 : (a.flags & zk::kFlagInitFromOut) ? 4.0 : 0.0);
-  const double written = mode == zk::kFused ? 14.0 : 4.0;
+  const bool momentum = mode == zk::kMomentum;   // one state array: 4 bytes read, 4 + 2 written
+  const double read = 2.0 * n_ranks + (mode == zk::kFused ? 12.0 : momentum || (a.flags & zk::kFlagInitFromOut) ? 4.0 : 0.0);
+  const double written = mode == zk::kFused ? 14.0 : momentum ? 6.0 : 4.0;
   const double gen_bytes = (double)resident * zk::kStepThreads * zk::kStepVec * (read + written);
   const bool fused = mode == zk::kFused;
   const double share = ndc == 16 ? (fused ? kAutoPeriodShare16 : kAutoPeriodShare)
@@ -184,7 +185,7 @@ void pick_window(int mode, int gdt, int pdt, int ndc, int n_ranks, int64_t elems
                  void* stream, zk::StepArgs& a) {
   a.win_period = 0;
   a.win_open = 0;
-  if (!vec || mode == zk::kFromReduced) return;
+  if (!vec || mode == zk::kFromReduced || mode == zk::kMomentumReduced || mode == zk::kApply) return;
   const uint64_t w = window_setting(stream);
   if (w != kWindowAuto) {
     a.win_period = (uint32_t)(w >> 32);
@@ -335,6 +336,35 @@ zero_status run_copies(std::vector<zk::CopyEnt>& ents, void* dst, int es, void* 
     const int err = zk::launch_copy(a, es, (int)blocks, stream);
     if (err != 0) return hip_fail(err);
   }
+  return ok();
+}
+
+// What the two halves of the Muon step check alike.
+zero_status check_muon(zero_plan_t p, int32_t rank, const zero_muon_hyper* hp) {
+  if (check_plan(p)) return ZERO_EINVAL;
+  if (rank < 0 || rank >= p->n_d) return fail(ZERO_EINVAL, "rank %d outside [0, %d)", rank, p->n_d);
+  if (!hp) return fail(ZERO_EINVAL, "hyper-parameters are NULL");
+  if (hp->nesterov != 0 && hp->nesterov != 1) return fail(ZERO_EINVAL, "nesterov must be 0 or 1 (got %d)", hp->nesterov);
+  const double all[] = {hp->lr, hp->momentum, hp->weight_decay, hp->grad_scale, 1.0 - hp->lr * hp->weight_decay};
+  for (double v : all)
+    if (!std::isfinite((float)v)) return fail(ZERO_EINVAL, "hyper-parameter %g is not finite in fp32", v);
+  return ok();
+}
+
+// An fp32 state array and a 16-bit destination, written, apart from each other and from what is read.
+zero_status check_muon_state(float* state, const char* state_name, void* dst, const char* dst_name, int64_t S,
+                             int64_t dst_elems, const std::vector<Range>& reads, bool& vec_ok) {
+  if (!state && S > 0) return fail(ZERO_EINVAL, "%s is NULL", state_name);
+  if (!aligned(state, 4)) return fail(ZERO_EINVAL, "%s is not 4-byte aligned", state_name);
+  if (!aligned(state, 16)) vec_ok = false;
+  if (!dst && dst_elems > 0) return fail(ZERO_EINVAL, "%s is NULL", dst_name);
+  if (!aligned(dst, 2)) return fail(ZERO_EINVAL, "%s is not 2-byte aligned", dst_name);
+  if (!aligned(dst, 8)) vec_ok = false;   // 4 elements (8 bytes) per store
+  const Range w[2] = {range_of(state, S, 4, state_name), range_of(dst, dst_elems, 2, dst_name)};
+  if (overlap(w[0], w[1])) return fail(ZERO_EINVAL, "%s overlaps %s", state_name, dst_name);
+  for (const Range& x : w)
+    for (const Range& r : reads)
+      if (overlap(x, r)) return fail(ZERO_EINVAL, "%s overlaps %s", x.what, r.what);
   return ok();
 }
 
@@ -728,6 +758,83 @@ zero_status zero_adam_step(zero_plan_t p, int32_t rank, const zero_adam_hyper* h
     return fail(ZERO_ENOMEM, "host allocation failed");
   } catch (...) {
     return fail(ZERO_EINVAL, "unexpected failure in zero_adam_step");
+  }
+}
+
+zero_status zero_muon_momentum(zero_plan_t p, int32_t rank, const zero_muon_hyper* hp, const zero_grad_src* slices,
+                               const float* reduced, float* momentum, void* update, zero_dtype update_dt,
+                               int32_t update_is_full, void* stream) {
+  try {
+    zk::StepArgs a;
+    memset(&a, 0, sizeof a);
+    if (zero_status st = check_muon(p, rank, hp)) return st;
+    if (!is16(update_dt)) return fail(ZERO_EUNSUPPORTED, "update dtype %d is not 16-bit", (int)update_dt);
+    const int64_t S = p->shard_total, out_elems = update_is_full ? p->psi_pad : S;
+    std::vector<Range> reads;
+    bool vec_ok = true;   // base alignment the vector kernel needs
+    if (slices && reduced) return fail(ZERO_EINVAL, "both slices and reduced are given");
+    if (slices) {
+      if (p->n_d > zk::kMaxRanks)
+        return fail(ZERO_EUNSUPPORTED, "fused step reads at most %d ranks; use zero_shard_reduce and pass reduced",
+                    zk::kMaxRanks);
+      if (zero_status st = check_src(*p, slices, reads, vec_ok)) return st;
+    } else {
+      if (!reduced && S > 0) return fail(ZERO_EINVAL, "both slices and reduced are NULL");
+      if (!aligned(reduced, 4)) return fail(ZERO_EINVAL, "reduced is not 4-byte aligned");
+      if (!aligned(reduced, 16)) vec_ok = false;
+      reads.push_back(range_of(reduced, S, 4, "reduced"));
+    }
+    if (zero_status st = check_muon_state(momentum, "momentum", update, "update", S, out_elems, reads, vec_ok)) return st;
+    const std::vector<Piece> ps = owner_pieces(*p, rank, update_is_full != 0);
+    a.c[0] = (float)hp->momentum;
+    a.c[8] = (float)hp->grad_scale;   // of slices; reduced holds the scale already
+    a.flags = hp->nesterov ? zk::kFlagNesterov : 0;
+    a.m = momentum;
+    a.dst = update;
+    if (slices) {
+      const bool uses_full = slices->is_full && std::any_of(slices->is_full, slices->is_full + slices->n, [](uint8_t f) { return f != 0; });
+      set_ranks(a, *slices, 0, p->n_d);
+      return run_step_all(a, ps, zk::kMomentum, slices->dtype, update_dt, vec_ok, uses_full, stream);
+    }
+    a.reduced = reduced;
+    return run_step_all(a, ps, zk::kMomentumReduced, ZERO_BF16, update_dt, vec_ok, false, stream);
+  } catch (const std::bad_alloc&) {
+    return fail(ZERO_ENOMEM, "host allocation failed");
+  } catch (...) {
+    return fail(ZERO_EINVAL, "unexpected failure in zero_muon_momentum");
+  }
+}
+
+zero_status zero_muon_apply(zero_plan_t p, int32_t rank, const zero_muon_hyper* hp, const void* direction,
+                            zero_dtype direction_dt, int32_t direction_is_full, float* master, void* param_dst,
+                            zero_dtype param_dt, int32_t dst_is_full, void* stream) {
+  try {
+    zk::StepArgs a;
+    memset(&a, 0, sizeof a);
+    if (zero_status st = check_muon(p, rank, hp)) return st;
+    if (!is16(direction_dt)) return fail(ZERO_EUNSUPPORTED, "direction dtype %d is not 16-bit", (int)direction_dt);
+    if (!is16(param_dt)) return fail(ZERO_EUNSUPPORTED, "parameter dtype %d is not 16-bit", (int)param_dt);
+    const int64_t S = p->shard_total, in_elems = direction_is_full ? p->psi_pad : S;
+    bool vec_ok = true;
+    if (!direction && in_elems > 0) return fail(ZERO_EINVAL, "direction is NULL");
+    if (!aligned(direction, 2)) return fail(ZERO_EINVAL, "direction is not 2-byte aligned");
+    if (!aligned(direction, 8)) vec_ok = false;
+    const std::vector<Range> reads = {range_of(direction, in_elems, 2, "direction")};
+    if (zero_status st = check_muon_state(master, "master", param_dst, "param_dst", S, dst_is_full ? p->psi_pad : S, reads, vec_ok))
+      return st;
+    const std::vector<Piece> ps = owner_pieces(*p, rank, dst_is_full != 0);
+    a.c[0] = (float)(1.0 - hp->lr * hp->weight_decay);
+    a.c[6] = (float)hp->lr;
+    a.master = master;
+    a.dst = param_dst;
+    a.grad[0] = direction;
+    a.full_mask[0] = direction_is_full ? 1u : 0u;
+    a.n_ranks = 1;
+    return run_step_all(a, ps, zk::kApply, direction_dt, param_dt, vec_ok, direction_is_full != 0, stream);
+  } catch (const std::bad_alloc&) {
+    return fail(ZERO_ENOMEM, "host allocation failed");
+  } catch (...) {
+    return fail(ZERO_EINVAL, "unexpected failure in zero_muon_apply");
   }
 }
 

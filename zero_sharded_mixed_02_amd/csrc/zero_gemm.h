@@ -1,0 +1,336 @@
+// zero_gemm.h -- the matrix-product core of the hidden-matrix operators:
+// device templates, included by the .hip files that instantiate them.
+//
+// C[m, n] = sum_k A(m, k) B(n, k), A and B of 16-bit elements in one of two
+// forms, sums in fp32 on the matrix units:
+//   form K   the operand's memory rows run along k  (x and W of x W^T)
+//   form M   the operand's memory rows run along m (or n), one row per k
+//            (W of dz W; both operands of dz^T x)
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include "zero.h"
+
+#pragma clang fp contract(off)
+
+namespace zk {
+namespace gemm {
+
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef short s16x4 __attribute__((ext_vector_type(4)));
+typedef short s16x8 __attribute__((ext_vector_type(8)));
+typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
+typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+
+#define ZK_LDS __attribute__((address_space(3)))
+
+enum Form : int { kFormK = 0, kFormM = 1 };
+
+constexpr int kBK = 64;          // depth of a stage, elements
+
+template <typename T>
+__device__ __forceinline__ f32x4 mfma(s16x8 a, s16x8 b, f32x4 c);
+template <>
+__device__ __forceinline__ f32x4 mfma<_Float16>(s16x8 a, s16x8 b, f32x4 c) {
+  return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(f16x8, a), __builtin_bit_cast(f16x8, b), c, 0, 0, 0);
+}
+template <>
+__device__ __forceinline__ f32x4 mfma<__bf16>(s16x8 a, s16x8 b, f32x4 c) {
+  return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, a), __builtin_bit_cast(bf16x8, b), c, 0, 0, 0);
+}
+
+// XOR of a row's 16-byte units in LDS.  Form K: rows of 128 bytes; a fragment
+// reads 16 rows at one unit, either consecutive rows (bits 0-3 run) or the
+// permuted ones of perm8 (bits 0, 1, 3, 4 run); with 64 banks both cover each
+// bank once.
+__device__ __forceinline__ int swz_k(int row) {
+  return ((row >> 1) & 1) | ((((row >> 2) ^ (row >> 4)) & 1) << 1) | (((row >> 3) & 1) << 2);
+}
+// Form M: rows of W elements, one per k; a transposing read takes 32 bytes of
+// each of four rows k .. k + 3 per 16 lanes, and of four rows 8 further on in the
+// next 16.
+template <int W>
+__device__ __forceinline__ int swz_m(int k) {
+  if constexpr (W >= 128) return ((k & 3) | (((k >> 3) & 1) << 2)) << 1;
+  else return (((k >> 1) & 1) | (((k >> 3) & 1) << 1)) << 1;
+}
+
+// One operand's panel of W rows (of the product) and its staging.
+template <int FORM, int W, int NT>
+struct Panel {
+  static constexpr int kBytes = W * kBK * 2;
+  static constexpr int kLoads = W * 8 / NT;       // 16-byte units a thread
+  static_assert(W * 8 % NT == 0, "the panel is a whole number of units a thread");
+
+  const char* base;       // first element of the panel at the current k
+  int64_t step;           // bytes from one stage to the next
+  int64_t span;           // bytes of the panel from base on (form K), or of a row (form M)
+  uint32_t ld;            // bytes between memory rows
+  int rows;               // rows of the product left in this panel (may exceed W)
+  uint32_t voff[kLoads];
+
+  __device__ __forceinline__ void init(const void* p, int64_t lde, int row0, int rows_total, int k0, int k_end, int tid) {
+    ld = (uint32_t)lde * 2u;
+    rows = rows_total - row0;
+    if constexpr (FORM == kFormK) {
+      base = (const char*)p + (int64_t)row0 * lde * 2 + (int64_t)k0 * 2;
+      step = kBK * 2;
+      const int last = (rows < W ? rows : W) - 1;
+      span = (int64_t)last * lde * 2 + (int64_t)(k_end - k0) * 2;
+#pragma unroll
+      for (int i = 0; i < kLoads; ++i) {
+        const int g = i * NT + tid, row = g >> 3, unit = (g & 7) ^ swz_k(row);
+        voff[i] = (uint32_t)row * ld + unit * 16u;
+      }
+    } else {
+      base = (const char*)p + (int64_t)k0 * lde * 2 + (int64_t)row0 * 2;
+      step = (int64_t)kBK * lde * 2;
+      span = (int64_t)rows * 2;
+      constexpr int U = W / 8;
+#pragma unroll
+      for (int i = 0; i < kLoads; ++i) {
+        const int g = i * NT + tid, k = g / U, unit = (g % U) ^ swz_m<W>(k);
+        voff[i] = (uint32_t)k * ld + unit * 16u;
+      }
+    }
+  }
+
+  // Bytes of this stage that may be read: what lies behind reads as zero.
+  __device__ __forceinline__ uint32_t records(int k_left) const {
+    if constexpr (FORM == kFormK) return (uint32_t)span;
+    const int kr = k_left < kBK ? k_left : kBK;
+    return (uint32_t)(kr - 1) * ld + (uint32_t)span;
+  }
+
+  __device__ __forceinline__ void advance() {
+    base += step;
+    if constexpr (FORM == kFormK) span -= step;
+  }
+
+  // Starts the loads of one stage straight into LDS (rows 16-byte aligned and
+  // a whole number of 16-byte units long).
+  __device__ __forceinline__ void load_direct(ZK_LDS char* lds, int wave, int tid, int k_left) {
+    const __amdgpu_buffer_rsrc_t rs = __builtin_amdgcn_make_buffer_rsrc((void*)base, 0, records(k_left), 0x00020000);
+    const bool tail = FORM == kFormK && k_left < kBK;
+#pragma unroll
+    for (int i = 0; i < kLoads; ++i) {
+      uint32_t off = voff[i];
+      if (tail) {   // units behind the last k would hold the next row's
+        const int g = i * NT + tid, unit = (g & 7) ^ swz_k(g >> 3);
+        if (unit * 8 >= k_left) off = 0x7ffffff0u;
+      }
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (ZK_LDS void*)(lds + (i * NT + wave * 64) * 16), 16, (int)off, 0, 0, 0);
+    }
+  }
+
+  // Any alignment: through registers.
+  __device__ __forceinline__ void load_regs(u32x4 (&r)[kLoads], int tid, int k_left) const {
+#pragma unroll
+    for (int i = 0; i < kLoads; ++i) {
+      const int g = i * NT + tid;
+      int have;             // elements of the unit that exist
+      bool row_ok;
+      if constexpr (FORM == kFormK) {
+        const int row = g >> 3, unit = (g & 7) ^ swz_k(row);
+        row_ok = row < rows;
+        have = k_left - unit * 8;
+      } else {
+        constexpr int U = W / 8;
+        const int k = g / U, unit = (g % U) ^ swz_m<W>(k);
+        row_ok = k < k_left;
+        have = rows - unit * 8;
+      }
+      u32x4 v = {0u, 0u, 0u, 0u};
+      const char* p = base + voff[i];
+      if (row_ok && have >= 8) {
+        typedef u32x4 __attribute__((aligned(2))) u32x4_2;
+        v = *(const __attribute__((address_space(1))) u32x4_2*)p;
+      } else if (row_ok && have > 0) {
+        uint32_t e[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) e[j] = j < have ? ((const __attribute__((address_space(1))) uint16_t*)p)[j] : 0u;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) v[j] = e[2 * j] | (e[2 * j + 1] << 16);
+      }
+      r[i] = v;
+    }
+  }
+  __device__ __forceinline__ void store_regs(ZK_LDS char* lds, int tid, const u32x4 (&r)[kLoads]) const {
+#pragma unroll
+    for (int i = 0; i < kLoads; ++i) *(ZK_LDS u32x4*)(lds + (i * NT + tid) * 16) = r[i];
+  }
+};
+
+// Which product row a fragment's lane holds.  Natural: tile t's rows are 16 t + c.
+// Permuted (form K of the n side): pairs of tiles are interleaved in fours, so
+// that a lane's two results of four make eight consecutive n.
+__device__ __forceinline__ int perm8(int t, int c) { return (t >> 1) * 32 + (c >> 2) * 8 + (t & 1) * 4 + (c & 3); }
+
+// Reads fragments of 16 rows by 32 k out of a staged panel.
+template <int FORM, int W, bool PERM>
+struct Frag {
+  // Form K: byte address of (row, unit 0) and the row's XOR; form M: of the
+  // lane's piece at k = 0.
+  __device__ static __forceinline__ s16x8 read(const ZK_LDS char* lds, int row0, int t, int s, int lane) {
+    const int c = lane & 15, q = lane >> 4;
+    if constexpr (FORM == kFormK) {
+      const int row = row0 + (PERM ? perm8(t, c) : t * 16 + c);
+      const int unit = (s * 4 + q) ^ swz_k(row);
+      return *(const ZK_LDS s16x8*)(lds + row * 128 + unit * 16);
+    } else {
+      const int p = c & 3, kr = c >> 2;
+      const int mb = (row0 + (PERM ? (t >> 1) * 32 + p * 8 + (t & 1) * 4 : t * 16 + p * 4)) * 2;   // byte within the row
+      const int k = s * 32 + q * 8 + kr;
+      const ZK_LDS char* a0 = lds + k * (W * 2) + (mb ^ (swz_m<W>(k) * 16));
+      const int k1 = k + 4;
+      const ZK_LDS char* a1 = lds + k1 * (W * 2) + (mb ^ (swz_m<W>(k1) * 16));
+      const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((ZK_LDS s16x4*)a0);
+      const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((ZK_LDS s16x4*)a1);
+      return __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
+    }
+  }
+};
+
+// Order of the workgroups.  They go to the eight dies in turn; each die gets a
+// run of consecutive pieces of work, so that its L2 holds the panels that its
+// workgroups share.
+__device__ __forceinline__ int die_order(int b, int n_blocks) {
+  const int per = n_blocks >> 3, more = n_blocks & 7, die = b & 7;
+  return die * per + (die < more ? die : more) + (b >> 3);
+}
+
+// Tile t of tm x tn: down eight rows of tiles at a time.
+__device__ __forceinline__ void place(int t, int tm, int tn, int& im, int& in) {
+  constexpr int G = 8;
+  const int group = G * tn, g = t / group, first = g * G;
+  const int gm = tm - first < G ? tm - first : G, r = t - g * group;
+  im = first + r % gm;
+  in = r / gm;
+}
+
+// Tile t of the tm (tm + 1) / 2 on and above the diagonal, column by column.
+__device__ __forceinline__ void place_upper(int t, int& im, int& in) {
+  int j = (int)((__builtin_sqrtf(8.0f * (float)t + 1.0f) - 1.0f) * 0.5f);
+  while (j > 0 && j * (j + 1) / 2 > t) --j;
+  while ((j + 1) * (j + 2) / 2 <= t) ++j;
+  im = t - j * (j + 1) / 2;
+  in = j;
+}
+
+template <typename T, int AF, int BF, int BM, int BN, int WM, int WN, bool DIRECT>
+struct Core {
+  static constexpr int NT = 64 * WM * WN;
+  static constexpr int TM = BM / WM / 16, TN = BN / WN / 16;
+  static constexpr bool kPerm = BF == kFormK && TN % 2 == 0;
+  static constexpr int kVec = kPerm ? 8 : 4;       // consecutive n a lane holds
+  typedef Panel<AF, BM, NT> PA;
+  typedef Panel<BF, BN, NT> PB;
+  static constexpr int kStage = PA::kBytes + PB::kBytes;
+
+  f32x4 acc[TM][TN];
+
+  __device__ __forceinline__ void stage_compute(const ZK_LDS char* lds, int wm, int wn, int lane) {
+    const ZK_LDS char* la = lds;
+    const ZK_LDS char* lb = lds + PA::kBytes;
+#pragma unroll
+    for (int s = 0; s < kBK / 32; ++s) {
+      s16x8 fa[TM], fb[TN];
+#pragma unroll
+      for (int j = 0; j < TN; ++j) fb[j] = Frag<BF, BN, kPerm>::read(lb, wn * TN * 16, j, s, lane);
+#pragma unroll
+      for (int i = 0; i < TM; ++i) fa[i] = Frag<AF, BM, false>::read(la, wm * TM * 16, i, s, lane);
+#pragma unroll
+      for (int i = 0; i < TM; ++i)
+#pragma unroll
+        for (int j = 0; j < TN; ++j) acc[i][j] = mfma<T>(fb[j], fa[i], acc[i][j]);
+    }
+  }
+
+  // Sums k0 .. k_end of the tile whose first rows are m0 and n0.
+  __device__ __forceinline__ void run(ZK_LDS char* lds, const void* a, int64_t lda, int m, const void* b, int64_t ldb, int n,
+                                      int m0, int n0, int k0, int k_end) {
+    const int tid = threadIdx.x, lane = tid & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int wm = wave / WN, wn = wave % WN;
+    PA pa;
+    PB pb;
+    pa.init(a, lda, m0, m, k0, k_end, tid);
+    pb.init(b, ldb, n0, n, k0, k_end, tid);
+#pragma unroll
+    for (int i = 0; i < TM; ++i)
+#pragma unroll
+      for (int j = 0; j < TN; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
+    int left = k_end - k0;
+    if (left <= 0) return;
+    if constexpr (DIRECT) {
+      pa.load_direct(lds, wave, tid, left);
+      pb.load_direct(lds + PA::kBytes, wave, tid, left);
+      int cur = 0;
+      for (; left > 0; left -= kBK) {
+        __syncthreads();      // this stage has arrived, and the other one is no longer read
+        if (left > kBK) {
+          pa.advance();
+          pb.advance();
+          ZK_LDS char* next = lds + (cur ^ 1) * kStage;
+          pa.load_direct(next, wave, tid, left - kBK);
+          pb.load_direct(next + PA::kBytes, wave, tid, left - kBK);
+        }
+        stage_compute(lds + cur * kStage, wm, wn, lane);
+        cur ^= 1;
+      }
+    } else {
+      u32x4 ra[PA::kLoads], rb[PB::kLoads];
+      pa.load_regs(ra, tid, left);
+      pb.load_regs(rb, tid, left);
+      int cur = 0;
+      for (; left > 0; left -= kBK) {
+        ZK_LDS char* here = lds + cur * kStage;
+        pa.store_regs(here, tid, ra);
+        pb.store_regs(here + PA::kBytes, tid, rb);
+        __syncthreads();
+        if (left > kBK) {
+          pa.advance();
+          pb.advance();
+          pa.load_regs(ra, tid, left - kBK);
+          pb.load_regs(rb, tid, left - kBK);
+        }
+        stage_compute(here, wm, wn, lane);
+        cur ^= 1;
+      }
+    }
+  }
+
+  // f(row, first n, values): kVec consecutive n of one row at a time.
+  template <typename F>
+  __device__ __forceinline__ void each(int m0, int n0, F f) const {
+    const int lane = threadIdx.x & 63, c = lane & 15, q = lane >> 4;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int wm = wave / WN, wn = wave % WN;
+#pragma unroll
+    for (int i = 0; i < TM; ++i) {
+      const int row = m0 + (wm * TM + i) * 16 + c;
+      if constexpr (kPerm) {
+#pragma unroll
+        for (int j = 0; j < TN; j += 2) {
+          const int col = n0 + wn * TN * 16 + j * 16 + q * 8;
+          const float v[8] = {acc[i][j][0], acc[i][j][1], acc[i][j][2], acc[i][j][3],
+                              acc[i][j + 1][0], acc[i][j + 1][1], acc[i][j + 1][2], acc[i][j + 1][3]};
+          f(row, col, v);
+        }
+      } else {
+#pragma unroll
+        for (int j = 0; j < TN; ++j) {
+          const int col = n0 + (wn * TN + j) * 16 + q * 4;
+          const float v[4] = {acc[i][j][0], acc[i][j][1], acc[i][j][2], acc[i][j][3]};
+          f(row, col, v);
+        }
+      }
+    }
+  }
+};
+
+}  // namespace gemm
+}  // namespace zk

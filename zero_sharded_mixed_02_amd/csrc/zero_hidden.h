@@ -1,0 +1,130 @@
+// zero_hidden.h -- structures shared by the host entries (zero_hidden_api.cpp)
+// and the gfx950 kernels (zero_linear.hip, zero_muon.hip) of the operators on a
+// model's hidden matrices.
+#pragma once
+
+#include <stdint.h>
+
+#include "zero.h"
+
+namespace zk {
+namespace hidden {
+
+constexpr int64_t kLaunchItems = int64_t(1) << 32;   // work items of a launch, exclusive
+inline int64_t most_blocks(int threads) { return (kLaunchItems - 1) / threads; }
+
+// Tiles of a product: rows x columns of the result per workgroup.
+enum Tile : int { kTile256 = 0, kTile128 = 1, kTile64 = 2, kTiles = 3 };
+constexpr int kTileSize[kTiles] = {256, 128, 64};
+constexpr int kTileThreads[kTiles] = {512, 256, 256};
+
+// What one product reads and how its tiles are laid out.
+struct Product {
+  const void* a;
+  const void* b;
+  int64_t lda, ldb;       // elements between memory rows
+  int32_t m, n, k;
+  int32_t tm, tn;         // tiles
+  int32_t splits;         // pieces of k
+  int32_t k_piece;        // elements of a piece, a multiple of the stage depth
+  int32_t tiles;          // tm * tn
+  float* part;            // fp32[splits][m][n_pad]: partial sums, or NULL
+  int32_t n_pad;          // n rounded up to 4
+  int32_t pad_;
+};
+
+// zero_linear (EPI 0) and zero_linear_input_grad (EPI 1).
+struct LinearArgs {
+  Product p;
+  void* out;
+  void* pre_out;          // EPI 0: the sum before act, or NULL
+  const void* pre_in;     // EPI 1: where act' is taken, or NULL
+  const void* add;        // residual or addend, or NULL
+  const void* bias;       // EPI 0, or NULL
+  int64_t ldo, ldpre, ldadd;
+  int32_t act;
+  int32_t pad_;
+};
+
+// zero_linear_weight_grad: m rows of the weight from row0 on, n columns.
+struct WeightGradArgs {
+  Product p;
+  void* dst;              // the element lo of the weight
+  int64_t lo, hi;         // elements of the weight that are written
+  int32_t row0;
+  int32_t dst_dt;
+  int32_t accumulate;
+  float scale;
+  // The bias: columns [b_lo, b_hi) of dz are summed.
+  void* bias_dst;         // the element b_lo of the bias
+  float* bias_part;       // fp32[chunks][columns]
+  int32_t b_lo, b_hi;
+  int32_t chunk_rows, chunks, col_blocks, bias_blocks;
+  int32_t join_blocks, pad_;
+};
+
+struct ActGradArgs {
+  const void* dy;
+  const void* pre;
+  void* dz;
+  int64_t n;
+  int32_t act;
+  int32_t pad_;
+};
+
+// zero_orthogonalize: one launch over `batch` matrices of one shape, which lie
+// `z*` elements apart in the workspace.
+constexpr int kMaxBatch = 128;
+enum OrthoEpi : int { kGram = 0, kPoly = 1, kNext = 2 };
+
+struct OrthoArgs {
+  Product p;              // of one matrix; part: fp32[batch][splits][m][n_pad]
+  int64_t za, zb, zout, zadd;
+  const float* factor;    // fp32[batch]: what the stored X is to be multiplied by
+  void* out;              // 16-bit result in the workspace, rows of ldo
+  float* out32;           // kNext: X in fp32, or NULL after the last step
+  const void* add;        // kPoly: A - shift I; kNext: X
+  int64_t ldo, ldadd;
+  int32_t batch, epi;
+  int32_t upper;          // the result is symmetric: tiles on and above the diagonal only
+  int32_t first;          // X as loaded: the factor applies, and add is 16-bit
+  int32_t last, dst_dt;   // the result goes to dst
+  float c0, c1, shift;    // kGram: factor^2 sum - shift I; kPoly: c0 add + c1 sum; kNext: factor (c0 add + sum)
+  int32_t rows, cols;     // of dst
+  void* dst;              // flat buffer
+  float scale[kMaxBatch];
+  int64_t dst_off[kMaxBatch];
+};
+
+// Norms and the first X of a batch.
+struct OrthoLoadArgs {
+  const void* src;
+  void* x;                // fp16, rows of ld, padded with zeros
+  double* sums;           // fp64[batch][kNormBlocks]
+  float* factor;
+  double eps;
+  int64_t numel, zx;
+  int32_t rows, cols, ld, rows_pad, batch, norm_blocks;
+  int64_t src_off[kMaxBatch];
+};
+constexpr int kNormBlocks = 64;      // most pieces of a matrix's norm
+constexpr int kLoadThreads = 256;
+
+constexpr int kBiasCols = 256;     // columns of a bias workgroup
+constexpr int kJoinThreads = 256;
+constexpr int kActThreads = 256;
+constexpr int kActVec = 8;
+
+// Launchers.  Return a hipError_t as int.
+int launch_linear(const LinearArgs& a, int epi, int dt, int tile, bool direct, void* stream);
+int launch_linear_join(const LinearArgs& a, int epi, int dt, int64_t blocks, void* stream);
+int launch_weight_grad(const WeightGradArgs& a, int dt, int tile, bool direct, int64_t blocks, void* stream);
+int launch_weight_grad_join(const WeightGradArgs& a, int64_t blocks, void* stream);
+int launch_ortho_norm(const OrthoLoadArgs& a, int dt, void* stream);
+int launch_ortho_load(const OrthoLoadArgs& a, int dt, int64_t blocks, void* stream);
+int launch_ortho(const OrthoArgs& a, int form_a, int form_b, int tile, int64_t blocks, void* stream);
+int launch_ortho_join(const OrthoArgs& a, int64_t blocks, void* stream);
+int launch_act_grad(const ActGradArgs& a, int dt, int64_t blocks, void* stream);
+
+}  // namespace hidden
+}  // namespace zk

@@ -1,0 +1,698 @@
+// zero_hidden_api.cpp -- host side of the operators on the hidden matrices:
+// argument checks, launch shapes and the extern "C" entry points declared in
+// include/zero.h.  As in zero_api.cpp, nothing allocates device memory and every
+// table travels in the kernel arguments.
+#include <stdint.h>
+#include <string.h>
+
+#include <algorithm>
+#include <cmath>
+#include <vector>
+
+#include "zero.h"
+#include "zero_hidden.h"
+#include "zero_host.h"
+
+using namespace zk::host;
+using namespace zk::hidden;
+
+namespace {
+
+constexpr int64_t kMaxWide = int64_t(1) << 21;    // of a row that is staged: 256 rows stay within 2^31 bytes
+constexpr int64_t kMaxLong = int64_t(1) << 30;
+constexpr int64_t kMaxSide = int64_t(1) << 20;    // of a matrix to orthogonalise
+constexpr int kStage = 64;                        // depth of a stage of the products
+
+int64_t round_up(int64_t n, int64_t to) { return ceil_div(n, to) * to; }
+
+// ---------------------------------------------------------------------------
+// Launch shapes
+// ---------------------------------------------------------------------------
+
+// Time of a product's launch in us, from what a stage takes on one CU: `alone`
+// with one workgroup there, `full` for each of `slots` that share it.
+struct TileCost { double alone, full; int slots; };
+constexpr TileCost kCost[kTiles] = {{1.85, 1.85, 1}, {0.75, 0.52, 2}, {0.45, 0.21, 4}};
+constexpr int kCus = 256;
+constexpr double kTileStart = 2.5;       // us: the first loads and the epilogue
+constexpr double kJoinStart = 4.0;       // us: a launch that joins pieces of k
+constexpr double kPartRate = 3.5e6;      // bytes a us, written and read again
+
+double cost_of(int tile, int64_t tiles, int64_t stages) {
+  const TileCost& c = kCost[tile];
+  const int64_t per_cu = ceil_div(tiles, kCus), rounds = per_cu / c.slots, rest = per_cu % c.slots;
+  const double last = rest ? std::max(c.alone, rest * c.full) : 0.0;
+  return (double)stages * ((double)rounds * c.slots * c.full + last) + kTileStart * (double)(rounds + (rest ? 1 : 0));
+}
+
+int64_t tiles_of(int tile, int64_t m, int64_t n) { return ceil_div(m, kTileSize[tile]) * ceil_div(n, kTileSize[tile]); }
+
+struct Pick { int tile, splits; double us; };
+
+// Tile and pieces of k of `batch` products.  splits > 0 is kept.
+Pick pick(int64_t m, int64_t n, int64_t k, int64_t batch, int splits, bool upper = false) {
+  const int64_t stages = std::max<int64_t>(1, ceil_div(k, kStage));
+  Pick best = {kTile64, 1, 1e300};
+  for (int tile = 0; tile < kTiles; ++tile) {
+    int64_t tiles = batch * tiles_of(tile, m, n);
+    const int64_t side = ceil_div(m, kTileSize[tile]);
+    for (int64_t s = splits ? splits : 1; s <= (splits ? splits : 64); s *= 2) {
+      if (!splits && s > 1 && stages / s < 4) break;    // a piece has four stages or more
+      const int64_t per = ceil_div(stages, s), now = ceil_div(stages, per);
+      const int64_t t = upper && now == 1 ? batch * side * (side + 1) / 2 : tiles;
+      double us = cost_of(tile, t * now, per);
+      if (now > 1) us += kJoinStart + (double)(batch * m) * (double)n * 4.0 * (double)(now + 1) / kPartRate;
+      if (us < best.us) best = {tile, (int)now, us};
+    }
+  }
+  return best;
+}
+
+void lay_out(Product& p, int64_t m, int64_t n, int64_t k, const Pick& c) {
+  const int64_t stages = std::max<int64_t>(1, ceil_div(k, kStage)), per = ceil_div(stages, c.splits);
+  p.m = (int32_t)m;
+  p.n = (int32_t)n;
+  p.k = (int32_t)k;
+  p.tm = (int32_t)ceil_div(m, kTileSize[c.tile]);
+  p.tn = (int32_t)ceil_div(n, kTileSize[c.tile]);
+  p.tiles = (int32_t)std::min<int64_t>(INT32_MAX, (int64_t)p.tm * p.tn);
+  p.k_piece = (int32_t)(per * kStage);
+  p.splits = (int32_t)ceil_div(stages, per);
+  p.n_pad = (int32_t)round_up(n, 4);
+}
+
+int64_t part_bytes(int64_t m, int64_t n, int splits) {
+  return splits > 1 ? (int64_t)splits * m * round_up(n, 4) * 4 : 0;
+}
+
+zero_status check_grid(int64_t blocks, int threads) {
+  if (blocks > most_blocks(threads))
+    return fail(ZERO_EUNSUPPORTED, "the call needs %lld workgroups of %d, one launch takes %lld", (long long)blocks, threads,
+                (long long)most_blocks(threads));
+  return ok();
+}
+
+// An operand's rows can be loaded 16 bytes at a time straight into LDS.
+bool direct_ok(const void* p, int64_t ld, int64_t width) { return aligned(p, 16) && ld % 8 == 0 && width % 8 == 0; }
+
+// ---------------------------------------------------------------------------
+// Arguments
+// ---------------------------------------------------------------------------
+
+// The weight: a tensor of the plan seen as rows of in_features elements.
+zero_status weight_of(zero_plan_t p, int32_t tensor, int64_t in_features, int64_t& out_features) {
+  if (check_plan(p)) return ZERO_EINVAL;
+  if (tensor < 0 || tensor >= (int32_t)p->t_numel.size()) return fail(ZERO_EINVAL, "weight tensor %d out of range", tensor);
+  if (in_features < 1) return fail(ZERO_EINVAL, "in_features must be >= 1 (got %lld)", (long long)in_features);
+  if (p->t_numel[tensor] % in_features)
+    return fail(ZERO_EINVAL, "tensor %d holds %lld elements, no multiple of in_features = %lld", tensor,
+                (long long)p->t_numel[tensor], (long long)in_features);
+  out_features = p->t_numel[tensor] / in_features;
+  if (in_features > kMaxWide)
+    return fail(ZERO_EUNSUPPORTED, "in_features %lld exceeds %lld", (long long)in_features, (long long)kMaxWide);
+  if (out_features > kMaxLong)
+    return fail(ZERO_EUNSUPPORTED, "%lld output features exceed %lld", (long long)out_features, (long long)kMaxLong);
+  return ok();
+}
+
+zero_status bias_of(zero_plan_t p, int32_t bias, int32_t weight, int64_t out_features) {
+  if (bias < 0) return ok();
+  if (bias >= (int32_t)p->t_numel.size()) return fail(ZERO_EINVAL, "bias tensor %d out of range", bias);
+  if (p->t_numel[bias] != out_features)
+    return fail(ZERO_EINVAL, "bias tensor %d holds %lld elements, the layer has %lld outputs", bias,
+                (long long)p->t_numel[bias], (long long)out_features);
+  return ok();
+}
+
+zero_status check_n(int64_t n) {
+  if (n < 0) return fail(ZERO_EINVAL, "n must be >= 0 (got %lld)", (long long)n);
+  if (n > kMaxLong) return fail(ZERO_EUNSUPPORTED, "n = %lld exceeds %lld", (long long)n, (long long)kMaxLong);
+  return ok();
+}
+
+zero_status check_16(int dt, const char* what) {
+  if (!valid_dt(dt)) return fail(ZERO_EINVAL, "unknown dtype %d", dt);
+  if (!is16(dt)) return fail(ZERO_EUNSUPPORTED, "%s are 16-bit, not fp32", what);
+  return ok();
+}
+
+zero_status check_act(int act) {
+  if (act < ZERO_ACT_NONE || act > ZERO_ACT_SILU) return fail(ZERO_EINVAL, "unknown activation %d", act);
+  return ok();
+}
+
+// n rows of `width` 16-bit elements; a staged operand's stride is bounded.
+zero_status check_rows(const void* p, int64_t n, int64_t width, int64_t stride, bool staged, const char* what, Range& r) {
+  if (stride < width)
+    return fail(ZERO_EINVAL, "the stride %lld of %s is shorter than a row of %lld", (long long)stride, what, (long long)width);
+  if (staged && stride > kMaxWide)
+    return fail(ZERO_EUNSUPPORTED, "the stride %lld of %s exceeds %lld", (long long)stride, what, (long long)kMaxWide);
+  const int64_t span = span_of(n, stride, width);
+  if (span < 0) return fail(ZERO_EINVAL, "the extent of %s overflows", what);
+  if (zero_status st = check_buffer(p, span, 2, what)) return st;
+  r = range_of(p, span, 2, what);
+  return ok();
+}
+
+bool same_place(const Range& a, const Range& b) { return a.lo == b.lo && a.hi == b.hi; }
+
+// The part of a tensor that rank's slice holds (all of it for rank < 0), and
+// where that part starts in dst.
+void part_of_tensor(const zero_plan_s& p, int32_t tensor, int32_t rank, int64_t& lo, int64_t& hi, int64_t& at) {
+  const int64_t off = p.t_off[tensor], numel = p.t_numel[tensor];
+  lo = 0;
+  hi = numel;
+  at = off;
+  if (rank >= 0) {
+    const auto& b = p.buckets[p.t_bucket[tensor]];
+    const int64_t own = b.flat_off + (int64_t)rank * b.shard_numel;
+    lo = std::max<int64_t>(0, own - off);
+    hi = std::min<int64_t>(numel, own + b.shard_numel - off);
+    at = b.shard_off + (off + lo - own);
+  }
+}
+
+// Rows of dz whose sums one bias workgroup takes: as many as leave about 256
+// workgroups, from n and the outputs alone.
+int64_t bias_chunk(int64_t n, int64_t out_features) {
+  const int64_t want = std::max<int64_t>(1, 256 / ceil_div(out_features, kBiasCols));
+  return std::max<int64_t>(32, ceil_div(n, want));
+}
+
+struct WeightShape {
+  int64_t lo, hi, at;       // elements of the weight, and their place in dst
+  int64_t row0, rows;
+  int splits;
+  int64_t part, bias_part;  // bytes
+};
+
+WeightShape weight_shape(const zero_plan_s& p, int32_t weight, int64_t in_features, int64_t out_features, int64_t n, int32_t rank) {
+  WeightShape s;
+  part_of_tensor(p, weight, rank, s.lo, s.hi, s.at);
+  s.row0 = s.rows = 0;
+  if (s.lo < s.hi) {
+    s.row0 = s.lo / in_features;
+    s.rows = (s.hi - 1) / in_features + 1 - s.row0;
+  }
+  // The pieces of k follow from the whole weight, so that a slice's sums are
+  // those of the full buffer.
+  s.splits = pick(out_features, in_features, n, 1, 0).splits;
+  s.part = part_bytes(s.rows, in_features, s.splits);
+  s.bias_part = round_up(ceil_div(n, bias_chunk(n, out_features)) * out_features * 4, 16);
+  return s;
+}
+
+zero_status run_linear(LinearArgs& a, int epi, int dt, const Pick& c, bool direct, void* ws, void* stream) {
+  if (zero_status st = check_grid((int64_t)a.p.tm * a.p.tn * a.p.splits, kTileThreads[c.tile])) return st;
+  const int64_t joins = a.p.splits > 1 ? ceil_div((int64_t)a.p.m * (a.p.n_pad / 4), kJoinThreads) : 0;
+  if (zero_status st = check_grid(joins, kJoinThreads)) return st;
+  a.p.part = a.p.splits > 1 ? (float*)ws : nullptr;
+  if (const int err = launch_linear(a, epi, dt, c.tile, direct, stream)) return hip_fail(err);
+  if (joins == 0) return ok();
+  return launched(launch_linear_join(a, epi, dt, joins, stream));
+}
+
+// ---------------------------------------------------------------------------
+// Orthogonalisation: groups of matrices of one shape
+// ---------------------------------------------------------------------------
+
+constexpr int kDefaultSteps = 5;
+const zero_newton_schulz kDefaultPoly = {kDefaultSteps, 3.4445, -4.7750, 2.0315, 1e-7};
+// From this step on A - I / 2 is stored in place of A.
+constexpr int kShiftFrom = 3;
+constexpr float kShift = 0.5f;
+
+struct Group {
+  int64_t rows, cols;
+  std::vector<int64_t> off;       // element of the flat buffer
+  std::vector<float> scale;
+};
+
+// Workspace of a batch of `batch` matrices, in bytes from its start.
+struct OrthoSpace {
+  int64_t ldx, ldn, rows_pad, side;   // padded columns of X, of A; padded rows of X
+  int64_t zx, zn;                     // elements of X and of A
+  int64_t sums, factor, x0, x1, x32, gram, poly, part, total;
+  Pick c[3];                          // of the three products
+};
+
+// As many matrices as one batch takes: enough to fill the GPU, and no more than
+// keep the batch's X, A and B near the caches.
+int64_t batch_of(int64_t rows, int64_t cols, int64_t count) {
+  const int64_t n = std::min(rows, cols), bytes = rows * cols * 8 + n * n * 4;
+  const int64_t most = std::max<int64_t>(1, (int64_t(192) << 20) / std::max<int64_t>(1, bytes));
+  const int64_t parts = ceil_div(count, std::min<int64_t>(most, kMaxBatch));
+  return ceil_div(count, parts);
+}
+
+OrthoSpace ortho_space(int64_t rows, int64_t cols, int64_t batch) {
+  OrthoSpace s;
+  s.ldx = round_up(cols, 8);
+  s.rows_pad = round_up(rows, 8);
+  s.side = std::min(s.rows_pad, s.ldx);
+  s.ldn = s.side;
+  const int64_t wide = std::max(s.rows_pad, s.ldx);
+  s.zx = s.rows_pad * s.ldx;
+  s.zn = s.side * s.ldn;
+  s.c[kGram] = pick(s.side, s.side, wide, batch, 0, true);
+  s.c[kPoly] = pick(s.side, s.side, s.side, batch, 0, true);
+  s.c[kNext] = pick(s.rows_pad, s.ldx, s.side, batch, 0);
+  int64_t at = 0;
+  auto take = [&](int64_t bytes) {
+    const int64_t here = at;
+    at += round_up(bytes, 256);
+    return here;
+  };
+  s.sums = take(batch * kNormBlocks * 8);
+  s.factor = take(batch * 4);
+  s.x0 = take(batch * s.zx * 2);
+  s.x1 = take(batch * s.zx * 2);
+  s.x32 = take(batch * s.zx * 4);
+  s.gram = take(batch * s.zn * 2);
+  s.poly = take(batch * s.zn * 2);
+  s.part = take(batch * std::max({part_bytes(s.side, s.side, s.c[kGram].splits), part_bytes(s.side, s.side, s.c[kPoly].splits),
+                                  part_bytes(s.rows_pad, s.ldx, s.c[kNext].splits)}));
+  s.total = at;
+  return s;
+}
+
+zero_status collect(zero_plan_t p, const zero_matrix* ms, int32_t n, std::vector<Group>& groups) {
+  if (check_plan(p)) return ZERO_EINVAL;
+  if (n < 0) return fail(ZERO_EINVAL, "n_matrices must be >= 0 (got %d)", n);
+  if (n > 0 && !ms) return fail(ZERO_EINVAL, "matrices is NULL");
+  std::vector<char> seen(p->t_numel.size(), 0);
+  for (int32_t i = 0; i < n; ++i) {
+    const zero_matrix& m = ms[i];
+    if (m.tensor < 0 || m.tensor >= (int32_t)p->t_numel.size())
+      return fail(ZERO_EINVAL, "matrix %d: tensor %d out of range", i, m.tensor);
+    if (seen[m.tensor]) return fail(ZERO_EINVAL, "matrix %d: tensor %d is listed twice", i, m.tensor);
+    seen[m.tensor] = 1;
+    if (m.rows < 1 || m.cols < 1)
+      return fail(ZERO_EINVAL, "matrix %d: rows and cols must be >= 1 (got %lld, %lld)", i, (long long)m.rows, (long long)m.cols);
+    if (m.rows > kMaxSide || m.cols > kMaxSide)
+      return fail(ZERO_EUNSUPPORTED, "matrix %d: %lld x %lld exceeds a side of %lld", i, (long long)m.rows, (long long)m.cols,
+                  (long long)kMaxSide);
+    const int64_t numel = p->t_numel[m.tensor], size = m.rows * m.cols;
+    if (numel % size)
+      return fail(ZERO_EINVAL, "matrix %d: tensor %d holds %lld elements, no multiple of %lld x %lld", i, m.tensor,
+                  (long long)numel, (long long)m.rows, (long long)m.cols);
+    if (!std::isfinite((float)m.scale)) return fail(ZERO_EINVAL, "matrix %d: scale %g is beyond fp32", i, m.scale);
+    auto g = std::find_if(groups.begin(), groups.end(), [&](const Group& x) { return x.rows == m.rows && x.cols == m.cols; });
+    if (g == groups.end()) {
+      groups.push_back({m.rows, m.cols, {}, {}});
+      g = groups.end() - 1;
+    }
+    for (int64_t k = 0; k < numel / size; ++k) {
+      g->off.push_back(p->t_off[m.tensor] + k * size);
+      g->scale.push_back((float)m.scale);
+    }
+  }
+  return ok();
+}
+
+int64_t ortho_bytes(const std::vector<Group>& groups) {
+  int64_t most = 0;
+  for (const Group& g : groups)
+    if (!g.off.empty()) most = std::max(most, ortho_space(g.rows, g.cols, batch_of(g.rows, g.cols, (int64_t)g.off.size())).total);
+  return most;
+}
+
+// One product of a step over the batch.
+zero_status run_ortho(OrthoArgs& a, int form_a, int form_b, int64_t m, int64_t n, int64_t k, const Pick& c, void* part, void* stream) {
+  lay_out(a.p, m, n, k, c);
+  a.upper = a.epi != kNext && a.p.splits == 1;
+  if (a.upper) {
+    const int64_t t = a.p.tm;
+    a.p.tiles = (int32_t)std::min<int64_t>(INT32_MAX, t * (t + 1) / 2);
+  }
+  a.p.part = a.p.splits > 1 ? (float*)part : nullptr;
+  const int64_t blocks = (int64_t)a.batch * a.p.tiles * a.p.splits;
+  const int64_t joins = a.p.splits > 1 ? a.batch * ceil_div((int64_t)a.p.m * (a.p.n_pad / 4), kJoinThreads) : 0;
+  if (zero_status st = check_grid(blocks, kTileThreads[c.tile])) return st;
+  if (zero_status st = check_grid(joins, kJoinThreads)) return st;
+  if (const int err = launch_ortho(a, form_a, form_b, c.tile, blocks, stream)) return hip_fail(err);
+  if (joins == 0) return ok();
+  return launched(launch_ortho_join(a, joins, stream));
+}
+
+zero_status ortho_batch(const Group& g, const OrthoSpace& s, int64_t first, int64_t batch, const zero_newton_schulz& poly, const void* src, int src_dt,
+                        void* dst, int dst_dt, char* ws, void* stream) {
+  const bool tall = g.rows > g.cols;
+  OrthoLoadArgs l;
+  memset(&l, 0, sizeof l);
+  l.src = src;
+  l.x = ws + s.x0;
+  l.sums = (double*)(ws + s.sums);
+  l.factor = (float*)(ws + s.factor);
+  l.eps = poly.eps;
+  l.numel = g.rows * g.cols;
+  l.zx = s.zx;
+  l.rows = (int32_t)g.rows;
+  l.cols = (int32_t)g.cols;
+  l.ld = (int32_t)s.ldx;
+  l.rows_pad = (int32_t)s.rows_pad;
+  l.batch = (int32_t)batch;
+  // A piece of a norm is 16 Ki elements or more.
+  l.norm_blocks = (int32_t)std::max<int64_t>(1, std::min<int64_t>(kNormBlocks, l.numel / 16384));
+  for (int64_t i = 0; i < batch; ++i) l.src_off[i] = g.off[first + i];
+  const int64_t load_blocks = batch * ceil_div(s.rows_pad * (s.ldx / 8), kLoadThreads);
+  if (zero_status st = check_grid(load_blocks, kLoadThreads)) return st;
+  if (const int err = launch_ortho_norm(l, src_dt, stream)) return hip_fail(err);
+  if (const int err = launch_ortho_load(l, src_dt, load_blocks, stream)) return hip_fail(err);
+
+  OrthoArgs a;
+  memset(&a, 0, sizeof a);
+  a.factor = l.factor;
+  a.batch = (int32_t)batch;
+  a.rows = (int32_t)g.rows;
+  a.cols = (int32_t)g.cols;
+  a.dst = dst;
+  a.dst_dt = dst_dt;
+  for (int64_t i = 0; i < batch; ++i) {
+    a.scale[i] = g.scale[first + i];
+    a.dst_off[i] = g.off[first + i];
+  }
+  char* x = ws + s.x0;
+  char* next = ws + s.x1;
+  const int64_t wide = std::max(s.rows_pad, s.ldx);
+  for (int step = 0; step < poly.steps; ++step) {
+    a.first = step == 0;
+    const double d = step >= kShiftFrom ? (double)kShift : 0.0;
+    // A - d I
+    a.epi = kGram;
+    a.last = 0;
+    a.p.a = a.p.b = x;
+    a.p.lda = a.p.ldb = s.ldx;
+    a.za = a.zb = s.zx;
+    a.out = ws + s.gram;
+    a.ldo = s.ldn;
+    a.zout = s.zn;
+    a.shift = (float)d;
+    const int form = tall ? 1 : 0;
+    if (zero_status st = run_ortho(a, form, form, s.side, s.side, wide, s.c[kGram], ws + s.part, stream)) return st;
+    // B
+    a.epi = kPoly;
+    a.p.a = a.p.b = ws + s.gram;
+    a.p.lda = a.p.ldb = s.ldn;
+    a.za = a.zb = s.zn;
+    a.add = ws + s.gram;
+    a.ldadd = s.ldn;
+    a.zadd = s.zn;
+    a.out = ws + s.poly;
+    a.c0 = (float)(poly.b + 2.0 * poly.c * d);
+    a.c1 = (float)poly.c;
+    if (zero_status st = run_ortho(a, 0, 0, s.side, s.side, s.side, s.c[kPoly], ws + s.part, stream)) return st;
+    // a X + B X, or a X + X B
+    a.epi = kNext;
+    a.last = step + 1 == poly.steps;
+    a.p.a = tall ? x : ws + s.poly;
+    a.p.b = tall ? ws + s.poly : x;
+    a.p.lda = tall ? s.ldx : s.ldn;
+    a.p.ldb = tall ? s.ldn : s.ldx;
+    a.za = tall ? s.zx : s.zn;
+    a.zb = tall ? s.zn : s.zx;
+    a.add = a.first ? x : ws + s.x32;
+    a.ldadd = s.ldx;
+    a.zadd = s.zx;
+    a.out32 = (float*)(ws + s.x32);
+    a.out = next;
+    a.ldo = s.ldx;
+    a.zout = s.zx;
+    a.c0 = (float)(poly.a + poly.b * d + poly.c * d * d);
+    if (zero_status st = run_ortho(a, 0, tall ? 0 : 1, s.rows_pad, s.ldx, s.side, s.c[kNext], ws + s.part, stream)) return st;
+    std::swap(x, next);
+  }
+  return ok();
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t zero_linear_workspace_bytes(zero_plan_t p, int32_t weight, int64_t in_features, int64_t n) {
+  int64_t out;
+  if (weight_of(p, weight, in_features, out) || check_n(n) || n == 0 || out == 0) return 0;
+  return (size_t)part_bytes(n, out, pick(n, out, in_features, 1, 0).splits);
+}
+
+zero_status zero_linear(zero_plan_t p, int32_t weight, int32_t bias, int64_t in_features, const void* params, zero_dtype dt,
+                        const void* x, int64_t n, int64_t x_stride, zero_act act, const void* residual,
+                        int64_t residual_stride, void* pre, int64_t pre_stride, void* y, int64_t y_stride, void* workspace,
+                        size_t ws_bytes, void* stream) {
+  return guarded("zero_linear", [&]() -> zero_status {
+    int64_t out = 0;
+    if (zero_status st = weight_of(p, weight, in_features, out)) return st;
+    if (zero_status st = bias_of(p, bias, weight, out)) return st;
+    if (zero_status st = check_16(dt, "the products")) return st;
+    if (zero_status st = check_act(act)) return st;
+    if (zero_status st = check_n(n)) return st;
+    if (zero_status st = check_buffer(params, p->psi_pad, 2, "params")) return st;
+    Range rx, ry, rr = {0, 0, "residual"}, rp = {0, 0, "pre"};
+    if (zero_status st = check_rows(x, n, in_features, x_stride, true, "x", rx)) return st;
+    if (zero_status st = check_rows(y, n, out, y_stride, false, "y", ry)) return st;
+    if (residual)
+      if (zero_status st = check_rows(residual, n, out, residual_stride, false, "residual", rr)) return st;
+    if (pre)
+      if (zero_status st = check_rows(pre, n, out, pre_stride, false, "pre", rp)) return st;
+    const Pick c = pick(n, out, in_features, 1, 0);
+    const size_t need = n && out ? (size_t)part_bytes(n, out, c.splits) : 0;
+    if (zero_status st = check_workspace(workspace, ws_bytes, need)) return st;
+    std::vector<Range> reads = {range_of(params, p->psi_pad, 2, "params"), rx};
+    std::vector<Range> writes = {ry, rp, range_of(workspace, (int64_t)need, 1, "workspace")};
+    if (zero_status st = check_disjoint(writes, reads)) return st;
+    const bool in_place = residual && same_place(ry, rr) && residual_stride == y_stride;
+    if (in_place) writes.erase(writes.begin());
+    if (zero_status st = check_disjoint(writes, {rr})) return st;
+    if (n == 0 || out == 0) return ok();
+    LinearArgs a;
+    memset(&a, 0, sizeof a);
+    a.p.a = x;
+    a.p.b = (const char*)params + p->t_off[weight] * 2;
+    a.p.lda = n > 1 ? x_stride : round_up(in_features, 8);     // a single row has no neighbour
+    a.p.ldb = in_features;
+    lay_out(a.p, n, out, in_features, c);
+    a.out = y;
+    a.pre_out = pre;
+    a.add = residual;
+    a.bias = bias >= 0 ? (const char*)params + p->t_off[bias] * 2 : nullptr;
+    a.ldo = y_stride;
+    a.ldpre = pre_stride;
+    a.ldadd = residual_stride;
+    a.act = act;
+    const bool direct = direct_ok(a.p.a, a.p.lda, in_features) && direct_ok(a.p.b, a.p.ldb, in_features);
+    return run_linear(a, 0, dt, c, direct, workspace, stream);
+  });
+}
+
+size_t zero_linear_input_grad_workspace_bytes(zero_plan_t p, int32_t weight, int64_t in_features, int64_t n) {
+  int64_t out;
+  if (weight_of(p, weight, in_features, out) || check_n(n) || n == 0) return 0;
+  return (size_t)part_bytes(n, in_features, pick(n, in_features, out, 1, 0).splits);
+}
+
+zero_status zero_linear_input_grad(zero_plan_t p, int32_t weight, int64_t in_features, const void* params, zero_dtype dt,
+                                   const void* dz, int64_t n, int64_t dz_stride, zero_act act, const void* pre,
+                                   int64_t pre_stride, const void* addend, int64_t addend_stride, void* dx,
+                                   int64_t dx_stride, void* workspace, size_t ws_bytes, void* stream) {
+  return guarded("zero_linear_input_grad", [&]() -> zero_status {
+    int64_t out = 0;
+    if (zero_status st = weight_of(p, weight, in_features, out)) return st;
+    if (out > kMaxWide) return fail(ZERO_EUNSUPPORTED, "%lld output features exceed %lld", (long long)out, (long long)kMaxWide);
+    if (zero_status st = check_16(dt, "the products")) return st;
+    if (zero_status st = check_act(act)) return st;
+    if (zero_status st = check_n(n)) return st;
+    if (zero_status st = check_buffer(params, p->psi_pad, 2, "params")) return st;
+    if (n > 0 && (act != ZERO_ACT_NONE) != (pre != nullptr))
+      return fail(ZERO_EINVAL, act == ZERO_ACT_NONE ? "pre is given without an activation" : "pre is NULL");
+    Range rz, rx, ra = {0, 0, "addend"}, rp = {0, 0, "pre"};
+    if (zero_status st = check_rows(dz, n, out, dz_stride, true, "dz", rz)) return st;
+    if (zero_status st = check_rows(dx, n, in_features, dx_stride, false, "dx", rx)) return st;
+    if (addend)
+      if (zero_status st = check_rows(addend, n, in_features, addend_stride, false, "addend", ra)) return st;
+    if (pre)
+      if (zero_status st = check_rows(pre, n, in_features, pre_stride, false, "pre", rp)) return st;
+    const Pick c = pick(n, in_features, out, 1, 0);
+    const size_t need = n ? (size_t)part_bytes(n, in_features, c.splits) : 0;
+    if (zero_status st = check_workspace(workspace, ws_bytes, need)) return st;
+    std::vector<Range> writes = {rx, range_of(workspace, (int64_t)need, 1, "workspace")};
+    if (zero_status st = check_disjoint(writes, {range_of(params, p->psi_pad, 2, "params"), rz, rp})) return st;
+    const bool in_place = addend && same_place(rx, ra) && addend_stride == dx_stride;
+    if (in_place) writes.erase(writes.begin());
+    if (zero_status st = check_disjoint(writes, {ra})) return st;
+    if (n == 0) return ok();
+    LinearArgs a;
+    memset(&a, 0, sizeof a);
+    a.p.a = dz;
+    a.p.b = (const char*)params + p->t_off[weight] * 2;
+    a.p.lda = n > 1 ? dz_stride : round_up(std::max<int64_t>(out, 1), 8);
+    a.p.ldb = in_features;
+    lay_out(a.p, n, in_features, out, c);
+    a.out = dx;
+    a.pre_in = pre;
+    a.add = addend;
+    a.ldo = dx_stride;
+    a.ldpre = pre_stride;
+    a.ldadd = addend_stride;
+    a.act = act;
+    const bool direct = direct_ok(a.p.a, a.p.lda, out) && direct_ok(a.p.b, a.p.ldb, in_features);
+    return run_linear(a, 1, dt, c, direct, workspace, stream);
+  });
+}
+
+size_t zero_linear_weight_grad_workspace_bytes(zero_plan_t p, int32_t weight, int64_t in_features, int64_t n, int32_t rank) {
+  int64_t out;
+  if (weight_of(p, weight, in_features, out) || check_n(n) || n == 0 || out == 0 || rank >= p->n_d) return 0;
+  const WeightShape s = weight_shape(*p, weight, in_features, out, n, rank);
+  return (size_t)(round_up(s.part, 16) + s.bias_part);
+}
+
+zero_status zero_linear_weight_grad(zero_plan_t p, int32_t weight, int32_t bias, int64_t in_features, const void* dz,
+                                    int64_t dz_stride, const void* x, int64_t x_stride, zero_dtype dt, int64_t n,
+                                    double scale, void* dst, zero_dtype dst_dt, int32_t rank, int32_t accumulate,
+                                    void* workspace, size_t ws_bytes, void* stream) {
+  return guarded("zero_linear_weight_grad", [&]() -> zero_status {
+    int64_t out = 0;
+    if (zero_status st = weight_of(p, weight, in_features, out)) return st;
+    if (zero_status st = bias_of(p, bias, weight, out)) return st;
+    if (bias == weight) return fail(ZERO_EINVAL, "weight and bias are the same tensor");
+    if (out > kMaxWide) return fail(ZERO_EUNSUPPORTED, "%lld output features exceed %lld", (long long)out, (long long)kMaxWide);
+    if (zero_status st = check_16(dt, "the products")) return st;
+    if (!valid_dt(dst_dt)) return fail(ZERO_EINVAL, "unknown dtype %d", (int)dst_dt);
+    if (zero_status st = check_n(n)) return st;
+    if (rank >= p->n_d) return fail(ZERO_EINVAL, "rank %d outside [0, %d)", rank, p->n_d);
+    if (accumulate != 0 && accumulate != 1) return fail(ZERO_EINVAL, "accumulate must be 0 or 1 (got %d)", accumulate);
+    if (!std::isfinite((float)scale)) return fail(ZERO_EINVAL, "scale %g is beyond fp32", scale);
+    Range rz, rx;
+    if (zero_status st = check_rows(dz, n, out, dz_stride, true, "dz", rz)) return st;
+    if (zero_status st = check_rows(x, n, in_features, x_stride, true, "x", rx)) return st;
+    const int64_t dst_elems = rank < 0 ? p->psi_pad : p->shard_total;
+    if (zero_status st = check_buffer(dst, dst_elems, esize(dst_dt), "dst")) return st;
+    const size_t need = zero_linear_weight_grad_workspace_bytes(p, weight, in_features, n, rank);
+    if (zero_status st = check_workspace(workspace, ws_bytes, need)) return st;
+    if (zero_status st = check_disjoint({range_of(dst, dst_elems, esize(dst_dt), "dst"),
+                                         range_of(workspace, (int64_t)need, 1, "workspace")}, {rz, rx}))
+      return st;
+    if (out == 0 || (accumulate && n == 0)) return ok();
+
+    const WeightShape s = weight_shape(*p, weight, in_features, out, n, rank);
+    WeightGradArgs a;
+    memset(&a, 0, sizeof a);
+    Pick c = {kTile64, 1, 0.0};
+    a.dst_dt = dst_dt;
+    a.accumulate = accumulate;
+    a.scale = (float)scale;
+    a.row0 = (int32_t)s.row0;
+    a.lo = s.lo;
+    a.hi = s.hi;
+    if (s.rows > 0) {
+      c = pick(s.rows, in_features, n, 1, s.splits);
+      a.dst = (char*)dst + s.at * esize(dst_dt);
+    }
+    a.p.a = (const char*)dz + s.row0 * 2;
+    a.p.b = x;
+    a.p.lda = n > 1 ? dz_stride : round_up(out, 8);
+    a.p.ldb = n > 1 ? x_stride : round_up(in_features, 8);
+    lay_out(a.p, s.rows, in_features, n, c);
+    a.p.part = a.p.splits > 1 ? (float*)workspace : nullptr;
+    if (bias >= 0) {
+      int64_t lo, hi, at;
+      part_of_tensor(*p, bias, rank, lo, hi, at);
+      if (lo < hi) {
+        a.bias_dst = (char*)dst + at * esize(dst_dt);
+        a.bias_part = (float*)((char*)workspace + round_up(s.part, 16));
+        a.b_lo = (int32_t)lo;
+        a.b_hi = (int32_t)hi;
+        const int64_t chunk = bias_chunk(n, out);
+        a.chunk_rows = (int32_t)chunk;
+        a.chunks = (int32_t)std::max<int64_t>(1, ceil_div(n, chunk));
+        a.col_blocks = (int32_t)ceil_div(hi - lo, kBiasCols);
+        a.bias_blocks = a.chunks * a.col_blocks;
+      }
+    }
+    const int64_t blocks = a.bias_blocks + (int64_t)a.p.tm * a.p.tn * a.p.splits;
+    if (blocks == 0) return ok();
+    a.join_blocks = a.p.splits > 1 ? (int32_t)std::min<int64_t>(INT32_MAX, ceil_div((int64_t)a.p.m * (a.p.n_pad / 4), kJoinThreads)) : 0;
+    const int64_t joins = a.join_blocks + (a.bias_blocks && a.chunks > 1 ? ceil_div(a.b_hi - a.b_lo, kJoinThreads) : 0);
+    if (zero_status st = check_grid(blocks, kTileThreads[c.tile])) return st;
+    if (zero_status st = check_grid(joins, kJoinThreads)) return st;
+    const bool direct = direct_ok(a.p.a, a.p.lda, s.rows) && direct_ok(a.p.b, a.p.ldb, in_features);
+    if (const int err = launch_weight_grad(a, dt, c.tile, direct, blocks, stream)) return hip_fail(err);
+    if (joins == 0) return ok();
+    return launched(launch_weight_grad_join(a, joins, stream));
+  });
+}
+
+zero_status zero_activation_grad(const void* dy, const void* pre, void* dz, int64_t n, zero_dtype dt, zero_act act, void* stream) {
+  return guarded("zero_activation_grad", [&]() -> zero_status {
+    if (zero_status st = check_16(dt, "the elements")) return st;
+    if (zero_status st = check_act(act)) return st;
+    if (n < 0 || n > kMaxElems) return fail(ZERO_EINVAL, "n = %lld is out of range", (long long)n);
+    if (zero_status st = check_buffer(dy, n, 2, "dy")) return st;
+    if (zero_status st = check_buffer(pre, n, 2, "pre")) return st;
+    if (zero_status st = check_buffer(dz, n, 2, "dz")) return st;
+    const Range rz = range_of(dz, n, 2, "dz");
+    std::vector<Range> reads = {range_of(pre, n, 2, "pre")};
+    if (dz != dy) reads.push_back(range_of(dy, n, 2, "dy"));
+    if (zero_status st = check_disjoint({rz}, reads)) return st;
+    const int64_t per = (int64_t)kActThreads * kActVec, part = most_blocks(kActThreads) * per;
+    for (int64_t i = 0; i < n; i += part) {
+      ActGradArgs a;
+      memset(&a, 0, sizeof a);
+      a.dy = (const char*)dy + i * 2;
+      a.pre = (const char*)pre + i * 2;
+      a.dz = (char*)dz + i * 2;
+      a.n = std::min(part, n - i);
+      a.act = act;
+      if (const int err = launch_act_grad(a, dt, ceil_div(a.n, per), stream)) return hip_fail(err);
+    }
+    return ok();
+  });
+}
+
+size_t zero_orthogonalize_workspace_bytes(zero_plan_t p, const zero_matrix* matrices, int32_t n_matrices) {
+  size_t need = 0;
+  guarded("zero_orthogonalize_workspace_bytes", [&]() -> zero_status {
+    std::vector<Group> groups;
+    if (zero_status st = collect(p, matrices, n_matrices, groups)) return st;
+    need = (size_t)ortho_bytes(groups);
+    return ok();
+  });
+  return need;
+}
+
+zero_status zero_orthogonalize(zero_plan_t p, const zero_matrix* matrices, int32_t n_matrices, const zero_newton_schulz* poly,
+                               const void* src, zero_dtype src_dt, void* dst, zero_dtype dst_dt, void* workspace,
+                               size_t ws_bytes, void* stream) {
+  return guarded("zero_orthogonalize", [&]() -> zero_status {
+    std::vector<Group> groups;
+    if (zero_status st = collect(p, matrices, n_matrices, groups)) return st;
+    const zero_newton_schulz q = poly ? *poly : kDefaultPoly;
+    if (q.steps < 1 || q.steps > 32) return fail(ZERO_EINVAL, "steps must lie in [1, 32] (got %d)", q.steps);
+    for (double v : {q.a, q.b, q.c})
+      if (!(std::fabs(v) <= 1000.0)) return fail(ZERO_EINVAL, "coefficient %g exceeds 1000", v);
+    if (!(q.eps > 0.0 && q.eps <= 1e30)) return fail(ZERO_EINVAL, "eps must lie in (0, 1e30] (got %g)", q.eps);
+    if (zero_status st = check_16(src_dt, "the matrices")) return st;
+    if (zero_status st = check_16(dst_dt, "the results")) return st;
+    if (zero_status st = check_buffer(src, p->psi_pad, 2, "src")) return st;
+    if (zero_status st = check_buffer(dst, p->psi_pad, 2, "dst")) return st;
+    const size_t need = (size_t)ortho_bytes(groups);
+    if (zero_status st = check_workspace(workspace, ws_bytes, need)) return st;
+    if (need && !aligned(workspace, 256)) return fail(ZERO_EINVAL, "workspace is not 256-byte aligned");
+    std::vector<Range> writes = {range_of(workspace, (int64_t)need, 1, "workspace")};
+    if (dst == src && dst_dt != src_dt) return fail(ZERO_EINVAL, "dst is src with another type");
+    if (dst != src) writes.push_back(range_of(dst, p->psi_pad, 2, "dst"));
+    if (zero_status st = check_disjoint(writes, {range_of(src, p->psi_pad, 2, "src")})) return st;
+    for (const Group& g : groups) {
+      const int64_t count = (int64_t)g.off.size();
+      if (count == 0) continue;
+      const int64_t batch = batch_of(g.rows, g.cols, count);
+      const OrthoSpace s = ortho_space(g.rows, g.cols, batch);   // a smaller last batch takes the same shapes
+      for (int64_t i = 0; i < count; i += batch)
+        if (zero_status st = ortho_batch(g, s, i, std::min(batch, count - i), q, src, src_dt, dst, dst_dt, (char*)workspace, stream))
+          return st;
+    }
+    return ok();
+  });
+}
+
+}  // extern "C"

@@ -42,12 +42,17 @@ struct StepSeg {
 enum StepMode : int {
   kFused = 0,        // reduce ranks in registers, then Adam, cast, store
   kFromReduced = 1,  // Adam reading an fp32 reduced gradient
-  kReduceOnly = 2    // fold ranks, write fp32
+  kReduceOnly = 2,   // fold ranks, write fp32
+  kMomentum = 3,     // fold ranks in registers, then momentum (m), cast, store
+  kMomentumReduced = 4,  // momentum from an fp32 reduced gradient
+  kApply = 5         // the one rank's "gradient" is a direction: decay and subtract, cast, store
 };
+constexpr int kStepModes = 6;
 
 enum StepFlags : int {
   kFlagInitFromOut = 1,   // reduce: continue the fold from the fp32 output
-  kFlagApplyScale = 2     // reduce: multiply by grad_scale at the end
+  kFlagApplyScale = 2,    // reduce: multiply by grad_scale at the end
+  kFlagNesterov = 4       // momentum: store g + mu m rather than m
 };
 
 struct StepArgs {
@@ -60,6 +65,7 @@ struct StepArgs {
   float* v;
   void* dst;
   float c[9];             // b1, 1-b1, b2, 1-b2, 1-b1^t, 1-b2^t, lr, eps, grad_scale
+                          // (momentum: mu and grad_scale; apply: 1 - lr decay and lr)
   int32_t n_ranks;
   int32_t n_seg;
   int32_t flags;

@@ -109,6 +109,22 @@ __device__ __forceinline__ void adam1(const AdamC& k, float g, float& w, float& 
   w = w - delta;
 }
 
+// Momentum on one element, and the value that goes on to the orthogonalisation.
+__device__ __forceinline__ float momentum1(float mu, bool nesterov, float g, float& m) {
+  const float m_old = mu * m;
+  m = m_old + g;
+  if (!nesterov) return m;
+  const float ahead = mu * m;
+  return g + ahead;
+}
+
+// Decay and a step along a direction.
+__device__ __forceinline__ void apply1(float keep, float lr, float o, float& w) {
+  const float kept = keep * w;
+  const float delta = lr * o;
+  w = kept - delta;
+}
+
 // Keeps the eight values computed before this point: the compiler may not
 // sink their arithmetic (and with it the loads feeding it) below a following
 // wait loop.
@@ -295,8 +311,10 @@ template <int MODE, int GDT, int PDT>
 __device__ __forceinline__ void step_one(const StepArgs& a, int64_t shard_off, int64_t full_off,
                                          int64_t dst_off, uint32_t e) {
   float g;
-  if constexpr (MODE == kFromReduced) {
+  if constexpr (MODE == kFromReduced || MODE == kMomentumReduced) {
     g = gaddr<const gf32*>(a.reduced)[shard_off + e];
+  } else if constexpr (MODE == kApply) {
+    g = widen1<GDT>(gaddr<const gu16*>(rank_base(a, 0, shard_off, full_off))[e]);
   } else {
     const int n = a.n_ranks;
     float acc;
@@ -316,7 +334,19 @@ __device__ __forceinline__ void step_one(const StepArgs& a, int64_t shard_off, i
     }
     g = acc * a.c[8];
   }
-  if constexpr (MODE != kReduceOnly) {
+  if constexpr (MODE == kMomentum || MODE == kMomentumReduced) {
+    gf32* mp = gaddr<gf32*>(a.m);
+    float m = mp[shard_off + e];
+    const float u = momentum1(a.c[0], a.flags & kFlagNesterov, g, m);
+    mp[shard_off + e] = m;
+    gaddr<gu16*>(a.dst)[dst_off + e] = (uint16_t)narrow1<PDT>(u);
+  } else if constexpr (MODE == kApply) {
+    gf32* wp = gaddr<gf32*>(a.master);
+    float w = wp[shard_off + e];
+    apply1(a.c[0], a.c[6], g, w);
+    wp[shard_off + e] = w;
+    gaddr<gu16*>(a.dst)[dst_off + e] = (uint16_t)narrow1<PDT>(w);
+  } else if constexpr (MODE != kReduceOnly) {
     const AdamC k = load_consts(a);
     gf32* wp = gaddr<gf32*>(a.master);
     gf32* mp = gaddr<gf32*>(a.m);
@@ -404,7 +434,41 @@ __global__ void __launch_bounds__(kStepThreads) step_vec_kernel(const StepArgs a
     if (tb)
       for (uint32_t e = ea + kHalf; e < len; ++e) step_one<MODE, GDT, PDT>(a, shard_off, full_off, dst_off, e);
     return;
-  } else if constexpr (MODE == kFused) {
+  } else if constexpr (MODE == kMomentumReduced || MODE == kApply) {
+    // As above, group by group.
+    gu32x2* const dp = gaddr<gu32x2*>((uint16_t*)a.dst + dst_off);
+    auto group = [&](uint32_t e) {
+      gf32x4* const sp = gaddr<gf32x4*>((MODE == kApply ? a.master : a.m) + shard_off) + (e >> 2);
+      f32x4 s4 = ld_nt((const gf32x4*)sp);
+      float x[4];
+      if constexpr (MODE == kApply) {
+        widen4<GDT>(ld_nt(grad_pair(a, 0, shard_off, full_off, e * 2u)), x);
+      } else {
+        const f32x4 g4 = ld_nt(gaddr<const gf32x4*>(a.reduced + shard_off) + (e >> 2));
+#pragma unroll
+        for (int i = 0; i < 4; ++i) x[i] = g4[i];   // the reduction has scaled it
+      }
+      uint32_t h[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        float s = s4[i];
+        if constexpr (MODE == kApply) {
+          apply1(a.c[0], a.c[6], x[i], s);
+          h[i] = narrow1<PDT>(s);
+        } else {
+          h[i] = narrow1<PDT>(momentum1(a.c[0], a.flags & kFlagNesterov, x[i], s));
+        }
+        s4[i] = s;
+      }
+      st_nt(sp, s4);
+      st_nt(dp + (e >> 2), u32x2{h[0] | (h[1] << 16), h[2] | (h[3] << 16)});
+    };
+    group(ea);
+    if (vb) group(eb);
+    if (tb)
+      for (uint32_t e = ea + kHalf; e < len; ++e) step_one<MODE, GDT, PDT>(a, shard_off, full_off, dst_off, e);
+    return;
+  } else if constexpr (MODE == kFused || MODE == kMomentum) {
     float acc[8];
     await_read_window(a.win_period, a.win_open);
     fold<GDT, NDC, false>(a, shard_off, full_off, ea * 2u, eb * 2u, acc);
@@ -431,7 +495,24 @@ __global__ void __launch_bounds__(kStepThreads) step_vec_kernel(const StepArgs a
     store_groups(a.out + shard_off, ea, eb, vb, acc);
   }
 
-  if constexpr (MODE != kReduceOnly) {
+  if constexpr (MODE == kMomentum) {
+    float m[8], u[8];
+    load_groups(a.m + shard_off, ea, eb, m);
+    const bool nesterov = a.flags & kFlagNesterov;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) u[i] = momentum1(a.c[0], nesterov, g[i], m[i]);
+    pin8(m);
+    pin8(u);
+    await_write_window(a.win_period, a.win_open);
+    store_groups(a.m + shard_off, ea, eb, vb, m);
+    const u32x2 pa = {narrow1<PDT>(u[0]) | (narrow1<PDT>(u[1]) << 16),
+                      narrow1<PDT>(u[2]) | (narrow1<PDT>(u[3]) << 16)};
+    const u32x2 pb = {narrow1<PDT>(u[4]) | (narrow1<PDT>(u[5]) << 16),
+                      narrow1<PDT>(u[6]) | (narrow1<PDT>(u[7]) << 16)};
+    gu32x2* const dp = gaddr<gu32x2*>((uint16_t*)a.dst + dst_off);
+    st_nt(dp + (ea >> 2), pa);
+    if (vb) st_nt(dp + (eb >> 2), pb);
+  } else if constexpr (MODE != kReduceOnly) {
     const AdamC k = load_consts(a);
     float w[8], m[8], v[8];
     load_groups(a.master + shard_off, ea, eb, w);
@@ -665,6 +746,11 @@ void* pick_step(int ndc, bool vec) {
   return pick_ndc<MODE, GDT, PDT>(ndc);
 }
 
+template <int MODE, int GDT, int PDT>
+void* pick_one(bool vec) {   // the rank count plays no part
+  return vec ? (void*)&step_vec_kernel<MODE, GDT, PDT, 1> : (void*)&step_elem_kernel<MODE, GDT, PDT>;
+}
+
 void* pick_kernel(int mode, int gdt, int pdt, int ndc, bool vec) {
   const bool gb = gdt == ZERO_BF16, pb = pdt == ZERO_BF16;
   if (mode == kFromReduced) {   // gradient type and rank count play no part
@@ -676,6 +762,18 @@ void* pick_kernel(int mode, int gdt, int pdt, int ndc, bool vec) {
   if (mode == kReduceOnly) {    // parameter type plays no part
     return gb ? pick_step<kReduceOnly, ZERO_BF16, ZERO_F16>(ndc, vec)
               : pick_step<kReduceOnly, ZERO_F16, ZERO_F16>(ndc, vec);
+  }
+  if (mode == kMomentum) {
+    if (gb && pb) return pick_step<kMomentum, ZERO_BF16, ZERO_BF16>(ndc, vec);
+    if (gb) return pick_step<kMomentum, ZERO_BF16, ZERO_F16>(ndc, vec);
+    if (pb) return pick_step<kMomentum, ZERO_F16, ZERO_BF16>(ndc, vec);
+    return pick_step<kMomentum, ZERO_F16, ZERO_F16>(ndc, vec);
+  }
+  if (mode == kMomentumReduced)
+    return pb ? pick_one<kMomentumReduced, ZERO_BF16, ZERO_BF16>(vec) : pick_one<kMomentumReduced, ZERO_BF16, ZERO_F16>(vec);
+  if (mode == kApply) {
+    if (gb) return pb ? pick_one<kApply, ZERO_BF16, ZERO_BF16>(vec) : pick_one<kApply, ZERO_BF16, ZERO_F16>(vec);
+    return pb ? pick_one<kApply, ZERO_F16, ZERO_BF16>(vec) : pick_one<kApply, ZERO_F16, ZERO_F16>(vec);
   }
   if (gb && pb) return pick_step<kFused, ZERO_BF16, ZERO_BF16>(ndc, vec);
   if (gb) return pick_step<kFused, ZERO_BF16, ZERO_F16>(ndc, vec);
@@ -709,9 +807,9 @@ int launch_warm(const WarmArgs& a, int n_blocks, void* stream) {
 int resident_blocks(int mode, int gdt, int pdt, int ndc, bool vec) {
   // Cached per kernel variant (all devices this library runs on are the same
   // gfx950 part); 0 = not yet known, -1 = query failed.
-  static std::atomic<int> cache[3][3][3][5][2];
+  static std::atomic<int> cache[kStepModes][3][3][5][2];
   const int ni = ndc == 4 ? 1 : ndc == 8 ? 2 : ndc == 16 ? 3 : ndc == 64 ? 4 : 0;
-  std::atomic<int>& slot = cache[mode % 3][gdt % 3][pdt % 3][ni][vec ? 1 : 0];
+  std::atomic<int>& slot = cache[mode % kStepModes][gdt % 3][pdt % 3][ni][vec ? 1 : 0];
   int r = slot.load(std::memory_order_relaxed);
   if (r != 0) return r < 0 ? 0 : r;
   int per_cu = 0, dev = 0, cus = 0;

@@ -1,0 +1,217 @@
+// zero_muon.hip -- gfx950 kernels that orthogonalise matrices by Newton-Schulz
+// products.
+//
+// X <- a X + (b A + c A A) X with A = X X^T drives every singular value of X
+// towards 1.  With n the shorter side a step is three products, two of which
+// have symmetric results of which only the tiles on and above the diagonal are
+// computed and the others mirrored.  A tall matrix takes A = X^T X and X A, so
+// that nothing is transposed in memory.
+//
+// Numbers between the products.  X is held in fp32 for the term a X, and in fp16
+// as the products' operand: directions that the gradient hardly holds are scaled
+// up by a in each step, and X rounded to 16 bits would carry its rounding up
+// with them (a matrix of exponentially falling singular values ends 1.3% off its
+// 64-bit result; with X in fp32 0.04%).  A and B = b A + c A A are held in fp16:
+// their entries are of order one and below, where fp16 has three bits more than
+// bf16 (1.0% of error against 0.14%).  From the fourth step on A's eigenvalues
+// lie around 1, and A - I/2 is stored in place of A, which halves its largest
+// entries and their rounding; the polynomial is rewritten for it:
+//   b A + c A^2 = (b d + c d^2) I + (b + 2 c d) D + c D^2,  D = A - d I,
+// and the multiple of I joins a.  The first X is the gradient times a power of
+// two, which rounds nothing that fp16 holds; the rest of 1 / |G| enters as a
+// factor of the first step's results.
+#include "zero_hidden_dev.h"
+
+#pragma clang fp contract(off)
+
+namespace zk {
+namespace hidden {
+namespace {
+
+template <int DT>
+__device__ __forceinline__ float widen1(uint16_t h) {
+  if constexpr (DT == ZERO_BF16) return __uint_as_float((uint32_t)h << 16);
+  else return (float)__builtin_bit_cast(_Float16, h);
+}
+
+// Sum of squares of a piece of a matrix, in fp64 (exact products of 16-bit
+// values, no overflow).
+template <typename T>
+__global__ void __launch_bounds__(kLoadThreads) ortho_norm_kernel(const OrthoLoadArgs a) {
+  const int z = blockIdx.x / a.norm_blocks, piece = blockIdx.x % a.norm_blocks;
+  const int64_t units = (a.numel + 7) / 8, per = (units + a.norm_blocks - 1) / a.norm_blocks;
+  const int64_t u1 = (piece + 1) * per < units ? (piece + 1) * per : units;
+  double s = 0.0;
+  for (int64_t u = piece * per + threadIdx.x; u < u1; u += kLoadThreads) {
+    float x[8];
+    const int64_t e = u * 8;
+    load_row<T, 8>(a.src, a.src_off[z] + e, a.numel - e < 8 ? (int)(a.numel - e) : 8, x);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) s += (double)x[i] * (double)x[i];
+  }
+  __shared__ double w[kLoadThreads];
+  w[threadIdx.x] = s;
+  __syncthreads();
+  for (int k = kLoadThreads / 2; k > 0; k >>= 1) {
+    if ((int)threadIdx.x < k) w[threadIdx.x] += w[threadIdx.x + k];
+    __syncthreads();
+  }
+  if (threadIdx.x == 0) a.sums[(int64_t)z * a.norm_blocks + piece] = w[0];
+}
+
+// X = G * 2^k in fp16 with |X| in [32, 64), padded with zeros to multiples of 8,
+// and the factor that is left of 1 / (|G| + eps).
+template <typename T>
+__global__ void __launch_bounds__(kLoadThreads) ortho_load_kernel(const OrthoLoadArgs a) {
+  const int upr = a.ld >> 3;
+  const int64_t per = (int64_t)a.rows_pad * upr, blocks = (per + kLoadThreads - 1) / kLoadThreads;
+  const int z = (int)(blockIdx.x / blocks);
+  double s = 0.0;
+  for (int i = 0; i < a.norm_blocks; ++i) s += a.sums[(int64_t)z * a.norm_blocks + i];
+  const double d = __builtin_sqrt(s) + a.eps;
+  const bool good = d < __builtin_inf();                          // not NaN either
+  const int e = good ? 6 - (ilogb(d) + 1) : 0;                   // d 2^e in [32, 64)
+  const int64_t u = (blockIdx.x - z * blocks) * kLoadThreads + threadIdx.x;
+  if (u == 0) a.factor[z] = good ? (float)(1.0 / ldexp(d, e)) : __builtin_nanf("");
+  if (u >= per) return;
+  const int row = (int)(u / upr), col = (int)(u - (int64_t)row * upr) * 8;
+  float x[8];
+  const int have = row < a.rows ? a.cols - col : 0;
+  load_row<T, 8>(a.src, a.src_off[z] + (int64_t)row * a.cols + col, have < 8 ? have : 8, x);
+#pragma unroll
+  for (int i = 0; i < 8; ++i) x[i] = good ? ldexpf(x[i], e) : 0.0f;
+  store_row<_Float16, 8>(a.x, z * a.zx + (int64_t)row * a.ld + col, 8, x);
+}
+
+// V sums of one row through the epilogue.
+template <int V>
+__device__ __forceinline__ void finish(const OrthoArgs& a, int z, int row, int col, const float (&acc)[V]) {
+  const int have = a.p.n - col;
+  float v[V], x[V];
+  if (a.epi == kGram) {
+    const float f = a.first ? a.factor[z] : 1.0f, f2 = f * f;
+#pragma unroll
+    for (int i = 0; i < V; ++i) v[i] = __builtin_fmaf(f2, acc[i], row == col + i ? -a.shift : 0.0f);
+  } else if (a.epi == kPoly) {
+    load_row<_Float16, V>(a.add, z * a.zadd + (int64_t)row * a.ldadd + col, have, x);
+#pragma unroll
+    for (int i = 0; i < V; ++i) v[i] = __builtin_fmaf(a.c1, acc[i], a.c0 * x[i]);
+  } else {
+    const int64_t e = z * a.zadd + (int64_t)row * a.ldadd + col;
+    if (a.first) {
+      load_row<_Float16, V>(a.add, e, have, x);
+    } else {
+      const AS1 float* p = (const AS1 float*)a.add + e;
+#pragma unroll
+      for (int i = 0; i < V; i += 4) {      // rows are padded to whole fours
+        const f32x4 t = col + i < a.p.n ? *(const AS1 f32x4*)(p + i) : f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int k = 0; k < 4; ++k) x[i + k] = t[k];
+      }
+    }
+    const float f = a.first ? a.factor[z] : 1.0f;
+#pragma unroll
+    for (int i = 0; i < V; ++i) v[i] = f * __builtin_fmaf(a.c0, x[i], acc[i]);
+    if (a.last) {
+      if (row >= a.rows || col >= a.cols) return;
+      const int left = a.cols - col;
+      const float s = a.scale[z];
+#pragma unroll
+      for (int i = 0; i < V; ++i) v[i] *= s;
+      const int64_t d = a.dst_off[z] + (int64_t)row * a.cols + col;
+      if (a.dst_dt == ZERO_BF16) store_row<__bf16, V>(a.dst, d, left, v);
+      else store_row<_Float16, V>(a.dst, d, left, v);
+      return;
+    }
+    AS1 float* p = (AS1 float*)a.out32 + e;
+#pragma unroll
+    for (int i = 0; i < V; i += 4)
+      if (col + i < a.p.n) *(AS1 f32x4*)(p + i) = f32x4{v[i], v[i + 1], v[i + 2], v[i + 3]};
+  }
+  store_row<_Float16, V>(a.out, z * a.zout + (int64_t)row * a.ldo + col, have, v);
+}
+
+template <int V>
+__device__ __forceinline__ void mirror(const OrthoArgs& a, int z, int row, int col, const float (&acc)[V]) {
+  const float f = a.first ? a.factor[z] : 1.0f, f2 = f * f;
+  float x[V];
+  if (a.epi == kPoly) load_row<_Float16, V>(a.add, z * a.zadd + (int64_t)row * a.ldadd + col, a.p.n - col, x);
+#pragma unroll
+  for (int i = 0; i < V; ++i) {
+    const float v = a.epi == kGram ? f2 * acc[i] : __builtin_fmaf(a.c1, acc[i], a.c0 * x[i]);
+    if (col + i < a.p.n) ((AS1 _Float16*)a.out)[z * a.zout + (int64_t)(col + i) * a.ldo + row] = (_Float16)v;
+  }
+}
+
+template <int AF, int BF, int TILE>
+__global__ void __launch_bounds__(kTileThreads[TILE]) ortho_kernel(const OrthoArgs a) {
+  typedef CoreOf<_Float16, AF, BF, TILE, true> C;
+  extern __shared__ __attribute__((aligned(1024))) char smem[];
+  constexpr int BM = Shape<TILE>::BM, BN = Shape<TILE>::BN;
+  const int t = die_order(blockIdx.x, gridDim.x), piece = t / a.p.tiles, z = piece / a.p.splits, split = piece - z * a.p.splits;
+  int im, in;
+  if (a.upper) place_upper(t - piece * a.p.tiles, im, in);
+  else place(t - piece * a.p.tiles, a.p.tm, a.p.tn, im, in);
+  const int k0 = split * a.p.k_piece, k_end = a.p.k - k0 < a.p.k_piece ? a.p.k : k0 + a.p.k_piece;
+  C core;
+  core.run((ZK_LDS char*)smem, (const _Float16*)a.p.a + z * a.za, a.p.lda, a.p.m, (const _Float16*)a.p.b + z * a.zb, a.p.ldb,
+           a.p.n, im * BM, in * BN, k0, k_end);
+  if (a.p.part) {
+    float* part = a.p.part + (int64_t)z * a.p.splits * a.p.m * a.p.n_pad;
+    core.each(im * BM, in * BN, [&](int row, int col, const float* v) {
+      if (row < a.p.m && col < a.p.n) store_part<C::kVec>(a.p, part, split, row, col, v);
+    });
+    return;
+  }
+  const bool twice = a.upper && im != in;
+  core.each(im * BM, in * BN, [&](int row, int col, const float* v) {
+    if (row < a.p.m && col < a.p.n) {
+      finish<C::kVec>(a, z, row, col, *(const float(*)[C::kVec])v);
+      if (twice) mirror<C::kVec>(a, z, row, col, *(const float(*)[C::kVec])v);
+    }
+  });
+}
+
+__global__ void __launch_bounds__(kJoinThreads) ortho_join_kernel(const OrthoArgs a) {
+  const int64_t per = ((int64_t)a.p.m * (a.p.n_pad >> 2) + kJoinThreads - 1) / kJoinThreads;
+  const int z = (int)(blockIdx.x / per);
+  int row, col;
+  float v[4];
+  if (join4(a.p, a.p.part + (int64_t)z * a.p.splits * a.p.m * a.p.n_pad, (blockIdx.x - z * per) * kJoinThreads + threadIdx.x, row,
+            col, v))
+    finish<4>(a, z, row, col, v);
+}
+
+template <int AF, int BF>
+int go(const OrthoArgs& a, int tile, int64_t blocks, void* stream) {
+  if (tile == kTile256)
+    return launch(&ortho_kernel<AF, BF, kTile256>, a, blocks, 512, 2 * CoreOf<_Float16, AF, BF, kTile256, true>::kStage, stream);
+  if (tile == kTile128)
+    return launch(&ortho_kernel<AF, BF, kTile128>, a, blocks, 256, 2 * CoreOf<_Float16, AF, BF, kTile128, true>::kStage, stream);
+  return launch(&ortho_kernel<AF, BF, kTile64>, a, blocks, 256, 2 * CoreOf<_Float16, AF, BF, kTile64, true>::kStage, stream);
+}
+
+}  // namespace
+
+int launch_ortho_norm(const OrthoLoadArgs& a, int dt, void* stream) {
+  const int64_t blocks = (int64_t)a.batch * a.norm_blocks;
+  return dt == ZERO_BF16 ? launch(&ortho_norm_kernel<__bf16>, a, blocks, kLoadThreads, 0, stream)
+                         : launch(&ortho_norm_kernel<_Float16>, a, blocks, kLoadThreads, 0, stream);
+}
+
+int launch_ortho_load(const OrthoLoadArgs& a, int dt, int64_t blocks, void* stream) {
+  return dt == ZERO_BF16 ? launch(&ortho_load_kernel<__bf16>, a, blocks, kLoadThreads, 0, stream)
+                         : launch(&ortho_load_kernel<_Float16>, a, blocks, kLoadThreads, 0, stream);
+}
+
+int launch_ortho(const OrthoArgs& a, int form_a, int form_b, int tile, int64_t blocks, void* stream) {
+  if (form_a == kFormM) return go<kFormM, kFormM>(a, tile, blocks, stream);
+  return form_b == kFormM ? go<kFormK, kFormM>(a, tile, blocks, stream) : go<kFormK, kFormK>(a, tile, blocks, stream);
+}
+
+int launch_ortho_join(const OrthoArgs& a, int64_t blocks, void* stream) {
+  return launch(&ortho_join_kernel, a, blocks, kJoinThreads, 0, stream);
+}
+
+}  // namespace hidden
+}  // namespace zk

@@ -26,7 +26,7 @@ constexpr int64_t kMaxHidden = int64_t(1) << 24;
 constexpr int64_t kMaxTokens = int64_t(1) << 30;
 constexpr int64_t kMaxVocab = int64_t(1) << 30;
 constexpr int64_t kInfinityCache = int64_t(256) << 20;   // memory-side cache of MI355X
-constexpr int64_t kMaxElems = int64_t(1) << 59;   // of one buffer: byte offsets stay in int64
+
 
 bool valid_it(int it) { return it == ZERO_I32 || it == ZERO_I64; }
 int isize(int it) { return it == ZERO_I64 ? 8 : 4; }
@@ -35,39 +35,6 @@ uint64_t mix64(uint64_t z) {
   z = (z ^ (z >> 30)) * kMix1;
   z = (z ^ (z >> 27)) * kMix2;
   return z ^ (z >> 31);
-}
-
-// Elements spanned by n rows of `width`, `stride` apart; -1 if too many.
-int64_t span_of(int64_t n, int64_t stride, int64_t width) {
-  if (n == 0 || width == 0) return 0;
-  int64_t s;
-  if (__builtin_mul_overflow(n - 1, stride, &s) || s > kMaxElems || width > kMaxElems - s) return -1;
-  return s + width;
-}
-
-zero_status check_buffer(const void* p, int64_t elems, int es, const char* what) {
-  if (!p && elems > 0) return fail(ZERO_EINVAL, "%s is NULL", what);
-  if (!aligned(p, es)) return fail(ZERO_EINVAL, "%s is not element aligned", what);
-  return ok();
-}
-
-zero_status check_workspace(const void* ws, size_t bytes, size_t need) {
-  if (need == 0) return ok();
-  if (!ws) return fail(ZERO_EINVAL, "workspace is NULL, %zu bytes are needed", need);
-  if (bytes < need) return fail(ZERO_EINVAL, "workspace holds %zu bytes, %zu are needed", bytes, need);
-  if (!aligned(ws, 16)) return fail(ZERO_EINVAL, "workspace is not 16-byte aligned");
-  return ok();
-}
-
-// No written range may overlap another written one or a read one.
-zero_status check_disjoint(const std::vector<Range>& writes, const std::vector<Range>& reads) {
-  for (size_t i = 0; i < writes.size(); ++i) {
-    for (size_t j = i + 1; j < writes.size(); ++j)
-      if (overlap(writes[i], writes[j])) return fail(ZERO_EINVAL, "%s overlaps %s", writes[i].what, writes[j].what);
-    for (const Range& r : reads)
-      if (overlap(writes[i], r)) return fail(ZERO_EINVAL, "%s overlaps %s", writes[i].what, r.what);
-  }
-  return ok();
 }
 
 // A dropout's kernel arguments and the factor of the elements it keeps.
@@ -102,8 +69,6 @@ zero_status table_of(zero_plan_t p, int32_t tensor, int64_t hidden, int64_t& row
   if (rows > kMaxRows) return fail(ZERO_EUNSUPPORTED, "%lld rows exceed %lld", (long long)rows, (long long)kMaxRows);
   return ok();
 }
-
-int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
 zero_status check_blocks(int64_t blocks, int threads) {
   if (blocks > most_blocks(threads))
@@ -190,19 +155,6 @@ zero_status check_logits(const void* logits, zero_dtype dt, int64_t n, int64_t v
   if (zero_status st = check_buffer(logits, span, esize(dt), "logits")) return st;
   return check_buffer(labels, n, isize(label_it), "labels");
 }
-
-template <typename F>
-zero_status guarded(const char* name, F f) {
-  try {
-    return f();
-  } catch (const std::bad_alloc&) {
-    return fail(ZERO_ENOMEM, "host allocation failed");
-  } catch (...) {
-    return fail(ZERO_EINVAL, "unexpected failure in %s", name);
-  }
-}
-
-zero_status launched(int err) { return err ? hip_fail(err) : ok(); }
 
 }  // namespace
 
