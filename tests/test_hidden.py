@@ -1,0 +1,212 @@
+"""The operators on the hidden matrices, without a GPU: the refusals of the C
+entries and of the binding (all before anything is launched), and the workspace
+sizes."""
+import ctypes
+import math
+
+import pytest
+
+BASE = 1 << 40        # fake addresses, never dereferenced
+GIB = 1 << 30
+
+
+def P(i):
+    return BASE + i * 64 * GIB
+
+
+@pytest.fixture()
+def Z(zero_lib):
+    return zero_lib
+
+
+@pytest.fixture()
+def plan(Z):
+    return Z.zero_plan(5 + 800 + 100 + 16, 2, [5, 800, 100, 16], 0, 8)     # weight 1: 100 x 8, bias 2
+
+
+def _linear(Z, plan, weight=1, bias=2, width=8, params=P(0), dt=2, x=P(1), n=10, xs=8, act=2, res=P(2), rs=100, pre=P(3),
+            ps=100, y=P(4), ys=100, ws=P(5), ws_bytes=1 << 30):
+    return Z.load().zero_linear(plan.handle if plan else None, weight, bias, width, params, dt, x, n, xs, act, res, rs, pre,
+                                ps, y, ys, ws, ws_bytes, None)
+
+
+def test_linear_refuses(Z, plan):
+    for kw in [dict(weight=4), dict(weight=-1), dict(bias=4), dict(bias=0), dict(width=0), dict(width=7), dict(params=0),
+               dict(params=P(0) + 1), dict(dt=3), dict(dt=-1), dict(x=0), dict(x=P(1) + 1), dict(n=-1), dict(xs=7),
+               dict(act=5), dict(act=-1), dict(rs=99), dict(ps=99), dict(ys=99), dict(y=0), dict(y=P(4) + 1),
+               dict(y=P(1)), dict(y=P(0) + 16), dict(y=P(3)), dict(y=P(2) + 2), dict(pre=P(2)), dict(pre=P(1) + 2),
+               dict(y=P(2), ys=101), dict(ys=1 << 60)]:
+        assert _linear(Z, plan, **kw) == Z.ZERO_EINVAL, kw
+        assert Z.zero_last_error()
+    assert _linear(Z, None) == Z.ZERO_EINVAL
+    assert _linear(Z, plan, dt=0) == Z.ZERO_EUNSUPPORTED
+    assert _linear(Z, plan, n=(1 << 30) + 1) == Z.ZERO_EUNSUPPORTED
+    assert _linear(Z, plan, xs=(1 << 21) + 1) == Z.ZERO_EUNSUPPORTED
+    assert _linear(Z, plan, xs=1 << 60) == Z.ZERO_EUNSUPPORTED
+    wide = Z.zero_plan(1 << 22, 1, [1 << 22], 0, 1)
+    assert _linear(Z, wide, weight=0, bias=-1, width=1 << 22, xs=1 << 22) == Z.ZERO_EUNSUPPORTED
+    assert _linear(Z, plan, n=0) == Z.ZERO_OK                  # nothing to do, nothing launched
+    assert _linear(Z, plan, n=0, x=0, y=0, res=0, pre=0, ws=0, ws_bytes=0) == Z.ZERO_OK
+    # A long inner side is cut into pieces, whose sums need the workspace.
+    deep = Z.zero_plan(64 * 65536, 1, [64 * 65536], 0, 1)
+    need = Z.zero_linear_workspace_bytes(deep, 0, 65536, 3)
+    assert need > 0
+    for kw in [dict(ws=0), dict(ws_bytes=need - 1), dict(ws=P(5) + 8), dict(ws=P(4)), dict(ws=P(1) + 16)]:
+        assert _linear(Z, deep, **{**dict(weight=0, bias=-1, width=65536, n=3, xs=65536, res=0, pre=0, ys=64), **kw}) == Z.ZERO_EINVAL, kw
+
+
+def _input(Z, plan, weight=1, width=8, params=P(0), dt=2, dz=P(1), n=10, zs=100, act=2, pre=P(2), ps=8, add=P(3), as_=8,
+           dx=P(4), xs=8, ws=P(5), ws_bytes=1 << 30):
+    return Z.load().zero_linear_input_grad(plan.handle if plan else None, weight, width, params, dt, dz, n, zs, act, pre, ps,
+                                           add, as_, dx, xs, ws, ws_bytes, None)
+
+
+def test_input_grad_refuses(Z, plan):
+    for kw in [dict(weight=9), dict(width=3), dict(params=0), dict(dt=7), dict(dz=0), dict(dz=P(1) + 1), dict(n=-1),
+               dict(zs=99), dict(act=9), dict(pre=0), dict(act=0), dict(ps=7), dict(as_=7), dict(xs=7), dict(dx=0),
+               dict(dx=P(1)), dict(dx=P(2)), dict(dx=P(3) + 2), dict(dx=P(3), xs=9), dict(dx=P(0))]:
+        assert _input(Z, plan, **kw) == Z.ZERO_EINVAL, kw
+    assert _input(Z, None) == Z.ZERO_EINVAL
+    assert _input(Z, plan, dt=0) == Z.ZERO_EUNSUPPORTED
+    assert _input(Z, plan, zs=(1 << 21) + 1) == Z.ZERO_EUNSUPPORTED
+    many = Z.zero_plan(1 << 22, 1, [1 << 22], 0, 1)
+    assert _input(Z, many, weight=0, width=1, zs=1 << 22, ps=1, as_=1, xs=1) == Z.ZERO_EUNSUPPORTED
+    assert _input(Z, plan, n=0, dz=0, pre=0, dx=0, add=0, ws=0, ws_bytes=0) == Z.ZERO_OK
+
+
+def _weight(Z, plan, weight=1, bias=2, width=8, dz=P(0), zs=100, x=P(1), xs=8, dt=2, n=10, scale=1.0, dst=P(2), ddt=2,
+            rank=-1, acc=0, ws=P(3), ws_bytes=1 << 30):
+    return Z.load().zero_linear_weight_grad(plan.handle if plan else None, weight, bias, width, dz, zs, x, xs, dt, n, scale,
+                                            dst, ddt, rank, acc, ws, ws_bytes, None)
+
+
+def test_weight_grad_refuses(Z, plan):
+    for kw in [dict(weight=7), dict(width=3, xs=3), dict(bias=3), dict(bias=1), dict(dz=0), dict(x=0), dict(zs=99), dict(xs=7), dict(dt=9),
+               dict(ddt=9), dict(n=-1), dict(scale=math.inf), dict(scale=1e39), dict(scale=math.nan), dict(dst=0),
+               dict(dst=P(2) + 1), dict(rank=2), dict(acc=2), dict(ws=0), dict(ws_bytes=4), dict(ws=P(3) + 8),
+               dict(dst=P(0) + 2), dict(dst=P(1)), dict(ws=P(2)), dict(ws=P(0) + 16)]:
+        assert _weight(Z, plan, **kw) == Z.ZERO_EINVAL, kw
+    assert _weight(Z, None) == Z.ZERO_EINVAL
+    assert _weight(Z, plan, dt=0) == Z.ZERO_EUNSUPPORTED
+    square = Z.zero_plan(32, 1, [16, 16], 0, 1)
+    assert _weight(Z, square, weight=0, bias=0, width=1, zs=16, xs=1) == Z.ZERO_EINVAL      # the same tensor
+    assert _weight(Z, plan, n=0, acc=1, dz=0, x=0, ws=0, ws_bytes=0) == Z.ZERO_OK
+
+
+def test_activation_grad_refuses(Z):
+    def call(dy=P(0), pre=P(1), dz=P(2), n=10, dt=2, act=2):
+        return Z.load().zero_activation_grad(dy, pre, dz, n, dt, act, None)
+    for kw in [dict(dy=0), dict(pre=0), dict(dz=0), dict(n=-1), dict(dt=5), dict(act=5), dict(dy=P(0) + 1),
+               dict(dz=P(1)), dict(dz=P(0) + 2), dict(dz=P(1) + 2)]:
+        assert call(**kw) == Z.ZERO_EINVAL, kw
+    assert call(dt=0) == Z.ZERO_EUNSUPPORTED
+    assert call(n=0, dy=0, pre=0, dz=0) == Z.ZERO_OK
+
+
+def _ortho(Z, plan, ms, poly=None, src=P(0), sdt=2, dst=P(1), ddt=2, ws=P(2), ws_bytes=1 << 34):
+    arr = (Z._Matrix * max(1, len(ms)))(*[Z._Matrix(*m) for m in ms])
+    q = None if poly is None else ctypes.byref(Z._NewtonSchulz(*poly))
+    return Z.load().zero_orthogonalize(plan.handle if plan else None, arr, len(ms), q, src, sdt, dst, ddt, ws, ws_bytes, None)
+
+
+def test_orthogonalize_refuses(Z, plan):
+    good = [(1, 100, 8, 1.0)]
+    ok = (5, 3.4, -4.8, 2.0, 1e-7)
+    for kw in [dict(ms=[(4, 2, 2, 1.0)]), dict(ms=[(-1, 2, 2, 1.0)]), dict(ms=good + good), dict(ms=[(1, 0, 8, 1.0)]),
+               dict(ms=[(1, 8, -1, 1.0)]), dict(ms=[(1, 7, 8, 1.0)]), dict(ms=[(1, 100, 8, 1e39)]),
+               dict(ms=[(1, 100, 8, math.nan)]), dict(poly=(0,) + ok[1:]), dict(poly=(33,) + ok[1:]),
+               dict(poly=(5, math.nan, 1.0, 1.0, 1e-7)), dict(poly=(5, 1.0, 1001.0, 1.0, 1e-7)),
+               dict(poly=ok[:4] + (0.0,)), dict(poly=ok[:4] + (math.nan,)), dict(poly=ok[:4] + (1e31,)),
+               dict(src=0), dict(dst=0), dict(src=P(0) + 1), dict(dst=P(1) + 1), dict(sdt=8), dict(ddt=8), dict(ws=0),
+               dict(ws_bytes=64), dict(ws=P(2) + 64), dict(ws=P(0)), dict(ws=P(1)), dict(dst=P(0) + 16),
+               dict(dst=P(0), ddt=1)]:
+        assert _ortho(Z, plan, **{**dict(ms=good), **kw}) == Z.ZERO_EINVAL, kw
+    assert _ortho(Z, None, good) == Z.ZERO_EINVAL
+    assert _ortho(Z, plan, good, sdt=0) == Z.ZERO_EUNSUPPORTED
+    assert _ortho(Z, plan, good, ddt=0) == Z.ZERO_EUNSUPPORTED
+    long = Z.zero_plan(1 << 22, 1, [1 << 22], 0, 1)
+    assert _ortho(Z, long, [(0, 1 << 21, 2, 1.0)]) == Z.ZERO_EUNSUPPORTED
+    assert _ortho(Z, plan, [], ws=0, ws_bytes=0) == Z.ZERO_OK
+    assert Z.load().zero_orthogonalize(plan.handle, None, 1, None, P(0), 2, P(1), 2, P(2), 1 << 30, None) == Z.ZERO_EINVAL
+    assert Z.load().zero_orthogonalize(plan.handle, None, -1, None, P(0), 2, P(1), 2, P(2), 1 << 30, None) == Z.ZERO_EINVAL
+
+
+def test_muon_refuses(Z):
+    p = Z.zero_plan(1000, 2, [1000], 0, 8)
+    L = Z.load()
+    ptrs = (ctypes.c_void_p * 2)(P(0), P(1))
+
+    def src(dtype=2, n=2, a=None):
+        return ctypes.byref(Z._GradSrc(dtype, n, ctypes.cast(ptrs if a is None else a, ctypes.POINTER(ctypes.c_void_p)), None))
+
+    def momentum(rank=0, hyper=(0.02, 0.95, 0.1, 0.5, 1), slices=src(), reduced=None, m=P(2), u=P(3), dt=2, full=1, h=True):
+        return L.zero_muon_momentum(p.handle, rank, ctypes.byref(Z._MuonHyper(*hyper)) if h else None, slices, reduced, m, u, dt,
+                                    full, None)
+
+    def apply(rank=0, hyper=(0.02, 0.95, 0.1, 0.5, 1), o=P(0), odt=2, ofull=1, w=P(1), d=P(2), dt=2, full=1, h=True):
+        return L.zero_muon_apply(p.handle, rank, ctypes.byref(Z._MuonHyper(*hyper)) if h else None, o, odt, ofull, w, d, dt, full,
+                                 None)
+
+    hypers = [dict(h=False), dict(hyper=(math.nan, 0.9, 0, 1, 0)), dict(hyper=(0.1, math.inf, 0, 1, 0)),
+              dict(hyper=(0.1, 0.9, 1e39, 1, 0)), dict(hyper=(0.1, 0.9, 0, math.nan, 0)), dict(hyper=(0.1, 0.9, 0, 1, 2)),
+              dict(hyper=(1e38, 0.9, 1e38, 1, 0)), dict(rank=-1), dict(rank=2)]
+    for kw in hypers + [dict(slices=None), dict(reduced=P(4)), dict(slices=src(n=3)), dict(m=0), dict(u=0), dict(m=P(2) + 2),
+                        dict(u=P(3) + 1), dict(u=P(2)), dict(m=P(0)), dict(u=P(1) + 16),
+                        dict(slices=None, reduced=P(4) + 2), dict(slices=None, reduced=P(2))]:
+        assert momentum(**kw) == Z.ZERO_EINVAL, kw
+    for kw in hypers + [dict(o=0), dict(o=P(0) + 1), dict(w=0), dict(w=P(1) + 2), dict(d=0), dict(d=P(2) + 1), dict(d=P(1)),
+                        dict(w=P(0)), dict(d=P(0) + 16)]:
+        assert apply(**kw) == Z.ZERO_EINVAL, kw
+    assert momentum(dt=0) == Z.ZERO_EUNSUPPORTED
+    assert momentum(slices=src(dtype=0)) == Z.ZERO_EUNSUPPORTED
+    assert apply(dt=0) == Z.ZERO_EUNSUPPORTED
+    assert apply(odt=0) == Z.ZERO_EUNSUPPORTED
+    assert L.zero_muon_momentum(None, 0, None, None, None, None, None, 2, 0, None) == Z.ZERO_EINVAL
+    many = Z.zero_plan(1000, 129, [1000], 0, 1)
+    a = (ctypes.c_void_p * 129)(*[P(0)] * 129)
+    assert L.zero_muon_momentum(many.handle, 0, ctypes.byref(Z._MuonHyper(0.1, 0.9, 0, 1, 0)), src(n=129, a=a), None, P(2), P(3), 2,
+                                0, None) == Z.ZERO_EUNSUPPORTED
+
+
+def test_workspaces(Z):
+    p = Z.zero_plan(768 * 768 + 768, 8, [768 * 768, 768], 0, 64)
+    assert Z.zero_linear_workspace_bytes(p, 0, 768, 0) == 0
+    assert Z.zero_linear_workspace_bytes(p, 0, 768, -1) == 0
+    assert Z.zero_linear_workspace_bytes(p, 0, 7, 10) == 0                  # refused by the call too
+    assert Z.zero_linear_input_grad_workspace_bytes(p, 5, 768, 10) == 0
+    assert Z.zero_linear_weight_grad_workspace_bytes(p, 0, 768, 0) == 0
+    assert Z.zero_linear_weight_grad_workspace_bytes(p, 0, 768, 8192, 8) == 0
+    full, part = (Z.zero_linear_weight_grad_workspace_bytes(p, 0, 768, 8192, r) for r in (-1, 3))
+    assert full > part > 0
+    m = Z.Matrices([(0, 768, 768, 1.0)])
+    need = Z.zero_orthogonalize_workspace_bytes(p, m)
+    assert need >= 768 * 768 * 12 and need % 256 == 0
+    assert Z.zero_orthogonalize_workspace_bytes(p, Z.Matrices([])) == 0
+    assert Z.zero_orthogonalize_workspace_bytes(p, Z.Matrices([(0, 7, 768, 1.0)])) == 0
+    # Matrices one after another in a tensor take what single ones of that shape take.
+    stack = Z.zero_plan(48 * 64 * 64, 1, [24 * 64 * 64] * 2, 0, 64)
+    lone = Z.zero_plan(48 * 64 * 64, 1, [64 * 64] * 48, 0, 64)
+    assert (Z.zero_orthogonalize_workspace_bytes(stack, Z.Matrices([(0, 64, 64, 1.0), (1, 64, 64, 1.0)]))
+            == Z.zero_orthogonalize_workspace_bytes(lone, Z.Matrices([(t, 64, 64, 1.0) for t in range(48)])))
+
+
+def test_binding_refuses(Z):
+    import torch
+    p = Z.zero_plan(800 + 100, 1, [800, 100], 0, 1)
+    cpu = torch.zeros(900, dtype=torch.bfloat16)
+    with pytest.raises(ValueError):
+        Z.zero_linear(p, 0, 8, cpu, Z.ZERO_BF16, P(1), P(2), n=4)            # not on a GPU
+    with pytest.raises(ValueError):
+        Z.zero_linear(p, 0, 7, P(0), Z.ZERO_BF16, P(1), P(2), n=4)
+    with pytest.raises(ValueError):
+        Z.zero_linear(p, 0, 8, P(0), Z.ZERO_BF16, P(1), P(2))                # an address: n is needed
+    with pytest.raises(ValueError):
+        Z.zero_linear_input_grad(p, 3, 8, P(0), Z.ZERO_BF16, P(1), P(2), n=4)
+    with pytest.raises(TypeError):
+        Z.zero_orthogonalize(p, [(0, 100, 8, 1.0)], P(0), Z.ZERO_BF16, P(1), Z.ZERO_BF16)
+    with pytest.raises(TypeError):
+        Z.zero_muon_apply(p, 0, None, P(0), Z.ZERO_BF16, True, P(1), P(2), Z.ZERO_BF16, True)
+    with pytest.raises(ValueError):
+        Z.zero_muon_momentum(p, 0, Z.MuonHyper(0.1), None, P(0), P(1), P(2), Z.ZERO_F32, True)
+    with pytest.raises(Z.ZeroError):
+        Z.zero_linear(p, 0, 8, P(0), Z.ZERO_F32, P(1), P(2), n=4, stream=0)

@@ -80,7 +80,7 @@ enum OrthoEpi : int { kGram = 0, kPoly = 1, kNext = 2 };
 struct OrthoArgs {
   Product p;              // of one matrix; part: fp32[batch][splits][m][n_pad]
   int64_t za, zb, zout, zadd;
-  const float* factor;    // fp32[batch]: what the stored X is to be multiplied by
+  const float* factor;    // fp32[batch][2]: what the first X is to be multiplied by, and whether to shift
   void* out;              // 16-bit result in the workspace, rows of ldo
   float* out32;           // kNext: X in fp32, or NULL after the last step
   const void* add;        // kPoly: A - shift I; kNext: X
@@ -89,7 +89,8 @@ struct OrthoArgs {
   int32_t upper;          // the result is symmetric: tiles on and above the diagonal only
   int32_t first;          // X as loaded: the factor applies, and add is 16-bit
   int32_t last, dst_dt;   // the result goes to dst
-  float c0, c1, shift;    // kGram: factor^2 sum - shift I; kPoly: c0 add + c1 sum; kNext: factor (c0 add + sum)
+  float a, b, c, shift;   // d = shift or 0: kGram: factor^2 sum - d I; kPoly: (b + 2 c d) add + c sum;
+                          // kNext: factor ((a + b d + c d^2) add + sum)
   int32_t rows, cols;     // of dst
   void* dst;              // flat buffer
   float scale[kMaxBatch];

@@ -264,7 +264,7 @@ OrthoSpace ortho_space(int64_t rows, int64_t cols, int64_t batch) {
     return here;
   };
   s.sums = take(batch * kNormBlocks * 8);
-  s.factor = take(batch * 4);
+  s.factor = take(batch * 8);
   s.x0 = take(batch * s.zx * 2);
   s.x1 = take(batch * s.zx * 2);
   s.x32 = take(batch * s.zx * 4);
@@ -372,12 +372,15 @@ zero_status ortho_batch(const Group& g, const OrthoSpace& s, int64_t first, int6
     a.scale[i] = g.scale[first + i];
     a.dst_off[i] = g.off[first + i];
   }
+  a.a = (float)poly.a;
+  a.b = (float)poly.b;
+  a.c = (float)poly.c;
   char* x = ws + s.x0;
   char* next = ws + s.x1;
   const int64_t wide = std::max(s.rows_pad, s.ldx);
   for (int step = 0; step < poly.steps; ++step) {
     a.first = step == 0;
-    const double d = step >= kShiftFrom ? (double)kShift : 0.0;
+    a.shift = step >= kShiftFrom ? kShift : 0.0f;
     // A - d I
     a.epi = kGram;
     a.last = 0;
@@ -387,7 +390,6 @@ zero_status ortho_batch(const Group& g, const OrthoSpace& s, int64_t first, int6
     a.out = ws + s.gram;
     a.ldo = s.ldn;
     a.zout = s.zn;
-    a.shift = (float)d;
     const int form = tall ? 1 : 0;
     if (zero_status st = run_ortho(a, form, form, s.side, s.side, wide, s.c[kGram], ws + s.part, stream)) return st;
     // B
@@ -399,8 +401,6 @@ zero_status ortho_batch(const Group& g, const OrthoSpace& s, int64_t first, int6
     a.ldadd = s.ldn;
     a.zadd = s.zn;
     a.out = ws + s.poly;
-    a.c0 = (float)(poly.b + 2.0 * poly.c * d);
-    a.c1 = (float)poly.c;
     if (zero_status st = run_ortho(a, 0, 0, s.side, s.side, s.side, s.c[kPoly], ws + s.part, stream)) return st;
     // a X + B X, or a X + X B
     a.epi = kNext;
@@ -418,7 +418,6 @@ zero_status ortho_batch(const Group& g, const OrthoSpace& s, int64_t first, int6
     a.out = next;
     a.ldo = s.ldx;
     a.zout = s.zx;
-    a.c0 = (float)(poly.a + poly.b * d + poly.c * d * d);
     if (zero_status st = run_ortho(a, 0, tall ? 0 : 1, s.rows_pad, s.ldx, s.side, s.c[kNext], ws + s.part, stream)) return st;
     std::swap(x, next);
   }

@@ -17,9 +17,11 @@
 // lie around 1, and A - I/2 is stored in place of A, which halves its largest
 // entries and their rounding; the polynomial is rewritten for it:
 //   b A + c A^2 = (b d + c d^2) I + (b + 2 c d) D + c D^2,  D = A - d I,
-// and the multiple of I joins a.  The first X is the gradient times a power of
-// two, which rounds nothing that fp16 holds; the rest of 1 / |G| enters as a
-// factor of the first step's results.
+// and the multiple of I joins a.  (Where |G| is below eps, X stays small for more
+// steps, and fp16 may lose it: there d is 0, so that B X stays small beside a X.)
+// The first X is the gradient times a power of two, which rounds nothing that
+// fp16 holds; the rest of 1 / (|G| + eps) enters as a factor of the first step's
+// results.
 #include "zero_hidden_dev.h"
 
 #pragma clang fp contract(off)
@@ -68,11 +70,14 @@ __global__ void __launch_bounds__(kLoadThreads) ortho_load_kernel(const OrthoLoa
   const int z = (int)(blockIdx.x / blocks);
   double s = 0.0;
   for (int i = 0; i < a.norm_blocks; ++i) s += a.sums[(int64_t)z * a.norm_blocks + i];
-  const double d = __builtin_sqrt(s) + a.eps;
+  const double norm = __builtin_sqrt(s), d = norm + a.eps;
   const bool good = d < __builtin_inf();                          // not NaN either
-  const int e = good ? 6 - (ilogb(d) + 1) : 0;                   // d 2^e in [32, 64)
+  const int e = good && norm > 0.0 ? 5 - ilogb(norm) : 0;        // |G| 2^e in [32, 64)
   const int64_t u = (blockIdx.x - z * blocks) * kLoadThreads + threadIdx.x;
-  if (u == 0) a.factor[z] = good ? (float)(1.0 / ldexp(d, e)) : __builtin_nanf("");
+  if (u == 0) {
+    a.factor[2 * z] = good ? (float)(1.0 / ldexp(d, e)) : __builtin_nanf("");
+    a.factor[2 * z + 1] = norm > a.eps ? 1.0f : 0.0f;
+  }
   if (u >= per) return;
   const int row = (int)(u / upr), col = (int)(u - (int64_t)row * upr) * 8;
   float x[8];
@@ -83,19 +88,23 @@ __global__ void __launch_bounds__(kLoadThreads) ortho_load_kernel(const OrthoLoa
   store_row<_Float16, 8>(a.x, z * a.zx + (int64_t)row * a.ld + col, 8, x);
 }
 
+__device__ __forceinline__ float factor_of(const OrthoArgs& a, int z) { return a.first ? a.factor[2 * z] : 1.0f; }
+__device__ __forceinline__ float shift_of(const OrthoArgs& a, int z) { return a.shift * a.factor[2 * z + 1]; }
+
 // V sums of one row through the epilogue.
 template <int V>
 __device__ __forceinline__ void finish(const OrthoArgs& a, int z, int row, int col, const float (&acc)[V]) {
   const int have = a.p.n - col;
   float v[V], x[V];
   if (a.epi == kGram) {
-    const float f = a.first ? a.factor[z] : 1.0f, f2 = f * f;
+    const float f = factor_of(a, z), f2 = f * f, d = shift_of(a, z);
 #pragma unroll
-    for (int i = 0; i < V; ++i) v[i] = __builtin_fmaf(f2, acc[i], row == col + i ? -a.shift : 0.0f);
+    for (int i = 0; i < V; ++i) v[i] = __builtin_fmaf(f2, acc[i], row == col + i ? -d : 0.0f);
   } else if (a.epi == kPoly) {
     load_row<_Float16, V>(a.add, z * a.zadd + (int64_t)row * a.ldadd + col, have, x);
+    const float b = __builtin_fmaf(2.0f * a.c, shift_of(a, z), a.b);
 #pragma unroll
-    for (int i = 0; i < V; ++i) v[i] = __builtin_fmaf(a.c1, acc[i], a.c0 * x[i]);
+    for (int i = 0; i < V; ++i) v[i] = __builtin_fmaf(a.c, acc[i], b * x[i]);
   } else {
     const int64_t e = z * a.zadd + (int64_t)row * a.ldadd + col;
     if (a.first) {
@@ -109,9 +118,10 @@ __device__ __forceinline__ void finish(const OrthoArgs& a, int z, int row, int c
         for (int k = 0; k < 4; ++k) x[i + k] = t[k];
       }
     }
-    const float f = a.first ? a.factor[z] : 1.0f;
+    const float f = factor_of(a, z), d = shift_of(a, z);
+    const float c0 = __builtin_fmaf(__builtin_fmaf(a.c, d, a.b), d, a.a);
 #pragma unroll
-    for (int i = 0; i < V; ++i) v[i] = f * __builtin_fmaf(a.c0, x[i], acc[i]);
+    for (int i = 0; i < V; ++i) v[i] = f * __builtin_fmaf(c0, x[i], acc[i]);
     if (a.last) {
       if (row >= a.rows || col >= a.cols) return;
       const int left = a.cols - col;
@@ -133,12 +143,12 @@ __device__ __forceinline__ void finish(const OrthoArgs& a, int z, int row, int c
 
 template <int V>
 __device__ __forceinline__ void mirror(const OrthoArgs& a, int z, int row, int col, const float (&acc)[V]) {
-  const float f = a.first ? a.factor[z] : 1.0f, f2 = f * f;
+  const float f = factor_of(a, z), f2 = f * f, b = __builtin_fmaf(2.0f * a.c, shift_of(a, z), a.b);
   float x[V];
   if (a.epi == kPoly) load_row<_Float16, V>(a.add, z * a.zadd + (int64_t)row * a.ldadd + col, a.p.n - col, x);
 #pragma unroll
   for (int i = 0; i < V; ++i) {
-    const float v = a.epi == kGram ? f2 * acc[i] : __builtin_fmaf(a.c1, acc[i], a.c0 * x[i]);
+    const float v = a.epi == kGram ? f2 * acc[i] : __builtin_fmaf(a.c, acc[i], b * x[i]);
     if (col + i < a.p.n) ((AS1 _Float16*)a.out)[z * a.zout + (int64_t)(col + i) * a.ldo + row] = (_Float16)v;
   }
 }
