@@ -100,6 +100,7 @@ struct Panel {
 
   // Bytes of this stage that may be read: what lies behind reads as zero.
   __device__ __forceinline__ uint32_t records(int k_left) const {
+    if (k_left <= 0) return 0;
     if constexpr (FORM == kFormK) return (uint32_t)span;
     const int kr = k_left < kBK ? k_left : kBK;
     return (uint32_t)(kr - 1) * ld + (uint32_t)span;
@@ -110,20 +111,24 @@ struct Panel {
     if constexpr (FORM == kFormK) span -= step;
   }
 
-  // Starts the loads of one stage straight into LDS (rows 16-byte aligned and
-  // a whole number of 16-byte units long).
-  __device__ __forceinline__ void load_direct(ZK_LDS char* lds, int wave, int tid, int k_left) {
-    const __amdgpu_buffer_rsrc_t rs = __builtin_amdgcn_make_buffer_rsrc((void*)base, 0, records(k_left), 0x00020000);
-    const bool tail = FORM == kFormK && k_left < kBK;
-#pragma unroll
-    for (int i = 0; i < kLoads; ++i) {
-      uint32_t off = voff[i];
-      if (tail) {   // units behind the last k would hold the next row's
-        const int g = i * NT + tid, unit = (g & 7) ^ swz_k(g >> 3);
-        if (unit * 8 >= k_left) off = 0x7ffffff0u;
-      }
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (ZK_LDS void*)(lds + (i * NT + wave * 64) * 16), 16, (int)off, 0, 0, 0);
+  // Starts load i of a stage straight into LDS (rows 16-byte aligned and a whole
+  // number of 16-byte units long).  Behind the last k it reads nothing and writes
+  // zeros.
+  __device__ __forceinline__ u32x4 source(int k_left) const {
+    const uint64_t p = (uint64_t)(uintptr_t)base;
+    return u32x4{(uint32_t)__builtin_amdgcn_readfirstlane((uint32_t)p), (uint32_t)__builtin_amdgcn_readfirstlane((uint32_t)(p >> 32)),
+                 (uint32_t)__builtin_amdgcn_readfirstlane(records(k_left)), 0x00020000u};
+  }
+  __device__ __forceinline__ void load_one(u32x4 rs, uint32_t lds, int i, int wave, int tid, int k_left) const {
+    uint32_t off = voff[i];
+    if (FORM == kFormK && k_left < kBK) {   // units behind the last k would hold the next row's
+      const int g = i * NT + tid, unit = (g & 7) ^ swz_k(g >> 3);
+      if (unit * 8 >= k_left) off = 0x7ffffff0u;
     }
+    // In assembly, since the compiler would have every later read of LDS wait for it.
+    // It has no result in registers; arrive() waits for what it puts into LDS.
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds"
+                 ::"s"(lds + (uint32_t)(i * NT + wave * 64) * 16u), "v"(off), "s"(rs));
   }
 
   // Any alignment: through registers.
@@ -229,24 +234,73 @@ struct Core {
   typedef Panel<AF, BM, NT> PA;
   typedef Panel<BF, BN, NT> PB;
   static constexpr int kStage = PA::kBytes + PB::kBytes;
+  static constexpr int kLds = 2 * kStage;
 
   f32x4 acc[TM][TN];
 
-  __device__ __forceinline__ void stage_compute(const ZK_LDS char* lds, int wm, int wn, int lane) {
-    const ZK_LDS char* la = lds;
-    const ZK_LDS char* lb = lds + PA::kBytes;
+  struct Frags { s16x8 a[TM], b[TN]; };
+
+  __device__ __forceinline__ static void read(Frags& f, const ZK_LDS char* lds, int s, int wm, int wn, int lane) {
 #pragma unroll
-    for (int s = 0; s < kBK / 32; ++s) {
-      s16x8 fa[TM], fb[TN];
+    for (int j = 0; j < TN; ++j) f.b[j] = Frag<BF, BN, kPerm>::read(lds + PA::kBytes, wn * TN * 16, j, s, lane);
 #pragma unroll
-      for (int j = 0; j < TN; ++j) fb[j] = Frag<BF, BN, kPerm>::read(lb, wn * TN * 16, j, s, lane);
+    for (int i = 0; i < TM; ++i) f.a[i] = Frag<AF, BM, false>::read(lds, wm * TM * 16, i, s, lane);
+  }
+  __device__ __forceinline__ void multiply(const Frags& f) {
 #pragma unroll
-      for (int i = 0; i < TM; ++i) fa[i] = Frag<AF, BM, false>::read(la, wm * TM * 16, i, s, lane);
+    for (int i = 0; i < TM; ++i)
 #pragma unroll
-      for (int i = 0; i < TM; ++i)
+      for (int j = 0; j < TN; ++j) acc[i][j] = mfma<T>(f.b[j], f.a[i], acc[i][j]);
+  }
+  static constexpr int kReads = TM * (AF == kFormK ? 1 : 2) + TN * (BF == kFormK ? 1 : 2);
+  static constexpr int kProducts = TM * TN;
+
+  static constexpr int kL = PA::kLoads + PB::kLoads, kF = TM + TN;
+
+  __device__ __forceinline__ static void read_one(Frags& f, const ZK_LDS char* lds, int i, int s, int wm, int wn, int lane) {
+    if (i < TN) f.b[i] = Frag<BF, BN, kPerm>::read(lds + PA::kBytes, wn * TN * 16, i, s, lane);
+    else f.a[i - TN] = Frag<AF, BM, false>::read(lds, wm * TM * 16, i - TN, s, lane);
+  }
+
+  // The products of `now`; between their rows the reads of `next`, and, with LOAD,
+  // the loads of a stage.
+  template <bool LOAD>
+  __device__ __forceinline__ void step(const Frags& now, Frags& next, const ZK_LDS char* from, int s, const PA& pa, const PB& pb,
+                                       uint32_t to, int wave, int tid, int left, int wm, int wn, int lane) {
+    const u32x4 ra = pa.source(left), rb = pb.source(left);
 #pragma unroll
-        for (int j = 0; j < TN; ++j) acc[i][j] = mfma<T>(fb[j], fa[i], acc[i][j]);
+    for (int i = 0; i < TM; ++i) {
+      if constexpr (LOAD) {
+#pragma unroll
+        for (int k = 0; k < kL; ++k) {
+          if (k < i * kL / TM || k >= (i + 1) * kL / TM) continue;
+          if (k < PA::kLoads) pa.load_one(ra, to, k, wave, tid, left);
+          else pb.load_one(rb, to + PA::kBytes, k - PA::kLoads, wave, tid, left);
+        }
+      }
+#pragma unroll
+      for (int k = 0; k < kF; ++k)
+        if (k >= i * kF / TM && k < (i + 1) * kF / TM) read_one(next, from, k, s, wm, wn, lane);
+#pragma unroll
+      for (int j = 0; j < TN; ++j) acc[i][j] = mfma<T>(now.b[j], now.a[i], acc[i][j]);
+      __builtin_amdgcn_sched_barrier(0);
     }
+  }
+
+  __device__ __forceinline__ static void load(const PA& pa, const PB& pb, uint32_t lds, int wave, int tid, int left) {
+    const u32x4 ra = pa.source(left), rb = pb.source(left);
+#pragma unroll
+    for (int i = 0; i < PA::kLoads; ++i) pa.load_one(ra, lds, i, wave, tid, left);
+#pragma unroll
+    for (int i = 0; i < PB::kLoads; ++i) pb.load_one(rb, lds + PA::kBytes, i, wave, tid, left);
+  }
+
+  // All of this wave's loads have arrived and its reads of LDS are done; then all
+  // waves' have.
+  __device__ __forceinline__ static void arrive() {
+    __builtin_amdgcn_sched_barrier(0);
+    asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
+    __builtin_amdgcn_sched_barrier(0);
   }
 
   // Sums k0 .. k_end of the tile whose first rows are m0 and n0.
@@ -266,21 +320,32 @@ struct Core {
     int left = k_end - k0;
     if (left <= 0) return;
     if constexpr (DIRECT) {
-      pa.load_direct(lds, wave, tid, left);
-      pb.load_direct(lds + PA::kBytes, wave, tid, left);
+      // Two stages in LDS.  While the products of one half of a stage run, the
+      // fragments of the next half are read; in the middle of a stage every wave
+      // has read all of it and the next has arrived, so that one barrier a stage is
+      // enough and the matrix units have work on both sides of it.
+      Frags f0, f1;
+      const uint32_t at = (uint32_t)(uintptr_t)lds;      // LDS address
+      load(pa, pb, at, wave, tid, left);
+      arrive();
+      pa.advance();
+      pb.advance();
+      load(pa, pb, at + kStage, wave, tid, left - kBK);
+      read(f0, lds, 0, wm, wn, lane);
       int cur = 0;
-      for (; left > 0; left -= kBK) {
-        __syncthreads();      // this stage has arrived, and the other one is no longer read
-        if (left > kBK) {
-          pa.advance();
-          pb.advance();
-          ZK_LDS char* next = lds + (cur ^ 1) * kStage;
-          pa.load_direct(next, wave, tid, left - kBK);
-          pb.load_direct(next + PA::kBytes, wave, tid, left - kBK);
-        }
-        stage_compute(lds + cur * kStage, wm, wn, lane);
+      for (; left > kBK; left -= kBK) {
+        const int here = cur * kStage;
         cur ^= 1;
+        step<false>(f0, f1, lds + here, 1, pa, pb, 0, wave, tid, 0, wm, wn, lane);
+        arrive();
+        pa.advance();
+        pb.advance();
+        step<true>(f1, f0, lds + cur * kStage, 0, pa, pb, at + here, wave, tid, left - 2 * kBK, wm, wn, lane);
       }
+      read(f1, lds + cur * kStage, 1, wm, wn, lane);
+      multiply(f0);
+      multiply(f1);
+      asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
     } else {
       u32x4 ra[PA::kLoads], rb[PB::kLoads];
       pa.load_regs(ra, tid, left);
@@ -297,7 +362,11 @@ struct Core {
           pa.load_regs(ra, tid, left - kBK);
           pb.load_regs(rb, tid, left - kBK);
         }
-        stage_compute(here, wm, wn, lane);
+        Frags f0, f1;
+        read(f0, here, 0, wm, wn, lane);
+        read(f1, here, 1, wm, wn, lane);
+        multiply(f0);
+        multiply(f1);
         cur ^= 1;
       }
     }

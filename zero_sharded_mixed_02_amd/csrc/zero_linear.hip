@@ -227,7 +227,7 @@ __global__ void __launch_bounds__(kActThreads) act_grad_kernel(const ActGradArgs
 template <typename T, int EPI, int TILE, bool DIRECT>
 int go_linear(const LinearArgs& a, void* stream) {
   return launch(&linear_kernel<T, EPI, TILE, DIRECT>, a, (int64_t)a.p.tiles * a.p.splits, kTileThreads[TILE],
-                2 * CoreOf<T, kFormK, EPI == 0 ? kFormK : kFormM, TILE, DIRECT>::kStage, stream);
+                CoreOf<T, kFormK, EPI == 0 ? kFormK : kFormM, TILE, DIRECT>::kLds, stream);
 }
 template <typename T, int EPI, int TILE>
 int go_linear(const LinearArgs& a, bool direct, void* stream) {
@@ -243,7 +243,7 @@ int go_linear(const LinearArgs& a, int tile, bool direct, void* stream) {
 template <typename T, int TILE, bool DIRECT>
 int go_weight(const WeightGradArgs& a, int64_t blocks, void* stream) {
   constexpr int bias = 8 * kBiasCols * 4;
-  constexpr int lds = 2 * CoreOf<T, kFormM, kFormM, TILE, DIRECT>::kStage;
+  constexpr int lds = CoreOf<T, kFormM, kFormM, TILE, DIRECT>::kLds;
   return launch(&weight_grad_kernel<T, TILE, DIRECT>, a, blocks, kTileThreads[TILE], lds > bias ? lds : bias, stream);
 }
 template <typename T, int TILE>

@@ -195,10 +195,10 @@ __global__ void __launch_bounds__(kJoinThreads) ortho_join_kernel(const OrthoArg
 template <int AF, int BF>
 int go(const OrthoArgs& a, int tile, int64_t blocks, void* stream) {
   if (tile == kTile256)
-    return launch(&ortho_kernel<AF, BF, kTile256>, a, blocks, 512, 2 * CoreOf<_Float16, AF, BF, kTile256, true>::kStage, stream);
+    return launch(&ortho_kernel<AF, BF, kTile256>, a, blocks, 512, CoreOf<_Float16, AF, BF, kTile256, true>::kLds, stream);
   if (tile == kTile128)
-    return launch(&ortho_kernel<AF, BF, kTile128>, a, blocks, 256, 2 * CoreOf<_Float16, AF, BF, kTile128, true>::kStage, stream);
-  return launch(&ortho_kernel<AF, BF, kTile64>, a, blocks, 256, 2 * CoreOf<_Float16, AF, BF, kTile64, true>::kStage, stream);
+    return launch(&ortho_kernel<AF, BF, kTile128>, a, blocks, 256, CoreOf<_Float16, AF, BF, kTile128, true>::kLds, stream);
+  return launch(&ortho_kernel<AF, BF, kTile64>, a, blocks, 256, CoreOf<_Float16, AF, BF, kTile64, true>::kLds, stream);
 }
 
 }  // namespace
