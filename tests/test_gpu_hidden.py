@@ -108,6 +108,11 @@ LINEAR = [
     (2048, 768, 768, 0, F16, NONE, True, False, False, 0),
     (1025, 328, 50257, 0, BF16, NONE, False, False, False, 0),     # a tied table's logits, odd rows
     (2049, 2048, 2056, 0, BF16, SILU, True, True, False, 16),      # the largest tiles, ragged
+    (100, 130, 134, 2, BF16, NONE, True, False, False, 2),         # rows 4-byte aligned, k inside a unit
+    (600, 30, 1030, 0, F16, GELU, True, True, True, 0),            # k shorter than a stage
+    (2050, 1090, 1042, 4, BF16, RELU, True, False, False, 6),
+    (1500, 1201, 1301, 3, F16, NONE, True, False, False, 0),       # odd rows in the larger tiles
+    (9, 3, 2, 0, BF16, NONE, False, False, False, 0),              # rows shorter than a unit
 ]
 
 
@@ -161,6 +166,10 @@ GRAD = [
     (5, 33, 20001, 1, F16, GELU_TANH, True, 2),
     (129, 328, 50257, 0, BF16, NONE, False, 0),       # back from a tied table's logits
     (2049, 2056, 2048, 0, BF16, SILU, True, 16),
+    (100, 134, 130, 2, BF16, NONE, False, 2),
+    (600, 1030, 30, 0, F16, GELU, True, 0),
+    (1500, 1301, 1201, 3, F16, NONE, True, 0),
+    (2050, 1042, 1090, 4, BF16, RELU, True, 6),
 ]
 
 
@@ -208,6 +217,12 @@ WEIGHT = [
     (2048, 768, 768, 64, BF16, BF16, 8, 0),
     (520, 1032, 2056, 0, F16, F16, 4, 16),
     (257, 328, 50257, 0, BF16, BF16, 8, 0),
+    (330, 130, 134, 2, BF16, BF16, 4, 2),
+    (1201, 1301, 1499, 3, F16, F16, 2, 0),
+    (1202, 1302, 1498, 4, F16, F32, 8, 6),
+    (70, 3, 5, 0, BF16, F32, 2, 0),
+    (90, 75, 131, 1, F16, F32, 2, 1),                  # odd rows an even distance apart
+    (65, 131, 67, 0, BF16, BF16, 3, 5),
 ]
 
 

@@ -70,6 +70,7 @@ struct Panel {
   int64_t span;           // bytes of the panel from base on (form K), or of a row (form M)
   uint32_t ld;            // bytes between memory rows
   int rows;               // rows of the product left in this panel (may exceed W)
+  int before;             // elements of a memory row before the panel
   uint32_t voff[kLoads];
 
   __device__ __forceinline__ void init(const void* p, int64_t lde, int row0, int rows_total, int k0, int k_end, int tid) {
@@ -78,17 +79,19 @@ struct Panel {
     if constexpr (FORM == kFormK) {
       base = (const char*)p + (int64_t)row0 * lde * 2 + (int64_t)k0 * 2;
       step = kBK * 2;
+      before = k0;
       const int last = (rows < W ? rows : W) - 1;
       span = (int64_t)last * lde * 2 + (int64_t)(k_end - k0) * 2;
 #pragma unroll
       for (int i = 0; i < kLoads; ++i) {
         const int g = i * NT + tid, row = g >> 3, unit = (g & 7) ^ swz_k(row);
-        voff[i] = (uint32_t)row * ld + unit * 16u;
+        voff[i] = (uint32_t)(row < last ? row : last) * ld + unit * 16u;
       }
     } else {
       base = (const char*)p + (int64_t)k0 * lde * 2 + (int64_t)row0 * 2;
       step = (int64_t)kBK * lde * 2;
       span = (int64_t)rows * 2;
+      before = row0;
       constexpr int U = W / 8;
 #pragma unroll
       for (int i = 0; i < kLoads; ++i) {
@@ -111,9 +114,10 @@ struct Panel {
     if constexpr (FORM == kFormK) span -= step;
   }
 
-  // Starts load i of a stage straight into LDS (rows 16-byte aligned and a whole
-  // number of 16-byte units long).  Behind the last k it reads nothing and writes
-  // zeros.
+  // Starts load i of a stage straight into LDS (rows 4-byte aligned; in form K a
+  // whole number of 16-byte units).  Behind the last k it reads nothing and writes
+  // zeros; in form M what lies behind a row's end reaches only sums that are
+  // dropped.
   __device__ __forceinline__ u32x4 source(int k_left) const {
     const uint64_t p = (uint64_t)(uintptr_t)base;
     return u32x4{(uint32_t)__builtin_amdgcn_readfirstlane((uint32_t)p), (uint32_t)__builtin_amdgcn_readfirstlane((uint32_t)(p >> 32)),
@@ -131,34 +135,58 @@ struct Panel {
                  ::"s"(lds + (uint32_t)(i * NT + wave * 64) * 16u), "v"(off), "s"(rs));
   }
 
-  // Any alignment: through registers.
+  // Any alignment: through registers, a stage of which every unit exists (rows behind
+  // the last are the last's again).
+  __device__ __forceinline__ void load_whole(u32x4 (&r)[kLoads]) const {
+    typedef u32x4 __attribute__((aligned(2))) u32x4_2;
+#pragma unroll
+    for (int i = 0; i < kLoads; ++i) r[i] = *(const __attribute__((address_space(1))) u32x4_2*)(base + voff[i]);
+  }
+  __device__ __forceinline__ bool whole() const { return FORM == kFormK || rows >= W; }
+
+  // The same where units may be missing.  A unit that ends behind its row is loaded so
+  // that it ends with the row, and shifted down.
   __device__ __forceinline__ void load_regs(u32x4 (&r)[kLoads], int tid, int k_left) const {
+    typedef u32x4 __attribute__((aligned(2))) u32x4_2;
+    typedef const __attribute__((address_space(1))) u32x4_2* Units;
 #pragma unroll
     for (int i = 0; i < kLoads; ++i) {
       const int g = i * NT + tid;
-      int have;             // elements of the unit that exist
+      int have, unit;       // elements of the unit that exist
       bool row_ok;
       if constexpr (FORM == kFormK) {
-        const int row = g >> 3, unit = (g & 7) ^ swz_k(row);
-        row_ok = row < rows;
+        unit = (g & 7) ^ swz_k(g >> 3);
+        row_ok = true;
         have = k_left - unit * 8;
       } else {
         constexpr int U = W / 8;
-        const int k = g / U, unit = (g % U) ^ swz_m<W>(k);
+        const int k = g / U;
+        unit = (g % U) ^ swz_m<W>(k);
         row_ok = k < k_left;
         have = rows - unit * 8;
       }
       u32x4 v = {0u, 0u, 0u, 0u};
-      const char* p = base + voff[i];
-      if (row_ok && have >= 8) {
-        typedef u32x4 __attribute__((aligned(2))) u32x4_2;
-        v = *(const __attribute__((address_space(1))) u32x4_2*)p;
-      } else if (row_ok && have > 0) {
-        uint32_t e[8];
+      if (row_ok && have > 0) {
+        const char* p = base + voff[i];
+        const int d = have < 8 ? 8 - have : 0;
+        if (d <= before + unit * 8) {
+          const u32x4 t = *(Units)(p - 2 * d);
+          uint64_t lo = t[0] | ((uint64_t)t[1] << 32), hi = t[2] | ((uint64_t)t[3] << 32);
+          if (d >= 4) {
+            lo = hi >> (16 * (d - 4));
+            hi = 0;
+          } else if (d > 0) {
+            lo = (lo >> (16 * d)) | (hi << (64 - 16 * d));
+            hi >>= 16 * d;
+          }
+          v = u32x4{(uint32_t)lo, (uint32_t)(lo >> 32), (uint32_t)hi, (uint32_t)(hi >> 32)};
+        } else {            // the row is shorter than a unit
+          uint32_t e[8];
 #pragma unroll
-        for (int j = 0; j < 8; ++j) e[j] = j < have ? ((const __attribute__((address_space(1))) uint16_t*)p)[j] : 0u;
+          for (int j = 0; j < 8; ++j) e[j] = j < have ? ((const __attribute__((address_space(1))) uint16_t*)p)[j] : 0u;
 #pragma unroll
-        for (int j = 0; j < 4; ++j) v[j] = e[2 * j] | (e[2 * j + 1] << 16);
+          for (int j = 0; j < 4; ++j) v[j] = e[2 * j] | (e[2 * j + 1] << 16);
+        }
       }
       r[i] = v;
     }
@@ -319,6 +347,10 @@ struct Core {
       for (int j = 0; j < TN; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
     int left = k_end - k0;
     if (left <= 0) return;
+    // A last stage that is not whole goes through registers, or, loaded directly, one
+    // that ends inside a unit of form K.
+    const int ragged = !DIRECT || ((AF == kFormK || BF == kFormK) && left % 8) ? left % kBK : 0;
+    left -= ragged;
     if constexpr (DIRECT) {
       // Two stages in LDS.  While the products of one half of a stage run, the
       // fragments of the next half are read; in the middle of a stage every wave
@@ -326,49 +358,86 @@ struct Core {
       // enough and the matrix units have work on both sides of it.
       Frags f0, f1;
       const uint32_t at = (uint32_t)(uintptr_t)lds;      // LDS address
-      load(pa, pb, at, wave, tid, left);
-      arrive();
-      pa.advance();
-      pb.advance();
-      load(pa, pb, at + kStage, wave, tid, left - kBK);
-      read(f0, lds, 0, wm, wn, lane);
-      int cur = 0;
-      for (; left > kBK; left -= kBK) {
-        const int here = cur * kStage;
-        cur ^= 1;
-        step<false>(f0, f1, lds + here, 1, pa, pb, 0, wave, tid, 0, wm, wn, lane);
+      if (left > 0) {
+        load(pa, pb, at, wave, tid, left);
         arrive();
         pa.advance();
         pb.advance();
-        step<true>(f1, f0, lds + cur * kStage, 0, pa, pb, at + here, wave, tid, left - 2 * kBK, wm, wn, lane);
-      }
-      read(f1, lds + cur * kStage, 1, wm, wn, lane);
-      multiply(f0);
-      multiply(f1);
-      asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
-    } else {
-      u32x4 ra[PA::kLoads], rb[PB::kLoads];
-      pa.load_regs(ra, tid, left);
-      pb.load_regs(rb, tid, left);
-      int cur = 0;
-      for (; left > 0; left -= kBK) {
-        ZK_LDS char* here = lds + cur * kStage;
-        pa.store_regs(here, tid, ra);
-        pb.store_regs(here + PA::kBytes, tid, rb);
-        __syncthreads();
-        if (left > kBK) {
+        load(pa, pb, at + kStage, wave, tid, left - kBK);
+        read(f0, lds, 0, wm, wn, lane);
+        int cur = 0;
+        for (; left > kBK; left -= kBK) {
+          const int here = cur * kStage;
+          cur ^= 1;
+          step<false>(f0, f1, lds + here, 1, pa, pb, 0, wave, tid, 0, wm, wn, lane);
+          arrive();
           pa.advance();
           pb.advance();
-          pa.load_regs(ra, tid, left - kBK);
-          pb.load_regs(rb, tid, left - kBK);
+          step<true>(f1, f0, lds + cur * kStage, 0, pa, pb, at + here, wave, tid, left - 2 * kBK, wm, wn, lane);
         }
-        Frags f0, f1;
-        read(f0, here, 0, wm, wn, lane);
-        read(f1, here, 1, wm, wn, lane);
+        read(f1, lds + cur * kStage, 1, wm, wn, lane);
         multiply(f0);
         multiply(f1);
-        cur ^= 1;
       }
+    } else {
+      // Through registers: a stage is loaded while the one before it is multiplied.
+      if (pa.whole() && pb.whole()) {
+        reg_loop(lds, pa, pb, left, wm, wn, lane, tid, [&](u32x4 (&ra)[PA::kLoads], u32x4 (&rb)[PB::kLoads]) {
+          pa.load_whole(ra);
+          pb.load_whole(rb);
+        });
+      } else {
+        reg_loop(lds, pa, pb, left, wm, wn, lane, tid, [&](u32x4 (&ra)[PA::kLoads], u32x4 (&rb)[PB::kLoads]) {
+          pa.load_regs(ra, tid, kBK);
+          pb.load_regs(rb, tid, kBK);
+        });
+      }
+    }
+    if (ragged) {
+      Frags f;
+      PA ta;
+      PB tb;
+      ta.init(a, lda, m0, m, k_end - ragged, k_end, tid);
+      tb.init(b, ldb, n0, n, k_end - ragged, k_end, tid);
+      u32x4 ra[PA::kLoads], rb[PB::kLoads];
+      ta.load_regs(ra, tid, ragged);
+      tb.load_regs(rb, tid, ragged);
+      arrive();           // no load is under way into this stage, and nobody reads it
+      ta.store_regs(lds, tid, ra);
+      tb.store_regs(lds + PA::kBytes, tid, rb);
+      __syncthreads();
+#pragma unroll
+      for (int s = 0; s < kBK / 32; ++s) {
+        read(f, lds, s, wm, wn, lane);
+        multiply(f);
+      }
+    }
+    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+  }
+
+  template <typename L>
+  __device__ __forceinline__ void reg_loop(ZK_LDS char* lds, PA& pa, PB& pb, int left, int wm, int wn, int lane, int tid, L fetch) {
+    if (left <= 0) return;
+    u32x4 ra[PA::kLoads], rb[PB::kLoads];
+    Frags f;
+    fetch(ra, rb);
+    int cur = 0;
+    for (; left > 0; left -= kBK) {
+      ZK_LDS char* here = lds + cur * kStage;
+      pa.store_regs(here, tid, ra);
+      pb.store_regs(here + PA::kBytes, tid, rb);
+      __syncthreads();
+      if (left > kBK) {
+        pa.advance();
+        pb.advance();
+        fetch(ra, rb);
+      }
+#pragma unroll
+      for (int s = 0; s < kBK / 32; ++s) {
+        read(f, here, s, wm, wn, lane);
+        multiply(f);
+      }
+      cur ^= 1;
     }
   }
 

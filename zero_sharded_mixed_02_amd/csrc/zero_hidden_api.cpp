@@ -92,8 +92,10 @@ zero_status check_grid(int64_t blocks, int threads) {
   return ok();
 }
 
-// An operand's rows can be loaded 16 bytes at a time straight into LDS.
-bool direct_ok(const void* p, int64_t ld, int64_t width) { return aligned(p, 16) && ld % 8 == 0 && width % 8 == 0; }
+// An operand's rows can be loaded straight into LDS, which takes addresses that are
+// multiples of 4, and whole words: form M's last row must not end inside one.
+bool direct_k(const void* p, int64_t ld) { return aligned(p, 4) && ld % 2 == 0; }
+bool direct_m(const void* p, int64_t ld, int64_t width) { return direct_k(p, ld) && width % 2 == 0; }
 
 // ---------------------------------------------------------------------------
 // Arguments
@@ -467,7 +469,7 @@ zero_status zero_linear(zero_plan_t p, int32_t weight, int32_t bias, int64_t in_
     memset(&a, 0, sizeof a);
     a.p.a = x;
     a.p.b = (const char*)params + p->t_off[weight] * 2;
-    a.p.lda = n > 1 ? x_stride : round_up(in_features, 8);     // a single row has no neighbour
+    a.p.lda = n > 1 ? x_stride : round_up(in_features, 2);     // a single row has no neighbour
     a.p.ldb = in_features;
     lay_out(a.p, n, out, in_features, c);
     a.out = y;
@@ -478,7 +480,7 @@ zero_status zero_linear(zero_plan_t p, int32_t weight, int32_t bias, int64_t in_
     a.ldpre = pre_stride;
     a.ldadd = residual_stride;
     a.act = act;
-    const bool direct = direct_ok(a.p.a, a.p.lda, in_features) && direct_ok(a.p.b, a.p.ldb, in_features);
+    const bool direct = direct_k(a.p.a, a.p.lda) && direct_k(a.p.b, a.p.ldb);
     return run_linear(a, 0, dt, c, direct, workspace, stream);
   });
 }
@@ -523,7 +525,7 @@ zero_status zero_linear_input_grad(zero_plan_t p, int32_t weight, int64_t in_fea
     memset(&a, 0, sizeof a);
     a.p.a = dz;
     a.p.b = (const char*)params + p->t_off[weight] * 2;
-    a.p.lda = n > 1 ? dz_stride : round_up(std::max<int64_t>(out, 1), 8);
+    a.p.lda = n > 1 ? dz_stride : round_up(std::max<int64_t>(out, 1), 2);
     a.p.ldb = in_features;
     lay_out(a.p, n, in_features, out, c);
     a.out = dx;
@@ -533,7 +535,7 @@ zero_status zero_linear_input_grad(zero_plan_t p, int32_t weight, int64_t in_fea
     a.ldpre = pre_stride;
     a.ldadd = addend_stride;
     a.act = act;
-    const bool direct = direct_ok(a.p.a, a.p.lda, out) && direct_ok(a.p.b, a.p.ldb, in_features);
+    const bool direct = direct_k(a.p.a, a.p.lda) && direct_m(a.p.b, a.p.ldb, in_features);
     return run_linear(a, 1, dt, c, direct, workspace, stream);
   });
 }
@@ -589,8 +591,8 @@ zero_status zero_linear_weight_grad(zero_plan_t p, int32_t weight, int32_t bias,
     }
     a.p.a = (const char*)dz + s.row0 * 2;
     a.p.b = x;
-    a.p.lda = n > 1 ? dz_stride : round_up(out, 8);
-    a.p.ldb = n > 1 ? x_stride : round_up(in_features, 8);
+    a.p.lda = n > 1 ? dz_stride : round_up(out, 2);
+    a.p.ldb = n > 1 ? x_stride : round_up(in_features, 2);
     lay_out(a.p, s.rows, in_features, n, c);
     a.p.part = a.p.splits > 1 ? (float*)workspace : nullptr;
     if (bias >= 0) {
@@ -614,7 +616,7 @@ zero_status zero_linear_weight_grad(zero_plan_t p, int32_t weight, int32_t bias,
     const int64_t joins = a.join_blocks + (a.bias_blocks && a.chunks > 1 ? ceil_div(a.b_hi - a.b_lo, kJoinThreads) : 0);
     if (zero_status st = check_grid(blocks, kTileThreads[c.tile])) return st;
     if (zero_status st = check_grid(joins, kJoinThreads)) return st;
-    const bool direct = direct_ok(a.p.a, a.p.lda, s.rows) && direct_ok(a.p.b, a.p.ldb, in_features);
+    const bool direct = direct_m(a.p.a, a.p.lda, s.rows) && direct_m(a.p.b, a.p.ldb, in_features);
     if (const int err = launch_weight_grad(a, dt, c.tile, direct, blocks, stream)) return hip_fail(err);
     if (joins == 0) return ok();
     return launched(launch_weight_grad_join(a, joins, stream));
