@@ -55,7 +55,8 @@ __device__ __forceinline__ int swz_k(int row) {
 template <int W>
 __device__ __forceinline__ int swz_m(int k) {
   if constexpr (W >= 128) return ((k & 3) | (((k >> 3) & 1) << 2)) << 1;
-  else return (((k >> 1) & 1) | (((k >> 3) & 1) << 1)) << 1;
+  else if constexpr (W == 64) return (((k >> 1) & 1) | (((k >> 3) & 1) << 1)) << 1;
+  else return ((k >> 3) & 1) << 1;
 }
 
 // One operand's panel of W rows (of the product) and its staging.
@@ -441,32 +442,67 @@ struct Core {
     }
   }
 
-  // f(row, first n, values): kVec consecutive n of one row at a time.
-  template <typename F>
-  __device__ __forceinline__ void each(int m0, int n0, F f) const {
-    const int lane = threadIdx.x & 63, c = lane & 15, q = lane >> 4;
-    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  // The tile's values, kVec consecutive n of a row at a time.  before(row, first n,
+  // p) starts what the epilogue reads, after(row, first n, values, p) ends it: of
+  // kBatch pieces the reads are under way together.
+  static constexpr int kPieces = TM * TN / (kPerm ? 2 : 1);
+  __device__ __forceinline__ void piece(int c, int m0, int n0, int& row, int& col, float (&v)[kVec]) const {
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int wm = wave / WN, wn = wave % WN;
+    constexpr int kRow = TN / (kPerm ? 2 : 1);
+    const int i = c / kRow, j = c % kRow * (kPerm ? 2 : 1);
+    row = m0 + (wm * TM + i) * 16 + (lane & 15);
+    col = n0 + (wn * TN + j) * 16 + (lane >> 4) * kVec;
 #pragma unroll
-    for (int i = 0; i < TM; ++i) {
-      const int row = m0 + (wm * TM + i) * 16 + c;
-      if constexpr (kPerm) {
+    for (int x = 0; x < kVec; ++x) v[x] = acc[i][j + x / 4][x % 4];
+  }
+  template <typename P, typename F, typename G>
+  __device__ __forceinline__ void each(int m0, int n0, F before, G after) const {
+    constexpr int kBatch = kPieces < 4 ? kPieces : 4;
 #pragma unroll
-        for (int j = 0; j < TN; j += 2) {
-          const int col = n0 + wn * TN * 16 + j * 16 + q * 8;
-          const float v[8] = {acc[i][j][0], acc[i][j][1], acc[i][j][2], acc[i][j][3],
-                              acc[i][j + 1][0], acc[i][j + 1][1], acc[i][j + 1][2], acc[i][j + 1][3]};
-          f(row, col, v);
-        }
-      } else {
+    for (int c = 0; c < kPieces; c += kBatch) {
+      P p[kBatch];
+      int row, col;
+      float v[kVec];
 #pragma unroll
-        for (int j = 0; j < TN; ++j) {
-          const int col = n0 + (wn * TN + j) * 16 + q * 4;
-          const float v[4] = {acc[i][j][0], acc[i][j][1], acc[i][j][2], acc[i][j][3]};
-          f(row, col, v);
-        }
+      for (int x = 0; x < kBatch; ++x) {
+        piece(c + x, m0, n0, row, col, v);
+        before(row, col, p[x]);
+      }
+#pragma unroll
+      for (int x = 0; x < kBatch; ++x) {
+        piece(c + x, m0, n0, row, col, v);
+        after(row, col, v, p[x]);
       }
     }
+  }
+
+  // A tile's 16-bit values on their way to the transposed place: put() takes what
+  // each() hands out, take(f) then calls f(n, first m, eight values of consecutive
+  // m).  A wave puts and takes its own part of LDS, which nobody reads any more
+  // (arrive() first).
+  static constexpr int kWaveN = TN * 16;
+  static constexpr int kWaveBytes = TM * 16 * kWaveN * 2;
+  static_assert(!DIRECT || kWaveBytes * WM * WN <= kLds, "the waves' parts fit");
+  __device__ __forceinline__ static ZK_LDS char* part_of(ZK_LDS char* lds) {
+    return lds + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6) * kWaveBytes;
+  }
+  template <typename H>
+  __device__ __forceinline__ static void put(ZK_LDS char* lds, int row, int col, H h) {
+    static_assert(sizeof(H) == kVec * 2, "a piece");
+    const int m = row % (TM * 16), n = col % kWaveN;
+    *(ZK_LDS H*)(part_of(lds) + m * (kWaveN * 2) + ((n * 2) ^ (swz_m<kWaveN>(m) * 16))) = h;
+  }
+  template <typename F>
+  __device__ __forceinline__ static void take(ZK_LDS char* lds, int m0, int n0, F f) {
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int wm = wave / WN, wn = wave % WN;
+#pragma unroll
+    for (int t = 0; t < TN; ++t)
+#pragma unroll
+      for (int s = 0; s < TM / 2; ++s)
+        f(n0 + (wn * TN + t) * 16 + (lane & 15), m0 + wm * TM * 16 + s * 32 + (lane >> 4) * 8,
+          Frag<kFormM, kWaveN, false>::read(part_of(lds), 0, t, s, lane));
   }
 };
 

@@ -192,9 +192,9 @@ WeightShape weight_shape(const zero_plan_s& p, int32_t weight, int64_t in_featur
   WeightShape s;
   part_of_tensor(p, weight, rank, s.lo, s.hi, s.at);
   s.row0 = s.rows = 0;
-  if (s.lo < s.hi) {
-    s.row0 = s.lo / in_features;
-    s.rows = (s.hi - 1) / in_features + 1 - s.row0;
+  if (s.lo < s.hi) {      // in whole eights where there are, for their loads' sake
+    s.row0 = s.lo / in_features / 8 * 8;
+    s.rows = std::min(round_up((s.hi - 1) / in_features + 1, 8), out_features) - s.row0;
   }
   // The pieces of k follow from the whole weight, so that a slice's sums are
   // those of the full buffer.

@@ -38,6 +38,23 @@ __device__ __forceinline__ void load_row(const void* base, int64_t e, int have, 
   }
 }
 
+// The same in two steps: the load, and its values when they are needed.
+template <typename T, int V>
+struct Row {
+  typedef T tv __attribute__((ext_vector_type(V)));
+  tv v;
+  __device__ __forceinline__ void load(const void* base, int64_t e, int have) {
+    typedef tv __attribute__((aligned(2))) tvu;
+    const AS1 T* p = (const AS1 T*)base + e;
+    if (have >= V) {
+      v = *(const AS1 tvu*)p;
+    } else {
+#pragma unroll
+      for (int i = 0; i < V; ++i) v[i] = i < have ? p[i] : (T)0.0f;
+    }
+  }
+};
+
 template <typename T, int V>
 __device__ __forceinline__ void store_row(void* base, int64_t e, int have, const float (&x)[V]) {
   typedef T tv __attribute__((ext_vector_type(V)));

@@ -13,44 +13,56 @@ namespace {
 
 using namespace zk::gemm;
 
-// V sums of row `row` from column `col` on, through the epilogue.  One rounding
-// to 16 bits, of the finished value.
+// What the epilogue of V sums of row `row` from column `col` on reads, and the
+// epilogue.  One rounding to 16 bits, of the finished value.
 template <typename T, int EPI, int V>
-__device__ __forceinline__ void finish(const LinearArgs& a, int64_t row, int col, const float (&acc)[V]) {
-  const int have = a.p.n - col;
-  float v[V], x[V];
-#pragma unroll
-  for (int i = 0; i < V; ++i) v[i] = acc[i];
-  if constexpr (EPI == 0) {
-    if (a.bias) {
-      load_row<T, V>(a.bias, col, have, x);
-#pragma unroll
-      for (int i = 0; i < V; ++i) v[i] += x[i];
-    }
-    if (a.pre_out) store_row<T, V>(a.pre_out, row * a.ldpre + col, have, v);
-    if (a.act != ZERO_ACT_NONE) {
-#pragma unroll
-      for (int i = 0; i < V; ++i) v[i] = act::forward(a.act, v[i]);
-    }
-  } else {
-    if (a.pre_in) {
-      load_row<T, V>(a.pre_in, row * a.ldpre + col, have, x);
-#pragma unroll
-      for (int i = 0; i < V; ++i) v[i] *= act::slope(a.act, x[i]);
-    }
-  }
-  if (a.add) {
-    load_row<T, V>(a.add, row * a.ldadd + col, have, x);
-#pragma unroll
-    for (int i = 0; i < V; ++i) v[i] += x[i];
-  }
-  store_row<T, V>(a.out, row * a.ldo + col, have, v);
-}
+struct Epilogue {
+  Row<T, V> side, add;      // the bias or the activation's argument; the residual or addend
 
-// Runs the tile of workgroup b and hands its values to part() or done().
-template <typename C, typename F>
+  __device__ __forceinline__ void load(const LinearArgs& a, int64_t row, int col) {
+    const int have = a.p.n - col;
+    if constexpr (EPI == 0) {
+      if (a.bias) side.load(a.bias, col, have);
+    } else {
+      if (a.pre_in) side.load(a.pre_in, row * a.ldpre + col, have);
+    }
+    if (a.add) add.load(a.add, row * a.ldadd + col, have);
+  }
+
+  __device__ __forceinline__ void finish(const LinearArgs& a, int64_t row, int col, const float (&acc)[V]) const {
+    const int have = a.p.n - col;
+    float v[V];
+#pragma unroll
+    for (int i = 0; i < V; ++i) v[i] = acc[i];
+    if constexpr (EPI == 0) {
+      if (a.bias) {
+#pragma unroll
+        for (int i = 0; i < V; ++i) v[i] += (float)side.v[i];
+      }
+      if (a.pre_out) store_row<T, V>(a.pre_out, row * a.ldpre + col, have, v);
+      if (a.act != ZERO_ACT_NONE) {
+#pragma unroll
+        for (int i = 0; i < V; ++i) v[i] = act::forward(a.act, v[i]);
+      }
+    } else {
+      if (a.pre_in) {
+#pragma unroll
+        for (int i = 0; i < V; ++i) v[i] *= act::slope(a.act, (float)side.v[i]);
+      }
+    }
+    if (a.add) {
+#pragma unroll
+      for (int i = 0; i < V; ++i) v[i] += (float)add.v[i];
+    }
+    store_row<T, V>(a.out, row * a.ldo + col, have, v);
+  }
+};
+
+// Runs the tile of workgroup b; its values go to the partial sums, or through
+// before() and after().
+template <typename P, typename C, typename F, typename G>
 __device__ __forceinline__ void run_tile(C& core, ZK_LDS char* lds, const Product& p, int b, int n_blocks, int bm, int bn,
-                                         F done) {
+                                         F before, G after) {
   int im, in;
   const int t = die_order(b, n_blocks), split = t / p.tiles;
   place(t - split * p.tiles, p.tm, p.tn, im, in);
@@ -58,13 +70,14 @@ __device__ __forceinline__ void run_tile(C& core, ZK_LDS char* lds, const Produc
   const int k_end = p.k - k0 < p.k_piece ? p.k : k0 + p.k_piece;
   core.run(lds, p.a, p.lda, p.m, p.b, p.ldb, p.n, im * bm, in * bn, k0, k_end);
   if (p.part) {
-    core.each(im * bm, in * bn, [&](int row, int col, const float* v) {
+    core.template each<int>(im * bm, in * bn, [](int, int, int&) {}, [&](int row, int col, const float (&v)[C::kVec], int) {
       if (row < p.m && col < p.n) store_part<C::kVec>(p, p.part, split, row, col, v);
     });
   } else {
-    core.each(im * bm, in * bn, [&](int row, int col, const float* v) {
-      if (row < p.m && col < p.n) done(row, col, v);
-    });
+    core.template each<P>(im * bm, in * bn, [&](int row, int col, P& x) { if (row < p.m && col < p.n) before(row, col, x); },
+                          [&](int row, int col, const float (&v)[C::kVec], const P& x) {
+                            if (row < p.m && col < p.n) after(row, col, v, x);
+                          });
   }
 }
 
@@ -74,15 +87,21 @@ __global__ void __launch_bounds__(kTileThreads[TILE]) linear_kernel(const Linear
   typedef CoreOf<T, kFormK, EPI == 0 ? kFormK : kFormM, TILE, DIRECT> C;
   extern __shared__ __attribute__((aligned(1024))) char smem[];
   C core;
-  run_tile(core, (ZK_LDS char*)smem, a.p, blockIdx.x, gridDim.x, Shape<TILE>::BM, Shape<TILE>::BN,
-           [&](int row, int col, const float* v) { finish<T, EPI, C::kVec>(a, row, col, *(const float(*)[C::kVec])v); });
+  typedef Epilogue<T, EPI, C::kVec> E;
+  run_tile<E>(core, (ZK_LDS char*)smem, a.p, blockIdx.x, gridDim.x, Shape<TILE>::BM, Shape<TILE>::BN,
+              [&](int row, int col, E& e) { e.load(a, row, col); },
+              [&](int row, int col, const float (&v)[C::kVec], const E& e) { e.finish(a, row, col, v); });
 }
 
 template <typename T, int EPI>
 __global__ void __launch_bounds__(kJoinThreads) linear_join_kernel(const LinearArgs a) {
   int row, col;
   float v[4];
-  if (join4(a.p, a.p.part, (int64_t)blockIdx.x * kJoinThreads + threadIdx.x, row, col, v)) finish<T, EPI, 4>(a, row, col, v);
+  if (join4(a.p, a.p.part, (int64_t)blockIdx.x * kJoinThreads + threadIdx.x, row, col, v)) {
+    Epilogue<T, EPI, 4> e;
+    e.load(a, row, col);
+    e.finish(a, row, col, v);
+  }
 }
 
 // ---------------------------------------------------------------------------
@@ -184,8 +203,9 @@ __global__ void __launch_bounds__(kTileThreads[TILE]) weight_grad_kernel(const W
     return;
   }
   C core;
-  run_tile(core, (ZK_LDS char*)smem, a.p, b, gridDim.x - a.bias_blocks, Shape<TILE>::BM, Shape<TILE>::BN,
-           [&](int row, int col, const float* v) { finish_weight<C::kVec>(a, row, col, *(const float(*)[C::kVec])v); });
+  run_tile<int>(core, (ZK_LDS char*)smem, a.p, b, gridDim.x - a.bias_blocks, Shape<TILE>::BM, Shape<TILE>::BN,
+                [](int, int, int&) {},
+                [&](int row, int col, const float (&v)[C::kVec], int) { finish_weight<C::kVec>(a, row, col, v); });
 }
 
 __global__ void __launch_bounds__(kJoinThreads) weight_grad_join_kernel(const WeightGradArgs a) {

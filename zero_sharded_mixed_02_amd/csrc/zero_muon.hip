@@ -91,67 +91,68 @@ __global__ void __launch_bounds__(kLoadThreads) ortho_load_kernel(const OrthoLoa
 __device__ __forceinline__ float factor_of(const OrthoArgs& a, int z) { return a.first ? a.factor[2 * z] : 1.0f; }
 __device__ __forceinline__ float shift_of(const OrthoArgs& a, int z) { return a.shift * a.factor[2 * z + 1]; }
 
-// V sums of one row through the epilogue.
+// What the epilogue of V sums of a row reads, and the epilogue.
 template <int V>
-__device__ __forceinline__ void finish(const OrthoArgs& a, int z, int row, int col, const float (&acc)[V]) {
-  const int have = a.p.n - col;
-  float v[V], x[V];
-  if (a.epi == kGram) {
-    const float f = factor_of(a, z), f2 = f * f, d = shift_of(a, z);
-#pragma unroll
-    for (int i = 0; i < V; ++i) v[i] = __builtin_fmaf(f2, acc[i], row == col + i ? -d : 0.0f);
-  } else if (a.epi == kPoly) {
-    load_row<_Float16, V>(a.add, z * a.zadd + (int64_t)row * a.ldadd + col, have, x);
-    const float b = __builtin_fmaf(2.0f * a.c, shift_of(a, z), a.b);
-#pragma unroll
-    for (int i = 0; i < V; ++i) v[i] = __builtin_fmaf(a.c, acc[i], b * x[i]);
-  } else {
-    const int64_t e = z * a.zadd + (int64_t)row * a.ldadd + col;
-    if (a.first) {
-      load_row<_Float16, V>(a.add, e, have, x);
-    } else {
-      const AS1 float* p = (const AS1 float*)a.add + e;
-#pragma unroll
-      for (int i = 0; i < V; i += 4) {      // rows are padded to whole fours
-        const f32x4 t = col + i < a.p.n ? *(const AS1 f32x4*)(p + i) : f32x4{0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-        for (int k = 0; k < 4; ++k) x[i + k] = t[k];
-      }
-    }
-    const float f = factor_of(a, z), d = shift_of(a, z);
-    const float c0 = __builtin_fmaf(__builtin_fmaf(a.c, d, a.b), d, a.a);
-#pragma unroll
-    for (int i = 0; i < V; ++i) v[i] = f * __builtin_fmaf(c0, x[i], acc[i]);
-    if (a.last) {
-      if (row >= a.rows || col >= a.cols) return;
-      const int left = a.cols - col;
-      const float s = a.scale[z];
-#pragma unroll
-      for (int i = 0; i < V; ++i) v[i] *= s;
-      const int64_t d = a.dst_off[z] + (int64_t)row * a.cols + col;
-      if (a.dst_dt == ZERO_BF16) store_row<__bf16, V>(a.dst, d, left, v);
-      else store_row<_Float16, V>(a.dst, d, left, v);
-      return;
-    }
-    AS1 float* p = (AS1 float*)a.out32 + e;
-#pragma unroll
-    for (int i = 0; i < V; i += 4)
-      if (col + i < a.p.n) *(AS1 f32x4*)(p + i) = f32x4{v[i], v[i + 1], v[i + 2], v[i + 3]};
-  }
-  store_row<_Float16, V>(a.out, z * a.zout + (int64_t)row * a.ldo + col, have, v);
-}
+struct Epilogue {
+  Row<_Float16, V> half;          // kPoly's A - d I; the first X
+  f32x4 full[V / 4];              // X later on
+  typedef typename Row<_Float16, V>::tv Half;
 
-template <int V>
-__device__ __forceinline__ void mirror(const OrthoArgs& a, int z, int row, int col, const float (&acc)[V]) {
-  const float f = factor_of(a, z), f2 = f * f, b = __builtin_fmaf(2.0f * a.c, shift_of(a, z), a.b);
-  float x[V];
-  if (a.epi == kPoly) load_row<_Float16, V>(a.add, z * a.zadd + (int64_t)row * a.ldadd + col, a.p.n - col, x);
+  __device__ __forceinline__ void load(const OrthoArgs& a, int z, int row, int col) {
+    if (a.epi == kGram) return;
+    const int64_t e = z * a.zadd + (int64_t)row * a.ldadd + col;
+    if (a.epi == kPoly || a.first) {
+      half.load(a.add, e, a.p.n - col);
+    } else {
 #pragma unroll
-  for (int i = 0; i < V; ++i) {
-    const float v = a.epi == kGram ? f2 * acc[i] : __builtin_fmaf(a.c, acc[i], b * x[i]);
-    if (col + i < a.p.n) ((AS1 _Float16*)a.out)[z * a.zout + (int64_t)(col + i) * a.ldo + row] = (_Float16)v;
+      for (int i = 0; i < V; i += 4)      // rows are padded to whole fours
+        full[i / 4] = col + i < a.p.n ? *(const AS1 f32x4*)((const AS1 float*)a.add + e + i) : f32x4{0.f, 0.f, 0.f, 0.f};
+    }
   }
-}
+
+  // Returns the 16-bit result.
+  __device__ __forceinline__ Half finish(const OrthoArgs& a, int z, int row, int col, const float (&acc)[V]) const {
+    const int have = a.p.n - col;
+    float v[V];
+    Half h = {};
+    if (a.epi == kGram) {
+      const float f = factor_of(a, z), f2 = f * f, d = shift_of(a, z);
+#pragma unroll
+      for (int i = 0; i < V; ++i) v[i] = __builtin_fmaf(f2, acc[i], row == col + i ? -d : 0.0f);
+    } else if (a.epi == kPoly) {
+      const float b = __builtin_fmaf(2.0f * a.c, shift_of(a, z), a.b);
+#pragma unroll
+      for (int i = 0; i < V; ++i) v[i] = __builtin_fmaf(a.c, acc[i], b * (float)half.v[i]);
+    } else {
+      const float f = factor_of(a, z), d = shift_of(a, z);
+      const float c0 = __builtin_fmaf(__builtin_fmaf(a.c, d, a.b), d, a.a);
+#pragma unroll
+      for (int i = 0; i < V; ++i) v[i] = f * __builtin_fmaf(c0, a.first ? (float)half.v[i] : full[i / 4][i % 4], acc[i]);
+      if (a.last) {
+        if (row < a.rows && col < a.cols) {
+          const float s = a.scale[z];
+#pragma unroll
+          for (int i = 0; i < V; ++i) v[i] *= s;
+          const int64_t d = a.dst_off[z] + (int64_t)row * a.cols + col;
+          if (a.dst_dt == ZERO_BF16) store_row<__bf16, V>(a.dst, d, a.cols - col, v);
+          else store_row<_Float16, V>(a.dst, d, a.cols - col, v);
+        }
+        return h;
+      }
+      AS1 float* p = (AS1 float*)a.out32 + z * a.zadd + (int64_t)row * a.ldadd + col;
+#pragma unroll
+      for (int i = 0; i < V; i += 4)
+        if (col + i < a.p.n) *(AS1 f32x4*)(p + i) = f32x4{v[i], v[i + 1], v[i + 2], v[i + 3]};
+    }
+#pragma unroll
+    for (int i = 0; i < V; ++i) h[i] = (_Float16)v[i];
+    // p.n, ldo and col are multiples of V or 4 apart: a piece is whole, or its first half is.
+    AS1 _Float16* out = (AS1 _Float16*)a.out + z * a.zout + (int64_t)row * a.ldo + col;
+    if (have >= V) *(AS1 Half*)out = h;
+    else store_row<_Float16, V>(a.out, z * a.zout + (int64_t)row * a.ldo + col, have, v);
+    return h;
+  }
+};
 
 template <int AF, int BF, int TILE>
 __global__ void __launch_bounds__(kTileThreads[TILE]) ortho_kernel(const OrthoArgs a) {
@@ -168,18 +169,25 @@ __global__ void __launch_bounds__(kTileThreads[TILE]) ortho_kernel(const OrthoAr
            a.p.n, im * BM, in * BN, k0, k_end);
   if (a.p.part) {
     float* part = a.p.part + (int64_t)z * a.p.splits * a.p.m * a.p.n_pad;
-    core.each(im * BM, in * BN, [&](int row, int col, const float* v) {
+    core.template each<int>(im * BM, in * BN, [](int, int, int&) {}, [&](int row, int col, const float (&v)[C::kVec], int) {
       if (row < a.p.m && col < a.p.n) store_part<C::kVec>(a.p, part, split, row, col, v);
     });
     return;
   }
-  const bool twice = a.upper && im != in;
-  core.each(im * BM, in * BN, [&](int row, int col, const float* v) {
-    if (row < a.p.m && col < a.p.n) {
-      finish<C::kVec>(a, z, row, col, *(const float(*)[C::kVec])v);
-      if (twice) mirror<C::kVec>(a, z, row, col, *(const float(*)[C::kVec])v);
-    }
-  });
+  typedef Epilogue<C::kVec> E;
+  const bool twice = a.upper && im != in;     // the mirrored tile too
+  if (twice) C::arrive();
+  core.template each<E>(im * BM, in * BN, [&](int row, int col, E& e) { if (row < a.p.m && col < a.p.n) e.load(a, z, row, col); },
+                        [&](int row, int col, const float (&v)[C::kVec], const E& e) {
+                          typename E::Half h = {};
+                          if (row < a.p.m && col < a.p.n) h = e.finish(a, z, row, col, v);
+                          if (twice) C::put((ZK_LDS char*)smem, row, col, h);
+                        });
+  if (twice) {
+    C::take((ZK_LDS char*)smem, im * BM, in * BN, [&](int n, int m, s16x8 h) {
+      if (n < a.p.n && m < a.p.m) *(AS1 s16x8*)((AS1 _Float16*)a.out + z * a.zout + (int64_t)n * a.ldo + m) = h;
+    });
+  }
 }
 
 __global__ void __launch_bounds__(kJoinThreads) ortho_join_kernel(const OrthoArgs a) {
@@ -188,8 +196,11 @@ __global__ void __launch_bounds__(kJoinThreads) ortho_join_kernel(const OrthoArg
   int row, col;
   float v[4];
   if (join4(a.p, a.p.part + (int64_t)z * a.p.splits * a.p.m * a.p.n_pad, (blockIdx.x - z * per) * kJoinThreads + threadIdx.x, row,
-            col, v))
-    finish<4>(a, z, row, col, v);
+            col, v)) {
+    Epilogue<4> e;
+    e.load(a, z, row, col);
+    e.finish(a, z, row, col, v);
+  }
 }
 
 template <int AF, int BF>
