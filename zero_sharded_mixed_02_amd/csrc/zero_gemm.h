@@ -42,21 +42,16 @@ __device__ __forceinline__ f32x4 mfma<__bf16>(s16x8 a, s16x8 b, f32x4 c) {
   return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, a), __builtin_bit_cast(bf16x8, b), c, 0, 0, 0);
 }
 
-// XOR of a row's 16-byte units in LDS.  Form K: rows of 128 bytes; a fragment
-// reads 16 rows at one unit, either consecutive rows (bits 0-3 run) or the
-// permuted ones of perm8 (bits 0, 1, 3, 4 run); with 64 banks both cover each
-// bank once.
-__device__ __forceinline__ int swz_k(int row) {
-  return ((row >> 1) & 1) | ((((row >> 2) ^ (row >> 4)) & 1) << 1) | (((row >> 3) & 1) << 2);
-}
+// XOR of a row's 16-byte units in LDS.  Form K: rows of 128 bytes; a fragment reads
+// 16 consecutive rows at one unit, which with 64 banks then covers each bank once.
+__device__ __forceinline__ int swz_k(int row) { return (row >> 1) & 7; }
 // Form M: rows of W elements, one per k; a transposing read takes 32 bytes of
 // each of four rows k .. k + 3 per 16 lanes, and of four rows 8 further on in the
 // next 16.
 template <int W>
 __device__ __forceinline__ int swz_m(int k) {
   if constexpr (W >= 128) return ((k & 3) | (((k >> 3) & 1) << 2)) << 1;
-  else if constexpr (W == 64) return (((k >> 1) & 1) | (((k >> 3) & 1) << 1)) << 1;
-  else return ((k >> 3) & 1) << 1;
+  else return (((k >> 1) & 1) | (((k >> 3) & 1) << 1)) << 1;
 }
 
 // One operand's panel of W rows (of the product) and its staging.
@@ -198,25 +193,20 @@ struct Panel {
   }
 };
 
-// Which product row a fragment's lane holds.  Natural: tile t's rows are 16 t + c.
-// Permuted (form K of the n side): pairs of tiles are interleaved in fours, so
-// that a lane's two results of four make eight consecutive n.
-__device__ __forceinline__ int perm8(int t, int c) { return (t >> 1) * 32 + (c >> 2) * 8 + (t & 1) * 4 + (c & 3); }
-
 // Reads fragments of 16 rows by 32 k out of a staged panel.
-template <int FORM, int W, bool PERM>
+template <int FORM, int W>
 struct Frag {
   // Form K: byte address of (row, unit 0) and the row's XOR; form M: of the
   // lane's piece at k = 0.
   __device__ static __forceinline__ s16x8 read(const ZK_LDS char* lds, int row0, int t, int s, int lane) {
     const int c = lane & 15, q = lane >> 4;
     if constexpr (FORM == kFormK) {
-      const int row = row0 + (PERM ? perm8(t, c) : t * 16 + c);
+      const int row = row0 + t * 16 + c;
       const int unit = (s * 4 + q) ^ swz_k(row);
       return *(const ZK_LDS s16x8*)(lds + row * 128 + unit * 16);
     } else {
       const int p = c & 3, kr = c >> 2;
-      const int mb = (row0 + (PERM ? (t >> 1) * 32 + p * 8 + (t & 1) * 4 : t * 16 + p * 4)) * 2;   // byte within the row
+      const int mb = (row0 + t * 16 + p * 4) * 2;   // byte within the row
       const int k = s * 32 + q * 8 + kr;
       const ZK_LDS char* a0 = lds + k * (W * 2) + (mb ^ (swz_m<W>(k) * 16));
       const int k1 = k + 4;
@@ -258,8 +248,6 @@ template <typename T, int AF, int BF, int BM, int BN, int WM, int WN, bool DIREC
 struct Core {
   static constexpr int NT = 64 * WM * WN;
   static constexpr int TM = BM / WM / 16, TN = BN / WN / 16;
-  static constexpr bool kPerm = BF == kFormK && TN % 2 == 0;
-  static constexpr int kVec = kPerm ? 8 : 4;       // consecutive n a lane holds
   typedef Panel<AF, BM, NT> PA;
   typedef Panel<BF, BN, NT> PB;
   static constexpr int kStage = PA::kBytes + PB::kBytes;
@@ -271,9 +259,9 @@ struct Core {
 
   __device__ __forceinline__ static void read(Frags& f, const ZK_LDS char* lds, int s, int wm, int wn, int lane) {
 #pragma unroll
-    for (int j = 0; j < TN; ++j) f.b[j] = Frag<BF, BN, kPerm>::read(lds + PA::kBytes, wn * TN * 16, j, s, lane);
+    for (int j = 0; j < TN; ++j) f.b[j] = Frag<BF, BN>::read(lds + PA::kBytes, wn * TN * 16, j, s, lane);
 #pragma unroll
-    for (int i = 0; i < TM; ++i) f.a[i] = Frag<AF, BM, false>::read(lds, wm * TM * 16, i, s, lane);
+    for (int i = 0; i < TM; ++i) f.a[i] = Frag<AF, BM>::read(lds, wm * TM * 16, i, s, lane);
   }
   __device__ __forceinline__ void multiply(const Frags& f) {
 #pragma unroll
@@ -287,8 +275,8 @@ struct Core {
   static constexpr int kL = PA::kLoads + PB::kLoads, kF = TM + TN;
 
   __device__ __forceinline__ static void read_one(Frags& f, const ZK_LDS char* lds, int i, int s, int wm, int wn, int lane) {
-    if (i < TN) f.b[i] = Frag<BF, BN, kPerm>::read(lds + PA::kBytes, wn * TN * 16, i, s, lane);
-    else f.a[i - TN] = Frag<AF, BM, false>::read(lds, wm * TM * 16, i - TN, s, lane);
+    if (i < TN) f.b[i] = Frag<BF, BN>::read(lds + PA::kBytes, wn * TN * 16, i, s, lane);
+    else f.a[i - TN] = Frag<AF, BM>::read(lds, wm * TM * 16, i - TN, s, lane);
   }
 
   // The products of `now`; between their rows the reads of `next`, and, with LOAD,
@@ -442,67 +430,65 @@ struct Core {
     }
   }
 
-  // The tile's values, kVec consecutive n of a row at a time.  before(row, first n,
-  // p) starts what the epilogue reads, after(row, first n, values, p) ends it: of
-  // kBatch pieces the reads are under way together.
-  static constexpr int kPieces = TM * TN / (kPerm ? 2 : 1);
-  __device__ __forceinline__ void piece(int c, int m0, int n0, int& row, int& col, float (&v)[kVec]) const {
+  // The tile's values on their way out, eight consecutive n of a row at a time, so
+  // that eight lanes write whole lines.  The sums go through LDS 32 rows of a wave at
+  // a time, in a loop: unrolled, the epilogue of a tile was 40 to 70 KB of code that
+  // each launch fetched anew (24 matrices of 768 x 768: 29 us a symmetric product,
+  // of which the products took 6).  before(row, first n, p) starts what the
+  // epilogue reads, after(row, first n, values, p) ends it; two pieces are under way
+  // together.  With `twice` each value also arrives at its transposed place.
+  static constexpr int kPitch = TN * 64 + 16;      // bytes between rows: 16 rows' 16 bytes lie in different banks
+  static constexpr int kWaveBytes = 32 * kPitch;
+  static_assert(kWaveBytes * WM * WN <= kLds, "the waves' parts fit");
+  template <typename P, bool MIRROR, typename F, typename G>
+  __device__ __forceinline__ void each(ZK_LDS char* lds, int m0, int n0, bool twice, F before, G after) {
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int wm = wave / WN, wn = wave % WN;
-    constexpr int kRow = TN / (kPerm ? 2 : 1);
-    const int i = c / kRow, j = c % kRow * (kPerm ? 2 : 1);
-    row = m0 + (wm * TM + i) * 16 + (lane & 15);
-    col = n0 + (wn * TN + j) * 16 + (lane >> 4) * kVec;
+    constexpr int kRow = TN * 2, kBatch = 2;      // pieces of a row, and under way together
+    ZK_LDS char* mine = lds + wave * kWaveBytes;
+    arrive();               // nobody reads a stage any more
+    m0 += wm * TM * 16;
+    n0 += wn * TN * 16;
+#pragma unroll 1
+    for (int i = 0; i < TM; i += 2, m0 += 32) {
 #pragma unroll
-    for (int x = 0; x < kVec; ++x) v[x] = acc[i][j + x / 4][x % 4];
-  }
-  template <typename P, typename F, typename G>
-  __device__ __forceinline__ void each(int m0, int n0, F before, G after) const {
-    constexpr int kBatch = kPieces < 4 ? kPieces : 4;
+      for (int x = 0; x < 2; ++x)
 #pragma unroll
-    for (int c = 0; c < kPieces; c += kBatch) {
-      P p[kBatch];
-      int row, col;
-      float v[kVec];
+        for (int j = 0; j < TN; ++j)
+          *(ZK_LDS f32x4*)(mine + (x * 16 + (lane & 15)) * kPitch + j * 64 + (lane >> 4) * 16) = acc[x][j];
 #pragma unroll
-      for (int x = 0; x < kBatch; ++x) {
-        piece(c + x, m0, n0, row, col, v);
-        before(row, col, p[x]);
+      for (int x = 2; x < TM; ++x)
+#pragma unroll
+        for (int j = 0; j < TN; ++j) acc[x - 2][j] = acc[x][j];
+#pragma unroll 1
+      for (int u = lane; u < 32 * kRow; u += kBatch * 64) {
+        P p[kBatch];
+#pragma unroll
+        for (int b = 0; b < kBatch; ++b) before(m0 + (u + b * 64) / kRow, n0 + (u + b * 64) % kRow * 8, p[b]);
+#pragma unroll
+        for (int b = 0; b < kBatch; ++b) {
+          const int row = (u + b * 64) / kRow, col = (u + b * 64) % kRow * 8;
+          const ZK_LDS char* at = mine + row * kPitch + col * 4;
+          const f32x4 lo = *(const ZK_LDS f32x4*)at, hi = *(const ZK_LDS f32x4*)(at + 16);
+          const float v[8] = {lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
+          after(m0 + row, n0 + col, v, p[b]);
+        }
       }
+      if constexpr (MIRROR) {
+        if (twice) {
+#pragma unroll 1
+          for (int u = lane; u < 32 * kRow; u += 64) {
+            const int row = n0 + u / 4, col = u % 4 * 8;
+            P p;
+            before(row, m0 + col, p);
+            float v[8];
 #pragma unroll
-      for (int x = 0; x < kBatch; ++x) {
-        piece(c + x, m0, n0, row, col, v);
-        after(row, col, v, p[x]);
+            for (int k = 0; k < 8; ++k) v[k] = *(const ZK_LDS float*)(mine + (col + k) * kPitch + u / 4 * 4);
+            after(row, m0 + col, v, p);
+          }
+        }
       }
     }
-  }
-
-  // A tile's 16-bit values on their way to the transposed place: put() takes what
-  // each() hands out, take(f) then calls f(n, first m, eight values of consecutive
-  // m).  A wave puts and takes its own part of LDS, which nobody reads any more
-  // (arrive() first).
-  static constexpr int kWaveN = TN * 16;
-  static constexpr int kWaveBytes = TM * 16 * kWaveN * 2;
-  static_assert(!DIRECT || kWaveBytes * WM * WN <= kLds, "the waves' parts fit");
-  __device__ __forceinline__ static ZK_LDS char* part_of(ZK_LDS char* lds) {
-    return lds + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6) * kWaveBytes;
-  }
-  template <typename H>
-  __device__ __forceinline__ static void put(ZK_LDS char* lds, int row, int col, H h) {
-    static_assert(sizeof(H) == kVec * 2, "a piece");
-    const int m = row % (TM * 16), n = col % kWaveN;
-    *(ZK_LDS H*)(part_of(lds) + m * (kWaveN * 2) + ((n * 2) ^ (swz_m<kWaveN>(m) * 16))) = h;
-  }
-  template <typename F>
-  __device__ __forceinline__ static void take(ZK_LDS char* lds, int m0, int n0, F f) {
-    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int wm = wave / WN, wn = wave % WN;
-#pragma unroll
-    for (int t = 0; t < TN; ++t)
-#pragma unroll
-      for (int s = 0; s < TM / 2; ++s)
-        f(n0 + (wn * TN + t) * 16 + (lane & 15), m0 + wm * TM * 16 + s * 32 + (lane >> 4) * 8,
-          Frag<kFormM, kWaveN, false>::read(part_of(lds), 0, t, s, lane));
   }
 };
 

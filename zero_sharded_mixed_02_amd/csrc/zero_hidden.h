@@ -86,6 +86,7 @@ struct OrthoArgs {
   const void* add;        // kPoly: A - shift I; kNext: X
   int64_t ldo, ldadd;
   int32_t batch, epi;
+  int32_t tall;           // rows > cols: A = X^T X, and X A
   int32_t upper;          // the result is symmetric: tiles on and above the diagonal only
   int32_t first;          // X as loaded: the factor applies, and add is 16-bit
   int32_t last, dst_dt;   // the result goes to dst
@@ -123,7 +124,7 @@ int launch_weight_grad(const WeightGradArgs& a, int dt, int tile, bool direct, i
 int launch_weight_grad_join(const WeightGradArgs& a, int64_t blocks, void* stream);
 int launch_ortho_norm(const OrthoLoadArgs& a, int dt, void* stream);
 int launch_ortho_load(const OrthoLoadArgs& a, int dt, int64_t blocks, void* stream);
-int launch_ortho(const OrthoArgs& a, int form_a, int form_b, int tile, int64_t blocks, void* stream);
+int launch_ortho(const OrthoArgs& a, int tile, int64_t blocks, void* stream);
 int launch_ortho_join(const OrthoArgs& a, int64_t blocks, void* stream);
 int launch_act_grad(const ActGradArgs& a, int dt, int64_t blocks, void* stream);
 

@@ -320,7 +320,7 @@ int64_t ortho_bytes(const std::vector<Group>& groups) {
 }
 
 // One product of a step over the batch.
-zero_status run_ortho(OrthoArgs& a, int form_a, int form_b, int64_t m, int64_t n, int64_t k, const Pick& c, void* part, void* stream) {
+zero_status run_ortho(OrthoArgs& a, int64_t m, int64_t n, int64_t k, const Pick& c, void* part, void* stream) {
   lay_out(a.p, m, n, k, c);
   a.upper = a.epi != kNext && a.p.splits == 1;
   if (a.upper) {
@@ -332,7 +332,7 @@ zero_status run_ortho(OrthoArgs& a, int form_a, int form_b, int64_t m, int64_t n
   const int64_t joins = a.p.splits > 1 ? a.batch * ceil_div((int64_t)a.p.m * (a.p.n_pad / 4), kJoinThreads) : 0;
   if (zero_status st = check_grid(blocks, kTileThreads[c.tile])) return st;
   if (zero_status st = check_grid(joins, kJoinThreads)) return st;
-  if (const int err = launch_ortho(a, form_a, form_b, c.tile, blocks, stream)) return hip_fail(err);
+  if (const int err = launch_ortho(a, c.tile, blocks, stream)) return hip_fail(err);
   if (joins == 0) return ok();
   return launched(launch_ortho_join(a, joins, stream));
 }
@@ -366,6 +366,7 @@ zero_status ortho_batch(const Group& g, const OrthoSpace& s, int64_t first, int6
   memset(&a, 0, sizeof a);
   a.factor = l.factor;
   a.batch = (int32_t)batch;
+  a.tall = tall;
   a.rows = (int32_t)g.rows;
   a.cols = (int32_t)g.cols;
   a.dst = dst;
@@ -392,8 +393,7 @@ zero_status ortho_batch(const Group& g, const OrthoSpace& s, int64_t first, int6
     a.out = ws + s.gram;
     a.ldo = s.ldn;
     a.zout = s.zn;
-    const int form = tall ? 1 : 0;
-    if (zero_status st = run_ortho(a, form, form, s.side, s.side, wide, s.c[kGram], ws + s.part, stream)) return st;
+    if (zero_status st = run_ortho(a, s.side, s.side, wide, s.c[kGram], ws + s.part, stream)) return st;
     // B
     a.epi = kPoly;
     a.p.a = a.p.b = ws + s.gram;
@@ -403,7 +403,7 @@ zero_status ortho_batch(const Group& g, const OrthoSpace& s, int64_t first, int6
     a.ldadd = s.ldn;
     a.zadd = s.zn;
     a.out = ws + s.poly;
-    if (zero_status st = run_ortho(a, 0, 0, s.side, s.side, s.side, s.c[kPoly], ws + s.part, stream)) return st;
+    if (zero_status st = run_ortho(a, s.side, s.side, s.side, s.c[kPoly], ws + s.part, stream)) return st;
     // a X + B X, or a X + X B
     a.epi = kNext;
     a.last = step + 1 == poly.steps;
@@ -420,7 +420,7 @@ zero_status ortho_batch(const Group& g, const OrthoSpace& s, int64_t first, int6
     a.out = next;
     a.ldo = s.ldx;
     a.zout = s.zx;
-    if (zero_status st = run_ortho(a, 0, tall ? 0 : 1, s.rows_pad, s.ldx, s.side, s.c[kNext], ws + s.part, stream)) return st;
+    if (zero_status st = run_ortho(a, s.rows_pad, s.ldx, s.side, s.c[kNext], ws + s.part, stream)) return st;
     std::swap(x, next);
   }
   return ok();

@@ -70,12 +70,13 @@ __device__ __forceinline__ void run_tile(C& core, ZK_LDS char* lds, const Produc
   const int k_end = p.k - k0 < p.k_piece ? p.k : k0 + p.k_piece;
   core.run(lds, p.a, p.lda, p.m, p.b, p.ldb, p.n, im * bm, in * bn, k0, k_end);
   if (p.part) {
-    core.template each<int>(im * bm, in * bn, [](int, int, int&) {}, [&](int row, int col, const float (&v)[C::kVec], int) {
-      if (row < p.m && col < p.n) store_part<C::kVec>(p, p.part, split, row, col, v);
+    core.template each<int, false>(lds, im * bm, in * bn, false, [](int, int, int&) {}, [&](int row, int col, const float (&v)[8], int) {
+      if (row < p.m && col < p.n) store_part<8>(p, p.part, split, row, col, v);
     });
   } else {
-    core.template each<P>(im * bm, in * bn, [&](int row, int col, P& x) { if (row < p.m && col < p.n) before(row, col, x); },
-                          [&](int row, int col, const float (&v)[C::kVec], const P& x) {
+    core.template each<P, false>(lds, im * bm, in * bn, false,
+                          [&](int row, int col, P& x) { if (row < p.m && col < p.n) before(row, col, x); },
+                          [&](int row, int col, const float (&v)[8], const P& x) {
                             if (row < p.m && col < p.n) after(row, col, v, x);
                           });
   }
@@ -87,10 +88,10 @@ __global__ void __launch_bounds__(kTileThreads[TILE]) linear_kernel(const Linear
   typedef CoreOf<T, kFormK, EPI == 0 ? kFormK : kFormM, TILE, DIRECT> C;
   extern __shared__ __attribute__((aligned(1024))) char smem[];
   C core;
-  typedef Epilogue<T, EPI, C::kVec> E;
+  typedef Epilogue<T, EPI, 8> E;
   run_tile<E>(core, (ZK_LDS char*)smem, a.p, blockIdx.x, gridDim.x, Shape<TILE>::BM, Shape<TILE>::BN,
               [&](int row, int col, E& e) { e.load(a, row, col); },
-              [&](int row, int col, const float (&v)[C::kVec], const E& e) { e.finish(a, row, col, v); });
+              [&](int row, int col, const float (&v)[8], const E& e) { e.finish(a, row, col, v); });
 }
 
 template <typename T, int EPI>
@@ -205,7 +206,7 @@ __global__ void __launch_bounds__(kTileThreads[TILE]) weight_grad_kernel(const W
   C core;
   run_tile<int>(core, (ZK_LDS char*)smem, a.p, b, gridDim.x - a.bias_blocks, Shape<TILE>::BM, Shape<TILE>::BN,
                 [](int, int, int&) {},
-                [&](int row, int col, const float (&v)[C::kVec], int) { finish_weight<C::kVec>(a, row, col, v); });
+                [&](int row, int col, const float (&v)[8], int) { finish_weight<8>(a, row, col, v); });
 }
 
 __global__ void __launch_bounds__(kJoinThreads) weight_grad_join_kernel(const WeightGradArgs a) {

@@ -91,35 +91,33 @@ __global__ void __launch_bounds__(kLoadThreads) ortho_load_kernel(const OrthoLoa
 __device__ __forceinline__ float factor_of(const OrthoArgs& a, int z) { return a.first ? a.factor[2 * z] : 1.0f; }
 __device__ __forceinline__ float shift_of(const OrthoArgs& a, int z) { return a.shift * a.factor[2 * z + 1]; }
 
-// What the epilogue of V sums of a row reads, and the epilogue.
-template <int V>
+// What the epilogue of V sums of a row reads, and the epilogue.  Rows in the
+// workspace are whole eights and 16-byte aligned.
+template <int EPI, int V>
 struct Epilogue {
   Row<_Float16, V> half;          // kPoly's A - d I; the first X
-  f32x4 full[V / 4];              // X later on
+  f32x4 full[EPI == kNext ? V / 4 : 1];      // X later on
   typedef typename Row<_Float16, V>::tv Half;
 
   __device__ __forceinline__ void load(const OrthoArgs& a, int z, int row, int col) {
-    if (a.epi == kGram) return;
+    if constexpr (EPI == kGram) return;
     const int64_t e = z * a.zadd + (int64_t)row * a.ldadd + col;
-    if (a.epi == kPoly || a.first) {
-      half.load(a.add, e, a.p.n - col);
-    } else {
+    if (EPI == kPoly || a.first) {
+      half.load(a.add, e, V);
+    } else if constexpr (EPI == kNext) {
 #pragma unroll
-      for (int i = 0; i < V; i += 4)      // rows are padded to whole fours
-        full[i / 4] = col + i < a.p.n ? *(const AS1 f32x4*)((const AS1 float*)a.add + e + i) : f32x4{0.f, 0.f, 0.f, 0.f};
+      for (int i = 0; i < V; i += 4) full[i / 4] = *(const AS1 f32x4*)((const AS1 float*)a.add + e + i);
     }
   }
 
-  // Returns the 16-bit result.
-  __device__ __forceinline__ Half finish(const OrthoArgs& a, int z, int row, int col, const float (&acc)[V]) const {
-    const int have = a.p.n - col;
+  __device__ __forceinline__ void finish(const OrthoArgs& a, int z, int row, int col, const float (&acc)[V]) const {
     float v[V];
     Half h = {};
-    if (a.epi == kGram) {
+    if constexpr (EPI == kGram) {
       const float f = factor_of(a, z), f2 = f * f, d = shift_of(a, z);
 #pragma unroll
       for (int i = 0; i < V; ++i) v[i] = __builtin_fmaf(f2, acc[i], row == col + i ? -d : 0.0f);
-    } else if (a.epi == kPoly) {
+    } else if constexpr (EPI == kPoly) {
       const float b = __builtin_fmaf(2.0f * a.c, shift_of(a, z), a.b);
 #pragma unroll
       for (int i = 0; i < V; ++i) v[i] = __builtin_fmaf(a.c, acc[i], b * (float)half.v[i]);
@@ -137,24 +135,19 @@ struct Epilogue {
           if (a.dst_dt == ZERO_BF16) store_row<__bf16, V>(a.dst, d, a.cols - col, v);
           else store_row<_Float16, V>(a.dst, d, a.cols - col, v);
         }
-        return h;
+        return;
       }
       AS1 float* p = (AS1 float*)a.out32 + z * a.zadd + (int64_t)row * a.ldadd + col;
 #pragma unroll
-      for (int i = 0; i < V; i += 4)
-        if (col + i < a.p.n) *(AS1 f32x4*)(p + i) = f32x4{v[i], v[i + 1], v[i + 2], v[i + 3]};
+      for (int i = 0; i < V; i += 4) *(AS1 f32x4*)(p + i) = f32x4{v[i], v[i + 1], v[i + 2], v[i + 3]};
     }
 #pragma unroll
     for (int i = 0; i < V; ++i) h[i] = (_Float16)v[i];
-    // p.n, ldo and col are multiples of V or 4 apart: a piece is whole, or its first half is.
-    AS1 _Float16* out = (AS1 _Float16*)a.out + z * a.zout + (int64_t)row * a.ldo + col;
-    if (have >= V) *(AS1 Half*)out = h;
-    else store_row<_Float16, V>(a.out, z * a.zout + (int64_t)row * a.ldo + col, have, v);
-    return h;
+    *(AS1 Half*)((AS1 _Float16*)a.out + z * a.zout + (int64_t)row * a.ldo + col) = h;
   }
 };
 
-template <int AF, int BF, int TILE>
+template <int EPI, int AF, int BF, int TILE>
 __global__ void __launch_bounds__(kTileThreads[TILE]) ortho_kernel(const OrthoArgs a) {
   typedef CoreOf<_Float16, AF, BF, TILE, true> C;
   extern __shared__ __attribute__((aligned(1024))) char smem[];
@@ -169,27 +162,23 @@ __global__ void __launch_bounds__(kTileThreads[TILE]) ortho_kernel(const OrthoAr
            a.p.n, im * BM, in * BN, k0, k_end);
   if (a.p.part) {
     float* part = a.p.part + (int64_t)z * a.p.splits * a.p.m * a.p.n_pad;
-    core.template each<int>(im * BM, in * BN, [](int, int, int&) {}, [&](int row, int col, const float (&v)[C::kVec], int) {
-      if (row < a.p.m && col < a.p.n) store_part<C::kVec>(a.p, part, split, row, col, v);
-    });
+    core.template each<int, false>((ZK_LDS char*)smem, im * BM, in * BN, false, [](int, int, int&) {},
+                            [&](int row, int col, const float (&v)[8], int) {
+                              if (row < a.p.m && col < a.p.n) store_part<8>(a.p, part, split, row, col, v);
+                            });
     return;
   }
-  typedef Epilogue<C::kVec> E;
-  const bool twice = a.upper && im != in;     // the mirrored tile too
-  if (twice) C::arrive();
-  core.template each<E>(im * BM, in * BN, [&](int row, int col, E& e) { if (row < a.p.m && col < a.p.n) e.load(a, z, row, col); },
-                        [&](int row, int col, const float (&v)[C::kVec], const E& e) {
-                          typename E::Half h = {};
-                          if (row < a.p.m && col < a.p.n) h = e.finish(a, z, row, col, v);
-                          if (twice) C::put((ZK_LDS char*)smem, row, col, h);
+  // A tile above the diagonal stands for its mirror image too, whose epilogue is the
+  // same (what kPoly adds is symmetric).
+  typedef Epilogue<EPI, 8> E;
+  core.template each<E, EPI != kNext>((ZK_LDS char*)smem, im * BM, in * BN, a.upper && im != in,
+                        [&](int row, int col, E& e) { if (row < a.p.m && col < a.p.n) e.load(a, z, row, col); },
+                        [&](int row, int col, const float (&v)[8], const E& e) {
+                          if (row < a.p.m && col < a.p.n) e.finish(a, z, row, col, v);
                         });
-  if (twice) {
-    C::take((ZK_LDS char*)smem, im * BM, in * BN, [&](int n, int m, s16x8 h) {
-      if (n < a.p.n && m < a.p.m) *(AS1 s16x8*)((AS1 _Float16*)a.out + z * a.zout + (int64_t)n * a.ldo + m) = h;
-    });
-  }
 }
 
+template <int EPI>
 __global__ void __launch_bounds__(kJoinThreads) ortho_join_kernel(const OrthoArgs a) {
   const int64_t per = ((int64_t)a.p.m * (a.p.n_pad >> 2) + kJoinThreads - 1) / kJoinThreads;
   const int z = (int)(blockIdx.x / per);
@@ -197,19 +186,21 @@ __global__ void __launch_bounds__(kJoinThreads) ortho_join_kernel(const OrthoArg
   float v[4];
   if (join4(a.p, a.p.part + (int64_t)z * a.p.splits * a.p.m * a.p.n_pad, (blockIdx.x - z * per) * kJoinThreads + threadIdx.x, row,
             col, v)) {
-    Epilogue<4> e;
+    Epilogue<EPI, 4> e;
     e.load(a, z, row, col);
     e.finish(a, z, row, col, v);
   }
 }
 
-template <int AF, int BF>
+template <int EPI, int AF, int BF, int TILE>
+int go(const OrthoArgs& a, int64_t blocks, void* stream) {
+  return launch(&ortho_kernel<EPI, AF, BF, TILE>, a, blocks, kTileThreads[TILE], CoreOf<_Float16, AF, BF, TILE, true>::kLds, stream);
+}
+template <int EPI, int AF, int BF>
 int go(const OrthoArgs& a, int tile, int64_t blocks, void* stream) {
-  if (tile == kTile256)
-    return launch(&ortho_kernel<AF, BF, kTile256>, a, blocks, 512, CoreOf<_Float16, AF, BF, kTile256, true>::kLds, stream);
-  if (tile == kTile128)
-    return launch(&ortho_kernel<AF, BF, kTile128>, a, blocks, 256, CoreOf<_Float16, AF, BF, kTile128, true>::kLds, stream);
-  return launch(&ortho_kernel<AF, BF, kTile64>, a, blocks, 256, CoreOf<_Float16, AF, BF, kTile64, true>::kLds, stream);
+  if (tile == kTile256) return go<EPI, AF, BF, kTile256>(a, blocks, stream);
+  if (tile == kTile128) return go<EPI, AF, BF, kTile128>(a, blocks, stream);
+  return go<EPI, AF, BF, kTile64>(a, blocks, stream);
 }
 
 }  // namespace
@@ -225,13 +216,17 @@ int launch_ortho_load(const OrthoLoadArgs& a, int dt, int64_t blocks, void* stre
                          : launch(&ortho_load_kernel<_Float16>, a, blocks, kLoadThreads, 0, stream);
 }
 
-int launch_ortho(const OrthoArgs& a, int form_a, int form_b, int tile, int64_t blocks, void* stream) {
-  if (form_a == kFormM) return go<kFormM, kFormM>(a, tile, blocks, stream);
-  return form_b == kFormM ? go<kFormK, kFormM>(a, tile, blocks, stream) : go<kFormK, kFormK>(a, tile, blocks, stream);
+int launch_ortho(const OrthoArgs& a, int tile, int64_t blocks, void* stream) {
+  if (a.epi == kGram)
+    return a.tall ? go<kGram, kFormM, kFormM>(a, tile, blocks, stream) : go<kGram, kFormK, kFormK>(a, tile, blocks, stream);
+  if (a.epi == kPoly) return go<kPoly, kFormK, kFormK>(a, tile, blocks, stream);
+  return a.tall ? go<kNext, kFormK, kFormK>(a, tile, blocks, stream) : go<kNext, kFormK, kFormM>(a, tile, blocks, stream);
 }
 
 int launch_ortho_join(const OrthoArgs& a, int64_t blocks, void* stream) {
-  return launch(&ortho_join_kernel, a, blocks, kJoinThreads, 0, stream);
+  if (a.epi == kGram) return launch(&ortho_join_kernel<kGram>, a, blocks, kJoinThreads, 0, stream);
+  if (a.epi == kPoly) return launch(&ortho_join_kernel<kPoly>, a, blocks, kJoinThreads, 0, stream);
+  return launch(&ortho_join_kernel<kNext>, a, blocks, kJoinThreads, 0, stream);
 }
 
 }  // namespace hidden
