@@ -433,22 +433,26 @@ struct Core {
   // The tile's values on their way out, eight consecutive n of a row at a time, so
   // that eight lanes write whole lines.  The sums go through LDS 32 rows of a wave at
   // a time, in a loop: unrolled, the epilogue of a tile was 40 to 70 KB of code that
-  // each launch fetched anew (24 matrices of 768 x 768: 29 us a symmetric product,
-  // of which the products took 6).  before(row, first n, p) starts what the
-  // epilogue reads, after(row, first n, values, p) ends it; two pieces are under way
-  // together.  With `twice` each value also arrives at its transposed place.
+  // each launch fetched anew.  before(row, first n, p) starts what the epilogue
+  // reads, 32 rows ahead; after(row, first n, values, p) ends it and leaves the
+  // finished values, which with `twice` mirror(row, first n, values) takes to the
+  // transposed place.
   static constexpr int kPitch = TN * 64 + 16;      // bytes between rows: 16 rows' 16 bytes lie in different banks
   static constexpr int kWaveBytes = 32 * kPitch;
   static_assert(kWaveBytes * WM * WN <= kLds, "the waves' parts fit");
-  template <typename P, bool MIRROR, typename F, typename G>
-  __device__ __forceinline__ void each(ZK_LDS char* lds, int m0, int n0, bool twice, F before, G after) {
+  template <typename P, typename F, typename G, typename H>
+  __device__ __forceinline__ void each(ZK_LDS char* lds, int m0, int n0, bool twice, F before, G after, H mirror) {
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int wm = wave / WN, wn = wave % WN;
-    constexpr int kRow = TN * 2, kBatch = 2;      // pieces of a row, and under way together
+    constexpr int kRow = TN * 2, kN = 32 * kRow / 64;      // pieces of a row, and of a lane in 32 rows
     ZK_LDS char* mine = lds + wave * kWaveBytes;
-    arrive();               // nobody reads a stage any more
-    m0 += wm * TM * 16;
+    m0 += wm * TM * 16 + lane / kRow;
     n0 += wn * TN * 16;
+    const int col = n0 + lane % kRow * 8;
+    P p[kN];
+#pragma unroll
+    for (int b = 0; b < kN; ++b) before(m0 + b * (64 / kRow), col, p[b]);
+    arrive();               // nobody reads a stage any more
 #pragma unroll 1
     for (int i = 0; i < TM; i += 2, m0 += 32) {
 #pragma unroll
@@ -460,31 +464,35 @@ struct Core {
       for (int x = 2; x < TM; ++x)
 #pragma unroll
         for (int j = 0; j < TN; ++j) acc[x - 2][j] = acc[x][j];
-#pragma unroll 1
-      for (int u = lane; u < 32 * kRow; u += kBatch * 64) {
-        P p[kBatch];
+      P q[kN];
+      if (i + 2 < TM) {
 #pragma unroll
-        for (int b = 0; b < kBatch; ++b) before(m0 + (u + b * 64) / kRow, n0 + (u + b * 64) % kRow * 8, p[b]);
-#pragma unroll
-        for (int b = 0; b < kBatch; ++b) {
-          const int row = (u + b * 64) / kRow, col = (u + b * 64) % kRow * 8;
-          const ZK_LDS char* at = mine + row * kPitch + col * 4;
-          const f32x4 lo = *(const ZK_LDS f32x4*)at, hi = *(const ZK_LDS f32x4*)(at + 16);
-          const float v[8] = {lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
-          after(m0 + row, n0 + col, v, p[b]);
-        }
+        for (int b = 0; b < kN; ++b) before(m0 + 32 + b * (64 / kRow), col, q[b]);
       }
-      if constexpr (MIRROR) {
+      ZK_LDS char* at = mine + lane / kRow * kPitch + lane % kRow * 32;
+#pragma unroll
+      for (int b = 0; b < kN; ++b) {
+        const f32x4 lo = *(ZK_LDS f32x4*)at, hi = *(ZK_LDS f32x4*)(at + 16);
+        float v[8] = {lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
+        after(m0 + b * (64 / kRow), col, v, p[b]);
+        if constexpr (!__is_same(H, int)) {
+          if (twice) {
+            *(ZK_LDS f32x4*)at = f32x4{v[0], v[1], v[2], v[3]};
+            *(ZK_LDS f32x4*)(at + 16) = f32x4{v[4], v[5], v[6], v[7]};
+          }
+        }
+        at += 64 / kRow * kPitch;
+        p[b] = q[b];
+      }
+      if constexpr (!__is_same(H, int)) {
         if (twice) {
-#pragma unroll 1
-          for (int u = lane; u < 32 * kRow; u += 64) {
-            const int row = n0 + u / 4, col = u % 4 * 8;
-            P p;
-            before(row, m0 + col, p);
+          const int first = m0 - lane / kRow + lane % 4 * 8;
+#pragma unroll 2
+          for (int n = lane / 4; n < TN * 16; n += 16) {
             float v[8];
 #pragma unroll
-            for (int k = 0; k < 8; ++k) v[k] = *(const ZK_LDS float*)(mine + (col + k) * kPitch + u / 4 * 4);
-            after(row, m0 + col, v, p);
+            for (int k = 0; k < 8; ++k) v[k] = *(const ZK_LDS float*)(mine + (lane % 4 * 8 + k) * kPitch + n * 4);
+            mirror(n0 + n, first, v);
           }
         }
       }

@@ -70,15 +70,15 @@ __device__ __forceinline__ void run_tile(C& core, ZK_LDS char* lds, const Produc
   const int k_end = p.k - k0 < p.k_piece ? p.k : k0 + p.k_piece;
   core.run(lds, p.a, p.lda, p.m, p.b, p.ldb, p.n, im * bm, in * bn, k0, k_end);
   if (p.part) {
-    core.template each<int, false>(lds, im * bm, in * bn, false, [](int, int, int&) {}, [&](int row, int col, const float (&v)[8], int) {
+    core.template each<int>(lds, im * bm, in * bn, false, [](int, int, int&) {}, [&](int row, int col, const float (&v)[8], int) {
       if (row < p.m && col < p.n) store_part<8>(p, p.part, split, row, col, v);
-    });
+    }, 0);
   } else {
-    core.template each<P, false>(lds, im * bm, in * bn, false,
+    core.template each<P>(lds, im * bm, in * bn, false,
                           [&](int row, int col, P& x) { if (row < p.m && col < p.n) before(row, col, x); },
                           [&](int row, int col, const float (&v)[8], const P& x) {
                             if (row < p.m && col < p.n) after(row, col, v, x);
-                          });
+                          }, 0);
   }
 }
 

@@ -91,41 +91,53 @@ __global__ void __launch_bounds__(kLoadThreads) ortho_load_kernel(const OrthoLoa
 __device__ __forceinline__ float factor_of(const OrthoArgs& a, int z) { return a.first ? a.factor[2 * z] : 1.0f; }
 __device__ __forceinline__ float shift_of(const OrthoArgs& a, int z) { return a.shift * a.factor[2 * z + 1]; }
 
-// What the epilogue of V sums of a row reads, and the epilogue.  Rows in the
-// workspace are whole eights and 16-byte aligned.
+template <int V>
+__device__ __forceinline__ void store_half(void* base, int64_t e, const float (&v)[V]) {
+  typename Row<_Float16, V>::tv h;
+#pragma unroll
+  for (int i = 0; i < V; ++i) h[i] = (_Float16)v[i];
+  *(AS1 typename Row<_Float16, V>::tv*)((AS1 _Float16*)base + e) = h;
+}
+
+// What the epilogue of V sums of a row reads, and the epilogue, which leaves the
+// finished values in place of the sums.  Rows in the workspace are whole eights and
+// 16-byte aligned.
 template <int EPI, int V>
 struct Epilogue {
-  Row<_Float16, V> half;          // kPoly's A - d I; the first X
-  f32x4 full[EPI == kNext ? V / 4 : 1];      // X later on
   typedef typename Row<_Float16, V>::tv Half;
+  // kPoly: A - d I (V halves); kNext: X, at first as V halves.
+  f32x4 x[EPI == kNext ? V / 4 : 1];
 
   __device__ __forceinline__ void load(const OrthoArgs& a, int z, int row, int col) {
     if constexpr (EPI == kGram) return;
     const int64_t e = z * a.zadd + (int64_t)row * a.ldadd + col;
     if (EPI == kPoly || a.first) {
-      half.load(a.add, e, V);
+      __builtin_memcpy(&x[0], (const AS1 _Float16*)a.add + e, V * 2);
     } else if constexpr (EPI == kNext) {
 #pragma unroll
-      for (int i = 0; i < V; i += 4) full[i / 4] = *(const AS1 f32x4*)((const AS1 float*)a.add + e + i);
+      for (int i = 0; i < V; i += 4) x[i / 4] = *(const AS1 f32x4*)((const AS1 float*)a.add + e + i);
     }
   }
+  __device__ __forceinline__ float half(int i) const {
+    Half h;
+    __builtin_memcpy(&h, &x[0], V * 2);
+    return (float)h[i];
+  }
 
-  __device__ __forceinline__ void finish(const OrthoArgs& a, int z, int row, int col, const float (&acc)[V]) const {
-    float v[V];
-    Half h = {};
+  __device__ __forceinline__ void finish(const OrthoArgs& a, int z, int row, int col, float (&v)[V]) const {
     if constexpr (EPI == kGram) {
       const float f = factor_of(a, z), f2 = f * f, d = shift_of(a, z);
 #pragma unroll
-      for (int i = 0; i < V; ++i) v[i] = __builtin_fmaf(f2, acc[i], row == col + i ? -d : 0.0f);
+      for (int i = 0; i < V; ++i) v[i] = __builtin_fmaf(f2, v[i], row == col + i ? -d : 0.0f);
     } else if constexpr (EPI == kPoly) {
       const float b = __builtin_fmaf(2.0f * a.c, shift_of(a, z), a.b);
 #pragma unroll
-      for (int i = 0; i < V; ++i) v[i] = __builtin_fmaf(a.c, acc[i], b * (float)half.v[i]);
+      for (int i = 0; i < V; ++i) v[i] = __builtin_fmaf(a.c, v[i], b * half(i));
     } else {
       const float f = factor_of(a, z), d = shift_of(a, z);
       const float c0 = __builtin_fmaf(__builtin_fmaf(a.c, d, a.b), d, a.a);
 #pragma unroll
-      for (int i = 0; i < V; ++i) v[i] = f * __builtin_fmaf(c0, a.first ? (float)half.v[i] : full[i / 4][i % 4], acc[i]);
+      for (int i = 0; i < V; ++i) v[i] = f * __builtin_fmaf(c0, a.first ? half(i) : x[i / 4][i % 4], v[i]);
       if (a.last) {
         if (row < a.rows && col < a.cols) {
           const float s = a.scale[z];
@@ -141,9 +153,7 @@ struct Epilogue {
 #pragma unroll
       for (int i = 0; i < V; i += 4) *(AS1 f32x4*)(p + i) = f32x4{v[i], v[i + 1], v[i + 2], v[i + 3]};
     }
-#pragma unroll
-    for (int i = 0; i < V; ++i) h[i] = (_Float16)v[i];
-    *(AS1 Half*)((AS1 _Float16*)a.out + z * a.zout + (int64_t)row * a.ldo + col) = h;
+    store_half<V>(a.out, z * a.zout + (int64_t)row * a.ldo + col, v);
   }
 };
 
@@ -162,20 +172,26 @@ __global__ void __launch_bounds__(kTileThreads[TILE]) ortho_kernel(const OrthoAr
            a.p.n, im * BM, in * BN, k0, k_end);
   if (a.p.part) {
     float* part = a.p.part + (int64_t)z * a.p.splits * a.p.m * a.p.n_pad;
-    core.template each<int, false>((ZK_LDS char*)smem, im * BM, in * BN, false, [](int, int, int&) {},
+    core.template each<int>((ZK_LDS char*)smem, im * BM, in * BN, false, [](int, int, int&) {},
                             [&](int row, int col, const float (&v)[8], int) {
                               if (row < a.p.m && col < a.p.n) store_part<8>(a.p, part, split, row, col, v);
-                            });
+                            }, 0);
     return;
   }
-  // A tile above the diagonal stands for its mirror image too, whose epilogue is the
-  // same (what kPoly adds is symmetric).
   typedef Epilogue<EPI, 8> E;
-  core.template each<E, EPI != kNext>((ZK_LDS char*)smem, im * BM, in * BN, a.upper && im != in,
-                        [&](int row, int col, E& e) { if (row < a.p.m && col < a.p.n) e.load(a, z, row, col); },
-                        [&](int row, int col, const float (&v)[8], const E& e) {
-                          if (row < a.p.m && col < a.p.n) e.finish(a, z, row, col, v);
-                        });
+  const auto before = [&](int row, int col, E& e) { if (row < a.p.m && col < a.p.n) e.load(a, z, row, col); };
+  const auto after = [&](int row, int col, float (&v)[8], const E& e) {
+    if (row < a.p.m && col < a.p.n) e.finish(a, z, row, col, v);
+  };
+  if constexpr (EPI == kNext) {
+    core.template each<E>((ZK_LDS char*)smem, im * BM, in * BN, false, before, after, 0);
+  } else {
+    // A tile above the diagonal stands for its mirror image too.
+    core.template each<E>((ZK_LDS char*)smem, im * BM, in * BN, a.upper && im != in, before, after,
+                          [&](int row, int col, const float (&v)[8]) {
+                            if (row < a.p.m && col < a.p.n) store_half<8>(a.out, z * a.zout + (int64_t)row * a.ldo + col, v);
+                          });
+  }
 }
 
 template <int EPI>
