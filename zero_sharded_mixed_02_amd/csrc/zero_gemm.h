@@ -470,11 +470,11 @@ struct Core {
         for (int b = 0; b < kN; ++b) before(m0 + 32 + b * (64 / kRow), col, q[b]);
       }
       ZK_LDS char* at = mine + lane / kRow * kPitch + lane % kRow * 32;
-#pragma unroll
+#pragma unroll 1
       for (int b = 0; b < kN; ++b) {
         const f32x4 lo = *(ZK_LDS f32x4*)at, hi = *(ZK_LDS f32x4*)(at + 16);
         float v[8] = {lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
-        after(m0 + b * (64 / kRow), col, v, p[b]);
+        after(m0 + b * (64 / kRow), col, v, p[0]);
         if constexpr (!__is_same(H, int)) {
           if (twice) {
             *(ZK_LDS f32x4*)at = f32x4{v[0], v[1], v[2], v[3]};
@@ -482,8 +482,11 @@ struct Core {
           }
         }
         at += 64 / kRow * kPitch;
-        p[b] = q[b];
+#pragma unroll
+        for (int x = 1; x < kN; ++x) p[x - 1] = p[x];
       }
+#pragma unroll
+      for (int b = 0; b < kN; ++b) p[b] = q[b];
       if constexpr (!__is_same(H, int)) {
         if (twice) {
           const int first = m0 - lane / kRow + lane % 4 * 8;
