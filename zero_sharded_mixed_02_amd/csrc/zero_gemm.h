@@ -437,6 +437,10 @@ struct Core {
   // reads, 32 rows ahead; after(row, first n, values, p) ends it and leaves the
   // finished values, which with `twice` mirror(row, first n, values) takes to the
   // transposed place.
+  // The first of a lane's eight columns, the same in all its pieces.
+  __device__ __forceinline__ static int column(int n0) {
+    return n0 + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6) % WN * TN * 16 + (threadIdx.x & 63) % (TN * 2) * 8;
+  }
   static constexpr int kPitch = TN * 64 + 16;      // bytes between rows: 16 rows' 16 bytes lie in different banks
   static constexpr int kWaveBytes = 32 * kPitch;
   static_assert(kWaveBytes * WM * WN <= kLds, "the waves' parts fit");
@@ -446,9 +450,9 @@ struct Core {
     const int wm = wave / WN, wn = wave % WN;
     constexpr int kRow = TN * 2, kN = 32 * kRow / 64;      // pieces of a row, and of a lane in 32 rows
     ZK_LDS char* mine = lds + wave * kWaveBytes;
+    const int col = column(n0);
     m0 += wm * TM * 16 + lane / kRow;
     n0 += wn * TN * 16;
-    const int col = n0 + lane % kRow * 8;
     P p[kN];
 #pragma unroll
     for (int b = 0; b < kN; ++b) before(m0 + b * (64 / kRow), col, p[b]);

@@ -24,13 +24,14 @@ struct Product {
   const void* b;
   int64_t lda, ldb;       // elements between memory rows
   int32_t m, n, k;
-  int32_t tm, tn;         // tiles
-  int32_t splits;         // pieces of k
-  int32_t k_piece;        // elements of a piece, a multiple of the stage depth
-  int32_t tiles;          // tm * tn
-  float* part;            // fp32[splits][m][n_pad]: partial sums, or NULL
-  int32_t n_pad;          // n rounded up to 4
+  int32_t tm, tn, tiles;  // of one result: rows, columns, how many are computed
+  int32_t size;           // rows and columns of a tile
+  int32_t whole;          // tiles (over all results) summed in one piece; the others ("cut") in
+  int32_t cut;            //   `splits` pieces of k,
+  int32_t splits;
+  int32_t k_piece;        //   of so many elements, a multiple of the stage depth
   int32_t pad_;
+  float* part;            // fp32[cut][splits][size][size]: partial sums
 };
 
 // zero_linear (EPI 0) and zero_linear_input_grad (EPI 1).
@@ -78,7 +79,7 @@ constexpr int kMaxBatch = 128;
 enum OrthoEpi : int { kGram = 0, kPoly = 1, kNext = 2 };
 
 struct OrthoArgs {
-  Product p;              // of one matrix; part: fp32[batch][splits][m][n_pad]
+  Product p;              // of one matrix
   int64_t za, zb, zout, zadd;
   const float* factor;    // fp32[batch][2]: what the first X is to be multiplied by, and whether to shift
   void* out;              // 16-bit result in the workspace, rows of ldo
@@ -87,7 +88,6 @@ struct OrthoArgs {
   int64_t ldo, ldadd;
   int32_t batch, epi;
   int32_t tall;           // rows > cols: A = X^T X, and X A
-  int32_t upper;          // the result is symmetric: tiles on and above the diagonal only
   int32_t first;          // X as loaded: the factor applies, and add is 16-bit
   int32_t last, dst_dt;   // the result goes to dst
   float a, b, c, shift;   // d = shift or 0: kGram: factor^2 sum - d I; kPoly: (b + 2 c d) add + c sum;

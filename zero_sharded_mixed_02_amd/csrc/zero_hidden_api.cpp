@@ -32,57 +32,81 @@ int64_t round_up(int64_t n, int64_t to) { return ceil_div(n, to) * to; }
 // Time of a product's launch in us, from what a stage takes on one CU: `alone`
 // with one workgroup there, `full` for each of `slots` that share it.
 struct TileCost { double alone, full; int slots; };
-constexpr TileCost kCost[kTiles] = {{1.85, 1.85, 1}, {0.75, 0.52, 2}, {0.45, 0.21, 4}};
+constexpr TileCost kCost[kTiles] = {{1.35, 1.70, 1}, {0.72, 0.55, 2}, {0.45, 0.21, 4}};
 constexpr int kCus = 256;
-constexpr double kTileStart = 2.5;       // us: the first loads and the epilogue
+constexpr double kTileStart = 3.0;       // us: the first loads and the epilogue
 constexpr double kJoinStart = 4.0;       // us: a launch that joins pieces of k
 constexpr double kPartRate = 3.5e6;      // bytes a us, written and read again
 
 double cost_of(int tile, int64_t tiles, int64_t stages) {
   const TileCost& c = kCost[tile];
   const int64_t per_cu = ceil_div(tiles, kCus), rounds = per_cu / c.slots, rest = per_cu % c.slots;
+  const double full = rounds ? c.full : c.alone;     // a chip of one round runs at a higher clock
   const double last = rest ? std::max(c.alone, rest * c.full) : 0.0;
-  return (double)stages * ((double)rounds * c.slots * c.full + last) + kTileStart * (double)(rounds + (rest ? 1 : 0));
+  return (double)stages * ((double)rounds * c.slots * full + last) + kTileStart * (double)(rounds + (rest ? 1 : 0));
 }
 
-int64_t tiles_of(int tile, int64_t m, int64_t n) { return ceil_div(m, kTileSize[tile]) * ceil_div(n, kTileSize[tile]); }
+// How a product is cut into workgroups: `whole` tiles in one piece, the others in
+// `splits` pieces of k.
+struct Pick {
+  int tile;
+  int64_t whole, cut;
+  int splits;
+  double us;
+};
 
-struct Pick { int tile, splits; double us; };
+int64_t part_bytes(const Pick& c) { return c.splits > 1 ? c.cut * c.splits * kTileSize[c.tile] * kTileSize[c.tile] * 4 : 0; }
 
-// Tile and pieces of k of `batch` products.  splits > 0 is kept.
+double join_cost(int tile, int64_t tiles, int64_t splits) {
+  return kJoinStart + (double)(tiles * kTileSize[tile]) * kTileSize[tile] * 4.0 * (double)(splits + 1) / kPartRate;
+}
+
+// For `batch` products of m x n x k.  With splits > 0 every tile is cut into so many
+// pieces.  Otherwise all tiles are cut alike, or only those of a last round that
+// would leave most CUs idle.
 Pick pick(int64_t m, int64_t n, int64_t k, int64_t batch, int splits, bool upper = false) {
   const int64_t stages = std::max<int64_t>(1, ceil_div(k, kStage));
-  Pick best = {kTile64, 1, 1e300};
+  Pick best = {kTile64, 0, 0, 1, 1e300};
   for (int tile = 0; tile < kTiles; ++tile) {
-    int64_t tiles = batch * tiles_of(tile, m, n);
-    const int64_t side = ceil_div(m, kTileSize[tile]);
+    const int64_t tm = ceil_div(m, kTileSize[tile]), tn = ceil_div(n, kTileSize[tile]);
+    const int64_t tiles = batch * (upper ? tm * (tm + 1) / 2 : tm * tn);
     for (int64_t s = splits ? splits : 1; s <= (splits ? splits : 64); s *= 2) {
       if (!splits && s > 1 && stages / s < 4) break;    // a piece has four stages or more
       const int64_t per = ceil_div(stages, s), now = ceil_div(stages, per);
-      const int64_t t = upper && now == 1 ? batch * side * (side + 1) / 2 : tiles;
-      double us = cost_of(tile, t * now, per);
-      if (now > 1) us += kJoinStart + (double)(batch * m) * (double)n * 4.0 * (double)(now + 1) / kPartRate;
-      if (us < best.us) best = {tile, (int)now, us};
+      double us = cost_of(tile, tiles * now, per);
+      if (now > 1) us += join_cost(tile, tiles, now);
+      if (us < best.us) best = now > 1 ? Pick{tile, 0, tiles, (int)now, us} : Pick{tile, tiles, 0, 1, us};
     }
+    const int64_t slots = (int64_t)kCus * kCost[tile].slots, whole = tiles / slots * slots, rest = tiles - whole;
+    if (splits || whole == 0 || rest == 0) continue;
+    const int64_t s = std::min(slots / rest, stages / 4);
+    if (s < 2) continue;
+    const int64_t per = ceil_div(stages, s), now = ceil_div(stages, per);
+    const double us = cost_of(tile, whole, stages) + cost_of(tile, rest * now, per) + join_cost(tile, rest, now);
+    if (now > 1 && us < best.us) best = {tile, whole, rest, (int)now, us};
   }
   return best;
 }
 
-void lay_out(Product& p, int64_t m, int64_t n, int64_t k, const Pick& c) {
+void lay_out(Product& p, int64_t m, int64_t n, int64_t k, const Pick& c, void* part, bool upper = false) {
   const int64_t stages = std::max<int64_t>(1, ceil_div(k, kStage)), per = ceil_div(stages, c.splits);
   p.m = (int32_t)m;
   p.n = (int32_t)n;
   p.k = (int32_t)k;
-  p.tm = (int32_t)ceil_div(m, kTileSize[c.tile]);
-  p.tn = (int32_t)ceil_div(n, kTileSize[c.tile]);
-  p.tiles = (int32_t)std::min<int64_t>(INT32_MAX, (int64_t)p.tm * p.tn);
+  p.size = kTileSize[c.tile];
+  p.tm = (int32_t)ceil_div(m, p.size);
+  p.tn = (int32_t)ceil_div(n, p.size);
+  p.tiles = (int32_t)std::min<int64_t>(INT32_MAX, upper ? (int64_t)p.tm * (p.tm + 1) / 2 : (int64_t)p.tm * p.tn);
+  p.whole = (int32_t)std::min<int64_t>(INT32_MAX, c.whole);
+  p.cut = (int32_t)std::min<int64_t>(INT32_MAX, c.cut);
+  p.splits = c.splits;
   p.k_piece = (int32_t)(per * kStage);
-  p.splits = (int32_t)ceil_div(stages, per);
-  p.n_pad = (int32_t)round_up(n, 4);
+  p.part = (float*)part;
 }
 
-int64_t part_bytes(int64_t m, int64_t n, int splits) {
-  return splits > 1 ? (int64_t)splits * m * round_up(n, 4) * 4 : 0;
+int64_t blocks_of(const Pick& c) { return c.whole + c.cut * c.splits; }
+int64_t joins_of(const Pick& c) {
+  return c.splits > 1 ? ceil_div(c.cut * kTileSize[c.tile] * (kTileSize[c.tile] / 4), kJoinThreads) : 0;
 }
 
 zero_status check_grid(int64_t blocks, int threads) {
@@ -181,10 +205,26 @@ int64_t bias_chunk(int64_t n, int64_t out_features) {
   return std::max<int64_t>(32, ceil_div(n, want));
 }
 
+// Pieces of k where every tile is to have the same.
+int alike(int64_t m, int64_t n, int64_t k) {
+  const int64_t stages = std::max<int64_t>(1, ceil_div(k, kStage));
+  double us = 1e300;
+  int best = 1;
+  for (int64_t s = 1; s <= 64 && (s == 1 || stages / s >= 4); s *= 2) {
+    const Pick c = pick(m, n, k, 1, (int)s);
+    if (c.us < us) {
+      us = c.us;
+      best = c.splits;
+    }
+  }
+  return best;
+}
+
 struct WeightShape {
   int64_t lo, hi, at;       // elements of the weight, and their place in dst
   int64_t row0, rows;
   int splits;
+  Pick c;
   int64_t part, bias_part;  // bytes
 };
 
@@ -196,19 +236,19 @@ WeightShape weight_shape(const zero_plan_s& p, int32_t weight, int64_t in_featur
     s.row0 = s.lo / in_features / 8 * 8;
     s.rows = std::min(round_up((s.hi - 1) / in_features + 1, 8), out_features) - s.row0;
   }
-  // The pieces of k follow from the whole weight, so that a slice's sums are
-  // those of the full buffer.
-  s.splits = pick(out_features, in_features, n, 1, 0).splits;
-  s.part = part_bytes(s.rows, in_features, s.splits);
+  // The pieces of k follow from the whole weight, and every tile has the same, so that
+  // a slice's sums are those of the full buffer.
+  s.splits = alike(out_features, in_features, n);
+  s.c = s.rows > 0 ? pick(s.rows, in_features, n, 1, s.splits) : Pick{kTile64, 0, 0, 1, 0.0};
+  s.part = part_bytes(s.c);
   s.bias_part = round_up(ceil_div(n, bias_chunk(n, out_features)) * out_features * 4, 16);
   return s;
 }
 
-zero_status run_linear(LinearArgs& a, int epi, int dt, const Pick& c, bool direct, void* ws, void* stream) {
-  if (zero_status st = check_grid((int64_t)a.p.tm * a.p.tn * a.p.splits, kTileThreads[c.tile])) return st;
-  const int64_t joins = a.p.splits > 1 ? ceil_div((int64_t)a.p.m * (a.p.n_pad / 4), kJoinThreads) : 0;
+zero_status run_linear(LinearArgs& a, int epi, int dt, const Pick& c, bool direct, void* stream) {
+  const int64_t joins = joins_of(c);
+  if (zero_status st = check_grid(blocks_of(c), kTileThreads[c.tile])) return st;
   if (zero_status st = check_grid(joins, kJoinThreads)) return st;
-  a.p.part = a.p.splits > 1 ? (float*)ws : nullptr;
   if (const int err = launch_linear(a, epi, dt, c.tile, direct, stream)) return hip_fail(err);
   if (joins == 0) return ok();
   return launched(launch_linear_join(a, epi, dt, joins, stream));
@@ -272,8 +312,7 @@ OrthoSpace ortho_space(int64_t rows, int64_t cols, int64_t batch) {
   s.x32 = take(batch * s.zx * 4);
   s.gram = take(batch * s.zn * 2);
   s.poly = take(batch * s.zn * 2);
-  s.part = take(batch * std::max({part_bytes(s.side, s.side, s.c[kGram].splits), part_bytes(s.side, s.side, s.c[kPoly].splits),
-                                  part_bytes(s.rows_pad, s.ldx, s.c[kNext].splits)}));
+  s.part = take(std::max({part_bytes(s.c[kGram]), part_bytes(s.c[kPoly]), part_bytes(s.c[kNext])}));
   s.total = at;
   return s;
 }
@@ -319,20 +358,20 @@ int64_t ortho_bytes(const std::vector<Group>& groups) {
   return most;
 }
 
-// One product of a step over the batch.
+// One product of a step over the batch.  A last batch of fewer matrices is laid out
+// as the others are, with as many tiles whole as it has.
 zero_status run_ortho(OrthoArgs& a, int64_t m, int64_t n, int64_t k, const Pick& c, void* part, void* stream) {
-  lay_out(a.p, m, n, k, c);
-  a.upper = a.epi != kNext && a.p.splits == 1;
-  if (a.upper) {
-    const int64_t t = a.p.tm;
-    a.p.tiles = (int32_t)std::min<int64_t>(INT32_MAX, t * (t + 1) / 2);
-  }
-  a.p.part = a.p.splits > 1 ? (float*)part : nullptr;
-  const int64_t blocks = (int64_t)a.batch * a.p.tiles * a.p.splits;
-  const int64_t joins = a.p.splits > 1 ? a.batch * ceil_div((int64_t)a.p.m * (a.p.n_pad / 4), kJoinThreads) : 0;
-  if (zero_status st = check_grid(blocks, kTileThreads[c.tile])) return st;
+  lay_out(a.p, m, n, k, c, part, a.epi != kNext);
+  Pick now = c;
+  const int64_t tiles = (int64_t)a.batch * a.p.tiles;
+  now.whole = std::min(c.whole, tiles);
+  now.cut = tiles - now.whole;
+  a.p.whole = (int32_t)now.whole;
+  a.p.cut = (int32_t)now.cut;
+  const int64_t joins = joins_of(now);
+  if (zero_status st = check_grid(blocks_of(now), kTileThreads[c.tile])) return st;
   if (zero_status st = check_grid(joins, kJoinThreads)) return st;
-  if (const int err = launch_ortho(a, c.tile, blocks, stream)) return hip_fail(err);
+  if (const int err = launch_ortho(a, c.tile, blocks_of(now), stream)) return hip_fail(err);
   if (joins == 0) return ok();
   return launched(launch_ortho_join(a, joins, stream));
 }
@@ -433,7 +472,7 @@ extern "C" {
 size_t zero_linear_workspace_bytes(zero_plan_t p, int32_t weight, int64_t in_features, int64_t n) {
   int64_t out;
   if (weight_of(p, weight, in_features, out) || check_n(n) || n == 0 || out == 0) return 0;
-  return (size_t)part_bytes(n, out, pick(n, out, in_features, 1, 0).splits);
+  return (size_t)part_bytes(pick(n, out, in_features, 1, 0));
 }
 
 zero_status zero_linear(zero_plan_t p, int32_t weight, int32_t bias, int64_t in_features, const void* params, zero_dtype dt,
@@ -456,7 +495,7 @@ zero_status zero_linear(zero_plan_t p, int32_t weight, int32_t bias, int64_t in_
     if (pre)
       if (zero_status st = check_rows(pre, n, out, pre_stride, false, "pre", rp)) return st;
     const Pick c = pick(n, out, in_features, 1, 0);
-    const size_t need = n && out ? (size_t)part_bytes(n, out, c.splits) : 0;
+    const size_t need = n && out ? (size_t)part_bytes(c) : 0;
     if (zero_status st = check_workspace(workspace, ws_bytes, need)) return st;
     std::vector<Range> reads = {range_of(params, p->psi_pad, 2, "params"), rx};
     std::vector<Range> writes = {ry, rp, range_of(workspace, (int64_t)need, 1, "workspace")};
@@ -471,7 +510,7 @@ zero_status zero_linear(zero_plan_t p, int32_t weight, int32_t bias, int64_t in_
     a.p.b = (const char*)params + p->t_off[weight] * 2;
     a.p.lda = n > 1 ? x_stride : round_up(in_features, 2);     // a single row has no neighbour
     a.p.ldb = in_features;
-    lay_out(a.p, n, out, in_features, c);
+    lay_out(a.p, n, out, in_features, c, workspace);
     a.out = y;
     a.pre_out = pre;
     a.add = residual;
@@ -481,14 +520,14 @@ zero_status zero_linear(zero_plan_t p, int32_t weight, int32_t bias, int64_t in_
     a.ldadd = residual_stride;
     a.act = act;
     const bool direct = direct_k(a.p.a, a.p.lda) && direct_k(a.p.b, a.p.ldb);
-    return run_linear(a, 0, dt, c, direct, workspace, stream);
+    return run_linear(a, 0, dt, c, direct, stream);
   });
 }
 
 size_t zero_linear_input_grad_workspace_bytes(zero_plan_t p, int32_t weight, int64_t in_features, int64_t n) {
   int64_t out;
   if (weight_of(p, weight, in_features, out) || check_n(n) || n == 0) return 0;
-  return (size_t)part_bytes(n, in_features, pick(n, in_features, out, 1, 0).splits);
+  return (size_t)part_bytes(pick(n, in_features, out, 1, 0));
 }
 
 zero_status zero_linear_input_grad(zero_plan_t p, int32_t weight, int64_t in_features, const void* params, zero_dtype dt,
@@ -513,7 +552,7 @@ zero_status zero_linear_input_grad(zero_plan_t p, int32_t weight, int64_t in_fea
     if (pre)
       if (zero_status st = check_rows(pre, n, in_features, pre_stride, false, "pre", rp)) return st;
     const Pick c = pick(n, in_features, out, 1, 0);
-    const size_t need = n ? (size_t)part_bytes(n, in_features, c.splits) : 0;
+    const size_t need = n ? (size_t)part_bytes(c) : 0;
     if (zero_status st = check_workspace(workspace, ws_bytes, need)) return st;
     std::vector<Range> writes = {rx, range_of(workspace, (int64_t)need, 1, "workspace")};
     if (zero_status st = check_disjoint(writes, {range_of(params, p->psi_pad, 2, "params"), rz, rp})) return st;
@@ -527,7 +566,7 @@ zero_status zero_linear_input_grad(zero_plan_t p, int32_t weight, int64_t in_fea
     a.p.b = (const char*)params + p->t_off[weight] * 2;
     a.p.lda = n > 1 ? dz_stride : round_up(std::max<int64_t>(out, 1), 2);
     a.p.ldb = in_features;
-    lay_out(a.p, n, in_features, out, c);
+    lay_out(a.p, n, in_features, out, c, workspace);
     a.out = dx;
     a.pre_in = pre;
     a.add = addend;
@@ -536,7 +575,7 @@ zero_status zero_linear_input_grad(zero_plan_t p, int32_t weight, int64_t in_fea
     a.ldadd = addend_stride;
     a.act = act;
     const bool direct = direct_k(a.p.a, a.p.lda) && direct_m(a.p.b, a.p.ldb, in_features);
-    return run_linear(a, 1, dt, c, direct, workspace, stream);
+    return run_linear(a, 1, dt, c, direct, stream);
   });
 }
 
@@ -578,23 +617,19 @@ zero_status zero_linear_weight_grad(zero_plan_t p, int32_t weight, int32_t bias,
     const WeightShape s = weight_shape(*p, weight, in_features, out, n, rank);
     WeightGradArgs a;
     memset(&a, 0, sizeof a);
-    Pick c = {kTile64, 1, 0.0};
+    const Pick& c = s.c;
     a.dst_dt = dst_dt;
     a.accumulate = accumulate;
     a.scale = (float)scale;
     a.row0 = (int32_t)s.row0;
     a.lo = s.lo;
     a.hi = s.hi;
-    if (s.rows > 0) {
-      c = pick(s.rows, in_features, n, 1, s.splits);
-      a.dst = (char*)dst + s.at * esize(dst_dt);
-    }
+    if (s.rows > 0) a.dst = (char*)dst + s.at * esize(dst_dt);
     a.p.a = (const char*)dz + s.row0 * 2;
     a.p.b = x;
     a.p.lda = n > 1 ? dz_stride : round_up(out, 2);
     a.p.ldb = n > 1 ? x_stride : round_up(in_features, 2);
-    lay_out(a.p, s.rows, in_features, n, c);
-    a.p.part = a.p.splits > 1 ? (float*)workspace : nullptr;
+    lay_out(a.p, s.rows, in_features, n, c, workspace);
     if (bias >= 0) {
       int64_t lo, hi, at;
       part_of_tensor(*p, bias, rank, lo, hi, at);
@@ -610,9 +645,9 @@ zero_status zero_linear_weight_grad(zero_plan_t p, int32_t weight, int32_t bias,
         a.bias_blocks = a.chunks * a.col_blocks;
       }
     }
-    const int64_t blocks = a.bias_blocks + (int64_t)a.p.tm * a.p.tn * a.p.splits;
+    const int64_t blocks = a.bias_blocks + blocks_of(c);
     if (blocks == 0) return ok();
-    a.join_blocks = a.p.splits > 1 ? (int32_t)std::min<int64_t>(INT32_MAX, ceil_div((int64_t)a.p.m * (a.p.n_pad / 4), kJoinThreads)) : 0;
+    a.join_blocks = (int32_t)std::min<int64_t>(INT32_MAX, joins_of(c));
     const int64_t joins = a.join_blocks + (a.bias_blocks && a.chunks > 1 ? ceil_div(a.b_hi - a.b_lo, kJoinThreads) : 0);
     if (zero_status st = check_grid(blocks, kTileThreads[c.tile])) return st;
     if (zero_status st = check_grid(joins, kJoinThreads)) return st;

@@ -84,22 +84,87 @@ struct Shape<kTile64> { static constexpr int BM = 64, BN = 64, WM = 2, WN = 2; }
 template <typename T, int AF, int BF, int TILE, bool DIRECT>
 using CoreOf = Core<T, AF, BF, Shape<TILE>::BM, Shape<TILE>::BN, Shape<TILE>::WM, Shape<TILE>::WN, DIRECT>;
 
-template <int V>
-__device__ __forceinline__ void store_part(const Product& p, float* part, int split, int row, int col, const float* v) {
-  AS1 float* d = (AS1 float*)(part + ((int64_t)split * p.m + row) * p.n_pad + col);
-#pragma unroll
-  for (int i = 0; i < V; i += 4)
-    if (col + i < p.n) *(AS1 f32x4*)(d + i) = f32x4{v[i], v[i + 1], v[i + 2], v[i + 3]};
+// The work of one workgroup: a tile, whole or a piece of k of it.
+struct Work {
+  int z, im, in;        // which result, which tile
+  int cut, split;       // which of the cut tiles (-1: whole), which piece
+  int k0, k_end;
+};
+
+// UPPER: the result is symmetric, tiles on and above the diagonal only.
+template <bool UPPER>
+__device__ __forceinline__ void tile_at(const Product& p, int t, int& z, int& im, int& in) {
+  z = t / p.tiles;
+  if constexpr (UPPER) place_upper(t - z * p.tiles, im, in);
+  else place(t - z * p.tiles, p.tm, p.tn, im, in);
 }
 
-// Four columns of a row from the pieces' sums, in the order of the pieces.
-__device__ __forceinline__ bool join4(const Product& p, const float* part, int64_t unit, int& row, int& col, float (&v)[4]) {
-  const int upr = p.n_pad >> 2;
-  if (unit >= (int64_t)p.m * upr) return false;
-  row = (int)(unit / upr);
-  col = (int)(unit - (int64_t)row * upr) * 4;
-  const AS1 f32x4* s = (const AS1 f32x4*)(part + (int64_t)row * p.n_pad + col);
-  const int64_t step = (int64_t)p.m * p.n_pad / 4;
+template <bool UPPER>
+__device__ __forceinline__ Work work_of(const Product& p, int b) {
+  Work w;
+  int tile;
+  if (b < p.whole) {
+    tile = die_order(b, p.whole);
+    w.cut = -1;
+    w.split = 0;
+    w.k0 = 0;
+    w.k_end = p.k;
+  } else {
+    // Pieces of one k lie together, so that a die's workgroups read the same rows.
+    const int t = die_order(b - p.whole, p.cut * p.splits);
+    w.split = t / p.cut;
+    w.cut = t - w.split * p.cut;
+    tile = p.whole + w.cut;
+    w.k0 = w.split * p.k_piece;
+    w.k_end = p.k - w.k0 < p.k_piece ? p.k : w.k0 + p.k_piece;
+  }
+  tile_at<UPPER>(p, tile, w.z, w.im, w.in);
+  w.z = __builtin_amdgcn_readfirstlane(w.z);       // the root leaves them in vector registers
+  w.im = __builtin_amdgcn_readfirstlane(w.im);
+  w.in = __builtin_amdgcn_readfirstlane(w.in);
+  return w;
+}
+
+__device__ __forceinline__ void store_part(const Product& p, const Work& w, int row, int col, const float (&v)[8]) {
+  AS1 float* d = (AS1 float*)p.part + (((int64_t)w.cut * p.splits + w.split) * p.size + (row - w.im * p.size)) * p.size + (col - w.in * p.size);
+  *(AS1 f32x4*)d = f32x4{v[0], v[1], v[2], v[3]};
+  *(AS1 f32x4*)(d + 4) = f32x4{v[4], v[5], v[6], v[7]};
+}
+
+// Sums a workgroup's work (operands of several results za and zb elements apart);
+// partial sums go where they are joined from.  Returns whether the tile is whole:
+// tile (m0, n0) of result z.
+template <bool UPPER, typename C>
+__device__ __forceinline__ bool run_tile(C& core, ZK_LDS char* lds, const Product& p, int b, int64_t za, int64_t zb, int& z, int& m0,
+                                         int& n0) {
+  const Work w = work_of<UPPER>(p, b);
+  z = w.z;
+  m0 = w.im * p.size;
+  n0 = w.in * p.size;
+  core.run(lds, (const uint16_t*)p.a + z * za, p.lda, p.m, (const uint16_t*)p.b + z * zb, p.ldb, p.n, m0, n0, w.k0, w.k_end);
+  if (w.cut < 0) return true;
+  core.template each<int>(lds, m0, n0, false, [](int, int, int&) {}, [&](int row, int col, const float (&v)[8], int) {
+    if (row < p.m && col < p.n) store_part(p, w, row, col, v);
+  }, 0);
+  return false;
+}
+
+// Four columns of a row of a cut tile from its pieces' sums, in the order of the
+// pieces.
+template <bool UPPER>
+__device__ __forceinline__ bool join4(const Product& p, int64_t unit, int& z, int& row, int& col, float (&v)[4], bool& twice) {
+  const int upr = p.size >> 2, per = p.size * upr;
+  const int cut = (int)(unit / per), u = (int)(unit - (int64_t)cut * per);
+  if (cut >= p.cut) return false;
+  int im, in;
+  tile_at<UPPER>(p, p.whole + cut, z, im, in);
+  const int r = u / upr, c = u % upr * 4;
+  row = im * p.size + r;
+  col = in * p.size + c;
+  twice = UPPER && im != in;
+  if (row >= p.m || col >= p.n) return false;
+  const AS1 f32x4* s = (const AS1 f32x4*)((const AS1 float*)p.part + ((int64_t)cut * p.splits * p.size + r) * p.size + c);
+  const int64_t step = (int64_t)p.size * upr;
   f32x4 t = s[0];
   for (int i = 1; i < p.splits; ++i) {
     s += step;

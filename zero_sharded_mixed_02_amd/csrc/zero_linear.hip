@@ -13,23 +13,23 @@ namespace {
 
 using namespace zk::gemm;
 
-// What the epilogue of V sums of row `row` from column `col` on reads, and the
-// epilogue.  One rounding to 16 bits, of the finished value.
+// What the epilogue of V sums of row `row` from column `col` on reads (the bias, of
+// the same columns for all of a lane's rows, comes from outside), and the epilogue.
+// One rounding to 16 bits, of the finished value.
 template <typename T, int EPI, int V>
 struct Epilogue {
-  Row<T, V> side, add;      // the bias or the activation's argument; the residual or addend
+  Row<T, V> pre[EPI];       // the activation's argument
+  Row<T, V> add;            // the residual or addend
 
   __device__ __forceinline__ void load(const LinearArgs& a, int64_t row, int col) {
     const int have = a.p.n - col;
-    if constexpr (EPI == 0) {
-      if (a.bias) side.load(a.bias, col, have);
-    } else {
-      if (a.pre_in) side.load(a.pre_in, row * a.ldpre + col, have);
+    if constexpr (EPI == 1) {
+      if (a.pre_in) pre[0].load(a.pre_in, row * a.ldpre + col, have);
     }
     if (a.add) add.load(a.add, row * a.ldadd + col, have);
   }
 
-  __device__ __forceinline__ void finish(const LinearArgs& a, int64_t row, int col, const float (&acc)[V]) const {
+  __device__ __forceinline__ void finish(const LinearArgs& a, int64_t row, int col, const float (&acc)[V], const Row<T, V>& bias) const {
     const int have = a.p.n - col;
     float v[V];
 #pragma unroll
@@ -37,7 +37,7 @@ struct Epilogue {
     if constexpr (EPI == 0) {
       if (a.bias) {
 #pragma unroll
-        for (int i = 0; i < V; ++i) v[i] += (float)side.v[i];
+        for (int i = 0; i < V; ++i) v[i] += (float)bias.v[i];
       }
       if (a.pre_out) store_row<T, V>(a.pre_out, row * a.ldpre + col, have, v);
       if (a.act != ZERO_ACT_NONE) {
@@ -47,7 +47,7 @@ struct Epilogue {
     } else {
       if (a.pre_in) {
 #pragma unroll
-        for (int i = 0; i < V; ++i) v[i] *= act::slope(a.act, (float)side.v[i]);
+        for (int i = 0; i < V; ++i) v[i] *= act::slope(a.act, (float)pre[0].v[i]);
       }
     }
     if (a.add) {
@@ -58,50 +58,35 @@ struct Epilogue {
   }
 };
 
-// Runs the tile of workgroup b; its values go to the partial sums, or through
-// before() and after().
-template <typename P, typename C, typename F, typename G>
-__device__ __forceinline__ void run_tile(C& core, ZK_LDS char* lds, const Product& p, int b, int n_blocks, int bm, int bn,
-                                         F before, G after) {
-  int im, in;
-  const int t = die_order(b, n_blocks), split = t / p.tiles;
-  place(t - split * p.tiles, p.tm, p.tn, im, in);
-  const int k0 = split * p.k_piece;
-  const int k_end = p.k - k0 < p.k_piece ? p.k : k0 + p.k_piece;
-  core.run(lds, p.a, p.lda, p.m, p.b, p.ldb, p.n, im * bm, in * bn, k0, k_end);
-  if (p.part) {
-    core.template each<int>(lds, im * bm, in * bn, false, [](int, int, int&) {}, [&](int row, int col, const float (&v)[8], int) {
-      if (row < p.m && col < p.n) store_part<8>(p, p.part, split, row, col, v);
-    }, 0);
-  } else {
-    core.template each<P>(lds, im * bm, in * bn, false,
-                          [&](int row, int col, P& x) { if (row < p.m && col < p.n) before(row, col, x); },
-                          [&](int row, int col, const float (&v)[8], const P& x) {
-                            if (row < p.m && col < p.n) after(row, col, v, x);
-                          }, 0);
-  }
-}
-
 // EPI 0: forms K and K; EPI 1: K and M.
 template <typename T, int EPI, int TILE, bool DIRECT>
 __global__ void __launch_bounds__(kTileThreads[TILE]) linear_kernel(const LinearArgs a) {
   typedef CoreOf<T, kFormK, EPI == 0 ? kFormK : kFormM, TILE, DIRECT> C;
   extern __shared__ __attribute__((aligned(1024))) char smem[];
   C core;
+  int z, m0, n0;
+  if (!run_tile<false>(core, (ZK_LDS char*)smem, a.p, blockIdx.x, 0, 0, z, m0, n0)) return;
   typedef Epilogue<T, EPI, 8> E;
-  run_tile<E>(core, (ZK_LDS char*)smem, a.p, blockIdx.x, gridDim.x, Shape<TILE>::BM, Shape<TILE>::BN,
-              [&](int row, int col, E& e) { e.load(a, row, col); },
-              [&](int row, int col, const float (&v)[8], const E& e) { e.finish(a, row, col, v); });
+  Row<T, 8> bias;
+  if (EPI == 0 && a.bias) bias.load(a.bias, C::column(n0), a.p.n - C::column(n0));
+  core.template each<E>((ZK_LDS char*)smem, m0, n0, false,
+                        [&](int row, int col, E& e) { if (row < a.p.m && col < a.p.n) e.load(a, row, col); },
+                        [&](int row, int col, const float (&v)[8], const E& e) {
+                          if (row < a.p.m && col < a.p.n) e.finish(a, row, col, v, bias);
+                        }, 0);
 }
 
 template <typename T, int EPI>
 __global__ void __launch_bounds__(kJoinThreads) linear_join_kernel(const LinearArgs a) {
-  int row, col;
+  int z, row, col;
+  bool twice;
   float v[4];
-  if (join4(a.p, a.p.part, (int64_t)blockIdx.x * kJoinThreads + threadIdx.x, row, col, v)) {
+  if (join4<false>(a.p, (int64_t)blockIdx.x * kJoinThreads + threadIdx.x, z, row, col, v, twice)) {
     Epilogue<T, EPI, 4> e;
+    Row<T, 4> bias;
+    if (EPI == 0 && a.bias) bias.load(a.bias, col, a.p.n - col);
     e.load(a, row, col);
-    e.finish(a, row, col, v);
+    e.finish(a, row, col, v, bias);
   }
 }
 
@@ -204,16 +189,20 @@ __global__ void __launch_bounds__(kTileThreads[TILE]) weight_grad_kernel(const W
     return;
   }
   C core;
-  run_tile<int>(core, (ZK_LDS char*)smem, a.p, b, gridDim.x - a.bias_blocks, Shape<TILE>::BM, Shape<TILE>::BN,
-                [](int, int, int&) {},
-                [&](int row, int col, const float (&v)[8], int) { finish_weight<8>(a, row, col, v); });
+  int z, m0, n0;
+  if (!run_tile<false>(core, (ZK_LDS char*)smem, a.p, b, 0, 0, z, m0, n0)) return;
+  core.template each<int>((ZK_LDS char*)smem, m0, n0, false, [](int, int, int&) {},
+                          [&](int row, int col, const float (&v)[8], int) {
+                            if (row < a.p.m && col < a.p.n) finish_weight<8>(a, row, col, v);
+                          }, 0);
 }
 
 __global__ void __launch_bounds__(kJoinThreads) weight_grad_join_kernel(const WeightGradArgs a) {
   if ((int)blockIdx.x < a.join_blocks) {
-    int row, col;
+    int z, row, col;
+    bool twice;
     float v[4];
-    if (join4(a.p, a.p.part, (int64_t)blockIdx.x * kJoinThreads + threadIdx.x, row, col, v)) finish_weight<4>(a, row, col, v);
+    if (join4<false>(a.p, (int64_t)blockIdx.x * kJoinThreads + threadIdx.x, z, row, col, v, twice)) finish_weight<4>(a, row, col, v);
     return;
   }
   const int cols = a.b_hi - a.b_lo;
@@ -247,7 +236,7 @@ __global__ void __launch_bounds__(kActThreads) act_grad_kernel(const ActGradArgs
 
 template <typename T, int EPI, int TILE, bool DIRECT>
 int go_linear(const LinearArgs& a, void* stream) {
-  return launch(&linear_kernel<T, EPI, TILE, DIRECT>, a, (int64_t)a.p.tiles * a.p.splits, kTileThreads[TILE],
+  return launch(&linear_kernel<T, EPI, TILE, DIRECT>, a, a.p.whole + (int64_t)a.p.cut * a.p.splits, kTileThreads[TILE],
                 CoreOf<T, kFormK, EPI == 0 ? kFormK : kFormM, TILE, DIRECT>::kLds, stream);
 }
 template <typename T, int EPI, int TILE>

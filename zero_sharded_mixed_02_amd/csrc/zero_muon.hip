@@ -161,33 +161,19 @@ template <int EPI, int AF, int BF, int TILE>
 __global__ void __launch_bounds__(kTileThreads[TILE]) ortho_kernel(const OrthoArgs a) {
   typedef CoreOf<_Float16, AF, BF, TILE, true> C;
   extern __shared__ __attribute__((aligned(1024))) char smem[];
-  constexpr int BM = Shape<TILE>::BM, BN = Shape<TILE>::BN;
-  const int t = die_order(blockIdx.x, gridDim.x), piece = t / a.p.tiles, z = piece / a.p.splits, split = piece - z * a.p.splits;
-  int im, in;
-  if (a.upper) place_upper(t - piece * a.p.tiles, im, in);
-  else place(t - piece * a.p.tiles, a.p.tm, a.p.tn, im, in);
-  const int k0 = split * a.p.k_piece, k_end = a.p.k - k0 < a.p.k_piece ? a.p.k : k0 + a.p.k_piece;
   C core;
-  core.run((ZK_LDS char*)smem, (const _Float16*)a.p.a + z * a.za, a.p.lda, a.p.m, (const _Float16*)a.p.b + z * a.zb, a.p.ldb,
-           a.p.n, im * BM, in * BN, k0, k_end);
-  if (a.p.part) {
-    float* part = a.p.part + (int64_t)z * a.p.splits * a.p.m * a.p.n_pad;
-    core.template each<int>((ZK_LDS char*)smem, im * BM, in * BN, false, [](int, int, int&) {},
-                            [&](int row, int col, const float (&v)[8], int) {
-                              if (row < a.p.m && col < a.p.n) store_part<8>(a.p, part, split, row, col, v);
-                            }, 0);
-    return;
-  }
+  int z, m0, n0;
+  if (!run_tile<EPI != kNext>(core, (ZK_LDS char*)smem, a.p, blockIdx.x, a.za, a.zb, z, m0, n0)) return;
   typedef Epilogue<EPI, 8> E;
   const auto before = [&](int row, int col, E& e) { if (row < a.p.m && col < a.p.n) e.load(a, z, row, col); };
   const auto after = [&](int row, int col, float (&v)[8], const E& e) {
     if (row < a.p.m && col < a.p.n) e.finish(a, z, row, col, v);
   };
   if constexpr (EPI == kNext) {
-    core.template each<E>((ZK_LDS char*)smem, im * BM, in * BN, false, before, after, 0);
+    core.template each<E>((ZK_LDS char*)smem, m0, n0, false, before, after, 0);
   } else {
     // A tile above the diagonal stands for its mirror image too.
-    core.template each<E>((ZK_LDS char*)smem, im * BM, in * BN, a.upper && im != in, before, after,
+    core.template each<E>((ZK_LDS char*)smem, m0, n0, m0 != n0, before, after,
                           [&](int row, int col, const float (&v)[8]) {
                             if (row < a.p.m && col < a.p.n) store_half<8>(a.out, z * a.zout + (int64_t)row * a.ldo + col, v);
                           });
@@ -196,15 +182,17 @@ __global__ void __launch_bounds__(kTileThreads[TILE]) ortho_kernel(const OrthoAr
 
 template <int EPI>
 __global__ void __launch_bounds__(kJoinThreads) ortho_join_kernel(const OrthoArgs a) {
-  const int64_t per = ((int64_t)a.p.m * (a.p.n_pad >> 2) + kJoinThreads - 1) / kJoinThreads;
-  const int z = (int)(blockIdx.x / per);
-  int row, col;
+  int z, row, col;
+  bool twice;
   float v[4];
-  if (join4(a.p, a.p.part + (int64_t)z * a.p.splits * a.p.m * a.p.n_pad, (blockIdx.x - z * per) * kJoinThreads + threadIdx.x, row,
-            col, v)) {
+  if (join4<EPI != kNext>(a.p, (int64_t)blockIdx.x * kJoinThreads + threadIdx.x, z, row, col, v, twice)) {
     Epilogue<EPI, 4> e;
     e.load(a, z, row, col);
     e.finish(a, z, row, col, v);
+    if (EPI != kNext && twice) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) ((AS1 _Float16*)a.out)[z * a.zout + (int64_t)(col + i) * a.ldo + row] = (_Float16)v[i];
+    }
   }
 }
 
