@@ -666,7 +666,7 @@ ZERO_API zero_status zero_linear_input_grad(zero_plan_t plan, int32_t weight, in
  * rank's contribution to zero_shard_reduce, zero_adam_step or
  * zero_muon_momentum, written where those read it.
  *   dW[o, j] = scale * sum_i dz[i, o] x[i, j],  db[o] = scale * sum_i dz[i, o]
- *   The sums are fp32, in an order fixed by n and the weight's shape; each
+ *   The sums are fp32, in an order fixed by n, the weight's shape and n_d; each
  *   value is rounded once.  Neither the rank, accumulate, dst_dt nor the
  *   buffers change that order: an owner's slice holds the bits that the full
  *   buffer holds there.

@@ -396,6 +396,9 @@ ORTHO = [
     ([(8, 8, 300)], BF16, BF16, 0),                          # more than one launch's table
     ([(768, 768, 5), (768, 2304, 2), (2304, 768, 2)], BF16, BF16, 64),
     ([(1100, 1030, 1)], BF16, BF16, 0),
+    ([(32, 512, 2), (512, 32, 1), (31, 511, 1), (127, 128, 3), (96, 160, 2), (160, 96, 1)], BF16, BF16, 1),   # the largest of one workgroup
+    ([(33, 512, 1), (129, 128, 1), (140, 130, 2), (200, 8, 1), (8, 300, 2)], F16, BF16, 0),                  # and the next
+    ([(4097, 200, 1), (200, 4097, 2)], BF16, BF16, 0),
     ([(2050, 2300, 1)], F16, BF16, 0),
 ]
 
@@ -441,9 +444,9 @@ def test_orthogonalize(T, Z, case, kind):
         assert T.equal(src[~rest], dst[~rest]) and T.equal(src[rest], kept[rest])
 
 
-def test_orthogonalize_values(T, Z):
+@pytest.mark.parametrize("n", [40, 150])
+def test_orthogonalize_values(T, Z, n):
     """Zeros, tiny and huge entries, NaN and infinities, each matrix on its own."""
-    n = 40
     plan = Z.zero_plan(7 * n * n, 1, [n * n] * 7, 0, 1)
     src = randn(T, (plan.psi_pad,), BF16, 1)
     g = src.view(7, n, n)
@@ -453,7 +456,7 @@ def test_orthogonalize_values(T, Z):
     g[4] *= 1e-25
     g[5] *= 1e35
     g[6] = 0
-    g[6, 39, 39] = 3.0
+    g[6, n - 1, n - 1] = 3.0
     m = Z.Matrices([(t, n, n, 1.0) for t in range(7)])
     ws = ws_of(T, Z.zero_orthogonalize_workspace_bytes(plan, m))
     dst = T.empty_like(src)
@@ -465,10 +468,11 @@ def test_orthogonalize_values(T, Z):
     assert bool(out[2].isnan().all()) and bool(out[3].isnan().all())
 
 
+@pytest.mark.parametrize("shape", [(96, 200), (64, 100), (100, 64)], ids=str)
 @pytest.mark.parametrize("poly", [(1, 3.4445, -4.7750, 2.0315, 1e-7), (7, 3.4445, -4.7750, 2.0315, 1e-7),
                                   (12, 1.875, -1.25, 0.375, 1e-12), (3, 2.0, 0.0, 0.0, 1e-7), (4, 1.5, -0.5, 0.0, 1.0)], ids=str)
-def test_orthogonalize_polynomials(T, Z, poly):
-    r, c = 96, 200
+def test_orthogonalize_polynomials(T, Z, poly, shape):
+    r, c = shape
     plan = Z.zero_plan(r * c, 1, [r * c], 0, 1)
     g = matrix(T, r, c, BF16, 3, "normal") * 1000
     dst = T.empty(plan.psi_pad, dtype=T.bfloat16, device="cuda")

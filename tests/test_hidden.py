@@ -109,12 +109,13 @@ def _ortho(Z, plan, ms, poly=None, src=P(0), sdt=2, dst=P(1), ddt=2, ws=P(2), ws
     return Z.load().zero_orthogonalize(plan.handle if plan else None, arr, len(ms), q, src, sdt, dst, ddt, ws, ws_bytes, None)
 
 
-def test_orthogonalize_refuses(Z, plan):
-    good = [(1, 100, 8, 1.0)]
+def test_orthogonalize_refuses(Z):
+    plan = Z.zero_plan(5 + 80000 + 100 + 16, 2, [5, 80000, 100, 16], 0, 8)
+    good = [(1, 1000, 80, 1.0)]
     ok = (5, 3.4, -4.8, 2.0, 1e-7)
     for kw in [dict(ms=[(4, 2, 2, 1.0)]), dict(ms=[(-1, 2, 2, 1.0)]), dict(ms=good + good), dict(ms=[(1, 0, 8, 1.0)]),
-               dict(ms=[(1, 8, -1, 1.0)]), dict(ms=[(1, 7, 8, 1.0)]), dict(ms=[(1, 100, 8, 1e39)]),
-               dict(ms=[(1, 100, 8, math.nan)]), dict(poly=(0,) + ok[1:]), dict(poly=(33,) + ok[1:]),
+               dict(ms=[(1, 8, -1, 1.0)]), dict(ms=[(1, 7, 8, 1.0)]), dict(ms=[(1, 1000, 80, 1e39)]),
+               dict(ms=[(1, 1000, 80, math.nan)]), dict(poly=(0,) + ok[1:]), dict(poly=(33,) + ok[1:]),
                dict(poly=(5, math.nan, 1.0, 1.0, 1e-7)), dict(poly=(5, 1.0, 1001.0, 1.0, 1e-7)),
                dict(poly=ok[:4] + (0.0,)), dict(poly=ok[:4] + (math.nan,)), dict(poly=ok[:4] + (1e31,)),
                dict(src=0), dict(dst=0), dict(src=P(0) + 1), dict(dst=P(1) + 1), dict(sdt=8), dict(ddt=8), dict(ws=0),
@@ -127,6 +128,8 @@ def test_orthogonalize_refuses(Z, plan):
     long = Z.zero_plan(1 << 22, 1, [1 << 22], 0, 1)
     assert _ortho(Z, long, [(0, 1 << 21, 2, 1.0)]) == Z.ZERO_EUNSUPPORTED
     assert _ortho(Z, plan, [], ws=0, ws_bytes=0) == Z.ZERO_OK
+    assert _ortho(Z, plan, [(0, 1, 5, 1.0)], ws=0, ws_bytes=0, dst=0) == Z.ZERO_EINVAL     # small ones need no workspace
+    assert Z.zero_orthogonalize_workspace_bytes(plan, Z.Matrices([(2, 10, 10, 1.0)])) == 0
     assert Z.load().zero_orthogonalize(plan.handle, None, 1, None, P(0), 2, P(1), 2, P(2), 1 << 30, None) == Z.ZERO_EINVAL
     assert Z.load().zero_orthogonalize(plan.handle, None, -1, None, P(0), 2, P(1), 2, P(2), 1 << 30, None) == Z.ZERO_EINVAL
 
@@ -184,10 +187,10 @@ def test_workspaces(Z):
     assert Z.zero_orthogonalize_workspace_bytes(p, Z.Matrices([])) == 0
     assert Z.zero_orthogonalize_workspace_bytes(p, Z.Matrices([(0, 7, 768, 1.0)])) == 0
     # Matrices one after another in a tensor take what single ones of that shape take.
-    stack = Z.zero_plan(48 * 64 * 64, 1, [24 * 64 * 64] * 2, 0, 64)
-    lone = Z.zero_plan(48 * 64 * 64, 1, [64 * 64] * 48, 0, 64)
-    assert (Z.zero_orthogonalize_workspace_bytes(stack, Z.Matrices([(0, 64, 64, 1.0), (1, 64, 64, 1.0)]))
-            == Z.zero_orthogonalize_workspace_bytes(lone, Z.Matrices([(t, 64, 64, 1.0) for t in range(48)])))
+    stack = Z.zero_plan(48 * 256 * 200, 1, [24 * 256 * 200] * 2, 0, 64)
+    lone = Z.zero_plan(48 * 256 * 200, 1, [256 * 200] * 48, 0, 64)
+    assert (Z.zero_orthogonalize_workspace_bytes(stack, Z.Matrices([(0, 256, 200, 1.0), (1, 256, 200, 1.0)]))
+            == Z.zero_orthogonalize_workspace_bytes(lone, Z.Matrices([(t, 256, 200, 1.0) for t in range(48)])) > 0)
 
 
 def test_binding_refuses(Z):

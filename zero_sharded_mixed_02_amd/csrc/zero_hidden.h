@@ -109,6 +109,21 @@ struct OrthoLoadArgs {
   int32_t rows, cols, ld, rows_pad, batch, norm_blocks;
   int64_t src_off[kMaxBatch];
 };
+// A batch of matrices of one shape that a workgroup each orthogonalises in LDS.
+constexpr int kSmallElems = 16384;
+constexpr int kSmallThreads = 512;
+struct OrthoSmallArgs {
+  const void* src;
+  void* dst;
+  double eps;
+  float a, b, c, shift;
+  int32_t shift_from, steps;
+  int32_t rows, cols, rp, cp;       // sides, and rounded up to 32
+  int32_t src_dt, dst_dt;
+  float scale[kMaxBatch];
+  int64_t off[kMaxBatch];
+};
+
 constexpr int kNormBlocks = 64;      // most pieces of a matrix's norm
 constexpr int kLoadThreads = 256;
 
@@ -122,6 +137,7 @@ int launch_linear(const LinearArgs& a, int epi, int dt, int tile, bool direct, v
 int launch_linear_join(const LinearArgs& a, int epi, int dt, int64_t blocks, void* stream);
 int launch_weight_grad(const WeightGradArgs& a, int dt, int tile, bool direct, int64_t blocks, void* stream);
 int launch_weight_grad_join(const WeightGradArgs& a, int64_t blocks, void* stream);
+int launch_ortho_small(const OrthoSmallArgs& a, int64_t batch, void* stream);
 int launch_ortho_norm(const OrthoLoadArgs& a, int dt, void* stream);
 int launch_ortho_load(const OrthoLoadArgs& a, int dt, int64_t blocks, void* stream);
 int launch_ortho(const OrthoArgs& a, int tile, int64_t blocks, void* stream);

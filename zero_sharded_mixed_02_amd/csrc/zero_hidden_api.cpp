@@ -31,19 +31,20 @@ int64_t round_up(int64_t n, int64_t to) { return ceil_div(n, to) * to; }
 
 // Time of a product's launch in us, from what a stage takes on one CU: `alone`
 // with one workgroup there, `full` for each of `slots` that share it.
-struct TileCost { double alone, full; int slots; };
-constexpr TileCost kCost[kTiles] = {{1.35, 1.70, 1}, {0.72, 0.55, 2}, {0.45, 0.21, 4}};
+// and `start` for a tile's first loads and its epilogue.  Fitted to 600 timed
+// launches (19 shapes, the three products, every tile and 1 to 32 pieces), whose
+// best choice it misses by 4% on average.
+struct TileCost { double alone, full, start; int slots; };
+constexpr TileCost kCost[kTiles] = {{1.35, 1.27, 9.0, 1}, {0.67, 0.57, 4.1, 2}, {0.47, 0.22, 2.9, 4}};
 constexpr int kCus = 256;
-constexpr double kTileStart = 3.0;       // us: the first loads and the epilogue
-constexpr double kJoinStart = 4.0;       // us: a launch that joins pieces of k
-constexpr double kPartRate = 3.5e6;      // bytes a us, written and read again
+constexpr double kJoinStart = 5.5;       // us: a launch that joins pieces of k
+constexpr double kPartRate = 4.4e6;      // bytes a us, written and read again
 
 double cost_of(int tile, int64_t tiles, int64_t stages) {
   const TileCost& c = kCost[tile];
   const int64_t per_cu = ceil_div(tiles, kCus), rounds = per_cu / c.slots, rest = per_cu % c.slots;
-  const double full = rounds ? c.full : c.alone;     // a chip of one round runs at a higher clock
   const double last = rest ? std::max(c.alone, rest * c.full) : 0.0;
-  return (double)stages * ((double)rounds * c.slots * full + last) + kTileStart * (double)(rounds + (rest ? 1 : 0));
+  return (double)stages * ((double)rounds * c.slots * c.full + last) + c.start * (double)(rounds + (rest ? 1 : 0));
 }
 
 // How a product is cut into workgroups: `whole` tiles in one piece, the others in
@@ -205,15 +206,17 @@ int64_t bias_chunk(int64_t n, int64_t out_features) {
   return std::max<int64_t>(32, ceil_div(n, want));
 }
 
-// Pieces of k where every tile is to have the same.
-int alike(int64_t m, int64_t n, int64_t k) {
+// Pieces of k where every tile is to have the same, for the whole result and a
+// share of its rows.
+int alike(int64_t m, int64_t n, int64_t k, int64_t shares) {
   const int64_t stages = std::max<int64_t>(1, ceil_div(k, kStage));
   double us = 1e300;
   int best = 1;
   for (int64_t s = 1; s <= 64 && (s == 1 || stages / s >= 4); s *= 2) {
     const Pick c = pick(m, n, k, 1, (int)s);
-    if (c.us < us) {
-      us = c.us;
+    const double both = shares > 1 ? c.us + pick(ceil_div(m, shares), n, k, 1, (int)s).us : c.us;
+    if (both < us) {
+      us = both;
       best = c.splits;
     }
   }
@@ -238,7 +241,7 @@ WeightShape weight_shape(const zero_plan_s& p, int32_t weight, int64_t in_featur
   }
   // The pieces of k follow from the whole weight, and every tile has the same, so that
   // a slice's sums are those of the full buffer.
-  s.splits = alike(out_features, in_features, n);
+  s.splits = alike(out_features, in_features, n, p.n_d);
   s.c = s.rows > 0 ? pick(s.rows, in_features, n, 1, s.splits) : Pick{kTile64, 0, 0, 1, 0.0};
   s.part = part_bytes(s.c);
   s.bias_part = round_up(ceil_div(n, bias_chunk(n, out_features)) * out_features * 4, 16);
@@ -351,10 +354,16 @@ zero_status collect(zero_plan_t p, const zero_matrix* ms, int32_t n, std::vector
   return ok();
 }
 
+// Matrices that one workgroup orthogonalises in its LDS: 16384 elements with the
+// sides rounded up to 32.
+bool is_small(int64_t rows, int64_t cols) {
+  return rows <= kSmallElems && cols <= kSmallElems && round_up(rows, 32) * round_up(cols, 32) <= kSmallElems;
+}
+
 int64_t ortho_bytes(const std::vector<Group>& groups) {
   int64_t most = 0;
   for (const Group& g : groups)
-    if (!g.off.empty()) most = std::max(most, ortho_space(g.rows, g.cols, batch_of(g.rows, g.cols, (int64_t)g.off.size())).total);
+    if (!g.off.empty() && !is_small(g.rows, g.cols)) most = std::max(most, ortho_space(g.rows, g.cols, batch_of(g.rows, g.cols, (int64_t)g.off.size())).total);
   return most;
 }
 
@@ -374,6 +383,32 @@ zero_status run_ortho(OrthoArgs& a, int64_t m, int64_t n, int64_t k, const Pick&
   if (const int err = launch_ortho(a, c.tile, blocks_of(now), stream)) return hip_fail(err);
   if (joins == 0) return ok();
   return launched(launch_ortho_join(a, joins, stream));
+}
+
+zero_status ortho_small(const Group& g, int64_t first, int64_t batch, const zero_newton_schulz& poly, const void* src, int src_dt,
+                        void* dst, int dst_dt, void* stream) {
+  OrthoSmallArgs a;
+  memset(&a, 0, sizeof a);
+  a.src = src;
+  a.dst = dst;
+  a.eps = poly.eps;
+  a.a = (float)poly.a;
+  a.b = (float)poly.b;
+  a.c = (float)poly.c;
+  a.shift = kShift;
+  a.shift_from = kShiftFrom;
+  a.steps = poly.steps;
+  a.rows = (int32_t)g.rows;
+  a.cols = (int32_t)g.cols;
+  a.rp = (int32_t)round_up(g.rows, 32);
+  a.cp = (int32_t)round_up(g.cols, 32);
+  a.src_dt = src_dt;
+  a.dst_dt = dst_dt;
+  for (int64_t i = 0; i < batch; ++i) {
+    a.scale[i] = g.scale[first + i];
+    a.off[i] = g.off[first + i];
+  }
+  return launched(launch_ortho_small(a, batch, stream));
 }
 
 zero_status ortho_batch(const Group& g, const OrthoSpace& s, int64_t first, int64_t batch, const zero_newton_schulz& poly, const void* src, int src_dt,
@@ -721,6 +756,11 @@ zero_status zero_orthogonalize(zero_plan_t p, const zero_matrix* matrices, int32
     for (const Group& g : groups) {
       const int64_t count = (int64_t)g.off.size();
       if (count == 0) continue;
+      if (is_small(g.rows, g.cols)) {
+        for (int64_t i = 0; i < count; i += kMaxBatch)
+          if (zero_status st = ortho_small(g, i, std::min<int64_t>(kMaxBatch, count - i), q, src, src_dt, dst, dst_dt, stream)) return st;
+        continue;
+      }
       const int64_t batch = batch_of(g.rows, g.cols, count);
       const OrthoSpace s = ortho_space(g.rows, g.cols, batch);   // a smaller last batch takes the same shapes
       for (int64_t i = 0; i < count; i += batch)

@@ -196,6 +196,168 @@ __global__ void __launch_bounds__(kJoinThreads) ortho_join_kernel(const OrthoArg
   }
 }
 
+// ---------------------------------------------------------------------------
+// Small matrices
+// ---------------------------------------------------------------------------
+
+// A whole matrix of up to 16384 elements by one workgroup: X, A and B in LDS in fp16,
+// X also in fp32 in the registers of the wave whose tiles of 16 x 16 it is, eight at
+// most.  One launch in the place of 17, each of which is latency alone (65 x 33: 70 us
+// with them).  Rows are 16 bytes apart beyond their length, so that a fragment's 16
+// rows lie in different banks.
+struct Small {
+  ZK_LDS char* p;
+  int pitch;            // bytes
+  __device__ __forceinline__ s16x8 along(int row0, int k0, int lane) const {     // 16 rows, 32 k along them
+    return *(const ZK_LDS s16x8*)(p + (row0 + (lane & 15)) * pitch + (k0 + (lane >> 4) * 8) * 2);
+  }
+  __device__ __forceinline__ s16x8 across(int col0, int k0, int lane) const {    // 16 columns, k down the rows
+    const int c = lane & 15;
+    const ZK_LDS char* a = p + (k0 + (lane >> 4) * 8 + (c >> 2)) * pitch + (col0 + (c & 3) * 4) * 2;
+    const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((ZK_LDS s16x4*)a);
+    const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((ZK_LDS s16x4*)(a + 4 * pitch));
+    return __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
+  }
+  typedef _Float16 half4 __attribute__((ext_vector_type(4)));
+  __device__ __forceinline__ ZK_LDS half4* at(int row, int col) const { return (ZK_LDS half4*)(p + row * pitch + col * 2); }
+};
+
+template <typename T>
+__global__ void __launch_bounds__(kSmallThreads) ortho_small_kernel(const OrthoSmallArgs a) {
+  extern __shared__ __attribute__((aligned(1024))) char smem[];
+  __shared__ double sums[kSmallThreads / 64];
+  constexpr int kWaves = kSmallThreads / 64, kMine = 8;
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), z = blockIdx.x;
+  const bool tall = a.rows > a.cols;
+  const int side = a.rp < a.cp ? a.rp : a.cp, wide = a.rp < a.cp ? a.cp : a.rp;
+  const Small X = {(ZK_LDS char*)smem, a.cp * 2 + 16};
+  const Small A = {X.p + a.rp * X.pitch, side * 2 + 16};
+  const Small B = {A.p + side * A.pitch, A.pitch};
+
+  // The matrix as it is, its norm in fp64, then times a power of two.
+  const int upr = a.cp / 8, units = a.rp * upr;
+  double s = 0.0;
+  for (int u = threadIdx.x; u < units; u += kSmallThreads) {
+    const int row = u / upr, col = u % upr * 8, have = row < a.rows ? a.cols - col : 0;
+    Row<T, 8> x;
+    if (have > 0) x.load(a.src, a.off[z] + (int64_t)row * a.cols + col, have);
+    else x.v = {};
+#pragma unroll
+    for (int i = 0; i < 8; ++i) s += (double)(float)x.v[i] * (double)(float)x.v[i];
+    *(ZK_LDS typename Row<T, 8>::tv*)X.at(row, col) = x.v;
+  }
+#pragma unroll
+  for (int k = 32; k > 0; k >>= 1) s += __shfl_xor(s, k);
+  if (lane == 0) sums[wave] = s;
+  __syncthreads();
+  s = 0.0;
+#pragma unroll
+  for (int k = 0; k < kWaves; ++k) s += sums[k];
+  const double norm = __builtin_sqrt(s), den = norm + a.eps;
+  const bool good = den < __builtin_inf();
+  const int e = good && norm > 0.0 ? 5 - ilogb(norm) : 0;
+  float f = good ? (float)(1.0 / ldexp(den, e)) : __builtin_nanf("");
+  const float may_shift = norm > a.eps ? a.shift : 0.0f;
+  for (int u = threadIdx.x; u < units; u += kSmallThreads) {
+    ZK_LDS char* at = (ZK_LDS char*)X.at(u / upr, u % upr * 8);
+    const typename Row<T, 8>::tv x = *(ZK_LDS typename Row<T, 8>::tv*)at;
+    f16x8 h;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) h[i] = good ? (_Float16)ldexpf((float)x[i], e) : (_Float16)0.0f;
+    *(ZK_LDS f16x8*)at = h;
+  }
+  __syncthreads();
+
+  const int rt = a.rp / 16, ct = a.cp / 16, nt = side / 16, mine = (rt * ct + kWaves - 1) / kWaves, mine_n = (nt * nt + kWaves - 1) / kWaves;
+  const int q = lane >> 4, c = lane & 15;
+  f32x4 x32[kMine], acc[kMine];
+#pragma unroll
+  for (int i = 0; i < kMine; ++i) {
+    const int t = wave * mine + i;
+    x32[i] = f32x4{0.f, 0.f, 0.f, 0.f};
+    if (i < mine && t < rt * ct) {
+      const Small::half4 h = *X.at(t / ct * 16 + c, t % ct * 16 + q * 4);
+      x32[i] = f32x4{(float)h[0], (float)h[1], (float)h[2], (float)h[3]};
+    }
+  }
+  // acc = the wave's tiles of a product, of `tiles` in rows of `across`.
+  auto product = [&](int tiles, int across, int each, int depth, auto left, auto right) {
+#pragma unroll
+    for (int i = 0; i < kMine; ++i) acc[i] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll 1
+    for (int k = 0; k < depth; k += 32) {
+#pragma unroll
+      for (int i = 0; i < kMine; ++i) {
+        const int t = wave * each + i;
+        if (i < each && t < tiles) acc[i] = mfma<_Float16>(right(t % across * 16, k), left(t / across * 16, k), acc[i]);
+      }
+    }
+  };
+#pragma unroll 1
+  for (int step = 0; step < a.steps; ++step) {
+    const float d = step >= a.shift_from ? may_shift : 0.0f;
+    if (tall)
+      product(nt * nt, nt, mine_n, wide, [&](int r, int k) { return X.across(r, k, lane); }, [&](int r, int k) { return X.across(r, k, lane); });
+    else
+      product(nt * nt, nt, mine_n, wide, [&](int r, int k) { return X.along(r, k, lane); }, [&](int r, int k) { return X.along(r, k, lane); });
+#pragma unroll
+    for (int i = 0; i < kMine; ++i) {
+      const int t = wave * mine_n + i, row = t / nt * 16 + c, col = t % nt * 16 + q * 4;
+      if (i < mine_n && t < nt * nt) {
+        Small::half4 h;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) h[k] = (_Float16)__builtin_fmaf(f * f, acc[i][k], row == col + k ? -d : 0.0f);
+        *A.at(row, col) = h;
+      }
+    }
+    __syncthreads();
+    product(nt * nt, nt, mine_n, side, [&](int r, int k) { return A.along(r, k, lane); }, [&](int r, int k) { return A.along(r, k, lane); });
+    const float b = __builtin_fmaf(2.0f * a.c, d, a.b), c0 = __builtin_fmaf(__builtin_fmaf(a.c, d, a.b), d, a.a);
+#pragma unroll
+    for (int i = 0; i < kMine; ++i) {
+      const int t = wave * mine_n + i, row = t / nt * 16 + c, col = t % nt * 16 + q * 4;
+      if (i < mine_n && t < nt * nt) {
+        const Small::half4 x = *A.at(row, col);
+        Small::half4 h;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) h[k] = (_Float16)__builtin_fmaf(a.c, acc[i][k], b * (float)x[k]);
+        *B.at(row, col) = h;
+      }
+    }
+    __syncthreads();
+    if (tall)
+      product(rt * ct, ct, mine, side, [&](int r, int k) { return X.along(r, k, lane); }, [&](int r, int k) { return B.along(r, k, lane); });
+    else
+      product(rt * ct, ct, mine, side, [&](int r, int k) { return B.along(r, k, lane); }, [&](int r, int k) { return X.across(r, k, lane); });
+    __syncthreads();        // nobody reads X any more
+    const bool last = step + 1 == a.steps;
+#pragma unroll
+    for (int i = 0; i < kMine; ++i) {
+      const int t = wave * mine + i, row = t / ct * 16 + c, col = t % ct * 16 + q * 4;
+      if (i < mine && t < rt * ct) {
+        float v[4];
+        Small::half4 h;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          x32[i][k] = v[k] = f * __builtin_fmaf(c0, x32[i][k], acc[i][k]);
+          h[k] = (_Float16)v[k];
+        }
+        if (!last) {
+          *X.at(row, col) = h;
+        } else if (row < a.rows && col < a.cols) {
+#pragma unroll
+          for (int k = 0; k < 4; ++k) v[k] *= a.scale[z];
+          const int64_t o = a.off[z] + (int64_t)row * a.cols + col;
+          if (a.dst_dt == ZERO_BF16) store_row<__bf16, 4>(a.dst, o, a.cols - col, v);
+          else store_row<_Float16, 4>(a.dst, o, a.cols - col, v);
+        }
+      }
+    }
+    f = 1.0f;
+    __syncthreads();
+  }
+}
+
 template <int EPI, int AF, int BF, int TILE>
 int go(const OrthoArgs& a, int64_t blocks, void* stream) {
   return launch(&ortho_kernel<EPI, AF, BF, TILE>, a, blocks, kTileThreads[TILE], CoreOf<_Float16, AF, BF, TILE, true>::kLds, stream);
@@ -208,6 +370,13 @@ int go(const OrthoArgs& a, int tile, int64_t blocks, void* stream) {
 }
 
 }  // namespace
+
+int launch_ortho_small(const OrthoSmallArgs& a, int64_t batch, void* stream) {
+  const int side = a.rp < a.cp ? a.rp : a.cp;
+  const int lds = a.rp * (a.cp * 2 + 16) + 2 * side * (side * 2 + 16);
+  return a.src_dt == ZERO_BF16 ? launch(&ortho_small_kernel<__bf16>, a, batch, kSmallThreads, lds, stream)
+                               : launch(&ortho_small_kernel<_Float16>, a, batch, kSmallThreads, lds, stream);
+}
 
 int launch_ortho_norm(const OrthoLoadArgs& a, int dt, void* stream) {
   const int64_t blocks = (int64_t)a.batch * a.norm_blocks;
