@@ -113,6 +113,9 @@ LINEAR = [
     (2050, 1090, 1042, 4, BF16, RELU, True, False, False, 6),
     (1500, 1201, 1301, 3, F16, NONE, True, False, False, 0),       # odd rows in the larger tiles
     (9, 3, 2, 0, BF16, NONE, False, False, False, 0),              # rows shorter than a unit
+    (3001, 1201, 1301, 3, BF16, GELU, True, True, True, 0),        # odd rows, copied first
+    (3001, 1200, 1301, 3, F16, NONE, False, False, False, 0),      # a weight behind an odd tensor
+    (3001, 1201, 1301, 0, BF16, NONE, True, False, False, 4),      # the same, odd strides
 ]
 
 
@@ -170,6 +173,10 @@ GRAD = [
     (600, 1030, 30, 0, F16, GELU, True, 0),
     (1500, 1301, 1201, 3, F16, NONE, True, 0),
     (2050, 1042, 1090, 4, BF16, RELU, True, 6),
+    (3001, 1201, 1301, 3, BF16, GELU, True, 0),
+    (3001, 1200, 1301, 3, F16, NONE, False, 0),
+    (3001, 1201, 1301, 0, BF16, SILU, True, 4),
+    (9001, 33, 6001, 0, BF16, NONE, False, 0),
 ]
 
 
@@ -223,6 +230,9 @@ WEIGHT = [
     (70, 3, 5, 0, BF16, F32, 2, 0),
     (90, 75, 131, 1, F16, F32, 2, 1),                  # odd rows an even distance apart
     (65, 131, 67, 0, BF16, BF16, 3, 5),
+    (3001, 1201, 1301, 3, BF16, BF16, 3, 0),
+    (9001, 33, 6001, 0, F16, F32, 2, 0),
+    (9001, 6001, 33, 0, BF16, BF16, 4, 2),
 ]
 
 

@@ -86,7 +86,7 @@ struct Panel {
     } else {
       base = (const char*)p + (int64_t)k0 * lde * 2 + (int64_t)row0 * 2;
       step = (int64_t)kBK * lde * 2;
-      span = (int64_t)rows * 2;
+      span = (int64_t)(rows + (rows & 1)) * 2;      // whole words: the row is even, or padded
       before = row0;
       constexpr int U = W / 8;
 #pragma unroll
@@ -251,7 +251,11 @@ struct Core {
   typedef Panel<AF, BM, NT> PA;
   typedef Panel<BF, BN, NT> PB;
   static constexpr int kStage = PA::kBytes + PB::kBytes;
-  static constexpr int kLds = 2 * kStage;
+  // Stages in LDS: three of the small tile, whose few products do not cover a load's
+  // latency (16 x 4096 x 4096: 10.4 us with three, 12.6 with two; with four, which
+  // leave a CU two workgroups, 2048 x 2048 x 4096 takes 42 us in place of 38).
+  static constexpr int kRing = DIRECT && kStage <= 16384 ? 3 : 2;
+  static constexpr int kLds = kRing * kStage;
 
   f32x4 acc[TM][TN];
 
@@ -312,11 +316,12 @@ struct Core {
     for (int i = 0; i < PB::kLoads; ++i) pb.load_one(rb, lds + PA::kBytes, i, wave, tid, left);
   }
 
-  // All of this wave's loads have arrived and its reads of LDS are done; then all
-  // waves' have.
+  // All but the youngest kKeep of this wave's loads have arrived and its reads of LDS
+  // are done; then all waves' have.
+  template <int kKeep = 0>
   __device__ __forceinline__ static void arrive() {
     __builtin_amdgcn_sched_barrier(0);
-    asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
+    asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(kKeep) : "memory");
     __builtin_amdgcn_sched_barrier(0);
   }
 
@@ -341,28 +346,30 @@ struct Core {
     const int ragged = !DIRECT || ((AF == kFormK || BF == kFormK) && left % 8) ? left % kBK : 0;
     left -= ragged;
     if constexpr (DIRECT) {
-      // Two stages in LDS.  While the products of one half of a stage run, the
-      // fragments of the next half are read; in the middle of a stage every wave
-      // has read all of it and the next has arrived, so that one barrier a stage is
-      // enough and the matrix units have work on both sides of it.
+      // A ring of stages in LDS.  While the products of one half of a stage run, the
+      // fragments of the next half are read; in the middle of a stage every wave has
+      // read all of it and the next has arrived, so that one barrier a stage is enough
+      // and the matrix units have work on both sides of it.
       Frags f0, f1;
       const uint32_t at = (uint32_t)(uintptr_t)lds;      // LDS address
       if (left > 0) {
-        load(pa, pb, at, wave, tid, left);
-        arrive();
-        pa.advance();
-        pb.advance();
-        load(pa, pb, at + kStage, wave, tid, left - kBK);
+#pragma unroll
+        for (int i = 0; i < kRing; ++i) {
+          load(pa, pb, at + i * kStage, wave, tid, left - i * kBK);
+          pa.advance();
+          pb.advance();
+        }
+        arrive<kL * (kRing - 1)>();
         read(f0, lds, 0, wm, wn, lane);
         int cur = 0;
         for (; left > kBK; left -= kBK) {
           const int here = cur * kStage;
-          cur ^= 1;
+          cur = cur + 1 == kRing ? 0 : cur + 1;
           step<false>(f0, f1, lds + here, 1, pa, pb, 0, wave, tid, 0, wm, wn, lane);
-          arrive();
+          arrive<kL * (kRing - 2)>();
+          step<true>(f1, f0, lds + cur * kStage, 0, pa, pb, at + here, wave, tid, left - kRing * kBK, wm, wn, lane);
           pa.advance();
           pb.advance();
-          step<true>(f1, f0, lds + cur * kStage, 0, pa, pb, at + here, wave, tid, left - 2 * kBK, wm, wn, lane);
         }
         read(f1, lds + cur * kStage, 1, wm, wn, lane);
         multiply(f0);

@@ -56,13 +56,24 @@ struct WeightGradArgs {
   int32_t dst_dt;
   int32_t accumulate;
   float scale;
-  // The bias: columns [b_lo, b_hi) of dz are summed.
+  // The bias: columns [b_lo, b_hi) of dz are summed (dz: column row0 of its first row).
+  const void* dz;
+  int64_t dz_stride;
   void* bias_dst;         // the element b_lo of the bias
   float* bias_part;       // fp32[chunks][columns]
   int32_t b_lo, b_hi;
   int32_t chunk_rows, chunks, col_blocks, bias_blocks;
   int32_t join_blocks, pad_;
 };
+
+// Rows of `width` 16-bit elements into rows of whole eights, padded with zeros.
+struct CopyRowsArgs {
+  const void* src;
+  void* dst;
+  int64_t rows, ld_src, ld_dst;
+  int32_t width, units;     // units of eight in a row of dst
+};
+constexpr int kCopyThreads = 256;
 
 struct ActGradArgs {
   const void* dy;
@@ -142,6 +153,7 @@ int launch_ortho_norm(const OrthoLoadArgs& a, int dt, void* stream);
 int launch_ortho_load(const OrthoLoadArgs& a, int dt, int64_t blocks, void* stream);
 int launch_ortho(const OrthoArgs& a, int tile, int64_t blocks, void* stream);
 int launch_ortho_join(const OrthoArgs& a, int64_t blocks, void* stream);
+int launch_copy_rows(const CopyRowsArgs& a, int64_t blocks, void* stream);
 int launch_act_grad(const ActGradArgs& a, int dt, int64_t blocks, void* stream);
 
 }  // namespace hidden

@@ -33,12 +33,12 @@ int64_t round_up(int64_t n, int64_t to) { return ceil_div(n, to) * to; }
 // with one workgroup there, `full` for each of `slots` that share it.
 // and `start` for a tile's first loads and its epilogue.  Fitted to 600 timed
 // launches (19 shapes, the three products, every tile and 1 to 32 pieces), whose
-// best choice it misses by 4% on average.
+// best choice it misses by 2% on average.
 struct TileCost { double alone, full, start; int slots; };
-constexpr TileCost kCost[kTiles] = {{1.35, 1.27, 9.0, 1}, {0.67, 0.57, 4.1, 2}, {0.47, 0.22, 2.9, 4}};
+constexpr TileCost kCost[kTiles] = {{1.35, 1.08, 9.7, 1}, {0.61, 0.50, 4.1, 2}, {0.23, 0.19, 3.0, 3}};
 constexpr int kCus = 256;
-constexpr double kJoinStart = 5.5;       // us: a launch that joins pieces of k
-constexpr double kPartRate = 4.4e6;      // bytes a us, written and read again
+constexpr double kJoinStart = 3.2;       // us: a launch that joins pieces of k
+constexpr double kPartRate = 4.5e6;      // bytes a us, written and read again
 
 double cost_of(int tile, int64_t tiles, int64_t stages) {
   const TileCost& c = kCost[tile];
@@ -121,6 +121,53 @@ zero_status check_grid(int64_t blocks, int threads) {
 // multiples of 4, and whole words: form M's last row must not end inside one.
 bool direct_k(const void* p, int64_t ld) { return aligned(p, 4) && ld % 2 == 0; }
 bool direct_m(const void* p, int64_t ld, int64_t width) { return direct_k(p, ld) && width % 2 == 0; }
+
+// Odd rows cannot be loaded straight into LDS; the products then run at 0.8 of
+// their rate in large tiles and half of it in small ones.  Where a quarter of the
+// product's time is more than copying the odd operands takes, they are copied into
+// the workspace first, with rows of whole eights (12527 x 33 x 12736 backward: COPYNOTE).
+struct Copies {
+  bool a, b;
+  int64_t lda, ldb, a_bytes, b_bytes;
+};
+
+constexpr double kCopyStart = 4.0;       // us
+constexpr double kCopyRate = 4.5e6;      // bytes a us, read and written
+
+Copies copies_of(const Pick& c, bool odd_a, int64_t rows_a, int64_t width_a, bool odd_b, int64_t rows_b, int64_t width_b) {
+  Copies p = {odd_a, odd_b, round_up(width_a, 8), round_up(width_b, 8), 0, 0};
+  if (odd_a) p.a_bytes = round_up(rows_a * p.lda * 2, 256);
+  if (odd_b) p.b_bytes = round_up(rows_b * p.ldb * 2, 256);
+  const double us = kCopyStart * (odd_a + odd_b) + 2.0 * (double)(p.a_bytes + p.b_bytes) / kCopyRate;
+  if (!(us < 0.25 * c.us)) p = {false, false, 0, 0, 0, 0};
+  return p;
+}
+
+zero_status copy_rows(const void* src, int64_t rows, int64_t width, int64_t ld_src, void* dst, int64_t ld_dst, void* stream) {
+  CopyRowsArgs a = {src, dst, rows, ld_src, ld_dst, (int32_t)width, (int32_t)(ld_dst / 8)};
+  const int64_t blocks = ceil_div(rows * a.units, kCopyThreads);
+  if (zero_status st = check_grid(blocks, kCopyThreads)) return st;
+  return launched(launch_copy_rows(a, blocks, stream));
+}
+
+// Puts the operands that are to be copied in their places behind `at` bytes of the
+// workspace.
+zero_status make_copies(Product& p, const Copies& c, int64_t rows_a, int64_t width_a, int64_t rows_b, int64_t width_b, void* ws,
+                        int64_t at, void* stream) {
+  if (c.a) {
+    char* d = (char*)ws + at;
+    if (zero_status st = copy_rows(p.a, rows_a, width_a, p.lda, d, c.lda, stream)) return st;
+    p.a = d;
+    p.lda = c.lda;
+  }
+  if (c.b) {
+    char* d = (char*)ws + at + c.a_bytes;
+    if (zero_status st = copy_rows(p.b, rows_b, width_b, p.ldb, d, c.ldb, stream)) return st;
+    p.b = d;
+    p.ldb = c.ldb;
+  }
+  return ok();
+}
 
 // ---------------------------------------------------------------------------
 // Arguments
@@ -228,7 +275,8 @@ struct WeightShape {
   int64_t row0, rows;
   int splits;
   Pick c;
-  int64_t part, bias_part;  // bytes
+  Copies copies;
+  int64_t part, bias_part, bytes;  // of the workspace
 };
 
 WeightShape weight_shape(const zero_plan_s& p, int32_t weight, int64_t in_features, int64_t out_features, int64_t n, int32_t rank) {
@@ -243,8 +291,28 @@ WeightShape weight_shape(const zero_plan_s& p, int32_t weight, int64_t in_featur
   // a slice's sums are those of the full buffer.
   s.splits = alike(out_features, in_features, n, p.n_d);
   s.c = s.rows > 0 ? pick(s.rows, in_features, n, 1, s.splits) : Pick{kTile64, 0, 0, 1, 0.0};
-  s.part = part_bytes(s.c);
-  s.bias_part = round_up(ceil_div(n, bias_chunk(n, out_features)) * out_features * 4, 16);
+  s.copies = copies_of(s.c, n > 1 && out_features % 2, n, s.rows, n > 1 && in_features % 2, n, in_features);
+  s.part = round_up(part_bytes(s.c), 256);
+  s.bias_part = round_up(ceil_div(n, bias_chunk(n, out_features)) * out_features * 4, 256);
+  s.bytes = s.part + s.bias_part + s.copies.a_bytes + s.copies.b_bytes;
+  return s;
+}
+
+// What zero_linear and zero_linear_input_grad run: n rows into `out` columns over
+// `inner` terms.  The operands that may be copied follow from the shapes and the plan.
+struct LinearShape {
+  Pick c;
+  Copies copies;
+  int64_t part, bytes;      // of the workspace
+};
+
+LinearShape linear_shape(const zero_plan_s& p, int32_t weight, int64_t in_features, int64_t out_features, int64_t n, bool grad) {
+  LinearShape s;
+  const int64_t cols = grad ? in_features : out_features, inner = grad ? out_features : in_features;
+  s.c = pick(n, cols, inner, 1, 0);
+  s.copies = copies_of(s.c, n > 1 && inner % 2, n, inner, in_features % 2 || p.t_off[weight] % 2, out_features, in_features);
+  s.part = round_up(part_bytes(s.c), 256);
+  s.bytes = s.part + s.copies.a_bytes + s.copies.b_bytes;
   return s;
 }
 
@@ -507,7 +575,7 @@ extern "C" {
 size_t zero_linear_workspace_bytes(zero_plan_t p, int32_t weight, int64_t in_features, int64_t n) {
   int64_t out;
   if (weight_of(p, weight, in_features, out) || check_n(n) || n == 0 || out == 0) return 0;
-  return (size_t)part_bytes(pick(n, out, in_features, 1, 0));
+  return (size_t)linear_shape(*p, weight, in_features, out, n, false).bytes;
 }
 
 zero_status zero_linear(zero_plan_t p, int32_t weight, int32_t bias, int64_t in_features, const void* params, zero_dtype dt,
@@ -529,8 +597,10 @@ zero_status zero_linear(zero_plan_t p, int32_t weight, int32_t bias, int64_t in_
       if (zero_status st = check_rows(residual, n, out, residual_stride, false, "residual", rr)) return st;
     if (pre)
       if (zero_status st = check_rows(pre, n, out, pre_stride, false, "pre", rp)) return st;
-    const Pick c = pick(n, out, in_features, 1, 0);
-    const size_t need = n && out ? (size_t)part_bytes(c) : 0;
+    const bool some = n > 0 && out > 0;
+    const LinearShape s = some ? linear_shape(*p, weight, in_features, out, n, false) : LinearShape{};
+    const Pick& c = s.c;
+    const size_t need = (size_t)s.bytes;
     if (zero_status st = check_workspace(workspace, ws_bytes, need)) return st;
     std::vector<Range> reads = {range_of(params, p->psi_pad, 2, "params"), rx};
     std::vector<Range> writes = {ry, rp, range_of(workspace, (int64_t)need, 1, "workspace")};
@@ -554,6 +624,7 @@ zero_status zero_linear(zero_plan_t p, int32_t weight, int32_t bias, int64_t in_
     a.ldpre = pre_stride;
     a.ldadd = residual_stride;
     a.act = act;
+    if (zero_status st = make_copies(a.p, s.copies, n, in_features, out, in_features, workspace, s.part, stream)) return st;
     const bool direct = direct_k(a.p.a, a.p.lda) && direct_k(a.p.b, a.p.ldb);
     return run_linear(a, 0, dt, c, direct, stream);
   });
@@ -562,7 +633,7 @@ zero_status zero_linear(zero_plan_t p, int32_t weight, int32_t bias, int64_t in_
 size_t zero_linear_input_grad_workspace_bytes(zero_plan_t p, int32_t weight, int64_t in_features, int64_t n) {
   int64_t out;
   if (weight_of(p, weight, in_features, out) || check_n(n) || n == 0) return 0;
-  return (size_t)part_bytes(pick(n, in_features, out, 1, 0));
+  return (size_t)linear_shape(*p, weight, in_features, out, n, true).bytes;
 }
 
 zero_status zero_linear_input_grad(zero_plan_t p, int32_t weight, int64_t in_features, const void* params, zero_dtype dt,
@@ -586,8 +657,9 @@ zero_status zero_linear_input_grad(zero_plan_t p, int32_t weight, int64_t in_fea
       if (zero_status st = check_rows(addend, n, in_features, addend_stride, false, "addend", ra)) return st;
     if (pre)
       if (zero_status st = check_rows(pre, n, in_features, pre_stride, false, "pre", rp)) return st;
-    const Pick c = pick(n, in_features, out, 1, 0);
-    const size_t need = n ? (size_t)part_bytes(c) : 0;
+    const LinearShape s = n > 0 ? linear_shape(*p, weight, in_features, out, n, true) : LinearShape{};
+    const Pick& c = s.c;
+    const size_t need = (size_t)s.bytes;
     if (zero_status st = check_workspace(workspace, ws_bytes, need)) return st;
     std::vector<Range> writes = {rx, range_of(workspace, (int64_t)need, 1, "workspace")};
     if (zero_status st = check_disjoint(writes, {range_of(params, p->psi_pad, 2, "params"), rz, rp})) return st;
@@ -609,7 +681,8 @@ zero_status zero_linear_input_grad(zero_plan_t p, int32_t weight, int64_t in_fea
     a.ldpre = pre_stride;
     a.ldadd = addend_stride;
     a.act = act;
-    const bool direct = direct_k(a.p.a, a.p.lda) && direct_m(a.p.b, a.p.ldb, in_features);
+    if (zero_status st = make_copies(a.p, s.copies, n, out, out, in_features, workspace, s.part, stream)) return st;
+    const bool direct = direct_k(a.p.a, a.p.lda) && direct_m(a.p.b, a.p.ldb, s.copies.b ? s.copies.ldb : in_features);
     return run_linear(a, 1, dt, c, direct, stream);
   });
 }
@@ -617,8 +690,7 @@ zero_status zero_linear_input_grad(zero_plan_t p, int32_t weight, int64_t in_fea
 size_t zero_linear_weight_grad_workspace_bytes(zero_plan_t p, int32_t weight, int64_t in_features, int64_t n, int32_t rank) {
   int64_t out;
   if (weight_of(p, weight, in_features, out) || check_n(n) || n == 0 || out == 0 || rank >= p->n_d) return 0;
-  const WeightShape s = weight_shape(*p, weight, in_features, out, n, rank);
-  return (size_t)(round_up(s.part, 16) + s.bias_part);
+  return (size_t)weight_shape(*p, weight, in_features, out, n, rank).bytes;
 }
 
 zero_status zero_linear_weight_grad(zero_plan_t p, int32_t weight, int32_t bias, int64_t in_features, const void* dz,
@@ -670,7 +742,7 @@ zero_status zero_linear_weight_grad(zero_plan_t p, int32_t weight, int32_t bias,
       part_of_tensor(*p, bias, rank, lo, hi, at);
       if (lo < hi) {
         a.bias_dst = (char*)dst + at * esize(dst_dt);
-        a.bias_part = (float*)((char*)workspace + round_up(s.part, 16));
+        a.bias_part = (float*)((char*)workspace + s.part);
         a.b_lo = (int32_t)lo;
         a.b_hi = (int32_t)hi;
         const int64_t chunk = bias_chunk(n, out);
@@ -686,7 +758,11 @@ zero_status zero_linear_weight_grad(zero_plan_t p, int32_t weight, int32_t bias,
     const int64_t joins = a.join_blocks + (a.bias_blocks && a.chunks > 1 ? ceil_div(a.b_hi - a.b_lo, kJoinThreads) : 0);
     if (zero_status st = check_grid(blocks, kTileThreads[c.tile])) return st;
     if (zero_status st = check_grid(joins, kJoinThreads)) return st;
-    const bool direct = direct_m(a.p.a, a.p.lda, s.rows) && direct_m(a.p.b, a.p.ldb, in_features);
+    // The bias is summed from dz itself.
+    a.dz = a.p.a;
+    a.dz_stride = a.p.lda;
+    if (zero_status st = make_copies(a.p, s.copies, n, s.rows, n, in_features, workspace, s.part + s.bias_part, stream)) return st;
+    const bool direct = direct_m(a.p.a, a.p.lda, s.copies.a ? s.copies.lda : s.rows) && direct_m(a.p.b, a.p.ldb, s.copies.b ? s.copies.ldb : in_features);
     if (const int err = launch_weight_grad(a, dt, c.tile, direct, blocks, stream)) return hip_fail(err);
     if (joins == 0) return ok();
     return launched(launch_weight_grad_join(a, joins, stream));

@@ -160,7 +160,7 @@ __device__ void bias_block(const WeightGradArgs& a, ZK_LDS float* lds, int b) {
   if (have > 0 && rl < RL) {
 #pragma unroll 4
     for (int r = r0 + rl; r < r1; r += RL) {
-      load_row<T, V>(a.p.a, (int64_t)r * a.p.lda + (col - a.row0), have, x);
+      load_row<T, V>(a.dz, (int64_t)r * a.dz_stride + (col - a.row0), have, x);
 #pragma unroll
       for (int i = 0; i < V; ++i) s[i] += x[i];
     }
@@ -230,6 +230,16 @@ __global__ void __launch_bounds__(kActThreads) act_grad_kernel(const ActGradArgs
   store_row<T, kActVec>(a.dz, e, have, dy);
 }
 
+__global__ void __launch_bounds__(kCopyThreads) copy_rows_kernel(const CopyRowsArgs a) {
+  const int64_t u = (int64_t)blockIdx.x * kCopyThreads + threadIdx.x;
+  const int64_t row = u / a.units;
+  if (row >= a.rows) return;
+  const int col = (int)(u - row * a.units) * 8;
+  Row<_Float16, 8> x;       // bits, whichever type
+  x.load(a.src, row * a.ld_src + col, a.width - col);
+  *(AS1 Row<_Float16, 8>::tv*)((AS1 _Float16*)a.dst + row * a.ld_dst + col) = x.v;
+}
+
 // ---------------------------------------------------------------------------
 // Dispatch
 // ---------------------------------------------------------------------------
@@ -290,6 +300,10 @@ int launch_weight_grad(const WeightGradArgs& a, int dt, int tile, bool direct, i
 
 int launch_weight_grad_join(const WeightGradArgs& a, int64_t blocks, void* stream) {
   return launch(&weight_grad_join_kernel, a, blocks, kJoinThreads, 0, stream);
+}
+
+int launch_copy_rows(const CopyRowsArgs& a, int64_t blocks, void* stream) {
+  return launch(&copy_rows_kernel, a, blocks, kCopyThreads, 0, stream);
 }
 
 int launch_act_grad(const ActGradArgs& a, int dt, int64_t blocks, void* stream) {
