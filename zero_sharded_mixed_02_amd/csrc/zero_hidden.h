@@ -135,8 +135,9 @@ struct OrthoSmallArgs {
   int64_t off[kMaxBatch];
 };
 
-constexpr int kNormBlocks = 64;      // most pieces of a matrix's norm
+constexpr int kNormBlocks = 1024;    // most pieces of a matrix's norm
 constexpr int kLoadThreads = 256;
+constexpr int kLoadUnits = 4;        // of eight elements, a thread
 
 constexpr int kBiasCols = 256;     // columns of a bias workgroup
 constexpr int kJoinThreads = 256;

@@ -30,12 +30,6 @@ namespace zk {
 namespace hidden {
 namespace {
 
-template <int DT>
-__device__ __forceinline__ float widen1(uint16_t h) {
-  if constexpr (DT == ZERO_BF16) return __uint_as_float((uint32_t)h << 16);
-  else return (float)__builtin_bit_cast(_Float16, h);
-}
-
 // Sum of squares of a piece of a matrix, in fp64 (exact products of 16-bit
 // values, no overflow).
 template <typename T>
@@ -44,6 +38,7 @@ __global__ void __launch_bounds__(kLoadThreads) ortho_norm_kernel(const OrthoLoa
   const int64_t units = (a.numel + 7) / 8, per = (units + a.norm_blocks - 1) / a.norm_blocks;
   const int64_t u1 = (piece + 1) * per < units ? (piece + 1) * per : units;
   double s = 0.0;
+#pragma unroll 4
   for (int64_t u = piece * per + threadIdx.x; u < u1; u += kLoadThreads) {
     float x[8];
     const int64_t e = u * 8;
@@ -62,30 +57,49 @@ __global__ void __launch_bounds__(kLoadThreads) ortho_norm_kernel(const OrthoLoa
 }
 
 // X = G * 2^k in fp16 with |X| in [32, 64), padded with zeros to multiples of 8,
-// and the factor that is left of 1 / (|G| + eps).
+// and the factor that is left of 1 / (|G| + eps).  A workgroup joins the norm's
+// pieces once for kLoadUnits pieces of eight a thread.
 template <typename T>
 __global__ void __launch_bounds__(kLoadThreads) ortho_load_kernel(const OrthoLoadArgs a) {
   const int upr = a.ld >> 3;
-  const int64_t per = (int64_t)a.rows_pad * upr, blocks = (per + kLoadThreads - 1) / kLoadThreads;
+  const int64_t per = (int64_t)a.rows_pad * upr, span = kLoadThreads * kLoadUnits, blocks = (per + span - 1) / span;
   const int z = (int)(blockIdx.x / blocks);
+  const int64_t u0 = (blockIdx.x - z * blocks) * span + threadIdx.x;
+  Row<T, 8> x[kLoadUnits];
+#pragma unroll
+  for (int i = 0; i < kLoadUnits; ++i) {
+    const int64_t u = u0 + i * kLoadThreads;
+    const int row = (int)(u / upr), col = (int)(u - (int64_t)row * upr) * 8;
+    const int have = u < per && row < a.rows ? a.cols - col : 0;
+    if (have > 0) x[i].load(a.src, a.src_off[z] + (int64_t)row * a.cols + col, have);
+    else x[i].v = {};
+  }
+  __shared__ double w[kLoadThreads / 64];
   double s = 0.0;
-  for (int i = 0; i < a.norm_blocks; ++i) s += a.sums[(int64_t)z * a.norm_blocks + i];
+  for (int i = threadIdx.x; i < a.norm_blocks; i += kLoadThreads) s += a.sums[(int64_t)z * a.norm_blocks + i];
+#pragma unroll
+  for (int k = 32; k > 0; k >>= 1) s += __shfl_xor(s, k);
+  if ((threadIdx.x & 63) == 0) w[threadIdx.x >> 6] = s;
+  __syncthreads();
+  s = 0.0;
+#pragma unroll
+  for (int k = 0; k < kLoadThreads / 64; ++k) s += w[k];
   const double norm = __builtin_sqrt(s), d = norm + a.eps;
   const bool good = d < __builtin_inf();                          // not NaN either
   const int e = good && norm > 0.0 ? 5 - ilogb(norm) : 0;        // |G| 2^e in [32, 64)
-  const int64_t u = (blockIdx.x - z * blocks) * kLoadThreads + threadIdx.x;
-  if (u == 0) {
+  if (u0 == 0) {
     a.factor[2 * z] = good ? (float)(1.0 / ldexp(d, e)) : __builtin_nanf("");
     a.factor[2 * z + 1] = norm > a.eps ? 1.0f : 0.0f;
   }
-  if (u >= per) return;
-  const int row = (int)(u / upr), col = (int)(u - (int64_t)row * upr) * 8;
-  float x[8];
-  const int have = row < a.rows ? a.cols - col : 0;
-  load_row<T, 8>(a.src, a.src_off[z] + (int64_t)row * a.cols + col, have < 8 ? have : 8, x);
 #pragma unroll
-  for (int i = 0; i < 8; ++i) x[i] = good ? ldexpf(x[i], e) : 0.0f;
-  store_row<_Float16, 8>(a.x, z * a.zx + (int64_t)row * a.ld + col, 8, x);
+  for (int i = 0; i < kLoadUnits; ++i) {
+    const int64_t u = u0 + i * kLoadThreads;
+    if (u >= per) break;
+    f16x8 h;
+#pragma unroll
+    for (int k = 0; k < 8; ++k) h[k] = good ? (_Float16)ldexpf((float)x[i].v[k], e) : (_Float16)0.0f;
+    *(AS1 f16x8*)((AS1 _Float16*)a.x + z * a.zx + u * 8) = h;
+  }
 }
 
 __device__ __forceinline__ float factor_of(const OrthoArgs& a, int z) { return a.first ? a.factor[2 * z] : 1.0f; }
