@@ -94,7 +94,7 @@ struct OrthoArgs {
   int64_t za, zb, zout, zadd;
   const float* factor;    // fp32[batch][2]: what the first X is to be multiplied by, and whether to shift
   void* out;              // 16-bit result in the workspace, rows of ldo
-  float* out32;           // kNext: X in fp32, or NULL after the last step
+  void* low;              // kNext: what X's rounding left, bf16, read (not at first) and written
   const void* add;        // kPoly: A - shift I; kNext: X
   int64_t ldo, ldadd;
   int32_t batch, epi;

@@ -346,14 +346,14 @@ struct Group {
 struct OrthoSpace {
   int64_t ldx, ldn, rows_pad, side;   // padded columns of X, of A; padded rows of X
   int64_t zx, zn;                     // elements of X and of A
-  int64_t sums, factor, x0, x1, x32, gram, poly, part, total;
+  int64_t sums, factor, x0, x1, low, gram, poly, part, total;
   Pick c[3];                          // of the three products
 };
 
 // As many matrices as one batch takes: as keep its X, A and B near the caches, or
 // as fill the GPU with tiles.
 int64_t batch_of(int64_t rows, int64_t cols, int64_t count) {
-  const int64_t n = std::min(rows, cols), bytes = rows * cols * 8 + n * n * 4;
+  const int64_t n = std::min(rows, cols), bytes = rows * cols * 6 + n * n * 4;
   const int64_t fill = ceil_div(kCus, ceil_div(rows, kTileSize[kTile256]) * ceil_div(cols, kTileSize[kTile256]));
   const int64_t most = std::max((int64_t(192) << 20) / bytes, fill);
   const int64_t parts = ceil_div(count, std::min<int64_t>(std::max<int64_t>(1, most), kMaxBatch));
@@ -382,7 +382,7 @@ OrthoSpace ortho_space(int64_t rows, int64_t cols, int64_t batch) {
   s.factor = take(batch * 8);
   s.x0 = take(batch * s.zx * 2);
   s.x1 = take(batch * s.zx * 2);
-  s.x32 = take(batch * s.zx * 4);
+  s.low = take(batch * s.zx * 2);
   s.gram = take(batch * s.zn * 2);
   s.poly = take(batch * s.zn * 2);
   s.part = take(std::max({part_bytes(s.c[kGram]), part_bytes(s.c[kPoly]), part_bytes(s.c[kNext])}));
@@ -498,7 +498,7 @@ zero_status ortho_batch(const Group& g, const OrthoSpace& s, int64_t first, int6
   l.ld = (int32_t)s.ldx;
   l.rows_pad = (int32_t)s.rows_pad;
   l.batch = (int32_t)batch;
-  // A piece of a norm is 16 Ki elements or more (8192 x 8192 : 37 us in 1024 pieces, 282 in 64).
+  // A piece of a norm is 16 Ki elements or more (8192 x 8192: 37 us in 1024 pieces, 282 in 64).
   l.norm_blocks = (int32_t)std::max<int64_t>(1, std::min<int64_t>(kNormBlocks, l.numel / 16384));
   for (int64_t i = 0; i < batch; ++i) l.src_off[i] = g.off[first + i];
   const int64_t load_blocks = batch * ceil_div(s.rows_pad * (s.ldx / 8), kLoadThreads * kLoadUnits);
@@ -557,10 +557,10 @@ zero_status ortho_batch(const Group& g, const OrthoSpace& s, int64_t first, int6
     a.p.ldb = tall ? s.ldn : s.ldx;
     a.za = tall ? s.zx : s.zn;
     a.zb = tall ? s.zn : s.zx;
-    a.add = a.first ? x : ws + s.x32;
+    a.add = x;
     a.ldadd = s.ldx;
     a.zadd = s.zx;
-    a.out32 = (float*)(ws + s.x32);
+    a.low = ws + s.low;
     a.out = next;
     a.ldo = s.ldx;
     a.zout = s.zx;

@@ -7,11 +7,14 @@
 // computed and the others mirrored.  A tall matrix takes A = X^T X and X A, so
 // that nothing is transposed in memory.
 //
-// Numbers between the products.  X is held in fp32 for the term a X, and in fp16
-// as the products' operand: directions that the gradient hardly holds are scaled
-// up by a in each step, and X rounded to 16 bits would carry its rounding up
-// with them (a matrix of exponentially falling singular values ends 1.3% off its
-// 64-bit result; with X in fp32 0.04%).  A and B = b A + c A A are held in fp16:
+// Numbers between the products.  X is held in 32 bits for the term a X, and its
+// fp16 rounding is the products' operand: directions that the gradient hardly holds
+// are scaled up by a in each step, and X rounded to 16 bits would carry its rounding
+// up with them (a matrix of exponentially falling singular values ends 1.3% off its
+// 64-bit result; with X in 32 bits 0.04%).  The 32 bits are the
+// fp16 rounding and what it left as bf16: 20 significant bits and more, 8 where
+// fp16 has nothing left (X below 2^-25), for two bytes less to write than an fp32
+// beside the operand.  A and B = b A + c A A are held in fp16:
 // their entries are of order one and below, where fp16 has three bits more than
 // bf16 (1.0% of error against 0.14%).  From the fourth step on A's eigenvalues
 // lie around 1, and A - I/2 is stored in place of A, which halves its largest
@@ -119,24 +122,18 @@ __device__ __forceinline__ void store_half(void* base, int64_t e, const float (&
 template <int EPI, int V>
 struct Epilogue {
   typedef typename Row<_Float16, V>::tv Half;
-  // kPoly: A - d I (V halves); kNext: X, at first as V halves.
-  f32x4 x[EPI == kNext ? V / 4 : 1];
+  typedef typename Row<__bf16, V>::tv Low;
+  Half x;               // kPoly: A - d I; kNext: X,
+  Low low;              // and what its rounding left
 
   __device__ __forceinline__ void load(const OrthoArgs& a, int z, int row, int col) {
     if constexpr (EPI == kGram) return;
     const int64_t e = z * a.zadd + (int64_t)row * a.ldadd + col;
-    if (EPI == kPoly || a.first) {
-      __builtin_memcpy(&x[0], (const AS1 _Float16*)a.add + e, V * 2);
-    } else if constexpr (EPI == kNext) {
-#pragma unroll
-      for (int i = 0; i < V; i += 4) x[i / 4] = *(const AS1 f32x4*)((const AS1 float*)a.add + e + i);
-    }
+    x = *(const AS1 Half*)((const AS1 _Float16*)a.add + e);
+    if (EPI == kNext && !a.first) low = *(const AS1 Low*)((const AS1 __bf16*)a.low + e);
+    else low = Low{};
   }
-  __device__ __forceinline__ float half(int i) const {
-    Half h;
-    __builtin_memcpy(&h, &x[0], V * 2);
-    return (float)h[i];
-  }
+  __device__ __forceinline__ float value(int i) const { return (float)x[i] + (float)low[i]; }
 
   __device__ __forceinline__ void finish(const OrthoArgs& a, int z, int row, int col, float (&v)[V]) const {
     if constexpr (EPI == kGram) {
@@ -146,12 +143,12 @@ struct Epilogue {
     } else if constexpr (EPI == kPoly) {
       const float b = __builtin_fmaf(2.0f * a.c, shift_of(a, z), a.b);
 #pragma unroll
-      for (int i = 0; i < V; ++i) v[i] = __builtin_fmaf(a.c, v[i], b * half(i));
+      for (int i = 0; i < V; ++i) v[i] = __builtin_fmaf(a.c, v[i], b * (float)x[i]);
     } else {
       const float f = factor_of(a, z), d = shift_of(a, z);
       const float c0 = __builtin_fmaf(__builtin_fmaf(a.c, d, a.b), d, a.a);
 #pragma unroll
-      for (int i = 0; i < V; ++i) v[i] = f * __builtin_fmaf(c0, a.first ? half(i) : x[i / 4][i % 4], v[i]);
+      for (int i = 0; i < V; ++i) v[i] = f * __builtin_fmaf(c0, value(i), v[i]);
       if (a.last) {
         if (row < a.rows && col < a.cols) {
           const float s = a.scale[z];
@@ -163,9 +160,10 @@ struct Epilogue {
         }
         return;
       }
-      AS1 float* p = (AS1 float*)a.out32 + z * a.zadd + (int64_t)row * a.ldadd + col;
+      Low left;
 #pragma unroll
-      for (int i = 0; i < V; i += 4) *(AS1 f32x4*)(p + i) = f32x4{v[i], v[i + 1], v[i + 2], v[i + 3]};
+      for (int i = 0; i < V; ++i) left[i] = (__bf16)(v[i] - (float)(_Float16)v[i]);
+      *(AS1 Low*)((AS1 __bf16*)a.low + z * a.zadd + (int64_t)row * a.ldadd + col) = left;
     }
     store_half<V>(a.out, z * a.zout + (int64_t)row * a.ldo + col, v);
   }
