@@ -409,6 +409,7 @@ ORTHO = [
     ([(32, 512, 2), (512, 32, 1), (31, 511, 1), (127, 128, 3), (96, 160, 2), (160, 96, 1)], BF16, BF16, 1),   # the largest of one workgroup
     ([(33, 512, 1), (129, 128, 1), (140, 130, 2), (200, 8, 1), (8, 300, 2)], F16, BF16, 0),                  # and the next
     ([(4097, 200, 1), (200, 4097, 2)], BF16, BF16, 0),
+    ([(130, 136, 131)], BF16, BF16, 3),                      # two batches, the last of which is shorter
     ([(2050, 2300, 1)], F16, BF16, 0),
 ]
 

@@ -350,16 +350,6 @@ struct OrthoSpace {
   Pick c[3];                          // of the three products
 };
 
-// As many matrices as one batch takes: as keep its X, A and B near the caches, or
-// as fill the GPU with tiles.
-int64_t batch_of(int64_t rows, int64_t cols, int64_t count) {
-  const int64_t n = std::min(rows, cols), bytes = rows * cols * 6 + n * n * 4;
-  const int64_t fill = ceil_div(kCus, ceil_div(rows, kTileSize[kTile256]) * ceil_div(cols, kTileSize[kTile256]));
-  const int64_t most = std::max((int64_t(192) << 20) / bytes, fill);
-  const int64_t parts = ceil_div(count, std::min<int64_t>(std::max<int64_t>(1, most), kMaxBatch));
-  return ceil_div(count, parts);
-}
-
 OrthoSpace ortho_space(int64_t rows, int64_t cols, int64_t batch) {
   OrthoSpace s;
   s.ldx = round_up(cols, 8);
@@ -388,6 +378,25 @@ OrthoSpace ortho_space(int64_t rows, int64_t cols, int64_t batch) {
   s.part = take(std::max({part_bytes(s.c[kGram]), part_bytes(s.c[kPoly]), part_bytes(s.c[kNext])}));
   s.total = at;
   return s;
+}
+
+// As many matrices as one batch takes: all of them where X, A and B stay within
+// 1 GiB, as launches of many tiles waste the least (48 matrices of 768 x 768 in one
+// batch, two and four: 870, 875 and 1160 us; 24 of 1024 x 4096 in one and two: 2370
+// and 2520), or a few batches more where those fill their rounds better.
+int64_t batch_of(int64_t rows, int64_t cols, int64_t count) {
+  const int64_t n = std::min(rows, cols), bytes = rows * cols * 6 + n * n * 4;
+  const int64_t most = std::min<int64_t>(std::max<int64_t>(1, (int64_t(1) << 30) / bytes), kMaxBatch);
+  const int64_t fewest = ceil_div(count, most);
+  int64_t best = 0;
+  double us = 1e300;
+  for (int64_t parts = fewest; parts <= std::min(count, fewest + 3); ++parts) {
+    const int64_t batch = ceil_div(count, parts);
+    const OrthoSpace s = ortho_space(rows, cols, batch);
+    const double now = (double)ceil_div(count, batch) * (s.c[kGram].us + s.c[kPoly].us + s.c[kNext].us);
+    if (now < us) us = now, best = batch;
+  }
+  return best;
 }
 
 zero_status collect(zero_plan_t p, const zero_matrix* ms, int32_t n, std::vector<Group>& groups) {
