@@ -346,7 +346,7 @@ struct Group {
 struct OrthoSpace {
   int64_t ldx, ldn, rows_pad, side;   // padded columns of X, of A; padded rows of X
   int64_t zx, zn;                     // elements of X and of A
-  int64_t sums, factor, x0, x1, low, gram, poly, part, total;
+  int64_t sums, factor, x0, x1, low, poly, part, total;    // A lies where the next X goes
   Pick c[3];                          // of the three products
 };
 
@@ -373,7 +373,6 @@ OrthoSpace ortho_space(int64_t rows, int64_t cols, int64_t batch) {
   s.x0 = take(batch * s.zx * 2);
   s.x1 = take(batch * s.zx * 2);
   s.low = take(batch * s.zx * 2);
-  s.gram = take(batch * s.zn * 2);
   s.poly = take(batch * s.zn * 2);
   s.part = take(std::max({part_bytes(s.c[kGram]), part_bytes(s.c[kPoly]), part_bytes(s.c[kNext])}));
   s.total = at;
@@ -385,7 +384,7 @@ OrthoSpace ortho_space(int64_t rows, int64_t cols, int64_t batch) {
 // batch, two and four: 870, 875 and 1160 us; 24 of 1024 x 4096 in one and two: 2370
 // and 2520), or a few batches more where those fill their rounds better.
 int64_t batch_of(int64_t rows, int64_t cols, int64_t count) {
-  const int64_t n = std::min(rows, cols), bytes = rows * cols * 6 + n * n * 4;
+  const int64_t n = std::min(rows, cols), bytes = rows * cols * 6 + n * n * 2;
   const int64_t most = std::min<int64_t>(std::max<int64_t>(1, (int64_t(1) << 30) / bytes), kMaxBatch);
   const int64_t fewest = ceil_div(count, most);
   int64_t best = 0;
@@ -543,16 +542,16 @@ zero_status ortho_batch(const Group& g, const OrthoSpace& s, int64_t first, int6
     a.p.a = a.p.b = x;
     a.p.lda = a.p.ldb = s.ldx;
     a.za = a.zb = s.zx;
-    a.out = ws + s.gram;
+    a.out = next;
     a.ldo = s.ldn;
     a.zout = s.zn;
     if (zero_status st = run_ortho(a, s.side, s.side, wide, s.c[kGram], ws + s.part, stream)) return st;
     // B
     a.epi = kPoly;
-    a.p.a = a.p.b = ws + s.gram;
+    a.p.a = a.p.b = next;
     a.p.lda = a.p.ldb = s.ldn;
     a.za = a.zb = s.zn;
-    a.add = ws + s.gram;
+    a.add = next;
     a.ldadd = s.ldn;
     a.zadd = s.zn;
     a.out = ws + s.poly;
