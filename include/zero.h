@@ -592,8 +592,8 @@ ZERO_API zero_status zero_token_logp_grad(const void* logits, zero_dtype dt, int
  *
  * The products read 16-bit operands (ZERO_F16 or ZERO_BF16, one type for a
  * call) on the matrix units, sum in fp32 and round the finished value once.
- * Rows may start at any element; operands whose rows are 16-byte aligned and a
- * multiple of 8 elements long are read faster.  Infinities and NaN go through
+ * Rows may start at any element; operands with rows of an even length that
+ * start on 4-byte addresses are read faster.  Infinities and NaN go through
  * as in the formulas.
  * --------------------------------------------------------------------- */
 
@@ -753,8 +753,8 @@ typedef struct zero_newton_schulz {
  *   X = G / (|G|_F + eps); `steps` times: A = X X^T, X = a X + (b A + c A A) X
  *   dst = scale * X
  *   (For rows > cols A = X^T X and X A take their places, which is the same X.)
- *   The norm is fp64.  X is held in fp32 and enters the products in fp16, as A
- *   and b A + c A A do; sums are fp32.  The result is within about 0.002 of the
+ *   The norm is fp64.  X is held in 32 bits and enters the products in fp16, as
+ *   A and b A + c A A do; sums are fp32.  The result is within about 0.002 of the
  *   64-bit one (2-norm over the matrix) for the default polynomial.  A matrix
  *   of zeros gives zeros, one that holds NaN or an infinity NaN throughout.
  *   matrices, n_matrices  host array.  No tensor twice.  Matrices of one shape
@@ -763,11 +763,13 @@ typedef struct zero_newton_schulz {
  *   dst, dst_dt the full flat 16-bit buffer of the results; it may be src, with
  *               its type.  Only the listed tensors' ranges are written.
  *   workspace, ws_bytes  zero_orthogonalize_workspace_bytes(...) bytes,
- *               256-byte aligned.
+ *               256-byte aligned: about 8 bytes an element of the shape that
+ *               needs most, up to 1 GiB or what a single matrix takes.
  * Errors: EINVAL for nulls, a tensor out of range or twice, rows or cols < 1 or
  * not dividing the tensor, a scale beyond fp32, a polynomial outside its
  * limits, misalignment, a short workspace or overlapping buffers; EUNSUPPORTED
- * for fp32 or rows or cols above 2^20.
+ * for fp32, rows or cols above 2^20, or a polynomial whose steps take X, A or
+ * b A + c A A beyond 30000, which fp16 would not hold.
  */
 ZERO_API size_t zero_orthogonalize_workspace_bytes(zero_plan_t plan, const zero_matrix* matrices, int32_t n_matrices);
 ZERO_API zero_status zero_orthogonalize(zero_plan_t plan, const zero_matrix* matrices, int32_t n_matrices,

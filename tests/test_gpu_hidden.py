@@ -679,6 +679,43 @@ def test_captured(T, Z):
             assert T.equal(a.view(T.int16) if a.dtype == T.bfloat16 else a, b.view(T.int16) if b.dtype == T.bfloat16 else b), i
 
 
+def test_captured_large(T, Z):
+    """Products of large tiles, with pieces of k and copied operands, and matrices
+    that take every launch of an orthogonalisation, captured and replayed."""
+    n, i, o = 2100, 1031, 770
+    plan = Z.zero_plan(o * i + o, 2, [o * i, o], 0, 8)
+    mats = Z.zero_plan(1100 * 1030, 1, [1100 * 1030], 0, 8)
+    m = Z.Matrices([(0, 1100, 1030, 0.5)])
+    params, x, dz = (randn(T, shape, BF16, k) for k, shape in enumerate([(plan.psi_pad,), (n, i), (n, o)]))
+    update = randn(T, (mats.psi_pad,), BF16, 4)
+    ws = ws_of(T, max(Z.zero_linear_workspace_bytes(plan, 0, i, n), Z.zero_linear_input_grad_workspace_bytes(plan, 0, i, n),
+                      Z.zero_linear_weight_grad_workspace_bytes(plan, 0, i, n, 1), Z.zero_orthogonalize_workspace_bytes(mats, m)))
+
+    def run(y, dx, grad, out):
+        Z.zero_linear(plan, 0, i, params, BF16, x, y, bias=1, act=Z.ZERO_ACT_GELU, workspace=ws)
+        Z.zero_linear_input_grad(plan, 0, i, params, BF16, dz, dx, workspace=ws)
+        Z.zero_linear_weight_grad(plan, 0, i, dz, x, BF16, 1.0, grad, BF16, bias=1, rank=1, workspace=ws)
+        Z.zero_orthogonalize(mats, m, update, BF16, out, BF16, workspace=ws)
+
+    def buffers():
+        return [T.zeros(s, dtype=T.bfloat16, device="cuda") for s in [(n, o), (n, i), (plan.shard_total,), (mats.psi_pad,)]]
+
+    got = buffers()
+    g = T.cuda.CUDAGraph()
+    with T.cuda.graph(g):
+        run(*got)
+    for k in range(3):
+        x.mul_(0.5)
+        update.add_(x.view(-1)[:update.numel()])
+        want = buffers()
+        run(*want)
+        T.cuda.synchronize()
+        g.replay()
+        T.cuda.synchronize()
+        for a, b in zip(want, got):
+            assert T.equal(a, b), k
+
+
 def test_two_streams(T, Z):
     """Two steps at once on two streams, each with its own workspace."""
     twins = [Block(T, Z, seed=s) for s in (0, 30)]

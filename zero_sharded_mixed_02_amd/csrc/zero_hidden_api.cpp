@@ -432,6 +432,25 @@ zero_status collect(zero_plan_t p, const zero_matrix* ms, int32_t n, std::vector
   return ok();
 }
 
+// Whether the matrices between the products stay within fp16: the largest singular
+// values of X, A and b A + c A A over the steps, by points a 256th of the range apart.
+zero_status check_growth(const zero_newton_schulz& q) {
+  constexpr double most = 30000.0;
+  double hi = 1.0;
+  for (int step = 0; step < q.steps; ++step) {
+    double next = 0.0, b = hi * hi;
+    for (int i = 1; i <= 256; ++i) {
+      const double s = hi * i / 256.0, s2 = s * s, t = (q.b + q.c * s2) * s2;
+      b = std::max(b, std::fabs(t));
+      next = std::max(next, std::fabs(s * (q.a + t)));
+    }
+    if (b > most || next > most)
+      return fail(ZERO_EUNSUPPORTED, "step %d of the polynomial reaches singular values of %g, beyond %g", step + 1, std::max(b, next), most);
+    hi = next;
+  }
+  return ok();
+}
+
 // Matrices that one workgroup orthogonalises in its LDS: 16384 elements with the
 // sides rounded up to 32.
 bool is_small(int64_t rows, int64_t cols) {
@@ -759,7 +778,9 @@ zero_status zero_linear_weight_grad(zero_plan_t p, int32_t weight, int32_t bias,
         a.chunk_rows = (int32_t)chunk;
         a.chunks = (int32_t)std::max<int64_t>(1, ceil_div(n, chunk));
         a.col_blocks = (int32_t)ceil_div(hi - lo, kBiasCols);
-        a.bias_blocks = a.chunks * a.col_blocks;
+        const int64_t bias_blocks = (int64_t)a.chunks * a.col_blocks;
+        if (zero_status st = check_grid(bias_blocks, kTileThreads[c.tile])) return st;
+        a.bias_blocks = (int32_t)bias_blocks;
       }
     }
     const int64_t blocks = a.bias_blocks + blocks_of(c);
@@ -828,6 +849,8 @@ zero_status zero_orthogonalize(zero_plan_t p, const zero_matrix* matrices, int32
     for (double v : {q.a, q.b, q.c})
       if (!(std::fabs(v) <= 1000.0)) return fail(ZERO_EINVAL, "coefficient %g exceeds 1000", v);
     if (!(q.eps > 0.0 && q.eps <= 1e30)) return fail(ZERO_EINVAL, "eps must lie in (0, 1e30] (got %g)", q.eps);
+    if (poly)
+      if (zero_status st = check_growth(q)) return st;
     if (zero_status st = check_16(src_dt, "the matrices")) return st;
     if (zero_status st = check_16(dst_dt, "the results")) return st;
     if (zero_status st = check_buffer(src, p->psi_pad, 2, "src")) return st;

@@ -209,6 +209,7 @@ __global__ void __launch_bounds__(kJoinThreads) weight_grad_join_kernel(const We
   const int j = ((int)blockIdx.x - a.join_blocks) * kJoinThreads + threadIdx.x;
   if (j >= cols) return;
   float t = a.bias_part[j];
+#pragma unroll 8
   for (int c = 1; c < a.chunks; ++c) t += a.bias_part[(int64_t)c * cols + j];
   finish_bias(a, a.b_lo + j, t);
 }
