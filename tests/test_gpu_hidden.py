@@ -411,6 +411,11 @@ ORTHO = [
     ([(4097, 200, 1), (200, 4097, 2)], BF16, BF16, 0),
     ([(130, 136, 131)], BF16, BF16, 3),                      # two batches, the last of which is shorter
     ([(2050, 2300, 1)], F16, BF16, 0),
+    # short sides: pieces of A, P X, tall and wide, odd, more than one batch
+    ([(8, 3000, 2), (3000, 8, 1), (17, 5001, 3), (5001, 17, 1), (57, 1000, 1)], BF16, BF16, 3),
+    ([(64, 300, 140), (300, 64, 2), (49, 33333, 1), (33333, 40, 2)], F16, BF16, 0),
+    ([(1, 70000, 1), (70000, 1, 1), (64, 257, 3), (257, 63, 1)], BF16, F16, 1),
+    ([(65, 300, 3), (300, 65, 1), (72, 1000, 2)], BF16, BF16, 0),            # the next longer
 ]
 
 
@@ -455,31 +460,31 @@ def test_orthogonalize(T, Z, case, kind):
         assert T.equal(src[~rest], dst[~rest]) and T.equal(src[rest], kept[rest])
 
 
-@pytest.mark.parametrize("n", [40, 150])
-def test_orthogonalize_values(T, Z, n):
+@pytest.mark.parametrize("n,k", [(40, 40), (150, 150), (40, 700), (700, 40)])
+def test_orthogonalize_values(T, Z, n, k):
     """Zeros, tiny and huge entries, NaN and infinities, each matrix on its own."""
-    plan = Z.zero_plan(7 * n * n, 1, [n * n] * 7, 0, 1)
+    plan = Z.zero_plan(7 * n * k, 1, [n * k] * 7, 0, 1)
     src = randn(T, (plan.psi_pad,), BF16, 1)
-    g = src.view(7, n, n)
+    g = src.view(7, n, k)
     g[1] = 0
     g[2, 3, 4] = math.nan
     g[3, 0, 0] = -math.inf
     g[4] *= 1e-25
     g[5] *= 1e35
     g[6] = 0
-    g[6, n - 1, n - 1] = 3.0
-    m = Z.Matrices([(t, n, n, 1.0) for t in range(7)])
+    g[6, n - 1, k - 1] = 3.0
+    m = Z.Matrices([(t, n, k, 1.0) for t in range(7)])
     ws = ws_of(T, Z.zero_orthogonalize_workspace_bytes(plan, m))
     dst = T.empty_like(src)
     Z.zero_orthogonalize(plan, m, src, BF16, dst, BF16, workspace=ws)
-    out = dst.view(7, n, n)
+    out = dst.view(7, n, k)
     for t in (0, 4, 5, 6):
         ortho_close(T, out[t], ortho64(T, g[t], 1.0), BF16, t)
     assert bool((out[1] == 0).all())
     assert bool(out[2].isnan().all()) and bool(out[3].isnan().all())
 
 
-@pytest.mark.parametrize("shape", [(96, 200), (64, 100), (100, 64)], ids=str)
+@pytest.mark.parametrize("shape", [(96, 200), (64, 100), (100, 64), (40, 900), (900, 40)], ids=str)
 @pytest.mark.parametrize("poly", [(1, 3.4445, -4.7750, 2.0315, 1e-7), (7, 3.4445, -4.7750, 2.0315, 1e-7),
                                   (12, 1.875, -1.25, 0.375, 1e-12), (3, 2.0, 0.0, 0.0, 1e-7), (4, 1.5, -0.5, 0.0, 1.0)], ids=str)
 def test_orthogonalize_polynomials(T, Z, poly, shape):

@@ -112,14 +112,27 @@ struct OrthoArgs {
 // Norms and the first X of a batch.
 struct OrthoLoadArgs {
   const void* src;
-  void* x;                // fp16, rows of ld, padded with zeros
+  void* x;                // fp16, rows `pitch` apart of ld elements, padded with zeros
   double* sums;           // fp64[batch][kNormBlocks]
   float* factor;
   double eps;
   int64_t numel, zx;
+  int64_t pitch, again;   // a second copy lies `again` elements behind the first (0: none)
   int32_t rows, cols, ld, rows_pad, batch, norm_blocks;
   int64_t src_off[kMaxBatch];
 };
+// The polynomials of a batch of matrices whose shorter side is at most kThinSide.
+constexpr int kThinSide = 64;
+constexpr int kThinThreads = 512;
+struct OrthoThinArgs {
+  const float* part;      // fp32[batch][splits][64][64]: pieces of X X^T
+  float* factor;          // as above; takes the power of two that is left out of p
+  void* p;                // fp16[batch][side][2 side]: P, and what its rounding left
+  float a, b, c;
+  int32_t steps, splits;
+  int32_t n, side;        // the shorter side, and rounded up to 8
+};
+
 // A batch of matrices of one shape that a workgroup each orthogonalises in LDS.
 constexpr int kSmallElems = 16384;
 constexpr int kSmallThreads = 512;
@@ -150,6 +163,7 @@ int launch_linear_join(const LinearArgs& a, int epi, int dt, int64_t blocks, voi
 int launch_weight_grad(const WeightGradArgs& a, int dt, int tile, bool direct, int64_t blocks, void* stream);
 int launch_weight_grad_join(const WeightGradArgs& a, int64_t blocks, void* stream);
 int launch_ortho_small(const OrthoSmallArgs& a, int64_t batch, void* stream);
+int launch_ortho_thin(const OrthoThinArgs& a, int64_t batch, void* stream);
 int launch_ortho_norm(const OrthoLoadArgs& a, int dt, void* stream);
 int launch_ortho_load(const OrthoLoadArgs& a, int dt, int64_t blocks, void* stream);
 int launch_ortho(const OrthoArgs& a, int tile, int64_t blocks, void* stream);

@@ -346,6 +346,7 @@ struct Group {
 struct OrthoSpace {
   int64_t ldx, ldn, rows_pad, side;   // padded columns of X, of A; padded rows of X
   int64_t zx, zn;                     // elements of X and of A
+  int64_t pitch, again;               // of X: elements between rows, and to its second copy (0: none)
   int64_t sums, factor, x0, x1, low, poly, part, total;    // A lies where the next X goes
   Pick c[3];                          // of the three products
 };
@@ -359,6 +360,8 @@ OrthoSpace ortho_space(int64_t rows, int64_t cols, int64_t batch) {
   const int64_t wide = std::max(s.rows_pad, s.ldx);
   s.zx = s.rows_pad * s.ldx;
   s.zn = s.side * s.ldn;
+  s.pitch = s.ldx;
+  s.again = 0;
   s.c[kGram] = pick(s.side, s.side, wide, batch, 0, true);
   s.c[kPoly] = pick(s.side, s.side, s.side, batch, 0, true);
   s.c[kNext] = pick(s.rows_pad, s.ldx, s.side, batch, 0);
@@ -379,6 +382,45 @@ OrthoSpace ortho_space(int64_t rows, int64_t cols, int64_t batch) {
   return s;
 }
 
+// The same for matrices with a short side (zn is P's): X twice along k, pieces of A.
+OrthoSpace thin_space(int64_t rows, int64_t cols, int64_t batch) {
+  OrthoSpace s;
+  memset(&s, 0, sizeof s);
+  const bool tall = rows > cols;
+  s.ldx = round_up(cols, 8);
+  s.rows_pad = round_up(rows, 8);
+  s.side = std::min(s.rows_pad, s.ldx);
+  s.ldn = 2 * s.side;
+  s.zx = 2 * s.rows_pad * s.ldx;
+  s.zn = s.side * s.ldn;
+  s.pitch = tall ? 2 * s.ldx : s.ldx;
+  s.again = tall ? s.ldx : s.rows_pad * s.ldx;
+  // Pieces of A: two workgroups a CU, of four stages or more.
+  const int64_t stages = ceil_div(std::max(s.rows_pad, s.ldx), kStage);
+  const int64_t want = std::max<int64_t>(1, std::min({ceil_div(2 * kCus, batch), stages / 4, int64_t(32)}));
+  s.c[kGram] = {kTile64, 0, batch, (int)ceil_div(stages, ceil_div(stages, want)), 0.0};
+  s.c[kNext] = pick(s.rows_pad, s.ldx, 2 * s.side, batch, 0);
+  int64_t at = 0;
+  auto take = [&](int64_t bytes) {
+    const int64_t here = at;
+    at += round_up(bytes, 256);
+    return here;
+  };
+  s.sums = take(batch * kNormBlocks * 8);
+  s.factor = take(batch * 8);
+  s.x0 = take(batch * s.zx * 2);
+  s.poly = take(batch * s.zn * 2);
+  s.part = take(std::max(batch * s.c[kGram].splits * kThinSide * kThinSide * 4, part_bytes(s.c[kNext])));
+  s.total = at;
+  return s;
+}
+
+bool is_thin(int64_t rows, int64_t cols) { return std::min(rows, cols) <= kThinSide; }
+
+OrthoSpace space_of(int64_t rows, int64_t cols, int64_t batch) {
+  return is_thin(rows, cols) ? thin_space(rows, cols, batch) : ortho_space(rows, cols, batch);
+}
+
 // As many matrices as one batch takes: all of them where X, A and B stay within
 // 1 GiB, as launches of many tiles waste the least (48 matrices of 768 x 768 in one
 // batch, two and four: 870, 875 and 1160 us; 24 of 1024 x 4096 in one and two: 2370
@@ -391,7 +433,7 @@ int64_t batch_of(int64_t rows, int64_t cols, int64_t count) {
   double us = 1e300;
   for (int64_t parts = fewest; parts <= std::min(count, fewest + 3); ++parts) {
     const int64_t batch = ceil_div(count, parts);
-    const OrthoSpace s = ortho_space(rows, cols, batch);
+    const OrthoSpace s = space_of(rows, cols, batch);
     const double now = (double)ceil_div(count, batch) * (s.c[kGram].us + s.c[kPoly].us + s.c[kNext].us);
     if (now < us) us = now, best = batch;
   }
@@ -460,7 +502,7 @@ bool is_small(int64_t rows, int64_t cols) {
 int64_t ortho_bytes(const std::vector<Group>& groups) {
   int64_t most = 0;
   for (const Group& g : groups)
-    if (!g.off.empty() && !is_small(g.rows, g.cols)) most = std::max(most, ortho_space(g.rows, g.cols, batch_of(g.rows, g.cols, (int64_t)g.off.size())).total);
+    if (!g.off.empty() && !is_small(g.rows, g.cols)) most = std::max(most, space_of(g.rows, g.cols, batch_of(g.rows, g.cols, (int64_t)g.off.size())).total);
   return most;
 }
 
@@ -508,9 +550,9 @@ zero_status ortho_small(const Group& g, int64_t first, int64_t batch, const zero
   return launched(launch_ortho_small(a, batch, stream));
 }
 
-zero_status ortho_batch(const Group& g, const OrthoSpace& s, int64_t first, int64_t batch, const zero_newton_schulz& poly, const void* src, int src_dt,
-                        void* dst, int dst_dt, char* ws, void* stream) {
-  const bool tall = g.rows > g.cols;
+// The norms and the first X of a batch.
+zero_status ortho_load(const Group& g, const OrthoSpace& s, int64_t first, int64_t batch, const zero_newton_schulz& poly, const void* src,
+                       int src_dt, char* ws, void* stream) {
   OrthoLoadArgs l;
   memset(&l, 0, sizeof l);
   l.src = src;
@@ -520,6 +562,8 @@ zero_status ortho_batch(const Group& g, const OrthoSpace& s, int64_t first, int6
   l.eps = poly.eps;
   l.numel = g.rows * g.cols;
   l.zx = s.zx;
+  l.pitch = s.pitch;
+  l.again = s.again;
   l.rows = (int32_t)g.rows;
   l.cols = (int32_t)g.cols;
   l.ld = (int32_t)s.ldx;
@@ -531,13 +575,15 @@ zero_status ortho_batch(const Group& g, const OrthoSpace& s, int64_t first, int6
   const int64_t load_blocks = batch * ceil_div(s.rows_pad * (s.ldx / 8), kLoadThreads * kLoadUnits);
   if (zero_status st = check_grid(load_blocks, kLoadThreads)) return st;
   if (const int err = launch_ortho_norm(l, src_dt, stream)) return hip_fail(err);
-  if (const int err = launch_ortho_load(l, src_dt, load_blocks, stream)) return hip_fail(err);
+  return launched(launch_ortho_load(l, src_dt, load_blocks, stream));
+}
 
-  OrthoArgs a;
+// What the products of a batch share.
+void ortho_args(OrthoArgs& a, const Group& g, const OrthoSpace& s, int64_t first, int64_t batch, void* dst, int dst_dt, char* ws) {
   memset(&a, 0, sizeof a);
-  a.factor = l.factor;
+  a.factor = (const float*)(ws + s.factor);
   a.batch = (int32_t)batch;
-  a.tall = tall;
+  a.tall = g.rows > g.cols;
   a.rows = (int32_t)g.rows;
   a.cols = (int32_t)g.cols;
   a.dst = dst;
@@ -546,6 +592,14 @@ zero_status ortho_batch(const Group& g, const OrthoSpace& s, int64_t first, int6
     a.scale[i] = g.scale[first + i];
     a.dst_off[i] = g.off[first + i];
   }
+}
+
+zero_status ortho_batch(const Group& g, const OrthoSpace& s, int64_t first, int64_t batch, const zero_newton_schulz& poly, const void* src, int src_dt,
+                        void* dst, int dst_dt, char* ws, void* stream) {
+  const bool tall = g.rows > g.cols;
+  if (zero_status st = ortho_load(g, s, first, batch, poly, src, src_dt, ws, stream)) return st;
+  OrthoArgs a;
+  ortho_args(a, g, s, first, batch, dst, dst_dt, ws);
   a.a = (float)poly.a;
   a.b = (float)poly.b;
   a.c = (float)poly.c;
@@ -595,6 +649,51 @@ zero_status ortho_batch(const Group& g, const OrthoSpace& s, int64_t first, int6
     std::swap(x, next);
   }
   return ok();
+}
+
+// Matrices with a short side: A's pieces, P from them, P X.
+zero_status ortho_thin(const Group& g, const OrthoSpace& s, int64_t first, int64_t batch, const zero_newton_schulz& poly, const void* src, int src_dt,
+                       void* dst, int dst_dt, char* ws, void* stream) {
+  const bool tall = g.rows > g.cols;
+  if (zero_status st = ortho_load(g, s, first, batch, poly, src, src_dt, ws, stream)) return st;
+  OrthoArgs a;
+  ortho_args(a, g, s, first, batch, dst, dst_dt, ws);
+  Pick c = s.c[kGram];
+  c.cut = batch;
+  a.epi = kGram;
+  a.p.a = a.p.b = ws + s.x0;
+  a.p.lda = a.p.ldb = s.pitch;
+  a.za = a.zb = s.zx;
+  lay_out(a.p, s.side, s.side, std::max(s.rows_pad, s.ldx), c, ws + s.part, true);
+  if (zero_status st = check_grid(blocks_of(c), kTileThreads[c.tile])) return st;
+  if (const int err = launch_ortho(a, c.tile, blocks_of(c), stream)) return hip_fail(err);
+
+  OrthoThinArgs t;
+  memset(&t, 0, sizeof t);
+  t.part = (const float*)(ws + s.part);
+  t.factor = (float*)(ws + s.factor);
+  t.p = ws + s.poly;
+  t.a = (float)poly.a;
+  t.b = (float)poly.b;
+  t.c = (float)poly.c;
+  t.steps = poly.steps;
+  t.splits = a.p.splits;
+  t.n = (int32_t)std::min(g.rows, g.cols);
+  t.side = (int32_t)s.side;
+  if (const int err = launch_ortho_thin(t, batch, stream)) return hip_fail(err);
+
+  a.epi = kNext;              // with a = b = c = 0, so that X itself adds nothing
+  a.first = a.last = 1;
+  a.p.a = tall ? ws + s.x0 : ws + s.poly;
+  a.p.b = tall ? ws + s.poly : ws + s.x0;
+  a.p.lda = tall ? s.pitch : s.ldn;
+  a.p.ldb = tall ? s.ldn : s.pitch;
+  a.za = tall ? s.zx : s.zn;
+  a.zb = tall ? s.zn : s.zx;
+  a.add = ws + s.x0;
+  a.ldadd = s.pitch;
+  a.zadd = s.zx;
+  return run_ortho(a, s.rows_pad, s.ldx, 2 * s.side, s.c[kNext], ws + s.part, stream);
 }
 
 }  // namespace
@@ -871,9 +970,10 @@ zero_status zero_orthogonalize(zero_plan_t p, const zero_matrix* matrices, int32
         continue;
       }
       const int64_t batch = batch_of(g.rows, g.cols, count);
-      const OrthoSpace s = ortho_space(g.rows, g.cols, batch);   // a smaller last batch takes the same shapes
+      const OrthoSpace s = space_of(g.rows, g.cols, batch);      // a smaller last batch takes the same shapes
+      const auto run = is_thin(g.rows, g.cols) ? ortho_thin : ortho_batch;
       for (int64_t i = 0; i < count; i += batch)
-        if (zero_status st = ortho_batch(g, s, i, std::min(batch, count - i), q, src, src_dt, dst, dst_dt, (char*)workspace, stream))
+        if (zero_status st = run(g, s, i, std::min(batch, count - i), q, src, src_dt, dst, dst_dt, (char*)workspace, stream))
           return st;
     }
     return ok();

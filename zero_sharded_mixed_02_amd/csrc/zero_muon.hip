@@ -102,7 +102,10 @@ __global__ void __launch_bounds__(kLoadThreads) ortho_load_kernel(const OrthoLoa
     f16x8 h;
 #pragma unroll
     for (int k = 0; k < 8; ++k) h[k] = good ? (_Float16)ldexpf((float)x[i].v[k], e) : (_Float16)0.0f;
-    *(AS1 f16x8*)((AS1 _Float16*)a.x + z * a.zx + u * 8) = h;
+    const int row = (int)(u / upr), col = (int)(u - (int64_t)row * upr) * 8;
+    AS1 _Float16* x16 = (AS1 _Float16*)a.x + z * a.zx + row * a.pitch + col;
+    *(AS1 f16x8*)x16 = h;
+    if (a.again) *(AS1 f16x8*)(x16 + a.again) = h;
   }
 }
 
@@ -210,6 +213,143 @@ __global__ void __launch_bounds__(kJoinThreads) ortho_join_kernel(const OrthoArg
 #pragma unroll
       for (int i = 0; i < 4; ++i) ((AS1 _Float16*)a.out)[z * a.zout + (int64_t)(col + i) * a.ldo + row] = (_Float16)v[i];
     }
+  }
+}
+
+// ---------------------------------------------------------------------------
+// Matrices with a short side
+// ---------------------------------------------------------------------------
+
+// With n = the shorter side up to 64 the steps need X only once: each multiplies X by
+// Q = a I + b A + c A^2, and the next A is Q A Q.  One workgroup forms P, the product
+// of the Q, in fp32 from A = X X^T, whose pieces a launch of products has summed from
+// the gradient's own bits; a last product takes X to P X, with P as two fp16 numbers
+// along k.  In fp32 A's rounding shows in P as 0.0005 of the result at most (falling
+// singular values, where rounding A to fp16 would leave nothing).  Five launches in
+// the place of 17 (43 matrices of 33 x 7489: 271 -> 86 us); this one is a chain of 18
+// products in LDS at the fp32 matrix rate of one CU (a side of 64: 29 us, 16: 9).
+template <int NT>      // tiles of 16 along a side
+__global__ void __launch_bounds__(kThinThreads) ortho_thin_kernel(const OrthoThinArgs a) {
+  extern __shared__ __attribute__((aligned(1024))) char smem[];
+  __shared__ float most[kThinThreads / 64];
+  constexpr int kPitch = kThinSide + 4;      // floats: 16 rows' 16 bytes lie in different banks
+  ZK_LDS float* const A = (ZK_LDS float*)(ZK_LDS char*)smem;
+  ZK_LDS float* const Q = A + kThinSide * kPitch;
+  ZK_LDS float* const P = Q + kThinSide * kPitch;
+  ZK_LDS float* const T = P + kThinSide * kPitch;
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), z = blockIdx.x;
+  const float f = a.factor[2 * z];
+
+  const AS1 float* part = (const AS1 float*)a.part + (int64_t)z * a.splits * kThinSide * kThinSide;
+  for (int u = threadIdx.x; u < kThinSide * kThinSide / 4; u += kThinThreads) {
+    const int row = u / (kThinSide / 4), col = u % (kThinSide / 4) * 4;
+    double s[4] = {0.0, 0.0, 0.0, 0.0};
+    if (row < a.side && col < a.side) {
+#pragma unroll 4
+      for (int i = 0; i < a.splits; ++i) {
+        const f32x4 v = *(const AS1 f32x4*)(part + (int64_t)i * kThinSide * kThinSide + u * 4);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) s[k] += (double)v[k];
+      }
+    }
+    f32x4 v, one;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      v[k] = (float)(s[k] * (double)f * (double)f);
+      one[k] = row == col + k && row < a.n ? 1.0f : 0.0f;
+    }
+    *(ZK_LDS f32x4*)(A + row * kPitch + col) = v;
+    *(ZK_LDS f32x4*)(P + row * kPitch + col) = one;
+  }
+  __syncthreads();
+
+  // A wave's tiles of 16 x 16, two at most; a lane has four columns of a row.
+  constexpr int kMine = (NT * NT + 7) / 8;
+  const auto place16 = [&](int i, int& row, int& col) {
+    const int t = wave * kMine + i;
+    row = t / NT * 16 + (lane & 15);
+    col = t % NT * 16 + (lane >> 4) * 4;
+    return t < NT * NT;
+  };
+  // l r for symmetric r.
+  const auto product = [&](const ZK_LDS float* l, const ZK_LDS float* r, f32x4 (&acc)[kMine]) {
+    f32x4 x[kMine][NT], y[kMine][NT];
+#pragma unroll
+    for (int k = 0; k < NT; ++k) {
+#pragma unroll
+      for (int i = 0; i < kMine; ++i) {
+        const int t = wave * kMine + i, tile = t < NT * NT ? t : 0;      // a wave too many does the first again
+        x[i][k] = *(const ZK_LDS f32x4*)(l + (tile / NT * 16 + (lane & 15)) * kPitch + (lane >> 4) * 4 + k * 16);
+        y[i][k] = *(const ZK_LDS f32x4*)(r + (tile % NT * 16 + (lane & 15)) * kPitch + (lane >> 4) * 4 + k * 16);
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < kMine; ++i) acc[i] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int k = 0; k < NT * 4; ++k)
+#pragma unroll
+      for (int i = 0; i < kMine; ++i)
+        acc[i] = __builtin_amdgcn_mfma_f32_16x16x4f32(y[i][k / 4][k % 4], x[i][k / 4][k % 4], acc[i], 0, 0, 0);
+  };
+  int row, col;
+  f32x4 s[kMine], t[kMine];
+#pragma unroll 1
+  for (int step = 0; step < a.steps; ++step) {
+    product(A, A, s);
+#pragma unroll
+    for (int i = 0; i < kMine; ++i) {
+      if (!place16(i, row, col)) continue;
+      const f32x4 x = *(const ZK_LDS f32x4*)(A + row * kPitch + col);
+      f32x4 q;
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+        q[k] = __builtin_fmaf(a.c, s[i][k], __builtin_fmaf(a.b, x[k], row == col + k && row < a.n ? a.a : 0.0f));
+      *(ZK_LDS f32x4*)(Q + row * kPitch + col) = q;
+    }
+    __syncthreads();
+    const bool last = step + 1 == a.steps;
+    product(Q, P, s);
+    if (!last) product(Q, A, t);
+    __syncthreads();        // nobody reads P and A any more
+#pragma unroll
+    for (int i = 0; i < kMine; ++i) {
+      if (!place16(i, row, col)) continue;
+      *(ZK_LDS f32x4*)(P + row * kPitch + col) = s[i];
+      if (!last) *(ZK_LDS f32x4*)(T + row * kPitch + col) = t[i];
+    }
+    __syncthreads();
+    if (last) break;
+    product(T, Q, s);
+#pragma unroll
+    for (int i = 0; i < kMine; ++i)
+      if (place16(i, row, col)) *(ZK_LDS f32x4*)(A + row * kPitch + col) = s[i];
+    __syncthreads();
+  }
+
+  // P times a power of two that brings its largest entry to 2^12.
+  float m = 0.0f;
+  for (int u = threadIdx.x; u < a.side * a.side; u += kThinThreads) {
+    const float x = __builtin_fabsf(P[u / a.side * kPitch + u % a.side]);
+    m = x > m ? x : m;
+  }
+#pragma unroll
+  for (int k = 32; k > 0; k >>= 1) {
+    const float x = __shfl_xor(m, k);
+    m = x > m ? x : m;
+  }
+  if (lane == 0) most[wave] = m;
+  __syncthreads();
+#pragma unroll
+  for (int k = 0; k < kThinThreads / 64; ++k) m = most[k] > m ? most[k] : m;
+  const int e = m > 0.0f && m < __builtin_inff() ? ilogbf(m) - 12 : 0;
+  if (threadIdx.x == 0) a.factor[2 * z] = ldexpf(f, e);
+  AS1 _Float16* const out = (AS1 _Float16*)a.p + (int64_t)z * a.side * 2 * a.side;
+  for (int u = threadIdx.x; u < a.side * a.side; u += kThinThreads) {
+    const int r = u / a.side, c = u % a.side;
+    const float x = ldexpf(P[r * kPitch + c], -e);
+    const _Float16 hi = (_Float16)x;
+    out[r * 2 * a.side + c] = hi;
+    out[r * 2 * a.side + a.side + c] = (_Float16)(x - (float)hi);
   }
 }
 
@@ -393,6 +533,16 @@ int launch_ortho_small(const OrthoSmallArgs& a, int64_t batch, void* stream) {
   const int lds = a.rp * (a.cp * 2 + 16) + 2 * side * (side * 2 + 16);
   return a.src_dt == ZERO_BF16 ? launch(&ortho_small_kernel<__bf16>, a, batch, kSmallThreads, lds, stream)
                                : launch(&ortho_small_kernel<_Float16>, a, batch, kSmallThreads, lds, stream);
+}
+
+int launch_ortho_thin(const OrthoThinArgs& a, int64_t batch, void* stream) {
+  const int lds = 4 * kThinSide * (kThinSide + 4) * 4;
+  switch ((a.side + 15) / 16) {
+    case 1: return launch(&ortho_thin_kernel<1>, a, batch, kThinThreads, lds, stream);
+    case 2: return launch(&ortho_thin_kernel<2>, a, batch, kThinThreads, lds, stream);
+    case 3: return launch(&ortho_thin_kernel<3>, a, batch, kThinThreads, lds, stream);
+    default: return launch(&ortho_thin_kernel<4>, a, batch, kThinThreads, lds, stream);
+  }
 }
 
 int launch_ortho_norm(const OrthoLoadArgs& a, int dt, void* stream) {
