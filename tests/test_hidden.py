@@ -1,11 +1,15 @@
 """The operators on the hidden matrices, without a GPU: the refusals of the C
-entries and of the binding (all before anything is launched), and the workspace
-sizes."""
+entries and of the binding (all before anything is launched), the workspace
+sizes and the launch shapes."""
 import ctypes
 import math
+import os
+import shutil
+import subprocess
 
 import pytest
 
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 BASE = 1 << 40        # fake addresses, never dereferenced
 GIB = 1 << 30
 
@@ -217,3 +221,21 @@ def test_binding_refuses(Z):
         Z.zero_muon_momentum(p, 0, Z.MuonHyper(0.1), None, P(0), P(1), P(2), Z.ZERO_F32, True)
     with pytest.raises(Z.ZeroError):
         Z.zero_linear(p, 0, 8, P(0), Z.ZERO_F32, P(1), P(2), n=4, stream=0)
+
+
+@pytest.mark.skipif(shutil.which("g++") is None, reason="g++ not available")
+def test_launch_shapes(tmp_path):
+    """The host code with stand-ins for the launchers, over random sizes,
+    strides, types, owners and lists of matrices: every launch covers its work
+    and stays inside its buffers, and parts of the workspace that have to be
+    apart are (tests/native/hidden_shapes.cpp)."""
+    exe = tmp_path / "hidden_shapes"
+    csrc = os.path.join(ROOT, "zero_sharded_mixed_02_amd", "csrc")
+    cmd = ["g++", "-std=c++17", "-O1", "-g", "-fsanitize=address,undefined", "-fno-sanitize-recover=undefined", "-Wall",
+           "-Werror", "-I", os.path.join(ROOT, "include"), "-I", csrc, os.path.join(ROOT, "tests", "native", "hidden_shapes.cpp"),
+           os.path.join(csrc, "zero_api.cpp"), os.path.join(csrc, "zero_hidden_api.cpp"), "-o", str(exe)]
+    subprocess.run(cmd, check=True, capture_output=True, text=True)
+    env = dict(os.environ, ASAN_OPTIONS="detect_leaks=1:verify_asan_link_order=0")
+    r = subprocess.run([str(exe)], capture_output=True, text=True, env=env, timeout=300)
+    assert r.returncode == 0, r.stdout + r.stderr
+    assert " 0 failures" in r.stdout
