@@ -359,8 +359,9 @@ __global__ void __launch_bounds__(kThinThreads) ortho_thin_kernel(const OrthoThi
 
 // A whole matrix of up to 16384 elements by one workgroup: X, A and B in LDS in fp16,
 // X also in fp32 in the registers of the wave whose tiles of 16 x 16 it is, eight at
-// most.  One launch in the place of 17, each of which is latency alone (65 x 33: 26.7 us,
-// 67 with them).  Rows are 16 bytes apart beyond their length, so that a fragment's 16
+// most.  One launch in the place of 17, each of which is latency alone (65 x 33: 13.1 us,
+// 67 with them; 26.7 while a wave's tiles were divided out in every product and its
+// fragments were not under way ahead).  Rows are 16 bytes apart beyond their length, so that a fragment's 16
 // rows lie in different banks.
 struct Small {
   ZK_LDS char* p;
@@ -379,11 +380,29 @@ struct Small {
   __device__ __forceinline__ ZK_LDS half4* at(int row, int col) const { return (ZK_LDS half4*)(p + row * pitch + col * 2); }
 };
 
-template <typename T>
+// A wave's tiles of 16 x 16, with the divisions done once.  Beyond the last tile it
+// does the first again and keeps nothing, so that no product has a branch.
+template <int N>
+struct SmallTiles {
+  int count, row[N], col[N];
+  __device__ __forceinline__ SmallTiles(int wave, int down, int across) : count(0) {
+    const int each = (down * across + kSmallThreads / 64 - 1) / (kSmallThreads / 64);
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const int t = wave * each + i;
+      const bool mine = i < each && t < down * across;
+      row[i] = mine ? t / across * 16 : 0;
+      col[i] = mine ? t % across * 16 : 0;
+      if (mine) count = i + 1;
+    }
+  }
+};
+
+template <typename T, int MX, int MN>      // tiles a wave of X, and of the n x n results, at most
 __global__ void __launch_bounds__(kSmallThreads) ortho_small_kernel(const OrthoSmallArgs a) {
   extern __shared__ __attribute__((aligned(1024))) char smem[];
   __shared__ double sums[kSmallThreads / 64];
-  constexpr int kWaves = kSmallThreads / 64, kMine = 8;
+  constexpr int kWaves = kSmallThreads / 64;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), z = blockIdx.x;
   const bool tall = a.rows > a.cols;
   const int side = a.rp < a.cp ? a.rp : a.cp, wide = a.rp < a.cp ? a.cp : a.rp;
@@ -425,78 +444,82 @@ __global__ void __launch_bounds__(kSmallThreads) ortho_small_kernel(const OrthoS
   }
   __syncthreads();
 
-  const int rt = a.rp / 16, ct = a.cp / 16, nt = side / 16, mine = (rt * ct + kWaves - 1) / kWaves, mine_n = (nt * nt + kWaves - 1) / kWaves;
+  // The wave's tiles of X and of the n x n results.
   const int q = lane >> 4, c = lane & 15;
-  f32x4 x32[kMine], acc[kMine];
+  const SmallTiles<MX> of_x(wave, a.rp / 16, a.cp / 16);
+  const SmallTiles<MN> of_n(wave, side / 16, side / 16);
+  f32x4 x32[MX], acc_x[MX], acc_n[MN];
 #pragma unroll
-  for (int i = 0; i < kMine; ++i) {
-    const int t = wave * mine + i;
-    x32[i] = f32x4{0.f, 0.f, 0.f, 0.f};
-    if (i < mine && t < rt * ct) {
-      const Small::half4 h = *X.at(t / ct * 16 + c, t % ct * 16 + q * 4);
-      x32[i] = f32x4{(float)h[0], (float)h[1], (float)h[2], (float)h[3]};
-    }
+  for (int i = 0; i < MX; ++i) {
+    const Small::half4 h = *X.at(of_x.row[i] + c, of_x.col[i] + q * 4);
+    x32[i] = f32x4{(float)h[0], (float)h[1], (float)h[2], (float)h[3]};
   }
-  // acc = the wave's tiles of a product, of `tiles` in rows of `across`.
-  auto product = [&](int tiles, int across, int each, int depth, auto left, auto right) {
+  // acc = the wave's tiles of a product; a depth is a multiple of 32.
+  auto product = [&](const auto& tiles, auto& acc, int depth, auto left, auto right) {
+    constexpr int N = sizeof(acc) / sizeof(acc[0]);
 #pragma unroll
-    for (int i = 0; i < kMine; ++i) acc[i] = f32x4{0.f, 0.f, 0.f, 0.f};
+    for (int i = 0; i < N; ++i) acc[i] = f32x4{0.f, 0.f, 0.f, 0.f};
+    s16x8 l[N], r[N];
+#pragma unroll
+    for (int i = 0; i < N; ++i) l[i] = left(tiles.row[i], 0), r[i] = right(tiles.col[i], 0);
 #pragma unroll 1
-    for (int k = 0; k < depth; k += 32) {
+    for (int k = 32; k < depth; k += 32) {      // the next fragments under way
+      s16x8 l1[N], r1[N];
 #pragma unroll
-      for (int i = 0; i < kMine; ++i) {
-        const int t = wave * each + i;
-        if (i < each && t < tiles) acc[i] = mfma<_Float16>(right(t % across * 16, k), left(t / across * 16, k), acc[i]);
-      }
+      for (int i = 0; i < N; ++i) l1[i] = left(tiles.row[i], k), r1[i] = right(tiles.col[i], k);
+#pragma unroll
+      for (int i = 0; i < N; ++i) acc[i] = mfma<_Float16>(r[i], l[i], acc[i]);
+#pragma unroll
+      for (int i = 0; i < N; ++i) l[i] = l1[i], r[i] = r1[i];
     }
+#pragma unroll
+    for (int i = 0; i < N; ++i) acc[i] = mfma<_Float16>(r[i], l[i], acc[i]);
   };
 #pragma unroll 1
   for (int step = 0; step < a.steps; ++step) {
     const float d = step >= a.shift_from ? may_shift : 0.0f;
-    if (tall)
-      product(nt * nt, nt, mine_n, wide, [&](int r, int k) { return X.across(r, k, lane); }, [&](int r, int k) { return X.across(r, k, lane); });
-    else
-      product(nt * nt, nt, mine_n, wide, [&](int r, int k) { return X.along(r, k, lane); }, [&](int r, int k) { return X.along(r, k, lane); });
+    if (tall) product(of_n, acc_n, wide, [&](int r, int k) { return X.across(r, k, lane); }, [&](int r, int k) { return X.across(r, k, lane); });
+    else product(of_n, acc_n, wide, [&](int r, int k) { return X.along(r, k, lane); }, [&](int r, int k) { return X.along(r, k, lane); });
 #pragma unroll
-    for (int i = 0; i < kMine; ++i) {
-      const int t = wave * mine_n + i, row = t / nt * 16 + c, col = t % nt * 16 + q * 4;
-      if (i < mine_n && t < nt * nt) {
+    for (int i = 0; i < MN; ++i) {
+      const int row = of_n.row[i] + c, col = of_n.col[i] + q * 4;
+      if (i < of_n.count) {
         Small::half4 h;
 #pragma unroll
-        for (int k = 0; k < 4; ++k) h[k] = (_Float16)__builtin_fmaf(f * f, acc[i][k], row == col + k ? -d : 0.0f);
+        for (int k = 0; k < 4; ++k) h[k] = (_Float16)__builtin_fmaf(f * f, acc_n[i][k], row == col + k ? -d : 0.0f);
         *A.at(row, col) = h;
       }
     }
     __syncthreads();
-    product(nt * nt, nt, mine_n, side, [&](int r, int k) { return A.along(r, k, lane); }, [&](int r, int k) { return A.along(r, k, lane); });
+    product(of_n, acc_n, side, [&](int r, int k) { return A.along(r, k, lane); }, [&](int r, int k) { return A.along(r, k, lane); });
     const float b = __builtin_fmaf(2.0f * a.c, d, a.b), c0 = __builtin_fmaf(__builtin_fmaf(a.c, d, a.b), d, a.a);
 #pragma unroll
-    for (int i = 0; i < kMine; ++i) {
-      const int t = wave * mine_n + i, row = t / nt * 16 + c, col = t % nt * 16 + q * 4;
-      if (i < mine_n && t < nt * nt) {
+    for (int i = 0; i < MN; ++i) {
+      const int row = of_n.row[i] + c, col = of_n.col[i] + q * 4;
+      if (i < of_n.count) {
         const Small::half4 x = *A.at(row, col);
         Small::half4 h;
 #pragma unroll
-        for (int k = 0; k < 4; ++k) h[k] = (_Float16)__builtin_fmaf(a.c, acc[i][k], b * (float)x[k]);
+        for (int k = 0; k < 4; ++k) h[k] = (_Float16)__builtin_fmaf(a.c, acc_n[i][k], b * (float)x[k]);
         *B.at(row, col) = h;
       }
     }
     __syncthreads();
     if (tall)
-      product(rt * ct, ct, mine, side, [&](int r, int k) { return X.along(r, k, lane); }, [&](int r, int k) { return B.along(r, k, lane); });
+      product(of_x, acc_x, side, [&](int r, int k) { return X.along(r, k, lane); }, [&](int r, int k) { return B.along(r, k, lane); });
     else
-      product(rt * ct, ct, mine, side, [&](int r, int k) { return B.along(r, k, lane); }, [&](int r, int k) { return X.across(r, k, lane); });
+      product(of_x, acc_x, side, [&](int r, int k) { return B.along(r, k, lane); }, [&](int r, int k) { return X.across(r, k, lane); });
     __syncthreads();        // nobody reads X any more
     const bool last = step + 1 == a.steps;
 #pragma unroll
-    for (int i = 0; i < kMine; ++i) {
-      const int t = wave * mine + i, row = t / ct * 16 + c, col = t % ct * 16 + q * 4;
-      if (i < mine && t < rt * ct) {
+    for (int i = 0; i < MX; ++i) {
+      const int row = of_x.row[i] + c, col = of_x.col[i] + q * 4;
+      if (i < of_x.count) {
         float v[4];
         Small::half4 h;
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
-          x32[i][k] = v[k] = f * __builtin_fmaf(c0, x32[i][k], acc[i][k]);
+          x32[i][k] = v[k] = f * __builtin_fmaf(c0, x32[i][k], acc_x[i][k]);
           h[k] = (_Float16)v[k];
         }
         if (!last) {
@@ -528,11 +551,29 @@ int go(const OrthoArgs& a, int tile, int64_t blocks, void* stream) {
 
 }  // namespace
 
+template <typename T, int MX>
+int go_small(const OrthoSmallArgs& a, int64_t batch, int n_tiles, int lds, void* stream) {
+  if (n_tiles <= 8) return launch(&ortho_small_kernel<T, MX, 1>, a, batch, kSmallThreads, lds, stream);
+  if constexpr (MX >= 2)
+    if (n_tiles <= 16) return launch(&ortho_small_kernel<T, MX, 2>, a, batch, kSmallThreads, lds, stream);
+  if constexpr (MX >= 5)
+    if (n_tiles <= 40) return launch(&ortho_small_kernel<T, MX, 5>, a, batch, kSmallThreads, lds, stream);
+  return launch(&ortho_small_kernel<T, MX, MX>, a, batch, kSmallThreads, lds, stream);
+}
+template <typename T>
+int go_small(const OrthoSmallArgs& a, int64_t batch, int lds, void* stream) {
+  const int side = (a.rp < a.cp ? a.rp : a.cp) / 16, tiles = (a.rp / 16) * (a.cp / 16), n = side * side;
+  if (tiles <= 8) return go_small<T, 1>(a, batch, n, lds, stream);
+  if (tiles <= 16) return go_small<T, 2>(a, batch, n, lds, stream);
+  if (tiles <= 24) return go_small<T, 3>(a, batch, n, lds, stream);
+  if (tiles <= 40) return go_small<T, 5>(a, batch, n, lds, stream);
+  return go_small<T, 8>(a, batch, n, lds, stream);
+}
+
 int launch_ortho_small(const OrthoSmallArgs& a, int64_t batch, void* stream) {
   const int side = a.rp < a.cp ? a.rp : a.cp;
   const int lds = a.rp * (a.cp * 2 + 16) + 2 * side * (side * 2 + 16);
-  return a.src_dt == ZERO_BF16 ? launch(&ortho_small_kernel<__bf16>, a, batch, kSmallThreads, lds, stream)
-                               : launch(&ortho_small_kernel<_Float16>, a, batch, kSmallThreads, lds, stream);
+  return a.src_dt == ZERO_BF16 ? go_small<__bf16>(a, batch, lds, stream) : go_small<_Float16>(a, batch, lds, stream);
 }
 
 int launch_ortho_thin(const OrthoThinArgs& a, int64_t batch, void* stream) {
