@@ -769,8 +769,10 @@ typedef struct zero_newton_schulz {
  * Errors: EINVAL for nulls, a tensor out of range or twice, rows or cols < 1 or
  * not dividing the tensor, a scale beyond fp32, a polynomial outside its
  * limits, misalignment, a short workspace or overlapping buffers; EUNSUPPORTED
- * for fp32, rows or cols above 2^20, or a polynomial whose steps take X, A or
- * b A + c A A beyond 30000, which fp16 would not hold.
+ * for fp32, rows or cols above 2^20, a polynomial whose steps take X, A or
+ * b A + c A A beyond 30000, which fp16 would not hold, or one with |a|^steps
+ * above 10000 (7 steps of the default's a), which would bring the rounding in
+ * directions that a matrix lacks up to the size of the others.
  */
 ZERO_API size_t zero_orthogonalize_workspace_bytes(zero_plan_t plan, const zero_matrix* matrices, int32_t n_matrices);
 ZERO_API zero_status zero_orthogonalize(zero_plan_t plan, const zero_matrix* matrices, int32_t n_matrices,

@@ -317,7 +317,7 @@ int main() {
     g_bytes[kX] = g_bytes[kOut] = psi_pad * 2;
     g_bytes[kWs] = ws;
     zk::hidden::g_matrices = zk::hidden::g_last = 0;
-    const zero_newton_schulz poly = {(int32_t)pick(1, 6), 1.875, -1.25, 0.375, 1e-7};
+    const zero_newton_schulz poly = {(int32_t)pick(1, 14), 1.875, -1.25, 0.375, 1e-7};
     const int st = zero_orthogonalize(plan, ms.data(), (int32_t)ms.size(), pick(0, 1) ? &poly : nullptr, fake(kX), ZERO_BF16, fake(kOut), ZERO_F16, fake(kWs), ws,
                                       nullptr);
     EXPECT(st == ZERO_OK, "zero_orthogonalize: %d, %s", st, zero_last_error());

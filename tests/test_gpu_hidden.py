@@ -498,6 +498,36 @@ def test_orthogonalize_polynomials(T, Z, poly, shape):
     ortho_close(T, dst.view(r, c), ortho64(T, g, 2.0, *poly), BF16, poly)
 
 
+@pytest.mark.parametrize("shape", [(24, 30), (40, 900), (900, 40), (64, 2000), (150, 200)], ids=str)
+@pytest.mark.parametrize("steps", [5, 10, 11, 14, 15, 16, 30])
+def test_orthogonalize_lacking_directions(T, Z, steps, shape):
+    """Equal, opposite and empty rows and columns: directions that the matrix has
+    nothing of, however many the steps."""
+    r, c = shape
+    g = matrix(T, r, c, BF16, 5, "normal")
+    n = min(r, c) // 3
+    g[1:1 + n] = g[0]
+    g[n:n + 4] *= -1
+    g[n + 5:n + 8] = 0
+    g[:, 2:2 + n] = g[:, :1]
+    g[:, n + 2:n + 5] = 0
+    plan = Z.zero_plan(r * c, 1, [r * c], 0, 1)
+    m = Z.Matrices([(0, r, c, 1.0)])
+    poly = (steps, 1.875, -1.25, 0.375, 1e-7)
+    dst = T.empty(plan.psi_pad, dtype=T.bfloat16, device="cuda")
+
+    def run():
+        Z.zero_orthogonalize(plan, m, g.reshape(-1).contiguous(), BF16, dst, BF16, poly=Z.NewtonSchulz(*poly),
+                             workspace=ws_of(T, Z.zero_orthogonalize_workspace_bytes(plan, m)))
+
+    if 1.875 ** steps > 10000:
+        with pytest.raises(Z.ZeroError):
+            run()
+        return
+    run()
+    ortho_close(T, dst.view(r, c), ortho64(T, g, 1.0, *poly), BF16, poly)
+
+
 # ---------------------------------------------------------------------------
 # The two halves of the step
 # ---------------------------------------------------------------------------

@@ -130,7 +130,8 @@ def test_orthogonalize_refuses(Z):
     assert _ortho(Z, plan, good, sdt=0) == Z.ZERO_EUNSUPPORTED
     assert _ortho(Z, plan, good, ddt=0) == Z.ZERO_EUNSUPPORTED
     # Steps that leave fp16's range: A past 30000 in the second step; B in the first; X growing by 8 a step.
-    for poly in [(2, 200.0, 0.0, 0.0, 1e-7), (2, 1.0, 900.0, -800.0, 1e-7), (6, 8.0, 0.0, 0.0, 1e-7), (32, 2.0, 1.0, 0.0, 1.0)]:
+    for poly in [(2, 200.0, 0.0, 0.0, 1e-7), (2, 1.0, 900.0, -800.0, 1e-7), (6, 8.0, 0.0, 0.0, 1e-7), (32, 2.0, 1.0, 0.0, 1.0),
+                 (8, 3.4445, -4.7750, 2.0315, 1e-7), (15, 1.875, -1.25, 0.375, 1e-7)]:        # a^steps above 10000
         assert _ortho(Z, plan, good, poly=poly) == Z.ZERO_EUNSUPPORTED, poly
         assert _ortho(Z, plan, [(3, 4, 4, 1.0)], poly=poly) == Z.ZERO_EUNSUPPORTED, poly
     long = Z.zero_plan(1 << 22, 1, [1 << 22], 0, 1)

@@ -417,15 +417,20 @@ OrthoSpace thin_space(int64_t rows, int64_t cols, int64_t batch) {
 
 bool is_thin(int64_t rows, int64_t cols) { return std::min(rows, cols) <= kThinSide; }
 
-OrthoSpace space_of(int64_t rows, int64_t cols, int64_t batch) {
-  return is_thin(rows, cols) ? thin_space(rows, cols, batch) : ortho_space(rows, cols, batch);
+// Whether P may stand for the steps.  What rounding leaves of A in directions that X
+// lacks (equal rows, say) grows by a^2 in each step, and P by a: 40 x 900 with 15 steps
+// of a = 1.875, which grow by 12400, ends 0.18 off.
+bool may_be_thin(const zero_newton_schulz& q) { return std::pow(std::fabs(q.a), q.steps) <= 1000.0; }
+
+OrthoSpace space_of(bool thin, int64_t rows, int64_t cols, int64_t batch) {
+  return thin ? thin_space(rows, cols, batch) : ortho_space(rows, cols, batch);
 }
 
 // As many matrices as one batch takes: all of them where X, A and B stay within
 // 1 GiB, as launches of many tiles waste the least (48 matrices of 768 x 768 in one
 // batch, two and four: 870, 875 and 1160 us; 24 of 1024 x 4096 in one and two: 2370
 // and 2520), or a few batches more where those fill their rounds better.
-int64_t batch_of(int64_t rows, int64_t cols, int64_t count) {
+int64_t batch_of(bool thin, int64_t rows, int64_t cols, int64_t count) {
   const int64_t n = std::min(rows, cols), bytes = rows * cols * 6 + n * n * 2;
   const int64_t most = std::min<int64_t>(std::max<int64_t>(1, (int64_t(1) << 30) / bytes), kMaxBatch);
   const int64_t fewest = ceil_div(count, most);
@@ -433,7 +438,7 @@ int64_t batch_of(int64_t rows, int64_t cols, int64_t count) {
   double us = 1e300;
   for (int64_t parts = fewest; parts <= std::min(count, fewest + 3); ++parts) {
     const int64_t batch = ceil_div(count, parts);
-    const OrthoSpace s = space_of(rows, cols, batch);
+    const OrthoSpace s = space_of(thin, rows, cols, batch);
     const double now = (double)ceil_div(count, batch) * (s.c[kGram].us + s.c[kPoly].us + s.c[kNext].us);
     if (now < us) us = now, best = batch;
   }
@@ -476,8 +481,12 @@ zero_status collect(zero_plan_t p, const zero_matrix* ms, int32_t n, std::vector
 
 // Whether the matrices between the products stay within fp16: the largest singular
 // values of X, A and b A + c A A over the steps, by points a 256th of the range apart.
+// And whether directions that the matrix lacks stay empty: the products' rounding puts
+// some 10^-7 there, which grows by a in each step.
 zero_status check_growth(const zero_newton_schulz& q) {
-  constexpr double most = 30000.0;
+  constexpr double most = 30000.0, grown = 10000.0;
+  if (std::pow(std::fabs(q.a), q.steps) > grown)
+    return fail(ZERO_EUNSUPPORTED, "%d steps of a = %g bring rounding up by more than %g", q.steps, q.a, grown);
   double hi = 1.0;
   for (int step = 0; step < q.steps; ++step) {
     double next = 0.0, b = hi * hi;
@@ -501,8 +510,11 @@ bool is_small(int64_t rows, int64_t cols) {
 
 int64_t ortho_bytes(const std::vector<Group>& groups) {
   int64_t most = 0;
-  for (const Group& g : groups)
-    if (!g.off.empty() && !is_small(g.rows, g.cols)) most = std::max(most, space_of(g.rows, g.cols, batch_of(g.rows, g.cols, (int64_t)g.off.size())).total);
+  for (const Group& g : groups) {
+    if (g.off.empty() || is_small(g.rows, g.cols)) continue;
+    for (int thin = is_thin(g.rows, g.cols); thin >= 0; --thin)      // either way may be taken, by the polynomial
+      most = std::max(most, space_of(thin, g.rows, g.cols, batch_of(thin, g.rows, g.cols, (int64_t)g.off.size())).total);
+  }
   return most;
 }
 
@@ -969,9 +981,10 @@ zero_status zero_orthogonalize(zero_plan_t p, const zero_matrix* matrices, int32
           if (zero_status st = ortho_small(g, i, std::min<int64_t>(kMaxBatch, count - i), q, src, src_dt, dst, dst_dt, stream)) return st;
         continue;
       }
-      const int64_t batch = batch_of(g.rows, g.cols, count);
-      const OrthoSpace s = space_of(g.rows, g.cols, batch);      // a smaller last batch takes the same shapes
-      const auto run = is_thin(g.rows, g.cols) ? ortho_thin : ortho_batch;
+      const bool thin = is_thin(g.rows, g.cols) && may_be_thin(q);
+      const int64_t batch = batch_of(thin, g.rows, g.cols, count);
+      const OrthoSpace s = space_of(thin, g.rows, g.cols, batch);      // a smaller last batch takes the same shapes
+      const auto run = thin ? ortho_thin : ortho_batch;
       for (int64_t i = 0; i < count; i += batch)
         if (zero_status st = run(g, s, i, std::min(batch, count - i), q, src, src_dt, dst, dst_dt, (char*)workspace, stream))
           return st;
