@@ -754,10 +754,12 @@ typedef struct zero_newton_schulz {
  *   dst = scale * X
  *   (For rows > cols A = X^T X and X A take their places, which is the same X.)
  *   The norm is fp64.  X is held in 32 bits and enters the products in fp16, as
- *   A and b A + c A A do; sums are fp32 (where the shorter side is at most 64
- *   and the matrix large, A and its polynomials are fp32).  The result is within about 0.002 of the
- *   64-bit one (2-norm over the matrix) for the default polynomial.  A matrix
- *   of zeros gives zeros, one that holds NaN or an infinity NaN throughout.
+ *   A and b A + c A A do; sums are fp32.  (Where the shorter side is at most 64
+ *   and the matrix large, A and its polynomials are fp32.)  For the default
+ *   polynomial the result is within about 0.001 of the 64-bit one (2-norm over
+ *   the matrix), small matrices with few strong directions within 0.004.  A
+ *   matrix of zeros gives zeros, one that holds NaN or an infinity NaN
+ *   throughout.
  *   matrices, n_matrices  host array.  No tensor twice.  Matrices of one shape
  *               run together, whatever their order.
  *   src, src_dt the full flat 16-bit buffer.
