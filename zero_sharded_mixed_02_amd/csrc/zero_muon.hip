@@ -60,6 +60,12 @@ __global__ void __launch_bounds__(kLoadThreads) ortho_norm_kernel(const OrthoLoa
   if (threadIdx.x == 0) a.sums[(int64_t)z * a.norm_blocks + piece] = w[0];
 }
 
+// What is left of 1 / (|G| + eps) beside 2^e, at most 1/32.  A matrix of zeros takes 1:
+// 1 / eps or its square may be beyond fp32, and zeros times infinity are no zeros.
+__device__ __forceinline__ float factor_left(bool good, double norm, double den, int e) {
+  return !good ? __builtin_nanf("") : norm > 0.0 ? (float)(1.0 / ldexp(den, e)) : 1.0f;
+}
+
 // X = G * 2^k in fp16 with |X| in [32, 64), padded with zeros to multiples of 8,
 // and the factor that is left of 1 / (|G| + eps).  A workgroup joins the norm's
 // pieces once for kLoadUnits pieces of eight a thread (8192 x 8192: 51 us, 5.2 TB/s).
@@ -92,7 +98,7 @@ __global__ void __launch_bounds__(kLoadThreads) ortho_load_kernel(const OrthoLoa
   const bool good = d < __builtin_inf();                          // not NaN either
   const int e = good && norm > 0.0 ? 5 - ilogb(norm) : 0;        // |G| 2^e in [32, 64)
   if (u0 == 0) {
-    a.factor[2 * z] = good ? (float)(1.0 / ldexp(d, e)) : __builtin_nanf("");
+    a.factor[2 * z] = factor_left(good, norm, d, e);
     a.factor[2 * z + 1] = norm > a.eps ? 1.0f : 0.0f;
   }
 #pragma unroll
@@ -432,7 +438,7 @@ __global__ void __launch_bounds__(kSmallThreads) ortho_small_kernel(const OrthoS
   const double norm = __builtin_sqrt(s), den = norm + a.eps;
   const bool good = den < __builtin_inf();
   const int e = good && norm > 0.0 ? 5 - ilogb(norm) : 0;
-  float f = good ? (float)(1.0 / ldexp(den, e)) : __builtin_nanf("");
+  float f = factor_left(good, norm, den, e);
   const float may_shift = norm > a.eps ? a.shift : 0.0f;
   for (int u = threadIdx.x; u < units; u += kSmallThreads) {
     ZK_LDS char* at = (ZK_LDS char*)X.at(u / upr, u % upr * 8);
