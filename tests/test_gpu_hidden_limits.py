@@ -74,3 +74,35 @@ def test_zeros_any_eps(T, Z, r, c, eps):
     out = orthogonalized(T, Z, g, poly)
     assert bool((out[1] == 0).all())
     assert float(off(T, out[::2], ortho64(T, g[::2], *poly)).max()) <= 0.02 + HALF
+
+
+# ---------------------------------------------------------------------------
+# Products
+# ---------------------------------------------------------------------------
+
+def test_longest_side(T, Z):
+    """2^30 rows of one element, and one row into 2^30 outputs."""
+    n = 1 << 30
+    plan, long = Z.zero_plan(2, 1, [1, 1], 0, 1), Z.zero_plan(n, 1, [n], 0, 1)
+    params = T.tensor([1.5, 0.25], dtype=T.bfloat16, device="cuda")
+    x = randn(T, (n, 1), BF16, 1)
+    y = T.empty_like(x)
+    ws = T.empty(max(Z.zero_linear_workspace_bytes(plan, 0, 1, n), Z.zero_linear_input_grad_workspace_bytes(plan, 0, 1, n),
+                     Z.zero_linear_weight_grad_workspace_bytes(plan, 0, 1, n), Z.zero_linear_workspace_bytes(long, 0, 1, 1)), dtype=T.uint8, device="cuda")
+    Z.zero_linear(plan, 0, 1, params, BF16, x, y, bias=1, workspace=ws)
+    same = lambda got, form: all(T.equal(a, form(b.float()).bfloat16()) for a, b in zip(got.view(-1).split(n // 8), x.view(-1).split(n // 8)))  # noqa: E731
+    assert same(y, lambda v: 1.5 * v + 0.25)
+    Z.zero_linear_input_grad(plan, 0, 1, params, BF16, x, y, workspace=ws)
+    assert same(y, lambda v: 1.5 * v)
+    # Whole numbers at places all over the rows: sums without rounding.
+    at = T.arange(64, device="cuda") * ((n - 1) // 63)
+    x.zero_()
+    y.zero_()
+    x.view(-1)[at] = T.arange(64, device="cuda").bfloat16()
+    y.view(-1)[at] = 2
+    grad = T.empty(2, device="cuda")
+    Z.zero_linear_weight_grad(plan, 0, 1, y, x, BF16, 1.0, grad, Z.ZERO_F32, bias=1, workspace=ws)
+    assert grad.tolist() == [2 * 63 * 64 / 2, 128]
+    x.normal_()
+    Z.zero_linear(long, 0, 1, x.view(-1), BF16, params[:1].view(1, 1), y.view(1, n), workspace=ws)
+    assert same(y, lambda v: 1.5 * v)

@@ -64,22 +64,24 @@ double join_cost(int tile, int64_t tiles, int64_t splits) {
 
 // For `batch` products of m x n x k.  With splits > 0 every tile is cut into so many
 // pieces.  Otherwise all tiles are cut alike, or only those of a last round that
-// would leave most CUs idle.
+// would leave most CUs idle.  Tiles too small for one launch to hold them all are left
+// out (2^30 rows into one column are 2^32 work items of the 64-row tile).
 Pick pick(int64_t m, int64_t n, int64_t k, int64_t batch, int splits, bool upper = false) {
   const int64_t stages = std::max<int64_t>(1, ceil_div(k, kStage));
-  Pick best = {kTile64, 0, 0, 1, 1e300};
+  Pick best = {kTile256, batch * ceil_div(m, kTileSize[kTile256]) * ceil_div(n, kTileSize[kTile256]), 0, 1, 1e300};
   for (int tile = 0; tile < kTiles; ++tile) {
     const int64_t tm = ceil_div(m, kTileSize[tile]), tn = ceil_div(n, kTileSize[tile]);
     const int64_t tiles = batch * (upper ? tm * (tm + 1) / 2 : tm * tn);
     for (int64_t s = splits ? splits : 1; s <= (splits ? splits : 64); s *= 2) {
       if (!splits && s > 1 && stages / s < 4) break;    // a piece has four stages or more
       const int64_t per = ceil_div(stages, s), now = ceil_div(stages, per);
+      if (tiles * now > most_blocks(kTileThreads[tile])) continue;
       double us = cost_of(tile, tiles * now, per);
       if (now > 1) us += join_cost(tile, tiles, now);
       if (us < best.us) best = now > 1 ? Pick{tile, 0, tiles, (int)now, us} : Pick{tile, tiles, 0, 1, us};
     }
     const int64_t slots = (int64_t)kCus * kCost[tile].slots, whole = tiles / slots * slots, rest = tiles - whole;
-    if (splits || whole == 0 || rest == 0) continue;
+    if (splits || whole == 0 || rest == 0 || tiles > most_blocks(kTileThreads[tile]) - slots) continue;
     const int64_t s = std::min(slots / rest, stages / 4);
     if (s < 2) continue;
     const int64_t per = ceil_div(stages, s), now = ceil_div(stages, per);
