@@ -39,6 +39,8 @@ int grid(const char* what, int64_t blocks, int threads) {
   return 0;
 }
 
+std::vector<zk::hidden::CopyRowsArgs> g_copies;      // of the running call, launches that go on from one another joined
+
 }  // namespace
 
 namespace zk {
@@ -57,7 +59,16 @@ int launch_linear(const LinearArgs& a, int, int, int tile, bool, void*) {
 int launch_linear_join(const LinearArgs&, int, int, int64_t blocks, void*) { return grid("join", blocks, kJoinThreads); }
 int launch_weight_grad(const WeightGradArgs&, int, int tile, bool, int64_t blocks, void*) { return grid("weight gradient", blocks, kTileThreads[tile]); }
 int launch_weight_grad_join(const WeightGradArgs&, int64_t blocks, void*) { return grid("weight gradient's join", blocks, kJoinThreads); }
-int launch_copy_rows(const CopyRowsArgs&, int64_t blocks, void*) { return grid("copy", blocks, kCopyThreads); }
+int launch_copy_rows(const CopyRowsArgs& a, int64_t blocks, void*) {
+  EXPECT(blocks * kCopyThreads >= a.rows * a.units, "copy: units");
+  CopyRowsArgs* l = g_copies.empty() ? nullptr : &g_copies.back();
+  if (l && (const char*)a.src == (const char*)l->src + l->rows * l->ld_src * 2 && (char*)a.dst == (char*)l->dst + l->rows * l->ld_dst * 2 &&
+      a.ld_src == l->ld_src && a.ld_dst == l->ld_dst && a.width == l->width)
+    l->rows += a.rows;
+  else
+    g_copies.push_back(a);
+  return grid("copy", blocks, kCopyThreads);
+}
 int launch_act_grad(const ActGradArgs&, int, int64_t blocks, void*) { return grid("activation gradient", blocks, kActThreads); }
 int launch_ortho_small(const OrthoSmallArgs&, int64_t batch, void*) { return grid("small matrices", batch, kSmallThreads); }
 int launch_ortho_norm(const OrthoLoadArgs& a, int, void*) { return grid("norms", (int64_t)a.batch * a.norm_blocks, kLoadThreads); }
@@ -71,6 +82,13 @@ int launch_ortho_join(const OrthoArgs&, int64_t blocks, void*) { return grid("st
 namespace {
 
 constexpr int64_t kMemory = int64_t(288) << 30;
+
+// Whole operands have been copied: two at most, of n or `out` rows.
+void copied(int64_t n, int64_t out) {
+  EXPECT(g_copies.size() <= 2, "%zu copies", g_copies.size());
+  for (const auto& c : g_copies) EXPECT(c.rows == n || c.rows == out, "%lld rows copied of %lld or %lld", (long long)c.rows, (long long)n, (long long)out);
+  g_copies.clear();
+}
 
 // The three products of a layer, where their operands fit a GPU's memory.
 void layer(int64_t n, int64_t in, int64_t out, int nd, int64_t odd, int64_t before) {
@@ -90,18 +108,21 @@ void layer(int64_t n, int64_t in, int64_t out, int nd, int64_t odd, int64_t befo
     const int st = zero_linear(plan, 1, 2, in, fake(0), ZERO_BF16, fake(1), n, xs, ZERO_ACT_GELU, nullptr, 0, nullptr, 0, fake(2), ys, fake(3), ws, nullptr);
     EXPECT(st == ZERO_OK, "linear %lld x %lld -> %lld: %s", (long long)n, (long long)in, (long long)out, zero_last_error());
     ++g_calls;
+    copied(n, out);
   }
   ws = (int64_t)zero_linear_input_grad_workspace_bytes(plan, 1, in, n);
   if (bytes + ws <= kMemory && ys <= 1 << 21) {
     const int st = zero_linear_input_grad(plan, 1, in, fake(0), ZERO_BF16, fake(1), n, ys, ZERO_ACT_NONE, nullptr, 0, nullptr, 0, fake(2), xs, fake(3), ws, nullptr);
     EXPECT(st == ZERO_OK, "input gradient %lld x %lld -> %lld: %s", (long long)n, (long long)in, (long long)out, zero_last_error());
     ++g_calls;
+    copied(n, out);
   }
   ws = (int64_t)zero_linear_weight_grad_workspace_bytes(plan, 1, in, n, nd - 1);
   if (bytes + 2 * (shard - pad) + ws <= kMemory && std::max(xs, ys) <= 1 << 21) {
     const int st = zero_linear_weight_grad(plan, 1, 2, in, fake(0), ys, fake(1), xs, ZERO_F16, n, 1.0, fake(2), ZERO_F16, nd - 1, 0, fake(3), ws, nullptr);
     EXPECT(st == ZERO_OK, "weight gradient %lld x %lld -> %lld: %s", (long long)n, (long long)in, (long long)out, zero_last_error());
     ++g_calls;
+    copied(n, out);
   }
   zero_plan_destroy(plan);
 }
@@ -114,19 +135,22 @@ int main() {
   auto log_pick = [&](double hi) { return std::max<int64_t>(1, (int64_t)exp2(log2(hi) * (double)(rng() % 4097) / 4096.0)); };
   const int64_t most = int64_t(1) << 30, wide = int64_t(1) << 21;
   // The longest sides, alone and with others that fill the memory.
-  for (int64_t one : {1, 2, 34, 62, 64, 128, 2050})
+  for (int64_t one : {1, 2, 33, 63, 64, 128, 2049})
     for (int64_t other : {1, 2, 31, 64, 100}) {
       layer(most, one, other, 1, 0, 0);
       layer(most, other, one, 1, 0, 0);
       layer(one, other, most, 1, 0, 0);
-      layer(most / 64, one, other * 34, 8, 0, 0);
+      layer(most / 64, one, other * 33, 8, 1, 3);
       layer(one, wide, other, 1, 0, 0);
       layer(one, other, wide, 1, 0, 0);
     }
+  // A layer without outputs: its input's gradient is the addend.
+  for (int64_t n : {int64_t(1), int64_t(100), int64_t(1) << 20, int64_t(1) << 24})
+    for (int64_t in : {1, 8, 33, 4097}) layer(n, in, 0, 2, 0, 1);
   for (int it = 0; it < 30000; ++it) {
-    const int64_t n = log_pick((double)most), in = 2 * log_pick((double)wide / 2), out = 2 * log_pick((pick(0, 3) ? (double)wide : (double)most) / 2);
+    const int64_t n = log_pick((double)most), in = log_pick((double)wide), out = log_pick(pick(0, 3) ? (double)wide : (double)most);
     if ((double)n * (double)(in + out) + (double)in * (double)out > 3e11) continue;
-    layer(n, in, out, (int)pick(1, 4), 0, 0);
+    layer(n, in, out, (int)pick(1, 4), pick(0, 2) ? 0 : 1, pick(0, 1));
   }
   printf("%d calls, %d failures\n", g_calls, g_fail);
   return g_fail != 0;

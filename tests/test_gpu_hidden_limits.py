@@ -106,3 +106,14 @@ def test_longest_side(T, Z):
     x.normal_()
     Z.zero_linear(long, 0, 1, x.view(-1), BF16, params[:1].view(1, 1), y.view(1, n), workspace=ws)
     assert same(y, lambda v: 1.5 * v)
+
+
+def test_no_outputs(T, Z):
+    """Back from a layer without outputs: the addend alone, whatever the sizes."""
+    for n, inner in ((5, 3), (1 << 20, 33)):
+        plan = Z.zero_plan(1, 1, [1, 0], 0, 1)
+        params = T.ones(1, dtype=T.bfloat16, device="cuda")
+        add, dx = randn(T, (n, inner), BF16, 1), T.empty((n, inner), dtype=T.bfloat16, device="cuda")
+        ws = T.empty(max(1, Z.zero_linear_input_grad_workspace_bytes(plan, 1, inner, n)), dtype=T.uint8, device="cuda")
+        Z.zero_linear_input_grad(plan, 1, inner, params, BF16, T.empty((n, 0), dtype=T.bfloat16, device="cuda"), dx, addend=add, workspace=ws)
+        assert T.equal(dx, add)

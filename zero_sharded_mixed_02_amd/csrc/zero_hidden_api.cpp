@@ -146,10 +146,14 @@ Copies copies_of(const Pick& c, bool odd_a, int64_t rows_a, int64_t width_a, boo
 }
 
 zero_status copy_rows(const void* src, int64_t rows, int64_t width, int64_t ld_src, void* dst, int64_t ld_dst, void* stream) {
-  CopyRowsArgs a = {src, dst, rows, ld_src, ld_dst, (int32_t)width, (int32_t)(ld_dst / 8)};
-  const int64_t blocks = ceil_div(rows * a.units, kCopyThreads);
-  if (zero_status st = check_grid(blocks, kCopyThreads)) return st;
-  return launched(launch_copy_rows(a, blocks, stream));
+  const int64_t units = ld_dst / 8, part = most_blocks(kCopyThreads) * kCopyThreads / units;      // rows a launch
+  for (int64_t row = 0; row < rows; row += part) {
+    const int64_t now = std::min(part, rows - row);
+    const CopyRowsArgs a = {(const char*)src + row * ld_src * 2, (char*)dst + row * ld_dst * 2, now, ld_src, ld_dst, (int32_t)width,
+                            (int32_t)units};
+    if (const int err = launch_copy_rows(a, ceil_div(now * units, kCopyThreads), stream)) return hip_fail(err);
+  }
+  return ok();
 }
 
 // Puts the operands that are to be copied in their places behind `at` bytes of the
