@@ -766,8 +766,10 @@ typedef struct zero_newton_schulz {
  *   dst, dst_dt the full flat 16-bit buffer of the results; it may be src, with
  *               its type.  Only the listed tensors' ranges are written.
  *   workspace, ws_bytes  zero_orthogonalize_workspace_bytes(...) bytes,
- *               256-byte aligned: about 8 bytes an element of the shape that
- *               needs most, up to 1 GiB or what a single matrix takes.
+ *               256-byte aligned.  The shape that needs most counts: about 8
+ *               bytes an element, with both sides rounded up to 8, 8 KiB a
+ *               matrix and what pieces of a sum take; for all its matrices
+ *               together, or as many as 1 GiB holds, one at the least.
  * Errors: EINVAL for nulls, a tensor out of range or twice, rows or cols < 1 or
  * not dividing the tensor, a scale beyond fp32, a polynomial outside its
  * limits, misalignment, a short workspace or overlapping buffers; EUNSUPPORTED

@@ -127,6 +127,28 @@ void layer(int64_t n, int64_t in, int64_t out, int nd, int64_t odd, int64_t befo
   zero_plan_destroy(plan);
 }
 
+// `count` matrices of a shape: the workspace stays within 1 GiB, or what one of them
+// takes, and the call succeeds.
+void matrices(int64_t rows, int64_t cols, int64_t count) {
+  const int64_t numel[2] = {rows * cols * count, rows * cols};
+  zero_plan_t plan;
+  if (zero_plan(numel[0] + numel[1], 1, numel, 2, 0, 1, &plan)) {
+    EXPECT(false, "plan");
+    return;
+  }
+  const zero_matrix all = {0, rows, cols, 1.0}, one = {1, rows, cols, 1.0};
+  const int64_t ws = (int64_t)zero_orthogonalize_workspace_bytes(plan, &all, 1), single = (int64_t)zero_orthogonalize_workspace_bytes(plan, &one, 1);
+  EXPECT(ws <= std::max(int64_t(1) << 30, single), "%lld of %lld x %lld take %lld bytes, one %lld", (long long)count, (long long)rows, (long long)cols,
+         (long long)ws, (long long)single);
+  const zero_newton_schulz fast = {7, 3.4445, -4.7750, 2.0315, 1e-7};      // beyond what short sides take a way of their own for
+  for (const zero_newton_schulz* q : {(const zero_newton_schulz*)nullptr, &fast}) {
+    const int st = zero_orthogonalize(plan, &all, 1, q, fake(0), ZERO_BF16, fake(1), ZERO_F16, fake(3), ws, nullptr);
+    EXPECT(st == ZERO_OK, "%lld of %lld x %lld: %s", (long long)count, (long long)rows, (long long)cols, zero_last_error());
+    ++g_calls;
+  }
+  zero_plan_destroy(plan);
+}
+
 }  // namespace
 
 int main() {
@@ -151,6 +173,17 @@ int main() {
     const int64_t n = log_pick((double)most), in = log_pick((double)wide), out = log_pick(pick(0, 3) ? (double)wide : (double)most);
     if ((double)n * (double)(in + out) + (double)in * (double)out > 3e11) continue;
     layer(n, in, out, (int)pick(1, 4), pick(0, 2) ? 0 : 1, pick(0, 1));
+  }
+  for (int64_t side : {1, 2, 3, 7, 8, 17, 33, 64, 65, 72, 200})
+    for (int64_t length : {16385, 70000, 1 << 18, 1 << 20})
+      for (int64_t count : {1, 2, 17, 128, 129, 500}) {
+        matrices(side, length, count);
+        matrices(length, side, count);
+      }
+  for (int it = 0; it < 3000; ++it) {
+    const int64_t rows = log_pick(1 << 20), cols = log_pick(1 << 20);
+    if (rows * cols > int64_t(1) << 31) continue;
+    matrices(rows, cols, std::max<int64_t>(1, std::min<int64_t>(log_pick(700), (int64_t(1) << 36) / (rows * cols))));
   }
   printf("%d calls, %d failures\n", g_calls, g_fail);
   return g_fail != 0;

@@ -432,19 +432,25 @@ OrthoSpace space_of(bool thin, int64_t rows, int64_t cols, int64_t batch) {
   return thin ? thin_space(rows, cols, batch) : ortho_space(rows, cols, batch);
 }
 
-// As many matrices as one batch takes: all of them where X, A and B stay within
-// 1 GiB, as launches of many tiles waste the least (48 matrices of 768 x 768 in one
-// batch, two and four: 870, 875 and 1160 us; 24 of 1024 x 4096 in one and two: 2370
+// As many matrices as one batch takes: all of them where the batch's workspace stays
+// within 1 GiB, as launches of many tiles waste the least (48 matrices of 768 x 768 in
+// one batch, two and four: 870, 875 and 1160 us; 24 of 1024 x 4096 in one and two: 2370
 // and 2520), or a few batches more where those fill their rounds better.
 int64_t batch_of(bool thin, int64_t rows, int64_t cols, int64_t count) {
-  const int64_t n = std::min(rows, cols), bytes = rows * cols * 6 + n * n * 2;
-  const int64_t most = std::min<int64_t>(std::max<int64_t>(1, (int64_t(1) << 30) / bytes), kMaxBatch);
+  constexpr int64_t limit = int64_t(1) << 30;
+  int64_t most = std::min<int64_t>(count, kMaxBatch);
+  while (most > 1) {
+    const int64_t total = space_of(thin, rows, cols, most).total;
+    if (total <= limit) break;
+    most = std::max<int64_t>(1, std::min(most - 1, (int64_t)((double)most * (double)limit / (double)total)));
+  }
   const int64_t fewest = ceil_div(count, most);
   int64_t best = 0;
   double us = 1e300;
-  for (int64_t parts = fewest; parts <= std::min(count, fewest + 3); ++parts) {
+  for (int64_t parts = fewest; parts <= count && (parts <= fewest + 3 || best == 0); ++parts) {
     const int64_t batch = ceil_div(count, parts);
     const OrthoSpace s = space_of(thin, rows, cols, batch);
+    if (s.total > limit && batch > 1) continue;       // fewer matrices may be cut into more pieces
     const double now = (double)ceil_div(count, batch) * (s.c[kGram].us + s.c[kPoly].us + s.c[kNext].us);
     if (now < us) us = now, best = batch;
   }
