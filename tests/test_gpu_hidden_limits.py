@@ -3,7 +3,7 @@ its limits, held to its own figures."""
 import pytest
 
 from tests import ops_reference as R
-from tests.ops_reference import BF16, F16
+from tests.ops_reference import BF16, F16, F32
 
 pytestmark = pytest.mark.gpu
 
@@ -74,6 +74,38 @@ def test_zeros_any_eps(T, Z, r, c, eps):
     out = orthogonalized(T, Z, g, poly)
     assert bool((out[1] == 0).all())
     assert float(off(T, out[::2], ortho64(T, g[::2], *poly)).max()) <= 0.02 + HALF
+
+
+def kinds(T, kind, n, r, c, seed):
+    k = min(r, c)
+    g = randn(T, (n, r, c), F32, seed)
+    if kind == "low rank":
+        q = min(8, k)
+        fade = T.arange(1, q + 1, device="cuda") ** 2.0
+        g = 1e-3 * g + T.bmm(randn(T, (n, r, q), F32, seed + 1) / fade, randn(T, (n, q, c), F32, seed + 2))
+    elif kind == "lower rank":
+        q = min(3, k)
+        g = 1e-5 * g + T.bmm(randn(T, (n, r, q), F32, seed + 1), randn(T, (n, q, c), F32, seed + 2))
+    elif kind == "diagonal":
+        d = T.exp(randn(T, (n, k), F32, seed))
+        g = T.zeros_like(g)
+        T.diagonal(g, dim1=1, dim2=2).copy_(d)
+    return g.to(T.bfloat16)
+
+
+SHORT = [(1, 1), (1, 5), (2, 2), (2, 3), (3, 2), (2, 16), (4, 4), (9, 4), (8, 8), (8, 64), (3, 512), (512, 3), (16, 16), (16, 17), (17, 16),
+         (15, 500), (500, 15), (16, 512)]
+
+
+@pytest.mark.parametrize("kind", ["normal", "low rank", "lower rank", "diagonal"])
+@pytest.mark.parametrize("r,c", SHORT)
+def test_short_sides(T, Z, r, c, kind):
+    """Sides of up to 16: within 0.001 for the default polynomial."""
+    g = kinds(T, kind, 300, r, c, 7)
+    got = orthogonalized(T, Z, g)
+    e = off(T, got, ortho64(T, g))
+    assert float(e.max()) <= 0.001 + HALF, (float(e.median()), float(e.max()))
+    assert T.equal(got, orthogonalized(T, Z, g))
 
 
 # ---------------------------------------------------------------------------

@@ -136,6 +136,7 @@ struct OrthoThinArgs {
 // A batch of matrices of one shape that a workgroup each orthogonalises in LDS.
 constexpr int kSmallElems = 16384;
 constexpr int kSmallThreads = 512;
+constexpr int kShortSide = 16;
 struct OrthoSmallArgs {
   const void* src;
   void* dst;
@@ -144,6 +145,7 @@ struct OrthoSmallArgs {
   int32_t shift_from, steps;
   int32_t rows, cols, rp, cp;       // sides, and rounded up to 32
   int32_t src_dt, dst_dt;
+  int32_t is_short, pad_;           // a side of at most kShortSide, and P may stand for the steps
   float scale[kMaxBatch];
   int64_t off[kMaxBatch];
 };

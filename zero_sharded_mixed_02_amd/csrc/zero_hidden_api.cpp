@@ -567,6 +567,7 @@ zero_status ortho_small(const Group& g, int64_t first, int64_t batch, const zero
   a.cp = (int32_t)round_up(g.cols, 32);
   a.src_dt = src_dt;
   a.dst_dt = dst_dt;
+  a.is_short = std::min(g.rows, g.cols) <= kShortSide && may_be_thin(poly);
   for (int64_t i = 0; i < batch; ++i) {
     a.scale[i] = g.scale[first + i];
     a.off[i] = g.off[first + i];

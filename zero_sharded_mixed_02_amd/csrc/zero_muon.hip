@@ -386,6 +386,55 @@ struct Small {
   __device__ __forceinline__ ZK_LDS half4* at(int row, int col) const { return (ZK_LDS half4*)(p + row * pitch + col * 2); }
 };
 
+// The matrix as it is into LDS in rows of X's length, its norm in fp64, then X = G 2^k in
+// fp16.  Returns what is left of 1 / (|G| + eps); may_shift: whether |G| is above eps.
+template <typename T, int NT>
+__device__ __forceinline__ float small_load(const OrthoSmallArgs& a, const Small& X, int rp, int cp, double* sums, bool& may_shift) {
+  const int upr = cp / 8, units = rp * upr, z = blockIdx.x;
+  double s = 0.0;
+  for (int u = threadIdx.x; u < units; u += NT) {
+    const int row = u / upr, col = u % upr * 8, have = row < a.rows ? a.cols - col : 0;
+    Row<T, 8> x;
+    if (have > 0) x.load(a.src, a.off[z] + (int64_t)row * a.cols + col, have);
+    else x.v = {};
+#pragma unroll
+    for (int i = 0; i < 8; ++i) s += (double)(float)x.v[i] * (double)(float)x.v[i];
+    *(ZK_LDS typename Row<T, 8>::tv*)X.at(row, col) = x.v;
+  }
+#pragma unroll
+  for (int k = 32; k > 0; k >>= 1) s += __shfl_xor(s, k);
+  if ((threadIdx.x & 63) == 0) sums[threadIdx.x >> 6] = s;
+  __syncthreads();
+  s = 0.0;
+#pragma unroll
+  for (int k = 0; k < NT / 64; ++k) s += sums[k];
+  const double norm = __builtin_sqrt(s), den = norm + a.eps;
+  const bool good = den < __builtin_inf();
+  const int e = good && norm > 0.0 ? 5 - ilogb(norm) : 0;
+  for (int u = threadIdx.x; u < units; u += NT) {
+    ZK_LDS char* at = (ZK_LDS char*)X.at(u / upr, u % upr * 8);
+    const typename Row<T, 8>::tv x = *(ZK_LDS typename Row<T, 8>::tv*)at;
+    f16x8 h;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) h[i] = good ? (_Float16)ldexpf((float)x[i], e) : (_Float16)0.0f;
+    *(ZK_LDS f16x8*)at = h;
+  }
+  __syncthreads();
+  may_shift = norm > a.eps;
+  return factor_left(good, norm, den, e);
+}
+
+// The result's four values of a row, on their way out.
+__device__ __forceinline__ void small_store(const OrthoSmallArgs& a, int row, int col, float (&v)[4]) {
+  if (row >= a.rows || col >= a.cols) return;
+  const int z = blockIdx.x;
+#pragma unroll
+  for (int k = 0; k < 4; ++k) v[k] *= a.scale[z];
+  const int64_t o = a.off[z] + (int64_t)row * a.cols + col;
+  if (a.dst_dt == ZERO_BF16) store_row<__bf16, 4>(a.dst, o, a.cols - col, v);
+  else store_row<_Float16, 4>(a.dst, o, a.cols - col, v);
+}
+
 // A wave's tiles of 16 x 16, with the divisions done once.  Beyond the last tile it
 // does the first again and keeps nothing, so that no product has a branch.
 template <int N>
@@ -408,47 +457,16 @@ template <typename T, int MX, int MN>      // tiles a wave of X, and of the n x 
 __global__ void __launch_bounds__(kSmallThreads) ortho_small_kernel(const OrthoSmallArgs a) {
   extern __shared__ __attribute__((aligned(1024))) char smem[];
   __shared__ double sums[kSmallThreads / 64];
-  constexpr int kWaves = kSmallThreads / 64;
-  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), z = blockIdx.x;
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const bool tall = a.rows > a.cols;
   const int side = a.rp < a.cp ? a.rp : a.cp, wide = a.rp < a.cp ? a.cp : a.rp;
   const Small X = {(ZK_LDS char*)smem, a.cp * 2 + 16};
   const Small A = {X.p + a.rp * X.pitch, side * 2 + 16};
   const Small B = {A.p + side * A.pitch, A.pitch};
 
-  // The matrix as it is, its norm in fp64, then times a power of two.
-  const int upr = a.cp / 8, units = a.rp * upr;
-  double s = 0.0;
-  for (int u = threadIdx.x; u < units; u += kSmallThreads) {
-    const int row = u / upr, col = u % upr * 8, have = row < a.rows ? a.cols - col : 0;
-    Row<T, 8> x;
-    if (have > 0) x.load(a.src, a.off[z] + (int64_t)row * a.cols + col, have);
-    else x.v = {};
-#pragma unroll
-    for (int i = 0; i < 8; ++i) s += (double)(float)x.v[i] * (double)(float)x.v[i];
-    *(ZK_LDS typename Row<T, 8>::tv*)X.at(row, col) = x.v;
-  }
-#pragma unroll
-  for (int k = 32; k > 0; k >>= 1) s += __shfl_xor(s, k);
-  if (lane == 0) sums[wave] = s;
-  __syncthreads();
-  s = 0.0;
-#pragma unroll
-  for (int k = 0; k < kWaves; ++k) s += sums[k];
-  const double norm = __builtin_sqrt(s), den = norm + a.eps;
-  const bool good = den < __builtin_inf();
-  const int e = good && norm > 0.0 ? 5 - ilogb(norm) : 0;
-  float f = factor_left(good, norm, den, e);
-  const float may_shift = norm > a.eps ? a.shift : 0.0f;
-  for (int u = threadIdx.x; u < units; u += kSmallThreads) {
-    ZK_LDS char* at = (ZK_LDS char*)X.at(u / upr, u % upr * 8);
-    const typename Row<T, 8>::tv x = *(ZK_LDS typename Row<T, 8>::tv*)at;
-    f16x8 h;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) h[i] = good ? (_Float16)ldexpf((float)x[i], e) : (_Float16)0.0f;
-    *(ZK_LDS f16x8*)at = h;
-  }
-  __syncthreads();
+  bool shifts;
+  float f = small_load<T, kSmallThreads>(a, X, a.rp, a.cp, sums, shifts);
+  const float may_shift = shifts ? a.shift : 0.0f;
 
   // The wave's tiles of X and of the n x n results.
   const int q = lane >> 4, c = lane & 15;
@@ -528,19 +546,103 @@ __global__ void __launch_bounds__(kSmallThreads) ortho_small_kernel(const OrthoS
           x32[i][k] = v[k] = f * __builtin_fmaf(c0, x32[i][k], acc_x[i][k]);
           h[k] = (_Float16)v[k];
         }
-        if (!last) {
-          *X.at(row, col) = h;
-        } else if (row < a.rows && col < a.cols) {
-#pragma unroll
-          for (int k = 0; k < 4; ++k) v[k] *= a.scale[z];
-          const int64_t o = a.off[z] + (int64_t)row * a.cols + col;
-          if (a.dst_dt == ZERO_BF16) store_row<__bf16, 4>(a.dst, o, a.cols - col, v);
-          else store_row<_Float16, 4>(a.dst, o, a.cols - col, v);
-        }
+        if (!last) *X.at(row, col) = h;
+        else small_store(a, row, col, v);
       }
     }
     f = 1.0f;
     __syncthreads();
+  }
+}
+
+// Small matrices with a side of up to 16.  Few entries' rounding to fp16 does not average
+// out (2 x 2 with A, B and X in fp16: up to 0.014 off, 0.002 at the median), so these go the way
+// of the large matrices with a short side: P in fp32 from A = X X^T, which is one tile of
+// 16 x 16, and P X with P as two fp16 numbers along k.  Every wave forms P by itself: a
+// product's result lies in a wave's registers as the next one's operands do.
+constexpr int kShortThreads = 256;
+template <typename T>
+__global__ void __launch_bounds__(kShortThreads) ortho_short_kernel(const OrthoSmallArgs a) {
+  extern __shared__ __attribute__((aligned(1024))) char smem[];
+  constexpr int kWaves = kShortThreads / 64, kPitchP = 80;      // bytes: 32 halves, and 16 to lie in other banks
+  __shared__ double sums[kWaves];
+  __shared__ f32x4 part[kWaves][64];
+  __shared__ __attribute__((aligned(16))) char halves[kWaves][16 * kPitchP];
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), c = lane & 15, q = lane >> 4;
+  const bool tall = a.rows > a.cols;
+  const int n = tall ? a.cols : a.rows, rp = tall ? a.rp : 16, cp = tall ? 16 : a.cp, wide = tall ? a.rp : a.cp;
+  const Small X = {(ZK_LDS char*)smem, cp * 2 + 16};
+  bool shifts;
+  const float f = small_load<T, kShortThreads>(a, X, rp, cp, sums, shifts);
+
+  // A: the waves take 32 k in turn, and join their sums in their order.
+  f32x4 acc = {0.f, 0.f, 0.f, 0.f};
+  for (int k = wave * 32; k < wide; k += kWaves * 32) {
+    const s16x8 x = tall ? X.across(0, k, lane) : X.along(0, k, lane);
+    acc = mfma<_Float16>(x, x, acc);
+  }
+  part[wave][lane] = acc;
+  __syncthreads();
+  // A lane has row c, columns 4 q to 4 q + 3, which as an operand are four k.
+  f32x4 A, P, one;
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    double s = 0.0;
+#pragma unroll
+    for (int w = 0; w < kWaves; ++w) s += (double)part[w][lane][k];
+    A[k] = (float)(s * (double)f * (double)f);
+    one[k] = q * 4 + k == c && c < n ? 1.0f : 0.0f;
+  }
+  P = one;
+  const auto product = [](const f32x4& l, const f32x4& r) {      // l r for symmetric r
+    f32x4 d = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int k = 0; k < 4; ++k) d = __builtin_amdgcn_mfma_f32_16x16x4f32(r[k], l[k], d, 0, 0, 0);
+    return d;
+  };
+#pragma unroll 1
+  for (int step = 0; step < a.steps; ++step) {
+    const f32x4 s = product(A, A);
+    f32x4 Q;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) Q[k] = __builtin_fmaf(a.c, s[k], __builtin_fmaf(a.b, A[k], a.a * one[k]));
+    P = product(Q, P);
+    A = product(product(Q, A), Q);
+  }
+
+  // P times a power of two that brings its largest entry to 2^12, as two halves.
+  float m = 0.0f;
+#pragma unroll
+  for (int k = 0; k < 4; ++k) m = __builtin_fabsf(P[k]) > m ? __builtin_fabsf(P[k]) : m;
+#pragma unroll
+  for (int k = 32; k > 0; k >>= 1) {
+    const float x = __shfl_xor(m, k);
+    m = x > m ? x : m;
+  }
+  const int e = m > 0.0f && m < __builtin_inff() ? ilogbf(m) - 12 : 0;
+  const Small H = {(ZK_LDS char*)(char*)halves[wave], kPitchP};
+  Small::half4 hi, lo;
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    const float x = ldexpf(P[k], -e);
+    hi[k] = (_Float16)x;
+    lo[k] = (_Float16)(x - (float)hi[k]);
+  }
+  *H.at(c, q * 4) = hi;
+  *H.at(c, 16 + q * 4) = lo;
+  __syncthreads();
+  const s16x8 p = H.along(0, 0, lane);
+  const float scale = ldexpf(f, e);
+  for (int t = wave; t < wide / 16; t += kWaves) {
+    // X's 16 rows or columns again for the second half of k.
+    const int k0 = (q & 1) * 8 - q * 8;
+    acc = f32x4{0.f, 0.f, 0.f, 0.f};
+    if (tall) acc = mfma<_Float16>(p, X.along(t * 16, k0, lane), acc);
+    else acc = mfma<_Float16>(X.across(t * 16, k0, lane), p, acc);
+    float v[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) v[k] = scale * acc[k];
+    small_store(a, (tall ? t * 16 : 0) + c, (tall ? 0 : t * 16) + q * 4, v);
   }
 }
 
@@ -577,6 +679,11 @@ int go_small(const OrthoSmallArgs& a, int64_t batch, int lds, void* stream) {
 }
 
 int launch_ortho_small(const OrthoSmallArgs& a, int64_t batch, void* stream) {
+  if (a.is_short) {
+    const int lds = a.rows > a.cols ? a.rp * (16 * 2 + 16) : 16 * (a.cp * 2 + 16);
+    return a.src_dt == ZERO_BF16 ? launch(&ortho_short_kernel<__bf16>, a, batch, kShortThreads, lds, stream)
+                                 : launch(&ortho_short_kernel<_Float16>, a, batch, kShortThreads, lds, stream);
+  }
   const int side = a.rp < a.cp ? a.rp : a.cp;
   const int lds = a.rp * (a.cp * 2 + 16) + 2 * side * (side * 2 + 16);
   return a.src_dt == ZERO_BF16 ? go_small<__bf16>(a, batch, lds, stream) : go_small<_Float16>(a, batch, lds, stream);
