@@ -1,6 +1,7 @@
 """The operators on the hidden matrices at the ends of what the header allows,
 without a GPU."""
 import os
+import re
 import shutil
 import subprocess
 
@@ -24,3 +25,17 @@ def test_limits(tmp_path):
     r = subprocess.run([str(exe)], capture_output=True, text=True, env=env, timeout=300)
     assert r.returncode == 0, r.stdout + r.stderr
     assert " 0 failures" in r.stdout
+
+
+@pytest.mark.skipif(not os.path.exists("/opt/rocm/bin/hipcc"), reason="hipcc not available")
+def test_small_matrices_registers():
+    """The kernels of an orthogonalisation keep their values in registers: what the
+    compiler reports of scratch stays below 64 bytes a lane (704 once made 128
+    matrices of 128 x 128 take 100 us in place of 61)."""
+    from zero_sharded_mixed_02_amd import _build
+    cmd = [_build.HIPCC, *_build.FLAGS, "--cuda-device-only", "-c", os.path.join(_build.CSRC, "zero_muon.hip"), "-o", os.devnull,
+           "-Rpass-analysis=kernel-resource-usage"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    assert r.returncode == 0, r.stderr[-2000:]
+    sizes = [int(x) for x in re.findall(r"ScratchSize \[bytes/lane\]: (\d+)", r.stderr)]
+    assert len(sizes) > 30 and max(sizes) < 64, sizes
