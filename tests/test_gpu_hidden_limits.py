@@ -108,6 +108,26 @@ def test_short_sides(T, Z, r, c, kind):
     assert T.equal(got, orthogonalized(T, Z, g))
 
 
+@pytest.mark.parametrize("kind", ["normal", "low rank", "lower rank", "diagonal"])
+@pytest.mark.parametrize("r,c", [(17, 17), (65, 33), (20, 500), (64, 64), (128, 128), (96, 160), (200, 260), (17, 5000), (64, 300)])
+def test_longer_sides(T, Z, r, c, kind):
+    """Longer ones: within 0.004 where many entries count, 0.02 where few do."""
+    g = kinds(T, kind, 60, r, c, 9)
+    e = off(T, orthogonalized(T, Z, g), ortho64(T, g))
+    assert float(e.max()) <= (0.02 if kind == "diagonal" else 0.004) + HALF, (float(e.median()), float(e.max()))
+
+
+@pytest.mark.parametrize("kind", ["normal", "low rank", "lower rank"])
+@pytest.mark.parametrize("r,c", [(9, 12), (24, 30), (150, 200), (256, 256), (40, 900), (900, 40)])
+@pytest.mark.parametrize("poly", [(7, 3.4445, -4.7750, 2.0315, 1e-7), (8, 1.875, -1.25, 0.375, 1e-7), (10, 1.875, -1.25, 0.375, 1e-7),
+                                  (12, 1.875, -1.25, 0.375, 1e-7), (14, 1.875, -1.25, 0.375, 1e-7), (22, 1.5, -0.5, 0.0, 1e-7)], ids=str)
+def test_other_polynomials(T, Z, poly, r, c, kind):
+    """Weak directions that the steps bring up: within 0.005 up to |a|^steps of 500, 0.02 up to 10000."""
+    g = kinds(T, kind, 10, r, c, 11)
+    e = off(T, orthogonalized(T, Z, g, poly), ortho64(T, g, *poly))
+    assert float(e.max()) <= (0.005 if poly[1] ** poly[0] <= 500 else 0.02) + HALF, (float(e.median()), float(e.max()))
+
+
 # ---------------------------------------------------------------------------
 # Products
 # ---------------------------------------------------------------------------

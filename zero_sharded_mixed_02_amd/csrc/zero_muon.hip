@@ -7,16 +7,17 @@
 // computed and the others mirrored.  A tall matrix takes A = X^T X and X A, so
 // that nothing is transposed in memory.
 //
-// Numbers between the products.  X is held in 32 bits for the term a X, and its
+// Numbers between the products.  X is held in two numbers of 16 bits for the term a X, and its
 // fp16 rounding is the products' operand: directions that the gradient hardly holds
 // are scaled up by a in each step, and X rounded to 16 bits would carry its rounding
 // up with them (a matrix of exponentially falling singular values ends 1.3% off its
-// 64-bit result; with X in 32 bits 0.04%).  The 32 bits are the
+// 64-bit result; with two numbers 0.04%).  They are the
 // fp16 rounding and what it left as bf16: 20 significant bits and more, 8 where
 // fp16 has nothing left (X below 2^-25), for two bytes less to write than an fp32
 // beside the operand.  A and B = b A + c A A are held in fp16:
 // their entries are of order one and below, where fp16 has three bits more than
-// bf16 (1.0% of error against 0.14%).  From the fourth step on A's eigenvalues
+// bf16 (1.0% of error against 0.14%).  Rounding X, A and B for the products is what the result is
+// off by: 0.0015 as a rule, up to 0.02 where few entries count and it does not average out.  From the fourth step on A's eigenvalues
 // lie around 1, and A - I/2 is stored in place of A, which halves its largest
 // entries and their rounding; the polynomial is rewritten for it:
 //   b A + c A^2 = (b d + c d^2) I + (b + 2 c d) D + c D^2,  D = A - d I,
