@@ -599,7 +599,10 @@ ZERO_API zero_status zero_token_logp_grad(const void* logits, zero_dtype dt, int
 
 /* gelu: z Phi(z); gelu_tanh: z sigmoid(2 sqrt(2/pi) (z + 0.044715 z^3)); silu:
  * z sigmoid(z).  gelu and silu are 0 at -inf, their limit; the slope of relu
- * at 0 is 0.  Evaluated in fp32, to a few 10^-6 of the value. */
+ * at 0 is 0.  Evaluated in fp32, to 5 10^-6 of the value from z = -4 on; further
+ * down, where the argument of the exponential is large, to 10^-5 (silu),
+ * 1.5 10^-5 (gelu) and 3.5 10^-5 (gelu_tanh); values below 2^-119 may be 0.  The
+ * slopes likewise, to 10^-6 where their terms cancel. */
 typedef enum zero_act {
   ZERO_ACT_NONE = 0,
   ZERO_ACT_RELU = 1,

@@ -1,11 +1,14 @@
 """The operators on the hidden matrices on the GPU: what the header promises at
 its limits, held to its own figures."""
+import math
+
 import pytest
 
 from tests import ops_reference as R
 from tests.ops_reference import BF16, F16, F32
 
 pytestmark = pytest.mark.gpu
+GELU, GELU_TANH, SILU = 2, 3, 4
 
 
 @pytest.fixture(scope="module")
@@ -169,3 +172,69 @@ def test_no_outputs(T, Z):
         ws = T.empty(max(1, Z.zero_linear_input_grad_workspace_bytes(plan, 1, inner, n)), dtype=T.uint8, device="cuda")
         Z.zero_linear_input_grad(plan, 1, inner, params, BF16, T.empty((n, 0), dtype=T.bfloat16, device="cuda"), dx, addend=add, workspace=ws)
         assert T.equal(dx, add)
+
+
+# ---------------------------------------------------------------------------
+# Activations
+# ---------------------------------------------------------------------------
+
+def act64(T, kind, z):
+    if kind == GELU:
+        return z * 0.5 * T.special.erfc(-z * math.sqrt(0.5))
+    if kind == GELU_TANH:
+        return z * T.sigmoid(2 * math.sqrt(2 / math.pi) * (z + 0.044715 * z ** 3))
+    return z * T.sigmoid(z)
+
+
+def slope64(T, kind, z):
+    z = z.detach().clone().requires_grad_(True)
+    return T.autograd.grad(act64(T, kind, z).sum(), z)[0]
+
+
+# exp2's argument t is rounded relative to itself, which exp2 makes an error of ln 2 |t| times
+# that; |t| is at most 126 where the value is not below the smallest normal number.  Roundings of
+# 2^-24 = 6e-8 and constants off by up to 3e-8, in all: silu 1 and one constant (7.3e-8), gelu 2 and
+# one (1.32e-7) beside erfcx's 1.2e-6, gelu_tanh 5 and two (3.5e-7); a few roundings of the rest.
+FAR = {GELU: 1.5e-5, GELU_TANH: 3.5e-5, SILU: 1e-5}
+NEAR = 5e-6           # from z = -4 on, where |t| is below 16 (gelu_tanh: 16 ln 2 3.5e-7 = 3.9e-6)
+
+
+@pytest.mark.parametrize("act", [GELU, GELU_TANH, SILU])
+def test_activation_accuracy(T, Z, act):
+    """An activation of sums that are no 16-bit numbers, seen to more bits than bf16
+    has: the first result comes back as the residual of a second call, which leaves
+    what it had rounded off."""
+    plan = Z.zero_plan(3, 1, [3], 0, 1)
+    w = T.tensor([1.0, 2.0 ** -8, 2.0 ** -15], dtype=T.bfloat16, device="cuda")
+    g = T.Generator(device="cuda").manual_seed(4)
+    x = T.randint(-127, 128, (1 << 21, 3), device="cuda", generator=g).bfloat16()      # sums of 22 bits: exact in fp32
+    x[:, 0].uniform_(-100 if act == SILU else -14, 14, generator=g)
+    x[:, 0].mul_(128).round_().div_(128)
+    y, r = (T.empty((x.shape[0], 1), dtype=T.bfloat16, device="cuda") for _ in range(2))
+    ws = T.empty(Z.zero_linear_workspace_bytes(plan, 0, 3, x.shape[0]), dtype=T.uint8, device="cuda")
+    Z.zero_linear(plan, 0, 3, w, BF16, x, y, act=act, workspace=ws)
+    Z.zero_linear(plan, 0, 3, w, BF16, x, r, act=act, residual=-y, workspace=ws)
+    z = x.double() @ w.double()
+    assert bool((z == z.float().double()).all())
+    want = act64(T, act, z)
+    err = (y[:, 0].double() + r[:, 0].double() - want).abs()
+    room = 2.0 ** -8 * r[:, 0].double().abs() + 2.0 ** -119      # r's own rounding, half a step of bf16
+    bound = T.where(z > -4, NEAR, FAR[act])
+    assert bool((err <= room + bound * want.abs()).all()), float(((err - room) / want.abs()).max())
+
+
+@pytest.mark.parametrize("act", [GELU, GELU_TANH, SILU])
+def test_slope_accuracy(T, Z, act):
+    """The same of the slopes, at every bf16 number, through the gradient's addend."""
+    bits = T.arange(-32768, 32768, dtype=T.int32, device="cuda").to(T.int16).view(T.bfloat16)
+    z = bits[bits.double().abs() < 128].view(-1, 1)
+    plan = Z.zero_plan(1, 1, [1], 0, 1)
+    one = T.ones(1, dtype=T.bfloat16, device="cuda")
+    dz = T.ones_like(z)
+    y, r = T.empty_like(z), T.empty_like(z)
+    Z.zero_linear_input_grad(plan, 0, 1, one, BF16, dz, y, act=act, pre=z)
+    Z.zero_linear_input_grad(plan, 0, 1, one, BF16, dz, r, act=act, pre=z, addend=-y)
+    want = slope64(T, act, z.double())
+    err = (y.double() + r.double() - want).abs()
+    room = 2.0 ** -8 * r.double().abs() + 2.0 ** -119 + T.where(z.abs() <= 3, 1e-6, 0.0)
+    assert bool((err <= room + FAR[act] * want.abs()).all()), float(((err - room) / want.abs()).max())
