@@ -238,3 +238,70 @@ def test_slope_accuracy(T, Z, act):
     err = (y.double() + r.double() - want).abs()
     room = 2.0 ** -8 * r.double().abs() + 2.0 ** -119 + T.where(z.abs() <= 3, 1e-6, 0.0)
     assert bool((err <= room + FAR[act] * want.abs()).all()), float(((err - room) / want.abs()).max())
+
+
+# ---------------------------------------------------------------------------
+# Gradients against differences
+# ---------------------------------------------------------------------------
+
+@pytest.mark.parametrize("act", [GELU, GELU_TANH, SILU])
+def test_gradients_against_differences(T, Z, act):
+    """Every entry of dx, dW and db against central differences of the layer itself,
+    in fp16, to a bound that half a gradient, or one and a half, could not meet."""
+    n, inner, outer = 9, 24, 17
+    sizes = [inner * outer, outer]
+    plan = Z.zero_plan(sum(sizes), 1, sizes, 0, 1)
+    # Multiples of 2^-6 and steps of 2^-3: exact in fp16, before and behind a step.
+    grid = lambda shape, seed, top: (randn(T, shape, F32, seed) * 32).round().clamp(-64 * top, 64 * top).div(64).half()   # noqa: E731
+    params, x, weight = grid((plan.psi_pad,), 1, 0.5), grid((n, inner), 2, 1), grid((n, outer), 3, 2) * 4
+    y, pre = (T.empty((n, outer), dtype=T.float16, device="cuda") for _ in range(2))
+
+    def layer(p, v):
+        Z.zero_linear(plan, 0, inner, p, F16, v, y, bias=1, act=act, pre=pre)
+        return y.double()
+
+    y0 = layer(params, x).clone()
+    farthest = float(pre.double().abs().max())
+    dz, dx = T.empty_like(y), T.empty_like(x)
+    Z.zero_activation_grad(weight, pre, dz, F16, act)
+    Z.zero_linear_input_grad(plan, 0, inner, params, F16, dz, dx)
+    grad = T.zeros(plan.psi_pad, device="cuda")
+    ws = T.empty(Z.zero_linear_weight_grad_workspace_bytes(plan, 0, inner, n), dtype=T.uint8, device="cuda")
+    Z.zero_linear_weight_grad(plan, 0, inner, dz, x, F16, 1.0, grad, F32, bias=1, workspace=ws)
+    step = 2.0 ** -3
+    c = weight.double()
+    t = T.linspace(-20, 20, 40001, dtype=T.float64, device="cuda")
+    z = t.clone().requires_grad_(True)
+    d = act64(T, act, z)
+    for _ in range(3):
+        d = T.autograd.grad(d.sum(), z, create_graph=True)[0]
+    third = float(d.abs().max())
+    for buf, got in ((x, dx), (params, grad)):
+        want, bound = [], []
+        for i in range(buf.numel()):
+            ends = []
+            for sign in (1, -1):
+                moved = buf.clone()
+                moved.view(-1)[i] += sign * step
+                ends.append((layer(params, moved) if buf is x else layer(moved, x)).clone())
+            want.append(float(((ends[0] - ends[1]) * c).sum()) / (2 * step))
+            # The outputs that the entry reaches, and how fast they move with it.
+            if buf is x:
+                rate = T.zeros(n, outer, dtype=T.float64, device="cuda")
+                rate[i // inner] = params[:sizes[0]].view(outer, inner)[:, i % inner].double().abs()
+            else:
+                o = i // inner if i < sizes[0] else i - sizes[0]
+                rate = T.zeros(n, outer, dtype=T.float64, device="cuda")
+                rate[:, o] = x[:, i % inner].double().abs() if i < sizes[0] else 1.0
+            # y rounded to 2^-11 of itself at both ends, which may lie 1.2 step rate farther out; a third
+            # derivative; dz rounded to 2^-11 of at most 1.2 |c| from a z that is rounded to 2^-11 of itself
+            # (a slope changes by at most 0.8 of that); fp32's and dx's own rounding.
+            size = y0.abs() + 1.2 * step * rate
+            e = (c.abs() * (2.0 ** -11 * size / step + step ** 2 / 6 * third * rate ** 3)) * (rate > 0)
+            e = e + c.abs() * rate * (2.0 ** -11 * 1.2 + 2.0 ** -11 * farthest * 0.8)
+            bound.append(float(e.sum()) + 2.0 ** -11 * abs(float(got.view(-1)[i])) + 1e-6)
+        want, bound, got = T.tensor(want), T.tensor(bound), got.view(-1).double().cpu()
+        assert bool(((want - got).abs() <= bound).all())
+        assert float(bound.norm()) <= 0.25 * float(got.norm())
+        for factor in (0.0, 0.5, 1.5, 2.0):
+            assert not bool(((want - factor * got).abs() <= bound).all())
