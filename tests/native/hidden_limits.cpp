@@ -45,7 +45,11 @@ std::vector<zk::hidden::CopyRowsArgs> g_copies;      // of the running call, lau
 
 namespace zk {
 const char* hip_error_string(int) { return "stub"; }
-int launch_step(const StepArgs&, int, int, int, int, bool, int, void*) { return 0; }
+int64_t g_elems;      // of the running call's launches
+int launch_step(const StepArgs& a, int, int, int, int, bool vec, int blocks, void*) {
+  for (int i = 0; i < a.n_seg; ++i) g_elems += a.seg[i].len;
+  return grid("step over the shard", blocks, vec ? kStepThreads : kThreads);
+}
 int launch_copy(const CopyArgs&, int, int, void*) { return 0; }
 int launch_warm(const WarmArgs&, int, void*) { return 0; }
 int resident_blocks(int, int, int, int, bool) { return 0; }
@@ -149,6 +153,27 @@ void matrices(int64_t rows, int64_t cols, int64_t count) {
   zero_plan_destroy(plan);
 }
 
+// The two halves of the step on buffers `off` bytes off their alignment.
+void step(int64_t n, int off) {
+  zero_plan_t plan;
+  if (zero_plan(n, 1, &n, 1, 0, 1, &plan)) {
+    EXPECT(false, "plan");
+    return;
+  }
+  const zero_muon_hyper hp = {0.02, 0.95, 0.1, 1.0, 1};
+  auto at = [&](int id, int es) { return (char*)fake(id) + off / 4 * es; };
+  const void* slices[1] = {at(0, 2)};
+  const zero_grad_src src = {ZERO_BF16, 1, slices, nullptr};
+  zk::g_elems = 0;
+  int st = zero_muon_momentum(plan, 0, &hp, &src, nullptr, (float*)at(1, 4), at(2, 2), ZERO_BF16, 1, nullptr);
+  EXPECT(st == ZERO_OK && zk::g_elems == n, "momentum of %lld: %s, %lld elements", (long long)n, zero_last_error(), (long long)zk::g_elems);
+  zk::g_elems = 0;
+  st = zero_muon_apply(plan, 0, &hp, at(0, 2), ZERO_BF16, 1, (float*)at(1, 4), at(2, 2), ZERO_F16, 1, nullptr);
+  EXPECT(st == ZERO_OK && zk::g_elems == n, "apply of %lld: %s, %lld elements", (long long)n, zero_last_error(), (long long)zk::g_elems);
+  g_calls += 2;
+  zero_plan_destroy(plan);
+}
+
 }  // namespace
 
 int main() {
@@ -185,6 +210,8 @@ int main() {
     if (rows * cols > int64_t(1) << 31) continue;
     matrices(rows, cols, std::max<int64_t>(1, std::min<int64_t>(log_pick(700), (int64_t(1) << 36) / (rows * cols))));
   }
+  for (int off : {0, 4})
+    for (int64_t n : {int64_t(1), int64_t(1001), int64_t(1) << 28, (int64_t(1) << 32) - 3, int64_t(1) << 32, (int64_t(1) << 34) + 5}) step(n, off);
   printf("%d calls, %d failures\n", g_calls, g_fail);
   return g_fail != 0;
 }

@@ -195,10 +195,11 @@ void pick_window(int mode, int gdt, int pdt, int ndc, int n_ranks, int64_t elems
   auto_window(mode, gdt, pdt, ndc, n_ranks, elems, blocks, a);
 }
 
-// Launch the step kernel over all pieces, in chunks of kMaxSeg.
+// Launch the step kernel over all pieces, in chunks of kMaxSeg that one launch can hold.
 zero_status run_step(zk::StepArgs& a, const std::vector<Piece>& ps, int mode, int gdt, int pdt,
                      bool vec, void* stream) {
-  const int per_block = vec ? zk::kStepThreads * zk::kStepVec : zk::kThreads;
+  const int threads = vec ? zk::kStepThreads : zk::kThreads, per_block = vec ? threads * zk::kStepVec : threads;
+  const int64_t most = ((int64_t(1) << 32) - 1) / threads;      // workgroups: a launch takes fewer than 2^32 work items
   size_t i = 0;
   while (i < ps.size()) {
     int nseg = 0;
@@ -207,7 +208,7 @@ zero_status run_step(zk::StepArgs& a, const std::vector<Piece>& ps, int mode, in
     for (; i < ps.size() && nseg < zk::kMaxSeg; ++i) {
       const Piece& q = ps[i];
       const int64_t nb = (q.len + per_block - 1) / per_block;
-      if (blocks + nb > INT32_MAX) break;
+      if (blocks + nb > most) break;      // a piece alone stays far below it
       zk::StepSeg& s = a.seg[nseg++];
       s.shard_off = q.shard_off;
       s.full_off = q.full_off;
