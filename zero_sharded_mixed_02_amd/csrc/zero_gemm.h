@@ -273,8 +273,6 @@ struct Core {
 #pragma unroll
       for (int j = 0; j < TN; ++j) acc[i][j] = mfma<T>(f.b[j], f.a[i], acc[i][j]);
   }
-  static constexpr int kReads = TM * (AF == kFormK ? 1 : 2) + TN * (BF == kFormK ? 1 : 2);
-  static constexpr int kProducts = TM * TN;
 
   static constexpr int kL = PA::kLoads + PB::kLoads, kF = TM + TN;
 

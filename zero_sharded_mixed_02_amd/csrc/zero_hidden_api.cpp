@@ -195,7 +195,7 @@ zero_status weight_of(zero_plan_t p, int32_t tensor, int64_t in_features, int64_
   return ok();
 }
 
-zero_status bias_of(zero_plan_t p, int32_t bias, int32_t weight, int64_t out_features) {
+zero_status bias_of(zero_plan_t p, int32_t bias, int64_t out_features) {
   if (bias < 0) return ok();
   if (bias >= (int32_t)p->t_numel.size()) return fail(ZERO_EINVAL, "bias tensor %d out of range", bias);
   if (p->t_numel[bias] != out_features)
@@ -740,7 +740,7 @@ zero_status zero_linear(zero_plan_t p, int32_t weight, int32_t bias, int64_t in_
   return guarded("zero_linear", [&]() -> zero_status {
     int64_t out = 0;
     if (zero_status st = weight_of(p, weight, in_features, out)) return st;
-    if (zero_status st = bias_of(p, bias, weight, out)) return st;
+    if (zero_status st = bias_of(p, bias, out)) return st;
     if (zero_status st = check_16(dt, "the products")) return st;
     if (zero_status st = check_act(act)) return st;
     if (zero_status st = check_n(n)) return st;
@@ -855,7 +855,7 @@ zero_status zero_linear_weight_grad(zero_plan_t p, int32_t weight, int32_t bias,
   return guarded("zero_linear_weight_grad", [&]() -> zero_status {
     int64_t out = 0;
     if (zero_status st = weight_of(p, weight, in_features, out)) return st;
-    if (zero_status st = bias_of(p, bias, weight, out)) return st;
+    if (zero_status st = bias_of(p, bias, out)) return st;
     if (bias == weight) return fail(ZERO_EINVAL, "weight and bias are the same tensor");
     if (out > kMaxWide) return fail(ZERO_EUNSUPPORTED, "%lld output features exceed %lld", (long long)out, (long long)kMaxWide);
     if (zero_status st = check_16(dt, "the products")) return st;

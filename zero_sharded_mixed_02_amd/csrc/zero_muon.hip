@@ -676,14 +676,20 @@ int go(const OrthoArgs& a, int tile, int64_t blocks, void* stream) {
 
 // A wave goes through as many tiles as its kernel was made for, so a rung takes about its
 // own time whatever the tiles are; the rungs are at most 1.7 times apart from three on.
+// Sides are 2, 4, 6 or 8 tiles where they are the shorter, so the n x n results 4, 16, 36
+// or 64.
 template <typename T, int MX>
 int go_small(const OrthoSmallArgs& a, int64_t batch, int n_tiles, int lds, void* stream) {
-  if (n_tiles <= 8) return launch(&ortho_small_kernel<T, MX, 1>, a, batch, kSmallThreads, lds, stream);
-  if constexpr (MX >= 2)
-    if (n_tiles <= 16) return launch(&ortho_small_kernel<T, MX, 2>, a, batch, kSmallThreads, lds, stream);
-  if constexpr (MX >= 5)
-    if (n_tiles <= 40) return launch(&ortho_small_kernel<T, MX, 5>, a, batch, kSmallThreads, lds, stream);
-  return launch(&ortho_small_kernel<T, MX, MX>, a, batch, kSmallThreads, lds, stream);
+  if constexpr (MX > 1) {
+    if (n_tiles > 8) {
+      if constexpr (MX > 5)
+        if (n_tiles > 40) return launch(&ortho_small_kernel<T, MX, 8>, a, batch, kSmallThreads, lds, stream);
+      if constexpr (MX > 3)
+        if (n_tiles > 16) return launch(&ortho_small_kernel<T, MX, 5>, a, batch, kSmallThreads, lds, stream);
+      return launch(&ortho_small_kernel<T, MX, 2>, a, batch, kSmallThreads, lds, stream);
+    }
+  }
+  return launch(&ortho_small_kernel<T, MX, 1>, a, batch, kSmallThreads, lds, stream);
 }
 template <typename T>
 int go_small(const OrthoSmallArgs& a, int64_t batch, int lds, void* stream) {
