@@ -780,7 +780,8 @@ typedef struct zero_newton_schulz {
  *               256-byte aligned.  The shape that needs most counts: about 8
  *               bytes an element, with both sides rounded up to 8, 8 KiB a
  *               matrix and what pieces of a sum take; for all its matrices
- *               together, or as many as 1 GiB holds, one at the least.
+ *               together, or as many as 1 GiB holds, 1.125 GiB with the pieces,
+ *               and one at the least.
  * Errors: EINVAL for nulls, a tensor out of range or twice, rows or cols < 1 or
  * not dividing the tensor, a scale beyond fp32, a polynomial outside its
  * limits, misalignment, a short workspace or overlapping buffers; EUNSUPPORTED

@@ -131,7 +131,7 @@ void layer(int64_t n, int64_t in, int64_t out, int nd, int64_t odd, int64_t befo
   zero_plan_destroy(plan);
 }
 
-// `count` matrices of a shape: the workspace stays within 1 GiB, or what one of them
+// `count` matrices of a shape: the workspace stays within 1.125 GiB, or what one of them
 // takes, and the call succeeds.
 void matrices(int64_t rows, int64_t cols, int64_t count) {
   const int64_t numel[2] = {rows * cols * count, rows * cols};
@@ -142,7 +142,7 @@ void matrices(int64_t rows, int64_t cols, int64_t count) {
   }
   const zero_matrix all = {0, rows, cols, 1.0}, one = {1, rows, cols, 1.0};
   const int64_t ws = (int64_t)zero_orthogonalize_workspace_bytes(plan, &all, 1), single = (int64_t)zero_orthogonalize_workspace_bytes(plan, &one, 1);
-  EXPECT(ws <= std::max(int64_t(1) << 30, single), "%lld of %lld x %lld take %lld bytes, one %lld", (long long)count, (long long)rows, (long long)cols,
+  EXPECT(ws <= std::max(int64_t(9) << 27, single), "%lld of %lld x %lld take %lld bytes, one %lld", (long long)count, (long long)rows, (long long)cols,
          (long long)ws, (long long)single);
   const zero_newton_schulz fast = {7, 3.4445, -4.7750, 2.0315, 1e-7};      // beyond what short sides take a way of their own for
   for (const zero_newton_schulz* q : {(const zero_newton_schulz*)nullptr, &fast}) {

@@ -433,13 +433,16 @@ OrthoSpace space_of(bool thin, int64_t rows, int64_t cols, int64_t batch) {
   return thin ? thin_space(rows, cols, batch) : ortho_space(rows, cols, batch);
 }
 
-// As many matrices as one batch takes: all of them where the batch's workspace stays
-// within 1 GiB, as launches of many tiles waste the least (48 matrices of 768 x 768 in
-// one batch, two and four: 870, 875 and 1160 us; 24 of 1024 x 4096 in one and two: 2370
-// and 2520), or a few batches more where those fill their rounds better.
+// As many matrices as one batch takes: all of them where X, A and B stay within
+// 1 GiB, as launches of many tiles waste the least (48 matrices of 768 x 768 in one
+// batch, two and four: 870, 875 and 1160 us; 24 of 1024 x 4096 in one and two: 2370
+// and 2520), or a few batches more where those fill their rounds better.  With padded
+// sides, norms and pieces of sums the workspace stays within an eighth more (32 of
+// 2048 x 2048, which are 1 GiB by themselves, in one batch and two: 6335 and 7047 us).
 int64_t batch_of(bool thin, int64_t rows, int64_t cols, int64_t count) {
-  constexpr int64_t limit = int64_t(1) << 30;
-  int64_t most = std::min<int64_t>(count, kMaxBatch);
+  constexpr int64_t bulk = int64_t(1) << 30, limit = bulk + bulk / 8;
+  const int64_t n = std::min(rows, cols), bytes = rows * cols * 6 + n * n * 2;
+  int64_t most = std::min<int64_t>({count, kMaxBatch, std::max<int64_t>(1, bulk / bytes)});
   while (most > 1) {
     const int64_t total = space_of(thin, rows, cols, most).total;
     if (total <= limit) break;
