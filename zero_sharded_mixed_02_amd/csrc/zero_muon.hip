@@ -574,7 +574,8 @@ __global__ void __launch_bounds__(kSmallThreads) ortho_small_kernel(const OrthoS
 // out (2 x 2 with A, B and X in fp16: up to 0.014 off, 0.002 at the median), so these go the way
 // of the large matrices with a short side: P in fp32 from A = X X^T, which is one tile of
 // 16 x 16, and P X with P as two fp16 numbers along k.  Every wave forms P by itself: a
-// product's result lies in a wave's registers as the next one's operands do.
+// product's result lies in a wave's registers as the next one's operands do (16 x 512: 8.3 us,
+// most of it the load, the norm and a chain of 18 products; 2 x 2: 5.0).
 constexpr int kShortThreads = 256;
 template <typename T>
 __global__ void __launch_bounds__(kShortThreads) ortho_short_kernel(const OrthoSmallArgs a) {
